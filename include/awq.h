@@ -29,6 +29,16 @@
  * channels kept in 16-bit, the rest quantized), a channel selector whose mask
  * the search accepts:
  *   awq_salient_channels  the n channels with the largest mean |x_j|
+ * Linears whose weight depends on the row (a serving model's routed experts
+ * and per-request adapters), beside the shared product:
+ *   awq_route_experts      which experts serve a token, and with what weight
+ *   awq_w4a16_experts_up   each token through its experts' packed weights,
+ *                          with the gated activation or without
+ *   awq_w4a16_experts_down each (token, expert) row through its expert's
+ *                          packed weights, weighted and summed over a token's
+ *                          experts
+ *   awq_lora_add           each row's low-rank adapter, added to the output
+ *                          of the shared product
  * Linears that read the same input (q, k and v; gate and up) are searched
  * together by passing their row-concatenated W to awq_search_scales: they then
  * share s, and one fold serves them all.
@@ -92,8 +102,23 @@ typedef enum awq_op {
   AWQ_OP_ACT_STATS = 0,
   AWQ_OP_SEARCH = 1,
   AWQ_OP_QUANTIZE = 2,
-  AWQ_OP_GEMM = 3
+  AWQ_OP_GEMM = 3,
+  AWQ_OP_EXPERTS_UP = 4,    /* M tokens, T = experts, n_alpha = top_k             */
+  AWQ_OP_EXPERTS_DOWN = 5,  /* the same                                           */
+  AWQ_OP_LORA = 6           /* M rows, T = adapters, n_alpha = rank               */
 } awq_op;
+
+/* Scores of awq_route_experts. */
+typedef enum awq_score {
+  AWQ_SCORE_SOFTMAX = 0,
+  AWQ_SCORE_SIGMOID = 1
+} awq_score;
+
+/* Epilogue of awq_w4a16_experts_up. */
+typedef enum awq_act {
+  AWQ_ACT_NONE = 0,
+  AWQ_ACT_SWIGLU = 1        /* silu(first half of the rows) * second half         */
+} awq_act;
 
 #define AWQ_GROUP 128           /* the usual group size; 64 and 256 are accepted too */
 #define AWQ_MAX_ALPHA 64
@@ -357,6 +382,113 @@ awq_status awq_w4a16_gemm_noalloc(const void* x, awq_dtype xdt, int64_t M, int64
  */
 awq_status awq_fold_scales(void* v, awq_dtype dt, int64_t rows, int64_t cols, int64_t ld, const float* s,
                            int axis, void* stream);
+
+/*
+ * Expert routing.  For token t with logits l_e, e = 0 .. E - 1:
+ *   score_e  = exp(l_e) / sum_i exp(l_i)      (AWQ_SCORE_SOFTMAX), or
+ *              1 / (1 + exp(-l_e))            (AWQ_SCORE_SIGMOID)
+ *   choice_e = score_e + bias_e               (bias == NULL: 0); the bias only
+ *              chooses, the weights come from the scores
+ *   groups   the E experts form n_group groups of E / n_group consecutive
+ *            ones.  With n_group > 1 a group is worth the sum of its
+ *            min(group_top, group size) largest choices, the topk_group most
+ *            valuable groups stay and the experts of the others are not usable
+ *   ids      the top_k usable experts of largest choice, largest first
+ *   weights  w_j = score_{id_j}; with renormalize divided by their sum
+ *            (unless it is 0); then multiplied by scale
+ * Ties, among groups and among experts, go to the lowest index.  A logit of
+ * -inf or NaN makes its expert not usable (score 0, choice -inf); +inf counts
+ * as the largest float.  Where fewer than top_k experts are usable the
+ * remaining ids are -1 with weight 0 (a row of -inf: all of them).  Choices are
+ * formed and compared in double precision, so close scores do not change
+ * places by rounding; weights are rounded once to float.
+ *
+ *   logits   [T][ldl] fp16, bf16 or f32 (ldt), aligned to its element
+ *   E        1 .. AWQ_MAX_EXPERTS
+ *   bias     [E] float, finite, or NULL
+ *   n_group  >= 1, divides E;  topk_group 1 .. n_group;  group_top 1 or 2
+ *   top_k    1 .. min(E / n_group * topk_group, AWQ_MAX_TOP_K)
+ *   ids      [T][top_k] int32;  weights [T][top_k] float
+ * n_group above 64 -> AWQ_ERR_UNSUPPORTED.  T == 0 is a no-op.
+ */
+#define AWQ_MAX_EXPERTS 1024
+#define AWQ_MAX_TOP_K 64
+awq_status awq_route_experts(const void* logits, awq_dtype ldt, int64_t T, int64_t E, int64_t ldl,
+                             const float* bias, awq_score score, int n_group, int topk_group,
+                             int group_top, int top_k, int renormalize, float scale, int32_t* ids,
+                             float* weights, void* stream);
+
+/*
+ * The routed W4A16 products: the E experts' weights are stacked, expert e's
+ * rows [e N, (e + 1) N) of qweight / scales / zeros, as awq_quantize_pack
+ * writes them for the [E N][K] row-concatenation.  A slot is a (token, choice)
+ * pair m top_k + j; ids (awq_route_experts' output) names its expert, and any
+ * id outside [0, E) means that the slot has none.
+ *   up    z = W_{ids[m][j]} x[m]                          (N outputs)
+ *         y[m top_k + j] = z                              (AWQ_ACT_NONE)
+ *         y[m top_k + j][c] = silu(z[c]) z[N/2 + c]       (AWQ_ACT_SWIGLU, c < N/2)
+ *         slots without an expert are written as zeros
+ *   down  y[m] = sum_j weights[m][j] W_{ids[m][j]} x[m top_k + j]
+ *         over the slots that have an expert (none: zeros); x rows of the
+ *         others are not read into the result
+ * with W_e[n][k] = step (q - z) as in awq_w4a16_gemm.  Products of the exact
+ * integers q - z with the activations (as fp16 scaled by an exact power of
+ * two) are summed in fp32 per group and scaled by the group's step in fp32;
+ * the activation function and the sum over j run in fp32 and the output is
+ * rounded once.  1/s is expected folded (awq_fold_scales): into the producer
+ * of x for up, into the up half's rows for down.
+ *
+ *   x         up: [M][ldx], down: [M top_k][ldx], fp16 or bf16 (xdt)
+ *   ids       [M][top_k] int32;  top_k 1 .. AWQ_MAX_TOP_K
+ *   weights   [M][top_k] float (down)
+ *   E         1 .. AWQ_MAX_EXPERTS
+ *   K         a multiple of group_size (64, 128 or 256), <= AWQ_MAX_K
+ *   N         up with AWQ_ACT_SWIGLU: even
+ *   y         up: [M top_k][ldy], down: [M][ldy], F16, BF16 or F32 (ydt)
+ *   ws        >= awq_workspace_bytes(AWQ_OP_EXPERTS_UP or _DOWN, M, N, K, E, top_k)
+ * M == 0 or N == 0 is a no-op.  More than 2^24 slots, 2^31 or more bytes in
+ * one expert's packed words or in the activations as packed fp16 rows ->
+ * AWQ_ERR_UNSUPPORTED.
+ */
+awq_status awq_w4a16_experts_up(const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                                const int32_t* ids, int top_k, const int32_t* qweight,
+                                const uint16_t* scales, const uint8_t* zeros, int64_t E, int64_t N,
+                                int group_size, awq_act act, void* y, awq_dtype ydt, int64_t ldy,
+                                void* ws, size_t ws_bytes, void* stream);
+awq_status awq_w4a16_experts_down(const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                                  const int32_t* ids, const float* weights, int top_k,
+                                  const int32_t* qweight, const uint16_t* scales,
+                                  const uint8_t* zeros, int64_t E, int64_t N, int group_size,
+                                  void* y, awq_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection: with
+ * a = adapter[m] and r_a = ranks[a] (ranks == NULL: R)
+ *   y[m] = base[m] + scaling[a] B_a[:, :r_a] (A_a[:r_a] x[m])
+ * and y[m] = base[m] for rows whose adapter is outside [0, n_adapters)
+ * (base == NULL: 0 in both).  base may be y itself (in place).  Sums and the
+ * intermediate A x are held in fp32 (the latter enters the second product as
+ * the sum of two 16-bit values); the output is rounded once.  What A and B
+ * hold past an adapter's rank is not used, whatever it is.
+ *
+ *   x        [M][ldx] fp16 or bf16 (xdt), K a multiple of 8, <= AWQ_MAX_K
+ *   adapter  [M] int32
+ *   a        [n_adapters][R][K] xdt;  b [n_adapters][N][R] xdt
+ *   R        a multiple of 8, 8 .. AWQ_MAX_RANK
+ *   ranks    [n_adapters] int32 (values are held to 0 .. R) or NULL
+ *   scaling  [n_adapters] float or NULL (1)
+ *   base     [M][ldb] of ydt or NULL;  y [M][ldy] F16, BF16 or F32 (ydt)
+ *   ws       >= awq_workspace_bytes(AWQ_OP_LORA, M, N, K, n_adapters, R)
+ * M == 0 or N == 0 is a no-op; with n_adapters == 0 every row is base.
+ * More than 2^24 rows or 16384 adapters -> AWQ_ERR_UNSUPPORTED.
+ */
+#define AWQ_MAX_RANK 256
+awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                        const int32_t* adapter, const void* a, const void* b, int64_t n_adapters,
+                        int64_t R, const int32_t* ranks, const float* scaling, const void* base,
+                        int64_t ldb, int64_t N, void* y, awq_dtype ydt, int64_t ldy, void* ws,
+                        size_t ws_bytes, void* stream);
 
 /* Diagnostic: a plain streaming read of `bytes` of device memory, the rate the
  * W4A16 products are measured against at their own sizes.  "AWQ Math",

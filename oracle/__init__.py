@@ -36,3 +36,4 @@ from .awq import (  # noqa: F401
     salient_channels,
     symmetric_rtn,
 )
+from .routed import expert_rows, lora, route_experts, swiglu  # noqa: F401,E402

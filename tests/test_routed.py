@@ -1,0 +1,652 @@
+"""The operators whose weight depends on the row (awq_route_experts,
+awq_w4a16_experts_up / _down, awq_lora_add) against float64, and what they
+refuse."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from tests.gpu_util import f32, gpu
+
+awq = pytest.importorskip("weight_only_int4_stats_amd")
+E = awq._abi
+
+DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture
+def on_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    awq.lib()
+
+
+# ---- tolerances ----------------------------------------------------------------
+# One output rounding is at most eps / 2 of the value (half the smallest
+# subnormal near 0).  A matrix-core sum of n products that are exact in fp32 is
+# off by at most n units of 2^-23 of the sum of their sizes (each addition is
+# within one unit of the running size, whatever its rounding).
+
+
+def rounding(ref, dtype):
+    i = torch.finfo(dtype)
+    return np.abs(ref) * (i.eps / 2) + (i.tiny * i.eps / 2 if dtype != torch.bfloat16 else i.tiny)
+
+
+def check(got, ref, slack, dtype, what=""):
+    """|got - ref| <= slack (what the computation may be off) + the rounding of
+    a value that far from ref."""
+    got = f32(got).astype(np.float64)
+    bound = slack + rounding(np.abs(ref) + slack, dtype)
+    off = np.abs(got - ref)
+    bad = ~(off <= bound)
+    assert not bad.any(), (what, int(bad.sum()), float(np.max(off / np.maximum(bound, 1e-300))),
+                           np.argwhere(bad)[:5].tolist())
+
+
+def product_slack(size, K, g):
+    """z = sum over groups of step (sum q x - z sum x): each group's sums have g
+    terms plus its start, the groups are added in fp32; five roundings per
+    group beside (the sum of x, its product with z, the step's and the row
+    scale's products, the addition)."""
+    return size * (g + K // g + 13) * 2.0 ** -23
+
+
+# ---- routing ---------------------------------------------------------------------
+
+
+def route_case(T, n, dtype, seed, spread=1.5, levels=0):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(0, spread, (T, n))
+    if levels:                                       # few different values: ties everywhere
+        x = np.round(x * levels) / levels
+    return torch.from_numpy(x).to(dtype)
+
+
+ROUTES = [
+    # T, E, top_k, n_group, topk_group, group_top, sigmoid, bias, renormalize, scale, dtype, tie levels
+    (1, 1, 1, 1, 1, 1, False, False, True, 1.0, "f32", 0),
+    (1, 64, 8, 1, 1, 1, False, False, True, 1.0, "bf16", 0),
+    (5, 3, 2, 1, 1, 1, True, True, False, 1.5, "f16", 0),
+    (257, 60, 4, 1, 1, 1, False, True, False, 1.0, "f32", 0),
+    (33, 64, 64, 1, 1, 1, True, False, True, 1.0, "bf16", 2),
+    (70, 65, 7, 1, 1, 1, False, False, True, 1.0, "f16", 1),
+    (130, 128, 6, 4, 2, 1, False, False, False, 16.0, "bf16", 4),
+    (130, 256, 8, 8, 4, 2, True, True, True, 2.5, "bf16", 0),
+    (67, 256, 8, 8, 4, 2, True, False, True, 2.5, "f32", 2),
+    (19, 96, 5, 32, 3, 2, False, True, True, 1.0, "f32", 0),     # groups of 3
+    (23, 160, 16, 8, 3, 2, False, True, True, 1.0, "f16", 3),    # groups of 20 over lanes of 4
+    (9, 64, 3, 64, 9, 2, True, True, False, 1.0, "f32", 0),      # groups of 1
+    (11, 512, 33, 2, 1, 2, False, False, True, 1.0, "bf16", 0),
+    (7, 1000, 50, 1, 1, 1, True, True, True, 1.0, "f32", 0),
+    (6, 1024, 64, 64, 8, 2, False, True, True, 1.0, "bf16", 0),
+]
+
+
+def compare_route(got, ref, what):
+    ids, weights = got[0].cpu().numpy(), got[1].cpu().numpy().astype(np.float64)
+    assert np.array_equal(ids, ref[0]), (what, np.argwhere(ids != ref[0])[:5].tolist())
+    # formed in double, rounded once to float
+    assert np.all(np.abs(weights - ref[1]) <= np.abs(ref[1]) * (2.0 ** -24 + 1e-12) + 2.0 ** -150), what
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", ROUTES, ids=lambda c: "x".join(str(v) for v in c[:6]))
+def test_route(on_gpu, case):
+    T, n, k, ng, tg, gt, sig, with_bias, renorm, scale, dt, levels = case
+    x = route_case(T, n, DTYPES[dt], n + T, levels=levels)
+    bias = np.random.default_rng(n).normal(0, 0.05, n).astype(np.float32) if with_bias else None
+    got = awq.awq_route_experts(gpu(x), k, bias=None if bias is None else gpu(torch.from_numpy(bias)),
+                                score="sigmoid" if sig else "softmax", n_group=ng, topk_group=tg, group_top=gt,
+                                renormalize=renorm, scale=scale)
+    ref = O.route_experts(f32(x), k, bias, sig, ng, tg, gt, renorm, scale)
+    compare_route(got, ref, case)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("groups", [(1, 1), (4, 2), (4, 4)])
+def test_route_masked_and_extreme_logits(on_gpu, sig, dt, groups):
+    """Rows of -inf, of NaN, with fewer usable experts than top_k, masked by the
+    type's lowest value, with +inf, and far apart."""
+    dtype = DTYPES[dt]
+    x = route_case(12, 48, dtype, 5)
+    low = torch.finfo(dtype).min
+    x[0] = -math.inf
+    x[1] = math.nan
+    x[2, 3:] = -math.inf
+    x[3] = low
+    x[4, :45] = low
+    x[5, 7] = math.inf
+    x[6, 11], x[6, 29] = math.inf, math.inf
+    x[7] = 60 * torch.arange(48).to(dtype)
+    x[8, ::2] = math.nan
+    x[9, 12:] = -math.inf                            # with groups: only the first has anyone
+    bias = torch.linspace(-0.1, 0.1, 48)
+    for b in (None, bias):
+        got = awq.awq_route_experts(gpu(x), 6, bias=None if b is None else gpu(b), score="sigmoid" if sig else "softmax",
+                                    n_group=groups[0], topk_group=groups[1], group_top=2)
+        ref = O.route_experts(f32(x), 6, None if b is None else b.numpy(), sig, groups[0], groups[1], 2)
+        compare_route(got, ref, (sig, dt, groups, b is not None))
+
+
+@pytest.mark.gpu
+def test_route_close_choices(on_gpu):
+    """Choices one double step apart in the scores but equal as floats keep
+    their order, and exact ties go to the lowest index."""
+    x = torch.zeros(64, 128)
+    for t in range(64):
+        x[t, 100 - t] = 2.0 ** -22                   # score differs by about 2e-9
+        x[t, 20] = 2.0 ** -22 if t % 2 else 0.0
+    got = awq.awq_route_experts(gpu(x), 4)
+    compare_route(got, O.route_experts(x.numpy(), 4), "close")
+
+
+@pytest.mark.gpu
+def test_route_strided_rows_and_given_outputs(on_gpu):
+    big = route_case(40, 100, torch.bfloat16, 9)
+    x = gpu(big)[:, 10:74]
+    ids = torch.full((42, 5), 77, dtype=torch.int32, device="cuda")
+    w = torch.full((42, 5), 7.0, device="cuda")
+    awq.awq_route_experts(x, 5, ids=ids[1:41], weights=w[1:41])
+    compare_route((ids[1:41], w[1:41]), O.route_experts(f32(big)[:, 10:74], 5), "strided")
+    assert (ids[0] == 77).all() and (ids[41] == 77).all() and (w[0] == 7).all() and (w[41] == 7).all()
+    i0, w0 = awq.awq_route_experts(x[:0], 5)
+    assert i0.shape == (0, 5) and w0.shape == (0, 5)
+
+
+# ---- the routed products -------------------------------------------------------------
+
+
+def stack(n_exp, N, K, g, seed):
+    rng = np.random.default_rng(seed)
+    words = rng.integers(-2 ** 31, 2 ** 31, (n_exp, N, K // 8), dtype=np.int64).astype(np.int32)
+    step = rng.uniform(2e-4, 4e-3, (n_exp, N, K // g)).astype(np.float16)
+    zero = rng.integers(0, 16, (n_exp, N, K // g)).astype(np.uint8)
+    return words, step, zero
+
+
+def acts(rows, K, dtype, seed):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(0, 1, (rows, K)) * np.where(rng.random(K) < 0.02, 20.0, 1.0)
+    return torch.from_numpy(x).to(dtype)
+
+
+def packed(w):
+    return tuple(gpu(torch.from_numpy(t)) for t in w)
+
+
+def choices(T, n_exp, k, seed, kind):
+    rng = np.random.default_rng(seed)
+    ids = np.stack([rng.permutation(n_exp)[:k] for _ in range(T)]).astype(np.int32)
+    if kind == "one":                                # every slot one expert
+        ids[:] = n_exp - 1
+    if kind == "holes":
+        ids[rng.random(ids.shape) < 0.3] = -1
+        ids[T // 2] = [-1, n_exp, 2 ** 31 - 1, -2 ** 31][T % 4]
+    if kind == "none":
+        ids[:] = -7
+    return ids
+
+
+def check_up(x, ids, w, g, act, out, y, what):
+    k = ids.shape[1]
+    K = x.shape[1]
+    z, size = O.expert_rows(np.repeat(f32(x), k, axis=0), ids.reshape(-1), *w)
+    slack = product_slack(size, K, g)
+    if act == "swiglu":
+        n = z.shape[1] // 2
+        ref = O.swiglu(z)
+        gate, up = np.abs(z[:, :n]), np.abs(z[:, n:])
+        dg, du = slack[:, :n], slack[:, n:]
+        # |silu'| <= 1.1, silu <= |gate|; exp, the sum, the division and the product: under 8 roundings
+        slack = 1.1 * dg * (up + du) + gate * du + 8 * 2.0 ** -24 * np.abs(ref)
+        z = ref
+    check(y, z, slack, out, what)
+
+
+def check_down(x, ids, weights, w, g, out, y, what):
+    T, k = ids.shape
+    K = x.shape[1]
+    flat = ids.reshape(-1)
+    ok = (flat >= 0) & (flat < w[0].shape[0])
+    xx = np.where(ok[:, None], f32(x), 0.0)
+    z, size = O.expert_rows(xx, flat, *w)
+    wt = np.where(ok, weights.reshape(-1).astype(np.float64), 0.0)[:, None]
+    ref = (z * wt).reshape(T, k, -1).sum(1)
+    # each term's own error, and k additions (and products) of the terms' sizes
+    slack = (product_slack(size, K, g) * np.abs(wt)).reshape(T, k, -1).sum(1)
+    slack += (k + 1) * 2.0 ** -23 * (np.abs(z * wt)).reshape(T, k, -1).sum(1)
+    check(y, ref, slack, out, what)
+
+
+PRODUCTS = [
+    # T, experts, top_k, K, N, group, x type, y type, choices
+    (1, 1, 1, 64, 2, 64, "f16", "f32", ""),
+    (1, 8, 2, 128, 16, 128, "bf16", "bf16", ""),
+    (1, 64, 8, 512, 130, 128, "f16", "f16", ""),
+    (2, 5, 3, 192, 66, 64, "bf16", "f32", "holes"),
+    (3, 4, 4, 256, 200, 256, "f16", "f32", "holes"),
+    (7, 3, 2, 384, 62, 128, "bf16", "f16", "holes"),
+    (40, 2, 1, 1152, 34, 128, "bf16", "f32", "one"),
+    (17, 16, 1, 2176, 18, 64, "f16", "f32", "one"),
+    (33, 7, 3, 2304, 66, 256, "bf16", "bf16", "holes"),
+    (50, 6, 2, 4224, 32, 128, "f16", "f32", ""),
+    (3, 2, 2, 320, 64, 64, "f16", "bf16", "none"),
+    (150, 4, 2, 320, 258, 64, "bf16", "f32", "holes"),
+    (300, 8, 2, 256, 130, 128, "f16", "f16", "holes"),
+    (700, 3, 2, 512, 390, 256, "bf16", "f32", ""),
+    (260, 2, 2, 128, 514, 128, "f16", "f32", "one"),
+    (1030, 16, 8, 192, 70, 64, "bf16", "bf16", "holes"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("case", PRODUCTS, ids=lambda c: "x".join(str(v) for v in c))
+def test_experts_up(on_gpu, case, act):
+    T, n_exp, k, K, N, g, xdt, ydt, kind = case
+    w = stack(n_exp, N, K, g, T + K)
+    x = acts(T, K, DTYPES[xdt], N)
+    ids = choices(T, n_exp, k, T * N, kind)
+    y = awq.awq_w4a16_experts_up(gpu(x), gpu(torch.from_numpy(ids)), *packed(w), act=act, out_dtype=DTYPES[ydt],
+                                 group_size=g)
+    check_up(x, ids, w, g, act, DTYPES[ydt], y, case)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", PRODUCTS, ids=lambda c: "x".join(str(v) for v in c))
+def test_experts_down(on_gpu, case):
+    T, n_exp, k, K, N, g, xdt, ydt, kind = case
+    N += N // 2 % 2                                  # odd numbers of outputs among them
+    w = stack(n_exp, N, K, g, T + K)
+    x = acts(T * k, K, DTYPES[xdt], N)
+    ids = choices(T, n_exp, k, T * N, kind)
+    weights = np.random.default_rng(T).uniform(-0.2, 1.0, (T, k)).astype(np.float32)
+    gone = (ids.reshape(-1) < 0) | (ids.reshape(-1) >= n_exp)
+    x[torch.from_numpy(gone)] = math.nan             # rows without an expert are not read into the result
+    weights.reshape(-1)[gone] = np.nan
+    y = awq.awq_w4a16_experts_down(gpu(x), gpu(torch.from_numpy(ids)), gpu(torch.from_numpy(weights)), *packed(w),
+                                   out_dtype=DTYPES[ydt], group_size=g)
+    check_down(x, ids, weights, w, g, DTYPES[ydt], y, case)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 90, 400])
+def test_experts_strides_and_neighbours(on_gpu, T):
+    """Padded input and output rows: what lies beside the output stays."""
+    n_exp, k, K, N, g = 4, 2, 256, 50, 128
+    w = stack(n_exp, N, K, g, 3)
+    ids = choices(T, n_exp, k, 8, "holes")
+    wide = acts(T * k, K + 24, torch.float16, 4)
+    weights = np.random.default_rng(4).uniform(0, 1, (T, k)).astype(np.float32)
+    p = packed(w)
+    gi = gpu(torch.from_numpy(ids))
+    for col in (3, 4):                               # output rows off and on 16 bytes
+        big = torch.full((T * k + 2, N + 14), 9.0, device="cuda")
+        awq.awq_w4a16_experts_up(gpu(wide)[:T, 8:8 + K], gi, *p, y=big[1:T * k + 1, col:col + N])
+        check_up(wide[:T, 8:8 + K], ids, w, g, "none", torch.float32, big[1:T * k + 1, col:col + N], "up")
+        big[1:T * k + 1, col:col + N] = 9.0
+        assert (big == 9.0).all()
+        big = torch.full((T + 2, N + 14), 9.0, dtype=torch.bfloat16, device="cuda")
+        awq.awq_w4a16_experts_down(gpu(wide)[:, 8:8 + K], gi, gpu(torch.from_numpy(weights)), *p,
+                                   y=big[1:T + 1, col:col + N])
+        check_down(wide[:, 8:8 + K], ids, weights, w, g, torch.bfloat16, big[1:T + 1, col:col + N], "down")
+        big[1:T + 1, col:col + N] = 9.0
+        assert (big == 9.0).all()
+
+
+@pytest.mark.gpu
+def test_experts_empty(on_gpu):
+    w = packed(stack(2, 16, 128, 128, 1))
+    x = gpu(acts(0, 128, torch.float16, 1))
+    ids = torch.zeros((0, 2), dtype=torch.int32, device="cuda")
+    assert awq.awq_w4a16_experts_up(x, ids, *w).shape == (0, 16)
+    assert awq.awq_w4a16_experts_down(x, ids, torch.zeros((0, 2), device="cuda"), *w).shape == (0, 16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 30, 600])
+def test_moe_layer(on_gpu, T):
+    """Routing, both products and a shared expert on weights this library
+    packed, one after another; then captured once and replayed on new inputs
+    with eager work between."""
+    n_exp, k, H, I = 8, 2, 512, 384
+    rng = np.random.default_rng(T)
+    dev = torch.device("cuda")
+    w1 = gpu(torch.from_numpy(rng.normal(0, 0.04, (n_exp * 2 * I, H))).to(torch.float16))
+    w2 = gpu(torch.from_numpy(rng.normal(0, 0.04, (n_exp * H, I))).to(torch.float16))
+    p1 = tuple(t.view(n_exp, 2 * I, -1) for t in awq.awq_quantize_pack(w1))
+    p2 = tuple(t.view(n_exp, H, -1) for t in awq.awq_quantize_pack(w2))
+    gate = gpu(torch.from_numpy(rng.normal(0, 0.1, (H, n_exp))).float())
+    n1, n2 = (tuple(t.cpu().numpy() for t in p) for p in (p1, p2))
+
+    def layer(x, logits):
+        ids, weights = awq.awq_route_experts(logits, k)
+        h = awq.awq_w4a16_experts_up(x, ids, *p1, act="swiglu")
+        return ids, weights, h, awq.awq_w4a16_experts_down(h, ids, weights, *p2)
+
+    def verify(x, logits, outs, what):
+        ids, weights, h, y = outs
+        compare_route((ids, weights), O.route_experts(f32(logits), k), what)
+        check_up(x, ids.cpu().numpy(), n1, 128, "swiglu", torch.float16, h, what)
+        check_down(h, ids.cpu().numpy(), weights.cpu().numpy(), n2, 128, torch.float16, y, what)
+
+    x = gpu(acts(T, H, torch.float16, 2))
+    logits = x.float() @ gate
+    eager = layer(x, logits)
+    verify(x, logits, eager, "eager")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(x, logits)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = layer(x, logits)
+    for seed in range(3):
+        x.copy_(gpu(acts(T, H, torch.float16, 10 + seed)))
+        logits.copy_(x.float() @ gate)
+        if T > 4:
+            logits[T // 2:] = -math.inf              # the rest of the batch is padding now
+        again = layer(x, logits)
+        torch.cuda.synchronize(dev)
+        for o in outs:
+            o.fill_(55)
+        graph.replay()
+        torch.cuda.synchronize(dev)
+        for a, b in zip(again, outs):
+            assert torch.equal(a, b), seed
+    verify(x, logits, outs, "replayed")
+
+
+# ---- adapters ---------------------------------------------------------------------------
+
+
+def check_lora(x, adapter, a, b, ranks, scaling, base, out, y, what):
+    ref, size_h, size_x = O.lora(f32(x), adapter, f32(a), f32(b), ranks, scaling)
+    # the first sum has K terms (and the parts' additions), the second 2 R; the
+    # intermediate enters as two 16-bit values: 2^-17 of it for bf16 (two
+    # roundings of 2^-9, the second of what the first left), less for fp16
+    slack = size_x * (x.shape[1] + 160) * 2.0 ** -23
+    slack += (size_h + slack) * (2.0 ** -17 + (2 * a.shape[1] + 8) * 2.0 ** -23)
+    if base is not None:
+        ref = ref + f32(base).astype(np.float64)
+        slack = slack + 2.0 ** -23 * (np.abs(ref) + slack)
+    check(y, ref, slack, out, what)
+
+
+LORAS = [
+    # rows, adapters, R, K, N, type, y type, ranks, scaling, base, adapter choice
+    (1, 1, 8, 8, 1, "f16", "f32", False, False, False, "mixed"),
+    (1, 8, 16, 512, 70, "bf16", "bf16", False, True, True, "mixed"),
+    (2, 3, 24, 136, 65, "f16", "f16", True, True, True, "mixed"),
+    (19, 5, 64, 264, 300, "bf16", "f32", True, True, False, "mixed"),
+    (64, 32, 40, 1032, 130, "f16", "f32", True, False, True, "mixed"),
+    (100, 2, 256, 64, 257, "bf16", "f32", True, True, True, "mixed"),
+    (37, 4, 136, 72, 64, "f16", "bf16", False, True, True, "none"),
+    (90, 0, 16, 64, 33, "f16", "f32", False, False, True, "mixed"),
+    (700, 0, 16, 64, 33, "bf16", "bf16", False, False, False, "mixed"),
+    (513, 9, 16, 200, 100, "bf16", "bf16", True, True, True, "mixed"),
+    (900, 3, 32, 128, 259, "f16", "f32", True, True, True, "runs"),
+    (1100, 600, 8, 64, 40, "f16", "f32", False, False, False, "mixed"),
+    (600, 1, 72, 96, 64, "bf16", "f32", False, True, True, "none"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", LORAS, ids=lambda c: "x".join(str(v) for v in c))
+def test_lora(on_gpu, case):
+    M, L, R, K, N, xdt, ydt, with_ranks, with_scaling, with_base, kind = case
+    dtype, out = DTYPES[xdt], DTYPES[ydt]
+    rng = np.random.default_rng(M + K + N)
+    x = acts(M, K, dtype, M)
+    a = torch.from_numpy(rng.normal(0, 1 / math.sqrt(K), (L, R, K))).to(dtype)
+    b = torch.from_numpy(rng.normal(0, 1, (L, N, R))).to(dtype)
+    adapter = rng.integers(-1, L + 1, M).astype(np.int32)
+    if kind == "runs":
+        adapter = np.sort(adapter)
+    if kind == "none":
+        adapter[:] = np.where(rng.random(M) < 0.5, -2 ** 31, L)
+    ranks = rng.integers(-1, R + 2, L).astype(np.int32) if with_ranks else None
+    if with_ranks:                                   # what lies past a rank is not used
+        for i, r in enumerate(np.clip(ranks, 0, R)):
+            a[i, r:] = math.nan
+            b[i, :, r:] = math.inf
+    scaling = rng.uniform(-2, 2, L).astype(np.float32) if with_scaling else None
+    base = torch.from_numpy(rng.normal(0, 1, (M, N))).to(out) if with_base else None
+    t = lambda v: None if v is None else gpu(torch.from_numpy(v))  # noqa: E731
+    gb = None if base is None else gpu(base)
+    y = awq.awq_lora_add(gpu(x), t(adapter), gpu(a), gpu(b), base=gb, scaling=t(scaling), ranks=t(ranks), out_dtype=out)
+    check_lora(x, adapter, a, b, ranks, scaling, base, out, y, case)
+    if base is not None:                             # in place
+        awq.awq_lora_add(gpu(x), t(adapter), gpu(a), gpu(b), base=gb, scaling=t(scaling), ranks=t(ranks), y=gb)
+        assert torch.equal(gb, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 20, 640])
+def test_lora_strides_and_neighbours(on_gpu, M):
+    L, R, K, N = 3, 16, 128, 50
+    rng = np.random.default_rng(M)
+    wide = acts(M, K + 24, torch.bfloat16, 1)
+    a = torch.from_numpy(rng.normal(0, 0.1, (L, R, K))).to(torch.bfloat16)
+    b = torch.from_numpy(rng.normal(0, 1, (L, N, R))).to(torch.bfloat16)
+    adapter = rng.integers(-1, L, M).astype(np.int32)
+    for col in (3, 8):
+        base = torch.from_numpy(rng.normal(0, 1, (M, N + 30))).to(torch.bfloat16)
+        big = torch.full((M + 2, N + 14), 9.0, dtype=torch.bfloat16, device="cuda")
+        awq.awq_lora_add(gpu(wide)[:, 8:8 + K], gpu(torch.from_numpy(adapter)), gpu(a), gpu(b),
+                         base=gpu(base)[:, 5:5 + N], y=big[1:M + 1, col:col + N])
+        check_lora(wide[:, 8:8 + K], adapter, a, b, None, None, base[:, 5:5 + N], torch.bfloat16,
+                   big[1:M + 1, col:col + N], col)
+        big[1:M + 1, col:col + N] = 9.0
+        assert (big == 9.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 48, 800])
+def test_lora_beside_the_shared_product(on_gpu, M):
+    """The packed product and the adapters of its rows, eager and captured."""
+    N, K, L, R = 384, 512, 5, 16
+    rng = np.random.default_rng(M)
+    w = gpu(torch.from_numpy(rng.normal(0, 0.04, (N, K))).to(torch.float16))
+    q, sc, z = awq.awq_quantize_pack(w)
+    x = gpu(acts(M, K, torch.float16, 3))
+    a = gpu(torch.from_numpy(rng.normal(0, 0.05, (L, R, K))).to(torch.float16))
+    b = gpu(torch.from_numpy(rng.normal(0, 0.3, (L, N, R))).to(torch.float16))
+    adapter = gpu(torch.from_numpy(rng.integers(-1, L, M).astype(np.int32)))
+
+    def step():
+        y = awq.awq_w4a16_gemm(x, q, sc, z, out_dtype=torch.float32)
+        return y, awq.awq_lora_add(x, adapter, a, b, base=y)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed in range(3):
+        x.copy_(gpu(acts(M, K, torch.float16, 20 + seed)))
+        adapter.copy_(torch.from_numpy(rng.integers(-1, L, M).astype(np.int32)))
+        again = step()
+        torch.cuda.synchronize()
+        for o in outs:
+            o.fill_(55)
+        graph.replay()
+        torch.cuda.synchronize()
+        for u, v in zip(again, outs):
+            assert torch.equal(u, v), seed
+        check_lora(x.cpu(), adapter.cpu().numpy(), a.cpu(), b.cpu(), None, None, again[0].cpu(), torch.float32,
+                   again[1], seed)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once(on_gpu):
+    """Calls on two streams with workspaces of their own do not meet."""
+    jobs = []
+    for i in range(2):
+        w = stack(8, 128, 512, 128, i)
+        x = acts(300, 512, torch.float16, i)
+        ids = choices(300, 8, 2, i, "")
+        jobs.append((w, x, ids, packed(w), gpu(x), gpu(torch.from_numpy(ids)), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        for w, x, ids, p, gx, gi, st in jobs:
+            with torch.cuda.stream(st):
+                outs.append(awq.awq_w4a16_experts_up(gx, gi, *p, out_dtype=torch.float32))
+    torch.cuda.synchronize()
+    for n, y in enumerate(outs):
+        w, x, ids = jobs[n % 2][:3]
+        check_up(x, ids, w, 128, "none", torch.float32, y, n)
+
+
+# ---- refusals (no launch, so no GPU) ----------------------------------------------------
+
+A, B, C, D = (ctypes.c_void_p(v << 16) for v in (1, 2, 3, 4))
+BAD = ctypes.c_void_p(0x10002)
+ODD = ctypes.c_void_p(0x10001)
+
+
+def test_route_refusals():
+    f = awq.lib().awq_route_experts
+
+    def call(**kw):
+        a = dict(x=A, dt=0, T=4, E=64, ld=64, bias=None, score=0, ng=8, tg=4, gt=2, k=8, rn=1, sc=1.0, ids=B, w=C)
+        a.update(kw)
+        return f(a["x"], a["dt"], a["T"], a["E"], a["ld"], a["bias"], a["score"], a["ng"], a["tg"], a["gt"], a["k"],
+                 a["rn"], a["sc"], a["ids"], a["w"], None)
+
+    assert call(T=0, x=None) == 0
+    assert call(x=None) == 1 and call(ids=None) == 1 and call(w=None) == 1
+    for kw in (dict(T=-1), dict(E=0), dict(ld=63), dict(ng=0), dict(ng=7), dict(tg=0), dict(tg=9), dict(gt=0),
+               dict(gt=3), dict(k=0), dict(k=33), dict(ng=1, tg=1, k=65)):
+        assert call(**kw) == 2, kw
+    assert call(dt=3) == 3
+    assert call(x=ODD) == 4 and call(dt=2, x=BAD) == 4 and call(ids=BAD) == 4 and call(w=BAD) == 4 and call(bias=BAD) == 4
+    assert call(score=2) == 5 and call(E=1032, ld=1032) == 5 and call(E=512, ld=512, ng=128) == 5
+    assert call(E=512, ld=512, ng=1, tg=1, k=65) == 5 and call(T=1 << 31) == 5
+
+
+@pytest.mark.parametrize("down", [False, True])
+def test_experts_refusals(down):
+    lib = awq.lib()
+
+    def call(**kw):
+        a = dict(x=A, dt=0, M=4, K=256, ld=256, ids=B, w=C, k=2, q=A, s=B, z=C, E=8, N=64, g=128, act=1, y=D, ydt=2,
+                 ldy=64, ws=D, wsb=1 << 40)
+        a.update(kw)
+        head = (a["x"], a["dt"], a["M"], a["K"], a["ld"], a["ids"])
+        mid = (a["q"], a["s"], a["z"], a["E"], a["N"], a["g"])
+        tail = (a["y"], a["ydt"], a["ldy"], a["ws"], a["wsb"], None)
+        if down:
+            return lib.awq_w4a16_experts_down(*head, a["w"], a["k"], *mid, *tail)
+        return lib.awq_w4a16_experts_up(*head, a["k"], *mid, a["act"], *tail)
+
+    assert call(M=0, x=None) == 0 and call(N=0, y=None) == 0
+    for name in ("x", "ids", "q", "s", "z", "y") + (("w",) if down else ()):
+        assert call(**{name: None}) == 1, name
+    for kw in (dict(M=-1), dict(N=-2), dict(E=0), dict(k=0), dict(K=0), dict(K=200, ld=256), dict(ld=128),
+               dict(ldy=31)):
+        assert call(**kw) == 2, kw
+    assert call(dt=2) == 3 and call(ydt=5) == 3
+    assert call(x=BAD) == 4 and call(q=BAD) == 4 and call(ids=BAD) == 4 and call(y=BAD) == 4 and call(ld=260) == 4
+    assert call(s=ODD) == 4
+    assert call(g=32) == 5 and call(E=1025) == 5 and call(k=65) == 5 and call(K=1 << 18, ld=1 << 18) == 5
+    assert call(M=1 << 24) == 5                      # more than 2^24 slots
+    assert call(N=1 << 24, ldy=1 << 24) == 5         # 2^31 bytes of words per expert
+    assert call(M=1 << 22, K=4096, ld=4096, k=1) == 5  # activations past 32-bit offsets
+    op = awq.AWQ_OP_EXPERTS_DOWN if down else awq.AWQ_OP_EXPERTS_UP
+    need = awq.awq_workspace_bytes(op, 4000, 64, 256, 8, 2)
+    if need:
+        big = dict(M=4000)
+        assert call(**big, wsb=need - 1) == 6 and call(**big, ws=None) == 6 and call(**big, ws=BAD) == 6
+    if down:
+        assert call(w=BAD) == 4
+    else:
+        assert call(N=63) == 2 and call(act=2) == 5 and call(act=0, ldy=63) == 2
+    assert awq.awq_workspace_bytes(op, -1, 64, 256, 8, 2) == 0
+
+
+def test_lora_refusals():
+    f = awq.lib().awq_lora_add
+
+    def call(**kw):
+        a = dict(x=A, dt=0, M=4, K=256, ld=256, ad=B, a=A, b=B, L=3, R=16, ranks=None, sc=None, base=None, ldb=0,
+                 N=64, y=D, ydt=2, ldy=64, ws=D, wsb=1 << 40)
+        a.update(kw)
+        return f(a["x"], a["dt"], a["M"], a["K"], a["ld"], a["ad"], a["a"], a["b"], a["L"], a["R"], a["ranks"], a["sc"],
+                 a["base"], a["ldb"], a["N"], a["y"], a["ydt"], a["ldy"], a["ws"], a["wsb"], None)
+
+    assert call(M=0, x=None) == 0 and call(N=0, y=None) == 0
+    for name in ("x", "ad", "a", "b", "y"):
+        assert call(**{name: None}) == 1, name
+    for kw in (dict(M=-1), dict(N=-1), dict(L=-1), dict(K=0), dict(R=0), dict(ld=128), dict(ldy=63),
+               dict(base=A, ldb=63)):
+        assert call(**kw) == 2, kw
+    assert call(dt=2) == 3 and call(ydt=3) == 3
+    for kw in (dict(K=252, ld=256), dict(R=12), dict(ld=260), dict(x=BAD), dict(a=BAD), dict(b=BAD), dict(ad=BAD),
+               dict(ranks=BAD), dict(sc=BAD), dict(base=BAD, ldb=64), dict(y=BAD), dict(ydt=0, y=ODD)):
+        assert call(**kw) == 4, kw
+    assert call(R=264) == 5 and call(L=16385) == 5 and call(M=(1 << 24) + 1) == 5 and call(K=1 << 18, ld=1 << 18) == 5
+    need = awq.awq_workspace_bytes(awq.AWQ_OP_LORA, 4, 64, 256, 3, 16)
+    assert need >= 4 * 16 * 4
+    assert call(wsb=need - 1) == 6 and call(ws=None) == 6 and call(ws=BAD) == 6
+    assert awq.awq_workspace_bytes(awq.AWQ_OP_LORA, -1, 64, 256, 3, 16) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_names():
+    x = torch.zeros(2, 64)
+    ids = torch.zeros(2, 1, dtype=torch.int32)
+    w = (torch.zeros(1, 8, 8, dtype=torch.int32), torch.zeros(1, 8, 1, dtype=torch.float16),
+         torch.zeros(1, 8, 1, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        awq.awq_route_experts(x, 1)
+    with pytest.raises(ValueError):
+        awq.awq_w4a16_experts_up(x.half(), ids, *w, group_size=64)
+    with pytest.raises(ValueError):
+        awq.awq_w4a16_experts_up(x.half(), ids, *w, group_size=64, act="gelu")
+    with pytest.raises(ValueError):
+        awq.awq_w4a16_experts_down(x.half(), ids, torch.zeros(2, 1), *w, group_size=64)
+    with pytest.raises(ValueError):
+        awq.awq_lora_add(x.half(), ids[:, 0], torch.zeros(1, 8, 64).half(), torch.zeros(1, 4, 8).half())
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_tensors(on_gpu):
+    w = packed(stack(2, 16, 128, 128, 1))
+    x = gpu(acts(3, 128, torch.float16, 1))
+    ids = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    up = awq.awq_w4a16_experts_up
+    for args in ((x, ids.long(), *w), (x, ids.t(), *w), (x[:2], ids, *w), (x, ids[:, 0], *w), (x, ids, w[0][0], *w[1:]),
+                 (x, ids, w[0], w[1].float(), w[2]), (x, ids, w[0], w[1], w[2][:1]), (x.t(), ids, *w),
+                 (x, ids.cpu(), *w)):
+        with pytest.raises(ValueError):
+            up(*args)
+    with pytest.raises(ValueError):
+        up(x, ids, *w, y=torch.zeros((6, 15), device="cuda"))
+    with pytest.raises(ValueError):
+        awq.awq_w4a16_experts_down(x, ids, torch.zeros((3, 2), device="cuda"), *w)
+    with pytest.raises(awq.AwqError):
+        up(x.float(), ids, *w)
+    with pytest.raises(ValueError):
+        awq.awq_route_experts(x, 2, ids=torch.zeros((3, 2), dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        awq.awq_route_experts(x, 2, bias=torch.zeros(127, device="cuda"))
+    with pytest.raises(awq.AwqError):
+        awq.awq_route_experts(x, 129)
+    a = torch.zeros((2, 8, 128), dtype=torch.float16, device="cuda")
+    b = torch.zeros((2, 16, 8), dtype=torch.float16, device="cuda")
+    ad = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for kw in (dict(a=a.bfloat16()), dict(b=b[:1]), dict(adapter=ad.long()), dict(adapter=ad[:2]),
+               dict(base=torch.zeros((3, 15), device="cuda")), dict(scaling=torch.zeros(3, device="cuda")),
+               dict(ranks=torch.zeros(2, device="cuda")), dict(a=a[:, :, ::2])):
+        args = dict(x=x, adapter=ad, a=a, b=b)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            awq.awq_lora_add(**args)

@@ -14,12 +14,13 @@ import ctypes
 import torch
 
 from . import _abi
-from ._abi import (AWQ_BF16, AWQ_F16, AWQ_F32, AWQ_GROUP, AWQ_OP_ACT_STATS, AWQ_OP_GEMM,  # noqa: F401
-                   AWQ_OP_QUANTIZE, AWQ_OP_SEARCH, AwqError, lib)
+from ._abi import (AWQ_ACT_NONE, AWQ_ACT_SWIGLU, AWQ_BF16, AWQ_F16, AWQ_F32, AWQ_GROUP, AWQ_OP_ACT_STATS,  # noqa: F401
+                   AWQ_OP_EXPERTS_DOWN, AWQ_OP_EXPERTS_UP, AWQ_OP_GEMM, AWQ_OP_LORA, AWQ_OP_QUANTIZE,
+                   AWQ_OP_SEARCH, AWQ_SCORE_SIGMOID, AWQ_SCORE_SOFTMAX, AwqError, lib)
 
 __all__ = ["awq_act_stats", "awq_search_scales", "awq_search_scales_ex", "awq_quantize_pack", "awq_quantize_codes",
            "awq_w4a16_gemm", "awq_w4a16_gemm_noalloc", "awq_read_stream", "awq_fold_scales", "awq_salient_channels", "awq_workspace_bytes",
-           "AwqError", "lib"]
+           "awq_route_experts", "awq_w4a16_experts_up", "awq_w4a16_experts_down", "awq_lora_add", "AwqError", "lib"]
 
 _DT = {torch.float16: AWQ_F16, torch.bfloat16: AWQ_BF16, torch.float32: AWQ_F32}
 
@@ -263,3 +264,184 @@ def awq_fold_scales(v: torch.Tensor, s: torch.Tensor, axis: int = 1, stream=None
                                _stream(v.device, stream))
     _abi.check("awq_fold_scales", st)
     return v
+
+
+# ---- operators whose weight depends on the row ---------------------------------
+_SCORES = {"softmax": AWQ_SCORE_SOFTMAX, "sigmoid": AWQ_SCORE_SIGMOID}
+_ACTS = {"none": AWQ_ACT_NONE, "swiglu": AWQ_ACT_SWIGLU}
+
+
+def _same(t: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dtype, shape: tuple) -> int | None:
+    """Address of a contiguous tensor of this type, shape and device (None for None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {dev}")
+    return t.data_ptr()
+
+
+def _out(y: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dtype | None, rows: int,
+         cols: int) -> tuple[torch.Tensor, int]:
+    """The output (a new one of dtype if y is None) and its row stride."""
+    if y is None:
+        return torch.empty((rows, cols), dtype=dtype, device=dev), cols
+    if y.device != dev or y.dim() != 2 or tuple(y.shape) != (rows, cols) or (rows and cols > 1 and y.stride(1) != 1):
+        raise ValueError(f"{name} must be a [{rows}, {cols}] tensor with unit column stride on {dev}")
+    if dtype is not None and y.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    return y, _ld(y)
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor; a single row's is its length."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _act_rows(x: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """rows, columns and row stride of activations; a single row may have any stride."""
+    _dev(x, name)
+    if x.dim() != 2 or (x.numel() and x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    return x.shape[0], x.shape[1], _ld(x)
+
+
+def _launch(name: str, device: torch.device, stream, args: tuple) -> None:
+    """Calls the entry point with the stream appended, on the tensors' device."""
+    fn = getattr(lib(), name)
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, raw)
+    if st:
+        _abi.check(name, st)
+
+
+def _ws(op: int, dev: torch.device, ws: torch.Tensor | None, M: int, N: int, K: int, T: int,
+        n: int) -> tuple[torch.Tensor | None, int | None, int]:
+    need = lib().awq_workspace_bytes(op, M, N, K, T, n)
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif ws.device != dev:
+        raise ValueError(f"ws must be on {dev}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def awq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, score: str = "softmax",
+                      n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                      scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                      stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Which experts serve each token: (ids int32 [T, top_k], weights float32 [T, top_k]).
+
+    score is "softmax" or "sigmoid"; bias (float32 [E]) only chooses; with
+    n_group > 1 only the topk_group best groups of consecutive experts stay,
+    a group worth the sum of its group_top (1 or 2) best choices.  A logit of
+    -inf or NaN switches an expert off; where fewer than top_k are left the ids
+    are -1 with weight 0."""
+    T, E, ldl = _act_rows(logits, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    dev = logits.device
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    _launch("awq_route_experts", dev, stream,
+            (logits.data_ptr(), _DT.get(logits.dtype, -1), T, E, ldl,
+             _same(bias, "bias", dev, torch.float32, (E,)), _SCORES[score], n_group, topk_group, group_top, top_k,
+             int(bool(renormalize)), scale, _same(ids, "ids", dev, torch.int32, (T, top_k)),
+             _same(weights, "weights", dev, torch.float32, (T, top_k))))
+    return ids, weights
+
+
+def _experts(name, op, x, ids, weights, qweight, scales, zeros, act, out_dtype, y, group_size, ws, stream):
+    rows, K, ldx = _act_rows(x, "x")
+    dev = x.device
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, top_k]")
+    M, top_k = ids.shape
+    if rows != (M if weights is None else M * top_k):
+        raise ValueError("x must have one row per token (up) or per slot (down)")
+    if qweight.dim() != 3 or qweight.shape[2] * 8 != K:
+        raise ValueError("qweight must be [experts, N, K/8]")
+    if group_size not in (64, 128, 256):
+        raise ValueError("group_size must be 64, 128 or 256")
+    E, N = qweight.shape[:2]
+    G = K // group_size
+    swiglu = act == AWQ_ACT_SWIGLU
+    out_rows, cols = (M * top_k, N // 2 if swiglu else N) if weights is None else (M, N)
+    y, ldy = _out(y, "y", dev, out_dtype if y is not None else out_dtype or x.dtype, out_rows, cols)
+    ws, wsp, wsb = _ws(op, dev, ws, M, N, K, E, top_k)
+    head = (x.data_ptr(), _DT.get(x.dtype, -1), M, K, ldx, _same(ids, "ids", dev, torch.int32, (M, top_k)))
+    packed = (_same(qweight, "qweight", dev, torch.int32, (E, N, K // 8)),
+              _same(scales, "scales", dev, torch.float16, (E, N, G)), _same(zeros, "zeros", dev, torch.uint8, (E, N, G)))
+    tail = (y.data_ptr(), _DT.get(y.dtype, -1), ldy, wsp, wsb)
+    if weights is None:
+        args = head + (top_k,) + packed + (E, N, group_size, act) + tail
+    else:
+        args = head + (_same(weights, "weights", dev, torch.float32, (M, top_k)), top_k) + packed + (E, N, group_size) + tail
+    _launch(name, dev, stream, args)
+    return y
+
+
+def awq_w4a16_experts_up(x: torch.Tensor, ids: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                         zeros: torch.Tensor, act: str = "none", out_dtype: torch.dtype | None = None,
+                         y: torch.Tensor | None = None, group_size: int = AWQ_GROUP,
+                         ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Each token's row through its experts' packed weights, [M top_k, N] (act
+    "swiglu": silu(first N/2 rows) * the other N/2, [M top_k, N/2]).
+
+    x [M, K]; ids int32 [M, top_k] (outside [0, experts): no expert, a row of
+    zeros); qweight [experts, N, K/8], scales and zeros [experts, N, K/g] as
+    awq_quantize_pack writes them for the [experts N, K] rows."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    return _experts("awq_w4a16_experts_up", AWQ_OP_EXPERTS_UP, x, ids, None, qweight, scales, zeros, _ACTS[act],
+                    out_dtype, y, group_size, ws, stream)
+
+
+def awq_w4a16_experts_down(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, qweight: torch.Tensor,
+                           scales: torch.Tensor, zeros: torch.Tensor, out_dtype: torch.dtype | None = None,
+                           y: torch.Tensor | None = None, group_size: int = AWQ_GROUP,
+                           ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[m] = sum_j weights[m, j] W_{ids[m, j]} x[m top_k + j], [M, N]; x has one
+    row per (token, choice), as awq_w4a16_experts_up writes them."""
+    return _experts("awq_w4a16_experts_down", AWQ_OP_EXPERTS_DOWN, x, ids, weights, qweight, scales, zeros, None,
+                    out_dtype, y, group_size, ws, stream)
+
+
+def awq_lora_add(x: torch.Tensor, adapter: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                 base: torch.Tensor | None = None, scaling: torch.Tensor | None = None,
+                 ranks: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                 y: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """base + scaling[i] b[i] (a[i] x) per row with i = adapter[row]; rows whose
+    adapter is outside [0, adapters) are base (0 without one).
+
+    x [M, K]; adapter int32 [M]; a [adapters, R, K] and b [adapters, N, R] of
+    x's dtype; ranks int32 [adapters] (None: R); scaling float32 [adapters].
+    base has the output's dtype and may be y itself."""
+    M, K, ldx = _act_rows(x, "x")
+    dev = x.device
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a must be [adapters, R, K] and b [adapters, N, R]")
+    L, R = a.shape[:2]
+    N = b.shape[1]
+    want = out_dtype or (base.dtype if base is not None else x.dtype if y is None else y.dtype)
+    y, ldy = _out(y, "y", dev, want, M, N)
+    ldb, basep = 0, None
+    if base is not None:
+        base, ldb = _out(base, "base", dev, y.dtype, M, N)
+        basep = base.data_ptr()
+    ws, wsp, wsb = _ws(_abi.AWQ_OP_LORA, dev, ws, M, N, K, L, R)
+    _launch("awq_lora_add", dev, stream,
+            (x.data_ptr(), _DT.get(x.dtype, -1), M, K, ldx, _same(adapter, "adapter", dev, torch.int32, (M,)),
+             _same(a, "a", dev, x.dtype, (L, R, K)), _same(b, "b", dev, x.dtype, (L, N, R)), L, R,
+             _same(ranks, "ranks", dev, torch.int32, (L,)), _same(scaling, "scaling", dev, torch.float32, (L,)),
+             basep, ldb, N, y.data_ptr(), _DT.get(y.dtype, -1), ldy, wsp, wsb))
+    return y

@@ -17,12 +17,17 @@ STATUS_NAMES = {0: "AWQ_OK", 1: "AWQ_ERR_NULL", 2: "AWQ_ERR_SHAPE", 3: "AWQ_ERR_
                 7: "AWQ_ERR_HIP"}
 AWQ_F16, AWQ_BF16, AWQ_F32 = 0, 1, 2
 AWQ_OP_ACT_STATS, AWQ_OP_SEARCH, AWQ_OP_QUANTIZE, AWQ_OP_GEMM = 0, 1, 2, 3
+AWQ_OP_EXPERTS_UP, AWQ_OP_EXPERTS_DOWN, AWQ_OP_LORA = 4, 5, 6
+AWQ_SCORE_SOFTMAX, AWQ_SCORE_SIGMOID = 0, 1
+AWQ_ACT_NONE, AWQ_ACT_SWIGLU = 0, 1
+AWQ_MAX_EXPERTS, AWQ_MAX_TOP_K, AWQ_MAX_RANK = 1024, 64, 256
 AWQ_GROUP = 128
 AWQ_MAX_ALPHA = 64
 AWQ_NOALLOC_SCRATCH_BYTES = 128 << 20
 
 # exported symbol -> (restype, argtypes)
 _i64, _p, _i, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_f = ctypes.c_float
 SIGNATURES = {
     "awq_abi_version": (ctypes.c_int, []),
     "awq_status_str": (ctypes.c_char_p, [_i]),
@@ -40,6 +45,13 @@ SIGNATURES = {
     "awq_fold_scales": (_i, [_p, _i, _i64, _i64, _i64, _p, _i, _p]),
     "awq_w4a16_gemm_noalloc": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p, _i64, _i, _p, _p, _i, _i64,
                                     _p]),
+    "awq_route_experts": (_i, [_p, _i, _i64, _i64, _i64, _p, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p]),
+    "awq_w4a16_experts_up": (_i, [_p, _i, _i64, _i64, _i64, _p, _i, _p, _p, _p, _i64, _i64, _i, _i, _p, _i,
+                                  _i64, _p, _sz, _p]),
+    "awq_w4a16_experts_down": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _i, _p, _p, _p, _i64, _i64, _i, _p, _i,
+                                    _i64, _p, _sz, _p]),
+    "awq_lora_add": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p, _i64, _i64, _p, _p, _p, _i64, _i64, _p, _i,
+                          _i64, _p, _sz, _p]),
     "awq_read_stream": (_i, [_p, _i64, _i, _i, _p, _p]),
 }
 

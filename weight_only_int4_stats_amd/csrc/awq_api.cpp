@@ -47,6 +47,11 @@ size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T
       return awq::search_ws_bytes((int)AWQ_BF16, N, K, T, n_alpha < 1 ? 1 : n_alpha);
     case AWQ_OP_QUANTIZE: return 0;
     case AWQ_OP_GEMM: return awq::gemm_ws_bytes(M, N, K, 64);   // the smallest group needs the most
+    case AWQ_OP_EXPERTS_UP:
+    case AWQ_OP_EXPERTS_DOWN:
+      if (M < 1 || N < 1 || K < 1 || T < 1 || n_alpha < 1) return 0;
+      return awq::experts_ws_bytes(op == AWQ_OP_EXPERTS_DOWN, M, N, K, T, n_alpha);
+    case AWQ_OP_LORA: return awq::lora_ws_bytes(M, K, T, n_alpha);
   }
   return 0;
 }

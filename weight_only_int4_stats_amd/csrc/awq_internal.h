@@ -93,6 +93,56 @@ hipError_t launch_skinny_st_chunked(const void* x, int xdt, int64_t M, int64_t K
                                     int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
                                     hipStream_t st);
 
+// ---- expert routing (k_route.hip) --------------------------------------------
+hipError_t launch_route(const void* logits, int dt, int64_t T, int64_t E, int64_t ldl, const float* bias,
+                        int sigmoid, int n_group, int topk_group, int group_top, int top_k, int renorm,
+                        float scale, int32_t* ids, float* weights, hipStream_t st);
+
+// ---- routed W4A16 products (k_experts.hip) ------------------------------------
+enum : int { EXPERTS_UP = 0, EXPERTS_SWIGLU = 1, EXPERTS_DOWN = 2 };
+
+// One call of awq_w4a16_experts_up / _down with checked arguments.
+struct ExpertsCall {
+  int mode;                    // EXPERTS_*
+  const uint16_t* x;
+  int xdt;
+  int64_t M, K, ldx;
+  const int32_t* ids;
+  const float* weights;        // down
+  int top_k;
+  const uint32_t* qw;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  int64_t E, N;
+  int group;
+  void* y;
+  int ydt;
+  int64_t ldy;
+};
+// of the sizes alone (M, K, top_k, E, N; every group size)
+size_t experts_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k);
+hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st);
+
+// ---- per-row low-rank adapters (k_lora.hip) -----------------------------------
+struct LoraCall {
+  const uint16_t* x;
+  int xdt;
+  int64_t M, K, ldx;
+  const int32_t* adapter;
+  const uint16_t* a;
+  const uint16_t* b;
+  int64_t n_adapters, R;
+  const int32_t* ranks;
+  const float* scaling;
+  const void* base;
+  int64_t ldb, N;
+  void* y;
+  int ydt;
+  int64_t ldy;
+};
+size_t lora_ws_bytes(int64_t M, int64_t K, int64_t n_adapters, int64_t R);
+hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st);
+
 // ---- plain streaming read (k_stream.hip): bytes a multiple of 1024, blocks
 // of 1024 threads, unroll 1, 2, 4 or 8 units in flight per wave
 hipError_t launch_read_stream(const void* p, int64_t bytes, int blocks, int unroll, uint32_t* block_xor,

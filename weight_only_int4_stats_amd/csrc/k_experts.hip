@@ -1,0 +1,420 @@
+// Routed W4A16 products for few rows per expert (include/awq.h,
+// awq_w4a16_experts_up / _down): decode steps and small batches, where the
+// product is bound by the chosen experts' packed words.
+//
+//   z[slot][n] = sum_g D[n][g] sum_{k in g} (q[n][k] - z[n][g]) x[row(slot)][k]
+//
+//  * A block of 8 waves owns 64 weight rows of one expert (four 16-row tiles
+//    of two waves each; a wave takes every other 256-channel pair of its
+//    tile's rows) and finds the expert's slots itself by scanning the ids, 16
+//    at a time, so a call needs no sorting launch and an expert without rows
+//    costs one scan.
+//  * With fewer slots than experts the grid has one block row per slot: the
+//    first slot of an expert takes all of its rows.  Otherwise one per expert.
+//  * v_mfma_f32_16x16x32_f16 with the tokens as the first operand (16 rows)
+//    and 16 weight rows as the second: a result lane holds the weight row whose
+//    words it read, so the group's step enters once, in fp32.
+//  * The codes reach the matrix cores as fp16 subnormals (word & 0x000F000F is
+//    q 2^-24, word & 0x00F000F0 is q 2^-20; odd nibbles meet activations
+//    divided by 16), and the zero point as the group's starting accumulator,
+//    -z 2^-24 sum_k X_k: five vector instructions per eight codes, products
+//    of exact integers.
+//  * The packed words come through a per-wave LDS ring by LDS DMA, a pair of
+//    128-channel units (16 rows x 128 bytes, whole lines) per step, two pairs
+//    ahead.
+//  * The rows' activations are staged in LDS a chunk of channels at a time (as
+//    many channels as fit: 2048 for up to 8 rows, 1024 for 16), as fp16 scaled
+//    by a power of two per (row, 128 channels), in the order the unpack yields,
+//    with the group sums; beside them the chunk's steps and zero points.
+#include "awq_device.h"
+#include "awq_internal.h"
+#include "k_experts.h"
+#include "k_rows_f16.h"
+
+#include <type_traits>
+
+namespace awqk {
+
+constexpr int kFewWaves = 8;
+constexpr int kFewThreads = kFewWaves * 64;
+constexpr int kFewTiles = 4;                       // 16-row tiles per block
+constexpr int kFewSlices = kFewWaves / kFewTiles;  // waves per tile
+constexpr int kFewPairs = 2;                       // 256-channel pairs in flight per wave
+constexpr int kFewX = 16 * (1024 + 8) * 2;         // staged activations, bytes
+constexpr int kFewUnits = 16;                      // groups (of 64 or 128 channels) per chunk, at most
+constexpr int kFewPitch = kFewUnits + 1;           // staged (step, zero) pairs per row
+constexpr int kFewOSums = kFewX;
+constexpr int kFewOPinv = kFewOSums + kFewUnits * 16 * 4;
+constexpr int kFewOMeta = kFewOPinv + kFewUnits * 16 * 4;
+constexpr int kFewORing = kFewOMeta + kFewTiles * 16 * kFewPitch * 8;
+constexpr int kFewOList = kFewORing + kFewWaves * kFewPairs * 2048;
+constexpr int kFewLds = kFewOList + 16 * 4 + kFewWaves * 4 + 32;   // two blocks per compute unit
+static_assert(kFewLds <= 80 * 1024, "two blocks per compute unit");
+static_assert(kFewORing % 16 == 0 && kFewOList % 16 == 0, "LDS regions");
+
+struct FewArgs {
+  const uint16_t* x;
+  int64_t K, ldx, N, ldy;
+  const int32_t* ids;
+  const uint32_t* qw;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  void* y;
+  int S, E, top_k, glog, ydt, by_slot, groups;
+};
+
+// One packed word -> 8 codes as fp16 subnormals, in the order (0,4 | 2,6 | 1,5 | 3,7).
+__device__ __forceinline__ u32x4 few_unpack(uint32_t w) {
+  const uint32_t w8 = w >> 8;
+  return u32x4{w & 0x000F000Fu, w8 & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x00F000F0u};
+}
+
+// 16 bytes per lane into LDS (LDS DMA, non-temporal; an offset past the
+// buffer's range writes 0).  Issued from asm, so the compiler adds no wait of
+// its own before the LDS reads: the caller waits on the vector memory counter.
+__device__ __forceinline__ void few_dma16(const i32x4& rs, uint32_t lds, uint32_t voff) {
+  uint32_t keep;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen nt lds\n\ts_mov_b32 m0, %0"
+               : "=&s"(keep) : "s"(lds), "v"(voff), "s"(rs) : "memory");
+}
+
+__device__ __forceinline__ void store_out(void* y, int ydt, int64_t i, float v) {
+  if (ydt == DT_F32) reinterpret_cast<float*>(y)[i] = v;
+  else if (ydt == DT_F16) reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_f16_bits(v);
+  else reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_bf16_bits(v);
+}
+
+// MODE: EXPERTS_UP (y per slot), EXPERTS_SWIGLU (y per slot, silu(gate) * up),
+// EXPERTS_DOWN (x per slot; y is the fp32 partial row of the slot).
+template <int DT, int MODE, bool G64>
+__global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rl = lane & 15, b = lane >> 4;
+  uint16_t* xs = reinterpret_cast<uint16_t*>(lds);
+  float* red = reinterpret_cast<float*>(lds);                    // after the last chunk
+  float* sums = reinterpret_cast<float*>(lds + kFewOSums);       // [group][16 rows]
+  float* pinv = reinterpret_cast<float*>(lds + kFewOPinv);       // [128-channel unit][16 rows]
+  float2* meta = reinterpret_cast<float2*>(lds + kFewOMeta);     // [weight row][kFewPitch]
+  int* list = reinterpret_cast<int*>(lds + kFewOList);           // [16] slots
+  int* wcount = list + 16;                                       // [kFewWaves]
+
+  const int grp = blockIdx.y;
+  const int64_t halfN = p.N >> 1;
+  // ---- the expert
+  int e;
+  bool zero_rows = false;                                        // this block row zeroes the slots without an expert
+  if (grp == p.groups) {
+    e = -1;
+    zero_rows = true;
+  } else {
+    e = p.by_slot ? p.ids[grp] : grp;
+    if (e < 0 || e >= p.E) return;
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  // ---- how many slots each wave's share of the ids holds
+  const int s0 = (int)((int64_t)wv * p.S / kFewWaves), s1 = (int)((int64_t)(wv + 1) * p.S / kFewWaves);
+  if (zero_rows) {
+    const int64_t cols = MODE == EXPERTS_SWIGLU ? halfN : p.N;
+    const int64_t per = MODE == EXPERTS_SWIGLU ? 8 * kFewTiles : 16 * kFewTiles;
+    const int64_t c = (int64_t)blockIdx.x * per + (lane % per);
+    for (int s = s0; s < s1; ++s) {
+      const int id = p.ids[s];
+      if ((id < 0 || id >= p.E) && lane < per && c < cols) store_out(p.y, p.ydt, (int64_t)s * p.ldy + c, 0.0f);
+    }
+    return;
+  }
+  int cnt = 0;
+  for (int s = s0; s < s1; s += 64) cnt += __popcll(__ballot(s + lane < s1 && p.ids[s + lane < s1 ? s + lane : s0] == e));
+  if (lane == 0) wcount[wv] = cnt;
+  __syncthreads();
+  int rows = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) {
+    const int c = wcount[w];
+    if (w < wv) before += c;
+    rows += c;
+  }
+  rows = __builtin_amdgcn_readfirstlane(rows);
+  if (rows == 0) return;
+
+  // ---- the block's weight rows: tile t holds rows tile_row(t) .. + 15 of the
+  // expert, rows_in(t) of them; with SwiGLU tiles alternate gate, up
+  const int64_t ncols = MODE == EXPERTS_SWIGLU ? halfN : p.N;
+  const int tile = wv / kFewSlices, slice = wv % kFewSlices;
+  auto tile_col = [&](int t) {
+    return MODE == EXPERTS_SWIGLU ? ((int64_t)blockIdx.x * (kFewTiles / 2) + (t >> 1)) * 16
+                                  : ((int64_t)blockIdx.x * kFewTiles + t) * 16;
+  };
+  auto rows_in = [&](int t) {
+    const int64_t left = ncols - tile_col(t);
+    return (int)(left < 0 ? 0 : left < 16 ? left : 16);
+  };
+  auto tile_row = [&](int t) {                     // within [0, N); for an empty tile any row
+    const int64_t c = tile_col(t);
+    return (c < ncols ? c : 0) + (MODE == EXPERTS_SWIGLU && (t & 1) ? halfN : 0);
+  };
+  const uint32_t rowb = (uint32_t)(p.K >> 1);      // bytes of a packed row
+  const int GW = (int)(p.K >> p.glog);             // groups per row
+  const int64_t wrow = (int64_t)e * p.N + tile_row(tile);
+  const i32x4 wrs = rsrc4(reinterpret_cast<const uint8_t*>(p.qw) + wrow * rowb, (uint32_t)rows_in(tile) * rowb);
+  const uint32_t ring = __builtin_amdgcn_readfirstlane(lds_addr(lds) + kFewORing + (uint32_t)wv * kFewPairs * 2048);
+  // A pair is two copies (rows 0..7 and 8..15, 128 bytes of each row) with
+  // chunk c of row r' of half h at 16-byte slot 8 r' + (c ^ (r'/2 + 4 h)).
+  const int dq = lane >> 3, ds = lane & 7;
+  const uint32_t dv0 = (uint32_t)dq * rowb + (uint32_t)((ds ^ (dq >> 1)) * 16);
+  const uint32_t dv1 = (uint32_t)(dq + 8) * rowb + (uint32_t)((ds ^ ((dq >> 1) | 4)) * 16);
+  const int npair = (int)((p.K + 255) >> 8);       // the last may hold 64, 128 or 192 channels
+  auto issue = [&](int slot, int q) {
+    const uint32_t off = __builtin_amdgcn_readfirstlane(q < npair ? (uint32_t)q * 128 : kBufferOob);
+    // past the row's end the copy takes the next row's words (or zeros): they
+    // meet activations staged as zeros
+    few_dma16(wrs, ring + (uint32_t)slot * 2048, dv0 + off);
+    few_dma16(wrs, ring + (uint32_t)slot * 2048 + 1024, dv1 + off);
+  };
+  const uint8_t* wlds = lds + kFewORing + wv * kFewPairs * 2048 + (rl >> 3) * 1024 + (rl & 7) * 128;
+  const int wsw = ((rl & 7) >> 1) | ((rl >> 3) << 2);
+
+  for (int r0 = 0; r0 < rows; r0 += 16) {
+    const int nr = rows - r0 < 16 ? rows - r0 : 16;
+    // ---- the pass's slots: ranks r0 .. r0 + nr - 1 among the expert's
+    int run = before;
+    for (int s = s0; s < s1; s += 64) {
+      const bool hit = s + lane < s1 && p.ids[s + lane < s1 ? s + lane : s0] == e;
+      const uint64_t m = __ballot(hit);
+      const int rank = run + __popcll(m & ((1ull << lane) - 1));
+      if (hit && rank >= r0 && rank < r0 + 16) list[rank - r0] = s + lane;
+      run += __popcll(m);
+    }
+    __syncthreads();
+    if (r0 == 0 && p.by_slot && list[0] != grp) return;          // another slot's block has this expert
+
+    // channels per chunk: whole pairs, as many as fit the staged activations and the steps
+    int kc = (kFewX / 2 / nr - 8) & ~255;
+    constexpr int kcap = G64 ? kFewUnits * 64 : kFewUnits * 128;
+    kc = kc < kcap ? kc : kcap;
+    const int kall = (int)((p.K + 255) & ~(int64_t)255);
+    kc = kc < kall ? kc : kall;
+    const int pitch = kc + 8;
+
+    int q = slice;                                 // this wave's next pair
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    int done = 0;                                  // pairs this wave has used: slot done % kFewPairs
+    for (int c0 = 0; c0 < (int)p.K; c0 += kc) {
+      if (c0) __syncthreads();                     // every wave has left the last chunk
+      const int kn = (int)p.K - c0 < kc ? (int)p.K - c0 : kc;    // channels in this chunk
+      // ---- the rows' activations: piece i = (row i / P, 8 channels i % P), P
+      // pieces per row rounded up to whole pairs (the tail is zeros)
+      const int P = ((kn + 255) & ~255) >> 3;
+      for (int i = tid; i < nr * P; i += kFewThreads) {
+        const int r = i / P, k8 = i - r * P;
+        const int slot = list[r];
+        const int64_t xrow = MODE == EXPERTS_DOWN ? slot : slot / p.top_k;
+        u32x4 raw = {0, 0, 0, 0};
+        if (k8 * 8 < kn) raw = ldg128(p.x + xrow * p.ldx + c0 + k8 * 8);
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[2 * c] = lo_f32<DT>(raw[c]);
+          v[2 * c + 1] = hi_f32<DT>(raw[c]);
+        }
+        float am = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) am = fmaxf(am, fabsf(v[c]));
+        am = fmaxf(am, quad_xor1(am));
+        am = fmaxf(am, quad_xor2(am));
+        am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
+        am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x140, 0xF, 0xF, false)));
+        const int pe = pow2_exp_for(am);
+        uint32_t h[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) h[c] = f32_to_f16_bits(ldexpf(v[c], (c & 1) ? pe - 4 : pe));
+        const u32x4 o = {h[0] | (h[4] << 16), h[2] | (h[6] << 16), h[1] | (h[5] << 16), h[3] | (h[7] << 16)};
+        *reinterpret_cast<u32x4*>(xs + r * pitch + k8 * 8) = o;
+        // sum of the operands exactly as the products see them
+        const f16x2 one2 = as_f16x2(0x3C003C00u), sixteen2 = as_f16x2(0x4C004C00u);
+        float s = __builtin_amdgcn_fdot2(as_f16x2(o[0]), one2, 0.0f, false);
+        s = __builtin_amdgcn_fdot2(as_f16x2(o[1]), one2, s, false);
+        s = __builtin_amdgcn_fdot2(as_f16x2(o[2]), sixteen2, s, false);
+        s = __builtin_amdgcn_fdot2(as_f16x2(o[3]), sixteen2, s, false);
+        s = ldexpf(s, -24);
+        s += quad_xor1(s);
+        s += quad_xor2(s);
+        s += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x141, 0xF, 0xF, false));
+        if constexpr (!G64)
+          s += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x140, 0xF, 0xF, false));
+        if ((lane & (G64 ? 7 : 15)) == 0) sums[(k8 >> (G64 ? 3 : 4)) * 16 + r] = s;
+        if ((lane & 15) == 0) pinv[(k8 >> 4) * 16 + r] = ldexpf(1.0f, -pe);
+      }
+      // ---- the chunk's steps (times 2^24, undoing the codes' 2^-24) and zero
+      // points, one (row, group) each; past the row's groups a step of 0
+      const int ug = G64 ? 64 : 128;
+      const int ng = ((kn + 255) & ~255) / ug;     // staged groups (of 64 or 128 channels)
+      for (int i = tid; i < kFewTiles * 16 * kFewUnits; i += kFewThreads) {
+        const int r = i / kFewUnits, u = i % kFewUnits;
+        const int t = r >> 4, g = (c0 + u * ug) >> p.glog;
+        float2 m = make_float2(0.0f, 0.0f);
+        if (u < ng && g < GW && (r & 15) < rows_in(t)) {
+          const int64_t at = ((int64_t)e * p.N + tile_row(t) + (r & 15)) * GW + g;
+          m = make_float2(ldexpf(f16_to_f32(p.scales[at]), 24), (float)p.zeros[at]);
+        }
+        if (u < ng) meta[r * kFewPitch + u] = m;
+      }
+      if (c0 == 0) {
+#pragma unroll
+        for (int d = 0; d < kFewPairs; ++d) issue(d, q + d * kFewSlices);
+      }
+      __syncthreads();
+      // ---- this wave's pairs of the chunk
+      const int qend = (c0 + kc) >> 8;
+      const uint16_t* xrow = xs + (rl < nr ? rl : nr - 1) * pitch;   // rows past nr repeat one; dropped
+      const float2* mrow = meta + (tile * 16 + rl) * kFewPitch;
+      for (; q < npair && q < qend; q += kFewSlices) {
+        const int slot = done & (kFewPairs - 1);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (kFewPairs - 1)) : "memory");
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int g = 2 * q + u - (c0 >> 7);     // unit within the chunk
+          const f32x4 pv = *reinterpret_cast<const f32x4*>(pinv + g * 16 + 4 * b);
+          if constexpr (!G64) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(wlds + slot * 2048 + (((4 * u + b) ^ wsw) * 16));
+            const uint16_t* xp = xrow + 128 * g + 32 * b;
+            const f32x4 sv = *reinterpret_cast<const f32x4*>(sums + g * 16 + 4 * b);
+            const float2 md = mrow[g];
+            f32x4 part;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) part[v] = -md.y * sv[v];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp + 8 * i), few_unpack(w[i]), part);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(md.x * pv[v], part[v], acc[v]);
+          } else {
+            // words 2 b, 2 b + 1 of each 64-channel half: chunk (4 u + 2 h + b / 2), half b % 2
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint2 w = *reinterpret_cast<const uint2*>(
+                  wlds + slot * 2048 + (((4 * u + 2 * h + (b >> 1)) ^ wsw) * 16) + (b & 1) * 8);
+              const uint16_t* xp = xrow + 128 * g + 64 * h + 16 * b;
+              const f32x4 sv = *reinterpret_cast<const f32x4*>(sums + (2 * g + h) * 16 + 4 * b);
+              const float2 md = mrow[2 * g + h];
+              f32x4 part;
+#pragma unroll
+              for (int v = 0; v < 4; ++v) part[v] = -md.y * sv[v];
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp), few_unpack(w.x), part);
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp + 8), few_unpack(w.y), part);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(md.x * pv[v], part[v], acc[v]);
+            }
+          }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // the slot's words are in registers
+        issue(slot, q + kFewPairs * kFewSlices);
+        ++done;
+      }
+    }
+    // ---- a tile's waves meet in LDS, in slice order
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");             // the ring's last (empty) copies
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[wv * 256 + (4 * b + v) * 16 + rl] = acc[v];
+    __syncthreads();
+    constexpr int kOut = MODE == EXPERTS_SWIGLU ? kFewTiles / 2 : kFewTiles;   // output tiles
+    for (int i = tid; i < nr * kOut * 16; i += kFewThreads) {
+      const int r = i / (kOut * 16), c = i % (kOut * 16);
+      const int t = c >> 4, cl = c & 15;
+      auto tile_sum = [&](int tl) {
+        float s = red[tl * kFewSlices * 256 + r * 16 + cl];
+#pragma unroll
+        for (int k = 1; k < kFewSlices; ++k) s += red[(tl * kFewSlices + k) * 256 + r * 16 + cl];
+        return s;
+      };
+      const int64_t col = (int64_t)blockIdx.x * kOut * 16 + c;
+      if (col >= ncols) continue;
+      float out;
+      if constexpr (MODE == EXPERTS_SWIGLU) out = swiglu(tile_sum(2 * t), tile_sum(2 * t + 1));
+      else out = tile_sum(t);
+      const int64_t at = (int64_t)list[r] * p.ldy + col;
+      if constexpr (MODE == EXPERTS_DOWN) reinterpret_cast<float*>(p.y)[at] = out;
+      else store_out(p.y, p.ydt, at, out);
+    }
+    __syncthreads();                               // red and list are free again
+  }
+}
+
+// y[m] = sum_j w[m][j] P[m top_k + j] over the slots that have an expert, in
+// slot order.  Four outputs per thread (P's rows are padded to a multiple of 4).
+template <int YDT>
+__global__ __launch_bounds__(256) void k_experts_combine(const float* __restrict__ P, int64_t ldp,
+                                                         const int32_t* __restrict__ ids,
+                                                         const float* __restrict__ weights, int top_k, int E,
+                                                         int64_t M, int64_t N, void* __restrict__ y, int64_t ldy) {
+  const int64_t n4 = (N + 3) >> 2;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * n4; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / n4, n = (i - m * n4) * 4;
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < top_k; ++j) {
+      const int id = ids[m * top_k + j];
+      if (id < 0 || id >= E) continue;
+      const float w = weights[m * top_k + j];
+      const f32x4 v = *reinterpret_cast<const f32x4*>(P + (m * top_k + j) * ldp + n);
+  #pragma unroll
+      for (int c = 0; c < 4; ++c) s[c] = __builtin_fmaf(w, v[c], s[c]);
+    }
+  #pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (n + c < N) store_out(y, YDT, m * ldy + n + c, s[c]);
+  }
+}
+
+template <int DT, int MODE>
+void few_launch(const FewArgs& a, const dim3& grid, hipStream_t st) {
+  if (a.glog == 6) hipLaunchKernelGGL((k_experts_few<DT, MODE, true>), grid, dim3(kFewThreads), kFewLds, st, a);
+  else hipLaunchKernelGGL((k_experts_few<DT, MODE, false>), grid, dim3(kFewThreads), kFewLds, st, a);
+}
+
+}  // namespace awqk
+
+namespace awq {
+using namespace awqk;
+
+static int64_t partial_ld(int64_t N) { return (N + 3) / 4 * 4; }
+
+size_t experts_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k) {
+  size_t b = 0;
+  if (down) b += align_up((size_t)(M * top_k) * (size_t)partial_ld(N) * 4, 256);
+  return b;
+}
+
+hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
+  const int64_t S = c.M * c.top_k;
+  FewArgs a{c.x, c.K, c.ldx, c.N, c.ldy, c.ids, c.qw, c.scales, c.zeros, c.y, (int)S, (int)c.E, c.top_k,
+            c.group == 64 ? 6 : c.group == 128 ? 7 : 8, c.ydt, S < c.E, (int)(S < c.E ? S : c.E)};
+  if (c.mode == EXPERTS_DOWN) {
+    a.y = ws;
+    a.ldy = partial_ld(c.N);
+  }
+  const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
+  const int64_t per = c.mode == EXPERTS_SWIGLU ? 8 * kFewTiles : 16 * kFewTiles;
+  const dim3 grid((unsigned)((cols + per - 1) / per), (unsigned)(a.groups + (c.mode == EXPERTS_DOWN ? 0 : 1)));
+  const bool bf = c.xdt == DT_BF16;
+  if (c.mode == EXPERTS_UP) bf ? few_launch<DT_BF16, EXPERTS_UP>(a, grid, st) : few_launch<DT_F16, EXPERTS_UP>(a, grid, st);
+  else if (c.mode == EXPERTS_SWIGLU) bf ? few_launch<DT_BF16, EXPERTS_SWIGLU>(a, grid, st) : few_launch<DT_F16, EXPERTS_SWIGLU>(a, grid, st);
+  else bf ? few_launch<DT_BF16, EXPERTS_DOWN>(a, grid, st) : few_launch<DT_F16, EXPERTS_DOWN>(a, grid, st);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || c.mode != EXPERTS_DOWN) return e;
+  int64_t blocks = (c.M * ((c.N + 3) / 4) + 255) / 256;
+  if (blocks > (1 << 20)) blocks = 1 << 20;
+  auto combine = [&](auto y) {
+    hipLaunchKernelGGL((k_experts_combine<decltype(y)::value>), dim3((unsigned)blocks), dim3(256), 0, st, (const float*)ws,
+                       a.ldy, c.ids, c.weights, c.top_k, (int)c.E, c.M, c.N, c.y, c.ldy);
+  };
+  if (c.ydt == DT_F32) combine(std::integral_constant<int, DT_F32>{});
+  else if (c.ydt == DT_F16) combine(std::integral_constant<int, DT_F16>{});
+  else combine(std::integral_constant<int, DT_BF16>{});
+  return hipGetLastError();
+}
+
+}  // namespace awq
