@@ -563,9 +563,9 @@ def test_experts_refusals(down):
     assert call(M=1 << 22, K=4096, ld=4096, k=1) == 5  # activations past 32-bit offsets
     op = awq.AWQ_OP_EXPERTS_DOWN if down else awq.AWQ_OP_EXPERTS_UP
     need = awq.awq_workspace_bytes(op, 4000, 64, 256, 8, 2)
-    if need:
-        big = dict(M=4000)
-        assert call(**big, wsb=need - 1) == 6 and call(**big, ws=None) == 6 and call(**big, ws=BAD) == 6
+    assert need > 0
+    big = dict(M=4000)
+    assert call(**big, wsb=need - 1) == 6 and call(**big, ws=None) == 6 and call(**big, ws=BAD) == 6
     if down:
         assert call(w=BAD) == 4
     else:

@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libawq_gfx950.so")
 SOURCES = ["awq_api.cpp", "k_act_stats.hip", "k_quantize.hip", "k_search.hip", "k_gram.hip", "k_w4a16.hip",
            "k_gemv1.hip", "k_fold.hip", "k_salient.hip", "awq_noalloc.hip", "k_mid.hip", "k_skinny.hip", "k_stream.hip",
-           "awq_routed.cpp", "k_route.hip", "k_groups.hip", "k_experts.hip", "k_lora.hip"]
+           "awq_routed.cpp", "k_route.hip", "k_groups.hip", "k_experts.hip",
+           "k_experts_gemm.hip", "k_lora.hip"]
 ARCH = "gfx950"
 
 

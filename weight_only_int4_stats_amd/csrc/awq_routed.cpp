@@ -34,6 +34,8 @@ awq_status experts(int mode, const void* x, awq_dtype xdt, int64_t M, int64_t K,
   if (!x || !ids || !qweight || !scales || !zeros || !y || (down && !weights)) return AWQ_ERR_NULL;
   if (M > kMaxRows / top_k || N > ((int64_t)1 << 32) / K - 1) return AWQ_ERR_UNSUPPORTED;
   if ((down ? M * top_k : M) * K * 2 >= (int64_t)1 << 31) return AWQ_ERR_UNSUPPORTED;
+  // block count of the tiled product (at least 32 rows x 64 columns each)
+  if ((M * top_k / 32 + E + 2) * (N / 64 + 1) > kMaxBlocks) return AWQ_ERR_UNSUPPORTED;
   if (ldx % 8 != 0 || !aligned(x, 16) || !aligned(qweight, 16) || !aligned(scales, 2) || !aligned(ids, 4) ||
       !aligned(y, bytes_of(ydt)) || (down && !aligned(weights, 4)))
     return AWQ_ERR_ALIGN;

@@ -10,6 +10,29 @@ using awq::EXPERTS_DOWN;
 using awq::EXPERTS_SWIGLU;
 using awq::EXPERTS_UP;
 
+// -z 2^-9 as fp16, twice.
+__device__ __forceinline__ uint32_t experts_nz(uint32_t z) {
+  return f32_to_f16_bits(-(float)z * 0x1p-9f) * 0x10001u;
+}
+
+// One packed word -> 8 operands (q - z) 2^-9 in fp16, exact, in the order
+// (0,4 | 2,6 | 1,5 | 3,7).  The masked nibbles are fp16 subnormals, q 2^-24 or
+// (odd nibbles) q 2^-20; a packed fma scales and subtracts.
+__device__ __forceinline__ u32x4 experts_unpack(uint32_t w, uint32_t nz) {
+  const f16x2 c15 = as_f16x2(0x78007800u), c11 = as_f16x2(0x68006800u), n = as_f16x2(nz);   // 2^15, 2^11
+  const uint32_t w8 = w >> 8;
+  return u32x4{__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w & 0x000F000Fu), c15, n)),
+               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w8 & 0x000F000Fu), c15, n)),
+               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w & 0x00F000F0u), c11, n)),
+               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w8 & 0x00F000F0u), c11, n))};
+}
+
+__device__ __forceinline__ void store_out(void* y, int ydt, int64_t i, float v) {
+  if (ydt == DT_F32) reinterpret_cast<float*>(y)[i] = v;
+  else if (ydt == DT_F16) reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_f16_bits(v);
+  else reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_bf16_bits(v);
+}
+
 // silu(gate) * up in fp32; a gate of -inf gives -0 up, the limit.
 __device__ __forceinline__ float swiglu(float gate, float up) {
   const float s = gate / (1.0f + expf(-gate));
@@ -17,3 +40,11 @@ __device__ __forceinline__ float swiglu(float gate, float up) {
 }
 
 }  // namespace awqk
+
+namespace awq {
+
+// The tiled form (k_experts_gemm.hip), into out [slots][ldo] (down: fp32).
+size_t experts_gemm_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k);
+hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, void* ws, hipStream_t st);
+
+}  // namespace awq

@@ -14,18 +14,19 @@
 //  * v_mfma_f32_16x16x32_f16 with the tokens as the first operand (16 rows)
 //    and 16 weight rows as the second: a result lane holds the weight row whose
 //    words it read, so the group's step enters once, in fp32.
-//  * The codes reach the matrix cores as fp16 subnormals (word & 0x000F000F is
-//    q 2^-24, word & 0x00F000F0 is q 2^-20; odd nibbles meet activations
-//    divided by 16), and the zero point as the group's starting accumulator,
-//    -z 2^-24 sum_k X_k: five vector instructions per eight codes, products
-//    of exact integers.
+//  * The codes reach the matrix cores as (q - z) 2^-9, exact normal fp16 values:
+//    the masked nibbles read as subnormals (q 2^-24 or q 2^-20), then one packed
+//    fma per pair.  Feeding the subnormals themselves and taking z out with
+//    the rows' sums saves those four of nine instructions per word, but the
+//    matrix cores align a subnormal operand by its nominal exponent and drop
+//    the low bits of its products: 2e-5 of a result against 2e-7.
 //  * The packed words come through a per-wave LDS ring by LDS DMA, a pair of
 //    128-channel units (16 rows x 128 bytes, whole lines) per step, two pairs
 //    ahead.
 //  * The rows' activations are staged in LDS a chunk of channels at a time (as
 //    many channels as fit: 2048 for up to 8 rows, 1024 for 16), as fp16 scaled
-//    by a power of two per (row, 128 channels), in the order the unpack yields,
-//    with the group sums; beside them the chunk's steps and zero points.
+//    by a power of two per (row, 128 channels), in the order the unpack yields;
+//    beside them the chunk's steps and zero points.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_experts.h"
@@ -43,8 +44,7 @@ constexpr int kFewPairs = 2;                       // 256-channel pairs in fligh
 constexpr int kFewX = 16 * (1024 + 8) * 2;         // staged activations, bytes
 constexpr int kFewUnits = 16;                      // groups (of 64 or 128 channels) per chunk, at most
 constexpr int kFewPitch = kFewUnits + 1;           // staged (step, zero) pairs per row
-constexpr int kFewOSums = kFewX;
-constexpr int kFewOPinv = kFewOSums + kFewUnits * 16 * 4;
+constexpr int kFewOPinv = kFewX;
 constexpr int kFewOMeta = kFewOPinv + kFewUnits * 16 * 4;
 constexpr int kFewORing = kFewOMeta + kFewTiles * 16 * kFewPitch * 8;
 constexpr int kFewOList = kFewORing + kFewWaves * kFewPairs * 2048;
@@ -63,12 +63,6 @@ struct FewArgs {
   int S, E, top_k, glog, ydt, by_slot, groups;
 };
 
-// One packed word -> 8 codes as fp16 subnormals, in the order (0,4 | 2,6 | 1,5 | 3,7).
-__device__ __forceinline__ u32x4 few_unpack(uint32_t w) {
-  const uint32_t w8 = w >> 8;
-  return u32x4{w & 0x000F000Fu, w8 & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x00F000F0u};
-}
-
 // 16 bytes per lane into LDS (LDS DMA, non-temporal; an offset past the
 // buffer's range writes 0).  Issued from asm, so the compiler adds no wait of
 // its own before the LDS reads: the caller waits on the vector memory counter.
@@ -76,12 +70,6 @@ __device__ __forceinline__ void few_dma16(const i32x4& rs, uint32_t lds, uint32_
   uint32_t keep;
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen nt lds\n\ts_mov_b32 m0, %0"
                : "=&s"(keep) : "s"(lds), "v"(voff), "s"(rs) : "memory");
-}
-
-__device__ __forceinline__ void store_out(void* y, int ydt, int64_t i, float v) {
-  if (ydt == DT_F32) reinterpret_cast<float*>(y)[i] = v;
-  else if (ydt == DT_F16) reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_f16_bits(v);
-  else reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_bf16_bits(v);
 }
 
 // MODE: EXPERTS_UP (y per slot), EXPERTS_SWIGLU (y per slot, silu(gate) * up),
@@ -95,9 +83,8 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
   const int rl = lane & 15, b = lane >> 4;
   uint16_t* xs = reinterpret_cast<uint16_t*>(lds);
   float* red = reinterpret_cast<float*>(lds);                    // after the last chunk
-  float* sums = reinterpret_cast<float*>(lds + kFewOSums);       // [group][16 rows]
   float* pinv = reinterpret_cast<float*>(lds + kFewOPinv);       // [128-channel unit][16 rows]
-  float2* meta = reinterpret_cast<float2*>(lds + kFewOMeta);     // [weight row][kFewPitch]
+  uint2* meta = reinterpret_cast<uint2*>(lds + kFewOMeta);       // [weight row][kFewPitch]: step 2^9, -z 2^-9
   int* list = reinterpret_cast<int*>(lds + kFewOList);           // [16] slots
   int* wcount = list + 16;                                       // [kFewWaves]
 
@@ -230,35 +217,22 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
         const int pe = pow2_exp_for(am);
         uint32_t h[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) h[c] = f32_to_f16_bits(ldexpf(v[c], (c & 1) ? pe - 4 : pe));
+        for (int c = 0; c < 8; ++c) h[c] = f32_to_f16_bits(ldexpf(v[c], pe));
         const u32x4 o = {h[0] | (h[4] << 16), h[2] | (h[6] << 16), h[1] | (h[5] << 16), h[3] | (h[7] << 16)};
         *reinterpret_cast<u32x4*>(xs + r * pitch + k8 * 8) = o;
-        // sum of the operands exactly as the products see them
-        const f16x2 one2 = as_f16x2(0x3C003C00u), sixteen2 = as_f16x2(0x4C004C00u);
-        float s = __builtin_amdgcn_fdot2(as_f16x2(o[0]), one2, 0.0f, false);
-        s = __builtin_amdgcn_fdot2(as_f16x2(o[1]), one2, s, false);
-        s = __builtin_amdgcn_fdot2(as_f16x2(o[2]), sixteen2, s, false);
-        s = __builtin_amdgcn_fdot2(as_f16x2(o[3]), sixteen2, s, false);
-        s = ldexpf(s, -24);
-        s += quad_xor1(s);
-        s += quad_xor2(s);
-        s += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x141, 0xF, 0xF, false));
-        if constexpr (!G64)
-          s += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x140, 0xF, 0xF, false));
-        if ((lane & (G64 ? 7 : 15)) == 0) sums[(k8 >> (G64 ? 3 : 4)) * 16 + r] = s;
         if ((lane & 15) == 0) pinv[(k8 >> 4) * 16 + r] = ldexpf(1.0f, -pe);
       }
-      // ---- the chunk's steps (times 2^24, undoing the codes' 2^-24) and zero
+      // ---- the chunk's steps (times 2^9, undoing the operands' 2^-9) and zero
       // points, one (row, group) each; past the row's groups a step of 0
       const int ug = G64 ? 64 : 128;
       const int ng = ((kn + 255) & ~255) / ug;     // staged groups (of 64 or 128 channels)
       for (int i = tid; i < kFewTiles * 16 * kFewUnits; i += kFewThreads) {
         const int r = i / kFewUnits, u = i % kFewUnits;
         const int t = r >> 4, g = (c0 + u * ug) >> p.glog;
-        float2 m = make_float2(0.0f, 0.0f);
+        uint2 m = make_uint2(0u, 0u);
         if (u < ng && g < GW && (r & 15) < rows_in(t)) {
           const int64_t at = ((int64_t)e * p.N + tile_row(t) + (r & 15)) * GW + g;
-          m = make_float2(ldexpf(f16_to_f32(p.scales[at]), 24), (float)p.zeros[at]);
+          m = make_uint2(__float_as_uint(f16_to_f32(p.scales[at]) * 512.0f), experts_nz(p.zeros[at]));
         }
         if (u < ng) meta[r * kFewPitch + u] = m;
       }
@@ -270,7 +244,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
       // ---- this wave's pairs of the chunk
       const int qend = (c0 + kc) >> 8;
       const uint16_t* xrow = xs + (rl < nr ? rl : nr - 1) * pitch;   // rows past nr repeat one; dropped
-      const float2* mrow = meta + (tile * 16 + rl) * kFewPitch;
+      const uint2* mrow = meta + (tile * 16 + rl) * kFewPitch;
       for (; q < npair && q < qend; q += kFewSlices) {
         const int slot = done & (kFewPairs - 1);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (kFewPairs - 1)) : "memory");
@@ -281,16 +255,13 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
           if constexpr (!G64) {
             const u32x4 w = *reinterpret_cast<const u32x4*>(wlds + slot * 2048 + (((4 * u + b) ^ wsw) * 16));
             const uint16_t* xp = xrow + 128 * g + 32 * b;
-            const f32x4 sv = *reinterpret_cast<const f32x4*>(sums + g * 16 + 4 * b);
-            const float2 md = mrow[g];
-            f32x4 part;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) part[v] = -md.y * sv[v];
+            const uint2 md = mrow[g];
+            f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              part = mfma16h(*reinterpret_cast<const u32x4*>(xp + 8 * i), few_unpack(w[i]), part);
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp + 8 * i), experts_unpack(w[i], md.y), part);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(md.x * pv[v], part[v], acc[v]);
+            for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(__uint_as_float(md.x) * pv[v], part[v], acc[v]);
           } else {
             // words 2 b, 2 b + 1 of each 64-channel half: chunk (4 u + 2 h + b / 2), half b % 2
 #pragma unroll
@@ -298,15 +269,12 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
               const uint2 w = *reinterpret_cast<const uint2*>(
                   wlds + slot * 2048 + (((4 * u + 2 * h + (b >> 1)) ^ wsw) * 16) + (b & 1) * 8);
               const uint16_t* xp = xrow + 128 * g + 64 * h + 16 * b;
-              const f32x4 sv = *reinterpret_cast<const f32x4*>(sums + (2 * g + h) * 16 + 4 * b);
-              const float2 md = mrow[2 * g + h];
-              f32x4 part;
+              const uint2 md = mrow[2 * g + h];
+              f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp), experts_unpack(w.x, md.y), part);
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp + 8), experts_unpack(w.y, md.y), part);
 #pragma unroll
-              for (int v = 0; v < 4; ++v) part[v] = -md.y * sv[v];
-              part = mfma16h(*reinterpret_cast<const u32x4*>(xp), few_unpack(w.x), part);
-              part = mfma16h(*reinterpret_cast<const u32x4*>(xp + 8), few_unpack(w.y), part);
-#pragma unroll
-              for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(md.x * pv[v], part[v], acc[v]);
+              for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(__uint_as_float(md.x) * pv[v], part[v], acc[v]);
             }
           }
         }
@@ -382,34 +350,44 @@ using namespace awqk;
 
 static int64_t partial_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
+// Few rows per expert (this file) or tiles (k_experts_gemm.hip).
+static bool few_rows(int64_t S, int64_t E) { return S <= 16 * E && S <= 4096; }
+
+static size_t partial_bytes(bool down, int64_t S, int64_t N) {
+  return down ? align_up((size_t)S * (size_t)partial_ld(N) * 4, 256) : 0;
+}
+
 size_t experts_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k) {
-  size_t b = 0;
-  if (down) b += align_up((size_t)(M * top_k) * (size_t)partial_ld(N) * 4, 256);
-  return b;
+  const int64_t S = M * top_k;
+  return partial_bytes(down, S, N) + (few_rows(S, E) ? 0 : experts_gemm_ws_bytes(down, M, N, K, E, top_k));
 }
 
 hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
   const int64_t S = c.M * c.top_k;
-  FewArgs a{c.x, c.K, c.ldx, c.N, c.ldy, c.ids, c.qw, c.scales, c.zeros, c.y, (int)S, (int)c.E, c.top_k,
-            c.group == 64 ? 6 : c.group == 128 ? 7 : 8, c.ydt, S < c.E, (int)(S < c.E ? S : c.E)};
-  if (c.mode == EXPERTS_DOWN) {
-    a.y = ws;
-    a.ldy = partial_ld(c.N);
+  const bool down = c.mode == EXPERTS_DOWN;
+  void* out = down ? ws : c.y;                     // down: fp32 rows per slot first
+  const int64_t ldo = down ? partial_ld(c.N) : c.ldy;
+  hipError_t e;
+  if (!few_rows(S, c.E)) {
+    e = launch_experts_gemm(c, out, ldo, reinterpret_cast<char*>(ws) + partial_bytes(down, S, c.N), st);
+  } else {
+    const FewArgs a{c.x, c.K, c.ldx, c.N, ldo, c.ids, c.qw, c.scales, c.zeros, out, (int)S, (int)c.E, c.top_k,
+                    c.group == 64 ? 6 : c.group == 128 ? 7 : 8, c.ydt, S < c.E, (int)(S < c.E ? S : c.E)};
+    const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
+    const int64_t per = c.mode == EXPERTS_SWIGLU ? 8 * kFewTiles : 16 * kFewTiles;
+    const dim3 grid((unsigned)((cols + per - 1) / per), (unsigned)(a.groups + (down ? 0 : 1)));
+    const bool bf = c.xdt == DT_BF16;
+    if (c.mode == EXPERTS_UP) bf ? few_launch<DT_BF16, EXPERTS_UP>(a, grid, st) : few_launch<DT_F16, EXPERTS_UP>(a, grid, st);
+    else if (c.mode == EXPERTS_SWIGLU) bf ? few_launch<DT_BF16, EXPERTS_SWIGLU>(a, grid, st) : few_launch<DT_F16, EXPERTS_SWIGLU>(a, grid, st);
+    else bf ? few_launch<DT_BF16, EXPERTS_DOWN>(a, grid, st) : few_launch<DT_F16, EXPERTS_DOWN>(a, grid, st);
+    e = hipGetLastError();
   }
-  const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
-  const int64_t per = c.mode == EXPERTS_SWIGLU ? 8 * kFewTiles : 16 * kFewTiles;
-  const dim3 grid((unsigned)((cols + per - 1) / per), (unsigned)(a.groups + (c.mode == EXPERTS_DOWN ? 0 : 1)));
-  const bool bf = c.xdt == DT_BF16;
-  if (c.mode == EXPERTS_UP) bf ? few_launch<DT_BF16, EXPERTS_UP>(a, grid, st) : few_launch<DT_F16, EXPERTS_UP>(a, grid, st);
-  else if (c.mode == EXPERTS_SWIGLU) bf ? few_launch<DT_BF16, EXPERTS_SWIGLU>(a, grid, st) : few_launch<DT_F16, EXPERTS_SWIGLU>(a, grid, st);
-  else bf ? few_launch<DT_BF16, EXPERTS_DOWN>(a, grid, st) : few_launch<DT_F16, EXPERTS_DOWN>(a, grid, st);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || c.mode != EXPERTS_DOWN) return e;
+  if (e != hipSuccess || !down) return e;
   int64_t blocks = (c.M * ((c.N + 3) / 4) + 255) / 256;
   if (blocks > (1 << 20)) blocks = 1 << 20;
   auto combine = [&](auto y) {
     hipLaunchKernelGGL((k_experts_combine<decltype(y)::value>), dim3((unsigned)blocks), dim3(256), 0, st, (const float*)ws,
-                       a.ldy, c.ids, c.weights, c.top_k, (int)c.E, c.M, c.N, c.y, c.ldy);
+                       ldo, c.ids, c.weights, c.top_k, (int)c.E, c.M, c.N, c.y, c.ldy);
   };
   if (c.ydt == DT_F32) combine(std::integral_constant<int, DT_F32>{});
   else if (c.ydt == DT_F16) combine(std::integral_constant<int, DT_F16>{});

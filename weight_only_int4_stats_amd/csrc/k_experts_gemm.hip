@@ -1,0 +1,399 @@
+// Routed W4A16 products for many rows per expert (include/awq.h,
+// awq_w4a16_experts_up / _down): prefills, where the matrix cores bound the
+// product.
+//
+//   z[slot][n] = sum_g D[n][g] sum_{k in g} (q[n][k] - z[n][g]) x[row(slot)][k]
+//
+//  * k_experts_prep (one launch): block 0 sorts the slots by expert and lists
+//    the row tiles; the others convert the activation rows to fp16 (scaled by a
+//    power of two per row, in the order the unpack yields), lay the steps and
+//    zero points out group by group, and zero the output rows of slots without
+//    an expert.
+//  * k_experts_gemm: tiles of BM = 32 MB rows of one expert x 128 weight rows,
+//    4 waves (2 x 2, each 16 MB x 64).  64 channels per stage, three LDS stages
+//    filled by LDS DMA two stages ahead; the rows of a tile are gathered by the
+//    copies' addresses.  v_mfma_f32_16x16x32_f16 multiplies the activations
+//    with the exact integers (q - z) 2^-9; a group's sums are folded into the
+//    result with its step, in fp32, when the group ends.  Rounding step (q - z)
+//    to fp16 instead would save the fold and a second set of accumulators, and
+//    cost 1e-4 of every result.
+//  * With SwiGLU a tile's columns alternate 16 gate rows and their 16 up rows,
+//    so both meet in one lane.  down writes fp32 rows per slot; the weighted sum
+//    over a token's slots is k_experts_combine's.
+//  * The tiles of one expert are ordered 8 row tiles at a time, rows fastest,
+//    and each L2 slice takes a contiguous eighth of the order.
+#include "awq_device.h"
+#include "awq_internal.h"
+#include "k_experts.h"
+#include "k_groups.h"
+#include "k_rows_f16.h"
+
+#include <type_traits>
+
+namespace awqk {
+
+constexpr int kGemmN = 128;                        // weight rows per tile
+constexpr int kGemmK = 64;                         // channels per stage
+constexpr int kGemmGroupM = 8;                     // row tiles taken together
+constexpr int kXcd = 8;                            // L2 slices
+
+struct GemmArgs {
+  const uint16_t* x;
+  int64_t K, ldx, N, ldy;
+  const int32_t* ids;
+  const uint32_t* qw;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  void* y;
+  int64_t xrows;
+  int S, E, top_k, group, ydt, vec;
+  // workspace
+  uint16_t* xq;                                    // [xrows][K]
+  int* pexp;                                       // [xrows]
+  uint32_t* ctab;                                  // [E][G][N]: step | -z 2^-9 << 16
+  GroupPlan plan;
+  // first block of each part of the preparation
+  int b_rows, b_consts, b_zero;
+};
+
+// One wave converts one row: fp16(x 2^p), p from the row's maximum, each
+// 8-channel piece in the order (0,4 | 2,6 | 1,5 | 3,7).
+template <int DT>
+__device__ __forceinline__ void prep_row(const GemmArgs& p, int64_t row) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t* src = p.x + row * p.ldx;
+  uint16_t* dst = p.xq + row * p.K;
+  const int n8 = (int)(p.K >> 3);
+  constexpr int kKeep = 8;                         // pieces per lane held in registers (K up to 4096)
+  u32x4 raw[kKeep];
+  float am = 0.0f;
+  auto piece_max = [&](const u32x4& w) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) am = fmaxf(am, fmaxf(fabsf(lo_f32<DT>(w[c])), fabsf(hi_f32<DT>(w[c]))));
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int c = lane + 64 * i;
+    raw[i] = c < n8 ? ldg128(src + c * 8) : u32x4{0, 0, 0, 0};
+    piece_max(raw[i]);
+  }
+  for (int c = lane + 64 * kKeep; c < n8; c += 64) piece_max(ldg128(src + c * 8));
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) am = fmaxf(am, __shfl_xor(am, off));
+  const int pe = pow2_exp_for(am);
+  if (lane == 0) p.pexp[row] = pe;
+  auto convert = [&](int c, const u32x4& w) {
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[2 * j] = f32_to_f16_bits(ldexpf(lo_f32<DT>(w[j]), pe));
+      h[2 * j + 1] = f32_to_f16_bits(ldexpf(hi_f32<DT>(w[j]), pe));
+    }
+    *reinterpret_cast<u32x4*>(dst + c * 8) = u32x4{h[0] | (h[4] << 16), h[2] | (h[6] << 16), h[1] | (h[5] << 16), h[3] | (h[7] << 16)};
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int c = lane + 64 * i;
+    if (c < n8) convert(c, raw[i]);
+  }
+  for (int c = lane + 64 * kKeep; c < n8; c += 64) convert(c, ldg128(src + c * 8));
+}
+
+template <int DT>
+__global__ __launch_bounds__(kPlanThreads) void k_experts_prep(const GemmArgs p, int tile_rows, int64_t cols) {
+  extern __shared__ int prep_lds[];
+  const int bid = blockIdx.x, tid = threadIdx.x;
+  if (bid < p.b_rows) {
+    group_plan_block(p.ids, p.S, p.E, tile_rows, p.plan, prep_lds);
+  } else if (bid < p.b_consts) {
+    const int64_t row = (int64_t)(bid - p.b_rows) * 16 + (tid >> 6);
+    if (row < p.xrows) prep_row<DT>(p, row);
+  } else if (bid < p.b_zero) {
+    const int64_t n = (int64_t)(bid - p.b_consts) * kPlanThreads + tid;   // row of the [E N] stack
+    if (n >= (int64_t)p.E * p.N) return;
+    const int G = (int)(p.K / p.group);
+    const int64_t e = n / p.N, r = n - e * p.N;
+    const uint16_t* s = p.scales + n * G;
+    const uint8_t* z = p.zeros + n * G;
+    uint32_t* c = p.ctab + e * G * p.N + r;
+#pragma unroll 8
+    for (int g = 0; g < G; ++g) c[(int64_t)g * p.N] = (uint32_t)s[g] | (experts_nz(z[g]) & 0xFFFF0000u);
+  } else {
+    const int64_t slot = (int64_t)(bid - p.b_zero) * 16 + (tid >> 6);
+    if (slot >= p.S) return;
+    const int id = p.ids[slot];
+    if (id >= 0 && id < p.E) return;
+    for (int64_t c = tid & 63; c < cols; c += 64) store_out(p.y, p.ydt, slot * p.ldy + c, 0.0f);
+  }
+}
+
+template <int MODE, int MB, int SPG>
+__global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
+  constexpr int BM = 32 * MB;
+  constexpr int kA = BM * kGemmK * 2, kB = kGemmN * 32, kC = 1024, kStage = kA + kB + kC;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wv >> 1, wn = wv & 1;
+  const int rl = lane & 15, b = lane >> 4;
+
+  // ---- the tile
+  const int64_t ncols = MODE == EXPERTS_SWIGLU ? p.N >> 1 : p.N;
+  constexpr int kCols = MODE == EXPERTS_SWIGLU ? kGemmN / 2 : kGemmN;     // output columns per tile
+  const int nt = (int)((ncols + kCols - 1) / kCols);
+  const int64_t total = (int64_t)p.plan.ntile[1] * nt;
+  const int64_t per = (total + kXcd - 1) / kXcd;
+  const int64_t in = blockIdx.x / kXcd, at = (int64_t)(blockIdx.x % kXcd) * per + in;
+  if (in >= per || at >= total) return;
+  const GroupTile q0 = p.plan.tiles[at / nt];
+  const int64_t rem = at - (int64_t)q0.before * nt;
+  const int gi = (int)(rem / (kGemmGroupM * nt));
+  const int gm = q0.tiles - gi * kGemmGroupM < kGemmGroupM ? q0.tiles - gi * kGemmGroupM : kGemmGroupM;
+  const int in_group = (int)(rem - (int64_t)gi * kGemmGroupM * nt);
+  const GroupTile q = p.plan.tiles[q0.before + gi * kGemmGroupM + in_group % gm];
+  const int64_t c0 = (int64_t)(in_group / gm) * kCols;
+  const int e = __builtin_amdgcn_readfirstlane(q.group);
+  const int rows = __builtin_amdgcn_readfirstlane(q.rows);
+  const int* perm = p.plan.perm + __builtin_amdgcn_readfirstlane(q.first);
+  auto xrow = [&](int slot) { return MODE == EXPERTS_DOWN ? slot : slot / p.top_k; };
+  // weight row of tile column c, -1 past the last
+  auto wrow = [&](int c) -> int64_t {
+    if constexpr (MODE == EXPERTS_SWIGLU) {
+      const int64_t n = c0 + (c >> 5) * 16 + (c & 15);
+      return n < ncols ? n + ((c >> 4) & 1) * ncols : -1;
+    } else {
+      return c0 + c < ncols ? c0 + c : -1;
+    }
+  };
+
+  // ---- copies: A rows of 128 bytes, 8 per copy, chunk c of row r at c ^ (r & 7);
+  // B per 32 columns the first then the last 16 bytes of each; C four entries a lane
+  const int64_t G = p.K / p.group;
+  const i32x4 ars = rsrc4(p.xq, (uint32_t)(p.xrows * p.K * 2));
+  const i32x4 brs = rsrc4(reinterpret_cast<const uint8_t*>(p.qw) + (int64_t)e * p.N * (p.K >> 1), (uint32_t)(p.N * (p.K >> 1)));
+  const i32x4 crs = rsrc4(p.ctab + (int64_t)e * G * p.N, (uint32_t)(G * p.N * 4));
+  uint32_t aoff[MB];
+#pragma unroll
+  for (int u = 0; u < MB; ++u) {
+    const int r = 8 * (MB * wv + u) + (lane >> 3);
+    aoff[u] = r < rows ? (uint32_t)((int64_t)xrow(perm[r]) * p.K * 2) + (uint32_t)(((lane & 7) ^ (r & 7)) * 16) : kBufferOob;
+  }
+  const int64_t bn = wrow(32 * wv + (lane & 31));
+  const uint32_t boff = bn < 0 ? kBufferOob : (uint32_t)(bn * (p.K >> 1)) + (uint32_t)((lane >> 5) * 16);
+  const int64_t cn = lane < 32 ? wrow(4 * lane) : -1;
+  const uint32_t coff = cn < 0 ? kBufferOob : (uint32_t)(cn * 4);
+  const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  const int S = (int)(p.K / kGemmK);
+  auto issue = [&](int s, int buf) {
+    const uint32_t lb = lbase + (uint32_t)buf * kStage;
+#pragma unroll
+    for (int u = 0; u < MB; ++u) dma16(ars, lb + (uint32_t)(MB * wv + u) * 1024, aoff[u], (uint32_t)s * 128);
+    dma16(brs, lb + kA + (uint32_t)wv * 1024, boff, (uint32_t)s * 32);
+    if (wv == 0) dma16(crs, lb + kA + kB, coff, (uint32_t)(s / SPG) * (uint32_t)(p.N * 4));
+  };
+
+  f32x4 acc[MB][4], part[MB][4];
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  issue(0, 0);
+  if (S > 1) issue(1, 1);
+  int buf = 0;
+  for (int s0 = 0; s0 < S; s0 += SPG) {
+    uint32_t cw[4];
+#pragma unroll
+    for (int i = 0; i < SPG; ++i) {
+      const int s = s0 + i;
+      // stage s has arrived when at most stage s + 1's copies are in flight
+      if (s + 1 < S) {
+        if (wv == 0) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(MB + 2));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(MB + 1));
+      } else {
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+      }
+      lds_barrier();
+      const int buf2 = buf >= 1 ? buf - 1 : 2;     // (buf + 2) mod 3: left by stage s - 1
+      if (s + 2 < S) issue(s + 2, buf2);
+      const uint8_t* base = lds + buf * kStage;
+      uint2 w[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int col = wn * 64 + n * 16 + rl;
+        w[n] = *reinterpret_cast<const uint2*>(base + kA + (col >> 5) * 1024 + (b >> 1) * 512 + (col & 31) * 16 + (b & 1) * 8);
+        if (i == 0) cw[n] = *reinterpret_cast<const uint32_t*>(base + kA + kB + col * 4);
+      }
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        u32x4 a[MB];
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+          const int r = wm * 16 * MB + m * 16 + rl;
+          a[m] = *reinterpret_cast<const u32x4*>(base + r * 128 + (((2 * b + st) ^ (r & 7)) * 16));
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t nz = (cw[n] >> 16) * 0x10001u;
+          const u32x4 o = experts_unpack(st ? w[n].y : w[n].x, nz);
+#pragma unroll
+          for (int m = 0; m < MB; ++m) {
+            if (i == 0 && st == 0) part[m][n] = mfma16h(a[m], o, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            else part[m][n] = mfma16h(a[m], o, part[m][n]);
+          }
+        }
+      }
+      buf = buf == 2 ? 0 : buf + 1;
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float d = f16_to_f32(cw[n] & 0xFFFFu) * 512.0f;
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[m][n][v] = __builtin_fmaf(d, part[m][n][v], acc[m][n][v]);
+    }
+  }
+
+  // ---- epilogue: 16 rows at a time through the wave's LDS area, then whole
+  // row pieces.  Result lane: column l % 16, rows 4 b + v.
+  __syncthreads();                                 // every wave is done with the stages
+  constexpr int kW = MODE == EXPERTS_SWIGLU ? 32 : 64;                    // outputs per row of the wave
+  float* stg = reinterpret_cast<float*>(lds) + wv * 16 * (kW + 4);
+  constexpr int kL = kW / 4;                       // lanes per row, four outputs each
+#pragma unroll
+  for (int m = 0; m < MB; ++m) {
+    const int r0 = wm * 16 * MB + m * 16;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int r = r0 + 4 * b + v;
+      const int pe = r < rows ? -p.pexp[xrow(perm[r])] : 0;
+      float* d = stg + (4 * b + v) * (kW + 4) + rl;
+      if constexpr (MODE == EXPERTS_SWIGLU) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) d[16 * h] = swiglu(ldexpf(acc[m][2 * h][v], pe), ldexpf(acc[m][2 * h + 1][v], pe));
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) d[16 * n] = ldexpf(acc[m][n][v], pe);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): the wave's writes landed
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 16 * kL / 64; ++i) {
+      const int r = i * (64 / kL) + lane / kL, c = (lane % kL) * 4;
+      const f32x4 o = *reinterpret_cast<const f32x4*>(stg + r * (kW + 4) + c);
+      if (r0 + r >= rows) continue;
+      const int64_t col = c0 + wn * kW + c, pos = (int64_t)perm[r0 + r] * p.ldy + col;
+      if (MODE == EXPERTS_DOWN || p.ydt == DT_F32) {
+        float* y = reinterpret_cast<float*>(p.y) + pos;
+        if (p.vec && col + 4 <= ncols) *reinterpret_cast<f32x4*>(y) = o;
+        else
+          for (int j = 0; j < 4; ++j)
+            if (col + j < ncols) y[j] = o[j];
+      } else {
+        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + pos;
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = p.ydt == DT_F16 ? f32_to_f16_bits(o[j]) : f32_to_bf16_bits(o[j]);
+        if (p.vec && col + 4 <= ncols) *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        else
+          for (int j = 0; j < 4; ++j)
+            if (col + j < ncols) y[j] = (uint16_t)h[j];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int MODE, int MB>
+void gemm_launch(const GemmArgs& a, const dim3& grid, hipStream_t st) {
+  constexpr size_t lds = 3 * (32 * MB * kGemmK * 2 + kGemmN * 32 + 1024);
+  if (a.group == 64) hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 1>), grid, dim3(256), lds, st, a);
+  else if (a.group == 128) hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 2>), grid, dim3(256), lds, st, a);
+  else hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 4>), grid, dim3(256), lds, st, a);
+}
+
+}  // namespace awqk
+
+namespace awq {
+using namespace awqk;
+
+// Rows per tile for S slots over E experts.
+static int gemm_tile_rows(int64_t S, int64_t E) {
+  const int64_t avg = S / E;
+  return avg > 96 ? 128 : avg > 40 ? 64 : 32;
+}
+
+struct GemmSpace {
+  size_t xq, pexp, ctab, plan, total;
+};
+static GemmSpace gemm_space(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k, int64_t group) {
+  const int64_t S = M * top_k, xrows = down ? S : M;
+  GemmSpace g;
+  g.xq = 0;
+  g.pexp = g.xq + align_up((size_t)xrows * (size_t)K * 2, 256);
+  g.ctab = g.pexp + align_up((size_t)xrows * 4, 256);
+  g.plan = g.ctab + align_up((size_t)E * (size_t)N * (size_t)(K / group) * 4, 256);
+  g.total = g.plan + group_plan_bytes(S, E, gemm_tile_rows(S, E));
+  return g;
+}
+
+size_t experts_gemm_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k) {
+  return gemm_space(down, M, N, K, E, top_k, 64).total;     // the smallest group needs the most
+}
+
+hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, void* ws, hipStream_t st) {
+  const bool down = c.mode == EXPERTS_DOWN;
+  const int64_t S = c.M * c.top_k;
+  const GemmSpace g = gemm_space(down, c.M, c.N, c.K, c.E, c.top_k, c.group);
+  const int tile = gemm_tile_rows(S, c.E);
+  char* w = reinterpret_cast<char*>(ws);
+  GemmArgs a{};
+  a.x = c.x;
+  a.K = c.K;
+  a.ldx = c.ldx;
+  a.N = c.N;
+  a.ldy = ldo;
+  a.ids = c.ids;
+  a.qw = c.qw;
+  a.scales = c.scales;
+  a.zeros = c.zeros;
+  a.y = out;
+  a.xrows = down ? S : c.M;
+  a.S = (int)S;
+  a.E = (int)c.E;
+  a.top_k = c.top_k;
+  a.group = c.group;
+  a.ydt = down ? DT_F32 : c.ydt;
+  const size_t es = a.ydt == DT_F32 ? 4 : 2;
+  a.vec = ldo % 4 == 0 && (uintptr_t)out % (4 * es) == 0;
+  a.xq = reinterpret_cast<uint16_t*>(w + g.xq);
+  a.pexp = reinterpret_cast<int*>(w + g.pexp);
+  a.ctab = reinterpret_cast<uint32_t*>(w + g.ctab);
+  a.plan = group_plan_at(w + g.plan, S, c.E, tile);
+  a.b_rows = 1;
+  a.b_consts = a.b_rows + (int)((a.xrows + 15) / 16);
+  a.b_zero = a.b_consts + (int)((c.E * c.N + kPlanThreads - 1) / kPlanThreads);
+  const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
+  const unsigned pb = (unsigned)(a.b_zero + (down ? 0 : (S + 15) / 16));
+  if (c.xdt == DT_F16) hipLaunchKernelGGL((k_experts_prep<DT_F16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
+  else hipLaunchKernelGGL((k_experts_prep<DT_BF16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t per = c.mode == EXPERTS_SWIGLU ? kGemmN / 2 : kGemmN;
+  const int64_t tiles = group_tiles_max(S, c.E, tile) * ((cols + per - 1) / per);
+  const dim3 grid((unsigned)((tiles + kXcd - 1) / kXcd * kXcd));
+  auto go = [&](auto mode) {
+    constexpr int MODE = decltype(mode)::value;
+    if (tile == 128) gemm_launch<MODE, 4>(a, grid, st);
+    else if (tile == 64) gemm_launch<MODE, 2>(a, grid, st);
+    else gemm_launch<MODE, 1>(a, grid, st);
+  };
+  if (c.mode == EXPERTS_UP) go(std::integral_constant<int, EXPERTS_UP>{});
+  else if (c.mode == EXPERTS_SWIGLU) go(std::integral_constant<int, EXPERTS_SWIGLU>{});
+  else go(std::integral_constant<int, EXPERTS_DOWN>{});
+  return hipGetLastError();
+}
+
+}  // namespace awq
