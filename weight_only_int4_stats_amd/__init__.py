@@ -10,6 +10,7 @@ functions raise if the library is missing or a tensor is not on the GPU.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -275,9 +276,23 @@ def _same(t: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dty
     """Address of a contiguous tensor of this type, shape and device (None for None)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {dev}")
     return t.data_ptr()
+
+
+def _act_rows(x: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """rows, columns and row stride of a 2-D tensor; a single row's stride is its length."""
+    _dev(x, name)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    rows, cols = x.shape
+    if x.is_contiguous():
+        return rows, cols, cols
+    ld, step = x.stride()
+    if rows and cols > 1 and step != 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    return rows, cols, ld if rows > 1 else cols
 
 
 def _out(y: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dtype | None, rows: int,
@@ -285,34 +300,20 @@ def _out(y: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dtyp
     """The output (a new one of dtype if y is None) and its row stride."""
     if y is None:
         return torch.empty((rows, cols), dtype=dtype, device=dev), cols
-    if y.device != dev or y.dim() != 2 or tuple(y.shape) != (rows, cols) or (rows and cols > 1 and y.stride(1) != 1):
-        raise ValueError(f"{name} must be a [{rows}, {cols}] tensor with unit column stride on {dev}")
-    if dtype is not None and y.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    return y, _ld(y)
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Row stride of a 2-D tensor; a single row's is its length."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _act_rows(x: torch.Tensor, name: str) -> tuple[int, int, int]:
-    """rows, columns and row stride of activations; a single row may have any stride."""
-    _dev(x, name)
-    if x.dim() != 2 or (x.numel() and x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit column stride")
-    return x.shape[0], x.shape[1], _ld(x)
+    r, c, ld = _act_rows(y, name)
+    if (r, c) != (rows, cols) or y.device != dev or (dtype is not None and y.dtype is not dtype):
+        raise ValueError(f"{name} must be a {dtype or y.dtype} tensor of shape [{rows}, {cols}] on {dev}")
+    return y, ld
 
 
 def _launch(name: str, device: torch.device, stream, args: tuple) -> None:
     """Calls the entry point with the stream appended, on the tensors' device."""
     fn = getattr(lib(), name)
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -321,15 +322,22 @@ def _launch(name: str, device: torch.device, stream, args: tuple) -> None:
         _abi.check(name, st)
 
 
+@functools.lru_cache(maxsize=4096)
+def _ws_need(op: int, M: int, N: int, K: int, T: int, n: int) -> int:
+    """awq_workspace_bytes of the operators below, which is a function of the sizes alone."""
+    return lib().awq_workspace_bytes(op, M, N, K, T, n)
+
+
 def _ws(op: int, dev: torch.device, ws: torch.Tensor | None, M: int, N: int, K: int, T: int,
         n: int) -> tuple[torch.Tensor | None, int | None, int]:
-    need = lib().awq_workspace_bytes(op, M, N, K, T, n)
     if ws is None:
+        need = _ws_need(op, M, N, K, T, n)
         if not need:
             return None, None, 0
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif ws.device != dev:
-        raise ValueError(f"ws must be on {dev}")
+        return ws, ws.data_ptr(), need
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
