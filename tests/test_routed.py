@@ -385,6 +385,13 @@ LORAS = [
     (1, 1, 8, 8, 1, "f16", "f32", False, False, False, "mixed"),
     (1, 8, 16, 512, 70, "bf16", "bf16", False, True, True, "mixed"),
     (2, 3, 24, 136, 65, "f16", "f16", True, True, True, "mixed"),
+    (3, 2, 48, 1000, 264, "bf16", "f32", True, True, True, "mixed"),
+    (21, 3, 64, 4096, 130, "bf16", "f32", True, True, True, "mixed"),
+    (130, 70, 32, 2056, 320, "f16", "f16", True, True, True, "mixed"),
+    (48, 40, 128, 600, 192, "bf16", "bf16", True, False, True, "mixed"),
+    (300, 12, 16, 4096, 96, "f16", "f32", False, True, True, "runs"),
+    (1500, 5, 64, 328, 128, "bf16", "f32", True, True, True, "runs"),
+    (700, 6, 200, 192, 320, "f16", "f16", True, True, True, "mixed"),
     (19, 5, 64, 264, 300, "bf16", "f32", True, True, False, "mixed"),
     (64, 32, 40, 1032, 130, "f16", "f32", True, False, True, "mixed"),
     (100, 2, 256, 64, 257, "bf16", "f32", True, True, True, "mixed"),
@@ -594,9 +601,10 @@ def test_lora_refusals():
                dict(ranks=BAD), dict(sc=BAD), dict(base=BAD, ldb=64), dict(y=BAD), dict(ydt=0, y=ODD)):
         assert call(**kw) == 4, kw
     assert call(R=264) == 5 and call(L=16385) == 5 and call(M=(1 << 24) + 1) == 5 and call(K=1 << 18, ld=1 << 18) == 5
-    need = awq.awq_workspace_bytes(awq.AWQ_OP_LORA, 4, 64, 256, 3, 16)
-    assert need >= 4 * 16 * 4
-    assert call(wsb=need - 1) == 6 and call(ws=None) == 6 and call(ws=BAD) == 6
+    big = dict(M=300, N=4096, ldy=4096, K=4096, ld=4096, L=30, R=64)
+    need = awq.awq_workspace_bytes(awq.AWQ_OP_LORA, 300, 4096, 4096, 30, 64)
+    assert need >= 300 * 64 * 4
+    assert call(**big, wsb=need - 1) == 6 and call(**big, ws=None) == 6 and call(**big, ws=BAD) == 6
     assert awq.awq_workspace_bytes(awq.AWQ_OP_LORA, -1, 64, 256, 3, 16) == 0
 
 

@@ -51,7 +51,7 @@ size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T
     case AWQ_OP_EXPERTS_DOWN:
       if (M < 1 || N < 1 || K < 1 || T < 1 || n_alpha < 1) return 0;
       return awq::experts_ws_bytes(op == AWQ_OP_EXPERTS_DOWN, M, N, K, T, n_alpha);
-    case AWQ_OP_LORA: return awq::lora_ws_bytes(M, K, T, n_alpha);
+    case AWQ_OP_LORA: return awq::lora_ws_bytes(M, N, K, T, n_alpha);
   }
   return 0;
 }

@@ -140,7 +140,7 @@ struct LoraCall {
   int ydt;
   int64_t ldy;
 };
-size_t lora_ws_bytes(int64_t M, int64_t K, int64_t n_adapters, int64_t R);
+size_t lora_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R);
 hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st);
 
 // ---- plain streaming read (k_stream.hip): bytes a multiple of 1024, blocks

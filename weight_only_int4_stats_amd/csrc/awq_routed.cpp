@@ -105,7 +105,7 @@ awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int6
     return AWQ_ERR_ALIGN;
   // block counts of the launches (256 columns, or a K split, per row group)
   if ((M / 16 + n_adapters + 1) * ((N + 255) / 256 + 32) > kMaxBlocks) return AWQ_ERR_UNSUPPORTED;
-  const size_t need = awq::lora_ws_bytes(M, K, n_adapters, R);
+  const size_t need = awq::lora_ws_bytes(M, N, K, n_adapters, R);
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return AWQ_ERR_WORKSPACE;
   const awq::LoraCall c{(const uint16_t*)x, (int)xdt, M, K, ldx, adapter, (const uint16_t*)a, (const uint16_t*)b,
                         n_adapters, R, ranks, scaling, base, ldb, N, y, (int)ydt, ldy};

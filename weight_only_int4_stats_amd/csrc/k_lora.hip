@@ -36,7 +36,7 @@ struct LoraArgs {
   int64_t ldy, N;
   float* h;                          // [ksplit][M][R]
   GroupPlan plan;
-  int M, K, R, n_adapters, ksplit, planned, by_row, nx;   // nx: blocks per block row
+  int M, K, R, n_adapters, ksplit, planned, by_row, nx, vec;   // nx: blocks per block row
 };
 
 template <int DT>
@@ -52,7 +52,7 @@ struct LoraRows {
 };
 
 // Finds the block's adapter and counts its rows; `first` by-row blocks leave
-// when another row's block has the adapter (n = 0).  count_lds: 8 ints.
+// when another row's block has the adapter (n = 0).  count_lds: two ints per wave.
 __device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int* count_lds, int& before) {
   LoraRows r{-1, 0, nullptr};
   before = 0;
@@ -77,14 +77,14 @@ __device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int* c
   }
   if (lane == 0) {
     count_lds[wv] = cnt;
-    count_lds[4 + wv] = first;
+    count_lds[nw + wv] = first;
   }
   __syncthreads();
   int n = 0, f = 0x7FFFFFFF;
   for (int w = 0; w < nw; ++w) {
     if (w < wv) before += count_lds[w];
     n += count_lds[w];
-    f = count_lds[4 + w] < f ? count_lds[4 + w] : f;
+    f = count_lds[nw + w] < f ? count_lds[nw + w] : f;
   }
   r.a = a;
   r.n = p.by_row && f != grp ? 0 : n;
@@ -116,15 +116,58 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& p, int a) {
   return r < 0 ? 0 : r > p.R ? p.R : r;
 }
 
-// h[part][m][r] for 16 rows of an adapter at a time.  Four waves share the
-// block's K range, 64 channels a step: lane (row or rank l % 16, b = l / 16)
-// holds channels 16 b .. 16 b + 15 of the step, so a row's 64 channels are one
-// 128-byte line.  RB: 16-rank blocks.
+// Steps of 64 channels whose loads are in flight together in a wave of the
+// shrink, by the number of 16-rank blocks (registers).
+template <int RB>
+constexpr int lora_unroll() { return RB <= 1 ? 4 : RB <= 2 ? 4 : RB <= 4 ? 2 : 1; }
+
+// acc[i] += 16 rows (xr: this lane's row) x ranks 16 i .. 16 i + 15 over the
+// steps k0, k0 + stride, ... < k1 of 64 channels: lane (row or rank l % 16,
+// b = l / 16) holds channels 16 b .. 16 b + 15 of a step, so a row's 64
+// channels are one 128-byte line.
+template <int DT, int RB>
+__device__ __forceinline__ void lora_shrink_steps(const LoraArgs& p, const uint16_t* xr, const uint16_t* A, int rank,
+                                                  int k0, int k1, int stride, f32x4 (&acc)[RB]) {
+  constexpr int U = lora_unroll<RB>();
+  const int lane = threadIdx.x & 63, rl = lane & 15, b = lane >> 4;
+  // rows past the rank repeat the first (from the cache); their results are dropped
+  const uint16_t* ar[RB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) ar[i] = A + (int64_t)(i * 16 + rl < rank ? i * 16 + rl : 0) * p.K;
+  // whole: every step lies inside the range and inside K, so no load is guarded
+  auto steps = [&](int s, auto whole) {
+    u32x4 xv[U][2], av[U][RB][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int k = (s + u * stride) * 64 + b * 16 + 8 * c;
+        const bool in = decltype(whole)::value || (s + u * stride < k1 && k < p.K);
+        xv[u][c] = in ? ldg128(xr + k) : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < RB; ++i) av[u][i][c] = in ? ldg128(ar[i] + k) : u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[i] = mfma16<DT>(xv[u][c], av[u][i][c], acc[i]);
+  };
+  for (int s = k0; s < k1; s += U * stride) {
+    if (s + (U - 1) * stride < k1 && (s + (U - 1) * stride + 1) * 64 <= p.K) steps(s, std::true_type{});
+    else steps(s, std::false_type{});
+  }
+}
+
+// h[part][m][r] for 16 rows of an adapter at a time; the four waves share the
+// block's K range.  RB: 16-rank blocks.
 template <int DT, int RB>
 __global__ __launch_bounds__(256) void k_lora_shrink(const LoraArgs p) {
   __shared__ int list[16];
   __shared__ int count[8];
-  __shared__ float red[4][256];
+  __shared__ float red[RB < 4 ? RB : 4][4][256];
+  constexpr int RG = RB < 4 ? RB : 4;              // rank blocks that meet in LDS together
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
@@ -136,7 +179,6 @@ __global__ __launch_bounds__(256) void k_lora_shrink(const LoraArgs p) {
   const int steps = (p.K + 63) >> 6;
   const int part = bx * 4 + wv, parts = p.ksplit * 4;
   const int k0 = (int)((int64_t)part * steps / parts), k1 = (int)((int64_t)(part + 1) * steps / parts);
-  const int rb = (rank + 15) >> 4;               // rank blocks in use
   const uint16_t* A = p.a + (int64_t)r.a * p.R * p.K;
   const int rstart = p.planned ? (by & 3) * 16 : 0;
   const int rend = p.planned && rstart + 16 < r.n ? rstart + 16 : r.n;
@@ -148,35 +190,23 @@ __global__ __launch_bounds__(256) void k_lora_shrink(const LoraArgs p) {
     f32x4 acc[RB];
 #pragma unroll
     for (int i = 0; i < RB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = k0; s < k1; ++s) {
-      const int k = s * 64 + b * 16;
-      u32x4 xv[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) xv[c] = k + 8 * c < p.K ? ldg128(xr + k + 8 * c) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        if (i < rb) {
-          const int rr = i * 16 + rl;
-          const uint16_t* ar = A + (int64_t)(rr < rank ? rr : 0) * p.K;   // ranks past the adapter's: dropped
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const u32x4 av = k + 8 * c < p.K ? ldg128(ar + k + 8 * c) : u32x4{0, 0, 0, 0};
-            acc[i] = mfma16<DT>(xv[c], av, acc[i]);
-          }
-        }
-      }
-    }
+    lora_shrink_steps<DT, RB>(p, xr, A, rank, k0, k1, 1, acc);
     // result lane: rank l % 16, rows 4 b + v; the waves' parts in wave order
     float* h = p.h + (int64_t)bx * p.M * p.R;
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      if (i < rb) {
+    for (int i0 = 0; i0 < RB; i0 += RG) {
+      if (i0 * 16 < rank) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) red[wv][(4 * b + v) * 16 + rl] = acc[i][v];
+        for (int i = 0; i < RG; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) red[i][wv][(4 * b + v) * 16 + rl] = acc[i0 + i][v];
         __syncthreads();
-        const int row = tid >> 4, rr = i * 16 + (tid & 15);
-        if (row < nr && rr < p.R)
-          h[(int64_t)list[row] * p.R + rr] = rr < rank ? ((red[0][tid] + red[1][tid]) + red[2][tid]) + red[3][tid] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < RG; ++i) {
+          const int row = tid >> 4, rr = (i0 + i) * 16 + (tid & 15);
+          if (row < nr && rr < rank)
+            h[(int64_t)list[row] * p.R + rr] = ((red[i][0][tid] + red[i][1][tid]) + red[i][2][tid]) + red[i][3][tid];
+        }
         __syncthreads();
       }
     }
@@ -184,32 +214,156 @@ __global__ __launch_bounds__(256) void k_lora_shrink(const LoraArgs p) {
   }
 }
 
-template <int YDT>
-__device__ __forceinline__ float lora_base(const LoraArgs& p, int64_t m, int64_t n) {
-  if (!p.base) return 0.0f;
-  if constexpr (YDT == DT_F32) return reinterpret_cast<const float*>(p.base)[m * p.ldb + n];
-  else return to_f32<YDT>(reinterpret_cast<const uint16_t*>(p.base)[m * p.ldb + n]);
+// One row of h as the sum of two 16-bit values, scaled by a power of two: 16
+// threads per row (j = thread % 16), get(r) gives rank r.  Writes ranks 0 ..
+// pad - 1 (zeros past the rank) and scaling / the power of two.
+template <int DT, int NI, typename F>
+__device__ __forceinline__ void lora_split_row(int j, int rank, int pad, float sc, uint16_t* hi, uint16_t* lo, float* back, F get) {
+  float v[NI];
+  float am = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = i * 16 + j;
+    v[i] = r < rank ? get(r) : 0.0f;
+    am = fmaxf(am, fabsf(v[i]));
+  }
+  am = fmaxf(am, quad_xor1(am));
+  am = fmaxf(am, quad_xor2(am));
+  am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
+  am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x140, 0xF, 0xF, false)));
+  const int pe = pow2_exp_for(am);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = i * 16 + j;
+    if (r < pad) {
+      const float f = ldexpf(v[i], pe);
+      const uint32_t h = from_f32<DT>(f);
+      hi[r] = (uint16_t)h;
+      lo[r] = (uint16_t)from_f32<DT>(f - to_f32<DT>(h));
+    }
+  }
+  if (j == 0) *back = ldexpf(sc, -pe);
 }
-template <int YDT>
-__device__ __forceinline__ void lora_store(const LoraArgs& p, int64_t m, int64_t n, float v) {
-  if constexpr (YDT == DT_F32) reinterpret_cast<float*>(p.y)[m * p.ldy + n] = v;
-  else reinterpret_cast<uint16_t*>(p.y)[m * p.ldy + n] = (uint16_t)from_f32<YDT>(v);
+
+// 8 ranks k .. k + 7 of column n of B; what B holds past the rank is not used.
+__device__ __forceinline__ u32x4 lora_b(const LoraArgs& p, const uint16_t* B, int64_t n, int k, int rank) {
+  u32x4 w = {0, 0, 0, 0};
+  if (n < p.N && k < rank) {
+    w = ldg128(B + n * p.R + k);
+    if (k + 8 > rank) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (k + 2 * c >= rank) w[c] = 0;
+        else if (k + 2 * c + 1 >= rank) w[c] &= 0xFFFFu;
+      }
+    }
+  }
+  return w;
 }
+
+// 4 NQ consecutive outputs of row m from column n: y = base + f acc.  vec:
+// base and y allow 16-byte (NQ = 1 and 16-bit outputs: 8-byte) accesses.
+template <int YDT, int NQ>
+struct LoraOut {
+  static constexpr int NW = YDT == DT_F32 ? 4 * NQ : 2 * NQ;   // 32-bit words
+  uint32_t w[NW];
+  __device__ __forceinline__ void load(const LoraArgs& p, int64_t m, int64_t n) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0;
+    if (!p.base) return;
+    if constexpr (YDT == DT_F32) {
+      const uint32_t* b = reinterpret_cast<const uint32_t*>(p.base) + m * p.ldb + n;
+      if (p.vec && n + 4 * NQ <= p.N) {
+#pragma unroll
+        for (int i = 0; i < NW; i += 4) {
+          const u32x4 t = ldg128(b + i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[i + j] = t[j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+          if (n + i < p.N) w[i] = b[i];
+      }
+    } else {
+      const uint16_t* b = reinterpret_cast<const uint16_t*>(p.base) + m * p.ldb + n;
+      if (p.vec && n + 4 * NQ <= p.N) {
+        if constexpr (NQ == 1) {
+          const uint2 t = *reinterpret_cast<const uint2*>(b);
+          w[0] = t.x;
+          w[1] = t.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < NW; i += 4) {
+            const u32x4 t = ldg128(b + 2 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i + j] = t[j];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4 * NQ; ++i)
+          if (n + i < p.N) w[i >> 1] |= (uint32_t)b[i] << (16 * (i & 1));
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const LoraArgs& p, int64_t m, int64_t n, float f, const f32x4* acc, bool add) {
+    uint32_t o[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) o[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * NQ; ++i) {
+      if constexpr (YDT == DT_F32) {
+        const float base = __uint_as_float(w[i]);
+        o[i] = __float_as_uint(add ? __builtin_fmaf(f, acc[i >> 2][i & 3], base) : base);
+      } else {
+        const float base = i & 1 ? hi_f32<YDT>(w[i >> 1]) : lo_f32<YDT>(w[i >> 1]);
+        o[i >> 1] |= from_f32<YDT>(add ? __builtin_fmaf(f, acc[i >> 2][i & 3], base) : base) << (16 * (i & 1));
+      }
+    }
+    if constexpr (YDT == DT_F32) {
+      uint32_t* y = reinterpret_cast<uint32_t*>(p.y) + m * p.ldy + n;
+      if (p.vec && n + 4 * NQ <= p.N) {
+#pragma unroll
+        for (int i = 0; i < NW; i += 4) *reinterpret_cast<u32x4*>(y + i) = u32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+      } else {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+          if (n + i < p.N) y[i] = o[i];
+      }
+    } else {
+      uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + m * p.ldy + n;
+      if (p.vec && n + 4 * NQ <= p.N) {
+        if constexpr (NQ == 1) {
+          *reinterpret_cast<uint2*>(y) = make_uint2(o[0], o[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NW; i += 4) *reinterpret_cast<u32x4*>(y + 2 * i) = u32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4 * NQ; ++i)
+          if (n + i < p.N) y[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+      }
+    }
+  }
+};
 
 constexpr int kLoraCols = 64;                      // columns per wave of the expand
-constexpr int kLoraHPitch = 256 + 8;               // staged h, 16-bit values per row
 
-// y = base + scaling B h for 16 rows of an adapter at a time, 64 columns per
+// y = base + scaling B h, PR rows of an adapter at a time, 64 columns per
 // wave.  B is the first operand (16 columns of y per product) and h the
-// second, so a result lane holds four values of one row; lane group b's
-// columns are 16 b .. 16 b + 15 over the four products, contiguous.  h, scaled
-// by a power of two per row, enters as the sum of two 16-bit values.
-template <int DT, int YDT>
+// second, so a result lane holds four values of one row; operand row i of
+// product q is column 16 (i / 4) + 4 q + i % 4, so that a lane's four products
+// give 16 consecutive columns.  A wave's part of B stays in registers for all
+// of the block's rows.  RK: 32-rank steps.
+template <int DT, int YDT, int RK, int PR>
 __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
-  __shared__ int list[16];
+  constexpr int kPitch = RK * 32 + 8;
+  __shared__ int list[PR];
   __shared__ int count[8];
-  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][kLoraHPitch];
-  __shared__ float back[16];                       // scaling / the row's power of two
+  __shared__ __attribute__((aligned(16))) uint16_t hs[2][PR][kPitch];
+  __shared__ float back[PR];                       // scaling / the row's power of two
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
@@ -218,88 +372,136 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
   const LoraRows r = lora_rows(p, by, count, before);
   if (r.n == 0) return;
   const int rank = r.a < 0 ? 0 : lora_rank(p, r.a);
-  const int rk = (rank + 31) >> 5;                 // 32-rank steps
+  const int rk = (rank + 31) >> 5;
   const uint16_t* B = p.b + (r.a < 0 ? 0 : (int64_t)r.a * p.N * p.R);
   const float sc = r.a < 0 ? 0.0f : p.scaling ? p.scaling[r.a] : 1.0f;
   const int64_t c0 = ((int64_t)bx * 4 + wv) * kLoraCols;
+  const int64_t cl = c0 + 16 * b;                  // this lane's first column
+  u32x4 w[RK][4];
+#pragma unroll
+  for (int s = 0; s < RK; ++s)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[s][q] = lora_b(p, B, c0 + 16 * (rl >> 2) + 4 * q + (rl & 3), s * 32 + 8 * b, rank);
+  for (int r0 = 0; r0 < r.n; r0 += PR) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PR; i += 16) lora_list(p, r, before, r0 + i, list + i);
+    __syncthreads();
+    const int nr = r.n - r0 < PR ? r.n - r0 : PR;
+    if (rank > 0) {
+      // 16 threads per row; the K parts are added in their order
+      const int64_t pitch = (int64_t)p.M * p.R;
+      for (int row = tid >> 4; row < (nr + 15) / 16 * 16; row += 16) {
+        const float* h = p.h + (int64_t)list[row < nr ? row : 0] * p.R;
+        lora_split_row<DT, RK * 2>(tid & 15, rank, rk * 32, sc, hs[0][row], hs[1][row], back + row, [&](int rr) {
+          float v = 0.0f;
+#pragma unroll 8
+          for (int s = 0; s < p.ksplit; ++s) v += h[s * pitch + rr];
+          return v;
+        });
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < PR; t += 16) {
+      if (t >= nr) break;
+      const int row = t + rl;
+      LoraOut<YDT, 4> out;
+      const int64_t m = list[row < nr ? row : 0];
+      if (row < nr) out.load(p, m, cl);
+      f32x4 acc[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < RK; ++s) {
+        if (s < rk) {
+          const u32x4 hi = *reinterpret_cast<const u32x4*>(&hs[0][row][s * 32 + 8 * b]);
+          const u32x4 lo = *reinterpret_cast<const u32x4*>(&hs[1][row][s * 32 + 8 * b]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[q] = mfma16<DT>(w[s][q], hi, acc[q]);
+            acc[q] = mfma16<DT>(w[s][q], lo, acc[q]);
+          }
+        }
+      }
+      if (row < nr) out.store(p, m, cl, rank > 0 ? back[row] : 0.0f, acc, rank > 0);
+    }
+  }
+}
+
+// Few rows and a small A: one launch in which every block forms its rows' h
+// itself (8 waves share K) and expands it to 128 columns, 16 per wave.
+constexpr int kLoraOneCols = 128;
+template <int DT, int YDT, int RB>
+__global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
+  constexpr int RK = (RB + 1) / 2, kPitch = RK * 32 + 8;
+  __shared__ int list[16];
+  __shared__ int count[16];
+  __shared__ float red[8][256];
+  __shared__ float hv[16][RB * 16 + 1];
+  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][kPitch];
+  __shared__ float back[16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rl = lane & 15, b = lane >> 4;
+  int before;
+  const int bx = (int)(blockIdx.x % (unsigned)p.nx), by = (int)(blockIdx.x / (unsigned)p.nx);
+  const LoraRows r = lora_rows(p, by, count, before);
+  if (r.n == 0) return;
+  const int rank = r.a < 0 ? 0 : lora_rank(p, r.a);
+  const int rk = (rank + 31) >> 5;
+  const float sc = r.a < 0 ? 0.0f : p.scaling ? p.scaling[r.a] : 1.0f;
+  const uint16_t* A = p.a + (r.a < 0 ? 0 : (int64_t)r.a * p.R * p.K);
+  const uint16_t* B = p.b + (r.a < 0 ? 0 : (int64_t)r.a * p.N * p.R);
+  const int64_t c0 = (int64_t)bx * kLoraOneCols + wv * 16;
+  u32x4 w[RK];
+#pragma unroll
+  for (int s = 0; s < RK; ++s) w[s] = lora_b(p, B, c0 + rl, s * 32 + 8 * b, rank);
   for (int r0 = 0; r0 < r.n; r0 += 16) {
     __syncthreads();
     lora_list(p, r, before, r0, list);
     __syncthreads();
     const int nr = r.n - r0 < 16 ? r.n - r0 : 16;
+    LoraOut<YDT, 1> out;
+    const int64_t m = list[rl < nr ? rl : 0];
+    if (rl < nr) out.load(p, m, c0 + 4 * b);
     if (rank > 0) {
-      // 16 threads per row, ranks j, j + 16, ...
-      const int row = tid >> 4, j = tid & 15;
-      const float* h = p.h + (int64_t)list[row < nr ? row : 0] * p.R;
-      float v[16];
-      float am = 0.0f;
+      f32x4 acc[RB];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        v[i] = 0.0f;
-        const int rr = i * 16 + j;
+      for (int i = 0; i < RB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      lora_shrink_steps<DT, RB>(p, p.x + m * p.ldx, A, rank, wv, (p.K + 63) >> 6, 8, acc);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
         if (i * 16 < rank) {
-          if (rr < rank)
-            for (int s = 0; s < p.ksplit; ++s) v[i] += h[(int64_t)s * p.M * p.R + rr];
-          am = fmaxf(am, fabsf(v[i]));
-        }
-      }
-      am = fmaxf(am, quad_xor1(am));
-      am = fmaxf(am, quad_xor2(am));
-      am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
-      am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x140, 0xF, 0xF, false)));
-      const int pe = pow2_exp_for(am);
+          __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (i * 16 < rk * 32) {
-          const float f = ldexpf(v[i], pe);
-          const uint32_t hi = from_f32<DT>(f);
-          hs[0][row][i * 16 + j] = (uint16_t)hi;
-          hs[1][row][i * 16 + j] = (uint16_t)from_f32<DT>(f - to_f32<DT>(hi));
-        }
-      }
-      if (j == 0) back[row] = ldexpf(sc, -pe);
-    }
-    __syncthreads();
-    f32x4 acc[4];
+          for (int v = 0; v < 4; ++v) red[wv][(4 * b + v) * 16 + rl] = acc[i][v];
+          __syncthreads();
+          if (tid < 256) {
+            float t = red[0][tid];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < rk; ++s) {
-      const int k = s * 32 + 8 * b;
-      const u32x4 hi = *reinterpret_cast<const u32x4*>(&hs[0][rl][k]);
-      const u32x4 lo = *reinterpret_cast<const u32x4*>(&hs[1][rl][k]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // operand row i of product q is column c0 + 16 (i / 4) + 4 q + i % 4
-        const int64_t n = c0 + 16 * (rl >> 2) + 4 * q + (rl & 3);
-        u32x4 w = {0, 0, 0, 0};
-        if (n < p.N && k < rank) {
-          w = ldg128(B + n * p.R + k);
-          if (k + 8 > rank) {                      // what B holds past the rank is not used
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (k + 2 * c >= rank) w[c] = 0;
-              else if (k + 2 * c + 1 >= rank) w[c] &= 0xFFFFu;
-            }
+            for (int k = 1; k < 8; ++k) t += red[k][tid];
+            hv[tid >> 4][i * 16 + (tid & 15)] = t;
           }
         }
-        acc[q] = mfma16<DT>(w, hi, acc[q]);
-        acc[q] = mfma16<DT>(w, lo, acc[q]);
+      }
+      __syncthreads();
+      if (tid < 256) {
+        const int row = tid >> 4;
+        lora_split_row<DT, RK * 2>(tid & 15, rank, rk * 32, sc, hs[0][row], hs[1][row], back + row,
+                                   [&](int rr) { return hv[row][rr]; });
+      }
+      __syncthreads();
+    }
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < RK; ++s) {
+      if (s < rk) {
+        acc = mfma16<DT>(w[s], *reinterpret_cast<const u32x4*>(&hs[0][rl][s * 32 + 8 * b]), acc);
+        acc = mfma16<DT>(w[s], *reinterpret_cast<const u32x4*>(&hs[1][rl][s * 32 + 8 * b]), acc);
       }
     }
-    if (rl < nr) {
-      const int64_t m = list[rl];
-      const float f = rank > 0 ? back[rl] : 0.0f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int64_t n = c0 + 16 * b + 4 * q + v;
-          if (n < p.N) {
-            const float base = lora_base<YDT>(p, m, n);
-            lora_store<YDT>(p, m, n, rank > 0 ? __builtin_fmaf(f, acc[q][v], base) : base);
-          }
-        }
-    }
+    if (rl < nr) out.store(p, m, c0 + 4 * b, rank > 0 ? back[rl] : 0.0f, &acc, rank > 0);
   }
 }
 
@@ -313,6 +515,13 @@ static bool lora_planned(int64_t M) { return M > kLoraScan; }
 // Block rows of the scan: one per row, or one per adapter and one for none.
 static int lora_groups(int64_t M, int64_t n_adapters) { return (int)(M < n_adapters + 1 ? M : n_adapters + 1); }
 
+// One launch (k_lora_one) while forming h again in every block costs less than
+// a second launch: A from the caches, at most 256 KB per block and 32 MB in all.
+static bool lora_one(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R) {
+  const int64_t a = R * K * 2, blocks = lora_groups(M, n_adapters) * ((N + kLoraOneCols - 1) / kLoraOneCols);
+  return !lora_planned(M) && R <= 64 && a <= (256 << 10) && a * blocks <= (32 << 20);
+}
+
 static int lora_ksplit(int64_t M, int64_t K, int64_t n_adapters) {
   const int64_t blocks = lora_planned(M) ? (M + 15) / 16 : lora_groups(M, n_adapters);
   const int64_t steps = (K + 63) / 64;
@@ -322,11 +531,13 @@ static int lora_ksplit(int64_t M, int64_t K, int64_t n_adapters) {
   return want < 1 ? 1 : (int)want;
 }
 
-size_t lora_ws_bytes(int64_t M, int64_t K, int64_t n_adapters, int64_t R) {
-  if (M <= 0 || K <= 0 || n_adapters < 0 || R <= 0) return 0;
-  size_t b = n_adapters ? align_up((size_t)lora_ksplit(M, K, n_adapters) * (size_t)M * (size_t)R * 4, 256) : 0;
-  if (lora_planned(M)) b += group_plan_bytes(M, n_adapters, kLoraTile);
-  return b;
+static size_t lora_h_bytes(int64_t M, int64_t K, int64_t n_adapters, int64_t R) {
+  return n_adapters ? align_up((size_t)lora_ksplit(M, K, n_adapters) * (size_t)M * (size_t)R * 4, 256) : 0;
+}
+
+size_t lora_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R) {
+  if (M <= 0 || N <= 0 || K <= 0 || n_adapters < 0 || R <= 0 || lora_one(M, N, K, n_adapters, R)) return 0;
+  return lora_h_bytes(M, K, n_adapters, R) + (lora_planned(M) ? group_plan_bytes(M, n_adapters, kLoraTile) : 0);
 }
 
 hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st) {
@@ -349,32 +560,51 @@ hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st) {
   p.n_adapters = (int)c.n_adapters;
   p.ksplit = lora_ksplit(c.M, c.K, c.n_adapters);
   p.planned = lora_planned(c.M);
-  p.nx = (int)((c.N + 4 * kLoraCols - 1) / (4 * kLoraCols));
   p.h = reinterpret_cast<float*>(ws);
   p.by_row = c.M < c.n_adapters + 1;
+  const uintptr_t es = c.ydt == DT_F32 ? 4 : 2, q = 16 / es;
+  p.vec = c.ldy % q == 0 && (uintptr_t)c.y % 16 == 0 && (!c.base || (c.ldb % q == 0 && (uintptr_t)c.base % 16 == 0));
   unsigned gy = (unsigned)lora_groups(c.M, c.n_adapters);
+  const bool one = lora_one(c.M, c.N, c.K, c.n_adapters, c.R);
+  const int64_t cols = one ? kLoraOneCols : 4 * kLoraCols;
+  p.nx = (int)((c.N + cols - 1) / cols);
   if (p.planned) {
-    const size_t hb = lora_ws_bytes(c.M, c.K, c.n_adapters, c.R) - group_plan_bytes(c.M, c.n_adapters, kLoraTile);
-    p.plan = group_plan_at(reinterpret_cast<char*>(ws) + hb, c.M, c.n_adapters, kLoraTile);
+    p.plan = group_plan_at(reinterpret_cast<char*>(ws) + lora_h_bytes(c.M, c.K, c.n_adapters, c.R), c.M, c.n_adapters, kLoraTile);
     const hipError_t e = launch_group_plan(c.adapter, c.M, c.n_adapters, kLoraTile, p.plan, st);
     if (e != hipSuccess) return e;
     gy = (unsigned)group_tiles_max(c.M, c.n_adapters, kLoraTile);
   }
-  auto go = [&](auto dtc) {
-    constexpr int DT = decltype(dtc)::value;
-    if (c.n_adapters > 0) {
-      const dim3 grid((unsigned)p.ksplit * (p.planned ? gy * 4 : gy)), block(256);
-      const int64_t rb = (c.R + 15) / 16;
-      if (rb <= 1) hipLaunchKernelGGL((k_lora_shrink<DT, 1>), grid, block, 0, st, p);
-      else if (rb <= 2) hipLaunchKernelGGL((k_lora_shrink<DT, 2>), grid, block, 0, st, p);
-      else if (rb <= 4) hipLaunchKernelGGL((k_lora_shrink<DT, 4>), grid, block, 0, st, p);
-      else if (rb <= 8) hipLaunchKernelGGL((k_lora_shrink<DT, 8>), grid, block, 0, st, p);
-      else hipLaunchKernelGGL((k_lora_shrink<DT, 16>), grid, block, 0, st, p);
+  const dim3 grid((unsigned)p.nx * gy);
+  auto typed = [&](auto dtc, auto ydc) {
+    constexpr int DT = decltype(dtc)::value, YDT = decltype(ydc)::value;
+    if (one) {
+      if (c.R <= 16) hipLaunchKernelGGL((k_lora_one<DT, YDT, 1>), grid, dim3(512), 0, st, p);
+      else if (c.R <= 32) hipLaunchKernelGGL((k_lora_one<DT, YDT, 2>), grid, dim3(512), 0, st, p);
+      else hipLaunchKernelGGL((k_lora_one<DT, YDT, 4>), grid, dim3(512), 0, st, p);
+      return;
     }
-    const dim3 grid((unsigned)p.nx * gy), block(256);
-    if (c.ydt == DT_F32) hipLaunchKernelGGL((k_lora_expand<DT, DT_F32>), grid, block, 0, st, p);
-    else if (c.ydt == DT_F16) hipLaunchKernelGGL((k_lora_expand<DT, DT_F16>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((k_lora_expand<DT, DT_BF16>), grid, block, 0, st, p);
+    if (c.n_adapters > 0) {
+      const dim3 sg((unsigned)p.ksplit * (p.planned ? gy * 4 : gy));
+      if (c.R <= 16) hipLaunchKernelGGL((k_lora_shrink<DT, 1>), sg, dim3(256), 0, st, p);
+      else if (c.R <= 32) hipLaunchKernelGGL((k_lora_shrink<DT, 2>), sg, dim3(256), 0, st, p);
+      else if (c.R <= 64) hipLaunchKernelGGL((k_lora_shrink<DT, 4>), sg, dim3(256), 0, st, p);
+      else if (c.R <= 128) hipLaunchKernelGGL((k_lora_shrink<DT, 8>), sg, dim3(256), 0, st, p);
+      else hipLaunchKernelGGL((k_lora_shrink<DT, 16>), sg, dim3(256), 0, st, p);
+    }
+    auto expand = [&](auto pr) {
+      constexpr int PR = decltype(pr)::value;
+      if (c.R <= 32) hipLaunchKernelGGL((k_lora_expand<DT, YDT, 1, PR>), grid, dim3(256), 0, st, p);
+      else if (c.R <= 64) hipLaunchKernelGGL((k_lora_expand<DT, YDT, 2, PR>), grid, dim3(256), 0, st, p);
+      else if (c.R <= 128) hipLaunchKernelGGL((k_lora_expand<DT, YDT, 4, 16>), grid, dim3(256), 0, st, p);
+      else hipLaunchKernelGGL((k_lora_expand<DT, YDT, 8, 16>), grid, dim3(256), 0, st, p);
+    };
+    if (p.planned) expand(std::integral_constant<int, kLoraTile>{});
+    else expand(std::integral_constant<int, 16>{});
+  };
+  auto go = [&](auto dtc) {
+    if (c.ydt == DT_F32) typed(dtc, std::integral_constant<int, DT_F32>{});
+    else if (c.ydt == DT_F16) typed(dtc, std::integral_constant<int, DT_F16>{});
+    else typed(dtc, std::integral_constant<int, DT_BF16>{});
   };
   if (c.xdt == DT_F16) go(std::integral_constant<int, DT_F16>{});
   else go(std::integral_constant<int, DT_BF16>{});
