@@ -9,14 +9,18 @@
 //    power of two per row, in the order the unpack yields), lay the steps and
 //    zero points out group by group, and zero the output rows of slots without
 //    an expert.
-//  * k_experts_gemm: tiles of BM = 32 MB rows of one expert x 128 weight rows,
-//    4 waves (2 x 2, each 16 MB x 64).  64 channels per stage, three LDS stages
-//    filled by LDS DMA two stages ahead; the rows of a tile are gathered by the
-//    copies' addresses.  v_mfma_f32_16x16x32_f16 multiplies the activations
-//    with the exact integers (q - z) 2^-9; a group's sums are folded into the
-//    result with its step, in fp32, when the group ends.  Rounding step (q - z)
-//    to fp16 instead would save the fold and a second set of accumulators, and
-//    cost 1e-4 of every result.
+//  * k_experts_gemm: tiles of BM = 16 MB rows of one expert x 256 weight rows, 4
+//    waves of BM x 64, two blocks per compute unit.  64 channels per stage,
+//    three LDS stages filled by LDS DMA two stages ahead; the rows of a tile are
+//    gathered by the copies' addresses.  v_mfma_f32_16x16x32_f16 multiplies the
+//    activations with the exact integers (q - z) 2^-9.  The accumulators hold
+//    the sum in units of the current group's step: a new group multiplies them
+//    by D[g - 1] / D[g] (fp32, one multiplication per value and group) and the
+//    epilogue by the last step.  So no operand is rounded, unlike step (q - z)
+//    in fp16 (1e-4 of every result), and no second set of accumulators is
+//    needed.  Unpacking costs 9 vector instructions per eight codes; a wave's
+//    tile is tall (128 rows) because they serve all of its rows: with 64 x 64
+//    tiles per wave the vector instructions, not the matrix cores, set the time.
 //  * With SwiGLU a tile's columns alternate 16 gate rows and their 16 up rows,
 //    so both meet in one lane.  down writes fp32 rows per slot; the weighted sum
 //    over a token's slots is k_experts_combine's.
@@ -32,7 +36,7 @@
 
 namespace awqk {
 
-constexpr int kGemmN = 128;                        // weight rows per tile
+constexpr int kGemmN = 256;                        // weight rows per tile
 constexpr int kGemmK = 64;                         // channels per stage
 constexpr int kGemmGroupM = 8;                     // row tiles taken together
 constexpr int kXcd = 8;                            // L2 slices
@@ -46,11 +50,11 @@ struct GemmArgs {
   const uint8_t* zeros;
   void* y;
   int64_t xrows;
-  int S, E, top_k, group, ydt, vec;
+  int S, E, top_k, group, unit, ydt, vec;          // unit: channels per constant (64 or 128, at most the group)
   // workspace
   uint16_t* xq;                                    // [xrows][K]
   int* pexp;                                       // [xrows]
-  uint32_t* ctab;                                  // [E][G][N]: step | -z 2^-9 << 16
+  uint2* ctab;                                     // [E][K / unit][N]: D[u - 1] / D[u], -z 2^-9 twice
   GroupPlan plan;
   // first block of each part of the preparation
   int b_rows, b_consts, b_zero;
@@ -109,15 +113,31 @@ __global__ __launch_bounds__(kPlanThreads) void k_experts_prep(const GemmArgs p,
     const int64_t row = (int64_t)(bid - p.b_rows) * 16 + (tid >> 6);
     if (row < p.xrows) prep_row<DT>(p, row);
   } else if (bid < p.b_zero) {
-    const int64_t n = (int64_t)(bid - p.b_consts) * kPlanThreads + tid;   // row of the [E N] stack
-    if (n >= (int64_t)p.E * p.N) return;
+    // a thread takes eight units of one row of the [E N] stack; a step of 0
+    // counts as 2^-40 so that the ratios stay finite
+    const int U = (int)(p.K / p.unit), sh = p.group == 256 ? 1 : 0;
     const int G = (int)(p.K / p.group);
+    const int64_t i = (int64_t)(bid - p.b_consts) * kPlanThreads + tid;
+    const int64_t rows = (int64_t)p.E * p.N, n = i % rows;
+    const int u0 = (int)(i / rows) * 8;
+    if (u0 >= U) return;
     const int64_t e = n / p.N, r = n - e * p.N;
     const uint16_t* s = p.scales + n * G;
     const uint8_t* z = p.zeros + n * G;
-    uint32_t* c = p.ctab + e * G * p.N + r;
-#pragma unroll 8
-    for (int g = 0; g < G; ++g) c[(int64_t)g * p.N] = (uint32_t)s[g] | (experts_nz(z[g]) & 0xFFFF0000u);
+    float d[9];
+    uint32_t zz[8];
+    d[0] = u0 ? f16_to_f32(s[(u0 - 1) >> sh]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int g = (u0 + j < U ? u0 + j : U - 1) >> sh;
+      d[j + 1] = f16_to_f32(s[g]);
+      zz[j] = z[g];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (u0 + j < U)
+        p.ctab[(e * U + u0 + j) * p.N + r] = make_uint2(
+            __float_as_uint(fmaxf(d[j], 0x1p-40f) / fmaxf(d[j + 1], 0x1p-40f)), experts_nz(zz[j]));
   } else {
     const int64_t slot = (int64_t)(bid - p.b_zero) * 16 + (tid >> 6);
     if (slot >= p.S) return;
@@ -129,12 +149,12 @@ __global__ __launch_bounds__(kPlanThreads) void k_experts_prep(const GemmArgs p,
 
 template <int MODE, int MB, int SPG>
 __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
-  constexpr int BM = 32 * MB;
-  constexpr int kA = BM * kGemmK * 2, kB = kGemmN * 32, kC = 1024, kStage = kA + kB + kC;
+  constexpr int BM = 16 * MB, HB = MB / 2;         // rows, 16-row blocks per sub-step
+  constexpr int kA = BM * kGemmK * 2, kB = kGemmN * 32, kC = kGemmN * 8, kStage = kA + kB + kC;
+  constexpr int kAc = BM / 32;                     // A copies per wave and stage
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wv >> 1, wn = wv & 1;
   const int rl = lane & 15, b = lane >> 4;
 
   // ---- the tile
@@ -167,103 +187,151 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   };
 
   // ---- copies: A rows of 128 bytes, 8 per copy, chunk c of row r at c ^ (r & 7);
-  // B per 32 columns the first then the last 16 bytes of each; C four entries a lane
+  // B per 32 columns the first then the last 16 bytes of each; C two entries a lane
   const int64_t G = p.K / p.group;
   const i32x4 ars = rsrc4(p.xq, (uint32_t)(p.xrows * p.K * 2));
   const i32x4 brs = rsrc4(reinterpret_cast<const uint8_t*>(p.qw) + (int64_t)e * p.N * (p.K >> 1), (uint32_t)(p.N * (p.K >> 1)));
-  const i32x4 crs = rsrc4(p.ctab + (int64_t)e * G * p.N, (uint32_t)(G * p.N * 4));
-  uint32_t aoff[MB];
+  const int64_t U = p.K / p.unit;
+  const i32x4 crs = rsrc4(p.ctab + (int64_t)e * U * p.N, (uint32_t)(U * p.N * 8));
+  uint32_t aoff[kAc];
 #pragma unroll
-  for (int u = 0; u < MB; ++u) {
-    const int r = 8 * (MB * wv + u) + (lane >> 3);
+  for (int u = 0; u < kAc; ++u) {
+    const int r = 8 * (kAc * wv + u) + (lane >> 3);
     aoff[u] = r < rows ? (uint32_t)((int64_t)xrow(perm[r]) * p.K * 2) + (uint32_t)(((lane & 7) ^ (r & 7)) * 16) : kBufferOob;
   }
-  const int64_t bn = wrow(32 * wv + (lane & 31));
-  const uint32_t boff = bn < 0 ? kBufferOob : (uint32_t)(bn * (p.K >> 1)) + (uint32_t)((lane >> 5) * 16);
-  const int64_t cn = lane < 32 ? wrow(4 * lane) : -1;
-  const uint32_t coff = cn < 0 ? kBufferOob : (uint32_t)(cn * 4);
+  uint32_t boff[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t n = wrow(64 * wv + 32 * u + (lane & 31));
+    boff[u] = n < 0 ? kBufferOob : (uint32_t)(n * (p.K >> 1)) + (uint32_t)((lane >> 5) * 16);
+  }
+  const int64_t cn = wv < 2 ? wrow(128 * wv + 2 * lane) : -1;
+  const uint32_t coff = cn < 0 ? kBufferOob : (uint32_t)(cn * 8);
   const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   const int S = (int)(p.K / kGemmK);
-  auto issue = [&](int s, int buf) {
+  // part q of stage s's copies into buffer buf: the A copies q, q + 4, ..., and
+  // the rest with the last
+  auto copy = [&](int s, int buf, int q) {
     const uint32_t lb = lbase + (uint32_t)buf * kStage;
 #pragma unroll
-    for (int u = 0; u < MB; ++u) dma16(ars, lb + (uint32_t)(MB * wv + u) * 1024, aoff[u], (uint32_t)s * 128);
-    dma16(brs, lb + kA + (uint32_t)wv * 1024, boff, (uint32_t)s * 32);
-    if (wv == 0) dma16(crs, lb + kA + kB, coff, (uint32_t)(s / SPG) * (uint32_t)(p.N * 4));
+    for (int u = 0; u < kAc; ++u)
+      if (u % 4 == q) dma16(ars, lb + (uint32_t)(kAc * wv + u) * 1024, aoff[u], (uint32_t)s * 128);
+    if (q == 2) dma16(brs, lb + kA + (uint32_t)wv * 2048, boff[0], (uint32_t)s * 32);
+    if (q == 3) {
+      dma16(brs, lb + kA + (uint32_t)wv * 2048 + 1024, boff[1], (uint32_t)s * 32);
+      if (wv < 2) dma16(crs, lb + kA + kB + (uint32_t)wv * 1024, coff, (uint32_t)(s / SPG) * (uint32_t)(p.N * 8));
+    }
+  };
+  // every LDS access of this wave done, and all copies but the newest stage's
+  auto wait_stage = [&](bool newest) {
+    if (!newest) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+    else if (wv < 2) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kAc + 3));
+    else __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kAc + 2));
   };
 
-  f32x4 acc[MB][4], part[MB][4];
+  f32x4 acc[MB][4];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  issue(0, 0);
-  if (S > 1) issue(1, 1);
+  uint2 w[4], cz[4];                               // a stage's words and constants of the lane's columns
+  auto load_w = [&](const uint8_t* base) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int col = wv * 64 + n * 16 + rl;
+      w[n] = *reinterpret_cast<const uint2*>(base + kA + (col >> 5) * 1024 + (b >> 1) * 512 + (col & 31) * 16 + (b & 1) * 8);
+      cz[n] = *reinterpret_cast<const uint2*>(base + kA + kB + col * 8);
+    }
+  };
+  // fragments of sub-step q = 2 st + hh: k32 step st, row blocks HB hh ..
+  auto load_a = [&](const uint8_t* base, int q, u32x4 (&a)[HB]) {
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+      const int r = ((q & 1) * HB + i) * 16 + rl;
+      a[i] = *reinterpret_cast<const u32x4*>(base + r * 128 + (((2 * b + (q >> 1)) ^ (r & 7)) * 16));
+    }
+  };
+  u32x4 aE[HB], aO[HB], bq[4];
+  float ratio[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) copy(0, 0, q);
+  if (S > 1)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) copy(1, 1, q);
+  wait_stage(S > 1);
+  lds_barrier();
+  load_a(lds, 0, aE);
+  load_w(lds);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) bq[n] = experts_unpack(w[n].x, cz[n].y);
+
+  // A stage runs in four sub-steps.  In sub-step 1 a column's operands are
+  // replaced by step 1's once its last product of step 0 is issued, in
+  // sub-step 3 by the next stage's, whose words are read right after the
+  // barrier: the unpacking runs between the products.
   int buf = 0;
-  for (int s0 = 0; s0 < S; s0 += SPG) {
-    uint32_t cw[4];
+  for (int s0 = 0; s0 < S; s0 += SPG) {             // SPG stages per unit
 #pragma unroll
     for (int i = 0; i < SPG; ++i) {
       const int s = s0 + i;
-      // stage s has arrived when at most stage s + 1's copies are in flight
-      if (s + 1 < S) {
-        if (wv == 0) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(MB + 2));
-        else __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(MB + 1));
-      } else {
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-      }
-      lds_barrier();
-      const int buf2 = buf >= 1 ? buf - 1 : 2;     // (buf + 2) mod 3: left by stage s - 1
-      if (s + 2 < S) issue(s + 2, buf2);
-      const uint8_t* base = lds + buf * kStage;
-      uint2 w[4];
+      const bool cp = s + 2 < S;
+      const int nxt = buf == 2 ? 0 : buf + 1, nxt2 = buf == 0 ? 2 : buf - 1;
+      const uint8_t* cur = lds + buf * kStage;
+      const uint8_t* ahead = lds + nxt * kStage;
+      if (i == 0) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int col = wn * 64 + n * 16 + rl;
-        w[n] = *reinterpret_cast<const uint2*>(base + kA + (col >> 5) * 1024 + (b >> 1) * 512 + (col & 31) * 16 + (b & 1) * 8);
-        if (i == 0) cw[n] = *reinterpret_cast<const uint32_t*>(base + kA + kB + col * 4);
+        for (int n = 0; n < 4; ++n) ratio[n] = __uint_as_float(cz[n].x);
       }
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        u32x4 a[MB];
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-          const int r = wm * 16 * MB + m * 16 + rl;
-          a[m] = *reinterpret_cast<const u32x4*>(base + r * 128 + (((2 * b + st) ^ (r & 7)) * 16));
+      for (int q = 0; q < 4; ++q) {
+        if (cp) copy(s + 2, nxt2, q);
+        if (q < 3) {
+          load_a(cur, q + 1, (q & 1) ? aE : aO);
+        } else {
+          wait_stage(cp);
+          lds_barrier();
+          load_a(ahead, 0, aE);
+          load_w(ahead);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        const u32x4 (&a)[HB] = (q & 1) ? aO : aE;
+        const int hh = q & 1;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const uint32_t nz = (cw[n] >> 16) * 0x10001u;
-          const u32x4 o = experts_unpack(st ? w[n].y : w[n].x, nz);
 #pragma unroll
-          for (int m = 0; m < MB; ++m) {
-            if (i == 0 && st == 0) part[m][n] = mfma16h(a[m], o, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-            else part[m][n] = mfma16h(a[m], o, part[m][n]);
+          for (int m = 0; m < HB; ++m) {
+            f32x4& c = acc[hh * HB + m][n];
+            if (i == 0 && q < 2) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) c[v] *= ratio[n];
+            }
+            c = mfma16h(a[m], bq[n], c);
           }
+          if (q & 1) bq[n] = experts_unpack(q == 1 ? w[n].y : w[n].x, cz[n].y);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      buf = buf == 2 ? 0 : buf + 1;
-    }
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const float d = f16_to_f32(cw[n] & 0xFFFFu) * 512.0f;
-#pragma unroll
-      for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[m][n][v] = __builtin_fmaf(d, part[m][n][v], acc[m][n][v]);
+      buf = nxt;
     }
   }
 
-  // ---- epilogue: 16 rows at a time through the wave's LDS area, then whole
-  // row pieces.  Result lane: column l % 16, rows 4 b + v.
+  // ---- epilogue: the last group's step, then 16 rows at a time through the
+  // wave's LDS area and out in whole row pieces.  Result lane: column l % 16,
+  // rows 4 b + v.
+  float step[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int64_t r = wrow(wv * 64 + n * 16 + rl);
+    step[n] = r < 0 ? 0.0f : fmaxf(f16_to_f32(p.scales[((int64_t)e * p.N + r) * G + G - 1]), 0x1p-40f) * 512.0f;
+  }
   __syncthreads();                                 // every wave is done with the stages
   constexpr int kW = MODE == EXPERTS_SWIGLU ? 32 : 64;                    // outputs per row of the wave
   float* stg = reinterpret_cast<float*>(lds) + wv * 16 * (kW + 4);
   constexpr int kL = kW / 4;                       // lanes per row, four outputs each
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
-    const int r0 = wm * 16 * MB + m * 16;
+    const int r0 = m * 16;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int r = r0 + 4 * b + v;
@@ -271,10 +339,11 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
       float* d = stg + (4 * b + v) * (kW + 4) + rl;
       if constexpr (MODE == EXPERTS_SWIGLU) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) d[16 * h] = swiglu(ldexpf(acc[m][2 * h][v], pe), ldexpf(acc[m][2 * h + 1][v], pe));
+        for (int h = 0; h < 2; ++h)
+          d[16 * h] = swiglu(ldexpf(acc[m][2 * h][v] * step[2 * h], pe), ldexpf(acc[m][2 * h + 1][v] * step[2 * h + 1], pe));
       } else {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) d[16 * n] = ldexpf(acc[m][n][v], pe);
+        for (int n = 0; n < 4; ++n) d[16 * n] = ldexpf(acc[m][n][v] * step[n], pe);
       }
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): the wave's writes landed
@@ -284,7 +353,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
       const int r = i * (64 / kL) + lane / kL, c = (lane % kL) * 4;
       const f32x4 o = *reinterpret_cast<const f32x4*>(stg + r * (kW + 4) + c);
       if (r0 + r >= rows) continue;
-      const int64_t col = c0 + wn * kW + c, pos = (int64_t)perm[r0 + r] * p.ldy + col;
+      const int64_t col = c0 + wv * kW + c, pos = (int64_t)perm[r0 + r] * p.ldy + col;
       if (MODE == EXPERTS_DOWN || p.ydt == DT_F32) {
         float* y = reinterpret_cast<float*>(p.y) + pos;
         if (p.vec && col + 4 <= ncols) *reinterpret_cast<f32x4*>(y) = o;
@@ -308,10 +377,9 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
 
 template <int MODE, int MB>
 void gemm_launch(const GemmArgs& a, const dim3& grid, hipStream_t st) {
-  constexpr size_t lds = 3 * (32 * MB * kGemmK * 2 + kGemmN * 32 + 1024);
+  constexpr size_t lds = 3 * (16 * MB * kGemmK * 2 + kGemmN * 40);
   if (a.group == 64) hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 1>), grid, dim3(256), lds, st, a);
-  else if (a.group == 128) hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 2>), grid, dim3(256), lds, st, a);
-  else hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 4>), grid, dim3(256), lds, st, a);
+  else hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 2>), grid, dim3(256), lds, st, a);   // 256: a ratio of 1 between halves
 }
 
 }  // namespace awqk
@@ -334,7 +402,7 @@ static GemmSpace gemm_space(bool down, int64_t M, int64_t N, int64_t K, int64_t 
   g.xq = 0;
   g.pexp = g.xq + align_up((size_t)xrows * (size_t)K * 2, 256);
   g.ctab = g.pexp + align_up((size_t)xrows * 4, 256);
-  g.plan = g.ctab + align_up((size_t)E * (size_t)N * (size_t)(K / group) * 4, 256);
+  g.plan = g.ctab + align_up((size_t)E * (size_t)N * (size_t)(K / (group == 64 ? 64 : 128)) * 8, 256);
   g.total = g.plan + group_plan_bytes(S, E, gemm_tile_rows(S, E));
   return g;
 }
@@ -365,16 +433,17 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, voi
   a.E = (int)c.E;
   a.top_k = c.top_k;
   a.group = c.group;
+  a.unit = c.group == 64 ? 64 : 128;
   a.ydt = down ? DT_F32 : c.ydt;
   const size_t es = a.ydt == DT_F32 ? 4 : 2;
   a.vec = ldo % 4 == 0 && (uintptr_t)out % (4 * es) == 0;
   a.xq = reinterpret_cast<uint16_t*>(w + g.xq);
   a.pexp = reinterpret_cast<int*>(w + g.pexp);
-  a.ctab = reinterpret_cast<uint32_t*>(w + g.ctab);
+  a.ctab = reinterpret_cast<uint2*>(w + g.ctab);
   a.plan = group_plan_at(w + g.plan, S, c.E, tile);
   a.b_rows = 1;
   a.b_consts = a.b_rows + (int)((a.xrows + 15) / 16);
-  a.b_zero = a.b_consts + (int)((c.E * c.N + kPlanThreads - 1) / kPlanThreads);
+  a.b_zero = a.b_consts + (int)((c.E * c.N * ((c.K / a.unit + 7) / 8) + kPlanThreads - 1) / kPlanThreads);
   const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
   const unsigned pb = (unsigned)(a.b_zero + (down ? 0 : (S + 15) / 16));
   if (c.xdt == DT_F16) hipLaunchKernelGGL((k_experts_prep<DT_F16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
@@ -386,9 +455,9 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, voi
   const dim3 grid((unsigned)((tiles + kXcd - 1) / kXcd * kXcd));
   auto go = [&](auto mode) {
     constexpr int MODE = decltype(mode)::value;
-    if (tile == 128) gemm_launch<MODE, 4>(a, grid, st);
-    else if (tile == 64) gemm_launch<MODE, 2>(a, grid, st);
-    else gemm_launch<MODE, 1>(a, grid, st);
+    if (tile == 128) gemm_launch<MODE, 8>(a, grid, st);
+    else if (tile == 64) gemm_launch<MODE, 4>(a, grid, st);
+    else gemm_launch<MODE, 2>(a, grid, st);
   };
   if (c.mode == EXPERTS_UP) go(std::integral_constant<int, EXPERTS_UP>{});
   else if (c.mode == EXPERTS_SWIGLU) go(std::integral_constant<int, EXPERTS_SWIGLU>{});

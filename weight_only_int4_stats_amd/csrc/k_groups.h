@@ -28,7 +28,7 @@ constexpr int kPlanThreads = 1024;
 inline int64_t group_tiles_max(int64_t S, int64_t E, int tile_rows) {
   return S / tile_rows + (S < E + 1 ? S : E + 1);
 }
-inline size_t group_plan_lds(int E) { return (size_t)(E + 1 + 32) * 4; }
+inline size_t group_plan_lds(int E) { return (size_t)(2 * E + 3 + 32) * 4; }
 inline size_t group_plan_bytes(int64_t S, int64_t E, int tile_rows) {
   return awq::align_up((size_t)S * 4, 256) +
          awq::align_up((size_t)group_tiles_max(S, E, tile_rows) * sizeof(GroupTile), 256) + 256;
@@ -42,18 +42,46 @@ inline GroupPlan group_plan_at(void* ws, int64_t S, int64_t E, int tile_rows) {
   return p;
 }
 
+// Adds 1 to counter[g] for every lane with g >= 0 and returns the counter
+// before the lane's own addition.  A wave of one g (runs of equal indices are
+// common) adds once: lanes at one counter would take their turns.
+__device__ __forceinline__ int group_add(int* counter, int g) {
+  const int lane = threadIdx.x & 63;
+  const int lead = __builtin_amdgcn_readfirstlane(g);
+  if (__all(g == lead)) {
+    if (lead < 0) return 0;
+    int base = 0;
+    if (lane == 0) base = atomicAdd(&counter[lead], 64);
+    return __builtin_amdgcn_readfirstlane(base) + lane;
+  }
+  return g >= 0 ? atomicAdd(&counter[g], 1) : 0;
+}
+
 // One block of kPlanThreads: a counting sort of the S indices in LDS
-// (group_plan_lds bytes at lds).  The positions inside a group come from LDS atomics.
+// (group_plan_lds bytes at lds).  The positions inside a group come from LDS
+// atomics.  Eight indices per thread are loaded together.
 __device__ inline void group_plan_block(const int32_t* __restrict__ ids, int S, int E, int tile_rows,
                                         const GroupPlan& plan, int* lds) {
   int* start = lds;                    // counts, then first positions
-  int* wsum = lds + E + 1;             // [16] rows, [16] tiles per wave
+  int* tstart = lds + E + 1;           // first tile of each group, and the end
+  int* wsum = lds + 2 * E + 3;         // [16] rows, [16] tiles per wave
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   for (int g = tid; g <= E; g += kPlanThreads) start[g] = 0;
   __syncthreads();
-  for (int s = tid; s < S; s += kPlanThreads) {
-    const int id = ids[s];
-    atomicAdd(&start[id < 0 || id >= E ? E : id], 1);
+  constexpr int kU = 8;
+  int g8[kU];
+  auto load8 = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int s = s0 + u * kPlanThreads + tid;
+      const int id = ids[s < S ? s : 0];
+      g8[u] = s >= S ? -1 : id < 0 || id >= E ? E : id;
+    }
+  };
+  for (int s0 = 0; s0 < S; s0 += kU * kPlanThreads) {
+    load8(s0);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) (void)group_add(start, g8[u]);
   }
   __syncthreads();
   // exclusive prefix sums of the counts and of the tile counts: each thread
@@ -86,17 +114,9 @@ __device__ inline void group_plan_block(const int32_t* __restrict__ ids, int S, 
   }
   for (int g = g0; g < g1; ++g) {
     const int c = start[g], tc = (c + tile_rows - 1) / tile_rows;
-    for (int i = 0; i < tc; ++i) {
-      GroupTile q;
-      q.group = g;
-      q.first = nb + i * tile_rows;
-      q.rows = c - i * tile_rows < tile_rows ? c - i * tile_rows : tile_rows;
-      q.before = tb;
-      q.tiles = tc;
-      q.pad[0] = q.pad[1] = q.pad[2] = 0;
-      plan.tiles[tb + i] = q;
-    }
+    tstart[g] = tb;
     if (g == E) {
+      tstart[E + 1] = tb + tc;
       plan.ntile[0] = tb + tc;
       plan.ntile[1] = tb;
     }
@@ -105,9 +125,35 @@ __device__ inline void group_plan_block(const int32_t* __restrict__ ids, int S, 
     tb += tc;
   }
   __syncthreads();
-  for (int s = tid; s < S; s += kPlanThreads) {
-    const int id = ids[s];
-    plan.perm[atomicAdd(&start[id < 0 || id >= E ? E : id], 1)] = s;
+  // one tile per thread: its group is the last whose first tile is not past it
+  const int tiles = tstart[E + 1];
+  for (int i = tid; i < tiles; i += kPlanThreads) {
+    int lo = 0, hi = E + 1;            // tstart[lo] <= i < tstart[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tstart[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    const int k = i - tstart[lo];
+    const int end = lo == E ? S : start[lo + 1];
+    GroupTile q;
+    q.group = lo;
+    q.first = start[lo] + k * tile_rows;
+    q.rows = end - q.first < tile_rows ? end - q.first : tile_rows;
+    q.before = tstart[lo];
+    q.tiles = tstart[lo + 1] - tstart[lo];
+    q.pad[0] = q.pad[1] = q.pad[2] = 0;
+    plan.tiles[i] = q;
+  }
+  __syncthreads();
+  for (int s0 = 0; s0 < S; s0 += kU * kPlanThreads) {
+    if (S > kU * kPlanThreads) load8(s0);          // else still held from the counting
+    int at[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) at[u] = group_add(start, g8[u]);
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (g8[u] >= 0) plan.perm[at[u]] = s0 + u * kPlanThreads + tid;
   }
 }
 

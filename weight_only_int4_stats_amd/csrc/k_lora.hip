@@ -45,21 +45,21 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f3
   else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// The rows a block works on: its adapter (-1: none), and rows [0, n) of it.
+// The rows a block works on: its adapter (-1: none) and how many.
 struct LoraRows {
   int a, n;
-  const int* perm;                   // planned: the rows; else they are listed 16 at a time
+  const int* perm;                   // planned: the rows
+  uint64_t mask;                     // up to 64 rows in all: which
+  int before;                        // else: rows before this wave's share of the index
 };
 
-// Finds the block's adapter and counts its rows; `first` by-row blocks leave
-// when another row's block has the adapter (n = 0).  count_lds: two ints per wave.
-__device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int* count_lds, int& before) {
-  LoraRows r{-1, 0, nullptr};
-  before = 0;
+// Finds the block's adapter and counts its rows; with a block per row, those
+// of all but the adapter's first row leave (n = 0).  count_lds: two ints per wave.
+__device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int* count_lds) {
+  LoraRows r{-1, 0, nullptr, 0, 0};
   if (p.planned) {
-    const int t = grp;
-    if (t >= p.plan.ntile[0]) return r;
-    const GroupTile q = p.plan.tiles[t];
+    if (grp >= p.plan.ntile[0]) return r;
+    const GroupTile q = p.plan.tiles[grp];
     r.a = q.group < p.n_adapters ? q.group : -1;
     r.n = q.rows;
     r.perm = p.plan.perm + q.first;
@@ -67,11 +67,18 @@ __device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int* c
   }
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = blockDim.x >> 6;
   auto norm = [&](int id) { return id < 0 || id >= p.n_adapters ? -1 : id; };
-  const int a = p.by_row ? norm(p.adapter[grp]) : grp < p.n_adapters ? grp : -1;
+  if (p.M <= 64) {                   // every wave sees the whole index
+    const int mine = norm(p.adapter[lane < p.M ? lane : 0]);
+    r.a = p.by_row ? __builtin_amdgcn_readlane(mine, grp) : grp < p.n_adapters ? grp : -1;
+    r.mask = __ballot(lane < p.M && mine == r.a);
+    r.n = p.by_row && __builtin_ctzll(r.mask) != grp ? 0 : __popcll(r.mask);
+    return r;
+  }
+  r.a = p.by_row ? norm(p.adapter[grp]) : grp < p.n_adapters ? grp : -1;
   const int s0 = wv * p.M / nw, s1 = (wv + 1) * p.M / nw;
   int cnt = 0, first = 0x7FFFFFFF;
   for (int s = s0; s < s1; s += 64) {
-    const uint64_t m = __ballot(s + lane < s1 && norm(p.adapter[s + lane < s1 ? s + lane : s0]) == a);
+    const uint64_t m = __ballot(s + lane < s1 && norm(p.adapter[s + lane < s1 ? s + lane : s0]) == r.a);
     if (m && first == 0x7FFFFFFF) first = s + __builtin_ctzll(m);
     cnt += __popcll(m);
   }
@@ -82,24 +89,28 @@ __device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int* c
   __syncthreads();
   int n = 0, f = 0x7FFFFFFF;
   for (int w = 0; w < nw; ++w) {
-    if (w < wv) before += count_lds[w];
+    if (w < wv) r.before += count_lds[w];
     n += count_lds[w];
     f = count_lds[nw + w] < f ? count_lds[nw + w] : f;
   }
-  r.a = a;
   r.n = p.by_row && f != grp ? 0 : n;
   return r;
 }
 
 // Rows r0 .. r0 + 15 of the block's into list[16]; the caller synchronises.
-__device__ __forceinline__ void lora_list(const LoraArgs& p, const LoraRows& r, int before, int r0, int* list) {
+__device__ __forceinline__ void lora_list(const LoraArgs& p, const LoraRows& r, int r0, int* list) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, nw = blockDim.x >> 6;
   if (r.perm) {
     if (threadIdx.x < 16 && r0 + (int)threadIdx.x < r.n) list[threadIdx.x] = r.perm[r0 + threadIdx.x];
     return;
   }
+  if (p.M <= 64) {                   // every wave writes the same
+    const int rank = __popcll(r.mask & ((1ull << lane) - 1));
+    if (((r.mask >> lane) & 1) && rank >= r0 && rank < r0 + 16) list[rank - r0] = lane;
+    return;
+  }
   const int s0 = wv * p.M / nw, s1 = (wv + 1) * p.M / nw;
-  int run = before;
+  int run = r.before;
   for (int s = s0; s < s1; s += 64) {
     const int id = p.adapter[s + lane < s1 ? s + lane : s0];
     const bool hit = s + lane < s1 && (id < 0 || id >= p.n_adapters ? -1 : id) == r.a;
@@ -117,42 +128,49 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& p, int a) {
 }
 
 // Steps of 64 channels whose loads are in flight together in a wave of the
-// shrink, by the number of 16-rank blocks (registers).
-template <int RB>
-constexpr int lora_unroll() { return RB <= 1 ? 4 : RB <= 2 ? 4 : RB <= 4 ? 2 : 1; }
+// shrink, for MT 16-row and RB 16-rank blocks (registers).
+template <int MT, int RB>
+constexpr int lora_unroll() { return MT + RB <= 2 ? 8 : MT + RB <= 3 ? 4 : MT + RB <= 6 ? 2 : 1; }
 
-// acc[i] += 16 rows (xr: this lane's row) x ranks 16 i .. 16 i + 15 over the
-// steps k0, k0 + stride, ... < k1 of 64 channels: lane (row or rank l % 16,
+// acc[t][i] += 16 rows (xr[t]: this lane's row) x ranks 16 i .. 16 i + 15 over
+// the steps k0, k0 + stride, ... < k1 of 64 channels: lane (row or rank l % 16,
 // b = l / 16) holds channels 16 b .. 16 b + 15 of a step, so a row's 64
 // channels are one 128-byte line.
-template <int DT, int RB>
-__device__ __forceinline__ void lora_shrink_steps(const LoraArgs& p, const uint16_t* xr, const uint16_t* A, int rank,
-                                                  int k0, int k1, int stride, f32x4 (&acc)[RB]) {
-  constexpr int U = lora_unroll<RB>();
+template <int DT, int MT, int RB>
+__device__ __forceinline__ void lora_shrink_steps(const LoraArgs& p, const uint16_t* const (&xr)[MT], const uint16_t* A,
+                                                  int rank, int k0, int k1, int stride, f32x4 (&acc)[MT][RB]) {
+  constexpr int U = lora_unroll<MT, RB>();
   const int lane = threadIdx.x & 63, rl = lane & 15, b = lane >> 4;
   // rows past the rank repeat the first (from the cache); their results are dropped
   const uint16_t* ar[RB];
 #pragma unroll
   for (int i = 0; i < RB; ++i) ar[i] = A + (int64_t)(i * 16 + rl < rank ? i * 16 + rl : 0) * p.K;
   // whole: every step lies inside the range and inside K, so no load is guarded
+  constexpr int CH = RB > 8 ? 1 : 2;               // halves of a step loaded together
   auto steps = [&](int s, auto whole) {
-    u32x4 xv[U][2], av[U][RB][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int c0 = 0; c0 < 2; c0 += CH) {
+      u32x4 xv[U][MT][CH], av[U][RB][CH];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int k = (s + u * stride) * 64 + b * 16 + 8 * c;
-        const bool in = decltype(whole)::value || (s + u * stride < k1 && k < p.K);
-        xv[u][c] = in ? ldg128(xr + k) : u32x4{0, 0, 0, 0};
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < RB; ++i) av[u][i][c] = in ? ldg128(ar[i] + k) : u32x4{0, 0, 0, 0};
-      }
+        for (int c = 0; c < CH; ++c) {
+          const int k = (s + u * stride) * 64 + b * 16 + 8 * (c0 + c);
+          const bool in = decltype(whole)::value || (s + u * stride < k1 && k < p.K);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+          for (int t = 0; t < MT; ++t) xv[u][t][c] = in ? ldg128(xr[t] + k) : u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < RB; ++i)
+          for (int i = 0; i < RB; ++i) av[u][i][c] = in ? ldg128(ar[i] + k) : u32x4{0, 0, 0, 0};
+        }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) acc[i] = mfma16<DT>(xv[u][c], av[u][i][c], acc[i]);
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) acc[t][i] = mfma16<DT>(xv[u][t][c], av[u][i][c], acc[t][i]);
+    }
   };
   for (int s = k0; s < k1; s += U * stride) {
     if (s + (U - 1) * stride < k1 && (s + (U - 1) * stride + 1) * 64 <= p.K) steps(s, std::true_type{});
@@ -160,73 +178,80 @@ __device__ __forceinline__ void lora_shrink_steps(const LoraArgs& p, const uint1
   }
 }
 
-// h[part][m][r] for 16 rows of an adapter at a time; the four waves share the
-// block's K range.  RB: 16-rank blocks.
-template <int DT, int RB>
-__global__ __launch_bounds__(256) void k_lora_shrink(const LoraArgs p) {
-  __shared__ int list[16];
-  __shared__ int count[8];
-  __shared__ float red[RB < 4 ? RB : 4][4][256];
-  constexpr int RG = RB < 4 ? RB : 4;              // rank blocks that meet in LDS together
+// h[part][m][r] for 16 MT rows of an adapter at a time; the block's eight
+// waves share its K range.  Planned, a block takes a whole tile with MT = 4,
+// so that A is read once per 64 rows, or a quarter of one with MT = 1.
+constexpr int kShrinkWaves = 8;
+template <int DT, int MT, int RB>
+__global__ __launch_bounds__(kShrinkWaves * 64) void k_lora_shrink(const LoraArgs p) {
+  constexpr int W = kShrinkWaves, RG = RB < 4 ? RB : 4;   // rank blocks that meet in LDS together
+  __shared__ int list[16 * MT];
+  __shared__ int count[2 * W];
+  __shared__ float red[RG][W][256];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
-  int before;
   const int bx = (int)(blockIdx.x % (unsigned)p.ksplit), by = (int)(blockIdx.x / (unsigned)p.ksplit);
-  const LoraRows r = lora_rows(p, p.planned ? by >> 2 : by, count, before);
+  constexpr int kSub = kLoraTile / (16 * MT);      // blocks per tile of the plan
+  const LoraRows r = lora_rows(p, p.planned ? by / kSub : by, count);
   if (r.a < 0 || r.n == 0) return;
   const int rank = lora_rank(p, r.a);
   const int steps = (p.K + 63) >> 6;
-  const int part = bx * 4 + wv, parts = p.ksplit * 4;
+  const int part = bx * W + wv, parts = p.ksplit * W;
   const int k0 = (int)((int64_t)part * steps / parts), k1 = (int)((int64_t)(part + 1) * steps / parts);
   const uint16_t* A = p.a + (int64_t)r.a * p.R * p.K;
-  const int rstart = p.planned ? (by & 3) * 16 : 0;
-  const int rend = p.planned && rstart + 16 < r.n ? rstart + 16 : r.n;
-  for (int r0 = rstart; r0 < rend; r0 += 16) {
-    lora_list(p, r, before, r0, list);
-    __syncthreads();
-    const int nr = rend - r0 < 16 ? rend - r0 : 16;
-    const uint16_t* xr = p.x + (int64_t)list[rl < nr ? rl : 0] * p.ldx;
-    f32x4 acc[RB];
+  const int rstart = p.planned ? by % kSub * 16 * MT : 0;
+  const int rend = p.planned && rstart + 16 * MT < r.n ? rstart + 16 * MT : r.n;
+  for (int r0 = rstart; r0 < rend; r0 += 16 * MT) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    lora_shrink_steps<DT, RB>(p, xr, A, rank, k0, k1, 1, acc);
+    for (int t = 0; t < MT; ++t) lora_list(p, r, r0 + 16 * t, list + 16 * t);
+    __syncthreads();
+    const int nr = rend - r0 < 16 * MT ? rend - r0 : 16 * MT;
+    const uint16_t* xr[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xr[t] = p.x + (int64_t)list[16 * t + rl < nr ? 16 * t + rl : 0] * p.ldx;
+    f32x4 acc[MT][RB];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < RB; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    lora_shrink_steps<DT, MT, RB>(p, xr, A, rank, k0, k1, 1, acc);
     // result lane: rank l % 16, rows 4 b + v; the waves' parts in wave order
     float* h = p.h + (int64_t)bx * p.M * p.R;
 #pragma unroll
-    for (int i0 = 0; i0 < RB; i0 += RG) {
-      if (i0 * 16 < rank) {
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int i = 0; i < RG; ++i)
+      for (int i0 = 0; i0 < RB; i0 += RG) {
+        if (i0 * 16 < rank && 16 * t < nr) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) red[i][wv][(4 * b + v) * 16 + rl] = acc[i0 + i][v];
-        __syncthreads();
+          for (int i = 0; i < RG; ++i)
 #pragma unroll
-        for (int i = 0; i < RG; ++i) {
-          const int row = tid >> 4, rr = (i0 + i) * 16 + (tid & 15);
-          if (row < nr && rr < rank)
-            h[(int64_t)list[row] * p.R + rr] = ((red[i][0][tid] + red[i][1][tid]) + red[i][2][tid]) + red[i][3][tid];
+            for (int v = 0; v < 4; ++v) red[i][wv][(4 * b + v) * 16 + rl] = acc[t][i0 + i][v];
+          __syncthreads();
+          for (int j = tid; j < RG * 256; j += W * 64) {
+            const int i = j >> 8, row = 16 * t + ((j >> 4) & 15), rr = (i0 + i) * 16 + (j & 15);
+            if (row < nr && rr < rank) {
+              float o = red[i][0][j & 255];
+#pragma unroll
+              for (int k = 1; k < W; ++k) o += red[i][k][j & 255];
+              h[(int64_t)list[row] * p.R + rr] = o;
+            }
+          }
+          __syncthreads();
         }
-        __syncthreads();
       }
-    }
     __syncthreads();                               // list is free again (also with rank 0)
   }
 }
 
 // One row of h as the sum of two 16-bit values, scaled by a power of two: 16
-// threads per row (j = thread % 16), get(r) gives rank r.  Writes ranks 0 ..
-// pad - 1 (zeros past the rank) and scaling / the power of two.
-template <int DT, int NI, typename F>
-__device__ __forceinline__ void lora_split_row(int j, int rank, int pad, float sc, uint16_t* hi, uint16_t* lo, float* back, F get) {
-  float v[NI];
+// threads per row, thread j of them holding ranks j, j + 16, ... in v (zeros
+// past the rank).  Writes ranks 0 .. pad - 1 and scaling / the power of two.
+template <int DT, int NI>
+__device__ __forceinline__ void lora_split_row(int j, int pad, float sc, uint16_t* hi, uint16_t* lo, float* back, const float (&v)[NI]) {
   float am = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = i * 16 + j;
-    v[i] = r < rank ? get(r) : 0.0f;
-    am = fmaxf(am, fabsf(v[i]));
-  }
+  for (int i = 0; i < NI; ++i) am = fmaxf(am, fabsf(v[i]));
   am = fmaxf(am, quad_xor1(am));
   am = fmaxf(am, quad_xor2(am));
   am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
@@ -367,9 +392,8 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
-  int before;
   const int bx = (int)(blockIdx.x % (unsigned)p.nx), by = (int)(blockIdx.x / (unsigned)p.nx);
-  const LoraRows r = lora_rows(p, by, count, before);
+  const LoraRows r = lora_rows(p, by, count);
   if (r.n == 0) return;
   const int rank = r.a < 0 ? 0 : lora_rank(p, r.a);
   const int rk = (rank + 31) >> 5;
@@ -385,20 +409,38 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
   for (int r0 = 0; r0 < r.n; r0 += PR) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < PR; i += 16) lora_list(p, r, before, r0 + i, list + i);
+    for (int i = 0; i < PR; i += 16) lora_list(p, r, r0 + i, list + i);
     __syncthreads();
     const int nr = r.n - r0 < PR ? r.n - r0 : PR;
+    LoraOut<YDT, 4> out[PR / 16];                  // base, on its way while h is staged
+#pragma unroll
+    for (int t = 0; t < PR; t += 16)
+      if (t + rl < nr) out[t / 16].load(p, list[t + rl], cl);
     if (rank > 0) {
-      // 16 threads per row; the K parts are added in their order
+      // 16 threads per row; the K parts, four at a time, are added in their order
       const int64_t pitch = (int64_t)p.M * p.R;
       for (int row = tid >> 4; row < (nr + 15) / 16 * 16; row += 16) {
         const float* h = p.h + (int64_t)list[row < nr ? row : 0] * p.R;
-        lora_split_row<DT, RK * 2>(tid & 15, rank, rk * 32, sc, hs[0][row], hs[1][row], back + row, [&](int rr) {
-          float v = 0.0f;
-#pragma unroll 8
-          for (int s = 0; s < p.ksplit; ++s) v += h[s * pitch + rr];
-          return v;
-        });
+        float v[RK * 2];
+#pragma unroll
+        for (int i = 0; i < RK * 2; ++i) v[i] = 0.0f;
+        for (int s0 = 0; s0 < p.ksplit; s0 += 4) {
+          float g[4][RK * 2];
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < RK * 2; ++i) {
+              const int rr = i * 16 + (tid & 15);
+              const bool in = s0 + s < p.ksplit && rr < rank;
+              const float f = h[in ? (s0 + s) * pitch + rr : 0];
+              g[s][i] = in ? f : 0.0f;
+            }
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < RK * 2; ++i) v[i] += g[s][i];
+        }
+        lora_split_row<DT, RK * 2>(tid & 15, rk * 32, sc, hs[0][row], hs[1][row], back + row, v);
       }
     }
     __syncthreads();
@@ -406,9 +448,6 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
     for (int t = 0; t < PR; t += 16) {
       if (t >= nr) break;
       const int row = t + rl;
-      LoraOut<YDT, 4> out;
-      const int64_t m = list[row < nr ? row : 0];
-      if (row < nr) out.load(p, m, cl);
       f32x4 acc[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -424,7 +463,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
           }
         }
       }
-      if (row < nr) out.store(p, m, cl, rank > 0 ? back[row] : 0.0f, acc, rank > 0);
+      if (row < nr) out[t / 16].store(p, list[row], cl, rank > 0 ? back[row] : 0.0f, acc, rank > 0);
     }
   }
 }
@@ -444,9 +483,8 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
-  int before;
   const int bx = (int)(blockIdx.x % (unsigned)p.nx), by = (int)(blockIdx.x / (unsigned)p.nx);
-  const LoraRows r = lora_rows(p, by, count, before);
+  const LoraRows r = lora_rows(p, by, count);
   if (r.n == 0) return;
   const int rank = r.a < 0 ? 0 : lora_rank(p, r.a);
   const int rk = (rank + 31) >> 5;
@@ -459,23 +497,24 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
   for (int s = 0; s < RK; ++s) w[s] = lora_b(p, B, c0 + rl, s * 32 + 8 * b, rank);
   for (int r0 = 0; r0 < r.n; r0 += 16) {
     __syncthreads();
-    lora_list(p, r, before, r0, list);
+    lora_list(p, r, r0, list);
     __syncthreads();
     const int nr = r.n - r0 < 16 ? r.n - r0 : 16;
     LoraOut<YDT, 1> out;
     const int64_t m = list[rl < nr ? rl : 0];
     if (rl < nr) out.load(p, m, c0 + 4 * b);
     if (rank > 0) {
-      f32x4 acc[RB];
+      f32x4 acc[1][RB];
 #pragma unroll
-      for (int i = 0; i < RB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      lora_shrink_steps<DT, RB>(p, p.x + m * p.ldx, A, rank, wv, (p.K + 63) >> 6, 8, acc);
+      for (int i = 0; i < RB; ++i) acc[0][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      const uint16_t* const xr[1] = {p.x + m * p.ldx};
+      lora_shrink_steps<DT, 1, RB>(p, xr, A, rank, wv, (p.K + 63) >> 6, 8, acc);
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
         if (i * 16 < rank) {
           __syncthreads();
 #pragma unroll
-          for (int v = 0; v < 4; ++v) red[wv][(4 * b + v) * 16 + rl] = acc[i][v];
+          for (int v = 0; v < 4; ++v) red[wv][(4 * b + v) * 16 + rl] = acc[0][i][v];
           __syncthreads();
           if (tid < 256) {
             float t = red[0][tid];
@@ -487,9 +526,11 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
       }
       __syncthreads();
       if (tid < 256) {
-        const int row = tid >> 4;
-        lora_split_row<DT, RK * 2>(tid & 15, rank, rk * 32, sc, hs[0][row], hs[1][row], back + row,
-                                   [&](int rr) { return hv[row][rr]; });
+        const int row = tid >> 4, j = tid & 15;
+        float v[RK * 2];
+#pragma unroll
+        for (int i = 0; i < RK * 2; ++i) v[i] = i * 16 + j < rank ? hv[row][i * 16 + j] : 0.0f;
+        lora_split_row<DT, RK * 2>(j, rk * 32, sc, hs[0][row], hs[1][row], back + row, v);
       }
       __syncthreads();
     }
@@ -523,10 +564,10 @@ static bool lora_one(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_
 }
 
 static int lora_ksplit(int64_t M, int64_t K, int64_t n_adapters) {
-  const int64_t blocks = lora_planned(M) ? (M + 15) / 16 : lora_groups(M, n_adapters);
+  const int64_t blocks = lora_planned(M) ? (M + kLoraTile - 1) / kLoraTile : lora_groups(M, n_adapters);
   const int64_t steps = (K + 63) / 64;
-  int64_t want = 512 / blocks;                     // about two blocks per compute unit
-  if (want > steps / 4) want = steps / 4;          // a step per wave at least
+  int64_t want = 256 / blocks;                     // about a block per compute unit
+  if (want > steps / kShrinkWaves) want = steps / kShrinkWaves;   // a step per wave at least
   if (want > kLoraMaxSplit) want = kLoraMaxSplit;
   return want < 1 ? 1 : (int)want;
 }
@@ -584,12 +625,20 @@ hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st) {
       return;
     }
     if (c.n_adapters > 0) {
-      const dim3 sg((unsigned)p.ksplit * (p.planned ? gy * 4 : gy));
-      if (c.R <= 16) hipLaunchKernelGGL((k_lora_shrink<DT, 1>), sg, dim3(256), 0, st, p);
-      else if (c.R <= 32) hipLaunchKernelGGL((k_lora_shrink<DT, 2>), sg, dim3(256), 0, st, p);
-      else if (c.R <= 64) hipLaunchKernelGGL((k_lora_shrink<DT, 4>), sg, dim3(256), 0, st, p);
-      else if (c.R <= 128) hipLaunchKernelGGL((k_lora_shrink<DT, 8>), sg, dim3(256), 0, st, p);
-      else hipLaunchKernelGGL((k_lora_shrink<DT, 16>), sg, dim3(256), 0, st, p);
+      auto shrink = [&](auto mt, auto rb) {
+        constexpr int MT = decltype(mt)::value, RB = decltype(rb)::value;
+        const dim3 sg((unsigned)p.ksplit * (p.planned ? gy * (kLoraTile / (16 * MT)) : gy));
+        hipLaunchKernelGGL((k_lora_shrink<DT, MT, RB>), sg, dim3(kShrinkWaves * 64), 0, st, p);
+      };
+      auto ranked = [&](auto mt) {
+        if (c.R <= 16) shrink(mt, std::integral_constant<int, 1>{});
+        else if (c.R <= 32) shrink(mt, std::integral_constant<int, 2>{});
+        else shrink(mt, std::integral_constant<int, 4>{});
+      };
+      if (c.R > 128) shrink(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
+      else if (c.R > 64) shrink(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+      else if (p.planned) ranked(std::integral_constant<int, 4>{});
+      else ranked(std::integral_constant<int, 1>{});
     }
     auto expand = [&](auto pr) {
       constexpr int PR = decltype(pr)::value;
