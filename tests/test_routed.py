@@ -242,6 +242,10 @@ PRODUCTS = [
     (700, 3, 2, 512, 390, 256, "bf16", "f32", ""),
     (260, 2, 2, 128, 514, 128, "f16", "f32", "one"),
     (1030, 16, 8, 192, 70, 64, "bf16", "bf16", "holes"),
+    (40, 9, 2, 2176, 34, 128, "bf16", "f32", "holes"),
+    (5, 40, 40, 576, 70, 64, "bf16", "f32", ""),
+    (3001, 5, 3, 128, 66, 128, "f16", "f32", "holes"),
+    (4099, 3, 2, 64, 18, 64, "bf16", "f32", "one"),
 ]
 
 
@@ -402,6 +406,8 @@ LORAS = [
     (900, 3, 32, 128, 259, "f16", "f32", True, True, True, "runs"),
     (1100, 600, 8, 64, 40, "f16", "f32", False, False, False, "mixed"),
     (600, 1, 72, 96, 64, "bf16", "f32", False, True, True, "none"),
+    (9000, 7, 8, 64, 40, "f16", "f32", True, True, True, "mixed"),
+    (5000, 1100, 16, 72, 24, "bf16", "f32", False, True, False, "runs"),
 ]
 
 

@@ -4,8 +4,8 @@
 //
 //   z[slot][n] = sum_g D[n][g] sum_{k in g} (q[n][k] - z[n][g]) x[row(slot)][k]
 //
-//  * k_experts_prep (one launch): block 0 sorts the slots by expert and lists
-//    the row tiles; the others convert the activation rows to fp16 (scaled by a
+//  * k_experts_prep: the first block (many slots: blocks, put together by a
+//    second launch) sorts the slots by expert and lists the row tiles; the others convert the activation rows to fp16 (scaled by a
 //    power of two per row, in the order the unpack yields), lay the steps and
 //    zero points out group by group, and zero the output rows of slots without
 //    an expert.
@@ -15,7 +15,8 @@
 //    gathered by the copies' addresses.  v_mfma_f32_16x16x32_f16 multiplies the
 //    activations with the exact integers (q - z) 2^-9.  The accumulators hold
 //    the sum in units of the current group's step: a new group multiplies them
-//    by D[g - 1] / D[g] (fp32, one multiplication per value and group) and the
+//    by D[g - 1] / D[g] (fp32, one multiplication per value and group; the
+//    hardware's reciprocal is within 1 unit in the last place) and the
 //    epilogue by the last step.  So no operand is rounded, unlike step (q - z)
 //    in fp16 (1e-4 of every result), and no second set of accumulators is
 //    needed.  Unpacking costs 9 vector instructions per eight codes; a wave's
@@ -54,7 +55,7 @@ struct GemmArgs {
   // workspace
   uint16_t* xq;                                    // [xrows][K]
   int* pexp;                                       // [xrows]
-  uint2* ctab;                                     // [E][K / unit][N]: D[u - 1] / D[u], -z 2^-9 twice
+  uint32_t* ctab;                                  // [E][K / unit][N]: D | -z 2^-9 << 16, both fp16
   GroupPlan plan;
   // first block of each part of the preparation
   int b_rows, b_consts, b_zero;
@@ -108,49 +109,69 @@ __global__ __launch_bounds__(kPlanThreads) void k_experts_prep(const GemmArgs p,
   extern __shared__ int prep_lds[];
   const int bid = blockIdx.x, tid = threadIdx.x;
   if (bid < p.b_rows) {
-    group_plan_block(p.ids, p.S, p.E, tile_rows, p.plan, prep_lds);
+    group_sort_block(p.ids, p.S, p.E, bid, p.b_rows, p.plan, prep_lds);
+    if (p.b_rows == 1) {
+      __syncthreads();
+      group_place_block(p.ids, p.S, p.E, 0, 1, tile_rows, p.plan, prep_lds);
+    }
   } else if (bid < p.b_consts) {
     const int64_t row = (int64_t)(bid - p.b_rows) * 16 + (tid >> 6);
     if (row < p.xrows) prep_row<DT>(p, row);
   } else if (bid < p.b_zero) {
-    // a thread takes eight units of one row of the [E N] stack; a step of 0
-    // counts as 2^-40 so that the ratios stay finite
-    const int U = (int)(p.K / p.unit), sh = p.group == 256 ? 1 : 0;
-    const int G = (int)(p.K / p.group);
+    // a thread takes eight groups of one row of the [E N] stack
+    const int G = (int)(p.K / p.group), U = (int)(p.K / p.unit), sh = p.group == 256 ? 1 : 0;
     const int64_t i = (int64_t)(bid - p.b_consts) * kPlanThreads + tid;
-    const int64_t rows = (int64_t)p.E * p.N, n = i % rows;
-    const int u0 = (int)(i / rows) * 8;
-    if (u0 >= U) return;
+    const int64_t n = i / ((G + 7) / 8);
+    const int g0 = (int)(i - n * ((G + 7) / 8)) * 8;
+    if (n >= (int64_t)p.E * p.N) return;
     const int64_t e = n / p.N, r = n - e * p.N;
-    const uint16_t* s = p.scales + n * G;
-    const uint8_t* z = p.zeros + n * G;
-    float d[9];
-    uint32_t zz[8];
-    d[0] = u0 ? f16_to_f32(s[(u0 - 1) >> sh]) : 0.0f;
+    const uint16_t* s = p.scales + n * G + g0;
+    const uint8_t* z = p.zeros + n * G + g0;
+    uint32_t sv[8], zv[8];
+    if ((G & 7) == 0 && (uintptr_t)p.scales % 16 == 0 && (uintptr_t)p.zeros % 8 == 0) {
+      const u32x4 s8 = ldg128(s);
+      const uint2 z8 = *reinterpret_cast<const uint2*>(z);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int g = (u0 + j < U ? u0 + j : U - 1) >> sh;
-      d[j + 1] = f16_to_f32(s[g]);
-      zz[j] = z[g];
+      for (int j = 0; j < 8; ++j) {
+        sv[j] = (s8[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+        zv[j] = ((j < 4 ? z8.x : z8.y) >> (8 * (j & 3))) & 0xFFu;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = g0 + j < G ? j : 0;
+        sv[j] = s[k];
+        zv[j] = z[k];
+      }
     }
+    uint32_t* c = p.ctab + (e * U + ((int64_t)g0 << sh)) * p.N + r;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (u0 + j < U)
-        p.ctab[(e * U + u0 + j) * p.N + r] = make_uint2(
-            __float_as_uint(fmaxf(d[j], 0x1p-40f) / fmaxf(d[j + 1], 0x1p-40f)), experts_nz(zz[j]));
+      if (g0 + j < G) {
+        const uint32_t v = sv[j] | (experts_nz(zv[j]) & 0xFFFF0000u);
+        c[((int64_t)j << sh) * p.N] = v;
+        if (sh) c[(((int64_t)j << sh) + 1) * p.N] = v;
+      }
   } else {
     const int64_t slot = (int64_t)(bid - p.b_zero) * 16 + (tid >> 6);
     if (slot >= p.S) return;
     const int id = p.ids[slot];
     if (id >= 0 && id < p.E) return;
-    for (int64_t c = tid & 63; c < cols; c += 64) store_out(p.y, p.ydt, slot * p.ldy + c, 0.0f);
+    const int es = p.ydt == DT_F32 ? 4 : 2, q = 16 / es;   // whole 16 bytes where the rows allow it
+    uint8_t* y = reinterpret_cast<uint8_t*>(p.y) + slot * p.ldy * es;
+    int64_t c = 0;
+    if (p.ldy % q == 0 && (uintptr_t)p.y % 16 == 0) {
+      c = cols / q * q;
+      for (int64_t i = tid & 63; i < cols / q; i += 64) *reinterpret_cast<u32x4*>(y + i * 16) = u32x4{0, 0, 0, 0};
+    }
+    for (c += tid & 63; c < cols; c += 64) store_out(p.y, p.ydt, slot * p.ldy + c, 0.0f);
   }
 }
 
 template <int MODE, int MB, int SPG>
 __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   constexpr int BM = 16 * MB, HB = MB / 2;         // rows, 16-row blocks per sub-step
-  constexpr int kA = BM * kGemmK * 2, kB = kGemmN * 32, kC = kGemmN * 8, kStage = kA + kB + kC;
+  constexpr int kA = BM * kGemmK * 2, kB = kGemmN * 32, kC = kGemmN * 4, kStage = kA + kB + kC;
   constexpr int kAc = BM / 32;                     // A copies per wave and stage
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -187,12 +208,12 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   };
 
   // ---- copies: A rows of 128 bytes, 8 per copy, chunk c of row r at c ^ (r & 7);
-  // B per 32 columns the first then the last 16 bytes of each; C two entries a lane
+  // B per 32 columns the first then the last 16 bytes of each; C four entries a lane
   const int64_t G = p.K / p.group;
   const i32x4 ars = rsrc4(p.xq, (uint32_t)(p.xrows * p.K * 2));
   const i32x4 brs = rsrc4(reinterpret_cast<const uint8_t*>(p.qw) + (int64_t)e * p.N * (p.K >> 1), (uint32_t)(p.N * (p.K >> 1)));
   const int64_t U = p.K / p.unit;
-  const i32x4 crs = rsrc4(p.ctab + (int64_t)e * U * p.N, (uint32_t)(U * p.N * 8));
+  const i32x4 crs = rsrc4(p.ctab + (int64_t)e * U * p.N, (uint32_t)(U * p.N * 4));
   uint32_t aoff[kAc];
 #pragma unroll
   for (int u = 0; u < kAc; ++u) {
@@ -205,8 +226,8 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
     const int64_t n = wrow(64 * wv + 32 * u + (lane & 31));
     boff[u] = n < 0 ? kBufferOob : (uint32_t)(n * (p.K >> 1)) + (uint32_t)((lane >> 5) * 16);
   }
-  const int64_t cn = wv < 2 ? wrow(128 * wv + 2 * lane) : -1;
-  const uint32_t coff = cn < 0 ? kBufferOob : (uint32_t)(cn * 8);
+  const int64_t cn = wrow(4 * lane);
+  const uint32_t coff = cn < 0 ? kBufferOob : (uint32_t)(cn * 4);
   const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   const int S = (int)(p.K / kGemmK);
   // part q of stage s's copies into buffer buf: the A copies q, q + 4, ..., and
@@ -219,13 +240,13 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
     if (q == 2) dma16(brs, lb + kA + (uint32_t)wv * 2048, boff[0], (uint32_t)s * 32);
     if (q == 3) {
       dma16(brs, lb + kA + (uint32_t)wv * 2048 + 1024, boff[1], (uint32_t)s * 32);
-      if (wv < 2) dma16(crs, lb + kA + kB + (uint32_t)wv * 1024, coff, (uint32_t)(s / SPG) * (uint32_t)(p.N * 8));
+      if (wv == 0) dma16(crs, lb + kA + kB, coff, (uint32_t)(s / SPG) * (uint32_t)(p.N * 4));
     }
   };
   // every LDS access of this wave done, and all copies but the newest stage's
   auto wait_stage = [&](bool newest) {
     if (!newest) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-    else if (wv < 2) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kAc + 3));
+    else if (wv == 0) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kAc + 3));
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kAc + 2));
   };
 
@@ -235,13 +256,14 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  uint2 w[4], cz[4];                               // a stage's words and constants of the lane's columns
+  uint2 w[4];                                      // a stage's words of the lane's columns
+  uint32_t cz[4];                                  // and constants
   auto load_w = [&](const uint8_t* base) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const int col = wv * 64 + n * 16 + rl;
       w[n] = *reinterpret_cast<const uint2*>(base + kA + (col >> 5) * 1024 + (b >> 1) * 512 + (col & 31) * 16 + (b & 1) * 8);
-      cz[n] = *reinterpret_cast<const uint2*>(base + kA + kB + col * 8);
+      cz[n] = *reinterpret_cast<const uint32_t*>(base + kA + kB + col * 4);
     }
   };
   // fragments of sub-step q = 2 st + hh: k32 step st, row blocks HB hh ..
@@ -253,7 +275,8 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
     }
   };
   u32x4 aE[HB], aO[HB], bq[4];
-  float ratio[4];
+  float ratio[4], last[4] = {1.0f, 1.0f, 1.0f, 1.0f};   // D of the last unit / this unit's; the last unit's
+  auto nz = [&](int n) { return (cz[n] >> 16) * 0x10001u; };
 #pragma unroll
   for (int q = 0; q < 4; ++q) copy(0, 0, q);
   if (S > 1)
@@ -264,7 +287,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   load_a(lds, 0, aE);
   load_w(lds);
 #pragma unroll
-  for (int n = 0; n < 4; ++n) bq[n] = experts_unpack(w[n].x, cz[n].y);
+  for (int n = 0; n < 4; ++n) bq[n] = experts_unpack(w[n].x, nz(n));
 
   // A stage runs in four sub-steps.  In sub-step 1 a column's operands are
   // replaced by step 1's once its last product of step 0 is issued, in
@@ -281,7 +304,11 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
       const uint8_t* ahead = lds + nxt * kStage;
       if (i == 0) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) ratio[n] = __uint_as_float(cz[n].x);
+        for (int n = 0; n < 4; ++n) {
+          const float d = fmaxf(f16_to_f32(cz[n] & 0xFFFFu), 0x1p-40f);   // a step of 0 keeps the ratios finite
+          ratio[n] = last[n] * __builtin_amdgcn_rcpf(d);
+          last[n] = d;
+        }
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -308,7 +335,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
             }
             c = mfma16h(a[m], bq[n], c);
           }
-          if (q & 1) bq[n] = experts_unpack(q == 1 ? w[n].y : w[n].x, cz[n].y);
+          if (q & 1) bq[n] = experts_unpack(q == 1 ? w[n].y : w[n].x, nz(n));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -319,12 +346,6 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   // ---- epilogue: the last group's step, then 16 rows at a time through the
   // wave's LDS area and out in whole row pieces.  Result lane: column l % 16,
   // rows 4 b + v.
-  float step[4];
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int64_t r = wrow(wv * 64 + n * 16 + rl);
-    step[n] = r < 0 ? 0.0f : fmaxf(f16_to_f32(p.scales[((int64_t)e * p.N + r) * G + G - 1]), 0x1p-40f) * 512.0f;
-  }
   __syncthreads();                                 // every wave is done with the stages
   constexpr int kW = MODE == EXPERTS_SWIGLU ? 32 : 64;                    // outputs per row of the wave
   float* stg = reinterpret_cast<float*>(lds) + wv * 16 * (kW + 4);
@@ -335,15 +356,15 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int r = r0 + 4 * b + v;
-      const int pe = r < rows ? -p.pexp[xrow(perm[r])] : 0;
+      const int pe = r < rows ? 9 - p.pexp[xrow(perm[r])] : 0;   // and the operands' 2^-9
       float* d = stg + (4 * b + v) * (kW + 4) + rl;
       if constexpr (MODE == EXPERTS_SWIGLU) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          d[16 * h] = swiglu(ldexpf(acc[m][2 * h][v] * step[2 * h], pe), ldexpf(acc[m][2 * h + 1][v] * step[2 * h + 1], pe));
+          d[16 * h] = swiglu(ldexpf(acc[m][2 * h][v] * last[2 * h], pe), ldexpf(acc[m][2 * h + 1][v] * last[2 * h + 1], pe));
       } else {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) d[16 * n] = ldexpf(acc[m][n][v] * step[n], pe);
+        for (int n = 0; n < 4; ++n) d[16 * n] = ldexpf(acc[m][n][v] * last[n], pe);
       }
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): the wave's writes landed
@@ -377,7 +398,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
 
 template <int MODE, int MB>
 void gemm_launch(const GemmArgs& a, const dim3& grid, hipStream_t st) {
-  constexpr size_t lds = 3 * (16 * MB * kGemmK * 2 + kGemmN * 40);
+  constexpr size_t lds = 3 * (16 * MB * kGemmK * 2 + kGemmN * 36);
   if (a.group == 64) hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 1>), grid, dim3(256), lds, st, a);
   else hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 2>), grid, dim3(256), lds, st, a);   // 256: a ratio of 1 between halves
 }
@@ -402,7 +423,7 @@ static GemmSpace gemm_space(bool down, int64_t M, int64_t N, int64_t K, int64_t 
   g.xq = 0;
   g.pexp = g.xq + align_up((size_t)xrows * (size_t)K * 2, 256);
   g.ctab = g.pexp + align_up((size_t)xrows * 4, 256);
-  g.plan = g.ctab + align_up((size_t)E * (size_t)N * (size_t)(K / (group == 64 ? 64 : 128)) * 8, 256);
+  g.plan = g.ctab + align_up((size_t)E * (size_t)N * (size_t)(K / (group == 64 ? 64 : 128)) * 4, 256);
   g.total = g.plan + group_plan_bytes(S, E, gemm_tile_rows(S, E));
   return g;
 }
@@ -439,16 +460,17 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, voi
   a.vec = ldo % 4 == 0 && (uintptr_t)out % (4 * es) == 0;
   a.xq = reinterpret_cast<uint16_t*>(w + g.xq);
   a.pexp = reinterpret_cast<int*>(w + g.pexp);
-  a.ctab = reinterpret_cast<uint2*>(w + g.ctab);
+  a.ctab = reinterpret_cast<uint32_t*>(w + g.ctab);
   a.plan = group_plan_at(w + g.plan, S, c.E, tile);
-  a.b_rows = 1;
+  a.b_rows = group_chunks(S);
   a.b_consts = a.b_rows + (int)((a.xrows + 15) / 16);
-  a.b_zero = a.b_consts + (int)((c.E * c.N * ((c.K / a.unit + 7) / 8) + kPlanThreads - 1) / kPlanThreads);
+  a.b_zero = a.b_consts + (int)((c.E * c.N * ((c.K / c.group + 7) / 8) + kPlanThreads - 1) / kPlanThreads);
   const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
   const unsigned pb = (unsigned)(a.b_zero + (down ? 0 : (S + 15) / 16));
-  if (c.xdt == DT_F16) hipLaunchKernelGGL((k_experts_prep<DT_F16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
-  else hipLaunchKernelGGL((k_experts_prep<DT_BF16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
+  if (c.xdt == DT_F16) hipLaunchKernelGGL((k_experts_prep<DT_F16>), dim3(pb), dim3(kPlanThreads), group_tiles_lds(a.E), st, a, tile, cols);
+  else hipLaunchKernelGGL((k_experts_prep<DT_BF16>), dim3(pb), dim3(kPlanThreads), group_tiles_lds(a.E), st, a, tile, cols);
   hipError_t e = hipGetLastError();
+  if (e == hipSuccess) e = launch_group_place(c.ids, S, c.E, tile, a.plan, st);
   if (e != hipSuccess) return e;
   const int64_t per = c.mode == EXPERTS_SWIGLU ? kGemmN / 2 : kGemmN;
   const int64_t tiles = group_tiles_max(S, c.E, tile) * ((cols + per - 1) / per);
