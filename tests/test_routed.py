@@ -147,6 +147,30 @@ def test_route_close_choices(on_gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("n", [24, 256, 600])
+def test_route_close_choices_under_a_bias(on_gpu, sig, n):
+    """Biases that bring choices within a few double steps of each other, and
+    groups whose values meet."""
+    rng = np.random.default_rng(n)
+    x = np.round(rng.normal(0, 1, (80, n)) * 4) / 4
+    x[:, n // 2:] = x[:, :n // 2]                    # the second half of the groups repeats the first
+    ref = O.route_experts(x, n, None, sig, renormalize=False)
+    score = np.zeros((80, n))
+    np.put_along_axis(score, ref[0], ref[1], axis=1)
+    # pulls the experts of row 0 to one choice, up to the bias's own rounding
+    bias = (0.5 - score[0]).astype(np.float32)
+    xt = torch.from_numpy(x).float()
+    for ng, tg, gt in ((1, 1, 1), (4, 2, 2), (n // 3, n // 6, 1) if n // 3 <= 64 else (8, 3, 1)):
+        got = awq.awq_route_experts(gpu(xt), 5, bias=gpu(torch.from_numpy(bias)), score="sigmoid" if sig else "softmax",
+                                    n_group=ng, topk_group=tg, group_top=gt)
+        compare_route(got, O.route_experts(x, 5, bias, sig, ng, tg, gt), (sig, n, ng))
+        got = awq.awq_route_experts(gpu(xt), 5, score="sigmoid" if sig else "softmax", n_group=ng, topk_group=tg,
+                                    group_top=gt)
+        compare_route(got, O.route_experts(x, 5, None, sig, ng, tg, gt), (sig, n, ng, "no bias"))
+
+
+@pytest.mark.gpu
 def test_route_strided_rows_and_given_outputs(on_gpu):
     big = route_case(40, 100, torch.bfloat16, 9)
     x = gpu(big)[:, 10:74]

@@ -10,6 +10,14 @@
 // maximum over the wave and one ballot, and only a tie of the roundings is
 // settled on the doubles.  Equal choices leave the lowest lane, and the lane's
 // lowest expert, first.
+//
+// The choosing runs in float first (route_float) wherever float can prove the
+// order: without a bias the logits themselves are the keys, with one the
+// choice's float error is far below the distance that two neighbours in the
+// order must have.  A row with a closer call (about one in a hundred) repeats it in
+// doubles.  16384 tokens, 256 experts in 8 groups, top 8 with a bias: 29 us
+// in doubles alone, 25 us with both
+// (issue bound: some thirty instructions per winner, and the scores).
 #include "awq_device.h"
 #include "awq_internal.h"
 
@@ -60,45 +68,259 @@ struct RouteArgs {
   int64_t T, ldl;
   int E;
   const float* bias;
-  int sigmoid, n_group, topk_group, group_top, top_k, renorm;
+  int sigmoid, n_group, gsize, topk_group, group_top, top_k, renorm;   // gsize: experts per group
   float scale;
   int32_t* ids;
   float* weights;
 };
 
-template <int DT, int V>
-__global__ __launch_bounds__(256) void k_route(const RouteArgs p) {
-  constexpr double kNone = -__builtin_inf();
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (t >= p.T) return;
-  const char* row = reinterpret_cast<const char*>(p.logits) + t * p.ldl * (DT == DT_F32 ? 4 : 2);
+// Floats as unsigned integers in the same order (-inf: kNoKey; 0 is below all).
+constexpr uint32_t kNoKey = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t to_key(float f) {
+  const uint32_t b = __float_as_uint(f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_key(uint32_t k) {
+  return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+  return v > o ? v : o;
+}
+// Maximum over the wave, as a scalar: shifts inside the 16-lane rows, the rows'
+// last lanes broadcast onwards, the last lane read.
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
+  v = max_dpp<0x111, 0xF>(v);
+  v = max_dpp<0x112, 0xF>(v);
+  v = max_dpp<0x114, 0xF>(v);
+  v = max_dpp<0x118, 0xF>(v);
+  v = max_dpp<0x142, 0xA>(v);
+  v = max_dpp<0x143, 0xC>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// (a1, a2) and another lane's pair: the two largest of both.
+__device__ __forceinline__ void merge_keys(uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
+  const uint32_t lo = a1 < b1 ? a1 : b1, hi2 = a2 > b2 ? a2 : b2;
+  a1 = a1 > b1 ? a1 : b1;
+  a2 = lo > hi2 ? lo : hi2;
+}
+template <int CTRL>
+__device__ __forceinline__ void merge_keys_dpp(uint32_t& a1, uint32_t& a2) {
+  merge_keys(a1, a2, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a1, CTRL, 0xF, 0xF, false),
+             (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a2, CTRL, 0xF, 0xF, false));
+}
 
-  float l[V];
-  bool ok[V];
+// exp(d + dl) within 2^-21 of the value (dl: the rounding error of d), and
+// within 2^-100 of it where d was held to -100 .. 80.
+__device__ __forceinline__ float exp_f32(float d, float dl) {
+  constexpr float kL = 0x1.715476p+0f, kLl = 0x1.4ae0bep-26f;   // log2(e) = kL + kLl
+  const bool in = d > -100.0f && d < 80.0f;
+  d = in ? d : d > 0.0f ? 80.0f : -100.0f;
+  dl = in ? dl : 0.0f;
+  const float t = d * kL;
+  const float lo = __builtin_fmaf(dl, kL, __builtin_fmaf(d, kLl, __builtin_fmaf(d, kL, -t)));
+  const float r = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(r * 0x1.62e43p-1f, lo, r);
+}
+
+// The choosing in float: lane j gets winner j's expert (-1: none left).
+// Returns false where the order is not certain.  l: -inf where not usable, mx
+// the largest; bias: the lane's.
+template <int V>
+__device__ __forceinline__ bool route_float(const RouteArgs& p, const float (&l)[V], const float (&bias)[V], float mx,
+                                            int& mine) {
+  constexpr float kNone = -__builtin_inff();
+  const int lane = threadIdx.x & 63;
+  const int gs = p.gsize;
+  const bool two = p.n_group > 1 && p.group_top == 2 && gs > 1;
+  const bool scores = p.bias || two;               // else the logits decide
+  uint32_t c[V];
+  float margin = 0.0f;                             // what choices must differ by, but for 2^-21 of themselves
+  if (scores) {
+    float s[V];
+    if (p.sigmoid) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    float f = -__builtin_inff();
-    if (e < p.E) {
-      if constexpr (DT == DT_F32) f = reinterpret_cast<const float*>(row)[e];
-      else f = to_f32<DT>(reinterpret_cast<const uint16_t*>(row)[e]);
+      for (int i = 0; i < V; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + exp_f32(-l[i], 0.0f));
+      margin = 0x1p-18f;
+    } else {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = l[i] - mx, b = d - l[i];   // the difference and its rounding error
+        const float x = exp_f32(d, (l[i] - (d - b)) - (mx + b));
+        s[i] = l[i] > kNone ? x : 0.0f;
+        sum += s[i];
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+      const float r = __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] *= r;
+      margin = r * 0x1p-18f;                       // no score exceeds r
     }
-    ok[i] = f > -__builtin_inff();                 // false for NaN too
-    l[i] = ok[i] ? fminf(f, 3.402823466e+38f) : -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = l[i] > kNone ? to_key(s[i] + bias[i]) : kNoKey;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = to_key(l[i]);
   }
 
-  // ---- scores and choices
-  double c[V];
-  double mx = 0.0, sum = 0.0;
-  if (!p.sigmoid) {
-    float m = l[0];
+  // ---- groups: their values, and whether the cut between the kept and the
+  // others is clear
+  if (p.n_group > 1) {
+    const int lg = gs / V;
+    const bool whole = gs % V == 0 && (lg & (lg - 1)) == 0;   // a group is a power of two of whole lanes
+    uint32_t a1, a2, gv = 0;
+    if (whole) {
+      a1 = c[0];
+      a2 = kNoKey;
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-    mx = (double)wave_max(m);                      // -inf: no expert is usable, every choice below is -inf
+      for (int i = 1; i < V; ++i) merge_keys(a1, a2, c[i], kNoKey);
+      if (lg > 1) merge_keys_dpp<0xB1>(a1, a2);    // lane ^ 1, ^ 2, then mirrors of equal halves
+      if (lg > 2) merge_keys_dpp<0x4E>(a1, a2);
+      if (lg > 4) merge_keys_dpp<0x141>(a1, a2);
+      if (lg > 8) merge_keys_dpp<0x140>(a1, a2);
+      if (lg > 16) merge_keys(a1, a2, (uint32_t)__shfl_xor((int)a1, 16), (uint32_t)__shfl_xor((int)a2, 16));
+      if (lg > 32) merge_keys(a1, a2, (uint32_t)__shfl_xor((int)a1, 32), (uint32_t)__shfl_xor((int)a2, 32));
+      if (two) a1 = to_key(from_key(a1) + from_key(a2));
+      gv = (uint32_t)__shfl((int)a1, (lane * lg) & 63);
+    } else {
+      for (int g = 0; g < p.n_group; ++g) {
+        a1 = a2 = kNoKey;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = lane * V + i;
+          if (e >= g * gs && e < (g + 1) * gs) merge_keys(a1, a2, c[i], kNoKey);
+        }
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+          merge_keys(a1, a2, (uint32_t)__shfl_xor((int)a1, off), (uint32_t)__shfl_xor((int)a2, off));
+        if (two) a1 = to_key(from_key(a1) + from_key(a2));
+        if (lane == g) gv = a1;
+      }
+    }
+    int rank = 0;
+    for (int g = 0; g < p.n_group; ++g) {
+      const uint32_t v = (uint32_t)__builtin_amdgcn_readlane((int)gv, g);
+      rank += (v > gv || (v == gv && g < lane)) ? 1 : 0;
+    }
+    const bool in = lane < p.n_group;
+    const uint64_t keep = __ballot(in && rank < p.topk_group);
+    if (p.topk_group < p.n_group) {
+      const float least = from_key(~wave_max_key(in && rank < p.topk_group ? ~gv : 0u));
+      const float most = from_key(wave_max_key(in && rank >= p.topk_group ? gv : 0u));
+      const float far = scores ? 2.0f * margin + 0x1p-20f * (fabsf(least) + fabsf(most))
+                               : 0x1p-18f * (1.0f + fabsf(least) + fabsf(most));
+      if (!(least - most > far)) return false;     // also where both are -inf
+    }
+    if (whole) {
+      const bool out = !((keep >> (lane >> (31 - __builtin_clz((unsigned)lg)))) & 1);
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = out ? kNoKey : c[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int g = (lane * V + i) / gs;
+        if (g < 64 && !((keep >> g) & 1)) c[i] = kNoKey;
+      }
+    }
+  }
+  const bool keys = !p.bias;                       // the logits order the experts
+  if (two && keys) {                               // the scores were for the groups alone
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = c[i] > kNoKey ? to_key(l[i]) : kNoKey;
+  }
+
+  // ---- the top k and the next, lane j keeping number j.  Up to four experts
+  // per lane in descending order (stable: equal keys keep the lower expert
+  // first), more searched for their largest.
+  constexpr bool kSorted = V <= 4;
+  uint32_t order = 0;                              // sorted: the lane's experts left, two bits each
+  if constexpr (kSorted) {
+    uint32_t id[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) id[i] = (uint32_t)i;
+#pragma unroll
+    for (int n = V - 1; n > 0; --n)
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const bool s = c[i + 1] > c[i];
+        const uint32_t hi = s ? c[i + 1] : c[i], lo = s ? c[i] : c[i + 1];
+        const uint32_t ih = s ? id[i + 1] : id[i], il = s ? id[i] : id[i + 1];
+        c[i] = hi;
+        c[i + 1] = lo;
+        id[i] = ih;
+        id[i + 1] = il;
+      }
+#pragma unroll
+    for (int i = 0; i < V; ++i) order |= id[i] << (2 * i);
+  }
+  uint32_t mykey = 0;
+  mine = -1;
+  for (int j = 0; j <= p.top_k; ++j) {
+    uint32_t cb = c[0], ib = order;
+    if constexpr (!kSorted) {
+      ib = 0;
+#pragma unroll
+      for (int i = 1; i < V; ++i) {
+        const bool g = c[i] > cb;
+        cb = g ? c[i] : cb;
+        ib = g ? (uint32_t)i : ib;
+      }
+    }
+    const uint32_t m = wave_max_key(cb);
+    const int w = __builtin_ctzll(__ballot(cb == m));
+    uint32_t wi = (uint32_t)__builtin_amdgcn_readlane((int)ib, w);
+    if constexpr (kSorted) wi &= 3;
+    mykey = lane == j ? m : mykey;
+    mine = lane == j ? w * V + (int)wi : mine;
+    const bool won = lane == w;
+    if constexpr (kSorted) {
+      order = won ? order >> 2 : order;
+#pragma unroll
+      for (int i = 0; i + 1 < V; ++i) c[i] = won ? c[i + 1] : c[i];
+      c[V - 1] = won ? kNoKey : c[V - 1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = (won && (uint32_t)i == wi) ? kNoKey : c[i];
+    }
+  }
+  // ---- was it certain?  Each winner's distance from the next; equal logits
+  // are ties.  Logits whose scores could meet in double, far down (softmax) or
+  // saturated, are not.
+  const uint32_t nextkey = (uint32_t)__shfl((int)mykey, lane + 1);
+  const float f = from_key(mykey), n = from_key(nextkey), gap = f - n;
+  bool sure;
+  if (keys) {
+    const float low = p.sigmoid ? -30.0f : mx - 600.0f, high = p.sigmoid ? 30.0f : __builtin_inff();
+    sure = f > low && f < high && (gap == 0.0f || gap > 0x1p-18f * (1.0f + fabsf(f)));
+  } else {
+    sure = gap > margin + 0x1p-21f * (fabsf(f) + fabsf(n));
+  }
+  const bool there = mykey > kNoKey, last = nextkey <= kNoKey;   // last: nothing usable after it
+  if (keys) {
+    const float low = p.sigmoid ? -30.0f : mx - 600.0f, high = p.sigmoid ? 30.0f : __builtin_inff();
+    sure = sure || (last && f > low && f < high);
+  } else {
+    sure = sure || last;
+  }
+  if (__any(lane < p.top_k && there && !sure)) return false;
+  mine = lane < p.top_k && there ? mine : -1;
+  return true;
+}
+
+// The choosing in double; also gives the softmax's sum.
+template <int V>
+__device__ __forceinline__ void route_double(const RouteArgs& p, const float (&l)[V], double mx, double& sum, int& mine) {
+  constexpr double kNone = -__builtin_inf();
+  const int lane = threadIdx.x & 63;
+  double c[V];
+  if (!p.sigmoid) {
+    sum = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      c[i] = ok[i] ? exp((double)l[i] - mx) : 0.0;
+      c[i] = l[i] > -__builtin_inff() ? exp((double)l[i] - mx) : 0.0;
       sum += c[i];
     }
     sum = wave_sum(sum);
@@ -112,12 +334,12 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs p) {
   for (int i = 0; i < V; ++i) {
     const int e = lane * V + i;
     if (p.bias && e < p.E) c[i] += (double)p.bias[e];
-    if (!ok[i]) c[i] = kNone;
+    if (!(l[i] > -__builtin_inff())) c[i] = kNone;
   }
 
   // ---- groups
   if (p.n_group > 1) {
-    const int gs = p.E / p.n_group;
+    const int gs = p.gsize;
     const bool two = p.group_top == 2 && gs > 1;
     const int lg = gs / V;                         // lanes per group
     double gv = kNone;                             // lane g: what group g is worth
@@ -160,7 +382,7 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs p) {
   }
 
   // ---- the top k: lane j keeps winner j
-  int mine = -1;
+  mine = -1;
   double cb;
   int ib;
   auto best = [&]() {
@@ -194,14 +416,58 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs p) {
     best();
   }
 
+}
+
+template <int DT, int V>
+__global__ __launch_bounds__(256) void k_route(const RouteArgs p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= p.T) return;
+  const char* row = reinterpret_cast<const char*>(p.logits) + t * p.ldl * (DT == DT_F32 ? 4 : 2);
+
+  // a logit of -inf or NaN switches its expert off; +inf counts as the largest float
+  float l[V], bias[V];
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane * V + i, at = e < p.E ? e : 0;
+    if constexpr (DT == DT_F32) l[i] = reinterpret_cast<const float*>(row)[at];
+    else l[i] = to_f32<DT>(reinterpret_cast<const uint16_t*>(row)[at]);
+    bias[i] = 0.0f;
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = p.bias[lane * V + i < p.E ? lane * V + i : 0];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float x = fminf(l[i], 3.402823466e+38f);
+    const bool in = (lane * V + i < p.E) & (l[i] > -__builtin_inff());
+    l[i] = in ? x + 0.0f : -__builtin_inff();      // -0 and 0 are one key
+    m = fmaxf(m, l[i]);
+  }
+  m = wave_max(m);                                 // -inf: no expert is usable
+
+  // the softmax's sum is left out where it cancels
+  const bool no_sum = p.sigmoid || p.renorm;
+  double sum = 1.0;
+  int mine;
+  if (!no_sum || !route_float<V>(p, l, bias, m, mine)) route_double<V>(p, l, (double)m, sum, mine);
+
   // ---- weights: the winners' scores again, from their logits
   double s = 0.0;
   if (mine >= 0) {
     const float f = route_load<DT>(row, mine);
-    s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)f)) : exp((double)f - mx) / sum;
+    s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)f)) : exp((double)f - (double)m) / sum;
   }
   if (p.renorm) {
-    const double total = wave_sum(s);
+    double total = s;                              // lanes past the winners hold 0
+    if (p.top_k > 16) {
+      total = wave_sum(s);
+    } else {
+#pragma unroll
+      for (int off = 8; off >= 1; off >>= 1) total += __shfl_xor(total, off);
+    }
     if (total > 0.0) s /= total;
   }
   if (lane < p.top_k) {
@@ -218,8 +484,8 @@ hipError_t launch_route(const void* logits, int dt, int64_t T, int64_t E, int64_
                         int sigmoid, int n_group, int topk_group, int group_top, int top_k, int renorm,
                         float scale, int32_t* ids, float* weights, hipStream_t st) {
   using namespace awqk;
-  const RouteArgs p{logits, T, ldl, (int)E, bias, sigmoid, n_group, topk_group, group_top, top_k, renorm,
-                    scale, ids, weights};
+  const RouteArgs p{logits, T, ldl, (int)E, bias, sigmoid, n_group, (int)E / n_group, topk_group, group_top, top_k,
+                    renorm, scale, ids, weights};
   const dim3 grid((unsigned)((T + 3) / 4)), block(256);
   auto go = [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
