@@ -254,6 +254,11 @@ PRODUCTS = [
     (1, 8, 2, 128, 16, 128, "bf16", "bf16", ""),
     (1, 64, 8, 512, 130, 128, "f16", "f16", ""),
     (2, 5, 3, 192, 66, 64, "bf16", "f32", "holes"),
+    (2, 40, 9, 2176, 70, 64, "bf16", "f32", "holes"),
+    (1, 20, 1, 4160, 34, 64, "f16", "f32", ""),
+    (4, 30, 3, 1792, 50, 256, "bf16", "f16", "holes"),
+    (3, 64, 8, 1920, 47 * 2, 128, "f16", "f32", "holes"),
+    (1, 12, 5, 3968, 18, 128, "bf16", "f32", "none"),
     (3, 4, 4, 256, 200, 256, "f16", "f32", "holes"),
     (7, 3, 2, 384, 62, 128, "bf16", "f16", "holes"),
     (40, 2, 1, 1152, 34, 128, "bf16", "f32", "one"),

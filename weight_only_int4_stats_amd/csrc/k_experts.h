@@ -10,6 +10,14 @@ using awq::EXPERTS_DOWN;
 using awq::EXPERTS_SWIGLU;
 using awq::EXPERTS_UP;
 
+// Maximum over each 16-lane row, in every lane.
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, quad_xor1(v));
+  v = fmaxf(v, quad_xor2(v));
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false)));
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false)));
+}
+
 // -z 2^-9 as fp16, twice.
 __device__ __forceinline__ uint32_t experts_nz(uint32_t z) {
   return f32_to_f16_bits(-(float)z * 0x1p-9f) * 0x10001u;

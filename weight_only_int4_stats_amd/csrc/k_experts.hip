@@ -210,10 +210,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
         float am = 0.0f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) am = fmaxf(am, fabsf(v[c]));
-        am = fmaxf(am, quad_xor1(am));
-        am = fmaxf(am, quad_xor2(am));
-        am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
-        am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x140, 0xF, 0xF, false)));
+        am = row16_max(am);
         const int pe = pow2_exp_for(am);
         uint32_t h[8];
 #pragma unroll
@@ -312,6 +309,158 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
   }
 }
 
+// down for single tokens: one block of 8 waves per (token, 16 weight rows)
+// forms the whole weighted sum, so nothing meets in memory and there is one
+// launch.  The waves share the token's slots and, with fewer slots than waves,
+// a slot's channels; each takes chunks of four 256-channel pairs (16 rows x
+// 1024 channels) whose words, constants and activations are all on their way
+// together, and multiplies the one row with the matrix cores (every operand
+// row repeats it).  8 of 64 experts, 1024 -> 2048: 5.4 us, where few-row blocks
+// and the sum in a second launch take 7 + 4.7 us.
+constexpr int kTokenPairs = 4;                     // pairs per chunk
+constexpr int kTokenX = kTokenPairs * 256 * 2;     // a wave's staged activations, bytes
+constexpr int kTokenMeta = 16 * 17 * 8;            // its steps and zero points
+constexpr int kTokenWave = kTokenPairs * 2048 + kTokenX + kTokenPairs * 2 * 4 + kTokenMeta;
+static_assert(kTokenWave % 16 == 0, "LDS regions");
+constexpr int kTokenLds = kFewWaves * kTokenWave + kFewWaves * 16 * 4;
+
+template <int DT, bool G64>
+__global__ __launch_bounds__(kFewThreads) void k_experts_token(const FewArgs p, const float* __restrict__ weights,
+                                                               int slices) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rl = lane & 15, b = lane >> 4;
+  uint8_t* mine = lds + wv * kTokenWave;                         // ring, activations, 2^-p per unit, constants
+  uint16_t* xs = reinterpret_cast<uint16_t*>(mine + kTokenPairs * 2048);
+  float* pinv = reinterpret_cast<float*>(mine + kTokenPairs * 2048 + kTokenX);
+  uint2* meta = reinterpret_cast<uint2*>(mine + kTokenPairs * 2048 + kTokenX + kTokenPairs * 2 * 4);   // [row][17]
+  float* red = reinterpret_cast<float*>(lds + kFewWaves * kTokenWave);
+  const uint32_t ring = __builtin_amdgcn_readfirstlane(lds_addr(mine));
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int nrows = (int)(p.N - n0 < 16 ? p.N - n0 : 16);
+  const int m = blockIdx.y;
+  const uint32_t rowb = (uint32_t)(p.K >> 1);
+  const int GW = (int)(p.K >> p.glog);
+  const int npair = (int)((p.K + 255) >> 8);
+  const int dq = lane >> 3, ds = lane & 7;
+  const uint32_t dv0 = (uint32_t)dq * rowb + (uint32_t)((ds ^ (dq >> 1)) * 16);
+  const uint32_t dv1 = (uint32_t)(dq + 8) * rowb + (uint32_t)((ds ^ ((dq >> 1) | 4)) * 16);
+  const uint8_t* wlds = mine + (rl >> 3) * 1024 + (rl & 7) * 128;
+  const int wsw = ((rl & 7) >> 1) | ((rl >> 3) << 2);
+  const int sl = wv % slices;
+  const int q0 = sl * npair / slices, q1 = (sl + 1) * npair / slices;
+  constexpr int ug = G64 ? 64 : 128, kU = kTokenPairs * 256 / ug;  // channels per constant, constants per row and chunk
+
+  float total = 0.0f;
+  for (int j = wv / slices; j < p.top_k; j += kFewWaves / slices) {
+    const int slot = m * p.top_k + j;
+    const int e = __builtin_amdgcn_readfirstlane(p.ids[slot]);
+    if (e < 0 || e >= p.E) continue;
+    const float wt = weights[slot];
+    const int64_t w0 = (int64_t)e * p.N + n0;
+    const i32x4 wrs = rsrc4(reinterpret_cast<const uint8_t*>(p.qw) + w0 * rowb, (uint32_t)nrows * rowb);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int qc = q0; qc < q1; qc += kTokenPairs) {
+      const int c0 = qc * 256;
+      const int cend = (q1 * 256 < (int)p.K ? q1 * 256 : (int)p.K);   // the slice's channels end here
+      // ---- everything the chunk needs, on its way together
+      u32x4 raw[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = c0 + (lane + 64 * i) * 8;
+        raw[i] = ldg128(p.x + (int64_t)slot * p.ldx + (k < cend ? k : 0));
+        if (k >= cend) raw[i] = u32x4{0, 0, 0, 0};
+      }
+      uint32_t sv[kU / 4], zv[kU / 4];
+#pragma unroll
+      for (int i = 0; i < kU / 4; ++i) {           // entry (row, unit) = (i 4 + lane / 16, lane % 16) or halves of it
+        const int at = lane + 64 * i, r = at / kU, g = (c0 + (at % kU) * ug) >> p.glog;
+        const bool in = r < nrows && g < GW;
+        const int64_t a = in ? (w0 + r) * GW + g : 0;
+        sv[i] = in ? p.scales[a] : 0u;
+        zv[i] = in ? p.zeros[a] : 0u;
+      }
+#pragma unroll
+      for (int d = 0; d < kTokenPairs; ++d) {
+        const uint32_t off = __builtin_amdgcn_readfirstlane(qc + d < q1 ? (uint32_t)(qc + d) * 128 : kBufferOob);
+        few_dma16(wrs, ring + (uint32_t)d * 2048, dv0 + off);
+        few_dma16(wrs, ring + (uint32_t)d * 2048 + 1024, dv1 + off);
+      }
+      // ---- activations: fp16 scaled by a power of two per 128 channels
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[2 * c] = lo_f32<DT>(raw[i][c]);
+          v[2 * c + 1] = hi_f32<DT>(raw[i][c]);
+        }
+        float am = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) am = fmaxf(am, fabsf(v[c]));
+        am = row16_max(am);
+        const int pe = pow2_exp_for(am);
+        uint32_t h[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) h[c] = f32_to_f16_bits(ldexpf(v[c], pe));
+        *reinterpret_cast<u32x4*>(xs + (lane + 64 * i) * 8) =
+            u32x4{h[0] | (h[4] << 16), h[2] | (h[6] << 16), h[1] | (h[5] << 16), h[3] | (h[7] << 16)};
+        if ((lane & 15) == 0) pinv[(lane >> 4) + 4 * i] = ldexpf(1.0f, -pe);
+      }
+#pragma unroll
+      for (int i = 0; i < kU / 4; ++i) {
+        const int at = lane + 64 * i;
+        meta[at / kU * 17 + at % kU] = make_uint2(__float_as_uint(f16_to_f32(sv[i]) * 512.0f), experts_nz(zv[i]));
+      }
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int d = 0; d < kTokenPairs; ++d) {
+        if (qc + d >= q1) break;                   // wave-uniform
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int g = 2 * d + u;
+          const float pv = pinv[g];
+          if constexpr (!G64) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(wlds + d * 2048 + (((4 * u + b) ^ wsw) * 16));
+            const uint16_t* xp = xs + 128 * g + 32 * b;
+            const uint2 md = meta[rl * 17 + g];
+            f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp + 8 * i), experts_unpack(w[i], md.y), part);
+            acc[0] = __builtin_fmaf(__uint_as_float(md.x) * pv, part[0], acc[0]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint2 w = *reinterpret_cast<const uint2*>(
+                  wlds + d * 2048 + (((4 * u + 2 * h + (b >> 1)) ^ wsw) * 16) + (b & 1) * 8);
+              const uint16_t* xp = xs + 128 * g + 64 * h + 16 * b;
+              const uint2 md = meta[rl * 17 + 2 * g + h];
+              f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp), experts_unpack(w.x, md.y), part);
+              part = mfma16h(*reinterpret_cast<const u32x4*>(xp + 8), experts_unpack(w.y, md.y), part);
+              acc[0] = __builtin_fmaf(__uint_as_float(md.x) * pv, part[0], acc[0]);
+            }
+          }
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");         // the chunk is in registers: its LDS is free
+      __builtin_amdgcn_wave_barrier();
+    }
+    total = __builtin_fmaf(wt, acc[0], total);
+  }
+  if (b == 0) red[wv * 16 + rl] = total;
+  __syncthreads();
+  if (tid < nrows) {
+    float s = red[tid];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) s += red[w * 16 + tid];
+    store_out(p.y, p.ydt, (int64_t)m * p.ldy + n0 + tid, s);
+  }
+}
+
 // y[m] = sum_j w[m][j] P[m top_k + j] over the slots that have an expert, in
 // slot order.  Four outputs per thread (P's rows are padded to a multiple of 4).
 template <int YDT>
@@ -335,6 +484,16 @@ __global__ __launch_bounds__(256) void k_experts_combine(const float* __restrict
     for (int c = 0; c < 4; ++c)
       if (n + c < N) store_out(y, YDT, m * ldy + n + c, s[c]);
   }
+}
+
+// Waves per slot of k_experts_token (0: the few-row kernel and a second
+// launch).  Few enough slots that two seldom share an expert (whose words would be
+// read twice), and at most two chunks per wave and slot.
+int token_slices(int64_t S, int64_t E, int64_t K, int top_k) {
+  int s = 1;
+  while (s * 2 * top_k <= kFewWaves) s *= 2;
+  const int64_t pairs = (K + 255) / 256;
+  return 2 * S <= E && (pairs + s - 1) / s <= 2 * kTokenPairs ? s : 0;
 }
 
 template <int DT, int MODE>
@@ -361,6 +520,7 @@ static size_t partial_bytes(bool down, int64_t S, int64_t N) {
 
 size_t experts_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k) {
   const int64_t S = M * top_k;
+  if (down && token_slices(S, E, K, (int)top_k)) return 0;
   return partial_bytes(down, S, N) + (few_rows(S, E) ? 0 : experts_gemm_ws_bytes(down, M, N, K, E, top_k));
 }
 
@@ -370,6 +530,17 @@ hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
   void* out = down ? ws : c.y;                     // down: fp32 rows per slot first
   const int64_t ldo = down ? partial_ld(c.N) : c.ldy;
   hipError_t e;
+  if (const int slices = down ? token_slices(S, c.E, c.K, c.top_k) : 0) {
+    const FewArgs a{c.x, c.K, c.ldx, c.N, c.ldy, c.ids, c.qw, c.scales, c.zeros, c.y, (int)S, (int)c.E, c.top_k,
+                    c.group == 64 ? 6 : c.group == 128 ? 7 : 8, c.ydt, 0, 0};
+    const dim3 grid((unsigned)((c.N + 15) / 16), (unsigned)c.M), block(kFewThreads);
+    const bool bf = c.xdt == DT_BF16, g64 = c.group == 64;
+    if (bf && g64) hipLaunchKernelGGL((k_experts_token<DT_BF16, true>), grid, block, kTokenLds, st, a, c.weights, slices);
+    else if (bf) hipLaunchKernelGGL((k_experts_token<DT_BF16, false>), grid, block, kTokenLds, st, a, c.weights, slices);
+    else if (g64) hipLaunchKernelGGL((k_experts_token<DT_F16, true>), grid, block, kTokenLds, st, a, c.weights, slices);
+    else hipLaunchKernelGGL((k_experts_token<DT_F16, false>), grid, block, kTokenLds, st, a, c.weights, slices);
+    return hipGetLastError();
+  }
   if (!few_rows(S, c.E)) {
     e = launch_experts_gemm(c, out, ldo, reinterpret_cast<char*>(ws) + partial_bytes(down, S, c.N), st);
   } else {

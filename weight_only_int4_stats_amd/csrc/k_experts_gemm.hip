@@ -209,7 +209,6 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
 
   // ---- copies: A rows of 128 bytes, 8 per copy, chunk c of row r at c ^ (r & 7);
   // B per 32 columns the first then the last 16 bytes of each; C four entries a lane
-  const int64_t G = p.K / p.group;
   const i32x4 ars = rsrc4(p.xq, (uint32_t)(p.xrows * p.K * 2));
   const i32x4 brs = rsrc4(reinterpret_cast<const uint8_t*>(p.qw) + (int64_t)e * p.N * (p.K >> 1), (uint32_t)(p.N * (p.K >> 1)));
   const int64_t U = p.K / p.unit;
