@@ -109,11 +109,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_experts_prep(const GemmArgs p,
   extern __shared__ int prep_lds[];
   const int bid = blockIdx.x, tid = threadIdx.x;
   if (bid < p.b_rows) {
-    group_sort_block(p.ids, p.S, p.E, bid, p.b_rows, p.plan, prep_lds);
-    if (p.b_rows == 1) {
-      __syncthreads();
-      group_place_block(p.ids, p.S, p.E, 0, 1, tile_rows, p.plan, prep_lds);
-    }
+    group_sort_block(p.ids, p.S, p.E, bid, p.b_rows, tile_rows, p.plan, prep_lds);
   } else if (bid < p.b_consts) {
     const int64_t row = (int64_t)(bid - p.b_rows) * 16 + (tid >> 6);
     if (row < p.xrows) prep_row<DT>(p, row);
@@ -466,8 +462,8 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, voi
   a.b_zero = a.b_consts + (int)((c.E * c.N * ((c.K / c.group + 7) / 8) + kPlanThreads - 1) / kPlanThreads);
   const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
   const unsigned pb = (unsigned)(a.b_zero + (down ? 0 : (S + 15) / 16));
-  if (c.xdt == DT_F16) hipLaunchKernelGGL((k_experts_prep<DT_F16>), dim3(pb), dim3(kPlanThreads), group_tiles_lds(a.E), st, a, tile, cols);
-  else hipLaunchKernelGGL((k_experts_prep<DT_BF16>), dim3(pb), dim3(kPlanThreads), group_tiles_lds(a.E), st, a, tile, cols);
+  if (c.xdt == DT_F16) hipLaunchKernelGGL((k_experts_prep<DT_F16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
+  else hipLaunchKernelGGL((k_experts_prep<DT_BF16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = launch_group_place(c.ids, S, c.E, tile, a.plan, st);
   if (e != hipSuccess) return e;

@@ -41,8 +41,7 @@ inline int group_chunks(int64_t S) {
 inline int64_t group_tiles_max(int64_t S, int64_t E, int tile_rows) {
   return S / tile_rows + (S < E + 1 ? S : E + 1);
 }
-inline size_t group_sort_lds(int E) { return (size_t)(E + 2 + 16) * 4; }
-inline size_t group_tiles_lds(int E) { return (size_t)(3 * (E + 2) + 32) * 4; }
+inline size_t group_plan_lds(int E) { return (size_t)(3 * (E + 2) + 32) * 4; }
 inline size_t group_plan_bytes(int64_t S, int64_t E, int tile_rows) {
   const size_t perm = awq::align_up((size_t)S * 4, 256);
   const int chunks = group_chunks(S);
@@ -103,18 +102,48 @@ __device__ inline int block_prefix(int* v, int n, int* wsum) {
   return total;
 }
 
+// Lists the tiles from the groups' sizes in tstart[0 .. E] (LDS; tiles per
+// group on the way out) and first rows start[0 .. E + 1].
+__device__ inline void group_tiles(int* start, int* tstart, int E, int tile_rows, const GroupPlan& plan, int* wsum, bool list) {
+  const int tid = threadIdx.x;
+  const int tiles = block_prefix(tstart, E + 1, wsum);
+  if (!list) return;
+  if (tid == 0) {
+    tstart[E + 1] = tiles;
+    plan.ntile[0] = tiles;
+    plan.ntile[1] = tstart[E];
+  }
+  __syncthreads();
+  // one tile per thread: its group is the last whose first tile is not past it
+  for (int i = tid; i < tiles; i += kPlanThreads) {
+    int lo = 0, hi = E + 1;            // tstart[lo] <= i < tstart[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tstart[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    GroupTile q;
+    q.group = lo;
+    q.first = start[lo] + (i - tstart[lo]) * tile_rows;
+    q.rows = start[lo + 1] - q.first < tile_rows ? start[lo + 1] - q.first : tile_rows;
+    q.before = tstart[lo];
+    q.tiles = tstart[lo + 1] - tstart[lo];
+    q.pad[0] = q.pad[1] = q.pad[2] = 0;
+    plan.tiles[i] = q;
+  }
+}
+
 // Chunk c of the rows by one block of kPlanThreads: a counting sort in LDS
-// (group_sort_lds bytes at lds).  One chunk: perm and lstart are final.
-__device__ inline void group_sort_block(const int32_t* __restrict__ ids, int S, int E, int c, int chunks,
+// (group_plan_lds bytes at lds).  One chunk: the whole plan.
+__device__ inline void group_sort_block(const int32_t* __restrict__ ids, int S, int E, int c, int chunks, int tile_rows,
                                         const GroupPlan& plan, int* lds) {
-  int* start = lds;                    // counts, then first positions
-  int* wsum = lds + E + 2;
+  int* start = lds;                    // [E + 2] counts, then first positions, and the end
+  int* tstart = lds + E + 2;           // [E + 2] the same for tiles (one chunk)
+  int* wsum = lds + 3 * (E + 2);
   const int tid = threadIdx.x, lane = tid & 63;
   const int lo = (int)((int64_t)c * S / chunks), hi = (int)((int64_t)(c + 1) * S / chunks);
   const int bits = 32 - __builtin_clz(E + 1);      // of 0 .. E + 1; E + 1: past the last row
   int* out = chunks > 1 ? plan.lperm : plan.perm;
-  for (int g = tid; g <= E; g += kPlanThreads) start[g] = 0;
-  __syncthreads();
   constexpr int kU = 4;                // rows per thread loaded together
   int g4[kU];
   auto load = [&](int s0) {
@@ -125,8 +154,11 @@ __device__ inline void group_sort_block(const int32_t* __restrict__ ids, int S, 
       g4[u] = s >= hi ? E + 1 : id < 0 || id >= E ? E : id;
     }
   };
+  load(lo);
+  for (int g = tid; g <= E; g += kPlanThreads) start[g] = 0;
+  __syncthreads();
   for (int s0 = lo; s0 < hi; s0 += kU * kPlanThreads) {
-    load(s0);
+    if (s0 > lo) load(s0);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (s0 + u * kPlanThreads >= hi) break;
@@ -135,10 +167,17 @@ __device__ inline void group_sort_block(const int32_t* __restrict__ ids, int S, 
     }
   }
   __syncthreads();
+  if (chunks == 1)
+    for (int g = tid; g <= E; g += kPlanThreads) tstart[g] = (start[g] + tile_rows - 1) / tile_rows;
   block_prefix(start, E + 1, wsum);
-  int* ls = plan.lstart + (int64_t)c * (E + 2);
-  for (int g = tid; g <= E; g += kPlanThreads) ls[g] = start[g];
-  if (tid == 0) ls[E + 1] = hi - lo;
+  if (chunks == 1) {
+    if (tid == 0) start[E + 1] = S;
+    group_tiles(start, tstart, E, tile_rows, plan, wsum, true);
+  } else {
+    int* ls = plan.lstart + (int64_t)c * (E + 2);
+    for (int g = tid; g <= E; g += kPlanThreads) ls[g] = start[g];
+    if (tid == 0) ls[E + 1] = hi - lo;
+  }
   __syncthreads();
   for (int s0 = lo; s0 < hi; s0 += kU * kPlanThreads) {
     if (hi - lo > kU * kPlanThreads) load(s0);     // else still held from the counting
@@ -155,9 +194,8 @@ __device__ inline void group_sort_block(const int32_t* __restrict__ ids, int S, 
   }
 }
 
-// Block c of `chunks` puts its chunk into the common order; block 0 lists the
-// tiles (one chunk: called by the sorting block, after it).  group_tiles_lds
-// bytes at lds.
+// Many chunks: block c puts its chunk into the common order; block 0 lists
+// the tiles.  group_plan_lds bytes at lds.
 __device__ inline void group_place_block(const int32_t* __restrict__ ids, int S, int E, int c, int chunks, int tile_rows,
                                          const GroupPlan& plan, int* lds) {
   int* start = lds;                    // [E + 2] first rows of the groups, and the end
@@ -186,41 +224,12 @@ __device__ inline void group_place_block(const int32_t* __restrict__ ids, int S,
   }
   __syncthreads();
   block_prefix(start, E + 1, wsum);
-  const int tiles = block_prefix(tstart, E + 1, wsum);
-  if (tid == 0) {
-    start[E + 1] = S;
-    tstart[E + 1] = tiles;
-  }
-  __syncthreads();
-  if (c == 0) {
-    if (tid == 0) {
-      plan.ntile[0] = tiles;
-      plan.ntile[1] = tstart[E];
-    }
-    // one tile per thread: its group is the last whose first tile is not past it
-    for (int i = tid; i < tiles; i += kPlanThreads) {
-      int lo = 0, hi = E + 1;          // tstart[lo] <= i < tstart[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tstart[mid] <= i) lo = mid;
-        else hi = mid;
-      }
-      GroupTile q;
-      q.group = lo;
-      q.first = start[lo] + (i - tstart[lo]) * tile_rows;
-      q.rows = start[lo + 1] - q.first < tile_rows ? start[lo + 1] - q.first : tile_rows;
-      q.before = tstart[lo];
-      q.tiles = tstart[lo + 1] - tstart[lo];
-      q.pad[0] = q.pad[1] = q.pad[2] = 0;
-      plan.tiles[i] = q;
-    }
-  }
-  if (chunks > 1) {
-    const int lo = (int)((int64_t)c * S / chunks), hi = (int)((int64_t)(c + 1) * S / chunks);
-    for (int i = lo + tid; i < hi; i += kPlanThreads) {
-      const int s = plan.lperm[i], id = ids[s], g = id < 0 || id >= E ? E : id;
-      plan.perm[start[g] + move[g] + (i - lo)] = s;
-    }
+  if (tid == 0) start[E + 1] = S;
+  group_tiles(start, tstart, E, tile_rows, plan, wsum, c == 0);
+  const int lo = (int)((int64_t)c * S / chunks), hi = (int)((int64_t)(c + 1) * S / chunks);
+  for (int i = lo + tid; i < hi; i += kPlanThreads) {
+    const int s = plan.lperm[i], id = ids[s], g = id < 0 || id >= E ? E : id;
+    plan.perm[start[g] + move[g] + (i - lo)] = s;
   }
 }
 

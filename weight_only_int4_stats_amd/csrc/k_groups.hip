@@ -9,11 +9,7 @@ namespace awqk {
 __global__ __launch_bounds__(kPlanThreads) void k_group_sort(const int32_t* __restrict__ ids, int S, int E, int chunks,
                                                              int tile_rows, GroupPlan plan) {
   extern __shared__ int group_lds[];
-  group_sort_block(ids, S, E, blockIdx.x, chunks, plan, group_lds);
-  if (chunks == 1) {
-    __syncthreads();
-    group_place_block(ids, S, E, 0, 1, tile_rows, plan, group_lds);
-  }
+  group_sort_block(ids, S, E, blockIdx.x, chunks, tile_rows, plan, group_lds);
 }
 
 __global__ __launch_bounds__(kPlanThreads) void k_group_place(const int32_t* __restrict__ ids, int S, int E, int chunks,
@@ -31,7 +27,7 @@ hipError_t launch_group_place(const int32_t* ids, int64_t S, int64_t E, int tile
                               hipStream_t st) {
   const int chunks = group_chunks(S);
   if (chunks == 1) return hipSuccess;
-  hipLaunchKernelGGL(k_group_place, dim3(chunks), dim3(kPlanThreads), group_tiles_lds((int)E), st, ids, (int)S, (int)E,
+  hipLaunchKernelGGL(k_group_place, dim3(chunks), dim3(kPlanThreads), group_plan_lds((int)E), st, ids, (int)S, (int)E,
                      chunks, tile_rows, plan);
   return hipGetLastError();
 }
@@ -39,7 +35,7 @@ hipError_t launch_group_place(const int32_t* ids, int64_t S, int64_t E, int tile
 hipError_t launch_group_plan(const int32_t* ids, int64_t S, int64_t E, int tile_rows, const GroupPlan& plan,
                              hipStream_t st) {
   const int chunks = group_chunks(S);
-  hipLaunchKernelGGL(k_group_sort, dim3(chunks), dim3(kPlanThreads), group_tiles_lds((int)E), st, ids, (int)S, (int)E,
+  hipLaunchKernelGGL(k_group_sort, dim3(chunks), dim3(kPlanThreads), group_plan_lds((int)E), st, ids, (int)S, (int)E,
                      chunks, tile_rows, plan);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : launch_group_place(ids, S, E, tile_rows, plan, st);

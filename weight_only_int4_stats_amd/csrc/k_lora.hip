@@ -121,10 +121,25 @@ __device__ __forceinline__ void lora_list(const LoraArgs& p, const LoraRows& r, 
   }
 }
 
-__device__ __forceinline__ int lora_rank(const LoraArgs& p, int a) {
-  if (!p.ranks) return p.R;
-  const int r = p.ranks[a];
-  return r < 0 ? 0 : r > p.R ? p.R : r;
+// The adapter's rank and scaling (0 for none).
+struct LoraAdapter {
+  int rank;
+  float scaling;
+};
+__device__ __forceinline__ LoraAdapter lora_adapter(const LoraArgs& p, int a) {
+  const int at = a < 0 ? 0 : a;
+  LoraAdapter d{p.R, 1.0f};
+  if (p.n_adapters == 0) return LoraAdapter{0, 0.0f};
+  if (p.ranks) d.rank = p.ranks[at];
+  if (p.scaling) d.scaling = p.scaling[at];
+  d.rank = a < 0 || d.rank < 0 ? 0 : d.rank > p.R ? p.R : d.rank;
+  return d;
+}
+// Block row grp's adapter where it is known without the rows, so that its rank
+// is on its way while they are looked for.
+__device__ __forceinline__ bool lora_known(const LoraArgs& p, int grp, int& a) {
+  a = grp < p.n_adapters ? grp : -1;
+  return !p.planned && !p.by_row;
 }
 
 // Steps of 64 channels whose loads are in flight together in a wave of the
@@ -193,9 +208,14 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void k_lora_shrink(const LoraArg
   const int rl = lane & 15, b = lane >> 4;
   const int bx = (int)(blockIdx.x % (unsigned)p.ksplit), by = (int)(blockIdx.x / (unsigned)p.ksplit);
   constexpr int kSub = kLoraTile / (16 * MT);      // blocks per tile of the plan
+  int known;
+  LoraAdapter ad{0, 0.0f};
+  const bool early = lora_known(p, by, known);
+  if (early) ad = lora_adapter(p, known);
   const LoraRows r = lora_rows(p, p.planned ? by / kSub : by, count);
   if (r.a < 0 || r.n == 0) return;
-  const int rank = lora_rank(p, r.a);
+  if (!early) ad = lora_adapter(p, r.a);
+  const int rank = ad.rank;
   const int steps = (p.K + 63) >> 6;
   const int part = bx * W + wv, parts = p.ksplit * W;
   const int k0 = (int)((int64_t)part * steps / parts), k1 = (int)((int64_t)(part + 1) * steps / parts);
@@ -270,19 +290,16 @@ __device__ __forceinline__ void lora_split_row(int j, int pad, float sc, uint16_
   if (j == 0) *back = ldexpf(sc, -pe);
 }
 
-// 8 ranks k .. k + 7 of column n of B; what B holds past the rank is not used.
+// 8 ranks k .. k + 7 of column n of B, and what of them the product may see:
+// nothing past the last column or the rank, whatever B holds there.  The load
+// is unconditional so that nothing waits for it here.
 __device__ __forceinline__ u32x4 lora_b(const LoraArgs& p, const uint16_t* B, int64_t n, int k, int rank) {
-  u32x4 w = {0, 0, 0, 0};
-  if (n < p.N && k < rank) {
-    w = ldg128(B + n * p.R + k);
-    if (k + 8 > rank) {
+  return ldg128(B + (n < p.N && k < rank ? n * p.R + k : 0));
+}
+__device__ __forceinline__ u32x4 lora_b_mask(u32x4 w, const LoraArgs& p, int64_t n, int k, int rank) {
+  const int left = n < p.N ? rank - k : 0;         // ranks of the eight that are there
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (k + 2 * c >= rank) w[c] = 0;
-        else if (k + 2 * c + 1 >= rank) w[c] &= 0xFFFFu;
-      }
-    }
-  }
+  for (int c = 0; c < 4; ++c) w[c] &= left > 2 * c + 1 ? 0xFFFFFFFFu : left > 2 * c ? 0xFFFFu : 0u;
   return w;
 }
 
@@ -378,13 +395,15 @@ constexpr int kLoraCols = 64;                      // columns per wave of the ex
 
 // y = base + scaling B h, PR rows of an adapter at a time, 64 columns per
 // wave.  B is the first operand (16 columns of y per product) and h the
-// second, so a result lane holds four values of one row; operand row i of
-// product q is column 16 (i / 4) + 4 q + i % 4, so that a lane's four products
-// give 16 consecutive columns.  A wave's part of B stays in registers for all
-// of the block's rows.  RK: 32-rank steps.
+// second, so a result lane holds four values of one row.  The products' rows
+// are dealt so that lane group b's values of NQ products are 4 NQ consecutive
+// columns (16 bytes) and the four groups' pieces lie side by side: an access
+// covers 64 bytes of each of 16 rows.  A wave's part of B stays in registers
+// for all of the block's rows.  RK: 32-rank steps.
 template <int DT, int YDT, int RK, int PR>
 __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
   constexpr int kPitch = RK * 32 + 8;
+  constexpr int NQ = YDT == DT_F32 ? 1 : 2, NC = 4 / NQ;   // products per piece, pieces per row
   __shared__ int list[PR];
   __shared__ int count[8];
   __shared__ __attribute__((aligned(16))) uint16_t hs[2][PR][kPitch];
@@ -393,29 +412,33 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
   const int bx = (int)(blockIdx.x % (unsigned)p.nx), by = (int)(blockIdx.x / (unsigned)p.nx);
+  int known;
+  LoraAdapter ad{0, 0.0f};
+  const bool early = lora_known(p, by, known);
+  if (early) ad = lora_adapter(p, known);
   const LoraRows r = lora_rows(p, by, count);
   if (r.n == 0) return;
-  const int rank = r.a < 0 ? 0 : lora_rank(p, r.a);
+  if (!early) ad = lora_adapter(p, r.a);
+  const int rank = ad.rank;
+  const float sc = ad.scaling;
   const int rk = (rank + 31) >> 5;
   const uint16_t* B = p.b + (r.a < 0 ? 0 : (int64_t)r.a * p.N * p.R);
-  const float sc = r.a < 0 ? 0.0f : p.scaling ? p.scaling[r.a] : 1.0f;
   const int64_t c0 = ((int64_t)bx * 4 + wv) * kLoraCols;
-  const int64_t cl = c0 + 16 * b;                  // this lane's first column
+  const int64_t cl = c0 + 4 * NQ * b;              // this lane's first piece; the others 16 NQ columns on
+  auto bcol = [&](int q) { return c0 + q / NQ * 16 * NQ + 4 * NQ * (rl >> 2) + 4 * (q % NQ) + (rl & 3); };
   u32x4 w[RK][4];
+  if (rank > 0) {
 #pragma unroll
-  for (int s = 0; s < RK; ++s)
+    for (int s = 0; s < RK; ++s)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) w[s][q] = lora_b(p, B, c0 + 16 * (rl >> 2) + 4 * q + (rl & 3), s * 32 + 8 * b, rank);
+      for (int q = 0; q < 4; ++q) w[s][q] = lora_b(p, B, bcol(q), s * 32 + 8 * b, rank);
+  }
   for (int r0 = 0; r0 < r.n; r0 += PR) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PR; i += 16) lora_list(p, r, r0 + i, list + i);
     __syncthreads();
     const int nr = r.n - r0 < PR ? r.n - r0 : PR;
-    LoraOut<YDT, 4> out[PR / 16];                  // base, on its way while h is staged
-#pragma unroll
-    for (int t = 0; t < PR; t += 16)
-      if (t + rl < nr) out[t / 16].load(p, list[t + rl], cl);
     if (rank > 0) {
       // 16 threads per row; the K parts, four at a time, are added in their order
       const int64_t pitch = (int64_t)p.M * p.R;
@@ -444,10 +467,23 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
       }
     }
     __syncthreads();
+    if (r0 == 0 && rank > 0) {
+#pragma unroll
+      for (int s = 0; s < RK; ++s)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          w[s][q] = lora_b_mask(w[s][q], p, bcol(q), s * 32 + 8 * b, rank);
+    }
 #pragma unroll
     for (int t = 0; t < PR; t += 16) {
       if (t >= nr) break;
       const int row = t + rl;
+      // base 16 rows at a time: for all of the block's rows ahead of the staging
+      // it cost registers and time (26 us instead of 21 us for 4096 rows)
+      LoraOut<YDT, NQ> out[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        if (row < nr) out[c].load(p, list[row], cl + 16 * NQ * c);
       f32x4 acc[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -463,7 +499,9 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
           }
         }
       }
-      if (row < nr) out[t / 16].store(p, list[row], cl, rank > 0 ? back[row] : 0.0f, acc, rank > 0);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        if (row < nr) out[c].store(p, list[row], cl + 16 * NQ * c, rank > 0 ? back[row] : 0.0f, acc + NQ * c, rank > 0);
     }
   }
 }
@@ -484,17 +522,24 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
   const int bx = (int)(blockIdx.x % (unsigned)p.nx), by = (int)(blockIdx.x / (unsigned)p.nx);
+  int known;
+  LoraAdapter ad{0, 0.0f};
+  const bool early = lora_known(p, by, known);
+  if (early) ad = lora_adapter(p, known);
   const LoraRows r = lora_rows(p, by, count);
   if (r.n == 0) return;
-  const int rank = r.a < 0 ? 0 : lora_rank(p, r.a);
+  if (!early) ad = lora_adapter(p, r.a);
+  const int rank = ad.rank;
+  const float sc = ad.scaling;
   const int rk = (rank + 31) >> 5;
-  const float sc = r.a < 0 ? 0.0f : p.scaling ? p.scaling[r.a] : 1.0f;
   const uint16_t* A = p.a + (r.a < 0 ? 0 : (int64_t)r.a * p.R * p.K);
   const uint16_t* B = p.b + (r.a < 0 ? 0 : (int64_t)r.a * p.N * p.R);
   const int64_t c0 = (int64_t)bx * kLoraOneCols + wv * 16;
   u32x4 w[RK];
+  if (rank > 0) {
 #pragma unroll
-  for (int s = 0; s < RK; ++s) w[s] = lora_b(p, B, c0 + rl, s * 32 + 8 * b, rank);
+    for (int s = 0; s < RK; ++s) w[s] = lora_b(p, B, c0 + rl, s * 32 + 8 * b, rank);
+  }
   for (int r0 = 0; r0 < r.n; r0 += 16) {
     __syncthreads();
     lora_list(p, r, r0, list);
@@ -533,6 +578,10 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
         lora_split_row<DT, RK * 2>(j, rk * 32, sc, hs[0][row], hs[1][row], back + row, v);
       }
       __syncthreads();
+    }
+    if (r0 == 0 && rank > 0) {
+#pragma unroll
+      for (int s = 0; s < RK; ++s) w[s] = lora_b_mask(w[s], p, c0 + rl, s * 32 + 8 * b, rank);
     }
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
