@@ -244,7 +244,10 @@ def check_down(x, ids, weights, w, g, out, y, what):
     ref = (z * wt).reshape(T, k, -1).sum(1)
     # each term's own error, and k additions (and products) of the terms' sizes
     slack = (product_slack(size, K, g) * np.abs(wt)).reshape(T, k, -1).sum(1)
-    slack += (k + 1) * 2.0 ** -23 * (np.abs(z * wt)).reshape(T, k, -1).sum(1)
+    terms = np.abs(z * wt).reshape(T, k, -1).sum(1)
+    slack += (k + 1) * 2.0 ** -23 * terms
+    if out == torch.bfloat16:                        # terms kept in fp16 (one rounding of 2^-11 each)
+        slack += 2.0 ** -11 * (terms + slack)
     check(y, ref, slack, out, what)
 
 

@@ -23,8 +23,12 @@
 //    tile is tall (128 rows) because they serve all of its rows: with 64 x 64
 //    tiles per wave the vector instructions, not the matrix cores, set the time.
 //  * With SwiGLU a tile's columns alternate 16 gate rows and their 16 up rows,
-//    so both meet in one lane.  down writes fp32 rows per slot; the weighted sum
-//    over a token's slots is k_experts_combine's.
+//    so both meet in one lane.  down writes a row per slot; the weighted sum
+//    over a token's slots is k_experts_combine's.  Rows are fp32, or for bf16
+//    outputs fp16 scaled by a power of two per 64 columns: each term is off by
+//    at most 2^-11 of itself, an eighth of the output's own rounding, and half
+//    the bytes are written and read back (4096 tokens, 8 of 64 experts, 1024 ->
+//    2048: 293 us with fp32 rows).
 //  * The tiles of one expert are ordered 8 row tiles at a time, rows fastest,
 //    and each L2 slice takes a contiguous eighth of the order.
 #include "awq_device.h"
@@ -51,6 +55,7 @@ struct GemmArgs {
   const uint8_t* zeros;
   void* y;
   int64_t xrows;
+  int8_t* rexp;                                    // down with 16-bit rows: their exponents, one per 64 columns
   int S, E, top_k, group, unit, ydt, vec;          // unit: channels per constant (64 or 128, at most the group)
   // workspace
   uint16_t* xq;                                    // [xrows][K]
@@ -209,6 +214,15 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   const i32x4 brs = rsrc4(reinterpret_cast<const uint8_t*>(p.qw) + (int64_t)e * p.N * (p.K >> 1), (uint32_t)(p.N * (p.K >> 1)));
   const int64_t U = p.K / p.unit;
   const i32x4 crs = rsrc4(p.ctab + (int64_t)e * U * p.N, (uint32_t)(U * p.N * 4));
+  // the rows' slots and exponents wait in LDS for the epilogue: fetched there,
+  // two dependent loads for every few rows, they took a tile 20 us
+  int* slots = reinterpret_cast<int*>(lds + 3 * kStage);
+  int* exps = slots + BM;
+  if (tid < rows) {
+    const int slot = perm[tid];
+    slots[tid] = slot;
+    exps[tid] = 9 - p.pexp[xrow(slot)];            // with the operands' 2^-9
+  }
   uint32_t aoff[kAc];
 #pragma unroll
   for (int u = 0; u < kAc; ++u) {
@@ -351,7 +365,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int r = r0 + 4 * b + v;
-      const int pe = r < rows ? 9 - p.pexp[xrow(perm[r])] : 0;   // and the operands' 2^-9
+      const int pe = r < rows ? exps[r] : 0;
       float* d = stg + (4 * b + v) * (kW + 4) + rl;
       if constexpr (MODE == EXPERTS_SWIGLU) {
 #pragma unroll
@@ -368,8 +382,22 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
     for (int i = 0; i < 16 * kL / 64; ++i) {
       const int r = i * (64 / kL) + lane / kL, c = (lane % kL) * 4;
       const f32x4 o = *reinterpret_cast<const f32x4*>(stg + r * (kW + 4) + c);
+      if (MODE == EXPERTS_DOWN && p.rexp) {
+        // fp16 scaled by a power of two per row and 64 columns
+        const float am = row16_max(fmaxf(fmaxf(fabsf(o[0]), fabsf(o[1])), fmaxf(fabsf(o[2]), fabsf(o[3]))));
+        const int pe = min(pow2_exp_for(am), 100);
+        const int64_t col = c0 + wv * kW + c;
+        if (r0 + r >= rows || col >= p.ldy) continue;
+        const int64_t slot = slots[r0 + r];
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = f32_to_f16_bits(ldexpf(o[j], pe));
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.y) + slot * p.ldy + col) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        if (c == 0) p.rexp[slot * (p.ldy >> 6) + (col >> 6)] = (int8_t)pe;
+        continue;
+      }
       if (r0 + r >= rows) continue;
-      const int64_t col = c0 + wv * kW + c, pos = (int64_t)perm[r0 + r] * p.ldy + col;
+      const int64_t col = c0 + wv * kW + c, pos = (int64_t)slots[r0 + r] * p.ldy + col;
       if (MODE == EXPERTS_DOWN || p.ydt == DT_F32) {
         float* y = reinterpret_cast<float*>(p.y) + pos;
         if (p.vec && col + 4 <= ncols) *reinterpret_cast<f32x4*>(y) = o;
@@ -393,7 +421,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
 
 template <int MODE, int MB>
 void gemm_launch(const GemmArgs& a, const dim3& grid, hipStream_t st) {
-  constexpr size_t lds = 3 * (16 * MB * kGemmK * 2 + kGemmN * 36);
+  constexpr size_t lds = 3 * (16 * MB * kGemmK * 2 + kGemmN * 36) + 16 * MB * 8;
   if (a.group == 64) hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 1>), grid, dim3(256), lds, st, a);
   else hipLaunchKernelGGL((k_experts_gemm<MODE, MB, 2>), grid, dim3(256), lds, st, a);   // 256: a ratio of 1 between halves
 }
@@ -427,7 +455,7 @@ size_t experts_gemm_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t
   return gemm_space(down, M, N, K, E, top_k, 64).total;     // the smallest group needs the most
 }
 
-hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, void* ws, hipStream_t st) {
+hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, int8_t* rexp, void* ws, hipStream_t st) {
   const bool down = c.mode == EXPERTS_DOWN;
   const int64_t S = c.M * c.top_k;
   const GemmSpace g = gemm_space(down, c.M, c.N, c.K, c.E, c.top_k, c.group);
@@ -444,6 +472,7 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, voi
   a.scales = c.scales;
   a.zeros = c.zeros;
   a.y = out;
+  a.rexp = rexp;
   a.xrows = down ? S : c.M;
   a.S = (int)S;
   a.E = (int)c.E;
