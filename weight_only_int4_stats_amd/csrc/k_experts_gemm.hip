@@ -192,11 +192,11 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   const int gi = (int)(rem / (kGemmGroupM * nt));
   const int gm = q0.tiles - gi * kGemmGroupM < kGemmGroupM ? q0.tiles - gi * kGemmGroupM : kGemmGroupM;
   const int in_group = (int)(rem - (int64_t)gi * kGemmGroupM * nt);
-  const GroupTile q = p.plan.tiles[q0.before + gi * kGemmGroupM + in_group % gm];
   const int64_t c0 = (int64_t)(in_group / gm) * kCols;
-  const int e = __builtin_amdgcn_readfirstlane(q.group);
-  const int rows = __builtin_amdgcn_readfirstlane(q.rows);
-  const int* perm = p.plan.perm + __builtin_amdgcn_readfirstlane(q.first);
+  const int r_tile = (gi * kGemmGroupM + in_group % gm) * BM;      // the tile's first row within the expert's
+  const int e = __builtin_amdgcn_readfirstlane(q0.group);
+  const int rows = __builtin_amdgcn_readfirstlane(q0.grows - r_tile < BM ? q0.grows - r_tile : BM);
+  const int* perm = p.plan.perm + __builtin_amdgcn_readfirstlane(q0.gfirst + r_tile);
   auto xrow = [&](int slot) { return MODE == EXPERTS_DOWN ? slot : slot / p.top_k; };
   // weight row of tile column c, -1 past the last
   auto wrow = [&](int c) -> int64_t {

@@ -12,7 +12,8 @@ namespace awqk {
 struct GroupTile {
   int group, first, rows;
   int before, tiles;           // tiles of all groups before this one, tiles of this group
-  int pad[3];
+  int gfirst, grows;           // the group's rows
+  int pad;
 };
 
 // In the caller's workspace.  perm: the rows in sorted order (within a group
@@ -128,7 +129,9 @@ __device__ inline void group_tiles(int* start, int* tstart, int E, int tile_rows
     q.rows = start[lo + 1] - q.first < tile_rows ? start[lo + 1] - q.first : tile_rows;
     q.before = tstart[lo];
     q.tiles = tstart[lo + 1] - tstart[lo];
-    q.pad[0] = q.pad[1] = q.pad[2] = 0;
+    q.gfirst = start[lo];
+    q.grows = start[lo + 1] - start[lo];
+    q.pad = 0;
     plan.tiles[i] = q;
   }
 }
