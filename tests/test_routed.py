@@ -214,6 +214,8 @@ def choices(T, n_exp, k, seed, kind):
         ids[T // 2] = [-1, n_exp, 2 ** 31 - 1, -2 ** 31][T % 4]
     if kind == "none":
         ids[:] = -7
+    if kind == "twice":                              # a token's choices all one expert
+        ids[:] = ids[:, :1]
     return ids
 
 
@@ -275,6 +277,9 @@ PRODUCTS = [
     (260, 2, 2, 128, 514, 128, "f16", "f32", "one"),
     (1030, 16, 8, 192, 70, 64, "bf16", "bf16", "holes"),
     (40, 9, 2, 2176, 34, 128, "bf16", "f32", "holes"),
+    (2, 32, 4, 512, 50, 128, "f16", "f32", "twice"),
+    (9, 20, 4, 512, 50, 128, "f16", "f32", "twice"),
+    (200, 5, 4, 256, 130, 128, "bf16", "f32", "twice"),
     (5, 40, 40, 576, 70, 64, "bf16", "f32", ""),
     (3001, 5, 3, 128, 66, 128, "f16", "f32", "holes"),
     (4099, 3, 2, 64, 18, 64, "bf16", "f32", "one"),
@@ -549,6 +554,113 @@ def test_two_streams_at_once(on_gpu):
     for n, y in enumerate(outs):
         w, x, ids = jobs[n % 2][:3]
         check_up(x, ids, w, 128, "none", torch.float32, y, n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 20, 500])
+def test_given_stream_workspace_and_output(on_gpu, T):
+    """On a stream handed in, as an object or a handle, with memory handed in
+    or made by the call; the memory the caller's own stream gets afterwards is
+    not the call's."""
+    n_exp, k, K, N = 16, 4, 512, 200
+    w = stack(n_exp, N, K, 128, T)
+    x = acts(T, K, torch.float16, 5)
+    ids = choices(T, n_exp, k, 6, "holes")
+    p, gx, gi = packed(w), gpu(x), gpu(torch.from_numpy(ids))
+    need = awq.awq_workspace_bytes(awq.AWQ_OP_EXPERTS_UP, T, N, K, n_exp, k)
+    own = torch.full((need + 256,), 7, dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for stream in (st, st.cuda_stream, torch.cuda.default_stream(), 0):
+        y = torch.empty((T * k, N), device="cuda")
+        torch.cuda.synchronize()
+        outs.append(awq.awq_w4a16_experts_up(gx, gi, *p, y=y, ws=own[:need] if need else None, stream=stream))
+        torch.cuda.synchronize()
+        outs.append(awq.awq_w4a16_experts_up(gx, gi, *p, out_dtype=torch.float32, stream=stream))
+        noise = torch.full((need + 1,), 255, dtype=torch.uint8, device="cuda")   # noqa: F841
+        torch.cuda.synchronize()
+    for y in outs:
+        check_up(x, ids, w, 128, "none", torch.float32, y, T)
+    assert (own[need:] == 7).all()
+    r = awq.awq_route_experts(gx, 3, stream=st)
+    lo = awq.awq_lora_add(gx, gi[:, 0].contiguous(), torch.ones(16, 8, K, dtype=torch.float16, device="cuda"),
+                          torch.ones(16, 8, 8, dtype=torch.float16, device="cuda"), stream=st)
+    torch.cuda.synchronize()
+    compare_route(r, O.route_experts(f32(x), 3), "stream")
+    assert torch.equal(lo, awq.awq_lora_add(gx, gi[:, 0].contiguous(),
+                                            torch.ones(16, 8, K, dtype=torch.float16, device="cuda"),
+                                            torch.ones(16, 8, 8, dtype=torch.float16, device="cuda")))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 90, 2500])
+def test_same_bits_every_time(on_gpu, T):
+    """The order in which rows of one expert or adapter are taken up varies;
+    the results do not."""
+    w = packed(stack(6, 130, 384, 128, 1))
+    x = gpu(acts(T, 384, torch.bfloat16, 2))
+    ids = gpu(torch.from_numpy(choices(T, 6, 3, 3, "holes")))
+    weights = torch.rand(T, 3, device="cuda")
+    h = gpu(acts(T * 3, 384, torch.bfloat16, 4))
+    a, b = torch.randn(6, 24, 384, device="cuda").bfloat16(), torch.randn(6, 100, 24, device="cuda").bfloat16()
+    first = None
+    for _ in range(6):
+        outs = [awq.awq_w4a16_experts_up(x, ids, *w, act="swiglu"), awq.awq_w4a16_experts_down(h, ids, weights, *w),
+                awq.awq_lora_add(x, ids[:, 0].contiguous(), a, b, out_dtype=torch.float32)]
+        if first is None:
+            first = outs
+        assert all(torch.equal(u, v) for u, v in zip(first, outs))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 12, 300])
+def test_experts_past_4_gigabytes(on_gpu, T):
+    """The last expert's words lie past 2^32 bytes of the stack."""
+    n_exp, N, K, k = 40, 8192, 28672, 2
+    q = torch.zeros((n_exp, N, K // 8), dtype=torch.int32, device="cuda")
+    sc = torch.zeros((n_exp, N, K // 256), dtype=torch.float16, device="cuda")
+    z = torch.zeros((n_exp, N, K // 256), dtype=torch.uint8, device="cuda")
+    rows = 96                                        # only these rows of the last expert are not zero
+    w = stack(1, rows, K, 256, T)
+    for big, part in zip((q, sc, z), packed(w)):
+        big[-1, N - rows:] = part[0]
+    sc[:-1] = 1.0                                    # the others' codes are zero points
+    x = acts(T, K, torch.bfloat16, 8)
+    ids = np.tile(np.array([[n_exp - 1, 3]], dtype=np.int32), (T, 1))
+    y = awq.awq_w4a16_experts_up(gpu(x), gpu(torch.from_numpy(ids)), q, sc, z, out_dtype=torch.float32, group_size=256)
+    assert (y[1::2] == 0).all() and (y[::2, :N - rows] == 0).all()
+    check_up(x, np.zeros((T, 1), dtype=np.int32), w, 256, "none", torch.float32, y[::2, N - rows:], T)
+    h = acts(T * k, K, torch.bfloat16, 9)
+    weights = np.random.default_rng(1).uniform(0, 1, (T, k)).astype(np.float32)
+    y = awq.awq_w4a16_experts_down(gpu(h), gpu(torch.from_numpy(ids)), gpu(torch.from_numpy(weights)), q, sc, z,
+                                   out_dtype=torch.float32, group_size=256)
+    assert (y[:, :N - rows] == 0).all()
+    check_down(h[::2], np.zeros((T, 1), dtype=np.int32), weights[:, :1], w, 256, torch.float32, y[:, N - rows:], T)
+
+
+@pytest.mark.gpu
+def test_lora_past_4_gigabytes(on_gpu):
+    """Rows of the output, and adapters, past 2^32 bytes."""
+    M, N, K, R, L = 70000, 32768, 64, 8, 3
+    x = gpu(acts(M, K, torch.bfloat16, 1))
+    a, b = torch.randn(L, R, K, device="cuda").bfloat16(), torch.randn(L, N, R, device="cuda").bfloat16()
+    adapter = torch.randint(-1, L, (M,), device="cuda", dtype=torch.int32)
+    y = torch.full((M, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    awq.awq_lora_add(x, adapter, a, b, base=y, y=y)
+    at = torch.tensor([0, 1, 32767, 65535, 65536, M - 2, M - 1], device="cuda")
+    check_lora(x[at].cpu(), adapter[at].cpu().numpy(), a.cpu(), b.cpu(), None, None,
+               torch.full((len(at), N), 3.0, dtype=torch.bfloat16), torch.bfloat16, y[at], "rows")
+    del y
+    M, N, K, R, L = 40, 16, 65536, 256, 140          # 140 adapters of 32 MiB
+    x = gpu(acts(M, K, torch.float16, 2))
+    a = torch.zeros((L, R, K), dtype=torch.float16, device="cuda")
+    a[-1] = torch.randn(R, K, device="cuda").half() / 256
+    b = torch.randn(L, N, R, device="cuda").half()
+    adapter = torch.full((M,), L - 1, dtype=torch.int32, device="cuda")
+    y = awq.awq_lora_add(x, adapter, a, b, out_dtype=torch.float32)
+    check_lora(x[:3].cpu(), np.zeros(3, dtype=np.int32), a[-1:].cpu(), b[-1:].cpu(), None, None, None, torch.float32,
+               y[:3], "adapters")
 
 
 # ---- refusals (no launch, so no GPU) ----------------------------------------------------

@@ -306,20 +306,26 @@ def _out(y: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dtyp
     return y, ld
 
 
-def _launch(name: str, device: torch.device, stream, args: tuple) -> None:
-    """Calls the entry point with the stream appended, on the tensors' device."""
+def _launch(name: str, device: torch.device, args: tuple) -> None:
+    """Calls the entry point on the tensors' device and its current stream."""
     fn = getattr(lib(), name)
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if device.index == torch._C._cuda_getDevice():
-        st = fn(*args, raw)
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, raw)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     if st:
         _abi.check(name, st)
+
+
+def _on_stream(stream, t: torch.Tensor):
+    """Makes a given stream (or its handle) the current one, so that outputs
+    and workspaces made for the call belong to it."""
+    _dev(t, "the first tensor")
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, t.device) if raw else torch.cuda.default_stream(t.device)
+    return torch.cuda.stream(stream)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -352,6 +358,10 @@ def awq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | Non
     a group worth the sum of its group_top (1 or 2) best choices.  A logit of
     -inf or NaN switches an expert off; where fewer than top_k are left the ids
     are -1 with weight 0."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return awq_route_experts(logits, top_k, bias, score, n_group, topk_group, group_top, renormalize, scale,
+                                     ids, weights)
     T, E, ldl = _act_rows(logits, "logits")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
@@ -360,7 +370,7 @@ def awq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | Non
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    _launch("awq_route_experts", dev, stream,
+    _launch("awq_route_experts", dev,
             (logits.data_ptr(), _DT.get(logits.dtype, -1), T, E, ldl,
              _same(bias, "bias", dev, torch.float32, (E,)), _SCORES[score], n_group, topk_group, group_top, top_k,
              int(bool(renormalize)), scale, _same(ids, "ids", dev, torch.int32, (T, top_k)),
@@ -369,6 +379,9 @@ def awq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | Non
 
 
 def _experts(name, op, x, ids, weights, qweight, scales, zeros, act, out_dtype, y, group_size, ws, stream):
+    if stream is not None:
+        with _on_stream(stream, x):
+            return _experts(name, op, x, ids, weights, qweight, scales, zeros, act, out_dtype, y, group_size, ws, None)
     rows, K, ldx = _act_rows(x, "x")
     dev = x.device
     if ids.dim() != 2:
@@ -394,7 +407,7 @@ def _experts(name, op, x, ids, weights, qweight, scales, zeros, act, out_dtype, 
         args = head + (top_k,) + packed + (E, N, group_size, act) + tail
     else:
         args = head + (_same(weights, "weights", dev, torch.float32, (M, top_k)), top_k) + packed + (E, N, group_size) + tail
-    _launch(name, dev, stream, args)
+    _launch(name, dev, args)
     return y
 
 
@@ -434,6 +447,9 @@ def awq_lora_add(x: torch.Tensor, adapter: torch.Tensor, a: torch.Tensor, b: tor
     x [M, K]; adapter int32 [M]; a [adapters, R, K] and b [adapters, N, R] of
     x's dtype; ranks int32 [adapters] (None: R); scaling float32 [adapters].
     base has the output's dtype and may be y itself."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return awq_lora_add(x, adapter, a, b, base, scaling, ranks, out_dtype, y, ws)
     M, K, ldx = _act_rows(x, "x")
     dev = x.device
     if a.dim() != 3 or b.dim() != 3:
@@ -447,7 +463,7 @@ def awq_lora_add(x: torch.Tensor, adapter: torch.Tensor, a: torch.Tensor, b: tor
         base, ldb = _out(base, "base", dev, y.dtype, M, N)
         basep = base.data_ptr()
     ws, wsp, wsb = _ws(_abi.AWQ_OP_LORA, dev, ws, M, N, K, L, R)
-    _launch("awq_lora_add", dev, stream,
+    _launch("awq_lora_add", dev,
             (x.data_ptr(), _DT.get(x.dtype, -1), M, K, ldx, _same(adapter, "adapter", dev, torch.int32, (M,)),
              _same(a, "a", dev, x.dtype, (L, R, K)), _same(b, "b", dev, x.dtype, (L, N, R)), L, R,
              _same(ranks, "ranks", dev, torch.int32, (L,)), _same(scaling, "scaling", dev, torch.float32, (L,)),
