@@ -358,7 +358,6 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   __syncthreads();                                 // every wave is done with the stages
   constexpr int kW = MODE == EXPERTS_SWIGLU ? 32 : 64;                    // outputs per row of the wave
   float* stg = reinterpret_cast<float*>(lds) + wv * 16 * (kW + 4);
-  constexpr int kL = kW / 4;                       // lanes per row, four outputs each
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
     const int r0 = m * 16;
@@ -378,41 +377,62 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): the wave's writes landed
     __builtin_amdgcn_wave_barrier();
+    if (MODE == EXPERTS_DOWN ? p.rexp == nullptr : p.ydt == DT_F32) {
+      constexpr int kL = kW / 4;                   // lanes per row, four outputs each
 #pragma unroll
-    for (int i = 0; i < 16 * kL / 64; ++i) {
-      const int r = i * (64 / kL) + lane / kL, c = (lane % kL) * 4;
-      const f32x4 o = *reinterpret_cast<const f32x4*>(stg + r * (kW + 4) + c);
-      if (MODE == EXPERTS_DOWN && p.rexp) {
-        // fp16 scaled by a power of two per row and 64 columns
-        const float am = row16_max(fmaxf(fmaxf(fabsf(o[0]), fabsf(o[1])), fmaxf(fabsf(o[2]), fabsf(o[3]))));
-        const int pe = min(pow2_exp_for(am), 100);
+      for (int i = 0; i < 16 * kL / 64; ++i) {
+        const int r = i * (64 / kL) + lane / kL, c = (lane % kL) * 4;
+        const f32x4 o = *reinterpret_cast<const f32x4*>(stg + r * (kW + 4) + c);
+        if (r0 + r >= rows) continue;
         const int64_t col = c0 + wv * kW + c;
-        if (r0 + r >= rows || col >= p.ldy) continue;
-        const int64_t slot = slots[r0 + r];
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = f32_to_f16_bits(ldexpf(o[j], pe));
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.y) + slot * p.ldy + col) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        if (c == 0) p.rexp[slot * (p.ldy >> 6) + (col >> 6)] = (int8_t)pe;
-        continue;
-      }
-      if (r0 + r >= rows) continue;
-      const int64_t col = c0 + wv * kW + c, pos = (int64_t)slots[r0 + r] * p.ldy + col;
-      if (MODE == EXPERTS_DOWN || p.ydt == DT_F32) {
-        float* y = reinterpret_cast<float*>(p.y) + pos;
+        float* y = reinterpret_cast<float*>(p.y) + (int64_t)slots[r0 + r] * p.ldy + col;
         if (p.vec && col + 4 <= ncols) *reinterpret_cast<f32x4*>(y) = o;
         else
           for (int j = 0; j < 4; ++j)
             if (col + j < ncols) y[j] = o[j];
-      } else {
-        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + pos;
-        uint32_t h[4];
+      }
+    } else {
+      constexpr int kL = kW / 8;                   // lanes per row, eight outputs each
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = p.ydt == DT_F16 ? f32_to_f16_bits(o[j]) : f32_to_bf16_bits(o[j]);
-        if (p.vec && col + 4 <= ncols) *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        else
-          for (int j = 0; j < 4; ++j)
-            if (col + j < ncols) y[j] = (uint16_t)h[j];
+      for (int i = 0; i < 16 * kL / 64; ++i) {
+        const int r = i * (64 / kL) + lane / kL, c = (lane % kL) * 8;
+        const f32x4 o0 = *reinterpret_cast<const f32x4*>(stg + r * (kW + 4) + c);
+        const f32x4 o1 = *reinterpret_cast<const f32x4*>(stg + r * (kW + 4) + c + 4);
+        const int64_t col = c0 + wv * kW + c;
+        uint32_t h[8];
+        if constexpr (MODE == EXPERTS_DOWN) {
+          // fp16 scaled by a power of two per row and 64 columns (eight lanes)
+          float am = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) am = fmaxf(am, fmaxf(fabsf(o0[j]), fabsf(o1[j])));
+          am = fmaxf(am, quad_xor1(am));
+          am = fmaxf(am, quad_xor2(am));
+          am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
+          const int pe = min(pow2_exp_for(am), 100);
+          if (r0 + r >= rows || col >= p.ldy) continue;
+          const int64_t slot = slots[r0 + r];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            h[j] = f32_to_f16_bits(ldexpf(o0[j], pe));
+            h[4 + j] = f32_to_f16_bits(ldexpf(o1[j], pe));
+          }
+          *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + slot * p.ldy + col) =
+              u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+          if (c == 0) p.rexp[slot * (p.ldy >> 6) + (col >> 6)] = (int8_t)pe;
+        } else {
+          if (r0 + r >= rows) continue;
+          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + (int64_t)slots[r0 + r] * p.ldy + col;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            h[j] = p.ydt == DT_F16 ? f32_to_f16_bits(o0[j]) : f32_to_bf16_bits(o0[j]);
+            h[4 + j] = p.ydt == DT_F16 ? f32_to_f16_bits(o1[j]) : f32_to_bf16_bits(o1[j]);
+          }
+          if (p.vec && col + 8 <= ncols)
+            *reinterpret_cast<u32x4*>(y) = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+          else
+            for (int j = 0; j < 8; ++j)
+              if (col + j < ncols) y[j] = (uint16_t)h[j];
+        }
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -480,8 +500,7 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, int
   a.group = c.group;
   a.unit = c.group == 64 ? 64 : 128;
   a.ydt = down ? DT_F32 : c.ydt;
-  const size_t es = a.ydt == DT_F32 ? 4 : 2;
-  a.vec = ldo % 4 == 0 && (uintptr_t)out % (4 * es) == 0;
+  a.vec = ldo % (a.ydt == DT_F32 ? 4 : 8) == 0 && (uintptr_t)out % 16 == 0;   // 16-byte stores
   a.xq = reinterpret_cast<uint16_t*>(w + g.xq);
   a.pexp = reinterpret_cast<int*>(w + g.pexp);
   a.ctab = reinterpret_cast<uint32_t*>(w + g.ctab);
