@@ -317,6 +317,22 @@ def test_experts_down(on_gpu, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    # rows dealt to many blocks, an even share each or all on one expert
+    (900, 2, 1, 192, 130, 64, "f16", "f32", "one"),
+    (2000, 30, 2, 384, 34, 128, "bf16", "f32", "one"),
+    (1500, 5, 2, 256, 18, 256, "f16", "bf16", "holes"),
+    # tiles of 64 rows and of 128 rows
+    (1100, 3, 2, 64, 4000, 64, "bf16", "f32", "holes"),
+    (6500, 5, 2, 64, 4098, 64, "f16", "bf16", "holes"),
+], ids=lambda c: "x".join(str(v) for v in c))
+def test_experts_dealt_rows_and_tall_tiles(on_gpu, case):
+    test_experts_up(on_gpu, case, "none")
+    test_experts_up(on_gpu, case, "swiglu")
+    test_experts_down(on_gpu, case)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [2, 90, 400])
 def test_experts_strides_and_neighbours(on_gpu, T):
     """Padded input and output rows: what lies beside the output stays."""

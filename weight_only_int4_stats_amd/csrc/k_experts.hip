@@ -107,7 +107,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
     const int64_t cols = MODE == EXPERTS_SWIGLU ? halfN : p.N;
     const int64_t per = MODE == EXPERTS_SWIGLU ? 8 * kFewTiles : 16 * kFewTiles;
     const int64_t c = (int64_t)blockIdx.x * per + (lane % per);
-    for (int s = s0; s < s1; ++s) {
+    for (int s = (int)blockIdx.z * kFewWaves + wv; s < p.S; s += (int)gridDim.z * kFewWaves) {
       const int id = p.ids[s];
       if ((id < 0 || id >= p.E) && lane < per && c < cols) store_out(p.y, p.ydt, (int64_t)s * p.ldy + c, 0.0f);
     }
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
     rows += c;
   }
   rows = __builtin_amdgcn_readfirstlane(rows);
-  if (rows == 0) return;
+  if (rows <= 16 * (int)blockIdx.z) return;
 
   // ---- the block's weight rows: tile t holds rows tile_row(t) .. + 15 of the
   // expert, rows_in(t) of them; with SwiGLU tiles alternate gate, up
@@ -164,7 +164,8 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
   const uint8_t* wlds = lds + kFewORing + wv * kFewPairs * 2048 + (rl >> 3) * 1024 + (rl & 7) * 128;
   const int wsw = ((rl & 7) >> 1) | ((rl >> 3) << 2);
 
-  for (int r0 = 0; r0 < rows; r0 += 16) {
+  const int rz = 16 * (int)gridDim.z;              // the rows are dealt to gridDim.z blocks, 16 at a time
+  for (int r0 = 16 * (int)blockIdx.z; r0 < rows; r0 += rz) {
     const int nr = rows - r0 < 16 ? rows - r0 : 16;
     // ---- the pass's slots: ranks r0 .. r0 + nr - 1 among the expert's
     int run = before;
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
       run += __popcll(m);
     }
     __syncthreads();
-    if (r0 == 0 && p.by_slot && list[0] != grp) return;          // another slot's block has this expert
+    if (p.by_slot && r0 == 0 && list[0] != grp) return;          // another slot's block has this expert
 
     // channels per chunk: whole pairs, as many as fit the staged activations and the steps
     int kc = (kFewX / 2 / nr - 8) & ~255;
@@ -546,10 +547,23 @@ using namespace awqk;
 
 static int64_t partial_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
-// Few rows per expert (this file) or tiles (k_experts_gemm.hip).  64 experts:
-// at 3 rows each (2048 -> 2 x 1024) 37 us against 43 us in tiles, at 12 rows
-// (1024 -> 2049) 62 us against 45 us.
-static bool few_rows(int64_t S, int64_t E) { return S <= 6 * E && S <= 4096; }
+// Few rows per expert (this file) or tiles (k_experts_gemm.hip): few rows per
+// expert, or 512 blocks (two per CU) do all 16-row passes at once while a
+// tile's one block walks all of K.  64 experts: at 3 rows each (2048 -> 2 x
+// 1024) 37 us against 43 us in tiles, at 12 rows (1024 -> 2049, 1650 blocks)
+// 62 us against 45 us.  344 rows on each of 5 (3200 -> 2 x 10, 110 blocks) 27
+// us against 45 us, 18 on each of 34 (2048 -> 231, 220 blocks) 24 us against 37
+// us; 34 on each of 16 (256 -> 1524, 1000 blocks) 23 us against 20 us.
+static bool few_rows(int64_t S, int64_t E, int64_t N) {
+  return S <= 4096 && (S <= 6 * E || (S / 16 + E / 2 + 1) * ((N + 63) / 64) <= 512);
+}
+
+// Blocks that share an expert's rows, 16 at a time: twice the even share.
+static unsigned few_deal(int64_t S, int64_t E) {
+  if (S < E) return 1;                             // one block row per slot: the first has all
+  const int64_t z = (S / E + 7) / 8;
+  return (unsigned)(z < 1 ? 1 : z > 256 ? 256 : z);
+}
 
 static int64_t partial16_ld(int64_t N) { return (N + 63) / 64 * 64; }
 static size_t partial16_rows(int64_t S, int64_t N) { return align_up((size_t)S * (size_t)partial16_ld(N) * 2, 256); }
@@ -565,7 +579,7 @@ static size_t partial_bytes(bool down, int64_t S, int64_t N) {
 size_t experts_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k) {
   const int64_t S = M * top_k;
   if (down && token_slices(S, E, K, (int)top_k)) return 0;
-  return partial_bytes(down, S, N) + (few_rows(S, E) ? 0 : experts_gemm_ws_bytes(down, M, N, K, E, top_k));
+  return partial_bytes(down, S, N) + (few_rows(S, E, N) ? 0 : experts_gemm_ws_bytes(down, M, N, K, E, top_k));
 }
 
 hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
@@ -585,7 +599,7 @@ hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
     else hipLaunchKernelGGL((k_experts_token<DT_F16, false>), grid, block, kTokenLds, st, a, c.weights, slices);
     return hipGetLastError();
   }
-  if (!few_rows(S, c.E)) {
+  if (!few_rows(S, c.E, c.N)) {
     char* rest = reinterpret_cast<char*>(ws) + partial_bytes(down, S, c.N);
     if (!down || c.ydt != DT_BF16) {
       e = launch_experts_gemm(c, out, ldo, nullptr, rest, st);
@@ -606,7 +620,7 @@ hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
                     c.group == 64 ? 6 : c.group == 128 ? 7 : 8, c.ydt, S < c.E, (int)(S < c.E ? S : c.E)};
     const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
     const int64_t per = c.mode == EXPERTS_SWIGLU ? 8 * kFewTiles : 16 * kFewTiles;
-    const dim3 grid((unsigned)((cols + per - 1) / per), (unsigned)(a.groups + (down ? 0 : 1)));
+    const dim3 grid((unsigned)((cols + per - 1) / per), (unsigned)(a.groups + (down ? 0 : 1)), few_deal(S, c.E));
     const bool bf = c.xdt == DT_BF16;
     if (c.mode == EXPERTS_UP) bf ? few_launch<DT_BF16, EXPERTS_UP>(a, grid, st) : few_launch<DT_F16, EXPERTS_UP>(a, grid, st);
     else if (c.mode == EXPERTS_SWIGLU) bf ? few_launch<DT_BF16, EXPERTS_SWIGLU>(a, grid, st) : few_launch<DT_F16, EXPERTS_SWIGLU>(a, grid, st);

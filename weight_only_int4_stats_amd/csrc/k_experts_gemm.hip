@@ -451,10 +451,14 @@ void gemm_launch(const GemmArgs& a, const dim3& grid, hipStream_t st) {
 namespace awq {
 using namespace awqk;
 
-// Rows per tile for S slots over E experts.
-static int gemm_tile_rows(int64_t S, int64_t E) {
-  const int64_t avg = S / E;
-  return avg > 96 ? 128 : avg > 40 ? 64 : 32;
+// Rows per tile for S slots over E experts: tall tiles spend the fewest
+// unpacks, but a tile walks all of K, so the card has to be full of them.
+// 7188 rows on 19 experts (1408 -> 1076): 84 us with 128 rows (330 tiles), 77
+// with 64 (600), 83 with 32 (1200).  25956 on 29 (1408 -> 2893): 325, 344, 407
+// (2600 tiles of 128).  5734 on 6 (3136 -> 2 x 47, 45 tiles of 128): 92, 69, 57.
+static int gemm_tile_rows(int64_t S, int64_t E, int64_t N) {
+  const int64_t avg = S / E, cols = (N + kGemmN - 1) / kGemmN;
+  return avg > 96 && S / 128 * cols >= 1536 ? 128 : avg > 40 && S / 64 * cols >= 512 ? 64 : 32;
 }
 
 struct GemmSpace {
@@ -467,7 +471,7 @@ static GemmSpace gemm_space(bool down, int64_t M, int64_t N, int64_t K, int64_t 
   g.pexp = g.xq + align_up((size_t)xrows * (size_t)K * 2, 256);
   g.ctab = g.pexp + align_up((size_t)xrows * 4, 256);
   g.plan = g.ctab + align_up((size_t)E * (size_t)N * (size_t)(K / (group == 64 ? 64 : 128)) * 4, 256);
-  g.total = g.plan + group_plan_bytes(S, E, gemm_tile_rows(S, E));
+  g.total = g.plan + group_plan_bytes(S, E, gemm_tile_rows(S, E, N));
   return g;
 }
 
@@ -479,7 +483,7 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, int
   const bool down = c.mode == EXPERTS_DOWN;
   const int64_t S = c.M * c.top_k;
   const GemmSpace g = gemm_space(down, c.M, c.N, c.K, c.E, c.top_k, c.group);
-  const int tile = gemm_tile_rows(S, c.E);
+  const int tile = gemm_tile_rows(S, c.E, c.N);
   char* w = reinterpret_cast<char*>(ws);
   GemmArgs a{};
   a.x = c.x;
