@@ -15,6 +15,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// The same at addresses that are only a multiple of 2 or 4 bytes: one access
+// all the same, where the caller's rows need not start on 16 bytes.
+typedef uint32_t u32x4a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // Element type tags: 0 = fp16, 1 = bf16 (same values as awq_dtype).
 enum : int { DT_F16 = 0, DT_BF16 = 1, DT_F32 = 2 };

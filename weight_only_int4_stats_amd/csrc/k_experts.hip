@@ -48,7 +48,7 @@ constexpr int kFewOPinv = kFewX;
 constexpr int kFewOMeta = kFewOPinv + kFewUnits * 16 * 4;
 constexpr int kFewORing = kFewOMeta + kFewTiles * 16 * kFewPitch * 8;
 constexpr int kFewOList = kFewORing + kFewWaves * kFewPairs * 2048;
-constexpr int kFewLds = kFewOList + 16 * 4 + kFewWaves * 4 + 32;   // two blocks per compute unit
+constexpr int kFewLds = kFewOList + 16 * 4 + 2 * kFewWaves * 4;   // two blocks per compute unit
 static_assert(kFewLds <= 80 * 1024, "two blocks per compute unit");
 static_assert(kFewORing % 16 == 0 && kFewOList % 16 == 0, "LDS regions");
 
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
   float* pinv = reinterpret_cast<float*>(lds + kFewOPinv);       // [128-channel unit][16 rows]
   uint2* meta = reinterpret_cast<uint2*>(lds + kFewOMeta);       // [weight row][kFewPitch]: step 2^9, -z 2^-9
   int* list = reinterpret_cast<int*>(lds + kFewOList);           // [16] slots
-  int* wcount = list + 16;                                       // [kFewWaves]
+  int* wcount = list + 16;                                       // [2][kFewWaves]
 
   const int grp = blockIdx.y;
   const int64_t halfN = p.N >> 1;
@@ -113,19 +113,34 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
     }
     return;
   }
-  int cnt = 0;
-  for (int s = s0; s < s1; s += 64) cnt += __popcll(__ballot(s + lane < s1 && p.ids[s + lane < s1 ? s + lane : s0] == e));
-  if (lane == 0) wcount[wv] = cnt;
+  // and, with a block row per slot, how many of them come before it
+  int cnt = 0, ahead = 0;
+  for (int s = s0; s < s1; s += 64) {
+    const uint64_t m = __ballot(s + lane < s1 && p.ids[s + lane < s1 ? s + lane : s0] == e);
+    cnt += __popcll(m);
+    ahead += s >= grp ? 0 : __popcll(grp - s < 64 ? m & ((1ull << (grp - s)) - 1) : m);
+  }
+  if (lane == 0) {
+    wcount[wv] = cnt;
+    wcount[kFewWaves + wv] = ahead;
+  }
   __syncthreads();
   int rows = 0, before = 0;
+  ahead = 0;
 #pragma unroll
   for (int w = 0; w < kFewWaves; ++w) {
     const int c = wcount[w];
     if (w < wv) before += c;
     rows += c;
+    ahead += wcount[kFewWaves + w];
   }
   rows = __builtin_amdgcn_readfirstlane(rows);
-  if (rows <= 16 * (int)blockIdx.z) return;
+  // The block's passes of 16 rows.  A block row per slot: 16 from its own on,
+  // of every 16th slot; a block row per expert: dealt to gridDim.z blocks.
+  const int r_first = p.by_slot ? __builtin_amdgcn_readfirstlane(ahead) : 16 * (int)blockIdx.z;
+  if (p.by_slot && (r_first & 15)) return;
+  const int r_step = 16 * (int)gridDim.z, r_end = p.by_slot && r_first + 16 < rows ? r_first + 16 : rows;
+  if (r_first >= r_end) return;
 
   // ---- the block's weight rows: tile t holds rows tile_row(t) .. + 15 of the
   // expert, rows_in(t) of them; with SwiGLU tiles alternate gate, up
@@ -164,8 +179,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
   const uint8_t* wlds = lds + kFewORing + wv * kFewPairs * 2048 + (rl >> 3) * 1024 + (rl & 7) * 128;
   const int wsw = ((rl & 7) >> 1) | ((rl >> 3) << 2);
 
-  const int rz = 16 * (int)gridDim.z;              // the rows are dealt to gridDim.z blocks, 16 at a time
-  for (int r0 = 16 * (int)blockIdx.z; r0 < rows; r0 += rz) {
+  for (int r0 = r_first; r0 < r_end; r0 += r_step) {
     const int nr = rows - r0 < 16 ? rows - r0 : 16;
     // ---- the pass's slots: ranks r0 .. r0 + nr - 1 among the expert's
     int run = before;
@@ -177,7 +191,6 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
       run += __popcll(m);
     }
     __syncthreads();
-    if (p.by_slot && r0 == 0 && list[0] != grp) return;          // another slot's block has this expert
 
     // channels per chunk: whole pairs, as many as fit the staged activations and the steps
     int kc = (kFewX / 2 / nr - 8) & ~255;
@@ -481,9 +494,17 @@ __global__ __launch_bounds__(256) void k_experts_combine(const float* __restrict
   #pragma unroll
       for (int c = 0; c < 4; ++c) s[c] = __builtin_fmaf(w, v[c], s[c]);
     }
-  #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (n + c < N) store_out(y, YDT, m * ldy + n + c, s[c]);
+    if (n + 4 <= N) {
+      if constexpr (YDT == DT_F32)
+        *reinterpret_cast<u32x4a4*>(reinterpret_cast<float*>(y) + m * ldy + n) = __builtin_bit_cast(u32x4, s);
+      else
+        *reinterpret_cast<u32x2a2*>(reinterpret_cast<uint16_t*>(y) + m * ldy + n) =
+            u32x2a2{from_f32<YDT>(s[0]) | (from_f32<YDT>(s[1]) << 16), from_f32<YDT>(s[2]) | (from_f32<YDT>(s[3]) << 16)};
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (n + c < N) store_out(y, YDT, m * ldy + n + c, s[c]);
+    }
   }
 }
 
@@ -494,8 +515,7 @@ __global__ __launch_bounds__(256) void k_experts_combine16(const uint16_t* __res
                                                            const int8_t* __restrict__ rexp,
                                                            const int32_t* __restrict__ ids,
                                                            const float* __restrict__ weights, int top_k, int E,
-                                                           int64_t M, int64_t N, void* __restrict__ y, int64_t ldy,
-                                                           int vec) {
+                                                           int64_t M, int64_t N, void* __restrict__ y, int64_t ldy) {
   const int64_t n8 = (N + 7) >> 3;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * n8; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / n8, n = (i - m * n8) * 8;
@@ -511,11 +531,11 @@ __global__ __launch_bounds__(256) void k_experts_combine16(const uint16_t* __res
       for (int c = 0; c < 8; ++c)
         s[c] = __builtin_fmaf(w, c & 1 ? hi_f32<DT_F16>(v[c >> 1]) : lo_f32<DT_F16>(v[c >> 1]), s[c]);
     }
-    if (vec && n + 8 <= N) {
+    if (n + 8 <= N) {
       u32x4 o;
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[c] = from_f32<YDT>(s[2 * c]) | (from_f32<YDT>(s[2 * c + 1]) << 16);
-      *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(y) + m * ldy + n) = o;
+      *reinterpret_cast<u32x4a2*>(reinterpret_cast<uint16_t*>(y) + m * ldy + n) = o;
     } else {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -560,7 +580,7 @@ static bool few_rows(int64_t S, int64_t E, int64_t N) {
 
 // Blocks that share an expert's rows, 16 at a time: twice the even share.
 static unsigned few_deal(int64_t S, int64_t E) {
-  if (S < E) return 1;                             // one block row per slot: the first has all
+  if (S < E) return 1;                             // block rows per slot
   const int64_t z = (S / E + 7) / 8;
   return (unsigned)(z < 1 ? 1 : z > 256 ? 256 : z);
 }
@@ -610,9 +630,8 @@ hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
       if (e != hipSuccess) return e;
       int64_t blocks = (c.M * ((c.N + 7) / 8) + 255) / 256;
       if (blocks > (1 << 20)) blocks = 1 << 20;
-      const int vec = c.ldy % 8 == 0 && (uintptr_t)c.y % 16 == 0;
       hipLaunchKernelGGL((k_experts_combine16<DT_BF16>), dim3((unsigned)blocks), dim3(256), 0, st, (const uint16_t*)ws,
-                         ld16, rexp, c.ids, c.weights, c.top_k, (int)c.E, c.M, c.N, c.y, c.ldy, vec);
+                         ld16, rexp, c.ids, c.weights, c.top_k, (int)c.E, c.M, c.N, c.y, c.ldy);
       return hipGetLastError();
     }
   } else {

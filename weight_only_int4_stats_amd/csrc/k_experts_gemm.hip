@@ -56,7 +56,7 @@ struct GemmArgs {
   void* y;
   int64_t xrows;
   int8_t* rexp;                                    // down with 16-bit rows: their exponents, one per 64 columns
-  int S, E, top_k, group, unit, ydt, vec;          // unit: channels per constant (64 or 128, at most the group)
+  int S, E, top_k, group, unit, ydt;          // unit: channels per constant (64 or 128, at most the group)
   // workspace
   uint16_t* xq;                                    // [xrows][K]
   int* pexp;                                       // [xrows]
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
         if (r0 + r >= rows) continue;
         const int64_t col = c0 + wv * kW + c;
         float* y = reinterpret_cast<float*>(p.y) + (int64_t)slots[r0 + r] * p.ldy + col;
-        if (p.vec && col + 4 <= ncols) *reinterpret_cast<f32x4*>(y) = o;
+        if (col + 4 <= ncols) *reinterpret_cast<u32x4a4*>(y) = __builtin_bit_cast(u32x4, o);
         else
           for (int j = 0; j < 4; ++j)
             if (col + j < ncols) y[j] = o[j];
@@ -427,8 +427,8 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
             h[j] = p.ydt == DT_F16 ? f32_to_f16_bits(o0[j]) : f32_to_bf16_bits(o0[j]);
             h[4 + j] = p.ydt == DT_F16 ? f32_to_f16_bits(o1[j]) : f32_to_bf16_bits(o1[j]);
           }
-          if (p.vec && col + 8 <= ncols)
-            *reinterpret_cast<u32x4*>(y) = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+          if (col + 8 <= ncols)
+            *reinterpret_cast<u32x4a2*>(y) = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
           else
             for (int j = 0; j < 8; ++j)
               if (col + j < ncols) y[j] = (uint16_t)h[j];
@@ -504,7 +504,6 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, int
   a.group = c.group;
   a.unit = c.group == 64 ? 64 : 128;
   a.ydt = down ? DT_F32 : c.ydt;
-  a.vec = ldo % (a.ydt == DT_F32 ? 4 : 8) == 0 && (uintptr_t)out % 16 == 0;   // 16-byte stores
   a.xq = reinterpret_cast<uint16_t*>(w + g.xq);
   a.pexp = reinterpret_cast<int*>(w + g.pexp);
   a.ctab = reinterpret_cast<uint32_t*>(w + g.ctab);

@@ -5,7 +5,8 @@
 //
 // Both products run on the matrix cores over 16 rows of one adapter.  Up to
 // kLoraScan rows, a block finds its adapter's rows by scanning the index (as
-// many block rows as rows or adapters, whichever is fewer); beyond that a plan
+// many block rows as rows or adapters, whichever is fewer; many rows of few
+// adapters are dealt to more blocks, 16 at a time); beyond that a plan
 // sorts the rows by adapter and a block takes 16 (shrink) or 64 (expand) of
 // one adapter's.  The shrink splits K over blocks and waves; the expand sums
 // the blocks' parts in their order.
@@ -18,7 +19,9 @@
 
 namespace awqk {
 
-constexpr int kLoraScan = 512;       // rows up to which the blocks find their rows themselves
+// Rows up to which the blocks find their rows themselves: at 1462 rows of 8
+// adapters (424 -> 4502) a call takes 98 us so, 30 us with a plan.
+constexpr int kLoraScan = 512;
 constexpr int kLoraTile = 64;        // rows per tile of the plan
 constexpr int kLoraMaxSplit = 32;    // K splits of the shrink
 
@@ -36,7 +39,7 @@ struct LoraArgs {
   int64_t ldy, N;
   float* h;                          // [ksplit][M][R]
   GroupPlan plan;
-  int M, K, R, n_adapters, ksplit, planned, by_row, nx, vec;   // nx: blocks per block row
+  int M, K, R, n_adapters, ksplit, planned, by_row, nx, deal;   // nx: blocks per block row; deal below
 };
 
 template <int DT>
@@ -48,20 +51,28 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f3
 // The rows a block works on: its adapter (-1: none) and how many.
 struct LoraRows {
   int a, n;
+  int first, end;                    // the block's passes start at ranks first, first + step, ... < end
   const int* perm;                   // planned: the rows
   uint64_t mask;                     // up to 64 rows in all: which
   int before;                        // else: rows before this wave's share of the index
 };
 
-// Finds the block's adapter and counts its rows; with a block per row, those
-// of all but the adapter's first row leave (n = 0).  count_lds: two ints per wave.
-__device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int* count_lds) {
-  LoraRows r{-1, 0, nullptr, 0, 0};
+// Finds the block's adapter, counts its rows and says which of them are the
+// block's (n = 0: none).  With a block per row, every 16th of an adapter's rows
+// is the first of 16; with a block row per adapter, p.deal blocks share it and
+// this is the part-th.  count_lds: two ints per wave.
+__device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int part, int* count_lds) {
+  LoraRows r{-1, 0, 0, 0, nullptr, 0, 0};
+  auto mine16 = [&](int n, int ahead) {
+    r.first = p.by_row ? ahead : 16 * part;
+    r.end = p.by_row && ahead + 16 < n ? ahead + 16 : n;
+    r.n = (p.by_row && (ahead & 15)) || r.first >= n ? 0 : n;
+  };
   if (p.planned) {
     if (grp >= p.plan.ntile[0]) return r;
     const GroupTile q = p.plan.tiles[grp];
     r.a = q.group < p.n_adapters ? q.group : -1;
-    r.n = q.rows;
+    r.n = r.end = q.rows;
     r.perm = p.plan.perm + q.first;
     return r;
   }
@@ -71,29 +82,30 @@ __device__ __forceinline__ LoraRows lora_rows(const LoraArgs& p, int grp, int* c
     const int mine = norm(p.adapter[lane < p.M ? lane : 0]);
     r.a = p.by_row ? __builtin_amdgcn_readlane(mine, grp) : grp < p.n_adapters ? grp : -1;
     r.mask = __ballot(lane < p.M && mine == r.a);
-    r.n = p.by_row && __builtin_ctzll(r.mask) != grp ? 0 : __popcll(r.mask);
+    mine16(__popcll(r.mask), __popcll(r.mask & ((1ull << (grp & 63)) - 1)));
     return r;
   }
   r.a = p.by_row ? norm(p.adapter[grp]) : grp < p.n_adapters ? grp : -1;
   const int s0 = wv * p.M / nw, s1 = (wv + 1) * p.M / nw;
-  int cnt = 0, first = 0x7FFFFFFF;
+  int cnt = 0, ahead = 0;            // of the wave's share; of them before row grp
   for (int s = s0; s < s1; s += 64) {
     const uint64_t m = __ballot(s + lane < s1 && norm(p.adapter[s + lane < s1 ? s + lane : s0]) == r.a);
-    if (m && first == 0x7FFFFFFF) first = s + __builtin_ctzll(m);
+    ahead += s >= grp ? 0 : __popcll(grp - s < 64 ? m & ((1ull << (grp - s)) - 1) : m);
     cnt += __popcll(m);
   }
   if (lane == 0) {
     count_lds[wv] = cnt;
-    count_lds[nw + wv] = first;
+    count_lds[nw + wv] = ahead;
   }
   __syncthreads();
-  int n = 0, f = 0x7FFFFFFF;
+  int n = 0;
+  ahead = 0;
   for (int w = 0; w < nw; ++w) {
     if (w < wv) r.before += count_lds[w];
     n += count_lds[w];
-    f = count_lds[nw + w] < f ? count_lds[nw + w] : f;
+    ahead += count_lds[nw + w];
   }
-  r.n = p.by_row && f != grp ? 0 : n;
+  mine16(n, ahead);
   return r;
 }
 
@@ -206,13 +218,14 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void k_lora_shrink(const LoraArg
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
-  const int bx = (int)(blockIdx.x % (unsigned)p.ksplit), by = (int)(blockIdx.x / (unsigned)p.ksplit);
+  const int bx = (int)(blockIdx.x % (unsigned)p.ksplit), byd = (int)(blockIdx.x / (unsigned)p.ksplit);
+  const int by = byd / p.deal, dealt = byd % p.deal;
   constexpr int kSub = kLoraTile / (16 * MT);      // blocks per tile of the plan
   int known;
   LoraAdapter ad{0, 0.0f};
   const bool early = lora_known(p, by, known);
   if (early) ad = lora_adapter(p, known);
-  const LoraRows r = lora_rows(p, p.planned ? by / kSub : by, count);
+  const LoraRows r = lora_rows(p, p.planned ? by / kSub : by, dealt, count);
   if (r.a < 0 || r.n == 0) return;
   if (!early) ad = lora_adapter(p, r.a);
   const int rank = ad.rank;
@@ -220,9 +233,9 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void k_lora_shrink(const LoraArg
   const int part = bx * W + wv, parts = p.ksplit * W;
   const int k0 = (int)((int64_t)part * steps / parts), k1 = (int)((int64_t)(part + 1) * steps / parts);
   const uint16_t* A = p.a + (int64_t)r.a * p.R * p.K;
-  const int rstart = p.planned ? by % kSub * 16 * MT : 0;
-  const int rend = p.planned && rstart + 16 * MT < r.n ? rstart + 16 * MT : r.n;
-  for (int r0 = rstart; r0 < rend; r0 += 16 * MT) {
+  const int rstart = p.planned ? by % kSub * 16 * MT : r.first;
+  const int rend = p.planned && rstart + 16 * MT < r.n ? rstart + 16 * MT : r.end;
+  for (int r0 = rstart; r0 < rend; r0 += 16 * MT * p.deal) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) lora_list(p, r, r0 + 16 * t, list + 16 * t);
     __syncthreads();
@@ -303,8 +316,9 @@ __device__ __forceinline__ u32x4 lora_b_mask(u32x4 w, const LoraArgs& p, int64_t
   return w;
 }
 
-// 4 NQ consecutive outputs of row m from column n: y = base + f acc.  vec:
-// base and y allow 16-byte (NQ = 1 and 16-bit outputs: 8-byte) accesses.
+// 4 NQ consecutive outputs of row m from column n: y = base + f acc.  Accesses
+// of 16 bytes (NQ = 1 and 16-bit outputs: 8) wherever the rows start: 3358 rows
+// of 3785 columns took 75 us one column at a time.
 template <int YDT, int NQ>
 struct LoraOut {
   static constexpr int NW = YDT == DT_F32 ? 4 * NQ : 2 * NQ;   // 32-bit words
@@ -315,10 +329,10 @@ struct LoraOut {
     if (!p.base) return;
     if constexpr (YDT == DT_F32) {
       const uint32_t* b = reinterpret_cast<const uint32_t*>(p.base) + m * p.ldb + n;
-      if (p.vec && n + 4 * NQ <= p.N) {
+      if (n + 4 * NQ <= p.N) {
 #pragma unroll
         for (int i = 0; i < NW; i += 4) {
-          const u32x4 t = ldg128(b + i);
+          const u32x4 t = *reinterpret_cast<const u32x4a4*>(b + i);
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[i + j] = t[j];
         }
@@ -329,15 +343,15 @@ struct LoraOut {
       }
     } else {
       const uint16_t* b = reinterpret_cast<const uint16_t*>(p.base) + m * p.ldb + n;
-      if (p.vec && n + 4 * NQ <= p.N) {
+      if (n + 4 * NQ <= p.N) {
         if constexpr (NQ == 1) {
-          const uint2 t = *reinterpret_cast<const uint2*>(b);
-          w[0] = t.x;
-          w[1] = t.y;
+          const u32x2a2 t = *reinterpret_cast<const u32x2a2*>(b);
+          w[0] = t[0];
+          w[1] = t[1];
         } else {
 #pragma unroll
           for (int i = 0; i < NW; i += 4) {
-            const u32x4 t = ldg128(b + 2 * i);
+            const u32x4 t = *reinterpret_cast<const u32x4a2*>(b + 2 * i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[i + j] = t[j];
           }
@@ -365,9 +379,9 @@ struct LoraOut {
     }
     if constexpr (YDT == DT_F32) {
       uint32_t* y = reinterpret_cast<uint32_t*>(p.y) + m * p.ldy + n;
-      if (p.vec && n + 4 * NQ <= p.N) {
+      if (n + 4 * NQ <= p.N) {
 #pragma unroll
-        for (int i = 0; i < NW; i += 4) *reinterpret_cast<u32x4*>(y + i) = u32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+        for (int i = 0; i < NW; i += 4) *reinterpret_cast<u32x4a4*>(y + i) = u32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
       } else {
 #pragma unroll
         for (int i = 0; i < NW; ++i)
@@ -375,12 +389,12 @@ struct LoraOut {
       }
     } else {
       uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + m * p.ldy + n;
-      if (p.vec && n + 4 * NQ <= p.N) {
+      if (n + 4 * NQ <= p.N) {
         if constexpr (NQ == 1) {
-          *reinterpret_cast<uint2*>(y) = make_uint2(o[0], o[1]);
+          *reinterpret_cast<u32x2a2*>(y) = u32x2a2{o[0], o[1]};
         } else {
 #pragma unroll
-          for (int i = 0; i < NW; i += 4) *reinterpret_cast<u32x4*>(y + 2 * i) = u32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+          for (int i = 0; i < NW; i += 4) *reinterpret_cast<u32x4a2*>(y + 2 * i) = u32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
         }
       } else {
 #pragma unroll
@@ -411,12 +425,13 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
-  const int bx = (int)(blockIdx.x % (unsigned)p.nx), by = (int)(blockIdx.x / (unsigned)p.nx);
+  const int bx = (int)(blockIdx.x % (unsigned)p.nx), byd = (int)(blockIdx.x / (unsigned)p.nx);
+  const int by = byd / p.deal, dealt = byd % p.deal;
   int known;
   LoraAdapter ad{0, 0.0f};
   const bool early = lora_known(p, by, known);
   if (early) ad = lora_adapter(p, known);
-  const LoraRows r = lora_rows(p, by, count);
+  const LoraRows r = lora_rows(p, by, dealt, count);
   if (r.n == 0) return;
   if (!early) ad = lora_adapter(p, r.a);
   const int rank = ad.rank;
@@ -433,12 +448,12 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) w[s][q] = lora_b(p, B, bcol(q), s * 32 + 8 * b, rank);
   }
-  for (int r0 = 0; r0 < r.n; r0 += PR) {
+  for (int r0 = r.first; r0 < r.end; r0 += PR * p.deal) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PR; i += 16) lora_list(p, r, r0 + i, list + i);
     __syncthreads();
-    const int nr = r.n - r0 < PR ? r.n - r0 : PR;
+    const int nr = r.end - r0 < PR ? r.end - r0 : PR;
     if (rank > 0) {
       // 16 threads per row; the K parts, four at a time, are added in their order
       const int64_t pitch = (int64_t)p.M * p.R;
@@ -467,7 +482,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
       }
     }
     __syncthreads();
-    if (r0 == 0 && rank > 0) {
+    if (r0 == r.first && rank > 0) {
 #pragma unroll
       for (int s = 0; s < RK; ++s)
 #pragma unroll
@@ -521,12 +536,13 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rl = lane & 15, b = lane >> 4;
-  const int bx = (int)(blockIdx.x % (unsigned)p.nx), by = (int)(blockIdx.x / (unsigned)p.nx);
+  const int bx = (int)(blockIdx.x % (unsigned)p.nx), byd = (int)(blockIdx.x / (unsigned)p.nx);
+  const int by = byd / p.deal, dealt = byd % p.deal;
   int known;
   LoraAdapter ad{0, 0.0f};
   const bool early = lora_known(p, by, known);
   if (early) ad = lora_adapter(p, known);
-  const LoraRows r = lora_rows(p, by, count);
+  const LoraRows r = lora_rows(p, by, dealt, count);
   if (r.n == 0) return;
   if (!early) ad = lora_adapter(p, r.a);
   const int rank = ad.rank;
@@ -540,11 +556,11 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
 #pragma unroll
     for (int s = 0; s < RK; ++s) w[s] = lora_b(p, B, c0 + rl, s * 32 + 8 * b, rank);
   }
-  for (int r0 = 0; r0 < r.n; r0 += 16) {
+  for (int r0 = r.first; r0 < r.end; r0 += 16 * p.deal) {
     __syncthreads();
     lora_list(p, r, r0, list);
     __syncthreads();
-    const int nr = r.n - r0 < 16 ? r.n - r0 : 16;
+    const int nr = r.end - r0 < 16 ? r.end - r0 : 16;
     LoraOut<YDT, 1> out;
     const int64_t m = list[rl < nr ? rl : 0];
     if (rl < nr) out.load(p, m, c0 + 4 * b);
@@ -579,7 +595,7 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
       }
       __syncthreads();
     }
-    if (r0 == 0 && rank > 0) {
+    if (r0 == r.first && rank > 0) {
 #pragma unroll
       for (int s = 0; s < RK; ++s) w[s] = lora_b_mask(w[s], p, c0 + rl, s * 32 + 8 * b, rank);
     }
@@ -605,6 +621,14 @@ static bool lora_planned(int64_t M) { return M > kLoraScan; }
 // Block rows of the scan: one per row, or one per adapter and one for none.
 static int lora_groups(int64_t M, int64_t n_adapters) { return (int)(M < n_adapters + 1 ? M : n_adapters + 1); }
 
+// Blocks of a block row, which take its rows 16 at a time in turn: twice the
+// even share (calls of 123 rows of one adapter, 1488 -> 3181: 31 us with one
+// block row, 13 us with 8; 289 rows of two, 168 -> 244: 34 us and 13 us).
+static int lora_deal(int64_t M, int64_t n_adapters) {
+  const int64_t deal = (M / (n_adapters + 1) + 7) / 8;
+  return lora_planned(M) || deal < 1 ? 1 : (int)deal;
+}
+
 // One launch (k_lora_one) while forming h again in every block costs less than
 // a second launch: A from the caches, at most 256 KB per block and 32 MB in all.
 static bool lora_one(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R) {
@@ -613,7 +637,8 @@ static bool lora_one(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_
 }
 
 static int lora_ksplit(int64_t M, int64_t K, int64_t n_adapters) {
-  const int64_t blocks = lora_planned(M) ? (M + kLoraTile - 1) / kLoraTile : lora_groups(M, n_adapters);
+  const int64_t blocks =
+      lora_planned(M) ? (M + kLoraTile - 1) / kLoraTile : lora_groups(M, n_adapters) * lora_deal(M, n_adapters);
   const int64_t steps = (K + 63) / 64;
   int64_t want = 256 / blocks;                     // about a block per compute unit
   if (want > steps / kShrinkWaves) want = steps / kShrinkWaves;   // a step per wave at least
@@ -652,9 +677,8 @@ hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st) {
   p.planned = lora_planned(c.M);
   p.h = reinterpret_cast<float*>(ws);
   p.by_row = c.M < c.n_adapters + 1;
-  const uintptr_t es = c.ydt == DT_F32 ? 4 : 2, q = 16 / es;
-  p.vec = c.ldy % q == 0 && (uintptr_t)c.y % 16 == 0 && (!c.base || (c.ldb % q == 0 && (uintptr_t)c.base % 16 == 0));
-  unsigned gy = (unsigned)lora_groups(c.M, c.n_adapters);
+  p.deal = lora_deal(c.M, c.n_adapters);
+  unsigned gy = (unsigned)(lora_groups(c.M, c.n_adapters) * p.deal);
   const bool one = lora_one(c.M, c.N, c.K, c.n_adapters, c.R);
   const int64_t cols = one ? kLoraOneCols : 4 * kLoraCols;
   p.nx = (int)((c.N + cols - 1) / cols);
