@@ -44,7 +44,7 @@ def route_experts(logits, top_k, bias=None, sigmoid=False, n_group=1, topk_group
 
 
 def expert_rows(x, expert, words, step, zero):
-    """z[i] = W_{expert[i]} x[i] and, beside it, sum_k step (q + z) |x| (the size
+    """z[i] = W_{expert[i]} x[i] and, beside it, sum_k |step| (q + z) |x| (the size
     of what a kernel adds up); rows whose expert is outside the stack are 0.
     words [E, N, K/8], step and zero [E, N, G]."""
     E, N, G = step.shape
@@ -61,7 +61,7 @@ def expert_rows(x, expert, words, step, zero):
         d = np.repeat(step[e].astype(np.float64), g, axis=1)
         z = np.repeat(zero[e].astype(np.float64), g, axis=1)
         out[rows] = x[rows] @ (d * (q - z)).T
-        size[rows] = np.abs(x[rows]) @ (d * (q + z)).T
+        size[rows] = np.abs(x[rows]) @ (np.abs(d) * (q + z)).T
     return out, size
 
 

@@ -333,6 +333,80 @@ def test_experts_dealt_rows_and_tall_tiles(on_gpu, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    # one token; few rows; tiles of 32, 64 and 128 rows
+    (1, 16, 2, 512, 96, 128, "bf16", "f32", ""),
+    (20, 6, 2, 512, 96, 64, "f16", "f32", "holes"),
+    (1500, 3, 3, 384, 96, 128, "f16", "f32", "holes"),
+    (1100, 3, 2, 128, 4000, 64, "bf16", "f32", "holes"),
+    (6500, 5, 2, 128, 4096, 128, "f16", "f32", "holes"),
+], ids=lambda c: "x".join(str(v) for v in c))
+def test_experts_steps_of_any_sign(on_gpu, case):
+    """Steps of zero (some groups, whole rows), below zero, the smallest and far
+    apart, and one that is not a number; activations that are not finite stay
+    in their rows."""
+    T, n_exp, k, K, N, g, xdt, ydt, kind = case
+    q, step, zero = stack(n_exp, N, K, g, T + K)
+    rng = np.random.default_rng(K)
+    step[:, 0::8] *= rng.choice([-1, 1], step[:, 0::8].shape).astype(np.float16)
+    step[:, 1::8] *= rng.integers(0, 2, step[:, 1::8].shape).astype(np.float16)
+    step[:, 2::8] = 0
+    step[:, 3::8] = 2.0 ** -24
+    step[:, 4::8, ::2] = 2.0 ** -24
+    step[:, 5::8, -1] = 0
+    w = (q, step, zero)
+    x = acts(T, K, DTYPES[xdt], N)
+    ids = choices(T, n_exp, k, T * N, kind)
+    p = packed(w)
+    gi = gpu(torch.from_numpy(ids))
+    y = awq.awq_w4a16_experts_up(gpu(x), gi, *p, out_dtype=DTYPES[ydt], group_size=g)
+    check_up(x, ids, w, g, "none", DTYPES[ydt], y, case)
+    h = acts(T * k, K, DTYPES[xdt], N)
+    weights = rng.uniform(-0.2, 1.0, (T, k)).astype(np.float32)
+    gw = gpu(torch.from_numpy(weights))
+    d = awq.awq_w4a16_experts_down(gpu(h), gi, gw, *p, out_dtype=DTYPES[ydt], group_size=g)
+    check_down(h, ids, weights, w, g, DTYPES[ydt], d, case)
+    # one step that is not a number: its column, of its expert's slots
+    p[1][n_exp - 1, 7, 0] = math.nan
+    ok = (ids.reshape(-1) >= 0) & (ids.reshape(-1) < n_exp)
+    hit = torch.from_numpy(ids.reshape(-1) == n_exp - 1)
+    want = torch.zeros((T * k, N), dtype=torch.bool)
+    want[hit, 7] = True
+    got = awq.awq_w4a16_experts_up(gpu(x), gi, *p, out_dtype=DTYPES[ydt], group_size=g)
+    assert torch.equal(got.view(T * k, N).isnan().cpu(), want)
+    assert torch.equal(got.view(T * k, N).cpu()[~want], y.view(T * k, N).cpu()[~want])
+    got = awq.awq_w4a16_experts_down(gpu(h), gi, gw, *p, out_dtype=DTYPES[ydt], group_size=g)
+    assert torch.equal(got.isnan().cpu(), want.view(T, k, N).any(1))
+    # rows that are not finite (no step of zero: 0 inf is not a number)
+    p[1].copy_(gpu(torch.from_numpy(np.where(step == 0, np.float16(1e-3), step))))
+    y = awq.awq_w4a16_experts_up(gpu(x), gi, *p, out_dtype=DTYPES[ydt], group_size=g).view(T, k, N)
+    x[T // 3, 5], x[T // 2, 6] = math.inf, math.nan
+    got = awq.awq_w4a16_experts_up(gpu(x), gi, *p, out_dtype=DTYPES[ydt], group_size=g).view(T, k, N)
+    rows = torch.zeros(T, dtype=torch.bool)
+    rows[[T // 3, T // 2]] = True
+    assert torch.equal(got[gpu(~rows)], y[gpu(~rows)])
+    assert not got[gpu(rows)].isfinite()[torch.from_numpy(ok).view(T, k)[rows].cuda()].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 8, 600])
+def test_experts_infinite_step_stays_in_its_column(on_gpu, T):
+    n_exp, k, K, N, g = 4, 2, 256, 1100, 128
+    w = stack(n_exp, N, K, g, T)
+    x = acts(T * k, K, torch.bfloat16, 2) * 8        # products past 4
+    ids = choices(T, n_exp, k, 1, "")
+    weights = np.random.default_rng(T).uniform(0.5, 1.0, (T, k)).astype(np.float32)
+    p = packed(w)
+    p[1][:, 7] = math.inf
+    y = awq.awq_w4a16_experts_down(gpu(x), gpu(torch.from_numpy(ids)), gpu(torch.from_numpy(weights)), *p,
+                                   out_dtype=torch.bfloat16, group_size=g).cpu()
+    assert not y[:, 7].isfinite().any()
+    w[1][:, 7] = 0
+    y[:, 7] = 0
+    check_down(x, ids, weights, w, g, torch.bfloat16, y, T)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [2, 90, 400])
 def test_experts_strides_and_neighbours(on_gpu, T):
     """Padded input and output rows: what lies beside the output stays."""

@@ -285,6 +285,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   };
   u32x4 aE[HB], aO[HB], bq[4];
   float ratio[4], last[4] = {1.0f, 1.0f, 1.0f, 1.0f};   // D of the last unit / this unit's; the last unit's
+  float any[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // the largest |D|: 0 and the column is 0
   auto nz = [&](int n) { return (cz[n] >> 16) * 0x10001u; };
 #pragma unroll
   for (int q = 0; q < 4; ++q) copy(0, 0, q);
@@ -314,7 +315,11 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
       if (i == 0) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const float d = fmaxf(f16_to_f32(cz[n] & 0xFFFFu), 0x1p-40f);   // a step of 0 keeps the ratios finite
+          // a step of 0 counts as 2^-60, which keeps the ratios finite and is
+          // below the fp32 rounding of any other (2^-24 at least)
+          const float f = f16_to_f32(cz[n] & 0xFFFFu);
+          const float d = fabsf(f) < 0x1p-60f ? 0x1p-60f : f;
+          any[n] = fmaxf(any[n], fabsf(f));
           ratio[n] = last[n] * __builtin_amdgcn_rcpf(d);
           last[n] = d;
         }
@@ -356,6 +361,9 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   // wave's LDS area and out in whole row pieces.  Result lane: column l % 16,
   // rows 4 b + v.
   __syncthreads();                                 // every wave is done with the stages
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+    if (any[n] == 0.0f) last[n] *= 0.0f;
   constexpr int kW = MODE == EXPERTS_SWIGLU ? 32 : 64;                    // outputs per row of the wave
   float* stg = reinterpret_cast<float*>(lds) + wv * 16 * (kW + 4);
 #pragma unroll
@@ -405,6 +413,11 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
           float am = 0.0f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) am = fmaxf(am, fmaxf(fabsf(o0[j]), fabsf(o1[j])));
+          if (am == __builtin_inff()) {            // of those that are finite, whatever an infinite step made of its column
+            am = 0.0f;
+            for (int j = 0; j < 4; ++j)
+              am = fmaxf(am, fmaxf(fabsf(o0[j]) < __builtin_inff() ? fabsf(o0[j]) : 0.0f, fabsf(o1[j]) < __builtin_inff() ? fabsf(o1[j]) : 0.0f));
+          }
           am = fmaxf(am, quad_xor1(am));
           am = fmaxf(am, quad_xor2(am));
           am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
