@@ -449,8 +449,8 @@ awq_status awq_route_experts(const void* logits, awq_dtype ldt, int64_t T, int64
  *   y         up: [M top_k][ldy], down: [M][ldy], F16, BF16 or F32 (ydt)
  *   ws        >= awq_workspace_bytes(AWQ_OP_EXPERTS_UP or _DOWN, M, N, K, E, top_k)
  * M == 0 or N == 0 is a no-op.  More than 2^24 slots, 2^31 or more bytes in
- * one expert's packed words or in the activations as packed fp16 rows ->
- * AWQ_ERR_UNSUPPORTED.
+ * one expert's packed words or in the activations as packed fp16 rows, or
+ * products for 2^32 threads (some 2^37 values) -> AWQ_ERR_UNSUPPORTED.
  */
 awq_status awq_w4a16_experts_up(const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
                                 const int32_t* ids, int top_k, const int32_t* qweight,
@@ -483,7 +483,8 @@ awq_status awq_w4a16_experts_down(const void* x, awq_dtype xdt, int64_t M, int64
  *   base     [M][ldb] of ydt or NULL;  y [M][ldy] F16, BF16 or F32 (ydt)
  *   ws       >= awq_workspace_bytes(AWQ_OP_LORA, M, N, K, n_adapters, R)
  * M == 0 or N == 0 is a no-op; with n_adapters == 0 every row is base.
- * More than 2^24 rows or 16384 adapters -> AWQ_ERR_UNSUPPORTED.
+ * More than 2^24 rows, 8192 adapters, or outputs for 2^32 threads (some 2^37
+ * values) -> AWQ_ERR_UNSUPPORTED.
  */
 #define AWQ_MAX_RANK 256
 awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,

@@ -325,6 +325,11 @@ def test_experts_down(on_gpu, case):
     # tiles of 64 rows and of 128 rows
     (1100, 3, 2, 64, 4000, 64, "bf16", "f32", "holes"),
     (6500, 5, 2, 64, 4098, 64, "f16", "bf16", "holes"),
+    # as many experts as there may be: few rows, and sorted in chunks for tiles
+    (800, 1024, 3, 64, 18, 64, "f16", "f32", "holes"),
+    (400, 1024, 20, 64, 18, 64, "bf16", "f32", "holes"),
+    # more experts than slots, all on one
+    (150, 300, 1, 192, 34, 64, "f16", "f32", "one"),
 ], ids=lambda c: "x".join(str(v) for v in c))
 def test_experts_dealt_rows_and_tall_tiles(on_gpu, case):
     test_experts_up(on_gpu, case, "none")
@@ -569,6 +574,34 @@ def test_lora(on_gpu, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M", [40, 600, 5000])
+def test_lora_as_many_adapters_as_there_may_be(on_gpu, M):
+    test_lora(on_gpu, (M, 8192, 8, 16, 24, "f16", "f32", True, True, True, "mixed"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [40, 200, 500])
+@pytest.mark.parametrize("L", [1, 3, 600])
+@pytest.mark.parametrize("one", [True, False])
+def test_lora_all_rows_one_adapter(on_gpu, M, L, one):
+    """Rows dealt to blocks (few adapters), or 16 from every 16th row's block
+    (more adapters than rows), in one launch or two."""
+    K, R, N = (256, 16, 70) if one else (2304, 72, 70)
+    rng = np.random.default_rng(M + L)
+    x = acts(M, K, torch.float16, M)
+    a = torch.from_numpy(rng.normal(0, 1 / math.sqrt(K), (L, R, K))).to(torch.float16)
+    b = torch.from_numpy(rng.normal(0, 1, (L, N, R))).to(torch.float16)
+    adapter = np.full(M, L - 1, np.int32)
+    adapter[M // 2:M // 2 + 3] = -1
+    base = torch.from_numpy(rng.normal(0, 1, (M, N))).float()
+    y = awq.awq_lora_add(gpu(x), gpu(torch.from_numpy(adapter)), gpu(a), gpu(b), base=gpu(base))
+    check_lora(x, adapter, a, b, None, None, base, torch.float32, y, (M, L, one))
+    adapter[:] = -1                                  # nobody's rows are dealt too
+    y = awq.awq_lora_add(gpu(x), gpu(torch.from_numpy(adapter)), gpu(a), gpu(b), base=gpu(base))
+    assert torch.equal(y.cpu(), base)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 20, 640])
 def test_lora_strides_and_neighbours(on_gpu, M):
     L, R, K, N = 3, 16, 128, 50
@@ -808,6 +841,7 @@ def test_experts_refusals(down):
     assert call(M=1 << 24) == 5                      # more than 2^24 slots
     assert call(N=1 << 24, ldy=1 << 24) == 5         # 2^31 bytes of words per expert
     assert call(M=1 << 22, K=4096, ld=4096, k=1) == 5  # activations past 32-bit offsets
+    assert call(M=1 << 23, K=64, ld=64, g=64, N=1 << 16, ldy=1 << 16) == 5   # more threads than a launch has
     op = awq.AWQ_OP_EXPERTS_DOWN if down else awq.AWQ_OP_EXPERTS_UP
     need = awq.awq_workspace_bytes(op, 4000, 64, 256, 8, 2)
     assert need > 0
@@ -840,7 +874,8 @@ def test_lora_refusals():
     for kw in (dict(K=252, ld=256), dict(R=12), dict(ld=260), dict(x=BAD), dict(a=BAD), dict(b=BAD), dict(ad=BAD),
                dict(ranks=BAD), dict(sc=BAD), dict(base=BAD, ldb=64), dict(y=BAD), dict(ydt=0, y=ODD)):
         assert call(**kw) == 4, kw
-    assert call(R=264) == 5 and call(L=16385) == 5 and call(M=(1 << 24) + 1) == 5 and call(K=1 << 18, ld=1 << 18) == 5
+    assert call(R=264) == 5 and call(L=8193) == 5 and call(L=16385) == 5 and call(M=(1 << 24) + 1) == 5 and call(K=1 << 18, ld=1 << 18) == 5
+    assert call(M=1 << 24, N=1 << 16, ldy=1 << 16) == 5  # more threads than a launch has
     big = dict(M=300, N=4096, ldy=4096, K=4096, ld=4096, L=30, R=64)
     need = awq.awq_workspace_bytes(awq.AWQ_OP_LORA, 300, 4096, 4096, 30, 64)
     assert need >= 300 * 64 * 4

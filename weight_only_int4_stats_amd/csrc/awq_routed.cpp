@@ -16,8 +16,8 @@ bool group_ok(int g) { return g == 64 || g == 128 || g == 256; }
 awq_status from_hip(hipError_t e) { return e == hipSuccess ? AWQ_OK : AWQ_ERR_HIP; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 24;       // slots, or rows with adapters
-constexpr int64_t kMaxAdapters = 16384;
-constexpr int64_t kMaxBlocks = 0x7FFFFFFF;
+constexpr int64_t kMaxAdapters = 8192;               // the sort's three tables in LDS: 96 KB
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;          // of a launch
 
 awq_status experts(int mode, const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx, const int32_t* ids,
                    const float* weights, int top_k, const int32_t* qweight, const uint16_t* scales,
@@ -34,8 +34,8 @@ awq_status experts(int mode, const void* x, awq_dtype xdt, int64_t M, int64_t K,
   if (!x || !ids || !qweight || !scales || !zeros || !y || (down && !weights)) return AWQ_ERR_NULL;
   if (M > kMaxRows / top_k || N > ((int64_t)1 << 32) / K - 1) return AWQ_ERR_UNSUPPORTED;
   if ((down ? M * top_k : M) * K * 2 >= (int64_t)1 << 31) return AWQ_ERR_UNSUPPORTED;
-  // block count of the tiled product (at least 32 rows x 64 columns each)
-  if ((M * top_k / 32 + E + 2) * (N / 64 + 1) > kMaxBlocks) return AWQ_ERR_UNSUPPORTED;
+  // the tiled product: 256 threads per 32 rows or more x 256 weight rows
+  if ((M * top_k / 32 + E + 2) * (N / 256 + 1) > kMaxThreads / 256) return AWQ_ERR_UNSUPPORTED;
   if (ldx % 8 != 0 || !aligned(x, 16) || !aligned(qweight, 16) || !aligned(scales, 2) || !aligned(ids, 4) ||
       !aligned(y, bytes_of(ydt)) || (down && !aligned(weights, 4)))
     return AWQ_ERR_ALIGN;
@@ -59,7 +59,7 @@ awq_status awq_route_experts(const void* logits, awq_dtype ldt, int64_t T, int64
   if (T < 0 || E < 1 || ldl < E || n_group < 1 || E % n_group != 0 || topk_group < 1 || topk_group > n_group ||
       group_top < 1 || group_top > 2 || top_k < 1 || top_k > E / n_group * topk_group)
     return AWQ_ERR_SHAPE;
-  if (E > AWQ_MAX_EXPERTS || n_group > 64 || top_k > AWQ_MAX_TOP_K || T > 0x7FFFFFFF) return AWQ_ERR_UNSUPPORTED;
+  if (E > AWQ_MAX_EXPERTS || n_group > 64 || top_k > AWQ_MAX_TOP_K || T > kMaxThreads / 64 - 3) return AWQ_ERR_UNSUPPORTED;
   if (T == 0) return AWQ_OK;
   if (!logits || !ids || !weights) return AWQ_ERR_NULL;
   if (!aligned(logits, bytes_of(ldt)) || !aligned(ids, 4) || !aligned(weights, 4) || (bias && !aligned(bias, 4)))
@@ -103,8 +103,9 @@ awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int6
       !aligned(adapter, 4) || (ranks && !aligned(ranks, 4)) || (scaling && !aligned(scaling, 4)) ||
       (base && !aligned(base, bytes_of(ydt))) || !aligned(y, bytes_of(ydt)))
     return AWQ_ERR_ALIGN;
-  // block counts of the launches (256 columns, or a K split, per row group)
-  if ((M / 16 + n_adapters + 1) * ((N + 255) / 256 + 32) > kMaxBlocks) return AWQ_ERR_UNSUPPORTED;
+  // the expand: 256 threads per 64 rows of one adapter (or up to 512 rows: 16) x 256 columns
+  const int64_t groups = (M <= 512 ? M / 16 : M / 64) + (M < n_adapters + 1 ? M : n_adapters + 1);
+  if (groups * (N / 256 + 1) > kMaxThreads / 256) return AWQ_ERR_UNSUPPORTED;
   const size_t need = awq::lora_ws_bytes(M, N, K, n_adapters, R);
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return AWQ_ERR_WORKSPACE;
   const awq::LoraCall c{(const uint16_t*)x, (int)xdt, M, K, ldx, adapter, (const uint16_t*)a, (const uint16_t*)b,
