@@ -412,6 +412,31 @@ def test_experts_infinite_step_stays_in_its_column(on_gpu, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 25, 1200])
+def test_experts_of_part_of_a_stack(on_gpu, T):
+    """Experts 1, 2, ... of a larger stack, whose steps and zero points start
+    off 16 bytes, in inputs that are parts of larger ones; rows of tokens that
+    have no expert may hold anything."""
+    n_exp, k, K, N, g = 9, 2, 192, 35, 64
+    w = stack(n_exp, N, K, g, T)
+    p = tuple(t[1:] for t in packed(w))
+    part = tuple(t[1:] for t in w)
+    assert T > 1 or p[2].data_ptr() % 8
+    ids = choices(T, n_exp - 1, k, 3, "holes")
+    x = acts(T, K, torch.float16, 4)
+    lost = ((ids < 0) | (ids >= n_exp - 1)).all(1)
+    x[torch.from_numpy(lost)] = math.nan
+    gi = gpu(torch.from_numpy(np.concatenate([ids[:1], ids])))[1:]
+    y = awq.awq_w4a16_experts_up(gpu(x), gi, *p, out_dtype=torch.float32, group_size=g)
+    x[torch.from_numpy(lost)] = 0
+    check_up(x, ids, part, g, "none", torch.float32, y, T)
+    h = acts(T * k, K, torch.bfloat16, 4)
+    weights = np.random.default_rng(T).uniform(0, 1, (T, k)).astype(np.float32)
+    d = awq.awq_w4a16_experts_down(gpu(h), gi, gpu(torch.from_numpy(weights)), *p, out_dtype=torch.bfloat16, group_size=g)
+    check_down(h, ids, weights, part, g, torch.bfloat16, d, T)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [2, 90, 400])
 def test_experts_strides_and_neighbours(on_gpu, T):
     """Padded input and output rows: what lies beside the output stays."""
