@@ -405,7 +405,7 @@ awq_status awq_fold_scales(void* v, awq_dtype dt, int64_t rows, int64_t cols, in
  *
  *   logits   [T][ldl] fp16, bf16 or f32 (ldt), aligned to its element
  *   E        1 .. AWQ_MAX_EXPERTS
- *   bias     [E] float, finite, or NULL
+ *   bias     [E] float, finite or -inf (that expert is not usable), or NULL
  *   n_group  >= 1, divides E;  topk_group 1 .. n_group;  group_top 1 or 2
  *   top_k    1 .. min(E / n_group * topk_group, AWQ_MAX_TOP_K)
  *   ids      [T][top_k] int32;  weights [T][top_k] float

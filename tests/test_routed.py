@@ -171,6 +171,24 @@ def test_route_close_choices_under_a_bias(on_gpu, sig, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 1), (4, 2, 2), (12, 5, 2)])
+def test_route_bias_switches_experts_off(on_gpu, sig, groups):
+    """A bias of -inf: never chosen, in a group worth less for it, whole groups off."""
+    n_group, topk_group, group_top = groups
+    x = route_case(40, 48, torch.float32, 8)
+    bias = np.random.default_rng(3).normal(0, 0.05, 48).astype(np.float32)
+    bias[::3] = -np.inf
+    bias[13:36] = -np.inf
+    for b in (bias, np.full(48, -np.inf, np.float32)):
+        got = awq.awq_route_experts(gpu(x), 8, bias=gpu(torch.from_numpy(b)), score="sigmoid" if sig else "softmax",
+                                    n_group=n_group, topk_group=topk_group, group_top=group_top)
+        ref = O.route_experts(f32(x), 8, b, sig, n_group, topk_group, group_top)
+        assert not np.isin(ref[0], np.nonzero(~np.isfinite(b))[0]).any()
+        compare_route(got, ref, groups)
+
+
+@pytest.mark.gpu
 def test_route_strided_rows_and_given_outputs(on_gpu):
     big = route_case(40, 100, torch.bfloat16, 9)
     x = gpu(big)[:, 10:74]
