@@ -272,18 +272,20 @@ _SCORES = {"softmax": AWQ_SCORE_SOFTMAX, "sigmoid": AWQ_SCORE_SIGMOID}
 _ACTS = {"none": AWQ_ACT_NONE, "swiglu": AWQ_ACT_SWIGLU}
 
 
-def _same(t: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dtype, shape: tuple) -> int | None:
-    """Address of a contiguous tensor of this type, shape and device (None for None)."""
+def _same(t: torch.Tensor | None, name: str, dev: int, dtype: torch.dtype, shape: tuple) -> int | None:
+    """Address of a contiguous tensor of this type, shape and GPU (None for None)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {dev}")
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
 def _act_rows(x: torch.Tensor, name: str) -> tuple[int, int, int]:
     """rows, columns and row stride of a 2-D tensor; a single row's stride is its length."""
-    _dev(x, name)
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        _dev(x, name)
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D with unit column stride")
     rows, cols = x.shape
@@ -295,25 +297,30 @@ def _act_rows(x: torch.Tensor, name: str) -> tuple[int, int, int]:
     return rows, cols, ld if rows > 1 else cols
 
 
+def _new(rows: int, cols: int, dtype: torch.dtype, dev: torch.device) -> torch.Tensor:
+    """An output (the strided form is 0.4 us a tensor cheaper on the host than empty)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
+
+
 def _out(y: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dtype | None, rows: int,
          cols: int) -> tuple[torch.Tensor, int]:
     """The output (a new one of dtype if y is None) and its row stride."""
     if y is None:
-        return torch.empty((rows, cols), dtype=dtype, device=dev), cols
+        return _new(rows, cols, dtype, dev), cols
     r, c, ld = _act_rows(y, name)
     if (r, c) != (rows, cols) or y.device != dev or (dtype is not None and y.dtype is not dtype):
         raise ValueError(f"{name} must be a {dtype or y.dtype} tensor of shape [{rows}, {cols}] on {dev}")
     return y, ld
 
 
-def _launch(name: str, device: torch.device, args: tuple) -> None:
-    """Calls the entry point on the tensors' device and its current stream."""
+def _launch(name: str, dev: int, args: tuple) -> None:
+    """Calls the entry point on the tensors' GPU and its current stream."""
     fn = getattr(lib(), name)
-    if device.index == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _abi.check(name, st)
 
@@ -365,16 +372,19 @@ def awq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | Non
     T, E, ldl = _act_rows(logits, "logits")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
-    dev = logits.device
+    device, dev = logits.device, logits.get_device()
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        ids = _new(T, top_k, torch.int32, device)
+    else:
+        _same(ids, "ids", dev, torch.int32, (T, top_k))
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        weights = _new(T, top_k, torch.float32, device)
+    else:
+        _same(weights, "weights", dev, torch.float32, (T, top_k))
     _launch("awq_route_experts", dev,
             (logits.data_ptr(), _DT.get(logits.dtype, -1), T, E, ldl,
              _same(bias, "bias", dev, torch.float32, (E,)), _SCORES[score], n_group, topk_group, group_top, top_k,
-             int(bool(renormalize)), scale, _same(ids, "ids", dev, torch.int32, (T, top_k)),
-             _same(weights, "weights", dev, torch.float32, (T, top_k))))
+             int(bool(renormalize)), scale, ids.data_ptr(), weights.data_ptr()))
     return ids, weights
 
 
@@ -383,25 +393,26 @@ def _experts(name, op, x, ids, weights, qweight, scales, zeros, act, out_dtype, 
         with _on_stream(stream, x):
             return _experts(name, op, x, ids, weights, qweight, scales, zeros, act, out_dtype, y, group_size, ws, None)
     rows, K, ldx = _act_rows(x, "x")
-    dev = x.device
+    device, dev = x.device, x.get_device()
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, top_k]")
     M, top_k = ids.shape
     if rows != (M if weights is None else M * top_k):
         raise ValueError("x must have one row per token (up) or per slot (down)")
-    if qweight.dim() != 3 or qweight.shape[2] * 8 != K:
+    packed = qweight.shape
+    if len(packed) != 3 or packed[2] * 8 != K:
         raise ValueError("qweight must be [experts, N, K/8]")
     if group_size not in (64, 128, 256):
         raise ValueError("group_size must be 64, 128 or 256")
-    E, N = qweight.shape[:2]
-    G = K // group_size
+    E, N, _ = packed
+    groups = (E, N, K // group_size)
     swiglu = act == AWQ_ACT_SWIGLU
     out_rows, cols = (M * top_k, N // 2 if swiglu else N) if weights is None else (M, N)
-    y, ldy = _out(y, "y", dev, out_dtype if y is not None else out_dtype or x.dtype, out_rows, cols)
-    ws, wsp, wsb = _ws(op, dev, ws, M, N, K, E, top_k)
+    y, ldy = _out(y, "y", device, out_dtype if y is not None else out_dtype or x.dtype, out_rows, cols)
+    ws, wsp, wsb = _ws(op, device, ws, M, N, K, E, top_k)
     head = (x.data_ptr(), _DT.get(x.dtype, -1), M, K, ldx, _same(ids, "ids", dev, torch.int32, (M, top_k)))
-    packed = (_same(qweight, "qweight", dev, torch.int32, (E, N, K // 8)),
-              _same(scales, "scales", dev, torch.float16, (E, N, G)), _same(zeros, "zeros", dev, torch.uint8, (E, N, G)))
+    packed = (_same(qweight, "qweight", dev, torch.int32, packed), _same(scales, "scales", dev, torch.float16, groups),
+              _same(zeros, "zeros", dev, torch.uint8, groups))
     tail = (y.data_ptr(), _DT.get(y.dtype, -1), ldy, wsp, wsb)
     if weights is None:
         args = head + (top_k,) + packed + (E, N, group_size, act) + tail
@@ -451,18 +462,18 @@ def awq_lora_add(x: torch.Tensor, adapter: torch.Tensor, a: torch.Tensor, b: tor
         with _on_stream(stream, x):
             return awq_lora_add(x, adapter, a, b, base, scaling, ranks, out_dtype, y, ws)
     M, K, ldx = _act_rows(x, "x")
-    dev = x.device
+    device, dev = x.device, x.get_device()
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a must be [adapters, R, K] and b [adapters, N, R]")
     L, R = a.shape[:2]
     N = b.shape[1]
     want = out_dtype or (base.dtype if base is not None else x.dtype if y is None else y.dtype)
-    y, ldy = _out(y, "y", dev, want, M, N)
+    y, ldy = _out(y, "y", device, want, M, N)
     ldb, basep = 0, None
     if base is not None:
-        base, ldb = _out(base, "base", dev, y.dtype, M, N)
+        base, ldb = _out(base, "base", device, y.dtype, M, N)
         basep = base.data_ptr()
-    ws, wsp, wsb = _ws(_abi.AWQ_OP_LORA, dev, ws, M, N, K, L, R)
+    ws, wsp, wsb = _ws(AWQ_OP_LORA, device, ws, M, N, K, L, R)
     _launch("awq_lora_add", dev,
             (x.data_ptr(), _DT.get(x.dtype, -1), M, K, ldx, _same(adapter, "adapter", dev, torch.int32, (M,)),
              _same(a, "a", dev, x.dtype, (L, R, K)), _same(b, "b", dev, x.dtype, (L, N, R)), L, R,
