@@ -549,10 +549,12 @@ def test_moe_layer(on_gpu, T):
 def check_lora(x, adapter, a, b, ranks, scaling, base, out, y, what):
     ref, size_h, size_x = O.lora(f32(x), adapter, f32(a), f32(b), ranks, scaling)
     # the first sum has K terms (and the parts' additions), the second 2 R; the
-    # intermediate enters as two 16-bit values: 2^-17 of it for bf16 (two
-    # roundings of 2^-9, the second of what the first left), less for fp16
+    # intermediate enters as two 16-bit values: 2^-17 of it for bf16 (half a
+    # step each, the second of what the first left), 2^-23 for fp16; with an
+    # fp32 output as three in bf16
     slack = size_x * (x.shape[1] + 160) * 2.0 ** -23
-    slack += (size_h + slack) * (2.0 ** -17 + (2 * a.shape[1] + 8) * 2.0 ** -23)
+    kept = 2.0 ** -23 if out == torch.float32 else 2.0 ** -17
+    slack += (size_h + slack) * (kept + (3 * a.shape[1] + 8) * 2.0 ** -23)
     if base is not None:
         ref = ref + f32(base).astype(np.float64)
         slack = slack + 2.0 ** -23 * (np.abs(ref) + slack)

@@ -282,11 +282,16 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void k_lora_shrink(const LoraArg
   }
 }
 
-// One row of h as the sum of two 16-bit values, scaled by a power of two: 16
+// One row of h as the sum of NP 16-bit values, scaled by a power of two: 16
 // threads per row, thread j of them holding ranks j, j + 16, ... in v (zeros
-// past the rank).  Writes ranks 0 .. pad - 1 and scaling / the power of two.
-template <int DT, int NI>
-__device__ __forceinline__ void lora_split_row(int j, int pad, float sc, uint16_t* hi, uint16_t* lo, float* back, const float (&v)[NI]) {
+// past the rank).  Writes ranks 0 .. pad - 1 of each part (stride apart) and
+// scaling / the power of two.  Two parts hold h to 2^-17 (bf16) or 2^-23 (fp16)
+// of itself, below the rounding of a 16-bit output; fp32 outputs of bf16
+// inputs take a third (1.4e-6 of an output with two, 1e-7 with three).
+template <int DT, int YDT>
+constexpr int lora_parts() { return DT == DT_BF16 && YDT == DT_F32 ? 3 : 2; }
+template <int DT, int NP, int NI>
+__device__ __forceinline__ void lora_split_row(int j, int pad, float sc, uint16_t* part, int stride, float* back, const float (&v)[NI]) {
   float am = 0.0f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) am = fmaxf(am, fabsf(v[i]));
@@ -299,10 +304,13 @@ __device__ __forceinline__ void lora_split_row(int j, int pad, float sc, uint16_
   for (int i = 0; i < NI; ++i) {
     const int r = i * 16 + j;
     if (r < pad) {
-      const float f = ldexpf(v[i], pe);
-      const uint32_t h = from_f32<DT>(f);
-      hi[r] = (uint16_t)h;
-      lo[r] = (uint16_t)from_f32<DT>(f - to_f32<DT>(h));
+      float f = ldexpf(v[i], pe);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const uint32_t h = from_f32<DT>(f);
+        part[k * stride + r] = (uint16_t)h;
+        f -= to_f32<DT>(h);
+      }
     }
   }
   if (j == 0) *back = ldexpf(sc, -pe);
@@ -421,11 +429,11 @@ constexpr int kLoraCols = 64;                      // columns per wave of the ex
 // for all of the block's rows.  RK: 32-rank steps.
 template <int DT, int YDT, int RK, int PR>
 __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
-  constexpr int kPitch = RK * 32 + 8;
+  constexpr int kPitch = RK * 32 + 8, NP = lora_parts<DT, YDT>();
   constexpr int NQ = YDT == DT_F32 ? 1 : 2, NC = 4 / NQ;   // products per piece, pieces per row
   __shared__ int list[PR];
   __shared__ int count[8];
-  __shared__ __attribute__((aligned(16))) uint16_t hs[2][PR][kPitch];
+  __shared__ __attribute__((aligned(16))) uint16_t hs[NP][PR][kPitch];
   __shared__ float back[PR];                       // scaling / the row's power of two
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -483,7 +491,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
 #pragma unroll
             for (int i = 0; i < RK * 2; ++i) v[i] += g[s][i];
         }
-        lora_split_row<DT, RK * 2>(tid & 15, rk * 32, sc, hs[0][row], hs[1][row], back + row, v);
+        lora_split_row<DT, NP>(tid & 15, rk * 32, sc, hs[0][row], PR * kPitch, back + row, v);
       }
     }
     __syncthreads();
@@ -510,13 +518,13 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
 #pragma unroll
       for (int s = 0; s < RK; ++s) {
         if (s < rk) {
-          const u32x4 hi = *reinterpret_cast<const u32x4*>(&hs[0][row][s * 32 + 8 * b]);
-          const u32x4 lo = *reinterpret_cast<const u32x4*>(&hs[1][row][s * 32 + 8 * b]);
+          u32x4 h[NP];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[q] = mfma16<DT>(w[s][q], hi, acc[q]);
-            acc[q] = mfma16<DT>(w[s][q], lo, acc[q]);
-          }
+          for (int k = 0; k < NP; ++k) h[k] = *reinterpret_cast<const u32x4*>(&hs[k][row][s * 32 + 8 * b]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int k = 0; k < NP; ++k) acc[q] = mfma16<DT>(w[s][q], h[k], acc[q]);
         }
       }
 #pragma unroll
@@ -531,12 +539,12 @@ __global__ __launch_bounds__(256) void k_lora_expand(const LoraArgs p) {
 constexpr int kLoraOneCols = 128;
 template <int DT, int YDT, int RB>
 __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
-  constexpr int RK = (RB + 1) / 2, kPitch = RK * 32 + 8;
+  constexpr int RK = (RB + 1) / 2, kPitch = RK * 32 + 8, NP = lora_parts<DT, YDT>();
   __shared__ int list[16];
   __shared__ int count[16];
   __shared__ float red[8][256];
   __shared__ float hv[16][RB * 16 + 1];
-  __shared__ __attribute__((aligned(16))) uint16_t hs[2][16][kPitch];
+  __shared__ __attribute__((aligned(16))) uint16_t hs[NP][16][kPitch];
   __shared__ float back[16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -596,7 +604,7 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
         float v[RK * 2];
 #pragma unroll
         for (int i = 0; i < RK * 2; ++i) v[i] = i * 16 + j < rank ? hv[row][i * 16 + j] : 0.0f;
-        lora_split_row<DT, RK * 2>(j, rk * 32, sc, hs[0][row], hs[1][row], back + row, v);
+        lora_split_row<DT, NP>(j, rk * 32, sc, hs[0][row], 16 * kPitch, back + row, v);
       }
       __syncthreads();
     }
@@ -608,8 +616,8 @@ __global__ __launch_bounds__(512) void k_lora_one(const LoraArgs p) {
 #pragma unroll
     for (int s = 0; s < RK; ++s) {
       if (s < rk) {
-        acc = mfma16<DT>(w[s], *reinterpret_cast<const u32x4*>(&hs[0][rl][s * 32 + 8 * b]), acc);
-        acc = mfma16<DT>(w[s], *reinterpret_cast<const u32x4*>(&hs[1][rl][s * 32 + 8 * b]), acc);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) acc = mfma16<DT>(w[s], *reinterpret_cast<const u32x4*>(&hs[k][rl][s * 32 + 8 * b]), acc);
       }
     }
     if (rl < nr) out.store(p, m, c0 + 4 * b, rank > 0 ? back[rl] : 0.0f, &acc, rank > 0);
