@@ -435,10 +435,8 @@ awq_status awq_route_experts(const void* logits, awq_dtype ldt, int64_t T, int64
  * integers q - z with the activations (as fp16 scaled by an exact power of
  * two) are summed in fp32 per group and scaled by the group's step in fp32;
  * the activation function and the sum over j run in fp32 and the output is
- * rounded once.  (down to bf16 with many rows per expert keeps the terms of
- * the sum over j in fp16 scaled by a power of two per 64 outputs: 2^-11 of
- * each term, an eighth of the output's rounding.)  1/s is expected folded (awq_fold_scales): into the producer
- * of x for up, into the up half's rows for down.
+ * rounded once.  1/s is expected folded (awq_fold_scales): into the producer of
+ * x for up, into the up half's rows for down.
  *
  *   x         up: [M][ldx], down: [M top_k][ldx], fp16 or bf16 (xdt)
  *   ids       [M][top_k] int32;  top_k 1 .. AWQ_MAX_TOP_K

@@ -430,6 +430,52 @@ def test_experts_infinite_step_stays_in_its_column(on_gpu, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("xdt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,g", [(1, 128), (40, 64), (1500, 64), (1500, 128), (3000, 256)])
+def test_down_terms_that_cancel(on_gpu, T, g, xdt, out):
+    """Whole numbers, so that every sum is exact in fp32: two rows that differ in
+    one channel, through one expert with weights 1 and -1, leave that
+    channel's weight exactly."""
+    n_exp, K, N = 3 if T > 1 else 16, 256, 203
+    rng = np.random.default_rng(T + g)
+    q = rng.integers(-2 ** 31, 2 ** 31, (n_exp, N, K // 8), dtype=np.int64).astype(np.int32)
+    step, zero = np.ones((n_exp, N, K // g), np.float16), np.full((n_exp, N, K // g), 8, np.uint8)
+    one = rng.integers(-127, 127, (T, 1, K)).astype(np.float32)
+    x = np.repeat(one, 2, axis=1)
+    at = rng.integers(0, K, T)
+    x[np.arange(T), 0, at] += 1
+    ids = np.repeat(rng.integers(0, n_exp, (T, 1)), 2, axis=1).astype(np.int32)
+    weights = np.tile(np.array([[1.0, -1.0]], np.float32), (T, 1))
+    y = awq.awq_w4a16_experts_down(gpu(torch.from_numpy(x.reshape(2 * T, K)).to(DTYPES[xdt])), gpu(torch.from_numpy(ids)),
+                                   gpu(torch.from_numpy(weights)), *packed((q, step, zero)), out_dtype=DTYPES[out],
+                                   group_size=g)
+    codes = np.stack([O.unpack_codes(q[e]) for e in range(n_exp)]).astype(np.float64) - 8
+    assert np.array_equal(f32(y).astype(np.float64), codes[ids[:, 0], :, at])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("N", [201, 257, 258, 259])
+def test_down_small_outputs_beside_a_huge_step(on_gpu, N, out):
+    """The first column's step is the largest there is, the others' the smallest:
+    what the tiles hold past the last column takes no part."""
+    T, n_exp, k, K, g = 1500, 3, 2, 256, 128
+    q, step, zero = stack(n_exp, N, K, g, N)
+    step[:] = 2.0 ** -24
+    step[:, :1] = 65504.0
+    zero[:] = 15
+    x = acts(T * k, K, torch.bfloat16, 3)
+    ids = choices(T, n_exp, k, 4, "holes")
+    weights = np.random.default_rng(T).uniform(0.5, 1.0, (T, k)).astype(np.float32)
+    if out == "f16":                                 # within its range
+        step[:, :1] = 2.0 ** -10
+    y = awq.awq_w4a16_experts_down(gpu(x), gpu(torch.from_numpy(ids)), gpu(torch.from_numpy(weights)),
+                                   *packed((q, step, zero)), out_dtype=DTYPES[out], group_size=g)
+    check_down(x, ids, weights, (q, step, zero), g, DTYPES[out], y, N)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 25, 1200])
 def test_experts_of_part_of_a_stack(on_gpu, T):
     """Experts 1, 2, ... of a larger stack, whose steps and zero points start

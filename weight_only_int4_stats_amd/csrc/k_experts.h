@@ -51,10 +51,8 @@ __device__ __forceinline__ float swiglu(float gate, float up) {
 
 namespace awq {
 
-// The tiled form (k_experts_gemm.hip), into out [slots][ldo]: down fp32, or
-// with rexp [slots][ldo / 64] fp16 scaled by 2^rexp.
+// The tiled form (k_experts_gemm.hip), into out [slots][ldo] (down: fp32).
 size_t experts_gemm_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k);
-hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, int8_t* rexp, void* ws,
-                               hipStream_t st);
+hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, void* ws, hipStream_t st);
 
 }  // namespace awq

@@ -512,42 +512,6 @@ __global__ __launch_bounds__(256) void k_experts_combine(const float* __restrict
   }
 }
 
-// The same from fp16 rows scaled by 2^rexp per 64 columns, eight outputs per
-// thread.
-template <int YDT>
-__global__ __launch_bounds__(256) void k_experts_combine16(const uint16_t* __restrict__ P, int64_t ldp,
-                                                           const int8_t* __restrict__ rexp,
-                                                           const int32_t* __restrict__ ids,
-                                                           const float* __restrict__ weights, int top_k, int E,
-                                                           int64_t M, int64_t N, void* __restrict__ y, int64_t ldy) {
-  const int64_t n8 = (N + 7) >> 3;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * n8; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / n8, n = (i - m * n8) * 8;
-    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int j = 0; j < top_k; ++j) {
-      const int64_t slot = m * top_k + j;
-      const int id = ids[slot];
-      if (id < 0 || id >= E) continue;
-      const float w = ldexpf(weights[slot], -rexp[slot * (ldp >> 6) + (n >> 6)]);
-      const u32x4 v = ldg128(P + slot * ldp + n);
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        s[c] = __builtin_fmaf(w, c & 1 ? hi_f32<DT_F16>(v[c >> 1]) : lo_f32<DT_F16>(v[c >> 1]), s[c]);
-    }
-    if (n + 8 <= N) {
-      u32x4 o;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] = from_f32<YDT>(s[2 * c]) | (from_f32<YDT>(s[2 * c + 1]) << 16);
-      *reinterpret_cast<u32x4a2*>(reinterpret_cast<uint16_t*>(y) + m * ldy + n) = o;
-    } else {
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (n + c < N) store_out(y, YDT, m * ldy + n + c, s[c]);
-    }
-  }
-}
-
 // Waves per slot of k_experts_token (0: the few-row kernel and a second
 // launch).  Few enough slots that two seldom share an expert (whose words would be
 // read twice), and at most two chunks per wave and slot.
@@ -589,15 +553,9 @@ static unsigned few_deal(int64_t S, int64_t E) {
   return (unsigned)(z < 1 ? 1 : z > 256 ? 256 : z);
 }
 
-static int64_t partial16_ld(int64_t N) { return (N + 63) / 64 * 64; }
-static size_t partial16_rows(int64_t S, int64_t N) { return align_up((size_t)S * (size_t)partial16_ld(N) * 2, 256); }
-
-// The rows per slot that down adds up, in either form.
+// The fp32 rows per slot that down adds up.
 static size_t partial_bytes(bool down, int64_t S, int64_t N) {
-  if (!down) return 0;
-  const size_t f32 = align_up((size_t)S * (size_t)partial_ld(N) * 4, 256);
-  const size_t f16 = partial16_rows(S, N) + align_up((size_t)S * (size_t)(partial16_ld(N) / 64), 256);
-  return f32 > f16 ? f32 : f16;
+  return down ? align_up((size_t)S * (size_t)partial_ld(N) * 4, 256) : 0;
 }
 
 size_t experts_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k) {
@@ -624,20 +582,7 @@ hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
     return hipGetLastError();
   }
   if (!few_rows(S, c.E, c.N)) {
-    char* rest = reinterpret_cast<char*>(ws) + partial_bytes(down, S, c.N);
-    if (!down || c.ydt != DT_BF16) {
-      e = launch_experts_gemm(c, out, ldo, nullptr, rest, st);
-    } else {
-      const int64_t ld16 = partial16_ld(c.N);
-      int8_t* rexp = reinterpret_cast<int8_t*>(ws) + partial16_rows(S, c.N);
-      e = launch_experts_gemm(c, ws, ld16, rexp, rest, st);
-      if (e != hipSuccess) return e;
-      int64_t blocks = (c.M * ((c.N + 7) / 8) + 255) / 256;
-      if (blocks > (1 << 20)) blocks = 1 << 20;
-      hipLaunchKernelGGL((k_experts_combine16<DT_BF16>), dim3((unsigned)blocks), dim3(256), 0, st, (const uint16_t*)ws,
-                         ld16, rexp, c.ids, c.weights, c.top_k, (int)c.E, c.M, c.N, c.y, c.ldy);
-      return hipGetLastError();
-    }
+    e = launch_experts_gemm(c, out, ldo, reinterpret_cast<char*>(ws) + partial_bytes(down, S, c.N), st);
   } else {
     const FewArgs a{c.x, c.K, c.ldx, c.N, ldo, c.ids, c.qw, c.scales, c.zeros, out, (int)S, (int)c.E, c.top_k,
                     c.group == 64 ? 6 : c.group == 128 ? 7 : 8, c.ydt, S < c.E, (int)(S < c.E ? S : c.E)};

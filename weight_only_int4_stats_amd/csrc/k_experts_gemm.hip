@@ -23,12 +23,11 @@
 //    tile is tall (128 rows) because they serve all of its rows: with 64 x 64
 //    tiles per wave the vector instructions, not the matrix cores, set the time.
 //  * With SwiGLU a tile's columns alternate 16 gate rows and their 16 up rows,
-//    so both meet in one lane.  down writes a row per slot; the weighted sum
-//    over a token's slots is k_experts_combine's.  Rows are fp32, or for bf16
-//    outputs fp16 scaled by a power of two per 64 columns: each term is off by
-//    at most 2^-11 of itself, an eighth of the output's own rounding, and half
-//    the bytes are written and read back (4096 tokens, 8 of 64 experts, 1024 ->
-//    2048: 225 us a call, 293 with fp32 rows).
+//    so both meet in one lane.  down writes an fp32 row per slot; the weighted
+//    sum over a token's slots is k_experts_combine's.  (fp16 rows, scaled by a
+//    power of two per 64 columns, halve the bytes between the two, 218 instead
+//    of 257 us a call for 4096 tokens, 8 of 64 experts, 1024 -> 2048, but they
+//    round every term to 2^-11 of itself and more beside a large one.)
 //  * 2048 tokens, 2 of 8 experts, 4096 -> 2 x 11008: 715 to 740 us a call (18 of
 //    them the preparation), 0.94 to 0.97 PFLOP/s where a large library product
 //    reaches 1.35; the clock settles under the load.
@@ -58,7 +57,6 @@ struct GemmArgs {
   const uint8_t* zeros;
   void* y;
   int64_t xrows;
-  int8_t* rexp;                                    // down with 16-bit rows: their exponents, one per 64 columns
   int S, E, top_k, group, unit, ydt;          // unit: channels per constant (64 or 128, at most the group)
   // workspace
   uint16_t* xq;                                    // [xrows][K]
@@ -388,7 +386,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): the wave's writes landed
     __builtin_amdgcn_wave_barrier();
-    if (MODE == EXPERTS_DOWN ? p.rexp == nullptr : p.ydt == DT_F32) {
+    if (MODE == EXPERTS_DOWN || p.ydt == DT_F32) {
       constexpr int kL = kW / 4;                   // lanes per row, four outputs each
 #pragma unroll
       for (int i = 0; i < 16 * kL / 64; ++i) {
@@ -411,44 +409,18 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
         const f32x4 o1 = *reinterpret_cast<const f32x4*>(stg + r * (kW + 4) + c + 4);
         const int64_t col = c0 + wv * kW + c;
         uint32_t h[8];
-        if constexpr (MODE == EXPERTS_DOWN) {
-          // fp16 scaled by a power of two per row and 64 columns (eight lanes)
-          float am = 0.0f;
+        if (r0 + r >= rows) continue;
+        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + (int64_t)slots[r0 + r] * p.ldy + col;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) am = fmaxf(am, fmaxf(fabsf(o0[j]), fabsf(o1[j])));
-          if (am == __builtin_inff()) {            // of those that are finite, whatever an infinite step made of its column
-            am = 0.0f;
-            for (int j = 0; j < 4; ++j)
-              am = fmaxf(am, fmaxf(fabsf(o0[j]) < __builtin_inff() ? fabsf(o0[j]) : 0.0f, fabsf(o1[j]) < __builtin_inff() ? fabsf(o1[j]) : 0.0f));
-          }
-          am = fmaxf(am, quad_xor1(am));
-          am = fmaxf(am, quad_xor2(am));
-          am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
-          const int pe = min(pow2_exp_for(am), 100);
-          if (r0 + r >= rows || col >= p.ldy) continue;
-          const int64_t slot = slots[r0 + r];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[j] = f32_to_f16_bits(ldexpf(o0[j], pe));
-            h[4 + j] = f32_to_f16_bits(ldexpf(o1[j], pe));
-          }
-          *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + slot * p.ldy + col) =
-              u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
-          if (c == 0) p.rexp[slot * (p.ldy >> 6) + (col >> 6)] = (int8_t)pe;
-        } else {
-          if (r0 + r >= rows) continue;
-          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + (int64_t)slots[r0 + r] * p.ldy + col;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[j] = p.ydt == DT_F16 ? f32_to_f16_bits(o0[j]) : f32_to_bf16_bits(o0[j]);
-            h[4 + j] = p.ydt == DT_F16 ? f32_to_f16_bits(o1[j]) : f32_to_bf16_bits(o1[j]);
-          }
-          if (col + 8 <= ncols)
-            *reinterpret_cast<u32x4a2*>(y) = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
-          else
-            for (int j = 0; j < 8; ++j)
-              if (col + j < ncols) y[j] = (uint16_t)h[j];
+        for (int j = 0; j < 4; ++j) {
+          h[j] = p.ydt == DT_F16 ? f32_to_f16_bits(o0[j]) : f32_to_bf16_bits(o0[j]);
+          h[4 + j] = p.ydt == DT_F16 ? f32_to_f16_bits(o1[j]) : f32_to_bf16_bits(o1[j]);
         }
+        if (col + 8 <= ncols)
+          *reinterpret_cast<u32x4a2*>(y) = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+        else
+          for (int j = 0; j < 8; ++j)
+            if (col + j < ncols) y[j] = (uint16_t)h[j];
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -495,7 +467,7 @@ size_t experts_gemm_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t
   return gemm_space(down, M, N, K, E, top_k, 64).total;     // the smallest group needs the most
 }
 
-hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, int8_t* rexp, void* ws, hipStream_t st) {
+hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, void* ws, hipStream_t st) {
   const bool down = c.mode == EXPERTS_DOWN;
   const int64_t S = c.M * c.top_k;
   const GemmSpace g = gemm_space(down, c.M, c.N, c.K, c.E, c.top_k, c.group);
@@ -512,7 +484,6 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, int
   a.scales = c.scales;
   a.zeros = c.zeros;
   a.y = out;
-  a.rexp = rexp;
   a.xrows = down ? S : c.M;
   a.S = (int)S;
   a.E = (int)c.E;
