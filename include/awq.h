@@ -469,8 +469,7 @@ awq_status awq_w4a16_experts_down(const void* x, awq_dtype xdt, int64_t M, int64
  * and y[m] = base[m] for rows whose adapter is outside [0, n_adapters)
  * (base == NULL: 0 in both).  base may be y itself (in place).  Sums and the
  * intermediate A x are held in fp32 (the latter enters the second product as
- * the sum of two 16-bit values, of three for fp32 outputs of bf16 inputs); the
- * output is rounded once.  What A and B hold past an adapter's rank is not
+ * the sum of two fp16 or three bf16 values); the output is rounded once.  What A and B hold past an adapter's rank is not
  * used, whatever it is.
  *
  *   x        [M][ldx] fp16 or bf16 (xdt), K a multiple of 8, <= AWQ_MAX_K

@@ -693,6 +693,31 @@ def test_lora_all_rows_one_adapter(on_gpu, M, L, one):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("xdt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,R", [(1, 8), (40, 8), (40, 72), (300, 136), (700, 32), (700, 136)])
+def test_lora_keeps_all_of_the_intermediate(on_gpu, M, R, xdt, out):
+    """Whole numbers, so that every sum is exact in fp32, and a base that takes
+    all but the last bits away: what is left of A x is right to the last bit."""
+    K, N, L = 1024, 90, 3
+    rng = np.random.default_rng(M + R)
+    x = rng.integers(-100, 101, (M, K)).astype(np.float64)
+    a = rng.integers(-100, 101, (L, R, K)).astype(np.float64)
+    b = rng.integers(-1, 2, (L, N, R)).astype(np.float64)
+    adapter = rng.integers(0, L, M).astype(np.int32)
+    h = np.einsum("mk,mrk->mr", x, a[adapter])
+    delta = np.einsum("mr,mnr->mn", h, b[adapter])
+    assert np.abs(h).max() > 2 ** 16 and np.einsum("mr,mnr->mn", np.abs(h), np.abs(b[adapter])).max() < 2 ** 24
+    scale = 2.0 ** -8                                # within fp16's range
+    base = torch.from_numpy(-delta * scale).to(DTYPES[out])
+    t = lambda v: gpu(torch.from_numpy(v).to(DTYPES[xdt]))  # noqa: E731
+    y = awq.awq_lora_add(t(x), gpu(torch.from_numpy(adapter)), t(a), t(b), base=gpu(base),
+                         scaling=torch.full((L,), scale, device="cuda"))
+    want = torch.from_numpy(delta * scale + f32(base).astype(np.float64)).to(DTYPES[out])
+    assert np.array_equal(f32(y), f32(want))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 20, 640])
 def test_lora_strides_and_neighbours(on_gpu, M):
     L, R, K, N = 3, 16, 128, 50
