@@ -172,6 +172,34 @@ def test_route_close_choices_under_a_bias(on_gpu, sig, n):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("size", [10.0, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("n,groups", [(4, (2, 1)), (64, (8, 3)), (96, (32, 9)), (256, (8, 4)), (1000, (4, 1))])
+def test_route_groups_whose_two_choices_cancel(on_gpu, sig, size, n, groups):
+    """A group's two choices of opposite sign leave a worth far below either, so
+    that what float loses of each choice decides."""
+    n_group, topk_group = groups
+    x = route_case(3000 if n <= 256 else 200, n, torch.float32, n, spread=0.5)
+    bias = np.full(n, -2 * size, np.float32)
+    bias[::n // n_group], bias[1::n // n_group] = size, -size   # the two largest of a group, the others far below
+    got = awq.awq_route_experts(gpu(x), 1, bias=gpu(torch.from_numpy(bias)), score="sigmoid" if sig else "softmax",
+                                n_group=n_group, topk_group=topk_group, group_top=2)
+    compare_route(got, O.route_experts(f32(x), 1, bias, sig, n_group, topk_group, 2), (sig, size, n))
+
+
+@pytest.mark.gpu
+def test_route_group_lost_by_float(on_gpu):
+    """Worths 1.00088 and 1.00054, in float 1.0 and 1.000977."""
+    x = torch.tensor([[0.0017578, 0.0017578, 0.0021484, 0.0]])
+    bias = np.array([1e4, -1e4, 1e4, -1e4], np.float32)
+    got = awq.awq_route_experts(gpu(x), 1, bias=gpu(torch.from_numpy(bias)), score="sigmoid", n_group=2, topk_group=1,
+                                group_top=2)
+    ref = O.route_experts(f32(x), 1, bias, True, 2, 1, 2)
+    assert ref[0][0, 0] == 0
+    compare_route(got, ref, "cancelling")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sig", [False, True])
 @pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 1), (4, 2, 2), (12, 5, 2)])
 def test_route_bias_switches_experts_off(on_gpu, sig, groups):
     """A bias of -inf: never chosen, in a group worth less for it, whole groups off."""

@@ -172,6 +172,15 @@ __device__ __forceinline__ bool route_float(const RouteArgs& p, const float (&l)
     const int lg = gs / V;
     const bool whole = gs % V == 0 && (lg & (lg - 1)) == 0;   // a group is a power of two of whole lanes
     uint32_t a1, a2, gv = 0;
+    // the size of the largest finite choice of the pairs that this lane sums:
+    // where a pair cancels, its rounding is what the sum is off by
+    float term = 0.0f;
+    auto pair = [&]() {
+      const float x = from_key(a1), y = from_key(a2);
+      if (fabsf(x) < __builtin_inff()) term = fmaxf(term, fabsf(x));
+      if (fabsf(y) < __builtin_inff()) term = fmaxf(term, fabsf(y));
+      a1 = to_key(x + y);
+    };
     if (whole) {
       a1 = c[0];
       a2 = kNoKey;
@@ -183,7 +192,7 @@ __device__ __forceinline__ bool route_float(const RouteArgs& p, const float (&l)
       if (lg > 8) merge_keys_dpp<0x140>(a1, a2);
       if (lg > 16) merge_keys(a1, a2, (uint32_t)__shfl_xor((int)a1, 16), (uint32_t)__shfl_xor((int)a2, 16));
       if (lg > 32) merge_keys(a1, a2, (uint32_t)__shfl_xor((int)a1, 32), (uint32_t)__shfl_xor((int)a2, 32));
-      if (two) a1 = to_key(from_key(a1) + from_key(a2));
+      if (two) pair();
       gv = (uint32_t)__shfl((int)a1, (lane * lg) & 63);
     } else {
       for (int g = 0; g < p.n_group; ++g) {
@@ -196,7 +205,7 @@ __device__ __forceinline__ bool route_float(const RouteArgs& p, const float (&l)
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1)
           merge_keys(a1, a2, (uint32_t)__shfl_xor((int)a1, off), (uint32_t)__shfl_xor((int)a2, off));
-        if (two) a1 = to_key(from_key(a1) + from_key(a2));
+        if (two) pair();
         if (lane == g) gv = a1;
       }
     }
@@ -210,9 +219,10 @@ __device__ __forceinline__ bool route_float(const RouteArgs& p, const float (&l)
     if (p.topk_group < p.n_group) {
       const float least = from_key(~wave_max_key(in && rank < p.topk_group ? ~gv : 0u));
       const float most = from_key(wave_max_key(in && rank >= p.topk_group ? gv : 0u));
-      const float far = scores ? 2.0f * margin + 0x1p-20f * (fabsf(least) + fabsf(most))
+      // a group is off by a margin and a float rounding (2^-24) of its choices and of their sum
+      const float far = scores ? 2.0f * margin + 0x1p-20f * (fabsf(least) + fabsf(most) + term)
                                : 0x1p-18f * (1.0f + fabsf(least) + fabsf(most));
-      if (!(least - most > far)) return false;     // also where both are -inf
+      if (__any(!(least - most > far))) return false;   // also where both are -inf
     }
     if (whole) {
       const bool out = !((keep >> (lane >> (31 - __builtin_clz((unsigned)lg)))) & 1);
