@@ -199,6 +199,24 @@ def test_route_group_lost_by_float(on_gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("groups", [(1, 1), (4, 2), (4, 1)])
+@pytest.mark.parametrize("top_k", [1, 5, 12])
+def test_route_sigmoid_near_saturation(on_gpu, groups, top_k):
+    """Logits of 20 to 40 whose sigmoids meet in double though the logits differ:
+    the lowest index wins wherever they are equal."""
+    rng = np.random.default_rng(top_k)
+    T, n = 400, 64
+    start = rng.uniform(20, 40, (T, 1))
+    x = start + np.cumsum(10.0 ** rng.uniform(-4, -2.5, (T, n)), axis=1)   # the larger logit at the higher index
+    x[::4] = x[::4, ::-1]
+    x[1::4, 32:] -= 60                               # half of the experts far down
+    xt = torch.from_numpy(x).float()
+    ref = O.route_experts(f32(xt), top_k, None, True, *groups, 1)
+    got = awq.awq_route_experts(gpu(xt), top_k, score="sigmoid", n_group=groups[0], topk_group=groups[1])
+    compare_route(got, ref, groups)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("sig", [False, True])
 @pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 1), (4, 2, 2), (12, 5, 2)])
 def test_route_bias_switches_experts_off(on_gpu, sig, groups):
