@@ -522,6 +522,27 @@ def test_down_small_outputs_beside_a_huge_step(on_gpu, N, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,g", [(30, 128), (1500, 64), (1500, 256)])
+@pytest.mark.parametrize("groups", [(0,), (1,), (0, 1), (1, 3), (3,), (2, 3)])
+def test_infinite_steps_give_infinity(on_gpu, T, g, groups):
+    """One or more groups of a row with an infinite step, of products above 0:
+    the row's outputs are infinite, the others what they were."""
+    n_exp, K, N = 3, 4 * g, 400
+    q, step, zero = stack(n_exp, N, K, g, T + g)
+    zero[:] = 0
+    q |= 0x11111111
+    x = torch.from_numpy(np.random.default_rng(T).uniform(0.5, 2.0, (T, K))).half()
+    ids = choices(T, n_exp, 2, T, "")
+    p, gi = packed((q, step, zero)), gpu(torch.from_numpy(ids))
+    y = f32(awq.awq_w4a16_experts_up(gpu(x), gi, *p, out_dtype=torch.float32, group_size=g))
+    for i in groups:
+        p[1][:, 5::7, i] = math.inf
+    got = f32(awq.awq_w4a16_experts_up(gpu(x), gi, *p, out_dtype=torch.float32, group_size=g))
+    y[:, 5::7] = np.inf
+    assert np.array_equal(got, y)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 25, 1200])
 def test_experts_of_part_of_a_stack(on_gpu, T):
     """Experts 1, 2, ... of a larger stack, whose steps and zero points start

@@ -286,7 +286,7 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   };
   u32x4 aE[HB], aO[HB], bq[4];
   float ratio[4], last[4] = {1.0f, 1.0f, 1.0f, 1.0f};   // D of the last unit / this unit's; the last unit's
-  float any[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // the largest |D|: 0 and the column is 0
+  float any[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // the largest |D|: 0 and the column is 0, or it is infinite
   auto nz = [&](int n) { return (cz[n] >> 16) * 0x10001u; };
 #pragma unroll
   for (int q = 0; q < 4; ++q) copy(0, 0, q);
@@ -317,10 +317,11 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           // a step of 0 counts as 2^-60, which keeps the ratios finite and is
-          // below the fp32 rounding of any other (2^-24 at least)
-          const float f = f16_to_f32(cz[n] & 0xFFFFu);
-          const float d = fabsf(f) < 0x1p-60f ? 0x1p-60f : f;
-          any[n] = fmaxf(any[n], fabsf(f));
+          // below the fp32 rounding of any other (2^-24 at least); an infinite
+          // one as 2^60, above any other, until the epilogue
+          const float f = f16_to_f32(cz[n] & 0xFFFFu), size = fabsf(f);
+          const float d = size < 0x1p-60f ? 0x1p-60f : size == __builtin_inff() ? copysignf(0x1p60f, f) : f;
+          any[n] = fmaxf(any[n], size);
           ratio[n] = last[n] * __builtin_amdgcn_rcpf(d);
           last[n] = d;
         }
@@ -363,8 +364,10 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
   // rows 4 b + v.
   __syncthreads();                                 // every wave is done with the stages
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < 4; ++n) {
     if (any[n] == 0.0f) last[n] *= 0.0f;
+    if (any[n] == __builtin_inff()) last[n] *= any[n];
+  }
   constexpr int kW = MODE == EXPERTS_SWIGLU ? 32 : 64;                    // outputs per row of the wave
   float* stg = reinterpret_cast<float*>(lds) + wv * 16 * (kW + 4);
 #pragma unroll
