@@ -522,6 +522,27 @@ def test_down_small_outputs_beside_a_huge_step(on_gpu, N, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,g", [(1500, 256, 64), (1500, 8192, 64), (6500, 2048, 128), (1500, 2048, 256)])
+def test_one_step_for_all_of_a_row(on_gpu, T, K, g):
+    """Rows whose groups share one step, of whole-number sums: the step enters
+    with one rounding, however many groups there are."""
+    n_exp, k, N = 3, 1 if T < 2000 else 2, 400
+    rng = np.random.default_rng(K)
+    q = rng.integers(-2 ** 31, 2 ** 31, (n_exp, N, K // 8), dtype=np.int64).astype(np.int32)
+    step = np.repeat(rng.uniform(2e-4, 4e-3, (n_exp, N, 1)).astype(np.float16), K // g, axis=2)
+    zero = np.full((n_exp, N, K // g), 8, np.uint8)
+    x = rng.integers(-31, 32, (T, K)).astype(np.float32)   # sums below 2^24
+    ids = rng.integers(0, n_exp, (T, k)).astype(np.int32)
+    y = awq.awq_w4a16_experts_up(gpu(torch.from_numpy(x).half()), gpu(torch.from_numpy(ids)), *packed((q, step, zero)),
+                                 out_dtype=torch.float32, group_size=g)
+    y = f32(y).reshape(T, k, N)
+    for e in range(n_exp):
+        z = x.astype(np.float64) @ (O.unpack_codes(q[e]).astype(np.float64) - 8).T * step[e, :, 0].astype(np.float64)
+        for j in range(k):
+            assert np.array_equal(y[ids[:, j] == e, j], z.astype(np.float32)[ids[:, j] == e]), (e, j)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,g", [(30, 128), (1500, 64), (1500, 256)])
 @pytest.mark.parametrize("groups", [(0,), (1,), (0, 1), (1, 3), (3,), (2, 3)])
 def test_infinite_steps_give_infinity(on_gpu, T, g, groups):

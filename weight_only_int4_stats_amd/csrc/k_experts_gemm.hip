@@ -16,10 +16,11 @@
 //    activations with the exact integers (q - z) 2^-9.  The accumulators hold
 //    the sum in units of the current group's step: a new group multiplies them
 //    by D[g - 1] / D[g] (fp32, one multiplication per value and group; the
-//    hardware's reciprocal is within 1 unit in the last place) and the
-//    epilogue by the last step.  So no operand is rounded, unlike step (q - z)
-//    in fp16 (1e-4 of every result), and no second set of accumulators is
-//    needed.  Unpacking costs 9 vector instructions per eight codes; a wave's
+//    quotient is within 1 unit of 2^-24 and 1 for equal steps: with the
+//    reciprocal's product alone, up to 4 units, a row of one step drifted by a
+//    unit a group) and the epilogue by the last step.  So no operand is
+//    rounded, unlike step (q - z) in fp16 (1e-4 of every result), and no second
+//    set of accumulators is needed.  Unpacking costs 9 vector instructions per eight codes; a wave's
 //    tile is tall (128 rows) because they serve all of its rows: with 64 x 64
 //    tiles per wave the vector instructions, not the matrix cores, set the time.
 //  * With SwiGLU a tile's columns alternate 16 gate rows and their 16 up rows,
@@ -322,7 +323,9 @@ __global__ __launch_bounds__(256, 2) void k_experts_gemm(const GemmArgs p) {
           const float f = f16_to_f32(cz[n] & 0xFFFFu), size = fabsf(f);
           const float d = size < 0x1p-60f ? 0x1p-60f : size == __builtin_inff() ? copysignf(0x1p60f, f) : f;
           any[n] = fmaxf(any[n], size);
-          ratio[n] = last[n] * __builtin_amdgcn_rcpf(d);
+          // the quotient, corrected by its remainder: equal steps give 1
+          const float r = __builtin_amdgcn_rcpf(d), t = last[n] * r;
+          ratio[n] = __builtin_fmaf(__builtin_fmaf(-t, d, last[n]), r, t);
           last[n] = d;
         }
       }
