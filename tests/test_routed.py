@@ -564,6 +564,38 @@ def test_infinite_steps_give_infinity(on_gpu, T, g, groups):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("xdt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,g", [(1, 128), (1, 64), (30, 128), (30, 64), (1500, 128), (1500, 64), (6500, 256)])
+def test_experts_infinite_activations(on_gpu, T, g, xdt):
+    """One infinite activation, whose weight is not 0, makes its rows' outputs
+    infinite with the sign of the weight's step; the row's other activations
+    are large and stay finite."""
+    n_exp, k, K, N = 16 if T == 1 else 3, 2, 512, 262
+    q, step, zero = stack(n_exp, N, K, g, T + g)
+    rng = np.random.default_rng(T)
+    step *= rng.choice([-1, 1], step.shape).astype(np.float16)
+    zero[:] = 0
+    q[:, :, 37 // 8] |= 1 << (4 * (37 % 8))          # the code of channel 37 is not 0
+    sign = np.sign(step[:, :, 37 // g].astype(np.float64))
+    ids = choices(T, n_exp, k, T, "")
+    p, gi = packed((q, step, zero)), gpu(torch.from_numpy(ids))
+    x = acts(T, K, DTYPES[xdt], 6) * 50
+    hit = rng.random(T) < 0.2
+    hit[0] = True
+    x[torch.from_numpy(hit), 37] = math.inf
+    y = f32(awq.awq_w4a16_experts_up(gpu(x), gi, *p, out_dtype=torch.float32, group_size=g)).reshape(T, k, N)
+    assert np.array_equal(y[hit], sign[ids[hit]] * np.inf) and np.isfinite(y[~hit]).all()
+    # down: one of the token's rows is infinite
+    h = acts(T * k, K, DTYPES[xdt], 7) * 50
+    h[::k][torch.from_numpy(hit), 37] = -math.inf
+    weights = rng.uniform(0.5, 1.0, (T, k)).astype(np.float32)
+    for out in ("f32", "bf16"):
+        y = f32(awq.awq_w4a16_experts_down(gpu(h), gi, gpu(torch.from_numpy(weights)), *p, out_dtype=DTYPES[out],
+                                           group_size=g))
+        assert np.array_equal(y[hit], -sign[ids[hit, 0]] * np.inf) and np.isfinite(y[~hit]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 25, 1200])
 def test_experts_of_part_of_a_stack(on_gpu, T):
     """Experts 1, 2, ... of a larger stack, whose steps and zero points start

@@ -18,6 +18,26 @@ __device__ __forceinline__ float row16_max(float v) {
   return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false)));
 }
 
+// |v|, 0 for what is not finite.  A row's power of two goes by its finite
+// values, so that an infinite activation does not push the others past fp16's
+// range: where the maximum turns out infinite it is formed again of these.
+__device__ __forceinline__ float finite_size(float v) { return fabsf(v) < __builtin_inff() ? fabsf(v) : 0.0f; }
+
+// The maximum of |v[0 .. 7]| over each 16-lane row, of the finite values.
+__device__ __forceinline__ float row16_finite_max(const float (&v)[8]) {
+  float am = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) am = fmaxf(am, fabsf(v[c]));
+  am = row16_max(am);
+  if (am == __builtin_inff()) {                    // whole 16-lane rows branch
+    am = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) am = fmaxf(am, finite_size(v[c]));
+    am = row16_max(am);
+  }
+  return am;
+}
+
 // -z 2^-9 as fp16, twice.
 __device__ __forceinline__ uint32_t experts_nz(uint32_t z) {
   return f32_to_f16_bits(-(float)z * 0x1p-9f) * 0x10001u;

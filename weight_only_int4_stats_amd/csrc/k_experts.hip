@@ -225,11 +225,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_few(const FewArgs p) {
           v[2 * c] = lo_f32<DT>(raw[c]);
           v[2 * c + 1] = hi_f32<DT>(raw[c]);
         }
-        float am = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) am = fmaxf(am, fabsf(v[c]));
-        am = row16_max(am);
-        const int pe = pow2_exp_for(am);
+        const int pe = pow2_exp_for(row16_finite_max(v));
         uint32_t h[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) h[c] = f32_to_f16_bits(ldexpf(v[c], pe));
@@ -414,11 +410,7 @@ __global__ __launch_bounds__(kFewThreads) void k_experts_token(const FewArgs p, 
           v[2 * c] = lo_f32<DT>(raw[i][c]);
           v[2 * c + 1] = hi_f32<DT>(raw[i][c]);
         }
-        float am = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) am = fmaxf(am, fabsf(v[c]));
-        am = row16_max(am);
-        const int pe = pow2_exp_for(am);
+        const int pe = pow2_exp_for(row16_finite_max(v));
         uint32_t h[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) h[c] = f32_to_f16_bits(ldexpf(v[c], pe));

@@ -92,6 +92,16 @@ __device__ __forceinline__ void prep_row(const GemmArgs& p, int64_t row) {
   for (int c = lane + 64 * kKeep; c < n8; c += 64) piece_max(ldg128(src + c * 8));
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) am = fmaxf(am, __shfl_xor(am, off));
+  if (am == __builtin_inff()) {                    // again, of the finite values
+    am = 0.0f;
+    for (int c = lane; c < n8; c += 64) {
+      const u32x4 w = ldg128(src + c * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) am = fmaxf(am, fmaxf(finite_size(lo_f32<DT>(w[j])), finite_size(hi_f32<DT>(w[j]))));
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) am = fmaxf(am, __shfl_xor(am, off));
+  }
   const int pe = pow2_exp_for(am);
   if (lane == 0) p.pexp[row] = pe;
   auto convert = [&](int c, const u32x4& w) {
