@@ -838,6 +838,28 @@ def test_lora_keeps_all_of_the_intermediate(on_gpu, M, R, xdt, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("xdt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,R", [(1, 8), (40, 24), (40, 72), (300, 136), (700, 32), (700, 136)])
+def test_lora_infinite_activations(on_gpu, M, R, xdt):
+    """An infinite activation makes A x infinite; B of the same signs makes the
+    row's outputs infinite, and no other row's."""
+    K, N, L = 264, 90, 3
+    rng = np.random.default_rng(M + R)
+    x = acts(M, K, DTYPES[xdt], M)
+    a = torch.from_numpy(rng.normal(0, 1 / math.sqrt(K), (L, R, K))).to(DTYPES[xdt])
+    b = torch.from_numpy(rng.uniform(0.5, 1.0, (L, N, R))).to(DTYPES[xdt])
+    b *= torch.where(a[:, :, 100] < 0, -1.0, 1.0).to(b.dtype)[:, None, :]
+    assert (a[:, :, 100] != 0).all()
+    adapter = rng.integers(0, L, M).astype(np.int32)
+    hit = rng.random(M) < 0.2
+    hit[0] = True
+    x[torch.from_numpy(hit), 100] = math.inf
+    for out in (torch.float32, DTYPES[xdt]):
+        y = f32(awq.awq_lora_add(gpu(x), gpu(torch.from_numpy(adapter)), gpu(a), gpu(b), out_dtype=out))
+        assert (y[hit] == np.inf).all() and np.isfinite(y[~hit]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 20, 640])
 def test_lora_strides_and_neighbours(on_gpu, M):
     L, R, K, N = 3, 16, 128, 50

@@ -294,9 +294,11 @@ template <int DT>
 constexpr int lora_parts() { return DT == DT_BF16 ? 3 : 2; }
 template <int DT, int NP, int NI>
 __device__ __forceinline__ void lora_split_row(int j, int pad, float sc, uint16_t* part, int stride, float* back, const float (&v)[NI]) {
+  // the power of two goes by the finite values: an infinite one stays infinite
+  // and the others what they are
   float am = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) am = fmaxf(am, fabsf(v[i]));
+  for (int i = 0; i < NI; ++i) am = fmaxf(am, fabsf(v[i]) < __builtin_inff() ? fabsf(v[i]) : 0.0f);
   am = fmaxf(am, quad_xor1(am));
   am = fmaxf(am, quad_xor2(am));
   am = fmaxf(am, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(am), 0x141, 0xF, 0xF, false)));
@@ -311,7 +313,7 @@ __device__ __forceinline__ void lora_split_row(int j, int pad, float sc, uint16_
       for (int k = 0; k < NP; ++k) {
         const uint32_t h = from_f32<DT>(f);
         part[k * stride + r] = (uint16_t)h;
-        f -= to_f32<DT>(h);
+        f = fabsf(f) < __builtin_inff() ? f - to_f32<DT>(h) : 0.0f;   // the first part says it all
       }
     }
   }
