@@ -1141,6 +1141,30 @@ def test_lora_refusals():
     assert awq.awq_workspace_bytes(awq.AWQ_OP_LORA, -1, 64, 256, 3, 16) == 0
 
 
+@pytest.mark.parametrize("M,L", [(512, 1), (500, 0), (512, 40), (600, 2)])
+def test_lora_refuses_more_threads_than_a_launch_has(M, L):
+    """The most columns whose launch still fits are answered (up to the missing
+    workspace), some more refused."""
+    def call(N):
+        return awq.lib().awq_lora_add(A, 0, M, 4096, 4096, B, A, B, L, 128, None, None, None, 0, N, D, 2, N, None, 0, None)
+
+    # block rows of 256 threads and 256 columns: 16 rows of an adapter each, dealt twice over, or tiles of 64
+    rows = (L + 1) * ((M // (L + 1) + 7) // 8) if M <= 512 else M // 64 + L + 1
+    most = ((1 << 32) - 1) // (256 * rows) * 256
+    if L:
+        assert call(most) == 6
+    assert call(most + 1) == 5 and call(most + (most >> 3)) == 5 and call(1 << 40) == 5
+
+
+def test_experts_refuse_more_threads_than_a_launch_has():
+    """The constants' layout takes a thread per weight row and eight groups."""
+    def call(M, n_exp, K, N):
+        return awq.lib().awq_w4a16_experts_up(A, 0, M, K, K, B, 2, A, B, C, n_exp, N, 64, 0, D, 2, N, None, 0, None)
+
+    assert call(4000, 1024, 1024, 2_000_000) == 6    # answered up to the missing workspace
+    assert call(4000, 1024, 1024, 3_000_000) == 5
+
+
 def test_binding_refuses_host_tensors_and_wrong_names():
     x = torch.zeros(2, 64)
     ids = torch.zeros(2, 1, dtype=torch.int32)

@@ -121,6 +121,8 @@ struct ExpertsCall {
 };
 // of the sizes alone (M, K, top_k, E, N; every group size)
 size_t experts_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k);
+// threads of the largest of its launches (which have 32-bit sizes)
+int64_t experts_threads(int mode, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k, int group);
 hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st);
 
 // ---- per-row low-rank adapters (k_lora.hip) -----------------------------------
@@ -141,6 +143,7 @@ struct LoraCall {
   int64_t ldy;
 };
 size_t lora_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R);
+int64_t lora_threads(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R);
 hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st);
 
 // ---- plain streaming read (k_stream.hip): bytes a multiple of 1024, blocks

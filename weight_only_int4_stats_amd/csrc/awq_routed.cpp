@@ -34,8 +34,7 @@ awq_status experts(int mode, const void* x, awq_dtype xdt, int64_t M, int64_t K,
   if (!x || !ids || !qweight || !scales || !zeros || !y || (down && !weights)) return AWQ_ERR_NULL;
   if (M > kMaxRows / top_k || N > ((int64_t)1 << 32) / K - 1) return AWQ_ERR_UNSUPPORTED;
   if ((down ? M * top_k : M) * K * 2 >= (int64_t)1 << 31) return AWQ_ERR_UNSUPPORTED;
-  // the tiled product: 256 threads per 32 rows or more x 256 weight rows
-  if ((M * top_k / 32 + E + 2) * (N / 256 + 1) > kMaxThreads / 256) return AWQ_ERR_UNSUPPORTED;
+  if (awq::experts_threads(mode, M, N, K, E, top_k, group_size) > kMaxThreads) return AWQ_ERR_UNSUPPORTED;
   if (ldx % 8 != 0 || !aligned(x, 16) || !aligned(qweight, 16) || !aligned(scales, 2) || !aligned(ids, 4) ||
       !aligned(y, bytes_of(ydt)) || (down && !aligned(weights, 4)))
     return AWQ_ERR_ALIGN;
@@ -103,9 +102,7 @@ awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int6
       !aligned(adapter, 4) || (ranks && !aligned(ranks, 4)) || (scaling && !aligned(scaling, 4)) ||
       (base && !aligned(base, bytes_of(ydt))) || !aligned(y, bytes_of(ydt)))
     return AWQ_ERR_ALIGN;
-  // the expand: 256 threads per 64 rows of one adapter (or up to 512 rows: 16) x 256 columns
-  const int64_t groups = (M <= 512 ? M / 16 : M / 64) + (M < n_adapters + 1 ? M : n_adapters + 1);
-  if (groups * (N / 256 + 1) > kMaxThreads / 256) return AWQ_ERR_UNSUPPORTED;
+  if (N > kMaxThreads || awq::lora_threads(M, N, K, n_adapters, R) > kMaxThreads) return AWQ_ERR_UNSUPPORTED;
   const size_t need = awq::lora_ws_bytes(M, N, K, n_adapters, R);
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return AWQ_ERR_WORKSPACE;
   const awq::LoraCall c{(const uint16_t*)x, (int)xdt, M, K, ldx, adapter, (const uint16_t*)a, (const uint16_t*)b,

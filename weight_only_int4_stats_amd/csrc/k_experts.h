@@ -73,6 +73,7 @@ namespace awq {
 
 // The tiled form (k_experts_gemm.hip), into out [slots][ldo] (down: fp32).
 size_t experts_gemm_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k);
+int64_t experts_gemm_threads(int mode, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k, int group);
 hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, void* ws, hipStream_t st);
 
 }  // namespace awq

@@ -556,6 +556,13 @@ size_t experts_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t E, i
   return partial_bytes(down, S, N) + (few_rows(S, E, N) ? 0 : experts_gemm_ws_bytes(down, M, N, K, E, top_k));
 }
 
+// (The few-row forms' grids are at most 32 N in any direction, and N K < 2^32.)
+int64_t experts_threads(int mode, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k, int group) {
+  const int64_t S = M * top_k;
+  if (few_rows(S, E, N) || (mode == EXPERTS_DOWN && token_slices(S, E, K, (int)top_k))) return 0;
+  return experts_gemm_threads(mode, M, N, K, E, top_k, group);
+}
+
 hipError_t launch_experts(const ExpertsCall& c, void* ws, hipStream_t st) {
   const int64_t S = c.M * c.top_k;
   const bool down = c.mode == EXPERTS_DOWN;

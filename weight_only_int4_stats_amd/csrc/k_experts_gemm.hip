@@ -483,6 +483,29 @@ size_t experts_gemm_ws_bytes(bool down, int64_t M, int64_t N, int64_t K, int64_t
   return gemm_space(down, M, N, K, E, top_k, 64).total;     // the smallest group needs the most
 }
 
+// Blocks of the preparation's parts: sort, rows, constants, zero rows.
+struct PrepBlocks {
+  int64_t sort, rows, consts, zero;
+  int64_t all() const { return sort + rows + consts + zero; }
+};
+static PrepBlocks prep_blocks(bool down, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k, int group) {
+  const int64_t S = M * top_k;
+  return PrepBlocks{group_chunks(S), ((down ? S : M) + 15) / 16,
+                    (E * N * ((K / group + 7) / 8) + kPlanThreads - 1) / kPlanThreads, down ? 0 : (S + 15) / 16};
+}
+
+static int64_t gemm_blocks(int mode, int64_t M, int64_t N, int64_t E, int64_t top_k) {
+  const int64_t per = mode == EXPERTS_SWIGLU ? kGemmN / 2 : kGemmN, cols = mode == EXPERTS_SWIGLU ? N / 2 : N;
+  const int64_t tiles = group_tiles_max(M * top_k, E, gemm_tile_rows(M * top_k, E, N)) * ((cols + per - 1) / per);
+  return (tiles + kXcd - 1) / kXcd * kXcd;
+}
+
+int64_t experts_gemm_threads(int mode, int64_t M, int64_t N, int64_t K, int64_t E, int64_t top_k, int group) {
+  const int64_t prep = prep_blocks(mode == EXPERTS_DOWN, M, N, K, E, top_k, group).all() * kPlanThreads;
+  const int64_t gemm = gemm_blocks(mode, M, N, E, top_k) * 256;
+  return prep > gemm ? prep : gemm;
+}
+
 hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, void* ws, hipStream_t st) {
   const bool down = c.mode == EXPERTS_DOWN;
   const int64_t S = c.M * c.top_k;
@@ -511,19 +534,18 @@ hipError_t launch_experts_gemm(const ExpertsCall& c, void* out, int64_t ldo, voi
   a.pexp = reinterpret_cast<int*>(w + g.pexp);
   a.ctab = reinterpret_cast<uint32_t*>(w + g.ctab);
   a.plan = group_plan_at(w + g.plan, S, c.E, tile);
-  a.b_rows = group_chunks(S);
-  a.b_consts = a.b_rows + (int)((a.xrows + 15) / 16);
-  a.b_zero = a.b_consts + (int)((c.E * c.N * ((c.K / c.group + 7) / 8) + kPlanThreads - 1) / kPlanThreads);
+  const PrepBlocks blocks = prep_blocks(down, c.M, c.N, c.K, c.E, c.top_k, c.group);
+  a.b_rows = (int)blocks.sort;
+  a.b_consts = a.b_rows + (int)blocks.rows;
+  a.b_zero = a.b_consts + (int)blocks.consts;
   const int64_t cols = c.mode == EXPERTS_SWIGLU ? c.N / 2 : c.N;
-  const unsigned pb = (unsigned)(a.b_zero + (down ? 0 : (S + 15) / 16));
+  const unsigned pb = (unsigned)blocks.all();
   if (c.xdt == DT_F16) hipLaunchKernelGGL((k_experts_prep<DT_F16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
   else hipLaunchKernelGGL((k_experts_prep<DT_BF16>), dim3(pb), dim3(kPlanThreads), group_plan_lds(a.E), st, a, tile, cols);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = launch_group_place(c.ids, S, c.E, tile, a.plan, st);
   if (e != hipSuccess) return e;
-  const int64_t per = c.mode == EXPERTS_SWIGLU ? kGemmN / 2 : kGemmN;
-  const int64_t tiles = group_tiles_max(S, c.E, tile) * ((cols + per - 1) / per);
-  const dim3 grid((unsigned)((tiles + kXcd - 1) / kXcd * kXcd));
+  const dim3 grid((unsigned)gemm_blocks(c.mode, c.M, c.N, c.E, c.top_k));
   auto go = [&](auto mode) {
     constexpr int MODE = decltype(mode)::value;
     if (tile == 128) gemm_launch<MODE, 8>(a, grid, st);

@@ -653,9 +653,13 @@ static bool lora_one(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_
   return !lora_planned(M) && R <= 64 && a <= (256 << 10) && a * blocks <= (32 << 20);
 }
 
+// Block rows of the expand, and of the one launch.
+static int64_t lora_block_rows(int64_t M, int64_t n_adapters) {
+  return lora_planned(M) ? group_tiles_max(M, n_adapters, kLoraTile) : lora_groups(M, n_adapters) * lora_deal(M, n_adapters);
+}
+
 static int lora_ksplit(int64_t M, int64_t K, int64_t n_adapters) {
-  const int64_t blocks =
-      lora_planned(M) ? (M + kLoraTile - 1) / kLoraTile : lora_groups(M, n_adapters) * lora_deal(M, n_adapters);
+  const int64_t blocks = lora_planned(M) ? (M + kLoraTile - 1) / kLoraTile : lora_block_rows(M, n_adapters);
   const int64_t steps = (K + 63) / 64;
   int64_t want = 256 / blocks;                     // about a block per compute unit
   if (want > steps / kShrinkWaves) want = steps / kShrinkWaves;   // a step per wave at least
@@ -670,6 +674,14 @@ static size_t lora_h_bytes(int64_t M, int64_t K, int64_t n_adapters, int64_t R) 
 size_t lora_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R) {
   if (M <= 0 || N <= 0 || K <= 0 || n_adapters < 0 || R <= 0 || lora_one(M, N, K, n_adapters, R)) return 0;
   return lora_h_bytes(M, K, n_adapters, R) + (lora_planned(M) ? group_plan_bytes(M, n_adapters, kLoraTile) : 0);
+}
+
+// Of the launch over all columns: the shrink has at most 4 blocks of 512 per
+// block row and K split, far from 2^32 at the most rows there may be.
+int64_t lora_threads(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R) {
+  const bool one = lora_one(M, N, K, n_adapters, R);
+  const int64_t cols = one ? kLoraOneCols : 4 * kLoraCols;
+  return (N + cols - 1) / cols * lora_block_rows(M, n_adapters) * (one ? 512 : 256);
 }
 
 hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st) {
@@ -695,7 +707,7 @@ hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st) {
   p.h = reinterpret_cast<float*>(ws);
   p.by_row = c.M < c.n_adapters + 1;
   p.deal = lora_deal(c.M, c.n_adapters);
-  unsigned gy = (unsigned)(lora_groups(c.M, c.n_adapters) * p.deal);
+  const unsigned gy = (unsigned)lora_block_rows(c.M, c.n_adapters);
   const bool one = lora_one(c.M, c.N, c.K, c.n_adapters, c.R);
   const int64_t cols = one ? kLoraOneCols : 4 * kLoraCols;
   p.nx = (int)((c.N + cols - 1) / cols);
@@ -703,7 +715,6 @@ hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st) {
     p.plan = group_plan_at(reinterpret_cast<char*>(ws) + lora_h_bytes(c.M, c.K, c.n_adapters, c.R), c.M, c.n_adapters, kLoraTile);
     const hipError_t e = launch_group_plan(c.adapter, c.M, c.n_adapters, kLoraTile, p.plan, st);
     if (e != hipSuccess) return e;
-    gy = (unsigned)group_tiles_max(c.M, c.n_adapters, kLoraTile);
   }
   const dim3 grid((unsigned)p.nx * gy);
   auto typed = [&](auto dtc, auto ydc) {
