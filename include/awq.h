@@ -135,7 +135,8 @@ int awq_abi_version(void);
 const char* awq_status_str(awq_status st);
 
 /* Workspace bytes a call needs for the given sizes (0 if it needs none), for
- * every group size.  Arguments that an op does not use are ignored. */
+ * every group size.  Arguments that an op does not use are ignored.  For the
+ * routed products and the adapters the bytes for M serve every smaller M too. */
 size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T, int n_alpha);
 
 /*

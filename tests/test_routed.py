@@ -1165,6 +1165,19 @@ def test_experts_refuse_more_threads_than_a_launch_has():
     assert call(4000, 1024, 1024, 3_000_000) == 5
 
 
+@pytest.mark.parametrize("op,N,K,T,n", [
+    ("LORA", 4096, 4096, 6, 64), ("LORA", 11008, 4096, 32, 64), ("LORA", 4096, 14336, 1, 128), ("LORA", 64, 96, 2, 8),
+    ("LORA", 300, 131072, 8192, 256), ("LORA", 4096, 4096, 0, 16),
+    ("EXPERTS_UP", 4096, 1024, 8, 2), ("EXPERTS_UP", 100, 64, 3, 1), ("EXPERTS_UP", 2048, 2048, 64, 64),
+    ("EXPERTS_DOWN", 2049, 1024, 64, 8), ("EXPERTS_DOWN", 4096, 64, 6, 1), ("EXPERTS_DOWN", 30, 8192, 1024, 2),
+])
+def test_workspace_of_the_largest_batch_serves_all(op, N, K, T, n):
+    """A program that makes its workspace once, for the most rows it takes."""
+    rows = sorted(set(range(1, 3000)) | set(range(3000, 70000, 37)) | {int(1.1 ** i) for i in range(80, 174)})
+    need = [awq.awq_workspace_bytes(getattr(awq._abi, "AWQ_OP_" + op), M, N, K, T, n) for M in rows]
+    assert need == sorted(need)
+
+
 def test_binding_refuses_host_tensors_and_wrong_names():
     x = torch.zeros(2, 64)
     ids = torch.zeros(2, 1, dtype=torch.int32)

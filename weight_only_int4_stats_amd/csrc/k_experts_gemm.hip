@@ -475,7 +475,7 @@ static GemmSpace gemm_space(bool down, int64_t M, int64_t N, int64_t K, int64_t 
   g.pexp = g.xq + align_up((size_t)xrows * (size_t)K * 2, 256);
   g.ctab = g.pexp + align_up((size_t)xrows * 4, 256);
   g.plan = g.ctab + align_up((size_t)E * (size_t)N * (size_t)(K / (group == 64 ? 64 : 128)) * 4, 256);
-  g.total = g.plan + group_plan_bytes(S, E, gemm_tile_rows(S, E, N));
+  g.total = g.plan + group_plan_bytes(S, E, 32);   // the lowest tiles need the most: fewer slots may take lower ones
   return g;
 }
 

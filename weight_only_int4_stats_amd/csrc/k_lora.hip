@@ -658,17 +658,26 @@ static int64_t lora_block_rows(int64_t M, int64_t n_adapters) {
   return lora_planned(M) ? group_tiles_max(M, n_adapters, kLoraTile) : lora_groups(M, n_adapters) * lora_deal(M, n_adapters);
 }
 
-static int lora_ksplit(int64_t M, int64_t K, int64_t n_adapters) {
-  const int64_t blocks = lora_planned(M) ? (M + kLoraTile - 1) / kLoraTile : lora_block_rows(M, n_adapters);
-  const int64_t steps = (K + 63) / 64;
-  int64_t want = 256 / blocks;                     // about a block per compute unit
-  if (want > steps / kShrinkWaves) want = steps / kShrinkWaves;   // a step per wave at least
-  if (want > kLoraMaxSplit) want = kLoraMaxSplit;
-  return want < 1 ? 1 : (int)want;
+// Parts that K may be split into: a step per wave at least.
+static int64_t lora_max_split(int64_t K) {
+  const int64_t want = (K + 63) / 64 / kShrinkWaves;
+  return want < 1 ? 1 : want > kLoraMaxSplit ? kLoraMaxSplit : want;
 }
 
+static int lora_ksplit(int64_t M, int64_t K, int64_t n_adapters) {
+  const int64_t blocks = lora_planned(M) ? (M + kLoraTile - 1) / kLoraTile : lora_block_rows(M, n_adapters);
+  const int64_t want = 256 / blocks, most = lora_max_split(K);   // about a block per compute unit
+  return want < 1 ? 1 : (int)(want < most ? want : most);
+}
+
+// The K parts of h, for M rows or any fewer (the split falls as the rows grow):
+// from 512 rows on 256 / (M / 64) parts of M rows, 16384 rows in all, or one.
 static size_t lora_h_bytes(int64_t M, int64_t K, int64_t n_adapters, int64_t R) {
-  return n_adapters ? align_up((size_t)lora_ksplit(M, K, n_adapters) * (size_t)M * (size_t)R * 4, 256) : 0;
+  if (!n_adapters) return 0;
+  int64_t rows = M * lora_max_split(K);
+  const int64_t all = 256 * kLoraTile;
+  if (lora_planned(M) && rows > all) rows = M > all ? M : all;
+  return align_up((size_t)rows * (size_t)R * 4, 256);
 }
 
 size_t lora_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R) {
