@@ -136,7 +136,8 @@ const char* awq_status_str(awq_status st);
 
 /* Workspace bytes a call needs for the given sizes (0 if it needs none), for
  * every group size.  Arguments that an op does not use are ignored.  For the
- * routed products and the adapters the bytes for M serve every smaller M too. */
+ * routed products and the adapters the bytes for M serve every smaller M too,
+ * and an M, N, K, T or n_alpha past what the calls accept gives 0. */
 size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T, int n_alpha);
 
 /*

@@ -1178,6 +1178,19 @@ def test_workspace_of_the_largest_batch_serves_all(op, N, K, T, n):
     assert need == sorted(need)
 
 
+@pytest.mark.parametrize("op", ["EXPERTS_UP", "EXPERTS_DOWN", "LORA"])
+def test_workspace_of_sizes_past_the_limits(op):
+    """Answers at once, with 0, whatever the sizes; a call with them is refused."""
+    most = (1 << 63) - 1
+    fine = (40, 64, 128, 8, 8)
+    for at, values in enumerate(((most, (1 << 24) + 1), (most,), (most, (1 << 17) + 1), (most, 8193),
+                                 ((1 << 31) - 1, 1 << 30, 257))):
+        for v in values:
+            args = list(fine)
+            args[at] = v
+            assert awq.awq_workspace_bytes(getattr(awq._abi, "AWQ_OP_" + op), *args) == 0, args
+
+
 def test_binding_refuses_host_tensors_and_wrong_names():
     x = torch.zeros(2, 64)
     ids = torch.zeros(2, 1, dtype=torch.int32)

@@ -50,8 +50,13 @@ size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T
     case AWQ_OP_EXPERTS_UP:
     case AWQ_OP_EXPERTS_DOWN:
       if (M < 1 || N < 1 || K < 1 || T < 1 || n_alpha < 1) return 0;
+      if (T > AWQ_MAX_EXPERTS || n_alpha > AWQ_MAX_TOP_K || M > awq::kMaxRows || K > AWQ_MAX_K ||
+          N > ((int64_t)1 << 32) / K)
+        return 0;
       return awq::experts_ws_bytes(op == AWQ_OP_EXPERTS_DOWN, M, N, K, T, n_alpha);
-    case AWQ_OP_LORA: return awq::lora_ws_bytes(M, N, K, T, n_alpha);
+    case AWQ_OP_LORA:
+      if (M > awq::kMaxRows || N > UINT32_MAX || K > AWQ_MAX_K || T > awq::kMaxAdapters || n_alpha > AWQ_MAX_RANK) return 0;
+      return awq::lora_ws_bytes(M, N, K, T, n_alpha);
   }
   return 0;
 }

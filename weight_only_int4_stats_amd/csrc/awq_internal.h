@@ -93,6 +93,10 @@ hipError_t launch_skinny_st_chunked(const void* x, int xdt, int64_t M, int64_t K
                                     int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
                                     hipStream_t st);
 
+// ---- limits of the operators whose weight depends on the row -------------------
+constexpr int64_t kMaxRows = (int64_t)1 << 24;       // slots, or rows with adapters
+constexpr int64_t kMaxAdapters = 8192;               // the sort's three tables in LDS: 96 KB
+
 // ---- expert routing (k_route.hip) --------------------------------------------
 hipError_t launch_route(const void* logits, int dt, int64_t T, int64_t E, int64_t ldl, const float* bias,
                         int sigmoid, int n_group, int topk_group, int group_top, int top_k, int renorm,

@@ -15,8 +15,8 @@ uintptr_t bytes_of(awq_dtype d) { return d == AWQ_F32 ? 4 : 2; }
 bool group_ok(int g) { return g == 64 || g == 128 || g == 256; }
 awq_status from_hip(hipError_t e) { return e == hipSuccess ? AWQ_OK : AWQ_ERR_HIP; }
 
-constexpr int64_t kMaxRows = (int64_t)1 << 24;       // slots, or rows with adapters
-constexpr int64_t kMaxAdapters = 8192;               // the sort's three tables in LDS: 96 KB
+using awq::kMaxAdapters;
+using awq::kMaxRows;
 constexpr int64_t kMaxThreads = 0xFFFFFFFF;          // of a launch
 
 awq_status experts(int mode, const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx, const int32_t* ids,
