@@ -1191,6 +1191,16 @@ def test_workspace_of_sizes_past_the_limits(op):
             assert awq.awq_workspace_bytes(getattr(awq._abi, "AWQ_OP_" + op), *args) == 0, args
 
 
+def test_lora_one_launch_only_where_it_reads_little():
+    """A call without a workspace forms A x again in every block: not where many
+    rows would read A and x a gigabyte over."""
+    ws = lambda M, N, K, L, R: awq.awq_workspace_bytes(awq.AWQ_OP_LORA, M, N, K, L, R)  # noqa: E731
+    for sizes in ((1, 4096, 4096, 8, 16), (8, 1024, 4096, 8, 16), (32, 4096, 1024, 1, 8), (1, 11008, 1024, 1, 64)):
+        assert ws(*sizes) == 0, sizes
+    for sizes in ((512, 16384, 4096, 1, 16), (512, 8192, 4096, 1, 32), (400, 4096, 4096, 3, 32), (512, 4096, 1024, 40, 8)):
+        assert ws(*sizes) > 0, sizes
+
+
 def test_binding_refuses_host_tensors_and_wrong_names():
     x = torch.zeros(2, 64)
     ids = torch.zeros(2, 1, dtype=torch.int32)
