@@ -112,9 +112,14 @@ __device__ __forceinline__ void merge_keys_dpp(uint32_t& a1, uint32_t& a2) {
 }
 
 // exp(d + dl) within 2^-21 of the value (dl: the rounding error of d), and
-// within 2^-100 of it where d was held to -100 .. 80.
+// within 2^-100 of it where d was held to -100 .. 80: 2^(d log2 e), the product
+// in two floats.  log2 e = kL + kLl (1 / ln 2 = 1.44269504088896340736,
+// its nearest float and the nearest float to the rest, 1.92596299e-8: the
+// splitting of a constant in two parts of Cody and Waite, Software Manual for
+// the Elementary Functions, 1980).
 __device__ __forceinline__ float exp_f32(float d, float dl) {
-  constexpr float kL = 0x1.715476p+0f, kLl = 0x1.4ae0bep-26f;   // log2(e) = kL + kLl
+  constexpr double kLog2e = 1.44269504088896340736;
+  constexpr float kL = (float)kLog2e, kLl = (float)(kLog2e - (double)kL);
   const bool in = d > -100.0f && d < 80.0f;
   d = in ? d : d > 0.0f ? 80.0f : -100.0f;
   dl = in ? dl : 0.0f;
