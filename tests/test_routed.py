@@ -3,6 +3,7 @@ awq_w4a16_experts_up / _down, awq_lora_add) against float64, and what they
 refuse."""
 import ctypes
 import math
+import types
 
 import numpy as np
 import pytest
@@ -1216,6 +1217,22 @@ def test_binding_refuses_host_tensors_and_wrong_names():
         awq.awq_w4a16_experts_down(x.half(), ids, torch.zeros(2, 1), *w, group_size=64)
     with pytest.raises(ValueError):
         awq.awq_lora_add(x.half(), ids[:, 0], torch.zeros(1, 8, 64).half(), torch.zeros(1, 4, 8).half())
+
+
+@pytest.mark.gpu
+def test_a_stream_of_another_gpu_is_refused(on_gpu):
+    """It would not order the call's work, which runs where its tensors are."""
+    other = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 7))
+    x = gpu(acts(3, 128, torch.float16, 1))
+    ids = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    w = packed(stack(2, 16, 128, 128, 1))
+    a, b = (torch.zeros(s, dtype=torch.float16, device="cuda") for s in ((2, 8, 128), (2, 16, 8)))
+    for call in (lambda: awq.awq_route_experts(x, 2, stream=other), lambda: awq.awq_w4a16_experts_up(x, ids, *w, stream=other),
+                 lambda: awq.awq_w4a16_experts_down(x, ids[:, :1].contiguous(), torch.ones((3, 1), device="cuda"), *w, stream=other),
+                 lambda: awq.awq_lora_add(x, ids[:, 0].contiguous(), a, b, stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    awq.awq_route_experts(x, 2, stream=torch.cuda.Stream())
 
 
 @pytest.mark.gpu

@@ -329,6 +329,8 @@ def _on_stream(stream, t: torch.Tensor):
     """Makes a given stream (or its handle) the current one, so that outputs
     and workspaces made for the call belong to it."""
     _dev(t, "the first tensor")
+    if getattr(stream, "device", t.device) != t.device:
+        raise ValueError(f"stream must belong to {t.device}, where the tensors are")
     if not isinstance(stream, torch.cuda.Stream):
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         stream = torch.cuda.ExternalStream(raw, t.device) if raw else torch.cuda.default_stream(t.device)
