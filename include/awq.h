@@ -435,7 +435,8 @@ awq_status awq_route_experts(const void* logits, awq_dtype ldt, int64_t T, int64
  *         others are not read into the result
  * with W_e[n][k] = step (q - z) as in awq_w4a16_gemm.  Products of the exact
  * integers q - z with the activations (as fp16 scaled by an exact power of
- * two) are summed in fp32 per group and scaled by the group's step in fp32;
+ * two per row; bf16 values below 2^-28 of the row's largest finite one lose
+ * bits) are summed in fp32 per group and scaled by the group's step in fp32;
  * the activation function and the sum over j run in fp32 and the output is
  * rounded once.  1/s is expected folded (awq_fold_scales): into the producer of
  * x for up, into the up half's rows for down.
@@ -471,8 +472,8 @@ awq_status awq_w4a16_experts_down(const void* x, awq_dtype xdt, int64_t M, int64
  * and y[m] = base[m] for rows whose adapter is outside [0, n_adapters)
  * (base == NULL: 0 in both).  base may be y itself (in place).  Sums and the
  * intermediate A x are held in fp32 (the latter enters the second product as
- * the sum of two fp16 or three bf16 values); the output is rounded once.  What A and B hold past an adapter's rank is not
- * used, whatever it is.
+ * the sum of two fp16 or three bf16 values); the output is rounded once.  What
+ * A and B hold past an adapter's rank is not used, whatever it is.
  *
  *   x        [M][ldx] fp16 or bf16 (xdt), K a multiple of 8, <= AWQ_MAX_K
  *   adapter  [M] int32

@@ -1,6 +1,5 @@
 // Routed W4A16 products for many rows per expert (include/awq.h,
-// awq_w4a16_experts_up / _down): prefills, where the matrix cores bound the
-// product.
+// awq_w4a16_experts_up / _down): prefills, whose floor is the matrix cores'.
 //
 //   z[slot][n] = sum_g D[n][g] sum_{k in g} (q[n][k] - z[n][g]) x[row(slot)][k]
 //
@@ -21,17 +20,18 @@
 //    unit a group) and the epilogue by the last step.  So no operand is
 //    rounded, unlike step (q - z) in fp16 (1e-4 of every result), and no second
 //    set of accumulators is needed.  Unpacking costs 9 vector instructions per eight codes; a wave's
-//    tile is tall (128 rows) because they serve all of its rows: with 64 x 64
-//    tiles per wave the vector instructions, not the matrix cores, set the time.
+//    tile is tall (128 rows) because they serve all of its rows: tiles of 64 rows
+//    take twice as many per product (times at gemm_tile_rows).
 //  * With SwiGLU a tile's columns alternate 16 gate rows and their 16 up rows,
 //    so both meet in one lane.  down writes an fp32 row per slot; the weighted
 //    sum over a token's slots is k_experts_combine's.  (fp16 rows, scaled by a
 //    power of two per 64 columns, halve the bytes between the two, 218 instead
 //    of 257 us a call for 4096 tokens, 8 of 64 experts, 1024 -> 2048, but they
 //    round every term to 2^-11 of itself and more beside a large one.)
-//  * 2048 tokens, 2 of 8 experts, 4096 -> 2 x 11008: 715 to 740 us a call (18 of
-//    them the preparation), 0.94 to 0.97 PFLOP/s where a large library product
-//    reaches 1.35; the clock settles under the load.
+//  * 2048 tokens, 2 of 8 experts, 4096 -> 2 x 11008: 700 to 740 us a call (18 of
+//    them the preparation), 0.94 to 0.99 PFLOP/s where a large library product
+//    reaches 1.35.  Neither pipe is full: the matrix pipe is busy 48 % of the
+//    cycles (33 % at K = 1024), with 3.6 other vector instructions per product.
 //  * The tiles of one expert are ordered 8 row tiles at a time, rows fastest,
 //    and each L2 slice takes a contiguous eighth of the order.
 #include "awq_device.h"

@@ -12,8 +12,8 @@
 // the blocks' parts in their order.
 //
 // 4096 rows of 6 adapters (rank 32, 4096 -> 4096, 16-bit base and output): plan
-// 7.5, shrink 13, expand 22 us, which a plain copy of base would take 17.5 of;
-// 64 rows of 32 adapters (rank up to 64, 4096 -> 11008): shrink 7, expand 15
+// 7.5, shrink 12, expand 22 us, which a plain copy of base would take 17.5 of;
+// 64 rows of 32 adapters (rank up to 64, 4096 -> 11008): shrink 8, expand 15
 // us, a chain of dependent loads (index, rank, h, base) at 2 TB/s of B.
 #include "awq_device.h"
 #include "awq_internal.h"

@@ -16,8 +16,8 @@
 // choice's float error is far below the distance that two neighbours in the
 // order must have.  A row with a closer call (about one in a hundred) repeats it in
 // doubles.  16384 tokens, 256 experts in 8 groups, top 8 with a bias: 29 us
-// in doubles alone, 23 to 25 us with both
-// (issue bound: some thirty instructions per winner, and the scores).
+// in doubles alone, 23 to 25 us with both: a winner takes some thirty
+// instructions, six of them steps across the lanes, for the wave's one token.
 #include "awq_device.h"
 #include "awq_internal.h"
 
