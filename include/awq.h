@@ -447,7 +447,8 @@ awq_status awq_route_experts(const void* logits, awq_dtype ldt, int64_t T, int64
  *   E         1 .. AWQ_MAX_EXPERTS
  *   K         a multiple of group_size (64, 128 or 256), <= AWQ_MAX_K
  *   N         up with AWQ_ACT_SWIGLU: even
- *   y         up: [M top_k][ldy], down: [M][ldy], F16, BF16 or F32 (ydt)
+ *   y         up: [M top_k][ldy], down: [M][ldy], F16, BF16 or F32 (ydt);
+ *             its rows share no memory with x's (AWQ_ERR_UNSUPPORTED)
  *   ws        >= awq_workspace_bytes(AWQ_OP_EXPERTS_UP or _DOWN, M, N, K, E, top_k)
  * M == 0 or N == 0 is a no-op.  More than 2^24 slots, 2^31 or more bytes in
  * one expert's packed words or in the activations as packed fp16 rows, or
@@ -481,7 +482,9 @@ awq_status awq_w4a16_experts_down(const void* x, awq_dtype xdt, int64_t M, int64
  *   R        a multiple of 8, 8 .. AWQ_MAX_RANK
  *   ranks    [n_adapters] int32 (values are held to 0 .. R) or NULL
  *   scaling  [n_adapters] float or NULL (1)
- *   base     [M][ldb] of ydt or NULL;  y [M][ldy] F16, BF16 or F32 (ydt)
+ *   base     [M][ldb] of ydt or NULL;  y [M][ldy] F16, BF16 or F32 (ydt); its
+ *            rows share no memory with x's, nor with base's unless y is base
+ *            with the same ld (AWQ_ERR_UNSUPPORTED)
  *   ws       >= awq_workspace_bytes(AWQ_OP_LORA, M, N, K, n_adapters, R)
  * M == 0 or N == 0 is a no-op; with n_adapters == 0 every row is base.
  * More than 2^24 rows, 8192 adapters, or outputs for 2^32 threads (some 2^37

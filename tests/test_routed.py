@@ -1202,6 +1202,64 @@ def test_lora_one_launch_only_where_it_reads_little():
         assert ws(*sizes) > 0, sizes
 
 
+def test_outputs_over_inputs_are_refused():
+    """Other blocks still read what one writes."""
+    at = lambda n: ctypes.c_void_p((1 << 24) + n)  # noqa: E731
+    far, far2 = ctypes.c_void_p(1 << 40), ctypes.c_void_p(1 << 41)
+    lib = awq.lib()
+
+    def lora(y, base=None, ldb=0, M=4, ldy=512, N=64):
+        return lib.awq_lora_add(at(0), 0, M, 256, 512, far, far, far, 2, 16, None, None, base, ldb, N, y, 0, ldy, far, 1 << 40, None)
+
+    def up(y, M=4, ldy=512):
+        return lib.awq_w4a16_experts_up(at(0), 0, M, 256, 512, far, 1, far, far, far, 8, 64, 128, 0, y, 0, ldy, far, 1 << 40, None)
+
+    def down(y, M=4, ldy=512):
+        return lib.awq_w4a16_experts_down(at(0), 0, M, 256, 512, far, far, 1, far, far, far, 8, 64, 128, y, 0, ldy, far, 1 << 40, None)
+
+    for f in (lora, up, down):
+        # x: rows of 512 bytes every 1024; y: rows of 128 bytes
+        for n in (0, 510, -126, 1024, 3 * 1024 + 510, -3 * 1024 - 126):
+            assert f(at(n)) == 5, (f, n)
+        assert f(at(600), ldy=64) == 5 and f(at(400), M=1, ldy=64) == 5
+    # base: 64 columns every 512 elements at far2
+    over = lambda n: ctypes.c_void_p((1 << 41) + n)  # noqa: E731
+    for y, ldy in ((over(2), 512), (over(126), 512), (over(1024), 512), (over(-2), 512), (over(0), 520), (over(0), 64)):
+        assert lora(y, far2, 512, ldy=ldy) == 5, (y, ldy)
+
+
+@pytest.mark.gpu
+def test_outputs_between_the_rows_of_inputs(on_gpu):
+    """Columns of one buffer beside each other, and the rows before and after."""
+    M, K, N, L = 40, 256, 72, 3
+    rng = np.random.default_rng(1)
+    buf = torch.zeros((M + 20, K + 2 * N + 8), dtype=torch.float16, device="cuda")
+    x = acts(M, K, torch.float16, 5)
+    xs = buf[10:M + 10, N:N + K]
+    xs.copy_(gpu(x))
+    w = stack(L, N, K, 128, 2)
+    ids = choices(M, L, 1, 3, "")
+    gi, weights = gpu(torch.from_numpy(ids)), rng.uniform(0, 1, (M, 1)).astype(np.float32)
+    a = torch.from_numpy(rng.normal(0, 0.1, (L, 16, K))).half()
+    b = torch.from_numpy(rng.normal(0, 1, (L, N, 16))).half()
+    for y in (buf[10:M + 10, :N], buf[10:M + 10, N + K:2 * N + K], buf[:M, :N], buf[20:, N + K + 8:]):
+        awq.awq_w4a16_experts_up(xs, gi, *packed(w), y=y)
+        check_up(x, ids, w, 128, "none", torch.float16, y, "up")
+        awq.awq_w4a16_experts_down(xs, gi, gpu(torch.from_numpy(weights)), *packed(w), y=y)
+        check_down(x, ids, weights, w, 128, torch.float16, y, "down")
+        base = y.cpu()
+        awq.awq_lora_add(xs, gi[:, 0].contiguous(), gpu(a), gpu(b), base=y, y=y)
+        check_lora(x, ids[:, 0], a, b, None, None, base, torch.float16, y, "adapters")
+    assert torch.equal(xs.cpu(), x)
+    for y in (xs[:, :N], buf[:M, N - 8:2 * N - 8], buf[:M, K:K + N]):
+        with pytest.raises(awq.AwqError):
+            awq.awq_w4a16_experts_up(xs, gi, *packed(w), y=y)
+        with pytest.raises(awq.AwqError):
+            awq.awq_lora_add(xs, gi[:, 0].contiguous(), gpu(a), gpu(b), y=y)
+    with pytest.raises(awq.AwqError):
+        awq.awq_lora_add(xs, gi[:, 0].contiguous(), gpu(a), gpu(b), base=buf[:M, :N], y=buf[1:M + 1, :N])
+
+
 def test_binding_refuses_host_tensors_and_wrong_names():
     x = torch.zeros(2, 64)
     ids = torch.zeros(2, 1, dtype=torch.int32)

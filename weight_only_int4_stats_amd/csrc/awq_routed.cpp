@@ -19,6 +19,20 @@ using awq::kMaxAdapters;
 using awq::kMaxRows;
 constexpr int64_t kMaxThreads = 0xFFFFFFFF;          // of a launch
 
+// Whether na rows of wa bytes, pa apart, from a and nb rows of wb, pb apart, from
+// b share a byte; rows of different distances: whether their extents meet.
+bool overlap(const void* a, int64_t na, int64_t wa, int64_t pa, const void* b, int64_t nb, int64_t wb, int64_t pb) {
+  const int64_t d = (int64_t)((intptr_t)b - (intptr_t)a);
+  if (d >= (__int128)(na - 1) * pa + wa || -d >= (__int128)(nb - 1) * pb + wb) return false;
+  if (na == 1) pa = pb;
+  if (nb == 1) pb = pa;
+  if (pa != pb || pa < wa || pa < wb) return true;
+  // b's row j starts r bytes into a's row j + q
+  const int64_t q = (d >= 0 ? d : d - (pa - 1)) / pa, r = d - q * pa;
+  auto rows_meet = [&](int64_t by) { return by < na && by + nb > 0; };
+  return (r < wa && rows_meet(q)) || (r + wb > pa && rows_meet(q + 1));
+}
+
 awq_status experts(int mode, const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx, const int32_t* ids,
                    const float* weights, int top_k, const int32_t* qweight, const uint16_t* scales,
                    const uint8_t* zeros, int64_t E, int64_t N, int group_size, void* y, awq_dtype ydt,
@@ -40,6 +54,8 @@ awq_status experts(int mode, const void* x, awq_dtype xdt, int64_t M, int64_t K,
     return AWQ_ERR_ALIGN;
   const size_t need = awq::experts_ws_bytes(down, M, N, K, E, top_k);
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return AWQ_ERR_WORKSPACE;
+  const int64_t slots = M * top_k, ob = (int64_t)bytes_of(ydt);
+  if (overlap(x, down ? slots : M, K * 2, ldx * 2, y, down ? M : slots, cols * ob, ldy * ob)) return AWQ_ERR_UNSUPPORTED;
   const awq::ExpertsCall c{mode, (const uint16_t*)x, (int)xdt, M, K, ldx, ids, weights, top_k,
                            (const uint32_t*)qweight, scales, zeros, E, N, group_size, y, (int)ydt, ldy};
   return from_hip(awq::launch_experts(c, ws, (hipStream_t)stream));
@@ -105,6 +121,11 @@ awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int6
   if (N > kMaxThreads || awq::lora_threads(M, N, K, n_adapters, R) > kMaxThreads) return AWQ_ERR_UNSUPPORTED;
   const size_t need = awq::lora_ws_bytes(M, N, K, n_adapters, R);
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return AWQ_ERR_WORKSPACE;
+  const int64_t ob = (int64_t)bytes_of(ydt);
+  const bool in_place = base == y && (ldb == ldy || M == 1);
+  if ((n_adapters > 0 && overlap(x, M, K * 2, ldx * 2, y, M, N * ob, ldy * ob)) ||
+      (base && !in_place && overlap(base, M, N * ob, ldb * ob, y, M, N * ob, ldy * ob)))
+    return AWQ_ERR_UNSUPPORTED;
   const awq::LoraCall c{(const uint16_t*)x, (int)xdt, M, K, ldx, adapter, (const uint16_t*)a, (const uint16_t*)b,
                         n_adapters, R, ranks, scaling, base, ldb, N, y, (int)ydt, ldy};
   return from_hip(awq::launch_lora(c, ws, (hipStream_t)stream));
