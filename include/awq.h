@@ -39,6 +39,16 @@
  *                          experts
  *   awq_lora_add           each row's low-rank adapter, added to the output
  *                          of the shared product
+ * The rest of a pre-norm block around the packed linears, and the gradients of
+ * what stays in full precision there while the packed weights are frozen (the
+ * norms, the biases, the router's gate):
+ *   awq_w4a16_linear          the product with bias, activation and residual
+ *                             in its epilogue
+ *   awq_bias_act_backward     the epilogue's backward pass
+ *   awq_w4a16_gemm_dx         the gradient of the product's input
+ *   awq_layer_norm, awq_layer_norm_backward   layer and RMS norm
+ *   awq_balance_loss, awq_balance_loss_backward   a router's balance loss and
+ *                             its experts' slot counts
  * Linears that read the same input (q, k and v; gate and up) are searched
  * together by passing their row-concatenated W to awq_search_scales: they then
  * share s, and one fold serves them all.
@@ -105,7 +115,12 @@ typedef enum awq_op {
   AWQ_OP_GEMM = 3,
   AWQ_OP_EXPERTS_UP = 4,    /* M tokens, T = experts, n_alpha = top_k             */
   AWQ_OP_EXPERTS_DOWN = 5,  /* the same                                           */
-  AWQ_OP_LORA = 6           /* M rows, T = adapters, n_alpha = rank               */
+  AWQ_OP_LORA = 6,          /* M rows, T = adapters, n_alpha = rank               */
+  AWQ_OP_LINEAR = 7,        /* M, N, K                                            */
+  AWQ_OP_BIAS_ACT_BACKWARD = 8,    /* M, N                                        */
+  AWQ_OP_GEMM_DX = 9,       /* M, N, K                                            */
+  AWQ_OP_LAYER_NORM_BACKWARD = 10, /* M, K                                        */
+  AWQ_OP_BALANCE_LOSS = 11  /* M tokens, T = experts                              */
 } awq_op;
 
 /* Scores of awq_route_experts. */
@@ -114,10 +129,15 @@ typedef enum awq_score {
   AWQ_SCORE_SIGMOID = 1
 } awq_score;
 
-/* Epilogue of awq_w4a16_experts_up. */
+/* Activations: AWQ_ACT_SWIGLU is the epilogue of awq_w4a16_experts_up, the ones
+ * after it those of awq_w4a16_linear; AWQ_ACT_NONE serves both. */
 typedef enum awq_act {
   AWQ_ACT_NONE = 0,
-  AWQ_ACT_SWIGLU = 1        /* silu(first half of the rows) * second half         */
+  AWQ_ACT_SWIGLU = 1,       /* silu(first half of the rows) * second half         */
+  AWQ_ACT_RELU = 2,         /* max(z, 0)                                          */
+  AWQ_ACT_GELU = 3,         /* z (1 + erf(z / sqrt 2)) / 2                        */
+  AWQ_ACT_GELU_TANH = 4,    /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2  */
+  AWQ_ACT_SILU = 5          /* z / (1 + exp(-z))                                  */
 } awq_act;
 
 #define AWQ_GROUP 128           /* the usual group size; 64 and 256 are accepted too */
@@ -135,9 +155,9 @@ int awq_abi_version(void);
 const char* awq_status_str(awq_status st);
 
 /* Workspace bytes a call needs for the given sizes (0 if it needs none), for
- * every group size.  Arguments that an op does not use are ignored.  For the
- * routed products and the adapters the bytes for M serve every smaller M too,
- * and an M, N, K, T or n_alpha past what the calls accept gives 0. */
+ * every group size.  Arguments that an op does not use are ignored.  From
+ * AWQ_OP_EXPERTS_UP on the bytes for M serve every smaller M too, and an M, N,
+ * K, T or n_alpha past what the calls accept gives 0. */
 size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T, int n_alpha);
 
 /*
@@ -496,6 +516,165 @@ awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int6
                         int64_t R, const int32_t* ranks, const float* scaling, const void* base,
                         int64_t ldb, int64_t N, void* y, awq_dtype ydt, int64_t ldy, void* ws,
                         size_t ws_bytes, void* stream);
+
+/*
+ * The fused W4A16 product with an epilogue: with W = step (q - z) as in
+ * awq_w4a16_gemm
+ *   z[m][n] = sum_k W[n][k] x[m][k] + bias[n]
+ *   y[m][n] = act(z[m][n]) + residual[m][n]
+ * bias == NULL, residual == NULL: 0.  1/s is expected folded (awq_fold_scales).
+ * pre, if not NULL, receives z: what awq_bias_act_backward needs of the
+ * forward pass.  The sum, the bias, the activation and the residual are held
+ * in fp32 and y (and pre) rounded once.  The sum itself is formed as in
+ * awq_w4a16_gemm: products of the exact integers q - z for one token and for
+ * the shapes of up to 16 tokens that one launch stages, else of the
+ * dequantized weights rounded once to fp16 (an F32 y shows that rounding).
+ * Activations as fp16 under exact powers of two: bf16 values below 2^-28 of
+ * the largest they share one with lose bits.
+ *
+ *   x         [M][ldx] fp16 or bf16 (xdt), finite
+ *   qweight, scales, zeros  as written by awq_quantize_pack (steps of any sign)
+ *   bias      [N] of bdt (F16, BF16 or F32) or NULL
+ *   act       AWQ_ACT_NONE, _RELU, _GELU, _GELU_TANH or _SILU
+ *   residual  [M][ldr] of ydt or NULL; it may be y itself (in place)
+ *   pre       [M][ldp] of ydt or NULL
+ *   y         [M][ldy] F16, BF16 or F32 (ydt)
+ *   ws        >= awq_workspace_bytes(AWQ_OP_LINEAR, M, N, K, 0, 0)
+ * Rows of y and pre share no memory with x's, with each other or with
+ * residual's, but for residual == y with the same ld (AWQ_ERR_UNSUPPORTED).
+ * M == 0 or N == 0 is a no-op.  More than 2^24 rows, N above
+ * AWQ_MAX_LINEAR_N, N K above 2^33, or tiles for 2^32 threads ->
+ * AWQ_ERR_UNSUPPORTED.
+ */
+#define AWQ_MAX_LINEAR_N 4194304
+awq_status awq_w4a16_linear(const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                            const int32_t* qweight, const uint16_t* scales, const uint8_t* zeros,
+                            int64_t N, int group_size, const void* bias, awq_dtype bdt, awq_act act,
+                            const void* residual, int64_t ldr, void* pre, int64_t ldp, void* y,
+                            awq_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward pass of awq_w4a16_linear's epilogue (the residual's gradient is dy):
+ *   dz[m][n]  = dy[m][n] act'(pre[m][n])
+ *   dbias[n]  = sum_m of the dz before its rounding
+ * in fp32, dz rounded once.  relu' is 0 at 0.  With AWQ_ACT_NONE dz is dy: pre
+ * and dz are not used, and dbias alone is formed.
+ *
+ *   dy, pre, dz  [M][ld] of one type dt (F16, BF16 or F32); dz may be dy or pre
+ *                itself (in place)
+ *   dbias     [N] float or NULL
+ *   ws        >= awq_workspace_bytes(AWQ_OP_BIAS_ACT_BACKWARD, M, N, 0, 0, 0);
+ *             not used without dbias
+ * M == 0 gives dbias = 0; N == 0 is a no-op.
+ */
+awq_status awq_bias_act_backward(const void* dy, awq_dtype dt, int64_t M, int64_t N, int64_t lddy,
+                                 const void* pre, int64_t ldp, awq_act act, void* dz, int64_t lddz,
+                                 float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The gradient of the W4A16 product's input, the packed weights contracted over
+ * their rows:
+ *   dx[m][k] = sum_n dz[m][n] step[n][k/g] (q[n][k] - z[n][k/g])
+ * dz enters as fp16 under an exact power of two per row of dz and per row of
+ * the weights (values below 2^-28 of the largest of a row of dz, each times its
+ * weights' power, lose bits), the dequantized weights are rounded once to fp16,
+ * the sum is held in fp32 and dx rounded once.
+ *
+ *   dz        [M][lddz] fp16 or bf16 (dzt)
+ *   qweight, scales, zeros  as written by awq_quantize_pack (steps of any sign)
+ *   dx        [M][lddx] F16, BF16 or F32 (dxt); its rows share no memory with
+ *             dz's (AWQ_ERR_UNSUPPORTED)
+ *   ws        >= awq_workspace_bytes(AWQ_OP_GEMM_DX, M, N, K, 0, 0)
+ * M == 0 is a no-op, N == 0 gives dx = 0.  Sizes as awq_w4a16_linear's.
+ */
+awq_status awq_w4a16_gemm_dx(const void* dz, awq_dtype dzt, int64_t M, int64_t N, int64_t lddz,
+                             const int32_t* qweight, const uint16_t* scales, const uint8_t* zeros,
+                             int64_t K, int group_size, void* dx, awq_dtype dxt, int64_t lddx,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Layer norm of each row, or RMS norm: the producer of x into whose weight and
+ * bias awq_fold_scales folds 1/s.
+ *   mean = sum_k x_k / K  (rms != 0: 0),  rstd = 1 / sqrt(sum_k (x_k - mean)^2 / K + eps)
+ *   y_k  = (x_k - mean) rstd weight_k + bias_k          (bias == NULL: 0)
+ * in fp32, the variance from the centred values; y rounded once.
+ *
+ *   x         [M][ldx] F16, BF16 or F32 (xdt), 1 <= K <= AWQ_MAX_K
+ *   weight    [K] of wdt, bias [K] of bdt (any of the three) or NULL
+ *   eps       >= 0, finite
+ *   y         [M][ldy] of ydt (any of the three); it may be x itself (in place)
+ *   mean, rstd  [M] float, for the backward pass; either may be NULL (mean is
+ *             written as 0 for RMS)
+ * Every pointer is aligned to its element only.  M == 0 is a no-op.  More than
+ * 2^24 rows (2^22 - 1 of more than 8192 values) -> AWQ_ERR_UNSUPPORTED.
+ */
+awq_status awq_layer_norm(const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                          const void* weight, awq_dtype wdt, const void* bias, awq_dtype bdt,
+                          float eps, int rms, void* y, awq_dtype ydt, int64_t ldy, float* mean,
+                          float* rstd, void* stream);
+
+/*
+ * Backward pass of awq_layer_norm: with xh = (x - mean) rstd and a = dy weight
+ *   dx      = rstd (a - (sum a) / K - xh (sum a xh) / K)     (RMS: without sum a)
+ *   dweight = sum over the rows of dy xh,  dbias = sum over the rows of dy
+ * in fp32, dx rounded once to x's type; the sums over the rows in a fixed order.
+ *
+ *   dy        [M][lddy] of dyt, x [M][ldx] and dx [M][lddx] of xdt
+ *   mean, rstd  [M] float, from the forward pass (mean is not used for RMS)
+ *   dx        may be dy or x itself (in place)
+ *   dweight, dbias  [K] float; either may be NULL
+ *   ws        >= awq_workspace_bytes(AWQ_OP_LAYER_NORM_BACKWARD, M, 0, K, 0, 0);
+ *             not used without dweight and dbias
+ * M == 0 gives dweight = dbias = 0.  More than 2^24 rows -> AWQ_ERR_UNSUPPORTED.
+ */
+awq_status awq_layer_norm_backward(const void* dy, awq_dtype dyt, int64_t M, int64_t K, int64_t lddy,
+                                   const void* x, awq_dtype xdt, int64_t ldx, const void* weight,
+                                   awq_dtype wdt, const float* mean, const float* rstd, int rms,
+                                   void* dx, int64_t lddx, float* dweight, float* dbias, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/*
+ * A router's balance loss and its experts' slot counts, of awq_route_experts'
+ * logits and ids.  A token counts if its mask is not 0 (mask == NULL: all) and
+ * it has a usable logit (-inf and NaN are not usable, +inf is the largest
+ * float); T' tokens count.  For those
+ *   p_te     = exp(l_te) / sum_i exp(l_ti)            (AWQ_SCORE_SOFTMAX), or
+ *              sigma(l_te) / sum_i sigma(l_ti)        (AWQ_SCORE_SIGMOID)
+ *   counts_e = their slots whose id is e (ids outside [0, E) count for none;
+ *              a token that names an expert twice counts twice)
+ *   slope_e  = coef E counts_e / (n T'),  n = sum_e counts_e     (n == 0: 0)
+ *   loss     = sum_e slope_e sum_t p_te
+ * so an even routing has loss = coef, and slope_e is the derivative of the loss
+ * by each p_te (the counts are constants).  The p are formed in fp32, their
+ * sums over the tokens end in double; the order of every sum is fixed.
+ *
+ *   logits    [T][ldl] fp16, bf16 or f32 (ldt), aligned to its element
+ *   E         1 .. AWQ_MAX_EXPERTS;  ids [T][top_k] int32, top_k 1 .. AWQ_MAX_TOP_K
+ *   mask      [T] uint8 or NULL
+ *   loss      [1] float;  counts [E] int32;  slope [E] float
+ *   ws        >= awq_workspace_bytes(AWQ_OP_BALANCE_LOSS, T, 0, 0, E, 0)
+ * T == 0 (and no token that counts) gives zeros.  More than 2^24 tokens ->
+ * AWQ_ERR_UNSUPPORTED.
+ */
+awq_status awq_balance_loss(const void* logits, awq_dtype ldt, int64_t T, int64_t E, int64_t ldl,
+                            const int32_t* ids, int top_k, const uint8_t* mask, awq_score score,
+                            double coef, float* loss, int32_t* counts, float* slope, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * The gradient of awq_balance_loss's loss by the logits:
+ *   dlogits_te = grad p_te (slope_e - sum_i p_ti slope_i)      (AWQ_SCORE_SOFTMAX)
+ *                the same times 1 - sigma(l_te)                (AWQ_SCORE_SIGMOID)
+ * and 0 for tokens that do not count and for logits that are not usable.
+ *
+ *   logits, mask, score  as given to awq_balance_loss;  slope as it wrote it
+ *   grad      [1] float on the device, the gradient of the loss, or NULL (1)
+ *   dlogits   [T][ldd] of ldt; it may be logits itself (in place)
+ */
+awq_status awq_balance_loss_backward(const void* logits, awq_dtype ldt, int64_t T, int64_t E,
+                                     int64_t ldl, const float* slope, const float* grad,
+                                     const uint8_t* mask, awq_score score, void* dlogits,
+                                     int64_t ldd, void* stream);
 
 /* Diagnostic: a plain streaming read of `bytes` of device memory, the rate the
  * W4A16 products are measured against at their own sizes.  "AWQ Math",

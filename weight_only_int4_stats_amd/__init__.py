@@ -15,13 +15,17 @@ import functools
 import torch
 
 from . import _abi
-from ._abi import (AWQ_ACT_NONE, AWQ_ACT_SWIGLU, AWQ_BF16, AWQ_F16, AWQ_F32, AWQ_GROUP, AWQ_OP_ACT_STATS,  # noqa: F401
+from ._abi import (AWQ_ACT_GELU, AWQ_ACT_GELU_TANH, AWQ_ACT_NONE, AWQ_ACT_RELU, AWQ_ACT_SILU, AWQ_ACT_SWIGLU,  # noqa: F401
+                   AWQ_BF16, AWQ_F16, AWQ_F32, AWQ_GROUP, AWQ_OP_ACT_STATS, AWQ_OP_BALANCE_LOSS,
+                   AWQ_OP_BIAS_ACT_BACKWARD, AWQ_OP_GEMM_DX, AWQ_OP_LAYER_NORM_BACKWARD, AWQ_OP_LINEAR,
                    AWQ_OP_EXPERTS_DOWN, AWQ_OP_EXPERTS_UP, AWQ_OP_GEMM, AWQ_OP_LORA, AWQ_OP_QUANTIZE,
                    AWQ_OP_SEARCH, AWQ_SCORE_SIGMOID, AWQ_SCORE_SOFTMAX, AwqError, lib)
 
 __all__ = ["awq_act_stats", "awq_search_scales", "awq_search_scales_ex", "awq_quantize_pack", "awq_quantize_codes",
            "awq_w4a16_gemm", "awq_w4a16_gemm_noalloc", "awq_read_stream", "awq_fold_scales", "awq_salient_channels", "awq_workspace_bytes",
-           "awq_route_experts", "awq_w4a16_experts_up", "awq_w4a16_experts_down", "awq_lora_add", "AwqError", "lib"]
+           "awq_route_experts", "awq_w4a16_experts_up", "awq_w4a16_experts_down", "awq_lora_add",
+           "awq_w4a16_linear", "awq_bias_act_backward", "awq_w4a16_gemm_dx", "awq_layer_norm", "awq_layer_norm_backward",
+           "awq_balance_loss", "awq_balance_loss_backward", "AwqError", "lib"]
 
 _DT = {torch.float16: AWQ_F16, torch.bfloat16: AWQ_BF16, torch.float32: AWQ_F32}
 
@@ -482,3 +486,252 @@ def awq_lora_add(x: torch.Tensor, adapter: torch.Tensor, a: torch.Tensor, b: tor
              _same(ranks, "ranks", dev, torch.int32, (L,)), _same(scaling, "scaling", dev, torch.float32, (L,)),
              basep, ldb, N, y.data_ptr(), _DT.get(y.dtype, -1), ldy, wsp, wsb))
     return y
+
+
+# ---- operators of a block around the packed linears ------------------------------
+_LINEAR_ACTS = {"none": AWQ_ACT_NONE, "relu": AWQ_ACT_RELU, "gelu": AWQ_ACT_GELU, "gelu_tanh": AWQ_ACT_GELU_TANH,
+                "silu": AWQ_ACT_SILU}
+
+
+def _act_of(act: str) -> int:
+    if act not in _LINEAR_ACTS:
+        raise ValueError(f"act must be one of {sorted(_LINEAR_ACTS)}")
+    return _LINEAR_ACTS[act]
+
+
+def _vector(t: torch.Tensor | None, name: str, dev: int, n: int) -> tuple[int | None, int]:
+    """Address and type of a contiguous vector of n values of any of the three types (None: NULL)."""
+    if t is None:
+        return None, AWQ_F32
+    dt = _DT.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if dt is None or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} values (float16, bfloat16 or float32) on cuda:{dev}")
+    return t.data_ptr(), dt
+
+
+def _packed(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int, dev: int) -> tuple:
+    """(qweight, scales, zeros addresses, N, K) of one packed linear."""
+    if not isinstance(qweight, torch.Tensor) or qweight.dim() != 2:
+        raise ValueError("qweight must be [N, K/8]")
+    if group_size not in (64, 128, 256):
+        raise ValueError("group_size must be 64, 128 or 256")
+    N, words = qweight.shape
+    K = words * 8
+    groups = (N, K // group_size)
+    return (_same(qweight, "qweight", dev, torch.int32, qweight.shape), _same(scales, "scales", dev, torch.float16, groups),
+            _same(zeros, "zeros", dev, torch.uint8, groups), N, K)
+
+
+def _rows_like(t: torch.Tensor | None, name: str, dev: torch.device, dtype: torch.dtype, rows: int,
+               cols: int) -> tuple[int | None, int]:
+    """Address and row stride of an optional [rows, cols] tensor of dtype."""
+    if t is None:
+        return None, 0
+    t, ld = _out(t, name, dev, dtype, rows, cols)
+    return t.data_ptr(), ld
+
+
+def _mask(mask: torch.Tensor | None, dev: int, T: int) -> int | None:
+    if mask is None:
+        return None
+    return _same(mask, "mask", dev, torch.bool if isinstance(mask, torch.Tensor) and mask.dtype is torch.bool else torch.uint8, (T,))
+
+
+def awq_w4a16_linear(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                     bias: torch.Tensor | None = None, act: str = "none", residual: torch.Tensor | None = None,
+                     pre: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                     y: torch.Tensor | None = None, group_size: int = AWQ_GROUP, ws: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """act(x (dequant W)^T + bias) + residual, [M, N].
+
+    act: "none", "relu", "gelu" (erf), "gelu_tanh" or "silu"; bias [N] of any
+    type; residual [M, N] of the output's type, which may be y itself.  pre, an
+    [M, N] tensor of the output's type, receives the value before the
+    activation, for awq_bias_act_backward.  The output's type is out_dtype, or
+    y's, or residual's, or x's."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return awq_w4a16_linear(x, qweight, scales, zeros, bias, act, residual, pre, out_dtype, y, group_size, ws)
+    kind = _act_of(act)
+    M, K, ldx = _act_rows(x, "x")
+    device, dev = x.device, x.get_device()
+    qp, sp, zp, N, Kw = _packed(qweight, scales, zeros, group_size, dev)
+    if Kw != K:
+        raise ValueError("qweight must be [N, K/8]")
+    want = out_dtype or (residual.dtype if y is None and residual is not None else x.dtype if y is None else y.dtype)
+    y, ldy = _out(y, "y", device, want, M, N)
+    resp, ldr = _rows_like(residual, "residual", device, y.dtype, M, N)
+    prep, ldp = _rows_like(pre, "pre", device, y.dtype, M, N)
+    bp, bdt = _vector(bias, "bias", dev, N)
+    ws, wsp, wsb = _ws(AWQ_OP_LINEAR, device, ws, M, N, K, 0, 0)
+    _launch("awq_w4a16_linear", dev,
+            (x.data_ptr(), _DT.get(x.dtype, -1), M, K, ldx, qp, sp, zp, N, group_size, bp, bdt, kind, resp, ldr, prep, ldp,
+             y.data_ptr(), _DT.get(y.dtype, -1), ldy, wsp, wsb))
+    return y
+
+
+def awq_bias_act_backward(dy: torch.Tensor, pre: torch.Tensor | None = None, act: str = "none",
+                          dz: torch.Tensor | None = None, dbias: torch.Tensor | bool = True,
+                          ws: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Backward pass of awq_w4a16_linear's epilogue: (dz [M, N] of dy's type,
+    dbias float32 [N]).  pre is what the forward pass wrote there.  With act
+    "none" dz is dy itself; dbias=False leaves the bias's gradient out; dz may
+    be dy or pre."""
+    if stream is not None:
+        with _on_stream(stream, dy):
+            return awq_bias_act_backward(dy, pre, act, dz, dbias, ws)
+    kind = _act_of(act)
+    M, N, lddy = _act_rows(dy, "dy")
+    device, dev = dy.device, dy.get_device()
+    pp, ldp, dzp, lddz = None, 0, None, 0
+    if kind == AWQ_ACT_NONE:
+        if dz is not None and dz is not dy:
+            raise ValueError("with act \"none\" dz is dy itself")
+        dz = dy
+    else:
+        if pre is None:
+            raise ValueError("pre is needed where there is an activation")
+        pp, ldp = _rows_like(pre, "pre", device, dy.dtype, M, N)
+        dz, lddz = _out(dz, "dz", device, dy.dtype, M, N)
+        dzp = dz.data_ptr()
+    if isinstance(dbias, bool):
+        dbias = torch.empty(N, dtype=torch.float32, device=device) if dbias else None
+    dbp = _same(dbias, "dbias", dev, torch.float32, (N,))
+    wsp, wsb = None, 0
+    if dbias is not None:
+        ws, wsp, wsb = _ws(AWQ_OP_BIAS_ACT_BACKWARD, device, ws, M, N, 0, 0, 0)
+    if kind != AWQ_ACT_NONE or dbias is not None:
+        _launch("awq_bias_act_backward", dev,
+                (dy.data_ptr(), _DT.get(dy.dtype, -1), M, N, lddy, pp, ldp, kind, dzp, lddz, dbp, wsp, wsb))
+    return dz, dbias
+
+
+def awq_w4a16_gemm_dx(dz: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                      out_dtype: torch.dtype | None = None, dx: torch.Tensor | None = None, group_size: int = AWQ_GROUP,
+                      ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dz (dequant W), [M, K]: the gradient of the W4A16 product's input."""
+    if stream is not None:
+        with _on_stream(stream, dz):
+            return awq_w4a16_gemm_dx(dz, qweight, scales, zeros, out_dtype, dx, group_size, ws)
+    M, N, lddz = _act_rows(dz, "dz")
+    device, dev = dz.device, dz.get_device()
+    qp, sp, zp, Nw, K = _packed(qweight, scales, zeros, group_size, dev)
+    if Nw != N:
+        raise ValueError("qweight must have one row per column of dz")
+    dx, lddx = _out(dx, "dx", device, out_dtype if dx is not None else out_dtype or dz.dtype, M, K)
+    ws, wsp, wsb = _ws(AWQ_OP_GEMM_DX, device, ws, M, N, K, 0, 0)
+    _launch("awq_w4a16_gemm_dx", dev,
+            (dz.data_ptr(), _DT.get(dz.dtype, -1), M, N, lddz, qp, sp, zp, K, group_size, dx.data_ptr(),
+             _DT.get(dx.dtype, -1), lddx, wsp, wsb))
+    return dx
+
+
+def awq_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
+                   rms: bool = False, out_dtype: torch.dtype | None = None, y: torch.Tensor | None = None,
+                   stats: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """(x - mean) / sqrt(var + eps) * weight + bias of each row (rms: mean 0),
+    [M, K] of out_dtype (default x's).  weight and bias [K] of any type; y may
+    be x.  stats, a float32 [2, M] tensor, receives each row's mean and
+    1 / sqrt(var + eps), for awq_layer_norm_backward."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return awq_layer_norm(x, weight, bias, eps, rms, out_dtype, y, stats)
+    M, K, ldx = _act_rows(x, "x")
+    device, dev = x.device, x.get_device()
+    if weight is None:
+        raise ValueError("weight must be a vector")
+    wp, wdt = _vector(weight, "weight", dev, K)
+    bp, bdt = _vector(bias, "bias", dev, K)
+    y, ldy = _out(y, "y", device, out_dtype if y is not None else out_dtype or x.dtype, M, K)
+    sp = _same(stats, "stats", dev, torch.float32, (2, M))
+    _launch("awq_layer_norm", dev,
+            (x.data_ptr(), _DT.get(x.dtype, -1), M, K, ldx, wp, wdt, bp, bdt, eps, int(bool(rms)), y.data_ptr(),
+             _DT.get(y.dtype, -1), ldy, sp, None if sp is None else sp + 4 * M))
+    return y
+
+
+def awq_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, stats: torch.Tensor,
+                            rms: bool = False, bias: bool = True, dx: torch.Tensor | None = None,
+                            dweight: torch.Tensor | bool = True, ws: torch.Tensor | None = None, stream=None):
+    """Backward pass of awq_layer_norm: (dx [M, K] of x's type, dweight float32
+    [K], dbias float32 [K]).  stats as the forward pass wrote it.  bias=False
+    (a norm without a bias) and dweight=False leave those sums out (None);
+    tensors given for them receive them.  dx may be dy or x."""
+    if stream is not None:
+        with _on_stream(stream, dy):
+            return awq_layer_norm_backward(dy, x, weight, stats, rms, bias, dx, dweight, ws)
+    M, K, lddy = _act_rows(dy, "dy")
+    device, dev = dy.device, dy.get_device()
+    if x.device != device or x.shape != dy.shape:
+        raise ValueError(f"x must be a tensor of shape [{M}, {K}] on {device}")
+    _, _, ldx = _act_rows(x, "x")
+    if weight is None or stats is None:
+        raise ValueError("weight and stats must be tensors")
+    wp, wdt = _vector(weight, "weight", dev, K)
+    sp = _same(stats, "stats", dev, torch.float32, (2, M))
+    dx, lddx = _out(dx, "dx", device, x.dtype, M, K)
+    dbias = bias
+    if isinstance(dbias, bool):
+        dbias = torch.empty(K, dtype=torch.float32, device=device) if dbias else None
+    if isinstance(dweight, bool):
+        dweight = torch.empty(K, dtype=torch.float32, device=device) if dweight else None
+    wsp, wsb = None, 0
+    if dweight is not None or dbias is not None:
+        ws, wsp, wsb = _ws(AWQ_OP_LAYER_NORM_BACKWARD, device, ws, M, 0, K, 0, 0)
+    _launch("awq_layer_norm_backward", dev,
+            (dy.data_ptr(), _DT.get(dy.dtype, -1), M, K, lddy, x.data_ptr(), _DT.get(x.dtype, -1), ldx, wp, wdt, sp,
+             sp + 4 * M, int(bool(rms)), dx.data_ptr(), lddx, _same(dweight, "dweight", dev, torch.float32, (K,)),
+             _same(dbias, "dbias", dev, torch.float32, (K,)), wsp, wsb))
+    return dx, dweight, dbias
+
+
+def awq_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float = 1.0, score: str = "softmax",
+                     mask: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """The balance loss of a router: (loss float32 [1], counts int32 [E], slope
+    float32 [E]), loss = coef E sum_e (counts_e / n) mean_t p_te over the tokens
+    that count, slope its derivative by each p.
+
+    logits [T, E]; ids int32 [T, top_k] as awq_route_experts writes them; score
+    "softmax" or "sigmoid" (divided by the row's sum); mask (bool or uint8 [T]):
+    tokens with 0 do not count, nor do tokens whose logits are all -inf or NaN."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return awq_balance_loss(logits, ids, coef, score, mask, ws)
+    T, E, ldl = _act_rows(logits, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [tokens, top_k]")
+    device, dev = logits.device, logits.get_device()
+    top_k = ids.shape[1]
+    out = torch.empty(2 * E + 1, dtype=torch.float32, device=device)   # one allocation: slope, counts, loss
+    slope, counts, loss = out[:E], out[E:2 * E].view(torch.int32), out[2 * E:]
+    ws, wsp, wsb = _ws(AWQ_OP_BALANCE_LOSS, device, ws, T, 0, 0, E, 0)
+    _launch("awq_balance_loss", dev,
+            (logits.data_ptr(), _DT.get(logits.dtype, -1), T, E, ldl, _same(ids, "ids", dev, torch.int32, (T, top_k)),
+             top_k, _mask(mask, dev, T), _SCORES[score], coef, loss.data_ptr(), counts.data_ptr(), slope.data_ptr(),
+             wsp, wsb))
+    return loss, counts, slope
+
+
+def awq_balance_loss_backward(logits: torch.Tensor, slope: torch.Tensor, grad: torch.Tensor | None = None,
+                              score: str = "softmax", mask: torch.Tensor | None = None,
+                              dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of awq_balance_loss's loss by the logits, [T, E] of their
+    type.  slope as awq_balance_loss returned it, score and mask as given to it;
+    grad: float32 [1], the gradient of the loss (None: 1).  dlogits may be
+    logits."""
+    if stream is not None:
+        with _on_stream(stream, logits):
+            return awq_balance_loss_backward(logits, slope, grad, score, mask, dlogits)
+    T, E, ldl = _act_rows(logits, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    device, dev = logits.device, logits.get_device()
+    if slope is None:
+        raise ValueError("slope must be a tensor")
+    dlogits, ldd = _out(dlogits, "dlogits", device, logits.dtype, T, E)
+    _launch("awq_balance_loss_backward", dev,
+            (logits.data_ptr(), _DT.get(logits.dtype, -1), T, E, ldl, _same(slope, "slope", dev, torch.float32, (E,)),
+             _same(grad, "grad", dev, torch.float32, (1,)), _mask(mask, dev, T), _SCORES[score], dlogits.data_ptr(), ldd))
+    return dlogits

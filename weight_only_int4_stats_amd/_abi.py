@@ -18,9 +18,13 @@ STATUS_NAMES = {0: "AWQ_OK", 1: "AWQ_ERR_NULL", 2: "AWQ_ERR_SHAPE", 3: "AWQ_ERR_
 AWQ_F16, AWQ_BF16, AWQ_F32 = 0, 1, 2
 AWQ_OP_ACT_STATS, AWQ_OP_SEARCH, AWQ_OP_QUANTIZE, AWQ_OP_GEMM = 0, 1, 2, 3
 AWQ_OP_EXPERTS_UP, AWQ_OP_EXPERTS_DOWN, AWQ_OP_LORA = 4, 5, 6
+AWQ_OP_LINEAR, AWQ_OP_BIAS_ACT_BACKWARD, AWQ_OP_GEMM_DX = 7, 8, 9
+AWQ_OP_LAYER_NORM_BACKWARD, AWQ_OP_BALANCE_LOSS = 10, 11
 AWQ_SCORE_SOFTMAX, AWQ_SCORE_SIGMOID = 0, 1
 AWQ_ACT_NONE, AWQ_ACT_SWIGLU = 0, 1
+AWQ_ACT_RELU, AWQ_ACT_GELU, AWQ_ACT_GELU_TANH, AWQ_ACT_SILU = 2, 3, 4, 5
 AWQ_MAX_EXPERTS, AWQ_MAX_TOP_K, AWQ_MAX_RANK = 1024, 64, 256
+AWQ_MAX_LINEAR_N = 4194304
 AWQ_GROUP = 128
 AWQ_MAX_ALPHA = 64
 AWQ_NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -52,6 +56,15 @@ SIGNATURES = {
                                     _i64, _p, _sz, _p]),
     "awq_lora_add": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p, _i64, _i64, _p, _p, _p, _i64, _i64, _p, _i,
                           _i64, _p, _sz, _p]),
+    "awq_w4a16_linear": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p, _i64, _i, _p, _i, _i, _p, _i64, _p, _i64, _p, _i,
+                              _i64, _p, _sz, _p]),
+    "awq_bias_act_backward": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _i, _p, _i64, _p, _p, _sz, _p]),
+    "awq_w4a16_gemm_dx": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p, _i64, _i, _p, _i, _i64, _p, _sz, _p]),
+    "awq_layer_norm": (_i, [_p, _i, _i64, _i64, _i64, _p, _i, _p, _i, _f, _i, _p, _i, _i64, _p, _p, _p]),
+    "awq_layer_norm_backward": (_i, [_p, _i, _i64, _i64, _i64, _p, _i, _i64, _p, _i, _p, _p, _i, _p, _i64, _p, _p, _p,
+                                     _sz, _p]),
+    "awq_balance_loss": (_i, [_p, _i, _i64, _i64, _i64, _p, _i, _p, _i, ctypes.c_double, _p, _p, _p, _p, _sz, _p]),
+    "awq_balance_loss_backward": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p, _i, _p, _i64, _p]),
     "awq_read_stream": (_i, [_p, _i64, _i, _i, _p, _p]),
 }
 

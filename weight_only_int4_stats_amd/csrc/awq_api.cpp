@@ -57,6 +57,12 @@ size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T
     case AWQ_OP_LORA:
       if (M > awq::kMaxRows || N > UINT32_MAX || K > AWQ_MAX_K || T > awq::kMaxAdapters || n_alpha > AWQ_MAX_RANK) return 0;
       return awq::lora_ws_bytes(M, N, K, T, n_alpha);
+    case AWQ_OP_LINEAR:
+    case AWQ_OP_BIAS_ACT_BACKWARD:
+    case AWQ_OP_GEMM_DX:
+    case AWQ_OP_LAYER_NORM_BACKWARD:
+    case AWQ_OP_BALANCE_LOSS:
+      return awq::block_ws_bytes((int)op, M, N, K, T);
   }
   return 0;
 }

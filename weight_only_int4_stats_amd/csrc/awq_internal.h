@@ -58,24 +58,42 @@ hipError_t launch_gram_loss(const uint16_t* E, int64_t N, int64_t K, const int* 
 hipError_t launch_fold_scales(void* v, int dt, int64_t rows, int64_t cols, int64_t ld, const float* s,
                               int axis, hipStream_t st);
 
+// ---- epilogue of the W4A16 product (k_epilogue.h) -----------------------------
+enum : int { LINEAR_NONE = 0, LINEAR_RELU = 2, LINEAR_GELU = 3, LINEAR_GELU_TANH = 4, LINEAR_SILU = 5 };
+
+// y = act(z + bias) + res, and z + bias itself into pre; NULL members are left
+// out.  res and pre are rows of y's type.
+struct Epilogue {
+  const void* bias;
+  const void* res;
+  void* pre;
+  int64_t ldr, ldp;
+  int bdt, ydt, act;
+};
+
 // ---- W4A16 product ----------------------------------------------------------
+// ep (optional): the epilogue; then inv_s is NULL and the weights are rounded
+// once (k_epilogue.h)
 // group: input channels per step / zero point (64, 128 or 256)
 bool gemv1_supported(int64_t K, int64_t N);   // batch-1 GEMV kernels cover this shape
 hipError_t launch_gemv1(const void* x, int xdt, int64_t K, const uint32_t* qw,
                         const uint16_t* scales, const uint8_t* zeros, int64_t N, int group,
-                        const float* r, void* y, int ydt, hipStream_t st);
+                        const float* r, void* y, int ydt, hipStream_t st, const Epilogue* ep = nullptr);
 size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int group);
 hipError_t launch_w4a16(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx,
                         const uint32_t* qw, const uint16_t* scales, const uint8_t* zeros,
                         int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
-                        void* ws, hipStream_t st);
+                        void* ws, hipStream_t st, const Epilogue* ep = nullptr);
+// threads of the tiled product's launch (which has 32-bit sizes)
+int64_t gemm_threads(int64_t M, int64_t N);
 
 // 2 <= M <= 64 (k_mid.hip): the memory-bound small-batch product
 bool mid_supported(int64_t M, int64_t N, int64_t K);
 size_t mid_ws_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mid(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                       const uint16_t* scales, const uint8_t* zeros, int64_t N, int group,
-                      const float* inv_s, void* y, int ydt, int64_t ldy, void* ws, hipStream_t st);
+                      const float* inv_s, void* y, int ydt, int64_t ldy, void* ws, hipStream_t st,
+                      const Epilogue* ep = nullptr);
 
 // 2 <= M <= 16 (k_skinny.hip): one block per compute unit with the
 // activations, steps and zero points staged in LDS; blocks (0: shape not
@@ -84,14 +102,14 @@ int skinny_st_blocks(int64_t M, int64_t N, int64_t K, int group);
 hipError_t launch_skinny_st(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx,
                             const uint32_t* qw, const uint16_t* scales, const uint8_t* zeros,
                             int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
-                            hipStream_t st);
+                            hipStream_t st, const Epilogue* ep = nullptr);
 // Layers whose rows exceed one launch's steps and zero points: the kernel on
 // row chunks, one launch each (chunks: 1 = one launch, 0 = not covered).
 int skinny_st_chunks(int64_t M, int64_t N, int64_t K, int group);
 hipError_t launch_skinny_st_chunked(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx,
                                     const uint32_t* qw, const uint16_t* scales, const uint8_t* zeros,
                                     int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
-                                    hipStream_t st);
+                                    hipStream_t st, const Epilogue* ep = nullptr);
 
 // ---- limits of the operators whose weight depends on the row -------------------
 constexpr int64_t kMaxRows = (int64_t)1 << 24;       // slots, or rows with adapters
@@ -149,6 +167,46 @@ struct LoraCall {
 size_t lora_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R);
 int64_t lora_threads(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_t R);
 hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st);
+
+// ---- operators of a block around the packed linears -----------------------------
+size_t block_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t T);
+
+// Column sums of partial rows (k_colsum.hip): columns [0, cols) to out0 and
+// [at1, at1 + cols) to out1 (either may be NULL); pitch a multiple of 64.
+hipError_t launch_col_reduce(const float* partial, int64_t rows, int64_t pitch, int64_t cols, float* out0,
+                             int64_t at1, float* out1, hipStream_t st);
+
+// The epilogue's backward pass (k_act_bias.hip); pre NULL: the bias's gradient
+// alone, dbias NULL: dz alone.
+size_t act_bias_ws_bytes(int64_t M, int64_t N);
+hipError_t launch_act_bias(const void* dy, int dt, int64_t M, int64_t N, int64_t lddy, const void* pre, int64_t ldp,
+                           int act, void* dz, int64_t lddz, float* dbias, void* ws, hipStream_t st);
+
+// The gradient of the product's input (k_gemm_dx.hip)
+size_t gemm_dx_ws_bytes(int64_t M, int64_t N, int64_t K, int group);
+size_t gemm_dx_ws_bytes_upto(int64_t M, int64_t N, int64_t K);
+int64_t gemm_dx_threads(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_dx(const void* dz, int dzt, int64_t M, int64_t N, int64_t lddz, const uint32_t* qw,
+                          const uint16_t* scales, const uint8_t* zeros, int64_t K, int group, void* dx, int dxt,
+                          int64_t lddx, void* ws, hipStream_t st);
+
+// Layer and RMS norm, forward and backward (k_norm.hip)
+int64_t norm_threads(int64_t M, int64_t K);
+hipError_t launch_norm(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx, const void* w, int wdt,
+                       const void* b, int bdt, float eps, int rms, void* y, int ydt, int64_t ldy, float* mean,
+                       float* rstd, hipStream_t st);
+size_t norm_grad_ws_bytes(int64_t M, int64_t K);
+hipError_t launch_norm_grad(const void* dy, int dyt, int64_t M, int64_t K, int64_t lddy, const void* x, int xdt,
+                            int64_t ldx, const void* w, int wdt, const float* mean, const float* rstd, int rms,
+                            void* dx, int64_t lddx, float* dw, float* db, void* ws, hipStream_t st);
+
+// Balance loss of a router and its gradient (k_balance.hip)
+size_t balance_ws_bytes(int64_t T, int64_t E);
+hipError_t launch_balance(const void* logits, int dt, int64_t T, int64_t E, int64_t ldl, const int32_t* ids, int top_k,
+                          const uint8_t* mask, int sigmoid, double coef, float* loss, int32_t* counts, float* slope,
+                          void* ws, hipStream_t st);
+hipError_t launch_balance_grad(const void* logits, int dt, int64_t T, int64_t E, int64_t ldl, const float* slope,
+                               const float* go, const uint8_t* mask, int sigmoid, void* dl, int64_t ldd, hipStream_t st);
 
 // ---- plain streaming read (k_stream.hip): bytes a multiple of 1024, blocks
 // of 1024 threads, unroll 1, 2, 4 or 8 units in flight per wave

@@ -5,6 +5,7 @@
 //   y[n] = sum_k step[n][g(k)] * (q[n][k] - z[n][g(k)]) * x[k] * r[k]
 #include "awq_device.h"
 #include "awq_internal.h"
+#include "k_epilogue.h"
 #include "k_rows_f16.h"
 
 namespace awqk {
@@ -19,6 +20,13 @@ template <int YDT>
 __device__ __forceinline__ void store_y1(void* y, int64_t idx, float v) {
   if constexpr (YDT == DT_F32) reinterpret_cast<float*>(y)[idx] = v;
   else reinterpret_cast<uint16_t*>(y)[idx] = (uint16_t)from_f32<YDT>(v);
+}
+
+// A finished row sum: stored, or through the epilogue.
+template <int YDT, class EP>
+__device__ __forceinline__ void finish_y1(const EP& ep, void* y, int64_t row, float v) {
+  if constexpr (kHasEpi<EP>) epi_store(ep, y, 0, 0, row, v);
+  else store_y1<YDT>(y, row, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -66,7 +74,10 @@ __device__ __forceinline__ void stage_load(const uint16_t* __restrict__ x, const
   }
 }
 
-template <int DT, bool HAS_R, int NS>
+// SCALE: fp16 input without 1/s gets a power of two too.  Without one its odd
+// elements, stored divided by 16, lose bits below 2^-10, which small
+// activations show.
+template <int DT, bool HAS_R, int NS, bool SCALE = false>
 __device__ __forceinline__ void stage_store(int64_t K, const u32x4 (&sx)[NS], const f32x4 (&sr0)[NS],
                                             const f32x4 (&sr1)[NS], uint32_t* xpair, float* xsum) {
   const int64_t n8 = K >> 3;
@@ -94,7 +105,7 @@ __device__ __forceinline__ void stage_store(int64_t K, const u32x4 (&sx)[NS], co
       amax = fmaxf(amax, quad_xor1(amax));
       amax = fmaxf(amax, quad_xor2(amax));
       int p = 0;
-      if constexpr (DT == DT_BF16 || HAS_R) p = pow2_exp_for(amax);
+      if constexpr (DT == DT_BF16 || HAS_R || SCALE) p = pow2_exp_for(amax);
       // even elements meet 1024 + q, odd ones 1024 + 16 q: the odd ones are
       // staged divided by 16 so one accumulator serves all four pairs
       uint32_t h[8];
@@ -105,7 +116,7 @@ __device__ __forceinline__ void stage_store(int64_t K, const u32x4 (&sx)[NS], co
           h[j] = f32_to_f16_bits(ldexpf(v[j], p - 4));
           so += f16_to_f32(h[j]);
         } else {
-          h[j] = (DT == DT_F16 && !HAS_R) ? (sx[i][j >> 1] & 0xFFFFu) : f32_to_f16_bits(ldexpf(v[j], p));
+          h[j] = (DT == DT_F16 && !HAS_R && !SCALE) ? (sx[i][j >> 1] & 0xFFFFu) : f32_to_f16_bits(ldexpf(v[j], p));
           sa += f16_to_f32(h[j]);
         }
       }
@@ -134,11 +145,11 @@ __device__ __forceinline__ void stage_store(int64_t K, const u32x4 (&sx)[NS], co
 }
 
 // UL: rows per wave; NS: 8-element activation chunks staged per thread.
-template <int DT, int YDT, bool HAS_R, int UL, int NS>
+template <int DT, int YDT, bool HAS_R, int UL, int NS, class EP>
 __global__ __launch_bounds__(1024) void k_gemv1_rows(
     const uint16_t* __restrict__ x, int64_t K, const uint32_t* __restrict__ qw,
     const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros, int64_t N,
-    const float* __restrict__ r, void* __restrict__ y, int nks, int gsh) {
+    const float* __restrict__ r, void* __restrict__ y, int nks, int gsh, const EP ep) {
   extern __shared__ uint32_t lds1[];
   const int nwv = blockDim.x >> 6;
   const int nrg = nwv / nks;
@@ -179,7 +190,7 @@ __global__ __launch_bounds__(1024) void k_gemv1_rows(
   __builtin_amdgcn_sched_barrier(0);
 
   // ---- 2. stage fp16(x r 2^p) per 32-chunk (4 threads per chunk)
-  stage_store<DT, HAS_R, NS>(K, sx, sr0, sr1, xpair, xsum);
+  stage_store<DT, HAS_R, NS, kHasEpi<EP>>(K, sx, sr0, sr1, xpair, xsum);
   __syncthreads();
   u32x4 xr[4];
 #pragma unroll
@@ -231,7 +242,7 @@ __global__ __launch_bounds__(1024) void k_gemv1_rows(
     float tot = 0.0f;
     for (int k2 = 0; k2 < nks; ++k2) tot += part[k2 * rowsb + t];
     const int64_t row = (int64_t)blockIdx.x * rowsb + t;
-    if (row < N) store_y1<YDT>(y, row, tot);
+    if (row < N) finish_y1<YDT>(ep, y, row, tot);
   }
 }
 
@@ -247,11 +258,11 @@ __global__ __launch_bounds__(1024) void k_gemv1_rows(
 // at once, otherwise the per-slice partial sums go to LDS and the slices are
 // added in a fixed order at the end.
 // ---------------------------------------------------------------------------
-template <int DT, int YDT, bool HAS_R, int NS, int D, int C>
+template <int DT, int YDT, bool HAS_R, int NS, int D, int C, class EP>
 __global__ __launch_bounds__(1024) void k_gemv1_cu(
     const uint16_t* __restrict__ x, int64_t K, const uint32_t* __restrict__ qw,
     const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros, int64_t N,
-    const float* __restrict__ r, void* __restrict__ y, int nks, int nrg, int rows_max, int gsh) {
+    const float* __restrict__ r, void* __restrict__ y, int nks, int nrg, int rows_max, int gsh, const EP ep) {
   static_assert(D >= 1 && D <= 4, "rows in flight");
   extern __shared__ uint32_t lds1[];
   const int lane = threadIdx.x & 63;
@@ -308,7 +319,7 @@ __global__ __launch_bounds__(1024) void k_gemv1_cu(
   __builtin_amdgcn_sched_barrier(0);
 
   // ---- 1. stage, then this wave's activation slice into registers
-  stage_store<DT, HAS_R, NS>(K, sx, sr0, sr1, xpair, xsum);
+  stage_store<DT, HAS_R, NS, kHasEpi<EP>>(K, sx, sr0, sr1, xpair, xsum);
   __syncthreads();
   u32x4 xr[C][4];
   f32x4 xc[C];
@@ -364,7 +375,7 @@ __global__ __launch_bounds__(1024) void k_gemv1_cu(
       constexpr int LB = D >= 3 ? 2 : D == 2 ? 1 : 0;
       const int jd = j0 + (lane >> (6 - LB));
       if ((lane & ((64 >> LB) - 1)) == 0 && jd < nj && jd < j0 + D) {
-        if (nks == 1) store_y1<YDT>(y, r0 + rg + nrg * jd, v);   // one K slice: the row is complete
+        if (nks == 1) finish_y1<YDT>(ep, y, r0 + rg + nrg * jd, v);   // one K slice: the row is complete
         else part[ks * rows_max + rg + nrg * jd] = v;
       }
       j0 += D;
@@ -377,17 +388,17 @@ __global__ __launch_bounds__(1024) void k_gemv1_cu(
   for (int t = threadIdx.x; t < nrows; t += blockDim.x) {
     float tot = 0.0f;
     for (int k2 = 0; k2 < nks; ++k2) tot += part[k2 * rows_max + t];
-    store_y1<YDT>(y, r0 + t, tot);
+    finish_y1<YDT>(ep, y, r0 + t, tot);
   }
 }
 
 constexpr size_t kCuLdsReserve = 81 * 1024;
 
 
-template <int DT, int YDT, bool HAS_R, int NS, int D, int C>
+template <int DT, int YDT, bool HAS_R, int NS, int D, int C, class EP>
 hipError_t gemv1_cu_launch(const uint16_t* x, int64_t K, const uint32_t* qw, const uint16_t* scales,
                          const uint8_t* zeros, int64_t N, int gsh, const float* r, void* y, int nblk,
-                         int nrg_max, hipStream_t st) {
+                         int nrg_max, hipStream_t st, const EP& ep) {
   const int64_t CH = K >> 5;
   const int nks = (int)((CH + 64 * C - 1) / (64 * C));
   if (nks > 16 || nblk <= 0 || nrg_max <= 0) return hipErrorInvalidValue;
@@ -401,25 +412,25 @@ hipError_t gemv1_cu_launch(const uint16_t* x, int64_t K, const uint32_t* qw, con
   // Over half of a compute unit's 160 KB of LDS: no two blocks share a unit,
   // so the grid of one block per unit spreads over all of them.
   if (lds < kCuLdsReserve) lds = kCuLdsReserve;
-  hipLaunchKernelGGL((k_gemv1_cu<DT, YDT, HAS_R, NS, D, C>), dim3((unsigned)nblk), dim3((unsigned)threads),
-                     lds, st, x, K, qw, scales, zeros, N, r, y, nks, nrg, rows_max, gsh);
+  hipLaunchKernelGGL((k_gemv1_cu<DT, YDT, HAS_R, NS, D, C, EP>), dim3((unsigned)nblk), dim3((unsigned)threads),
+                     lds, st, x, K, qw, scales, zeros, N, r, y, nks, nrg, rows_max, gsh, ep);
   return hipGetLastError();
 }
 
 // Launch with nrg row groups per block; the block stages the whole activation
 // (NS chunks of 8 per thread must cover K / 8, rounded up to whole quads).
-template <int DT, int YDT, bool HAS_R, int UL, int NS>
+template <int DT, int YDT, bool HAS_R, int UL, int NS, class EP>
 hipError_t gemv1_rows_launch(const uint16_t* x, int64_t K, const uint32_t* qw, const uint16_t* scales,
                         const uint8_t* zeros, int64_t N, int gsh, const float* r, void* y, int nrg,
-                        hipStream_t st) {
+                        hipStream_t st, const EP& ep) {
   const int64_t CH = K >> 5;
   const int nks = (int)((CH + 63) / 64);
   const int64_t rows = (int64_t)nrg * UL;
   const int64_t threads = (int64_t)nks * nrg * 64;
   if (threads > 1024 || ((K >> 3) + 3) / 4 * 4 > NS * threads) return hipErrorInvalidValue;
   const size_t lds = (size_t)CH * 16 * 4 + (size_t)CH * 4 * 4 + (size_t)nks * rows * 4;
-  hipLaunchKernelGGL((k_gemv1_rows<DT, YDT, HAS_R, UL, NS>), dim3((unsigned)((N + rows - 1) / rows)),
-                     dim3((unsigned)threads), lds, st, x, K, qw, scales, zeros, N, r, y, nks, gsh);
+  hipLaunchKernelGGL((k_gemv1_rows<DT, YDT, HAS_R, UL, NS, EP>), dim3((unsigned)((N + rows - 1) / rows)),
+                     dim3((unsigned)threads), lds, st, x, K, qw, scales, zeros, N, r, y, nks, gsh, ep);
   return hipGetLastError();
 }
 
@@ -451,10 +462,10 @@ inline int gemv1_path(int64_t K, int64_t N) {
 }
 
 // gsh: log2 of the 32-code chunks per group (1, 2, 3 for groups of 64, 128, 256)
-template <int DT, int YDT, bool HAS_R>
+template <int DT, int YDT, bool HAS_R, class EP>
 hipError_t gemv1_dispatch(const uint16_t* x, int64_t K, const uint32_t* qw, const uint16_t* scales,
                           const uint8_t* zeros, int64_t N, int gsh, const float* r, void* y,
-                          hipStream_t st) {
+                          hipStream_t st, const EP& ep) {
   const int path = gemv1_path(K, N);
   const int64_t need = ((K >> 3) + 3) / 4 * 4;     // staged 8-element pieces, whole quads
   if (path == 2) {
@@ -466,12 +477,12 @@ hipError_t gemv1_dispatch(const uint16_t* x, int64_t K, const uint32_t* qw, cons
     const int64_t threads = nks * (16 / nks) * 64;
     if (need <= threads) {
       if (K <= 4096)
-        return gemv1_cu_launch<DT, YDT, HAS_R, 1, 1, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nblk, 16, st);
-      return gemv1_cu_launch<DT, YDT, HAS_R, 1, 2, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nblk, 16, st);
+        return gemv1_cu_launch<DT, YDT, HAS_R, 1, 1, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nblk, 16, st, ep);
+      return gemv1_cu_launch<DT, YDT, HAS_R, 1, 2, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nblk, 16, st, ep);
     }
     if (need <= 2 * threads)
-      return gemv1_cu_launch<DT, YDT, HAS_R, 2, 2, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nblk, 16, st);
-    return gemv1_cu_launch<DT, YDT, HAS_R, 4, 4, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nblk, 16, st);
+      return gemv1_cu_launch<DT, YDT, HAS_R, 2, 2, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nblk, 16, st, ep);
+    return gemv1_cu_launch<DT, YDT, HAS_R, 4, 4, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nblk, 16, st, ep);
   }
   if (path == 0) return hipErrorInvalidValue;
   const int64_t CH = K >> 5;
@@ -479,9 +490,9 @@ hipError_t gemv1_dispatch(const uint16_t* x, int64_t K, const uint32_t* qw, cons
   int nrg = nks >= 8 ? 1 : 8 / nks;
   if (nks * nrg > 16) nrg = 16 / nks;
   const int64_t threads = (int64_t)nks * nrg * 64;
-  if (need <= threads) return gemv1_rows_launch<DT, YDT, HAS_R, 4, 1>(x, K, qw, scales, zeros, N, gsh, r, y, nrg, st);
-  if (need <= 2 * threads) return gemv1_rows_launch<DT, YDT, HAS_R, 4, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nrg, st);
-  return gemv1_rows_launch<DT, YDT, HAS_R, 4, kG1MaxStage>(x, K, qw, scales, zeros, N, gsh, r, y, nrg, st);
+  if (need <= threads) return gemv1_rows_launch<DT, YDT, HAS_R, 4, 1>(x, K, qw, scales, zeros, N, gsh, r, y, nrg, st, ep);
+  if (need <= 2 * threads) return gemv1_rows_launch<DT, YDT, HAS_R, 4, 2>(x, K, qw, scales, zeros, N, gsh, r, y, nrg, st, ep);
+  return gemv1_rows_launch<DT, YDT, HAS_R, 4, kG1MaxStage>(x, K, qw, scales, zeros, N, gsh, r, y, nrg, st, ep);
 }
 
 }  // namespace awqk
@@ -504,14 +515,19 @@ bool gemv1_supported(int64_t K, int64_t N) { return awqk::gemv1_path(K, N) != 0;
 
 hipError_t launch_gemv1(const void* x, int xdt, int64_t K, const uint32_t* qw,
                         const uint16_t* scales, const uint8_t* zeros, int64_t N, int group,
-                        const float* r, void* y, int ydt, hipStream_t st) {
+                        const float* r, void* y, int ydt, hipStream_t st, const Epilogue* ep) {
   using namespace awqk;
   const uint16_t* xp = (const uint16_t*)x;
   const int gsh = group == 64 ? 1 : group == 128 ? 2 : group == 256 ? 3 : -1;
   if (gsh < 0) return hipErrorInvalidValue;
+  if (ep) {
+    if (r) return hipErrorInvalidValue;
+    return xdt == DT_F16 ? gemv1_dispatch<DT_F16, DT_F32, false>(xp, K, qw, scales, zeros, N, gsh, r, y, st, *ep)
+                         : gemv1_dispatch<DT_BF16, DT_F32, false>(xp, K, qw, scales, zeros, N, gsh, r, y, st, *ep);
+  }
 #define AWQ_G1(DT, YDT)                                                                         \
-  return r ? gemv1_dispatch<DT, YDT, true>(xp, K, qw, scales, zeros, N, gsh, r, y, st)          \
-           : gemv1_dispatch<DT, YDT, false>(xp, K, qw, scales, zeros, N, gsh, r, y, st)
+  return r ? gemv1_dispatch<DT, YDT, true>(xp, K, qw, scales, zeros, N, gsh, r, y, st, NoEpi{})          \
+           : gemv1_dispatch<DT, YDT, false>(xp, K, qw, scales, zeros, N, gsh, r, y, st, NoEpi{})
   if (xdt == DT_F16) {
     if (ydt == DT_F16) AWQ_G1(DT_F16, DT_F16);
     if (ydt == DT_BF16) AWQ_G1(DT_F16, DT_BF16);

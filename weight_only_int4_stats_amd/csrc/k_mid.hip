@@ -30,6 +30,7 @@
 // the L2 back (measured 8x slower).
 #include "awq_device.h"
 #include "awq_internal.h"
+#include "k_epilogue.h"
 #include "k_rows_f16.h"
 
 namespace awqk {
@@ -66,6 +67,13 @@ __device__ __forceinline__ u32x4 mid_dequant(uint32_t w, f16x2 c24, f16x2 c20, f
   return out;
 }
 
+// A finished sum: stored, or through the epilogue.
+template <int YDT, class EP>
+__device__ __forceinline__ void finish_ym(const EP& ep, void* y, int64_t ldy, int64_t m, int64_t n, float v) {
+  if constexpr (kHasEpi<EP>) epi_store(ep, y, ldy, m, n, v);
+  else store_ym<YDT>(y, m * ldy + n, v);
+}
+
 // TG: 16-token groups (1..4); T: 16-row tiles per block (every wave runs all
 // of them, so one load of an activation operand serves T tiles); SPLIT: S > 1.
 // Block (s, b) takes rows [b N / nb, (b + 1) N / nb) (at most 16 T) and the
@@ -75,12 +83,13 @@ __device__ __forceinline__ u32x4 mid_dequant(uint32_t w, f16x2 c24, f16x2 c20, f
 // b4 of weight row rl of each tile (one 128-bit chunk) and of token rl of each
 // token group (four 128-bit chunks of x_q, read straight from memory: x_q is a
 // few hundred KB, so after the first reads it is served by the L2).
-template <int YDT, int TG, int T, bool SPLIT>
+template <int YDT, int TG, int T, bool SPLIT, class EP>
 __global__ __launch_bounds__(64 * kMidWaves) void k_gemm_mid(
     const uint16_t* __restrict__ xq, const int* __restrict__ pm, int M, int64_t K,
     const uint32_t* __restrict__ qw, const uint16_t* __restrict__ scales,
     const uint8_t* __restrict__ zeros, int64_t N, int64_t nb, int glog, int S,
-    float* __restrict__ partial, int* __restrict__ en, void* __restrict__ y, int64_t ldy) {
+    float* __restrict__ partial, int* __restrict__ en, void* __restrict__ y, int64_t ldy, const EP ep) {
+  constexpr bool ONCE = kHasEpi<EP>;
   constexpr int R = 16 * T;                      // rows a block can hold
   constexpr int TILE = 16 * kMidPad;             // floats of one partial 16 x 16 tile in LDS
   extern __shared__ __attribute__((aligned(16))) float red[];   // [waves][T][TG][16 tokens][kMidPad]
@@ -159,21 +168,16 @@ __global__ __launch_bounds__(64 * kMidWaves) void k_gemm_mid(
           srs, row < nrows ? (uint32_t)row * GW * 2 + 16 * pc : kBufferOob, 0, 0);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (pc * 8 + j < GW) mx = fmaxf(mx, f16_to_f32((v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu));
+        if (pc * 8 + j < GW) mx = fmaxf(mx, step_size<ONCE>((v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu));
     }
     const auto r32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
     mx = fmaxf(__uint_as_float(r32[0]), __uint_as_float(r32[1]));
     const auto r16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
     mx = fmaxf(__uint_as_float(r16[0]), __uint_as_float(r16[1]));
-    e[t] = 0;
-    if (mx > 0.0f) {
-      int ex;
-      frexpf(mx, &ex);
-      e[t] = -9 - ex;
-    }
+    e[t] = step_pow<ONCE>(mx);
     if (wv == 0 && b4 == 0) {
-      e_s[row] = e[t];
-      if (SPLIT && bs == 0 && row < nrows) en[n0 + row] = e[t];
+      e_s[row] = sum_pow<ONCE>(e[t]);
+      if (SPLIT && bs == 0 && row < nrows) en[n0 + row] = sum_pow<ONCE>(e[t]);
     }
   }
 
@@ -191,15 +195,21 @@ __global__ __launch_bounds__(64 * kMidWaves) void k_gemm_mid(
 #pragma unroll
         for (int t = 0; t < T; ++t) {
           const float D = ldexpf(f16_to_f32(sr[d][t]), e[t]);
-          const uint32_t h24 = f32_to_f16_bits(D * 16777216.0f);
-          const uint32_t h20 = f32_to_f16_bits(D * 1048576.0f);
-          const uint32_t hz = f32_to_f16_bits(-(D * (float)zr[d][t]));
-          const f16x2 c24 = as_f16x2(h24 | (h24 << 16));
-          const f16x2 c20 = as_f16x2(h20 | (h20 << 16));
-          const f16x2 nzd = as_f16x2(hz | (hz << 16));
           u32x4 a[4];
+          if constexpr (ONCE) {
+            const uint32_t mult = f32_to_f16_bits(D) * 0x10001u, nz = once_zero(zr[d][t]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = mid_dequant(wa[d][t][i], c24, c20, nzd);
+            for (int i = 0; i < 4; ++i) a[i] = once_dequant(wa[d][t][i], mult, nz);
+          } else {
+            const uint32_t h24 = f32_to_f16_bits(D * 16777216.0f);
+            const uint32_t h20 = f32_to_f16_bits(D * 1048576.0f);
+            const uint32_t hz = f32_to_f16_bits(-(D * (float)zr[d][t]));
+            const f16x2 c24 = as_f16x2(h24 | (h24 << 16));
+            const f16x2 c20 = as_f16x2(h20 | (h20 << 16));
+            const f16x2 nzd = as_f16x2(hz | (hz << 16));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = mid_dequant(wa[d][t][i], c24, c20, nzd);
+          }
 #pragma unroll
           for (int g = 0; g < TG; ++g)
 #pragma unroll
@@ -230,23 +240,23 @@ __global__ __launch_bounds__(64 * kMidWaves) void k_gemm_mid(
       for (int w = 0; w < kMidWaves; ++w) tot += red[((size_t)w * T * TG + tg) * TILE + otok * kMidPad + orr];
       const int64_t n = n0 + orow;
       if constexpr (SPLIT) partial[((int64_t)bs * M + m) * N + n] = tot;
-      else store_ym<YDT>(y, (int64_t)m * ldy + n, ldexpf(tot, -(pm[m] + e_s[orow])));
+      else finish_ym<YDT>(ep, y, ldy, m, n, ldexpf(tot, -(pm[m] + e_s[orow])));
     }
   }
 }
 
 // y[m][n] = (sum over slices s = 0..S-1 of partial[s][m][n]) 2^-(pm[m] + en[n])
-template <int YDT>
+template <int YDT, class EP>
 __global__ __launch_bounds__(256) void k_mid_reduce(const float* __restrict__ partial, int S, int M,
                                                     int64_t N, const int* __restrict__ pm,
                                                     const int* __restrict__ en, void* __restrict__ y,
-                                                    int64_t ldy) {
+                                                    int64_t ldy, const EP ep) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)M * N) return;
   const int64_t m = i / N, n = i - m * N;
   float tot = 0.0f;
   for (int s = 0; s < S; ++s) tot += partial[(int64_t)s * M * N + i];
-  store_ym<YDT>(y, m * ldy + n, ldexpf(tot, -(pm[m] + en[n])));
+  finish_ym<YDT>(ep, y, ldy, m, n, ldexpf(tot, -(pm[m] + en[n])));
 }
 
 struct MidPlan {
@@ -320,53 +330,53 @@ inline MidWs mid_ws(void* ws, int64_t M, int64_t N, int64_t K, int S) {
   return w;
 }
 
-template <int YDT, int TG, int T>
+template <int YDT, int TG, int T, class EP>
 hipError_t mid_launch_t(const MidWs& w, int64_t M, int64_t K, const uint32_t* qw, const uint16_t* scales,
                         const uint8_t* zeros, int64_t N, int glog, void* y, int64_t ldy, const MidPlan& p,
-                        hipStream_t st) {
+                        hipStream_t st, const EP& ep) {
   if (p.S == 1) {
-    hipLaunchKernelGGL((k_gemm_mid<YDT, TG, T, false>), dim3((unsigned)p.blocks), dim3(64 * kMidWaves), p.lds,
+    hipLaunchKernelGGL((k_gemm_mid<YDT, TG, T, false, EP>), dim3((unsigned)p.blocks), dim3(64 * kMidWaves), p.lds,
                        st, w.xq, w.pm, (int)M, K, qw, scales, zeros, N, p.nb, glog, p.S, w.partial, w.en, y,
-                       ldy);
+                       ldy, ep);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((k_gemm_mid<YDT, TG, T, true>), dim3((unsigned)p.blocks), dim3(64 * kMidWaves), p.lds,
+  hipLaunchKernelGGL((k_gemm_mid<YDT, TG, T, true, EP>), dim3((unsigned)p.blocks), dim3(64 * kMidWaves), p.lds,
                      st, w.xq, w.pm, (int)M, K, qw, scales, zeros, N, p.nb, glog, p.S, w.partial, w.en, y,
-                     ldy);
-  hipLaunchKernelGGL((k_mid_reduce<YDT>), dim3((unsigned)((M * N + 255) / 256)), dim3(256), 0, st,
-                     w.partial, p.S, (int)M, N, w.pm, w.en, y, ldy);
+                     ldy, ep);
+  hipLaunchKernelGGL((k_mid_reduce<YDT, EP>), dim3((unsigned)((M * N + 255) / 256)), dim3(256), 0, st,
+                     w.partial, p.S, (int)M, N, w.pm, w.en, y, ldy, ep);
   return hipGetLastError();
 }
 
-template <int DT, int YDT, bool HAS_R, int TG>
+template <int DT, int YDT, bool HAS_R, int TG, class EP>
 hipError_t mid_launch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                       const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog, const float* r,
-                      void* y, int64_t ldy, const MidPlan& p, void* ws, hipStream_t st) {
+                      void* y, int64_t ldy, const MidPlan& p, void* ws, hipStream_t st, const EP& ep) {
   const MidWs w = mid_ws(ws, M, N, K, p.S);
   hipLaunchKernelGGL((k_rows_f16<DT, HAS_R, true, true>), dim3((unsigned)M), dim3(256), 0, st, x, K, ldx, r,
                      w.xq, w.pm);
   switch (p.T) {
-    case 1: return mid_launch_t<YDT, TG, 1>(w, M, K, qw, scales, zeros, N, glog, y, ldy, p, st);
-    case 2: return mid_launch_t<YDT, TG, 2>(w, M, K, qw, scales, zeros, N, glog, y, ldy, p, st);
+    case 1: return mid_launch_t<YDT, TG, 1>(w, M, K, qw, scales, zeros, N, glog, y, ldy, p, st, ep);
+    case 2: return mid_launch_t<YDT, TG, 2>(w, M, K, qw, scales, zeros, N, glog, y, ldy, p, st, ep);
     default:
       if constexpr (TG <= 2) {
-        if (p.T == 3) return mid_launch_t<YDT, TG, 3>(w, M, K, qw, scales, zeros, N, glog, y, ldy, p, st);
-        return mid_launch_t<YDT, TG, 4>(w, M, K, qw, scales, zeros, N, glog, y, ldy, p, st);
+        if (p.T == 3) return mid_launch_t<YDT, TG, 3>(w, M, K, qw, scales, zeros, N, glog, y, ldy, p, st, ep);
+        return mid_launch_t<YDT, TG, 4>(w, M, K, qw, scales, zeros, N, glog, y, ldy, p, st, ep);
       }
       return hipErrorInvalidValue;
   }
 }
 
-template <int DT, int YDT, bool HAS_R>
+template <int DT, int YDT, bool HAS_R, class EP>
 hipError_t mid_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                         const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog, const float* r,
-                        void* y, int64_t ldy, void* ws, hipStream_t st) {
+                        void* y, int64_t ldy, void* ws, hipStream_t st, const EP& ep) {
   const MidPlan p = mid_plan(M, N, K);
   if (p.S == 0) return hipErrorInvalidValue;
   switch (p.tg) {                                // M >= 17: two to four token groups
-    case 2: return mid_launch<DT, YDT, HAS_R, 2>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, p, ws, st);
-    case 3: return mid_launch<DT, YDT, HAS_R, 3>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, p, ws, st);
-    default: return mid_launch<DT, YDT, HAS_R, 4>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, p, ws, st);
+    case 2: return mid_launch<DT, YDT, HAS_R, 2>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, p, ws, st, ep);
+    case 3: return mid_launch<DT, YDT, HAS_R, 3>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, p, ws, st, ep);
+    default: return mid_launch<DT, YDT, HAS_R, 4>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, p, ws, st, ep);
   }
 }
 
@@ -383,14 +393,21 @@ size_t mid_ws_bytes(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mid(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                       const uint16_t* scales, const uint8_t* zeros, int64_t N, int group,
-                      const float* inv_s, void* y, int ydt, int64_t ldy, void* ws, hipStream_t st) {
+                      const float* inv_s, void* y, int ydt, int64_t ldy, void* ws, hipStream_t st,
+                      const Epilogue* ep) {
   using namespace awqk;
   const uint16_t* xp = (const uint16_t*)x;
   const int glog = group == 64 ? 6 : group == 128 ? 7 : group == 256 ? 8 : -1;
   if (glog < 0) return hipErrorInvalidValue;
+  if (ep) {
+    if (inv_s) return hipErrorInvalidValue;
+    return xdt == DT_F16
+               ? mid_dispatch<DT_F16, DT_F32, false>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st, *ep)
+               : mid_dispatch<DT_BF16, DT_F32, false>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st, *ep);
+  }
 #define AWQ_MD(XT, YT)                                                                           \
-  return inv_s ? mid_dispatch<XT, YT, true>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st) \
-               : mid_dispatch<XT, YT, false>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st)
+  return inv_s ? mid_dispatch<XT, YT, true>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st, NoEpi{}) \
+               : mid_dispatch<XT, YT, false>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st, NoEpi{})
   if (xdt == DT_F16) {
     if (ydt == DT_F16) AWQ_MD(DT_F16, DT_F16);
     if (ydt == DT_BF16) AWQ_MD(DT_F16, DT_BF16);

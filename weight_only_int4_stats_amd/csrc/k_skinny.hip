@@ -49,6 +49,7 @@
 //    everything and then issue theirs.
 #include "awq_device.h"
 #include "awq_internal.h"
+#include "k_epilogue.h"
 #include "k_rows_f16.h"
 
 #include <type_traits>
@@ -67,6 +68,13 @@ template <int YDT>
 __device__ __forceinline__ void store_yst(void* y, int64_t idx, float v) {
   if constexpr (YDT == DT_F32) reinterpret_cast<float*>(y)[idx] = v;
   else reinterpret_cast<uint16_t*>(y)[idx] = (uint16_t)from_f32<YDT>(v);
+}
+
+// A finished sum: stored, or through the epilogue.
+template <int YDT, class EP>
+__device__ __forceinline__ void finish_yst(const EP& ep, void* y, int64_t ldy, int64_t m, int64_t n, float v) {
+  if constexpr (kHasEpi<EP>) epi_store(ep, y, ldy, m, n, v);
+  else store_yst<YDT>(y, m * ldy + n, v);
 }
 
 // One packed word -> its 8 codes as fp16 subnormals, in the order
@@ -159,12 +167,13 @@ __device__ __forceinline__ void st_dma16(const i32x4& rs, uint32_t lds, uint32_t
                : "=&s"(keep) : "s"(lds), "v"(voff), "s"(rs) : "memory");
 }
 
-template <int DT, int YDT, bool HAS_R, int NP, bool G64, bool SPLIT, bool MULTI, bool LW>
+template <int DT, int YDT, bool HAS_R, int NP, bool G64, bool SPLIT, bool MULTI, bool LW, class EP>
 __global__ __launch_bounds__(1024) void k_gemm_skinny_st(
     const uint16_t* __restrict__ x, int M, int64_t K, int64_t ldx, const float* __restrict__ r,
     const uint32_t* __restrict__ qw, const uint16_t* __restrict__ scales,
     const uint8_t* __restrict__ zeros, int64_t N, void* __restrict__ y, int64_t ldy, int glog,
-    uint32_t o_sums, uint32_t o_pinv, uint32_t o_meta, int mp, int kpass, uint32_t o_ring) {
+    uint32_t o_sums, uint32_t o_pinv, uint32_t o_meta, int mp, int kpass, uint32_t o_ring,
+    const EP ep) {
   static_assert(!LW || (!MULTI && !G64), "words through LDS: one pass, groups >= 128");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds_st[];
   const int tid = threadIdx.x;
@@ -538,7 +547,7 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_st(
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int t = 4 * b + v;
-      if (t < M && tile * 16 + rl < nrows) store_yst<YDT>(y, (int64_t)t * ldy + r0 + tile * 16 + rl, a[v]);
+      if (t < M && tile * 16 + rl < nrows) finish_yst<YDT>(ep, y, ldy, t, r0 + tile * 16 + rl, a[v]);
     }
   };
   // The first item runs on the words loaded before the staging; later items
@@ -609,15 +618,15 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_st(
       const int tl = t >> 8, tk = (t >> 4) & 15, row = t & 15;
       float tot = 0.0f;
       for (int ks = 0; ks < ksl; ++ks) tot += red[(tl * ksl + ks) * 256 + tk * 16 + row];
-      if (tk < M && tl * 16 + row < nrows) store_yst<YDT>(y, (int64_t)tk * ldy + r0 + tl * 16 + row, tot);
+      if (tk < M && tl * 16 + row < nrows) finish_yst<YDT>(ep, y, ldy, tk, r0 + tl * 16 + row, tot);
     }
   }
 }
 
-template <int DT, int YDT, bool HAS_R>
+template <int DT, int YDT, bool HAS_R, class EP>
 hipError_t st_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                        const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog, const float* r,
-                       void* y, int64_t ldy, int nblk, hipStream_t st) {
+                       void* y, int64_t ldy, int nblk, hipStream_t st, const EP& ep) {
   const int64_t rows_max = (N + nblk - 1) / nblk;
   const int64_t kp = st_kpass(M, K, rows_max, glog);
   const bool multi = kp < K;
@@ -629,9 +638,9 @@ hipError_t st_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, con
   const int np = split ? st_pieces(M, K, 512) : st_pieces(M, kp);
   const dim3 grid((unsigned)nblk), block(1024);
 #define AWQ_ST(NP, G64, SPLIT, MULTI, LW)                                                            \
-  hipLaunchKernelGGL((k_gemm_skinny_st<DT, YDT, HAS_R, NP, G64, SPLIT, MULTI, LW>), grid, block, lds, st, x, \
+  hipLaunchKernelGGL((k_gemm_skinny_st<DT, YDT, HAS_R, NP, G64, SPLIT, MULTI, LW, EP>), grid, block, lds, st, x, \
                      (int)M, K, ldx, r, qw, scales, zeros, N, y, ldy, glog, (uint32_t)L.sums,         \
-                     (uint32_t)L.pinv, (uint32_t)L.meta, L.meta_pitch, (int)kp, (uint32_t)L.ring)
+                     (uint32_t)L.pinv, (uint32_t)L.meta, L.meta_pitch, (int)kp, (uint32_t)L.ring, ep)
 #define AWQ_STG(NP)                                     \
   if (multi) {                                          \
     if (glog == 6) AWQ_ST(NP < 4 ? NP : 4, true, false, true, false); \
@@ -687,15 +696,21 @@ int skinny_st_chunks(int64_t M, int64_t N, int64_t K, int group) {
 hipError_t launch_skinny_st(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx,
                             const uint32_t* qw, const uint16_t* scales, const uint8_t* zeros,
                             int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
-                            hipStream_t st) {
+                            hipStream_t st, const Epilogue* ep) {
   using namespace awqk;
   const int nblk = skinny_st_blocks(M, N, K, group);
   if (nblk == 0) return hipErrorInvalidValue;
   const int glog = group == 64 ? 6 : group == 128 ? 7 : 8;
   const uint16_t* xp = (const uint16_t*)x;
+  if (ep) {
+    if (inv_s) return hipErrorInvalidValue;
+    return xdt == DT_F16
+               ? st_dispatch<DT_F16, DT_F32, false>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, nblk, st, *ep)
+               : st_dispatch<DT_BF16, DT_F32, false>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, nblk, st, *ep);
+  }
 #define AWQ_SD(XT, YT)                                                                                \
-  return inv_s ? st_dispatch<XT, YT, true>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, nblk, st) \
-               : st_dispatch<XT, YT, false>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, nblk, st)
+  return inv_s ? st_dispatch<XT, YT, true>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, nblk, st, NoEpi{}) \
+               : st_dispatch<XT, YT, false>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, nblk, st, NoEpi{})
   if (xdt == DT_F16) {
     if (ydt == DT_F16) AWQ_SD(DT_F16, DT_F16);
     if (ydt == DT_BF16) AWQ_SD(DT_F16, DT_BF16);
@@ -710,15 +725,23 @@ hipError_t launch_skinny_st(const void* x, int xdt, int64_t M, int64_t K, int64_
 hipError_t launch_skinny_st_chunked(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx,
                                     const uint32_t* qw, const uint16_t* scales, const uint8_t* zeros,
                                     int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
-                                    hipStream_t st) {
+                                    hipStream_t st, const Epilogue* ep) {
   const int c = skinny_st_chunks(M, N, K, group);
   if (c == 0) return hipErrorInvalidValue;
   const int64_t G = K / group;
   const int64_t yb = ydt == awqk::DT_F32 ? 4 : 2;
   for (int i = 0; i < c; ++i) {
     const int64_t n0 = (int64_t)i * N / c, n1 = (int64_t)(i + 1) * N / c;
+    Epilogue epc{};
+    if (ep) {                                       // the chunk's columns of the epilogue's arrays
+      epc = *ep;
+      const int64_t bb = ep->bdt == awqk::DT_F32 ? 4 : 2;
+      if (ep->bias) epc.bias = (const uint8_t*)ep->bias + n0 * bb;
+      if (ep->res) epc.res = (const uint8_t*)ep->res + n0 * yb;
+      if (ep->pre) epc.pre = (uint8_t*)ep->pre + n0 * yb;
+    }
     const hipError_t e = launch_skinny_st(x, xdt, M, K, ldx, qw + n0 * (K >> 3), scales + n0 * G, zeros + n0 * G,
-                                          n1 - n0, group, inv_s, (uint8_t*)y + n0 * yb, ydt, ldy, st);
+                                          n1 - n0, group, inv_s, (uint8_t*)y + n0 * yb, ydt, ldy, st, ep ? &epc : nullptr);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
