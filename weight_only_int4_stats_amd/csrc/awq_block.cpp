@@ -52,13 +52,22 @@ bool linear_sizes(int64_t M, int64_t N, int64_t K) {
 
 namespace awq {
 
-// The bytes for M rows serve every smaller M.
+// The bytes for M rows serve every smaller M, whatever the group (which kernel
+// serves a shape depends on it).
 size_t linear_ws_bytes_upto(int64_t M, int64_t N, int64_t K) {
-  size_t most = gemm_ws_bytes(M, N, K, 64);
-  for (int64_t m = 1; m < M && m <= 64; ++m) {
-    const size_t b = gemm_ws_bytes(m, N, K, 64);
-    most = b > most ? b : most;
-  }
+  size_t most = 0;
+  auto upto = [&](int64_t m) {
+    for (int g = 64; g <= 256; g *= 2) {
+      const size_t b = K % g == 0 ? linear_ws_bytes(m, N, K, g) : 0;
+      most = b > most ? b : most;
+    }
+  };
+  upto(M);
+  for (int64_t m = 1; m < M && m <= 64; ++m) upto(m);
+  // fewer rows may be split into more slices, the same for each 16 rows; past
+  // 4 rounds of the tallest tiles nothing is split
+  const int64_t split = 4 * (int64_t)device_cus() * 256;
+  for (int64_t m = 80; m < M && m <= split; m += 16) upto(m);
   return most;
 }
 
@@ -71,7 +80,7 @@ size_t block_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t T) {
     case AWQ_OP_GEMM_DX:
       return M < 1 || N < 1 || K < 1 || !linear_sizes(M, N, K) ? 0 : gemm_dx_ws_bytes_upto(M, N, K);
     case AWQ_OP_LAYER_NORM_BACKWARD:
-      return M < 1 || K < 1 || M > kMaxRows || K > AWQ_MAX_K ? 0 : norm_grad_ws_bytes(M, K);
+      return M < 1 || K < 1 || M > kMaxRows || K > AWQ_MAX_K ? 0 : norm_grad_ws_bytes_upto(M, K);
     case AWQ_OP_BALANCE_LOSS:
       return M < 1 || T < 1 || M > kMaxRows || T > AWQ_MAX_EXPERTS ? 0 : balance_ws_bytes(M, T);
   }
@@ -93,18 +102,18 @@ awq_status awq_w4a16_linear(const void* x, awq_dtype xdt, int64_t M, int64_t K, 
   if (K > AWQ_MAX_K) return AWQ_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return AWQ_OK;
   if (!x || !qweight || !scales || !zeros || !y) return AWQ_ERR_NULL;
-  if (!linear_sizes(M, N, K) || awq::gemm_threads(M, N) > kMaxThreads) return AWQ_ERR_UNSUPPORTED;
+  if (!linear_sizes(M, N, K) || awq::linear_threads(M, N, K) > kMaxThreads) return AWQ_ERR_UNSUPPORTED;
   const uintptr_t yb = bytes_of(ydt);
   if (ldx % 8 != 0 || !aligned(x, 16) || !aligned(qweight, 16) || !aligned(scales, 2) || !aligned(y, yb) ||
       (bias && !aligned(bias, bytes_of(bdt))) || (residual && !aligned(residual, yb)) || (pre && !aligned(pre, yb)))
     return AWQ_ERR_ALIGN;
-  if (!ws_ok(ws, ws_bytes, awq::gemm_ws_bytes(M, N, K, group_size))) return AWQ_ERR_WORKSPACE;
+  if (!ws_ok(ws, ws_bytes, awq::linear_ws_bytes(M, N, K, group_size))) return AWQ_ERR_WORKSPACE;
   const Rows rx = rows_of(x, M, K, ldx, xdt), ry = rows_of(y, M, N, ldy, ydt), rr = rows_of(residual, M, N, ldr, ydt),
              rp = rows_of(pre, M, N, ldp, ydt);
   if (meet(rx, ry) || meet(rx, rp) || meet(ry, rp) || meet(rr, rp) || meet_apart(rr, ry)) return AWQ_ERR_UNSUPPORTED;
   const awq::Epilogue ep{bias, residual, pre, ldr, ldp, (int)bdt, (int)ydt, (int)act};
-  return from_hip(awq::launch_w4a16(x, (int)xdt, M, K, ldx, (const uint32_t*)qweight, scales, zeros, N, group_size,
-                                    nullptr, y, (int)ydt, ldy, ws, (hipStream_t)stream, &ep));
+  return from_hip(awq::launch_linear(x, (int)xdt, M, K, ldx, (const uint32_t*)qweight, scales, zeros, N, group_size, y,
+                                     ldy, ep, ws, (hipStream_t)stream));
 }
 
 awq_status awq_bias_act_backward(const void* dy, awq_dtype dt, int64_t M, int64_t N, int64_t lddy, const void* pre,

@@ -72,8 +72,8 @@ struct Epilogue {
 };
 
 // ---- W4A16 product ----------------------------------------------------------
-// ep (optional): the epilogue; then inv_s is NULL and the weights are rounded
-// once (k_epilogue.h)
+// ep (optional, for awq_w4a16_linear): the epilogue; then inv_s is NULL and the
+// weights are rounded once (k_epilogue.h)
 // group: input channels per step / zero point (64, 128 or 256)
 bool gemv1_supported(int64_t K, int64_t N);   // batch-1 GEMV kernels cover this shape
 hipError_t launch_gemv1(const void* x, int xdt, int64_t K, const uint32_t* qw,
@@ -83,9 +83,7 @@ size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int group);
 hipError_t launch_w4a16(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx,
                         const uint32_t* qw, const uint16_t* scales, const uint8_t* zeros,
                         int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
-                        void* ws, hipStream_t st, const Epilogue* ep = nullptr);
-// threads of the tiled product's launch (which has 32-bit sizes)
-int64_t gemm_threads(int64_t M, int64_t N);
+                        void* ws, hipStream_t st);
 
 // 2 <= M <= 64 (k_mid.hip): the memory-bound small-batch product
 bool mid_supported(int64_t M, int64_t N, int64_t K);
@@ -171,6 +169,18 @@ hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st);
 // ---- operators of a block around the packed linears -----------------------------
 size_t block_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t T);
 
+// The product with an epilogue (k_w4a16.hip chooses, k_linear.hip: the tiles)
+bool linear_mid(int64_t M, int64_t N, int64_t K);    // the 17 .. 64 token kernel serves this shape
+size_t linear_ws_bytes(int64_t M, int64_t N, int64_t K, int group);
+size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K);
+int64_t linear_threads(int64_t M, int64_t N, int64_t K);   // of the largest of its launches
+hipError_t launch_linear(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
+                         const uint16_t* scales, const uint8_t* zeros, int64_t N, int group, void* y, int64_t ldy,
+                         const Epilogue& ep, void* ws, hipStream_t st);
+hipError_t launch_linear_tiles(const uint16_t* xq, const int* pm, const int* en, const uint32_t* ctab, const uint32_t* qw,
+                               int64_t M, int64_t N, int64_t K, int group, float* partial, void* y, int64_t ldy,
+                               const Epilogue& ep, hipStream_t st);
+
 // Column sums of partial rows (k_colsum.hip): columns [0, cols) to out0 and
 // [at1, at1 + cols) to out1 (either may be NULL); pitch a multiple of 64.
 hipError_t launch_col_reduce(const float* partial, int64_t rows, int64_t pitch, int64_t cols, float* out0,
@@ -196,6 +206,7 @@ hipError_t launch_norm(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx
                        const void* b, int bdt, float eps, int rms, void* y, int ydt, int64_t ldy, float* mean,
                        float* rstd, hipStream_t st);
 size_t norm_grad_ws_bytes(int64_t M, int64_t K);
+size_t norm_grad_ws_bytes_upto(int64_t M, int64_t K);
 hipError_t launch_norm_grad(const void* dy, int dyt, int64_t M, int64_t K, int64_t lddy, const void* x, int xdt,
                             int64_t ldx, const void* w, int wdt, const float* mean, const float* rstd, int rms,
                             void* dx, int64_t lddx, float* dw, float* db, void* ws, hipStream_t st);

@@ -6,11 +6,14 @@
 //   dl_te  = go p_te (slope_e - sum_i p_ti slope_i)       (sigmoid: times 1 - sigma(l_te))
 // over the T' rows that are not masked out and have a usable logit.
 //
-//   1. k_balance: a wave per row, its logits in registers (lane l: experts
-//      l, l + 64, ...); the p of a wave's rows add up in registers, the ids in
-//      an integer histogram in LDS; a block leaves one partial row of both.
-//   2. k_balance_finish: one block adds the partial rows in their order (the p
-//      in double), and forms slopes and loss.
+//   1. k_balance: a wave per row, its logits in registers (lane l: V adjacent
+//      experts from V l on, one access; 2 x 8 above 512 experts), the next
+//      row's on their way meanwhile; the p of a wave's rows add up in
+//      registers, the ids in an integer histogram in LDS; the block's waves
+//      meet in LDS in their order and leave one partial row.
+//   2. k_balance_finish: a block per 64 experts adds the partial rows in their
+//      order (the p in double) and forms slopes and loss.  (One block for all of
+//      256 experts took 13 us to read half a megabyte.)
 //   3. k_balance_grad: a wave per row again.
 // Bound by reading the logits (and writing their gradient); nothing is added
 // by floating-point atomics, so the results do not depend on an order.
@@ -20,137 +23,303 @@
 
 namespace awqk {
 
-constexpr int kBalWaves = 4;
+constexpr int kBalWaves = 8;           // of k_balance's block
+constexpr int kBalGradWaves = 4;       // of k_balance_grad's
+
+// Experts of lane l: V adjacent ones from V l on, H times, 64 V apart.
+template <int V, int H>
+struct BalMap {
+  static constexpr int N = V * H;
+  static __device__ __forceinline__ int first(int lane, int h) { return (h * 64 + lane) * V; }
+};
+
+// V adjacent values of a row from e on; -inf past its end.
+template <int DT, int V>
+__device__ __forceinline__ void bal_load(const void* p, int64_t row, int e, int E, float* v) {
+  constexpr float off = -__builtin_inff();
+  if (e + V <= E) {
+    if constexpr (DT == DT_F32) {
+      const float* q = reinterpret_cast<const float*>(p) + row + e;
+      if constexpr (V >= 4) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+          const u32x4a4 a = *reinterpret_cast<const u32x4a4*>(q + j);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j + i] = __uint_as_float(a[i]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = q[j];
+      }
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + row + e;
+      uint32_t w[(V + 1) / 2];
+      if constexpr (V == 8) {
+        const u32x4a2 a = *reinterpret_cast<const u32x4a2*>(q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = a[i];
+      } else if constexpr (V == 4) {
+        const u32x2a2 a = *reinterpret_cast<const u32x2a2*>(q);
+        w[0] = a[0];
+        w[1] = a[1];
+      } else if constexpr (V == 2) {
+        w[0] = (uint32_t)q[0] | ((uint32_t)q[1] << 16);
+      } else {
+        w[0] = q[0];
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = j & 1 ? hi_f32<DT>(w[j / 2]) : lo_f32<DT>(w[j / 2]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = e + j < E ? load_any(p, DT, row + e + j) : off;
+  }
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void bal_store(void* p, int64_t row, int e, int E, const float* v) {
+  if constexpr (V >= 4) {
+    if (e + V <= E) {
+      if constexpr (DT == DT_F32) {
+        float* q = reinterpret_cast<float*>(p) + row + e;
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+          u32x4a4 a;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(v[j + i]);
+          *reinterpret_cast<u32x4a4*>(q + j) = a;
+        }
+      } else {
+        uint16_t* q = reinterpret_cast<uint16_t*>(p) + row + e;
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+          u32x2a2 a;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) a[i] = from_f32<DT>(v[j + 2 * i]) | (from_f32<DT>(v[j + 2 * i + 1]) << 16);
+          *reinterpret_cast<u32x2a2*>(q + j) = a;
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (e + j < E) store_any(p, DT, row + e + j, v[j]);
+}
+
+// exp(x) for x <= 0: 2^(x log2 e) with the product's rounding error (and what
+// log2 e leaves of its fp32 value) put back in first order, so that far scores
+// keep fp32's precision.  Past -126 in the exponent the result is 0.
+__device__ __forceinline__ float bal_exp(float x) {
+  constexpr float hi = 1.44269502f, lo = (float)(1.4426950408889634 - (double)1.44269502f);
+  const float p = fmaxf(x, -1000.0f) * hi;       // (-inf: no inf - inf below)
+  const float r = __builtin_fmaf(x > -1000.0f ? x : -1000.0f, hi, -p) + (x > -1000.0f ? x : -1000.0f) * lo;
+  const float e = __builtin_amdgcn_exp2f(p);
+  return __builtin_fmaf(e, r * 0.69314718f, e);
+}
 
 // A row's scores in s (not yet divided by their sum, which is returned; 0: no
 // usable logit) and, for the sigmoid, what is left of one in rest (1 - sigma).
 // -inf and NaN are not usable; +inf counts as the largest float.  Sigmoid
 // scores carry a common factor exp(-min(max l, 0)), so that a row of very low
 // logits does not underflow.
-template <int EPL, bool SIG, bool REST>
-__device__ __forceinline__ float bal_scores(float (&s)[EPL], float (&rest)[EPL]) {
+template <int N, bool SIG, bool REST>
+__device__ __forceinline__ float bal_scores(float (&s)[N], float (&rest)[N]) {
   float mx = -__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
+  for (int i = 0; i < N; ++i) {
     s[i] = s[i] > -__builtin_inff() ? fminf(s[i], 3.4028234663852886e38f) : -__builtin_inff();   // NaN: not greater
     mx = fmaxf(mx, s[i]);
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
+  mx = wave_max(mx);
   if (mx == -__builtin_inff()) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = rest[i] = 0.0f;
+    for (int i = 0; i < N; ++i) s[i] = rest[i] = 0.0f;
     return 0.0f;
   }
   float sum = 0.0f;
-  const float c = SIG ? fminf(mx, 0.0f) : mx, ec = SIG ? expf(c) : 0.0f;
+  const float c = SIG ? fminf(mx, 0.0f) : mx, ec = SIG ? bal_exp(c) : 0.0f;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
+  for (int i = 0; i < N; ++i) {
     if constexpr (SIG) {
       // l >= 0 (then c = 0): 1 / (1 + e^-l);  l < 0: e^(l - c) / (1 + e^(l - c) e^c)
       const float l = s[i];
-      const float a = expf(l >= 0.0f ? -l : l - c);
-      const float d = 1.0f / (l >= 0.0f ? 1.0f + a : __builtin_fmaf(a, ec, 1.0f));
+      const float a = bal_exp(l >= 0.0f ? -l : l - c);
+      const float d = quick_rcp(l >= 0.0f ? 1.0f + a : __builtin_fmaf(a, ec, 1.0f));
       s[i] = l >= 0.0f ? d : a * d;
       if constexpr (REST) rest[i] = l >= 0.0f ? a * d : d;
     } else {
-      s[i] = expf(s[i] - c);
+      s[i] = bal_exp(s[i] - c);
     }
     sum += s[i];
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-  return sum;
+  return wave_sum(sum);
 }
+
+// What the blocks of k_balance_finish leave for the one that ends last.
+struct BalanceEnd {
+  double part[16];       // E <= 1024
+  unsigned done;
+};
 
 struct BalanceArgs {
   const void* logits;
   const int32_t* ids;
   const uint8_t* mask;
-  float* psum;           // [blocks][pitch]
-  int32_t* count;        // [blocks][pitch], the number of counted rows at E
+  float2* partial;       // [blocks][pitch]: sum of p, slots (an integer's bits); at E (the bits of) all slots, rows
+  BalanceEnd* last;
   int64_t T, ldl, pitch;
-  int E, top_k, dt;
+  int E, top_k;
 };
 
-template <int EPL, bool SIG>
+template <int DT, int V, int H, bool SIG>
 __global__ __launch_bounds__(64 * kBalWaves) void k_balance(const BalanceArgs a) {
+  using Map = BalMap<V, H>;
+  constexpr int N = Map::N;
   extern __shared__ int32_t bal_lds[];
-  int32_t* hist = bal_lds;                                       // [E + 1]
-  float* meet = reinterpret_cast<float*>(bal_lds + a.E + 1);     // [kBalWaves][64 EPL]
+  int32_t* hist = bal_lds;                                       // [E + 2]: slots of each expert, of all, rows
+  float* meet = reinterpret_cast<float*>(bal_lds + a.E + 2);     // [kBalWaves][64 N]
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e <= a.E; e += 64 * kBalWaves) hist[e] = 0;
+  for (int e = threadIdx.x; e <= a.E + 1; e += 64 * kBalWaves) hist[e] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.last->done = 0;
   __syncthreads();
-  float acc[EPL];
+  float acc[N], next[N];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * kBalWaves + wv; t < a.T; t += (int64_t)gridDim.x * kBalWaves) {
-    if (a.mask && a.mask[t] == 0) continue;                      // wave-uniform
-    float s[EPL], rest[EPL];
+  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * kBalWaves;
+  int64_t t = (int64_t)blockIdx.x * kBalWaves + wv;
+  int next_id = -1;
+  bool next_on = false;
+  auto fetch = [&](int64_t r) {                                  // row r < T
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 64 * i;
-      s[i] = e < a.E ? load_any(a.logits, a.dt, t * a.ldl + e) : -__builtin_inff();
-    }
-    const int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
-    const float sum = bal_scores<EPL, SIG, false>(s, rest);
+    for (int h = 0; h < H; ++h) bal_load<DT, V>(a.logits, r * a.ldl, Map::first(lane, h), a.E, next + h * V);
+    next_id = lane < a.top_k ? a.ids[r * a.top_k + lane] : -1;
+    next_on = !a.mask || a.mask[r] != 0;
+  };
+  if (t < a.T) fetch(t);
+  for (; t < a.T; t += step) {                                   // wave-uniform
+    float s[N], rest[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = next[i];
+    const int id = next_id;
+    const bool on = next_on;
+    if (t + step < a.T) fetch(t + step);
+    if (!on) continue;
+    const float sum = bal_scores<N, SIG, false>(s, rest);
     if (sum == 0.0f) continue;
     const float inv = 1.0f / sum;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) acc[i] = __builtin_fmaf(s[i], inv, acc[i]);
-    if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
-    if (lane == 0) atomicAdd(&hist[a.E], 1);
+    for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(s[i], inv, acc[i]);
+    const bool named = id >= 0 && id < a.E;
+    if (named) atomicAdd(&hist[id], 1);
+    const int all = __popcll(__ballot(named));
+    if (lane == 0) {
+      atomicAdd(&hist[a.E], all);
+      atomicAdd(&hist[a.E + 1], 1);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) meet[wv * 64 * EPL + 64 * i + lane] = acc[i];
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int j = 0; j < V; ++j) meet[wv * 64 * N + Map::first(lane, h) + j] = acc[h * V + j];
   __syncthreads();
   for (int e = threadIdx.x; e <= a.E; e += 64 * kBalWaves) {
-    a.count[blockIdx.x * a.pitch + e] = hist[e];
+    float2 v = make_float2(0.0f, __int_as_float(hist[e]));
     if (e < a.E) {
-      float t = 0.0f;
-      for (int w = 0; w < kBalWaves; ++w) t += meet[w * 64 * EPL + e];
-      a.psum[blockIdx.x * a.pitch + e] = t;
+#pragma unroll
+      for (int w = 0; w < kBalWaves; ++w) v.x += meet[w * 64 * N + e];
+    } else {
+      v = make_float2(__int_as_float(hist[a.E]), __int_as_float(hist[a.E + 1]));
     }
+    a.partial[blockIdx.x * a.pitch + e] = v;
   }
 }
 
-// One block; thread e takes expert e.
-__global__ __launch_bounds__(1024) void k_balance_finish(const float* __restrict__ psum, const int32_t* __restrict__ count,
-                                                         int blocks, int64_t pitch, int E, double coef,
-                                                         float* __restrict__ loss, int32_t* __restrict__ counts,
-                                                         float* __restrict__ slope) {
-  __shared__ double part[16];
-  __shared__ long long total[16];
-  const int e = threadIdx.x, lane = e & 63, wv = e >> 6;
+// Block j adds the partial rows of experts 64 j .. 64 j + 63 in their order (16
+// waves, every sixteenth row each, meeting in LDS in their order) and forms
+// their counts and slopes; n and the number of rows come from the last column
+// (slots, rows), which every block adds up for itself.  The parts of the loss
+// meet in the block that ends last, again in their order: `last` holds the
+// parts and a count of the blocks that are done, zeroed by k_balance.
+__global__ __launch_bounds__(1024) void k_balance_finish(const float2* __restrict__ partial, int blocks, int64_t pitch,
+                                                         int E, double coef, float* __restrict__ loss,
+                                                         int32_t* __restrict__ counts, float* __restrict__ slope,
+                                                         BalanceEnd* __restrict__ last) {
+  __shared__ double p_s[16][64];
+  __shared__ int32_t c_s[16][64];
+  __shared__ long long tot[2][16];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
+  const int ec = e < E ? e : 0;
   double p = 0.0;
-  long long c = 0, rows = 0;
-  if (e < E)
-    for (int b = 0; b < blocks; ++b) {
-      p += psum[b * pitch + e];
-      c += count[b * pitch + e];
+  int32_t c = 0;
+  long long slots = 0, rows = 0;
+  constexpr int U = 16;                                          // partial rows in flight
+  for (int b0 = wv; b0 < blocks; b0 += 16 * U) {
+    float2 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + 16 * u;                                 // past the end: the first row, not used
+      v[u] = partial[(int64_t)(b < blocks ? b : 0) * pitch + ec];
     }
-  for (int b = 0; b < blocks; ++b) rows += count[b * pitch + E];
-  long long n = c;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off);
-  if (lane == 0) total[wv] = n;
+    for (int u = 0; u < U; ++u) {
+      const bool ok = b0 + 16 * u < blocks;
+      p += ok ? v[u].x : 0.0f;
+      c += ok ? __float_as_int(v[u].y) : 0;
+    }
+  }
+  for (int b = threadIdx.x; b < blocks; b += 1024) {
+    const float2 v = partial[(int64_t)b * pitch + E];
+    slots += __float_as_int(v.x);
+    rows += __float_as_int(v.y);
+  }
+  p_s[wv][lane] = p;
+  c_s[wv][lane] = c;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    slots += __shfl_xor(slots, off);
+    rows += __shfl_xor(rows, off);
+  }
+  if (lane == 0) {
+    tot[0][wv] = slots;
+    tot[1][wv] = rows;
+  }
   __syncthreads();
-  n = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) n += total[w];
-  const double sl = n > 0 && rows > 0 ? coef * (double)E * (double)c / ((double)n * (double)rows) : 0.0;
+  if (wv > 0) return;
+  for (int w = 1; w < 16; ++w) {
+    p += p_s[w][lane];
+    c += c_s[w][lane];
+    slots += tot[0][w];
+    rows += tot[1][w];
+  }
+  const double sl = slots > 0 && rows > 0 ? coef * (double)E * (double)c / ((double)slots * (double)rows) : 0.0;
   double l = e < E ? sl * p : 0.0;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off);
-  if (lane == 0) part[wv] = l;
-  __syncthreads();
   if (e < E) {
-    counts[e] = (int32_t)c;
+    counts[e] = c;
     slope[e] = (float)sl;
   }
-  if (e == 0) {
-    l = 0.0;
-    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) l += part[w];
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off);
+  if (lane > 0) return;
+  if (gridDim.x == 1) {
     loss[0] = (float)l;
+    return;
+  }
+  __hip_atomic_store(&last->part[blockIdx.x], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (__hip_atomic_fetch_add(&last->done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) != gridDim.x - 1) return;
+  l = 0.0;
+  for (unsigned j = 0; j < gridDim.x; ++j) l += __hip_atomic_load(&last->part[j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  loss[0] = (float)l;
+}
+
+// No tokens: zeros.
+__global__ __launch_bounds__(256) void k_balance_none(int E, float* __restrict__ loss, int32_t* __restrict__ counts,
+                                                      float* __restrict__ slope) {
+  const int e = blockIdx.x * 256 + threadIdx.x;
+  if (e == 0) loss[0] = 0.0f;
+  if (e < E) {
+    counts[e] = 0;
+    slope[e] = 0.0f;
   }
 }
 
@@ -161,62 +330,101 @@ struct BalanceGradArgs {
   const uint8_t* mask;
   void* dl;
   int64_t T, ldl, ldd;
-  int E, dt;
+  int E;
 };
 
-template <int EPL, bool SIG>
-__global__ __launch_bounds__(64 * kBalWaves) void k_balance_grad(const BalanceGradArgs a) {
+template <int DT, int V, int H, bool SIG>
+__global__ __launch_bounds__(64 * kBalGradWaves) void k_balance_grad(const BalanceGradArgs a) {
+  using Map = BalMap<V, H>;
+  constexpr int N = Map::N;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t step = (int64_t)gridDim.x * kBalGradWaves;
+  int64_t t = (int64_t)blockIdx.x * kBalGradWaves + wv;
+  float next[N];
+  auto fetch = [&](int64_t r) {
+    const bool on = !a.mask || a.mask[r] != 0;                   // wave-uniform
+#pragma unroll
+    for (int h = 0; h < H; ++h) bal_load<DT, V>(a.logits, r * a.ldl, Map::first(lane, h), on ? a.E : 0, next + h * V);
+  };
+  if (t < a.T) fetch(t);
   // the slopes about their mean, which the gradient does not see: what is left
   // cancels little in slope - sum p slope
-  float d[EPL];
+  float d[N];
   float mean = 0.0f;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 64 * i;
-    d[i] = e < a.E ? a.slope[e] : 0.0f;
-    mean += d[i];
-  }
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = Map::first(lane, h) + j;
+      d[h * V + j] = e < a.E ? a.slope[e] : 0.0f;
+      mean += d[h * V + j];
+    }
+  const float go = a.go ? a.go[0] : 1.0f;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) mean += __shfl_xor(mean, off);
   mean /= (float)a.E;
-  const float go = a.go ? a.go[0] : 1.0f;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) d[i] -= mean;
-  for (int64_t t = (int64_t)blockIdx.x * kBalWaves + wv; t < a.T; t += (int64_t)gridDim.x * kBalWaves) {
-    float s[EPL], rest[EPL], o[EPL];
-    const bool on = !a.mask || a.mask[t] != 0;
+  for (int i = 0; i < N; ++i) d[i] -= mean;
+  for (; t < a.T; t += step) {
+    float s[N], rest[N];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 64 * i;
-      s[i] = on && e < a.E ? load_any(a.logits, a.dt, t * a.ldl + e) : -__builtin_inff();
-    }
-    const float sum = bal_scores<EPL, SIG, SIG>(s, rest);
+    for (int i = 0; i < N; ++i) s[i] = next[i];
+    if (t + step < a.T) fetch(t + step);
+    const float sum = bal_scores<N, SIG, SIG>(s, rest);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     float q = 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
+    for (int i = 0; i < N; ++i) {
       s[i] *= inv;
       q = __builtin_fmaf(s[i], d[i], q);
     }
+    q = wave_sum(q);
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) q += __shfl_xor(q, off);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
+    for (int i = 0; i < N; ++i) {
       // a score of 0 (masked, off, or far below) has no gradient, whatever go is
-      o[i] = s[i] > 0.0f ? go * s[i] * (d[i] - q) : 0.0f;
-      if constexpr (SIG) o[i] *= rest[i];
-      const int e = lane + 64 * i;
-      if (e < a.E) store_any(a.dl, a.dt, t * a.ldd + e, o[i]);
+      const float o = s[i] > 0.0f ? go * s[i] * (d[i] - q) : 0.0f;
+      s[i] = SIG ? o * rest[i] : o;
     }
+#pragma unroll
+    for (int h = 0; h < H; ++h) bal_store<DT, V>(a.dl, t * a.ldd, Map::first(lane, h), a.E, s + h * V);
   }
 }
 
 inline int64_t balance_blocks(int64_t T) {
   const int64_t want = (T + kBalWaves - 1) / kBalWaves;
-  return want < 128 ? want : 128;
+  return want < 256 ? want : 256;
 }
 inline int64_t balance_pitch(int64_t E) { return (E + 1 + 63) / 64 * 64; }
+
+template <int DT, int V, int H>
+hipError_t balance_launch(const BalanceArgs& a, bool sigmoid, int64_t blocks, hipStream_t st) {
+  const size_t lds = (size_t)(a.E + 2 + kBalWaves * 64 * V * H) * 4;
+  const dim3 grid((unsigned)blocks), block(64 * kBalWaves);
+  if (sigmoid) hipLaunchKernelGGL((k_balance<DT, V, H, true>), grid, block, lds, st, a);
+  else hipLaunchKernelGGL((k_balance<DT, V, H, false>), grid, block, lds, st, a);
+  return hipGetLastError();
+}
+template <int DT, int V, int H>
+hipError_t balance_launch(const BalanceGradArgs& a, bool sigmoid, int64_t blocks, hipStream_t st) {
+  const dim3 grid((unsigned)blocks), block(64 * kBalGradWaves);
+  if (sigmoid) hipLaunchKernelGGL((k_balance_grad<DT, V, H, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_balance_grad<DT, V, H, false>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+template <int DT, class A>
+hipError_t balance_dispatch(const A& a, bool sigmoid, int64_t blocks, hipStream_t st) {
+  if (a.E <= 64) return balance_launch<DT, 1, 1>(a, sigmoid, blocks, st);
+  if (a.E <= 128) return balance_launch<DT, 2, 1>(a, sigmoid, blocks, st);
+  if (a.E <= 256) return balance_launch<DT, 4, 1>(a, sigmoid, blocks, st);
+  if (a.E <= 512) return balance_launch<DT, 8, 1>(a, sigmoid, blocks, st);
+  return balance_launch<DT, 8, 2>(a, sigmoid, blocks, st);
+}
+template <class A>
+hipError_t balance_typed(const A& a, int dt, bool sigmoid, int64_t blocks, hipStream_t st) {
+  if (dt == DT_F16) return balance_dispatch<DT_F16>(a, sigmoid, blocks, st);
+  if (dt == DT_BF16) return balance_dispatch<DT_BF16>(a, sigmoid, blocks, st);
+  return balance_dispatch<DT_F32>(a, sigmoid, blocks, st);
+}
 
 }  // namespace awqk
 
@@ -224,7 +432,7 @@ namespace awq {
 
 size_t balance_ws_bytes(int64_t T, int64_t E) {
   if (T <= 0 || E <= 0) return 0;
-  return align_up((size_t)(awqk::balance_blocks(T) * awqk::balance_pitch(E)) * 8, 256);
+  return align_up((size_t)(awqk::balance_blocks(T) * awqk::balance_pitch(E)) * 8, 256) + 256;   // and a BalanceEnd
 }
 
 hipError_t launch_balance(const void* logits, int dt, int64_t T, int64_t E, int64_t ldl, const int32_t* ids, int top_k,
@@ -232,47 +440,26 @@ hipError_t launch_balance(const void* logits, int dt, int64_t T, int64_t E, int6
                           void* ws, hipStream_t st) {
   using namespace awqk;
   const int64_t blocks = T > 0 ? balance_blocks(T) : 0, pitch = balance_pitch(E);
-  float* psum = (float*)ws;
-  int32_t* count = (int32_t*)(psum + blocks * pitch);
-  if (blocks > 0) {
-    const BalanceArgs a{logits, ids, mask, psum, count, T, ldl, pitch, (int)E, top_k, dt};
-#define AWQ_B(EPL)                                                                                              \
-  {                                                                                                             \
-    const size_t lds = (size_t)(E + 1 + kBalWaves * 64 * EPL) * 4;                                              \
-    if (sigmoid) hipLaunchKernelGGL((k_balance<EPL, true>), dim3((unsigned)blocks), dim3(64 * kBalWaves), lds, st, a); \
-    else hipLaunchKernelGGL((k_balance<EPL, false>), dim3((unsigned)blocks), dim3(64 * kBalWaves), lds, st, a); \
+  if (blocks == 0) {
+    hipLaunchKernelGGL(k_balance_none, dim3((unsigned)((E + 255) / 256)), dim3(256), 0, st, (int)E, loss, counts, slope);
+    return hipGetLastError();
   }
-    if (E <= 64) AWQ_B(1)
-    else if (E <= 128) AWQ_B(2)
-    else if (E <= 256) AWQ_B(4)
-    else if (E <= 512) AWQ_B(8)
-    else AWQ_B(16)
-#undef AWQ_B
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(k_balance_finish, dim3(1), dim3((unsigned)((E + 63) / 64 * 64)), 0, st, psum, count, (int)blocks,
-                     pitch, (int)E, coef, loss, counts, slope);
+  BalanceEnd* last = (BalanceEnd*)ws;
+  static_assert(sizeof(BalanceEnd) <= 256, "ahead of the partial rows");
+  float2* partial = (float2*)((char*)ws + 256);
+  const hipError_t e = balance_typed(BalanceArgs{logits, ids, mask, partial, last, T, ldl, pitch, (int)E, top_k}, dt,
+                                     sigmoid != 0, blocks, st);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_balance_finish, dim3((unsigned)((E + 63) / 64)), dim3(1024), 0, st, partial, (int)blocks, pitch,
+                     (int)E, coef, loss, counts, slope, last);
   return hipGetLastError();
 }
 
 hipError_t launch_balance_grad(const void* logits, int dt, int64_t T, int64_t E, int64_t ldl, const float* slope,
                                const float* go, const uint8_t* mask, int sigmoid, void* dl, int64_t ldd, hipStream_t st) {
   using namespace awqk;
-  const BalanceGradArgs a{logits, slope, go, mask, dl, T, ldl, ldd, (int)E, dt};
-  const int64_t want = (T + kBalWaves - 1) / kBalWaves, blocks = want < 2048 ? want : 2048;
-#define AWQ_BG(EPL)                                                                                             \
-  {                                                                                                             \
-    if (sigmoid) hipLaunchKernelGGL((k_balance_grad<EPL, true>), dim3((unsigned)blocks), dim3(64 * kBalWaves), 0, st, a); \
-    else hipLaunchKernelGGL((k_balance_grad<EPL, false>), dim3((unsigned)blocks), dim3(64 * kBalWaves), 0, st, a); \
-  }
-  if (E <= 64) AWQ_BG(1)
-  else if (E <= 128) AWQ_BG(2)
-  else if (E <= 256) AWQ_BG(4)
-  else if (E <= 512) AWQ_BG(8)
-  else AWQ_BG(16)
-#undef AWQ_BG
-  return hipGetLastError();
+  const int64_t want = (T + kBalGradWaves - 1) / kBalGradWaves, blocks = want < 2048 ? want : 2048;
+  return balance_typed(BalanceGradArgs{logits, slope, go, mask, dl, T, ldl, ldd, (int)E}, dt, sigmoid != 0, blocks, st);
 }
 
 }  // namespace awq

@@ -2,6 +2,8 @@
 // residual applied in fp32 to a finished sum, and the activations' slopes.
 #pragma once
 
+#include <type_traits>
+
 #include "awq_device.h"
 #include "awq_internal.h"
 
@@ -16,6 +18,28 @@ template <class EP>
 constexpr bool kHasEpi = false;
 template <>
 inline constexpr bool kHasEpi<Epilogue> = true;
+
+// Sum and maximum over a wave, in every lane: four exchanges within the 16-lane
+// rows and two swaps between them, no LDS traffic (a shuffle each would be six
+// round trips through LDS).
+__device__ __forceinline__ float wave_sum(float v) {
+  v += quad_xor1(v);
+  v += quad_xor2(v);
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));   // row_half_mirror
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));   // row_mirror
+  v = pair_sum16(v, v);
+  return pair_sum32(v, v);
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, quad_xor1(v));
+  v = fmaxf(v, quad_xor2(v));
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false)));
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false)));
+  const auto r16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(r16[0]), __uint_as_float(r16[1]));
+  const auto r32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r32[0]), __uint_as_float(r32[1]));
+}
 
 // Element i of an array of type dt.
 __device__ __forceinline__ float load_any(const void* p, int dt, int64_t i) {
@@ -81,26 +105,77 @@ __device__ __forceinline__ void store8_any(void* p, int dt, int64_t i, int cnt, 
   }
 }
 
-// 1 / (1 + exp(-z))
-__device__ __forceinline__ float logistic(float z) { return 1.0f / (1.0f + expf(-z)); }
-
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f;     // sqrt(2 / pi)
 constexpr float kGeluK = 0.044715f;
-constexpr float kSqrtHalf = 0.7071067811865476f;
 constexpr float kPhi0 = 0.3989422804014327f;      // 1 / sqrt(2 pi)
+
+// 1 / d for d in [1, 2^20]: the hardware's estimate and one Newton step.  (The
+// IEEE division and expf, erfcf of the device library take 2.5 times as long:
+// the epilogue's backward pass over 2048 x 11008 values was bound by them.)
+__device__ __forceinline__ float quick_rcp(float d) {
+  const float r = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
+// s = 1 / (1 + exp(-z)) and t = 1 - s, both without cancellation.  The
+// exponential's argument is rounded: |z| 2^-24 of the smaller of the two.
+__device__ __forceinline__ void logistic(float z, float& s, float& t) {
+  const float a = __builtin_amdgcn_exp2f(-kLog2E * fabsf(z));
+  const float r = quick_rcp(1.0f + a), q = a * r;
+  s = z < 0.0f ? q : r;
+  t = z < 0.0f ? r : q;
+}
+
+// e = exp(-z^2 / 2) and the normal distribution's Phi(z).  Its tail is
+// Phi(-|z|) = e P(t) with t = 1 / (1 + 0.3 |z| / sqrt 2): erfc(x) exp(x^2) / 2 as
+// a polynomial of degree 9 in t, fitted over x in [0, 13] for the least
+// largest relative error (2.1e-8; 5e-7 as evaluated in fp32).
+__device__ __forceinline__ void normal_tail(float z, float& e, float& phi) {
+  const float t = quick_rcp(__builtin_fmaf(0.21213203f, fminf(fabsf(z), 1e4f), 1.0f));
+  float p = -0.06526048481464386f;
+  p = __builtin_fmaf(p, t, 0.24551217257976532f);
+  p = __builtin_fmaf(p, t, -0.26261571049690247f);
+  p = __builtin_fmaf(p, t, 0.2825837731361389f);
+  p = __builtin_fmaf(p, t, -0.05466487631201744f);
+  p = __builtin_fmaf(p, t, 0.11145494133234024f);
+  p = __builtin_fmaf(p, t, 0.0727686658501625f);
+  p = __builtin_fmaf(p, t, 0.08566296100616455f);
+  p = __builtin_fmaf(p, t, 0.08455654978752136f);
+  p = __builtin_fmaf(p, t, 2.01171861e-06f);
+  e = __builtin_amdgcn_exp2f(-0.5f * kLog2E * z * z);
+  p *= e;
+  phi = z < 0.0f ? p : 1.0f - p;
+}
 
 // act(z).  Below -1e4 every one of them is 0 in fp32; said here, -inf gives its
 // limit and not -inf 0.
 __device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case awq::LINEAR_RELU: return z <= 0.0f ? 0.0f : z;
-    case awq::LINEAR_GELU: return z < -1e4f ? -0.0f : 0.5f * z * erfcf(-z * kSqrtHalf);
-    // 0.5 z (1 + tanh u) = z / (1 + exp(-2 u)),  u = sqrt(2 / pi) (z + 0.044715 z^3)
-    case awq::LINEAR_GELU_TANH:
-      return z < -1e4f ? -0.0f : z * logistic(2.0f * kGeluC * z * __builtin_fmaf(kGeluK * z, z, 1.0f));
-    case awq::LINEAR_SILU: return z < -1e4f ? -0.0f : z * logistic(z);
-    default: return z;
+  if (act == awq::LINEAR_NONE) return z;
+  if (act == awq::LINEAR_RELU) return z <= 0.0f ? 0.0f : z;
+  float s, t;
+  if (act == awq::LINEAR_GELU) {
+    normal_tail(z, t, s);
+  } else {
+    // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)),  u = sqrt(2 / pi) (z + 0.044715 z^3)
+    const float u = act == awq::LINEAR_GELU_TANH ? 2.0f * kGeluC * z * __builtin_fmaf(kGeluK * z, z, 1.0f) : z;
+    logistic(u, s, t);
   }
+  return z < -1e4f ? -0.0f : z * s;
+}
+
+// act of sixteen values, the choice made once.
+__device__ __forceinline__ void act_values(int act, float (&z)[4][4]) {
+  auto all = [&](auto kind) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[v][j] = act_value(decltype(kind)::value, z[v][j]);
+  };
+  if (act == awq::LINEAR_RELU) all(std::integral_constant<int, awq::LINEAR_RELU>{});
+  else if (act == awq::LINEAR_GELU) all(std::integral_constant<int, awq::LINEAR_GELU>{});
+  else if (act == awq::LINEAR_GELU_TANH) all(std::integral_constant<int, awq::LINEAR_GELU_TANH>{});
+  else if (act == awq::LINEAR_SILU) all(std::integral_constant<int, awq::LINEAR_SILU>{});
 }
 
 // act'(z).  Past 1e4 they are 0 and 1 in fp32; held there, infinities give
@@ -108,44 +183,95 @@ __device__ __forceinline__ float act_value(int act, float z) {
 __device__ __forceinline__ float act_slope(int act, float z) {
   if (act == awq::LINEAR_RELU) return z <= 0.0f ? 0.0f : (z > 0.0f ? 1.0f : z);   // NaN stays
   z = z > 1e4f ? 1e4f : z < -1e4f ? -1e4f : z;
+  float s, t;
   if (act == awq::LINEAR_GELU) {
-    const float d = kPhi0 * expf(-0.5f * z * z);
-    return __builtin_fmaf(z, d, 0.5f * erfcf(-z * kSqrtHalf));
+    normal_tail(z, t, s);
+    return __builtin_fmaf(z * kPhi0, t, s);
   }
+  float u = z, du = 1.0f;
   if (act == awq::LINEAR_GELU_TANH) {
-    const float u2 = 2.0f * kGeluC * z * __builtin_fmaf(kGeluK * z, z, 1.0f);
-    const float s = logistic(u2), t = logistic(-u2);        // t = 1 - s without its cancellation
-    const float du2 = 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluK * z, z, 1.0f);
-    return __builtin_fmaf(z * du2, s * t, s);
+    u = 2.0f * kGeluC * z * __builtin_fmaf(kGeluK * z, z, 1.0f);
+    du = 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluK * z, z, 1.0f);
   }
-  const float s = logistic(z), t = logistic(-z);
-  return s * __builtin_fmaf(z, t, 1.0f);
+  logistic(u, s, t);
+  return __builtin_fmaf(z * du, s * t, s);
 }
 
-// One output: z the finished sum of (row m, column n).
-__device__ __forceinline__ void epi_store(const Epilogue& ep, void* y, int64_t ldy, int64_t m, int64_t n, float z) {
-  if (ep.bias) z += load_any(ep.bias, ep.bdt, n);
+// One output (row m, column n) in two steps: what it needs from memory, asked
+// for ahead of the work that ends in its sum (a load behind an earlier output's
+// store would wait for it: with both at the store the batch-1 product of 4096
+// -> 11008 took 8.1 us), and the finished sum z through the epilogue.
+struct EpiIn {
+  float bias, res;
+};
+template <class EP>
+__device__ __forceinline__ EpiIn epi_fetch(const EP& ep, bool live, int64_t m, int64_t n) {
+  EpiIn f{0.0f, 0.0f};
+  if constexpr (kHasEpi<EP>) {
+    if (ep.bias && live) f.bias = load_any(ep.bias, ep.bdt, n);
+    if (ep.res && live) f.res = load_any(ep.res, ep.ydt, m * ep.ldr + n);
+  }
+  return f;
+}
+__device__ __forceinline__ void epi_store(const Epilogue& ep, void* y, int64_t ldy, int64_t m, int64_t n, float z,
+                                          const EpiIn& f) {
+  z += f.bias;
   if (ep.pre) store_any(ep.pre, ep.ydt, m * ep.ldp + n, z);
-  float o = act_value(ep.act, z);
-  if (ep.res) o += load_any(ep.res, ep.ydt, m * ep.ldr + n);
-  store_any(y, ep.ydt, m * ldy + n, o);
+  store_any(y, ep.ydt, m * ldy + n, act_value(ep.act, z) + f.res);
 }
 
-// Columns n .. n + cnt - 1 of row m, their bias in b.
-__device__ __forceinline__ void epi_store8(const Epilogue& ep, void* y, int64_t ldy, int64_t m, int64_t n, int cnt,
-                                           float (&z)[8], const float (&b)[8]) {
-  float r[8];
-  if (ep.res) load8_any(ep.res, ep.ydt, m * ep.ldr + n, cnt, r);
+// Elements i .. i + cnt - 1 (cnt <= 4; the others read as 0).
+__device__ __forceinline__ void load4_any(const void* p, int dt, int64_t i, int cnt, float (&v)[4]) {
+  if (cnt >= 4) {
+    if (dt == DT_F32) {
+      const u32x4a4 a = *reinterpret_cast<const u32x4a4*>(reinterpret_cast<const float*>(p) + i);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) z[j] += b[j];
-  if (ep.pre) store8_any(ep.pre, ep.ydt, m * ep.ldp + n, cnt, z);
+      for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(a[j]);
+    } else {
+      const u32x2a2 a = *reinterpret_cast<const u32x2a2*>(reinterpret_cast<const uint16_t*>(p) + i);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) z[j] = act_value(ep.act, z[j]);
-  if (ep.res) {
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t w = a[j];
+        v[2 * j] = dt == DT_F16 ? f16_to_f32(w & 0xFFFFu) : __uint_as_float(w << 16);
+        v[2 * j + 1] = dt == DT_F16 ? f16_to_f32(w >> 16) : __uint_as_float(w & 0xFFFF0000u);
+      }
+    }
+  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] += r[j];
+    for (int j = 0; j < 4; ++j) v[j] = j < cnt ? load_any(p, dt, i + j) : 0.0f;
   }
-  store8_any(y, ep.ydt, m * ldy + n, cnt, z);
+}
+__device__ __forceinline__ void store4_any(void* p, int dt, int64_t i, int cnt, const float (&v)[4]) {
+  if (cnt >= 4) {
+    if (dt == DT_F32) {
+      u32x4a4 a;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = __float_as_uint(v[j]);
+      *reinterpret_cast<u32x4a4*>(reinterpret_cast<float*>(p) + i) = a;
+    } else {
+      u32x2a2 a;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        a[j] = dt == DT_F16 ? f32_to_f16_bits(v[2 * j]) | (f32_to_f16_bits(v[2 * j + 1]) << 16)
+                            : f32_to_bf16_bits(v[2 * j]) | (f32_to_bf16_bits(v[2 * j + 1]) << 16);
+      *reinterpret_cast<u32x2a2*>(reinterpret_cast<uint16_t*>(p) + i) = a;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < cnt) store_any(p, dt, i + j, v[j]);
+  }
+}
+
+// Columns n .. n + cnt - 1 of row m; z with its bias.
+__device__ __forceinline__ void epi_store4(const Epilogue& ep, void* y, int64_t ldy, int64_t m, int64_t n, int cnt,
+                                           float (&z)[4]) {
+  float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (ep.res) load4_any(ep.res, ep.ydt, m * ep.ldr + n, cnt, r);
+  if (ep.pre) store4_any(ep.pre, ep.ydt, m * ep.ldp + n, cnt, z);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) z[j] = act_value(ep.act, z[j]) + r[j];
+  store4_any(y, ep.ydt, m * ldy + n, cnt, z);
 }
 
 // ---- weights rounded once -------------------------------------------------------

@@ -24,8 +24,8 @@ __device__ __forceinline__ void store_y1(void* y, int64_t idx, float v) {
 
 // A finished row sum: stored, or through the epilogue.
 template <int YDT, class EP>
-__device__ __forceinline__ void finish_y1(const EP& ep, void* y, int64_t row, float v) {
-  if constexpr (kHasEpi<EP>) epi_store(ep, y, 0, 0, row, v);
+__device__ __forceinline__ void finish_y1(const EP& ep, void* y, int64_t row, float v, const EpiIn& f) {
+  if constexpr (kHasEpi<EP>) epi_store(ep, y, 0, 0, row, v, f);
   else store_y1<YDT>(y, row, v);
 }
 
@@ -173,6 +173,9 @@ __global__ __launch_bounds__(1024) void k_gemv1_rows(
   u32x4 sx[NS];
   f32x4 sr0[NS], sr1[NS];
   stage_load<DT, HAS_R, NS>(x, r, K, sx, sr0, sr1);
+  // what the epilogue of the row this thread finishes needs
+  const int64_t fin = (int64_t)blockIdx.x * rowsb + threadIdx.x;
+  const EpiIn mine = epi_fetch(ep, (int64_t)threadIdx.x < rowsb && fin < N, 0, fin);
   // ---- 1. weights, steps, zero points (branch-free: rows clamped, masked later)
   u32x4 wq[UL];
   uint32_t sraw[UL], zraw[UL];
@@ -242,7 +245,7 @@ __global__ __launch_bounds__(1024) void k_gemv1_rows(
     float tot = 0.0f;
     for (int k2 = 0; k2 < nks; ++k2) tot += part[k2 * rowsb + t];
     const int64_t row = (int64_t)blockIdx.x * rowsb + t;
-    if (row < N) finish_y1<YDT>(ep, y, row, tot);
+    if (row < N) finish_y1<YDT>(ep, y, row, tot, t < (int)blockDim.x ? mine : epi_fetch(ep, true, 0, row));
   }
 }
 
@@ -314,6 +317,10 @@ __global__ __launch_bounds__(1024) void k_gemv1_cu(
       zb[slot][c] = __builtin_amdgcn_raw_buffer_load_b8(zrs, ok ? rl * G32 + g : kBufferOob, 0, 0);
     }
   };
+  // what the epilogue needs: with one K slice lane l holds the wave's row l (the
+  // rows past 64 fetch theirs late), else thread t the block's row t
+  const int64_t fin = nks == 1 ? rg + (int64_t)nrg * lane : (int64_t)threadIdx.x;
+  const EpiIn mine = epi_fetch(ep, nks == 1 ? lane < nj : fin < nrows, 0, r0 + fin);
 #pragma unroll
   for (int d = 0; d < D; ++d) load_row(d, d);
   __builtin_amdgcn_sched_barrier(0);
@@ -374,8 +381,10 @@ __global__ __launch_bounds__(1024) void k_gemv1_cu(
       v = row16_sum(v);
       constexpr int LB = D >= 3 ? 2 : D == 2 ? 1 : 0;
       const int jd = j0 + (lane >> (6 - LB));
+      EpiIn f{0.0f, 0.0f};
+      if constexpr (kHasEpi<EP>) f = EpiIn{__shfl(mine.bias, jd & 63), __shfl(mine.res, jd & 63)};
       if ((lane & ((64 >> LB) - 1)) == 0 && jd < nj && jd < j0 + D) {
-        if (nks == 1) finish_y1<YDT>(ep, y, r0 + rg + nrg * jd, v);   // one K slice: the row is complete
+        if (nks == 1) finish_y1<YDT>(ep, y, r0 + rg + nrg * jd, v, jd < 64 ? f : epi_fetch(ep, true, 0, r0 + rg + nrg * jd));   // one K slice: the row is complete
         else part[ks * rows_max + rg + nrg * jd] = v;
       }
       j0 += D;
@@ -388,7 +397,7 @@ __global__ __launch_bounds__(1024) void k_gemv1_cu(
   for (int t = threadIdx.x; t < nrows; t += blockDim.x) {
     float tot = 0.0f;
     for (int k2 = 0; k2 < nks; ++k2) tot += part[k2 * rows_max + t];
-    finish_y1<YDT>(ep, y, r0 + t, tot);
+    finish_y1<YDT>(ep, y, r0 + t, tot, t < (int)blockDim.x ? mine : epi_fetch(ep, true, 0, r0 + t));
   }
 }
 

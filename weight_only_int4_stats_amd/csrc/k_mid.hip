@@ -69,8 +69,8 @@ __device__ __forceinline__ u32x4 mid_dequant(uint32_t w, f16x2 c24, f16x2 c20, f
 
 // A finished sum: stored, or through the epilogue.
 template <int YDT, class EP>
-__device__ __forceinline__ void finish_ym(const EP& ep, void* y, int64_t ldy, int64_t m, int64_t n, float v) {
-  if constexpr (kHasEpi<EP>) epi_store(ep, y, ldy, m, n, v);
+__device__ __forceinline__ void finish_ym(const EP& ep, void* y, int64_t ldy, int64_t m, int64_t n, float v, const EpiIn& f) {
+  if constexpr (kHasEpi<EP>) epi_store(ep, y, ldy, m, n, v, f);
   else store_ym<YDT>(y, m * ldy + n, v);
 }
 
@@ -235,12 +235,14 @@ __global__ __launch_bounds__(64 * kMidWaves) void k_gemm_mid(
     const int orr = j & 15, otok = (j >> 4) & 15, tg = j >> 8;
     const int orow = (tg / TG) * 16 + orr, m = (tg % TG) * 16 + otok;
     if (orow < nrows && m < M) {
+      EpiIn f{0.0f, 0.0f};
+      if constexpr (!SPLIT) f = epi_fetch(ep, true, m, n0 + orow);
       float tot = 0.0f;
 #pragma unroll
       for (int w = 0; w < kMidWaves; ++w) tot += red[((size_t)w * T * TG + tg) * TILE + otok * kMidPad + orr];
       const int64_t n = n0 + orow;
       if constexpr (SPLIT) partial[((int64_t)bs * M + m) * N + n] = tot;
-      else finish_ym<YDT>(ep, y, ldy, m, n, ldexpf(tot, -(pm[m] + e_s[orow])));
+      else finish_ym<YDT>(ep, y, ldy, m, n, ldexpf(tot, -(pm[m] + e_s[orow])), f);
     }
   }
 }
@@ -254,9 +256,10 @@ __global__ __launch_bounds__(256) void k_mid_reduce(const float* __restrict__ pa
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)M * N) return;
   const int64_t m = i / N, n = i - m * N;
+  const EpiIn f = epi_fetch(ep, true, m, n);
   float tot = 0.0f;
   for (int s = 0; s < S; ++s) tot += partial[(int64_t)s * M * N + i];
-  finish_ym<YDT>(ep, y, ldy, m, n, ldexpf(tot, -(pm[m] + en[n])));
+  finish_ym<YDT>(ep, y, ldy, m, n, ldexpf(tot, -(pm[m] + en[n])), f);
 }
 
 struct MidPlan {

@@ -21,9 +21,7 @@ namespace awqk {
 template <int T, int NV>
 __device__ __forceinline__ void group_sum(float (&v)[NV], float (*red)[16][NV], int turn) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v[i] += __shfl_xor(v[i], off);
+  for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
   if constexpr (T > 64) {
     const int wv = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -172,14 +170,33 @@ struct NormGradArgs {
   int dyt, wdt;
 };
 
-// 1024 threads: RB = 1024 / T rows at a time, KEEP chunks of eight values per
-// lane.  Block b takes the rows b RB + i, (b + grid) RB + i, ...
-template <int XDT, int T, int KEEP, bool RMS>
-__global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a) {
-  constexpr int RB = 1024 / T;
+// Sums over the W waves of a row group, as group_sum with W known at run time.
+__device__ __forceinline__ void waves_sum(float (&v)[2], float (*red)[16][2], int turn, int w0, int W) {
+  v[0] = wave_sum(v[0]);
+  v[1] = wave_sum(v[1]);
+  if (W == 1) return;                                            // block-uniform
+  if ((threadIdx.x & 63) == 0) {
+    red[turn][threadIdx.x >> 6][0] = v[0];
+    red[turn][threadIdx.x >> 6][1] = v[1];
+  }
+  __syncthreads();
+  v[0] = red[turn][w0][0];
+  v[1] = red[turn][w0][1];
+  for (int w = 1; w < W; ++w) {
+    v[0] += red[turn][w0 + w][0];
+    v[1] += red[turn][w0 + w][1];
+  }
+}
+
+// RB row groups of W waves each (W RB <= 16), KEEP chunks of eight values per
+// lane.  Block b takes the rows b RB + i, (b + grid) RB + i, ...; W is just
+// enough for a row, so that a width of 5120 leaves no lane idle.
+template <int XDT, int KEEP, bool RMS>
+__global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W, int RB) {
   __shared__ float red[2][16][2];
-  extern __shared__ float meet[];                                // [RB - 1][T KEEP 8], for the rows' groups to meet
-  const int t = threadIdx.x % T, rg = threadIdx.x / T;
+  extern __shared__ float meet[];                                // [RB - 1][KEEP 8][T], for the row groups to meet
+  const int T = 64 * W, wv = threadIdx.x >> 6, rg = wv / W, w0 = rg * W;
+  const int t = threadIdx.x - w0 * 64;
   int cnt[KEEP];
   float w[KEEP][8], dw[KEEP][8], db[KEEP][8];
 #pragma unroll
@@ -215,7 +232,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a) {
         s[0] = __builtin_fmaf(g[i][j], xh[i][j], s[0]);
         s[1] += g[i][j];
       }
-    group_sum<T, 2>(s, red, turn);
+    waves_sum(s, red, turn, w0, W);
     turn ^= 1;
     const float mx = s[0] * inv_k, ma = RMS ? 0.0f : s[1] * inv_k;
 #pragma unroll
@@ -227,12 +244,12 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a) {
     }
   }
   if (!a.partial) return;
-  // the groups' sums meet in the first one's, in their order
+  // the row groups' sums meet in the first one's, in their order
   float* out = a.partial + (int64_t)blockIdx.x * 2 * a.pitch;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     float (&d)[KEEP][8] = half ? db : dw;
-    if constexpr (RB > 1) {
+    if (RB > 1) {                                                // block-uniform
       __syncthreads();
       if (rg > 0) {
 #pragma unroll
@@ -331,35 +348,44 @@ hipError_t norm_dispatch(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Lanes per row of the backward pass (0: rows too long for registers).
-inline int norm_grad_lanes(int64_t K) {
-  return K <= 512 ? 64 : K <= 1024 ? 128 : K <= 2048 ? 256 : K <= 4096 ? 512 : K <= 16384 ? 1024 : 0;
-}
-inline int64_t norm_grad_blocks(int64_t M, int64_t K) {
-  const int T = norm_grad_lanes(K), rb = T ? 1024 / T : 1;
-  const int64_t want = (M + rb - 1) / rb, cus = awq::device_cus();
-  return want < cus ? want : cus;
+// Waves per row of the backward pass (0: rows too long for registers), chunks
+// per lane and row groups per block.
+struct NormGradPlan {
+  int waves, keep, groups;
+  int64_t blocks;
+};
+inline NormGradPlan norm_grad_plan(int64_t M, int64_t K) {
+  NormGradPlan p{};
+  const int64_t cus = awq::device_cus() > 0 ? awq::device_cus() : 256;
+  if (K <= 16384) {
+    p.keep = K <= 8192 ? 1 : 2;
+    p.waves = (int)((K + 512 * p.keep - 1) / (512 * p.keep));
+    p.groups = 16 / p.waves;
+  } else {
+    p.groups = 1;
+  }
+  // one block per compute unit, with as many rows each as make the whole; a
+  // block's partial sums cost as much as a row or two, so few rows make fewer
+  // blocks
+  const int64_t sets = (M + p.groups - 1) / p.groups;
+  const int64_t each = (sets + cus - 1) / cus;
+  p.blocks = each > 0 ? (sets + each - 1) / each : 0;
+  return p;
 }
 inline int64_t norm_pitch(int64_t K) { return (K + 63) / 64 * 64; }
 
 template <int XDT, bool RMS>
 hipError_t norm_grad_dispatch(const NormGradArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)norm_grad_blocks(a.M, a.K)), block(1024);
-#define AWQ_NG(T, KEEP)                                                                                       \
-  hipLaunchKernelGGL((k_norm_grad<XDT, T, KEEP, RMS>), grid, block,                                           \
-                     a.partial ? (size_t)(1024 / T - 1) * T * KEEP * 8 * 4 : 0, st, a)
-  switch (norm_grad_lanes(a.K)) {
-    case 64: AWQ_NG(64, 1); break;
-    case 128: AWQ_NG(128, 1); break;
-    case 256: AWQ_NG(256, 1); break;
-    case 512: AWQ_NG(512, 1); break;
-    case 1024:
-      if (a.K <= 8192) AWQ_NG(1024, 1);
-      else AWQ_NG(1024, 2);
-      break;
-    default: hipLaunchKernelGGL((k_norm_grad_long<XDT, RMS>), grid, block, 0, st, a);
+  const NormGradPlan p = norm_grad_plan(a.M, a.K);
+  const dim3 grid((unsigned)p.blocks);
+  if (p.waves == 0) {
+    hipLaunchKernelGGL((k_norm_grad_long<XDT, RMS>), grid, dim3(1024), 0, st, a);
+    return hipGetLastError();
   }
-#undef AWQ_NG
+  const dim3 block((unsigned)(64 * p.waves * p.groups));
+  const size_t lds = a.partial ? (size_t)(p.groups - 1) * 64 * p.waves * p.keep * 8 * 4 : 0;
+  if (p.keep == 1) hipLaunchKernelGGL((k_norm_grad<XDT, 1, RMS>), grid, block, lds, st, a, p.waves, p.groups);
+  else hipLaunchKernelGGL((k_norm_grad<XDT, 2, RMS>), grid, block, lds, st, a, p.waves, p.groups);
   return hipGetLastError();
 }
 
@@ -383,7 +409,15 @@ hipError_t launch_norm(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx
 
 size_t norm_grad_ws_bytes(int64_t M, int64_t K) {
   if (M <= 0 || K <= 0) return 0;
-  return (size_t)(awqk::norm_grad_blocks(M, K) * 2 * awqk::norm_pitch(K)) * 4;
+  return (size_t)(awqk::norm_grad_plan(M, K).blocks * 2 * awqk::norm_pitch(K)) * 4;
+}
+
+// The most that any M' <= M needs: at most one block per compute unit.
+size_t norm_grad_ws_bytes_upto(int64_t M, int64_t K) {
+  if (M <= 0 || K <= 0) return 0;
+  const int64_t groups = awqk::norm_grad_plan(1, K).groups, sets = (M + groups - 1) / groups;
+  const int64_t cus = device_cus() > 0 ? device_cus() : 256;
+  return (size_t)((sets < cus ? sets : cus) * 2 * awqk::norm_pitch(K)) * 4;
 }
 
 hipError_t launch_norm_grad(const void* dy, int dyt, int64_t M, int64_t K, int64_t lddy, const void* x, int xdt,
@@ -401,7 +435,7 @@ hipError_t launch_norm_grad(const void* dy, int dyt, int64_t M, int64_t K, int64
     if (e != hipSuccess) return e;
   }
   if (!sums) return hipSuccess;
-  return launch_col_reduce((const float*)ws, M > 0 ? norm_grad_blocks(M, K) : 0, 2 * pitch, K, dw, pitch, db, st);
+  return launch_col_reduce((const float*)ws, M > 0 ? norm_grad_plan(M, K).blocks : 0, 2 * pitch, K, dw, pitch, db, st);
 }
 
 }  // namespace awq

@@ -72,8 +72,8 @@ __device__ __forceinline__ void store_yst(void* y, int64_t idx, float v) {
 
 // A finished sum: stored, or through the epilogue.
 template <int YDT, class EP>
-__device__ __forceinline__ void finish_yst(const EP& ep, void* y, int64_t ldy, int64_t m, int64_t n, float v) {
-  if constexpr (kHasEpi<EP>) epi_store(ep, y, ldy, m, n, v);
+__device__ __forceinline__ void finish_yst(const EP& ep, void* y, int64_t ldy, int64_t m, int64_t n, float v, const EpiIn& f) {
+  if constexpr (kHasEpi<EP>) epi_store(ep, y, ldy, m, n, v, f);
   else store_yst<YDT>(y, m * ldy + n, v);
 }
 
@@ -544,10 +544,13 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_st(
   };
   // 16 x 16 result layout: weight row = lane % 16, tokens 4 (lane / 16) + v
   auto store_direct = [&](const f32x4& a) {
+    EpiIn f[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) f[v] = epi_fetch(ep, 4 * b + v < M && tile * 16 + rl < nrows, 4 * b + v, r0 + tile * 16 + rl);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int t = 4 * b + v;
-      if (t < M && tile * 16 + rl < nrows) finish_yst<YDT>(ep, y, ldy, t, r0 + tile * 16 + rl, a[v]);
+      if (t < M && tile * 16 + rl < nrows) finish_yst<YDT>(ep, y, ldy, t, r0 + tile * 16 + rl, a[v], f[v]);
     }
   };
   // The first item runs on the words loaded before the staging; later items
@@ -616,9 +619,10 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_st(
     st_sync();
     for (int t = tid; t < ntile * 256; t += 1024) {
       const int tl = t >> 8, tk = (t >> 4) & 15, row = t & 15;
+      const EpiIn f = epi_fetch(ep, tk < M && tl * 16 + row < nrows, tk, r0 + tl * 16 + row);
       float tot = 0.0f;
       for (int ks = 0; ks < ksl; ++ks) tot += red[(tl * ksl + ks) * 256 + tk * 16 + row];
-      if (tk < M && tl * 16 + row < nrows) finish_yst<YDT>(ep, y, ldy, tk, r0 + tl * 16 + row, tot);
+      if (tk < M && tl * 16 + row < nrows) finish_yst<YDT>(ep, y, ldy, tk, r0 + tl * 16 + row, tot, f);
     }
   }
 }

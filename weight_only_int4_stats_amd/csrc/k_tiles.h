@@ -1,0 +1,221 @@
+// The loop that k_gemm_dx and k_linear_tiles share: fp16 rows (A) times packed
+// 4-bit weights on the matrix cores, tiles of 16 MB WM rows x 256 columns per
+// block of 4 WM waves (WM along the rows x 4 along the columns, each 16 MB x
+// 64), 64 of the contraction per stage, NS stages in LDS.
+//
+//  * Every stage arrives by LDS DMA, NS stages ahead: few rows leave a block
+//    little to do per stage, and what covers the memory's latency is the number
+//    of stages on their way (MB = 2, 172 blocks of 16 stages: 19.5 us with three
+//    in LDS, two on their way).
+//  * One barrier per stage, ahead of its last sub-step's products: by then
+//    every wave has read the stage's last operands into registers, so its slot
+//    takes the copies of stage s + NS, and the next stage's first operands are
+//    read while the last products run.
+//  * A column block's operands are dequantized in place as soon as its last
+//    product of a k32 step is issued, a few vector instructions after each
+//    product.
+#pragma once
+
+#include "awq_device.h"
+#include "k_epilogue.h"
+
+namespace awqk {
+
+constexpr int kTileK = 64;                // contraction per stage
+constexpr int kTileCols = 256;
+constexpr int kTileXcds = 8;              // L2 slices (block i -> slice i mod 8)
+
+// Position of an A row's 16-byte chunk c in LDS: c ^ ((r / 2) mod 8).
+__device__ __forceinline__ int tile_swz(int r) { return (r >> 1) & 7; }
+
+// The work item of this block: block i runs on L2 slice i mod 8, which takes the
+// i-th eighth of the items, slices of the contraction slowest, then groups of GM
+// row tiles, then columns, then the group's rows.  The 32 or 64 blocks that a
+// slice runs at once so share few distinct stages of both operands.
+template <int GM>
+__device__ __forceinline__ bool tile_item(int64_t block, int64_t mtiles, int64_t ctiles, int S, int& slice, int64_t& mt,
+                                          int64_t& ct) {
+  const int64_t tiles = mtiles * ctiles, items = tiles * S, per = (items + kTileXcds - 1) / kTileXcds;
+  const int64_t slot = block / kTileXcds, item = (block % kTileXcds) * per + slot;
+  if (slot >= per || item >= items) return false;
+  slice = (int)(item / tiles);
+  const int64_t t = item - slice * tiles, g = t / (GM * ctiles), r = t - g * GM * ctiles;
+  const int64_t gm = mtiles - g * GM < GM ? mtiles - g * GM : GM;
+  mt = g * GM + r % gm;
+  ct = r / gm;
+  return true;
+}
+
+// OP, the packed operand: bytes of its part of a stage (OP::Bytes), the copies
+// of this wave (op.copies, BW or one more), issue(s, lds, live), load(lds): a stage's
+// words and constants into registers, begin(st) and column(st, c): the operand
+// of column block c for k32 step st; chunk(st, b4): the A chunk that goes with it.
+template <int MB, int WM, int NS, class OP>
+struct Tile {
+  static constexpr int Waves = 4 * WM;
+  static constexpr int Threads = 64 * Waves;
+  static constexpr int Rows = 16 * MB * WM;
+  static constexpr int GM = Rows >= 128 ? 4 : 8;        // row tiles of a group
+  static constexpr int A = Rows * kTileK * 2;
+  static constexpr int Stage = A + OP::Bytes;
+  static constexpr int Lds = NS * Stage;
+  static constexpr int AW = MB >= 2 ? MB / 2 : 1;       // A copies of a wave that has any
+  static constexpr int H = MB > 4 ? 2 : 1;              // sub-steps per k32 step
+  static constexpr int MH = MB / H;                     // 16-row blocks per sub-step
+  static constexpr int BW = 8 / Waves;                  // copies of packed words per wave
+  static_assert((NS - 1) * (AW + BW + 1) <= 63, "copies in flight");
+
+  // rows of xq from row m0 on (pitch Kp, a multiple of 64), stages [s0, s1)
+  static __device__ __forceinline__ void run(uint8_t* lds, OP& op, const uint16_t* __restrict__ xq, int64_t m0,
+                                             int rows, int64_t Kp, int64_t s0, int64_t s1, f32x4 (&acc)[MB][4]) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wv >> 2, rl = lane & 15, b4 = lane >> 4;
+    const bool has_a = MB >= 2 || wv < 2 * WM;
+    uint32_t aoff[AW];
+#pragma unroll
+    for (int u = 0; u < AW; ++u) {
+      // lane i of a copy: row 8 j + i / 8, chunk (i % 8) ^ swizzle
+      const int r = 8 * (AW * wv + u) + (lane >> 3);
+      aoff[u] = (uint32_t)(r * Kp * 2 + (((lane & 7) ^ tile_swz(r)) * 16));
+    }
+    auto issue = [&](int64_t s, uint32_t slot) {
+      const bool live = s < s1;                          // past the end: copies of nothing, so that the counts stay
+      const uint32_t lb = __builtin_amdgcn_readfirstlane(lds_addr(lds) + slot * Stage);
+      if (has_a) {
+        const i32x4 ars = rsrc4(xq + m0 * Kp, live ? (uint32_t)(rows * Kp * 2) : 0u);
+#pragma unroll
+        for (int u = 0; u < AW; ++u) dma16(ars, lb + (AW * wv + u) * 1024, aoff[u], live ? (uint32_t)(s * kTileK * 2) : 0u);
+      }
+      op.issue(s, lb + A, live);
+    };
+    // all but the newest n stages' copies landed, and this wave's LDS reads done
+    auto wait = [&](auto n) {
+      constexpr int k = decltype(n)::value;
+      const int nops = (has_a ? AW : 0) + op.copies;
+      if (nops == AW + BW + 1) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(k * (AW + BW + 1)));
+      else if (nops == AW + BW) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(k * (AW + BW)));
+      else __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(k * BW));          // MB = 1: a wave without rows
+    };
+    // A fragments of sub-step q = H st + hh
+    u32x4 a0[MH], a1[MH];
+    const uint32_t alane = (uint32_t)((wm * 16 * MB + rl) * 128);
+    const int sw = tile_swz(rl);                          // the same for rows 16 apart
+    auto load_a = [&](const uint8_t* base, int q, u32x4 (&a)[MH]) {
+      const int st = q / H, hh = q % H;
+#pragma unroll
+      for (int i = 0; i < MH; ++i)
+        a[i] = *reinterpret_cast<const u32x4*>(base + alane + (hh * MH + i) * 2048 + ((OP::chunk(st, b4) ^ sw) * 16));
+    };
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[a][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (s0 >= s1) return;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) issue(s0 + j, j);
+    wait(std::integral_constant<int, NS - 1>{});
+    lds_barrier();
+    u32x4 bq[4];
+    load_a(lds, 0, a0);
+    op.load(lds + A);
+    op.begin(0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) bq[c] = op.column(0, c);
+    uint32_t slot = 0;
+    for (int64_t s = s0; s < s1; ++s) {
+      const uint32_t nslot = slot + 1 == NS ? 0 : slot + 1;
+      const uint8_t* cur = lds + slot * Stage;
+      const uint8_t* nxt = lds + nslot * Stage;
+#pragma unroll
+      for (int q = 0; q < 2 * H; ++q) {
+        u32x4 (&ac)[MH] = (q & 1) ? a1 : a0;
+        u32x4 (&an)[MH] = (q & 1) ? a0 : a1;
+        if (q < 2 * H - 1) {
+          load_a(cur, q + 1, an);
+        } else {
+          wait(std::integral_constant<int, NS - 2>{});    // stage s + 1 landed, this wave done with s
+          lds_barrier();
+          issue(s + NS, slot);
+          load_a(nxt, 0, an);
+          op.load(nxt + A);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const bool turn = q % H == H - 1;                 // the k32 step's last products
+        const int st = q / H;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int i = 0; i < MH; ++i) {
+            const int b = (q % H) * MH + i;
+            acc[b][c] = mfma16h(ac[i], bq[c], acc[b][c]);
+          }
+          if (turn) {
+            if (c == 0) op.begin(st ^ 1);
+            bq[c] = op.column(st ^ 1, c);
+          }
+        }
+        if (turn && MH >= 4) {
+#pragma unroll
+          for (int i = 0; i < 4 * MH; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                    // one matrix product
+            if (i >= 2) __builtin_amdgcn_sched_group_barrier(0x002, OP::VAlu, 0);  // vector instructions
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      slot = nslot;
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));       // the copies past the end
+    lds_barrier();                                        // LDS is free for what follows
+  }
+};
+
+// A tile's shape and its time per stage on a compute unit by itself and two at
+// once (0: its LDS leaves room for one), in us.
+struct TileShape {
+  int mb, wm;
+  double one, two;
+};
+
+struct TilePlan {
+  int mb = 1, wm = 1, S = 1;
+  double cost = 1e300;
+};
+
+// Time of `items` tiles of `stages` stages each: whole rounds of one tile (or
+// two at once) per compute unit, and what a round costs beside its stages
+// (start, first copies, stores).
+inline double tile_time(const TileShape& h, int64_t items, int64_t stages, int64_t cus) {
+  const int64_t load = (items + cus - 1) / cus;
+  const double per = h.two > 0.0 ? (double)(load / 2) * h.two + (double)(load % 2) * h.one : (double)load * h.one;
+  const double rounds = (double)(h.two > 0.0 ? (load + 1) / 2 : load);
+  return per * (double)stages + 9.0 * rounds;
+}
+
+// The shape and the number of slices of the contraction with the least
+// estimated time.  Slices cost a second launch and their sums' way through
+// memory (6.5 TB/s: they partly stay in the last cache).  Rows count in whole
+// 16s, so that the choice is the same up to the next multiple.
+template <int NSHAPES>
+inline TilePlan tile_plan(const TileShape (&shapes)[NSHAPES], int64_t M, int64_t cols, int64_t stages, int64_t cus) {
+  const int64_t ct = (cols + kTileCols - 1) / kTileCols, M16 = (M + 15) / 16 * 16;
+  TilePlan best;
+  for (const TileShape& h : shapes) {
+    const int64_t tiles = (M + 16 * h.mb * h.wm - 1) / (16 * h.mb * h.wm) * ct;
+    for (int S = 1; S == 1 || (S <= 16 && S * 2 <= stages && tiles * S < 4 * cus); S *= 2) {
+      const double cost = tile_time(h, tiles * S, (stages + S - 1) / S, cus) + (S > 1 ? 2.5 + (double)S * M16 * cols * 8 / 6.5e6 : 0.0);
+      if (cost < best.cost) {
+        best.mb = h.mb;
+        best.wm = h.wm;
+        best.S = S;
+        best.cost = cost;
+      }
+    }
+  }
+  return best;
+}
+
+inline int64_t tile_blocks(int64_t items) { return kTileXcds * ((items + kTileXcds - 1) / kTileXcds); }
+
+}  // namespace awqk

@@ -32,13 +32,6 @@ __device__ __forceinline__ void store_y(void* y, int64_t idx, float v) {
   else reinterpret_cast<uint16_t*>(y)[idx] = (uint16_t)from_f32<YDT>(v);
 }
 
-// A finished sum: stored, or through the epilogue.
-template <int YDT, class EP>
-__device__ __forceinline__ void finish_y(const EP& ep, void* y, int64_t ldy, int64_t m, int64_t n, float v) {
-  if constexpr (kHasEpi<EP>) epi_store(ep, y, ldy, m, n, v);
-  else store_y<YDT>(y, m * ldy + n, v);
-}
-
 // ===========================================================================
 // matrix-core GEMM
 // ===========================================================================
@@ -48,7 +41,7 @@ __device__ __forceinline__ void finish_y(const EP& ep, void* y, int64_t ldy, int
 // fp16; then, for every group g, the fp16 constants of the packed-fma
 // dequantization, group-major so a block's columns are contiguous:
 //   ctab[g][n] = (fp16(D' 2^24) | fp16(D' 2^20) << 16, fp16(-D' z) twice).
-// ONCE (under an epilogue): max_g |step[n][g]| 2^e_n in [2^14, 2^15) and
+// ONCE (for awq_w4a16_linear's tiles): max_g |step[n][g]| 2^e_n in [2^14, 2^15) and
 //   ctab[g][n] = (fp16(step 2^e_n) twice, fp16(-z 2^-9) twice).
 constexpr int kConstRows = 16;   // weight rows per block of the constants pre-pass
 template <bool ONCE>
@@ -216,14 +209,14 @@ inline GemmPlan gemm_plan(int64_t M, int64_t N) {
 
 // One output tile of width 64 NB over the columns [nb, ne): tile t of that
 // region in grouped order.
-template <int YDT, int NB, class EP>
+template <int YDT, int NB>
 __device__ __forceinline__ void gemm_tile(uint8_t* __restrict__ lds0, uint8_t* __restrict__ lds1,
                                           uint8_t* __restrict__ lds2, int64_t t,
                                           const uint16_t* __restrict__ xq, int64_t M, int64_t K,
                                           const int* __restrict__ pm, const uint32_t* __restrict__ qw,
                                           const uint32_t* __restrict__ ctab, const int* __restrict__ en,
                                           int64_t N, int64_t nb, int64_t ne, void* __restrict__ y,
-                                          int64_t ldy, int glog, int vec_ok, const EP& ep) {
+                                          int64_t ldy, int glog, int vec_ok) {
   using Tl = GemmTile<NB>;
   constexpr int NT = Tl::NT;
   const int64_t ntile = (ne - nb + NT - 1) / NT, mtile = (M + kMT - 1) / kMT;
@@ -330,11 +323,6 @@ __device__ __forceinline__ void gemm_tile(uint8_t* __restrict__ lds0, uint8_t* _
     }
   };
 
-  auto dequant = [](uint32_t w, uint32_t cx, uint32_t cz) {
-    if constexpr (kHasEpi<EP>) return once_dequant(w, cx, cz);
-    else return dequant_word_f16(w, cx, cz);
-  };
-
   Raw R;                // a stage's packed words and constants, straight from LDS
   u32x4 aE[4], aO[4];   // fragments of even and odd sub-steps
   u32x4 bq[NB];         // dequantized column blocks of the current k32 step
@@ -345,7 +333,7 @@ __device__ __forceinline__ void gemm_tile(uint8_t* __restrict__ lds0, uint8_t* _
   load_a(lds0, 0, aE);
   load_raw(lds0, R);
 #pragma unroll
-  for (int nbk = 0; nbk < NB; ++nbk) bq[nbk] = dequant(R.w[nbk].x, R.c[nbk].x, R.c[nbk].y);
+  for (int nbk = 0; nbk < NB; ++nbk) bq[nbk] = dequant_word_f16(R.w[nbk].x, R.c[nbk].x, R.c[nbk].y);
 
   // One stage (64 k) in four sub-steps q = 2 st + hh.  The operands of k32
   // step 0 are ready when the stage starts.  In sub-step 1 each column block's
@@ -378,7 +366,7 @@ __device__ __forceinline__ void gemm_tile(uint8_t* __restrict__ lds0, uint8_t* _
       for (int nbk = 0; nbk < NB; ++nbk) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[hh * 4 + i][nbk] = mfma16h(a[i], bq[nbk], acc[hh * 4 + i][nbk]);
-        if (q & 1) bq[nbk] = dequant(q == 1 ? R.w[nbk].y : R.w[nbk].x, R.c[nbk].x, R.c[nbk].y);
+        if (q & 1) bq[nbk] = dequant_word_f16(q == 1 ? R.w[nbk].y : R.w[nbk].x, R.c[nbk].x, R.c[nbk].y);
       }
       if (q & 1) {
 #pragma unroll
@@ -415,58 +403,6 @@ __device__ __forceinline__ void gemm_tile(uint8_t* __restrict__ lds0, uint8_t* _
   for (int nbk = 0; nbk < NB; ++nbk) {
     const int64_t n = n0 + wn * kWc + nbk * 16 + (lane & 15);
     en_l[nbk] = n < ne ? en[n] : 0;
-  }
-  if constexpr (kHasEpi<EP>) {
-    // Through the epilogue: the sums pass the wave's LDS area as floats, 32
-    // rows at a time, and a lane finishes eight columns of a row, the same
-    // eight for all of its rows (their exponents and bias held in registers).
-    constexpr int kFl = kWc * 4 + 16;                     // padded LDS pitch
-    constexpr int kFr = kWc / 8;                          // lanes per row
-    static_assert(4 * 32 * kFl <= Tl::Stage, "four waves' staging in one stage array");
-    __syncthreads();                                      // every wave done with the stages
-    uint8_t* fst = (wv < 4 ? lds0 : lds1) + (wv & 3) * 32 * kFl;
-    const int c8 = (lane % kFr) * 8;
-    const int64_t n = n0 + wn * kWc + c8;
-    const int cnt = ne - n < 8 ? (int)(ne > n ? ne - n : 0) : 8;
-    int e8[8];
-    float b8[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e8[j] = j < cnt ? en[n + j] : 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) b8[j] = 0.0f;
-    if (ep.bias && cnt > 0) load8_any(ep.bias, ep.bdt, n, cnt, b8);
-#pragma unroll
-    for (int hp = 0; hp < 4; ++hp) {                      // rows wm 128 + hp 32 + 0..31
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-#pragma unroll
-          for (int nbk = 0; nbk < NB; ++nbk)
-            *reinterpret_cast<float*>(fst + (h * 16 + 4 * (lane >> 4) + v) * kFl + (nbk * 16 + (lane & 15)) * 4) =
-                acc[2 * hp + h][nbk][v];
-      __builtin_amdgcn_s_waitcnt(0xC07F);                 // lgkmcnt(0): the wave's writes landed
-      __builtin_amdgcn_wave_barrier();
-      for (int i = 0; i < 32 * kFr / 64; ++i) {
-        const int r = i * (64 / kFr) + lane / kFr;
-        const f32x4 z0 = *reinterpret_cast<const f32x4*>(fst + r * kFl + c8 * 4);
-        const f32x4 z1 = *reinterpret_cast<const f32x4*>(fst + r * kFl + c8 * 4 + 16);
-        const int64_t m = m0 + wm * 128 + hp * 32 + r;
-        if (m < M && cnt > 0) {
-          const int p = pm[m];
-          float z[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z[j] = ldexpf(z0[j], -(p + e8[j]));
-            z[4 + j] = ldexpf(z1[j], -(p + e8[4 + j]));
-          }
-          epi_store8(ep, y, ldy, m, n, cnt, z, b8);
-        }
-      }
-      __builtin_amdgcn_s_waitcnt(0xC07F);                 // the wave's reads done before it writes again
-      __builtin_amdgcn_wave_barrier();
-    }
-    return;
   }
   if (!vec_ok) {
 #pragma unroll
@@ -535,7 +471,7 @@ __device__ __forceinline__ void gemm_tile(uint8_t* __restrict__ lds0, uint8_t* _
 // tiles of columns [0, nsplit), the rest the 128-wide tiles of [nsplit, N).
 // Within each part, block i runs on L2 slice i mod 8, and slice x takes the
 // x-th eighth of that part's tiles.
-template <int YDT, class EP>
+template <int YDT>
 __global__ __launch_bounds__(512) void k_gemm(const uint16_t* __restrict__ xq, int64_t M, int64_t K,
                                              const int* __restrict__ pm,
                                              const uint32_t* __restrict__ qw,
@@ -543,7 +479,7 @@ __global__ __launch_bounds__(512) void k_gemm(const uint16_t* __restrict__ xq, i
                                              const int* __restrict__ en, int64_t N,
                                              void* __restrict__ y, int64_t ldy, int glog, int vec_ok,
                                              int64_t nsplit, int64_t wide_tiles, int64_t wide_blocks,
-                                             int64_t narrow_tiles, const EP ep) {
+                                             int64_t narrow_tiles) {
   // three LDS arrays, the loop unrolled by three: each stage is a known array
   __shared__ __attribute__((aligned(16))) uint8_t lds0[kStageMax];
   __shared__ __attribute__((aligned(16))) uint8_t lds1[kStageMax];
@@ -553,15 +489,13 @@ __global__ __launch_bounds__(512) void k_gemm(const uint16_t* __restrict__ xq, i
     const int64_t per = (wide_tiles + kXcds - 1) / kXcds, slot = b / kXcds;
     const int64_t t = (b % kXcds) * per + slot;
     if (slot >= per || t >= wide_tiles) return;
-    gemm_tile<YDT, 4>(lds0, lds1, lds2, t, xq, M, K, pm, qw, ctab, en, N, 0, nsplit, y, ldy, glog, vec_ok,
-                      ep);
+    gemm_tile<YDT, 4>(lds0, lds1, lds2, t, xq, M, K, pm, qw, ctab, en, N, 0, nsplit, y, ldy, glog, vec_ok);
   } else {
     const int64_t bn = b - wide_blocks;
     const int64_t per = (narrow_tiles + kXcds - 1) / kXcds, slot = bn / kXcds;
     const int64_t t = (bn % kXcds) * per + slot;
     if (slot >= per || t >= narrow_tiles) return;
-    gemm_tile<YDT, 2>(lds0, lds1, lds2, t, xq, M, K, pm, qw, ctab, en, N, nsplit, N, y, ldy, glog, vec_ok,
-                      ep);
+    gemm_tile<YDT, 2>(lds0, lds1, lds2, t, xq, M, K, pm, qw, ctab, en, N, nsplit, N, y, ldy, glog, vec_ok);
   }
 }
 
@@ -585,14 +519,13 @@ constexpr int kSkP = 2;                 // groups in flight per wave
 constexpr int64_t kSkMaxM = 16;         // tokens per B tile
 
 
-template <int YDT, int P, class EP>
+template <int YDT, int P>
 __global__ __launch_bounds__(256) void k_gemm_skinny(const uint16_t* __restrict__ xq, int M, int64_t K,
                                                      const int* __restrict__ pm,
                                                      const uint32_t* __restrict__ qw,
                                                      const uint16_t* __restrict__ scales,
                                                      const uint8_t* __restrict__ zeros, int64_t N,
-                                                     void* __restrict__ y, int64_t ldy, int glog, const EP ep) {
-  constexpr bool ONCE = kHasEpi<EP>;
+                                                     void* __restrict__ y, int64_t ldy, int glog) {
   __shared__ float red[kSkW][16 * 16];
   __shared__ float rmax[kSkW][16];
   const int lane = threadIdx.x & 63;
@@ -649,7 +582,7 @@ __global__ __launch_bounds__(256) void k_gemm_skinny(const uint16_t* __restrict_
   auto piece_max = [&](const u32x4& v, int pc, float m) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (pc * 8 + j < GW) m = fmaxf(m, step_size<ONCE>((v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu));
+      if (pc * 8 + j < GW) m = fmaxf(m, f16_to_f32((v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu));
     return m;
   };
   float mx = piece_max(sp0, b, 0.0f);
@@ -661,7 +594,12 @@ __global__ __launch_bounds__(256) void k_gemm_skinny(const uint16_t* __restrict_
     const auto r16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
     mx = fmaxf(__uint_as_float(r16[0]), __uint_as_float(r16[1]));
   }
-  const int e = step_pow<ONCE>(mx);              // max step 2^e in [2^-10, 2^-9)
+  int e = 0;
+  if (mx > 0.0f) {
+    int ex;
+    frexpf(mx, &ex);
+    e = -9 - ex;                                 // max step 2^e in [2^-10, 2^-9)
+  }
 
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int gb = g0; gb < g1; gb += P) {
@@ -676,10 +614,7 @@ __global__ __launch_bounds__(256) void k_gemm_skinny(const uint16_t* __restrict_
       const f16x2 c20 = as_f16x2(h20 | (h20 << 16));
       const f16x2 nzd = as_f16x2(hz | (hz << 16));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (ONCE) acc = mfma16h(once_dequant(wa[d][i], f32_to_f16_bits(D) * 0x10001u, once_zero(zr[d])), xb[d][i], acc);
-        else acc = mfma16h(dequant_word_f16(wa[d][i], c24, c20, nzd), xb[d][i], acc);
-      }
+      for (int i = 0; i < 4; ++i) acc = mfma16h(dequant_word_f16(wa[d][i], c24, c20, nzd), xb[d][i], acc);
     }
     if (gb + P >= g1) break;                     // wave-uniform
 #pragma unroll
@@ -689,7 +624,7 @@ __global__ __launch_bounds__(256) void k_gemm_skinny(const uint16_t* __restrict_
   // ---- add the four K quarters; 16 x 16 layout: token = lane % 16, row = 4 (lane / 16) + v
 #pragma unroll
   for (int v = 0; v < 4; ++v) red[wv][(4 * b + v) * 16 + rl] = acc[v];
-  if (b == 0) rmax[wv][rl] = (float)sum_pow<ONCE>(e);
+  if (b == 0) rmax[wv][rl] = (float)e;
   __syncthreads();
   const int t = threadIdx.x;                     // one (row, token) per thread
   const int row = t >> 4, tok = t & 15;
@@ -697,7 +632,7 @@ __global__ __launch_bounds__(256) void k_gemm_skinny(const uint16_t* __restrict_
 #pragma unroll
   for (int w = 0; w < kSkW; ++w) tot += red[w][t];
   if (row < nrows && tok < M)
-    finish_y<YDT>(ep, y, ldy, tok, n0 + row, ldexpf(tot, -(pm[tok] + (int)rmax[0][row])));
+    store_y<YDT>(y, (int64_t)tok * ldy + n0 + row, ldexpf(tot, -(pm[tok] + (int)rmax[0][row])));
 }
 
 struct GemmWs {
@@ -725,12 +660,9 @@ inline GemmWs gemm_ws(void* ws, int64_t M, int64_t N, int64_t K, int group) {
   return w;
 }
 
-template <int DT, int YDT, bool HAS_R, class EP>
-hipError_t gemm_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
-                         const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog,
-                         const float* r, void* y, int64_t ldy, void* ws, hipStream_t st, const EP& ep) {
-  constexpr bool ONCE = kHasEpi<EP>;
-  const GemmWs w = gemm_ws(ws, M, N, K, 1 << glog);
+template <int DT, bool HAS_R, bool ONCE>
+void gemm_prep(const GemmWs& w, const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint16_t* scales,
+               const uint8_t* zeros, int64_t N, int glog, const float* r, hipStream_t st) {
   const dim3 pgrid((unsigned)(M + (N + kConstRows - 1) / kConstRows));
   if (K > 256 * 8 * kRowsKeep)
     hipLaunchKernelGGL((k_gemm_prep<DT, HAS_R, 2 * kRowsKeep, ONCE>), pgrid, dim3(256), 0, st, x, M, K, ldx, r,
@@ -738,13 +670,21 @@ hipError_t gemm_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, c
   else
     hipLaunchKernelGGL((k_gemm_prep<DT, HAS_R, kRowsKeep, ONCE>), pgrid, dim3(256), 0, st, x, M, K, ldx, r,
                        w.xq, w.pm, scales, zeros, N, K >> glog, w.en, w.ctab);
+}
+
+template <int DT, int YDT, bool HAS_R>
+hipError_t gemm_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
+                         const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog,
+                         const float* r, void* y, int64_t ldy, void* ws, hipStream_t st) {
+  const GemmWs w = gemm_ws(ws, M, N, K, 1 << glog);
+  gemm_prep<DT, HAS_R, false>(w, x, M, K, ldx, scales, zeros, N, glog, r, st);
   // 16-byte output stores need a 16-byte aligned y and row pitch
   const int es = YDT == DT_F32 ? 4 : 2;
   const int vec_ok = ((uintptr_t)y % 16 == 0) && ((ldy * es) % 16 == 0);
   const GemmPlan pl = gemm_plan(M, N);
-  hipLaunchKernelGGL((k_gemm<YDT, EP>), dim3((unsigned)pl.blocks), dim3(512), 0, st, w.xq, M, K, w.pm,
+  hipLaunchKernelGGL((k_gemm<YDT>), dim3((unsigned)pl.blocks), dim3(512), 0, st, w.xq, M, K, w.pm,
                      qw, w.ctab, w.en, N, y, ldy, glog, vec_ok, pl.nsplit, pl.wide_tiles, pl.wide_blocks,
-                     pl.narrow_tiles, ep);
+                     pl.narrow_tiles);
   return hipGetLastError();
 }
 
@@ -772,12 +712,11 @@ inline size_t skinny_cu_lds(int64_t M, int64_t K, int64_t rows_max) {
          (size_t)ntile * 16 * 4;
 }
 
-template <int DT, int YDT, bool HAS_R, int NP, int P, class EP>
+template <int DT, int YDT, bool HAS_R, int NP, int P>
 __global__ __launch_bounds__(1024) void k_gemm_skinny_cu(
     const uint16_t* __restrict__ x, int M, int64_t K, int64_t ldx, const float* __restrict__ r,
     const uint32_t* __restrict__ qw, const uint16_t* __restrict__ scales,
-    const uint8_t* __restrict__ zeros, int64_t N, void* __restrict__ y, int64_t ldy, int glog, const EP ep) {
-  constexpr bool ONCE = kHasEpi<EP>;
+    const uint8_t* __restrict__ zeros, int64_t N, void* __restrict__ y, int64_t ldy, int glog) {
   extern __shared__ __attribute__((aligned(16))) uint32_t lds_sc[];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -937,7 +876,7 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_cu(
     auto piece_max = [&](const u32x4& pv, int pc, float m) {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (pc * 8 + q < GW) m = fmaxf(m, step_size<ONCE>((pv[q >> 1] >> (16 * (q & 1))) & 0xFFFFu));
+        if (pc * 8 + q < GW) m = fmaxf(m, f16_to_f32((pv[q >> 1] >> (16 * (q & 1))) & 0xFFFFu));
       return m;
     };
     float mx = piece_max(sp0, b, 0.0f);
@@ -948,7 +887,12 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_cu(
       const auto r16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
       mx = fmaxf(__uint_as_float(r16[0]), __uint_as_float(r16[1]));
     }
-    const int e = step_pow<ONCE>(mx);            // max step 2^e in [2^-10, 2^-9)
+    int e = 0;
+    if (mx > 0.0f) {
+      int ex;
+      frexpf(mx, &ex);
+      e = -9 - ex;                               // max step 2^e in [2^-10, 2^-9)
+    }
 
     // ring of P groups: slot d is refilled with group g + P right after group
     // g is consumed (reads past the slice's end are out of range and return 0)
@@ -973,10 +917,7 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_cu(
           const f16x2 nzd = as_f16x2(hz | (hz << 16));
           f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (ONCE) part = mfma16h(once_dequant(wa[d][i], f32_to_f16_bits(D) * 0x10001u, once_zero(zr[d])), xb[i], part);
-            else part = mfma16h(dequant_word_f16(wa[d][i], c24, c20, nzd), xb[i], part);
-          }
+          for (int i = 0; i < 4; ++i) part = mfma16h(dequant_word_f16(wa[d][i], c24, c20, nzd), xb[i], part);
 #pragma unroll
           for (int vv = 0; vv < 4; ++vv) acc[vv] = __builtin_fmaf(part[vv], gscale, acc[vv]);
         }
@@ -989,14 +930,14 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_cu(
 #pragma unroll
       for (int vv = 0; vv < 4; ++vv) {
         const int row = 4 * b + vv;
-        const int erw = __shfl(sum_pow<ONCE>(e), row);
+        const int erw = __shfl(e, row);
         if (tile * 16 + row < nrows && rl < M)
-          finish_y<YDT>(ep, y, ldy, rl, r0 + tile * 16 + row, ldexpf(acc[vv], -erw));
+          store_y<YDT>(y, (int64_t)rl * ldy + r0 + tile * 16 + row, ldexpf(acc[vv], -erw));
       }
     } else {
 #pragma unroll
       for (int vv = 0; vv < 4; ++vv) red[it * 256 + (4 * b + vv) * 16 + rl] = acc[vv];
-      if (it % ksl == 0 && b == 0) erow[tile * 16 + rl] = sum_pow<ONCE>(e);
+      if (it % ksl == 0 && b == 0) erow[tile * 16 + rl] = e;
     }
   }
   if (ksl > 1) {
@@ -1006,7 +947,7 @@ __global__ __launch_bounds__(1024) void k_gemm_skinny_cu(
       float tot = 0.0f;
       for (int ks = 0; ks < ksl; ++ks) tot += red[(tl * ksl + ks) * 256 + row * 16 + tk];
       if (tl * 16 + row < nrows && tk < M)
-        finish_y<YDT>(ep, y, ldy, tk, r0 + tl * 16 + row, ldexpf(tot, -erow[tl * 16 + row]));
+        store_y<YDT>(y, (int64_t)tk * ldy + r0 + tl * 16 + row, ldexpf(tot, -erow[tl * 16 + row]));
     }
   }
 }
@@ -1029,10 +970,10 @@ inline int skinny_cu_blocks(int64_t M, int64_t N, int64_t K) {
   return (int)nblk;
 }
 
-template <int DT, int YDT, bool HAS_R, int P, class EP>
+template <int DT, int YDT, bool HAS_R, int P = 2>
 hipError_t skinny_cu_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                               const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog,
-                              const float* r, void* y, int64_t ldy, int nblk, hipStream_t st, const EP& ep) {
+                              const float* r, void* y, int64_t ldy, int nblk, hipStream_t st) {
   if (nblk > N) nblk = (int)N;
   const int64_t rows_max = (N + nblk - 1) / nblk;
   size_t lds = skinny_cu_lds(M, K, rows_max);
@@ -1043,8 +984,8 @@ hipError_t skinny_cu_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t l
   if (lds < 81 * 1024) lds = 81 * 1024;           // one block per compute unit
   const dim3 grid((unsigned)nblk), block(1024);
 #define AWQ_SC(NP)                                                                                    \
-  hipLaunchKernelGGL((k_gemm_skinny_cu<DT, YDT, HAS_R, NP, P, EP>), grid, block, lds, st, x, (int)M, K, ldx, r, \
-                     qw, scales, zeros, N, y, ldy, glog, ep)
+  hipLaunchKernelGGL((k_gemm_skinny_cu<DT, YDT, HAS_R, NP, P>), grid, block, lds, st, x, (int)M, K, ldx, r, \
+                     qw, scales, zeros, N, y, ldy, glog)
   if (np == 1) AWQ_SC(1);
   else if (np == 2) AWQ_SC(2);
   else if (np == 4) AWQ_SC(4);
@@ -1053,60 +994,97 @@ hipError_t skinny_cu_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t l
   return hipGetLastError();
 }
 
-template <int DT, int YDT, bool HAS_R, class EP>
+template <int DT, int YDT, bool HAS_R, int P = kSkP>
 hipError_t skinny_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                            const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog,
-                           const float* r, void* y, int64_t ldy, void* ws, hipStream_t st, const EP& ep) {
+                           const float* r, void* y, int64_t ldy, void* ws, hipStream_t st) {
   const GemmWs w = gemm_ws(ws, M, N, K, 1 << glog);
   hipLaunchKernelGGL((k_rows_f16<DT, HAS_R, true>), dim3((unsigned)M), dim3(256), 0, st, x, K, ldx,
                      r, w.xq, w.pm);
-  hipLaunchKernelGGL((k_gemm_skinny<YDT, kSkP, EP>), dim3((unsigned)((N + 15) / 16)), dim3(64 * kSkW), 0, st,
-                     w.xq, (int)M, K, w.pm, qw, scales, zeros, N, y, ldy, glog, ep);
+  hipLaunchKernelGGL((k_gemm_skinny<YDT, P>), dim3((unsigned)((N + 15) / 16)), dim3(64 * kSkW), 0, st,
+                     w.xq, (int)M, K, w.pm, qw, scales, zeros, N, y, ldy, glog);
   return hipGetLastError();
 }
 
-template <int DT, int YDT, class EP>
+template <int DT, int YDT>
 hipError_t w4a16_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                           const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog,
-                          const float* r, void* y, int64_t ldy, void* ws, hipStream_t st, const EP& ep) {
-  const awq::Epilogue* e = nullptr;
-  if constexpr (kHasEpi<EP>) {
-    e = &ep;
-    if (r) return hipErrorInvalidValue;
-  }
+                          const float* r, void* y, int64_t ldy, void* ws, hipStream_t st) {
   if (M == 1 && awq::gemv1_supported(K, N))
-    return awq::launch_gemv1(x, DT, K, qw, scales, zeros, N, 1 << glog, r, y, YDT, st, e);
+    return awq::launch_gemv1(x, DT, K, qw, scales, zeros, N, 1 << glog, r, y, YDT, st);
   if (awq::mid_supported(M, N, K))
-    return awq::launch_mid(x, DT, M, K, ldx, qw, scales, zeros, N, 1 << glog, r, y, YDT, ldy, ws, st, e);
+    return awq::launch_mid(x, DT, M, K, ldx, qw, scales, zeros, N, 1 << glog, r, y, YDT, ldy, ws, st);
   if (awq::skinny_st_blocks(M, N, K, 1 << glog))
-    return awq::launch_skinny_st(x, DT, M, K, ldx, qw, scales, zeros, N, 1 << glog, r, y, YDT, ldy, st, e);
+    return awq::launch_skinny_st(x, DT, M, K, ldx, qw, scales, zeros, N, 1 << glog, r, y, YDT, ldy, st);
   if (awq::skinny_st_chunks(M, N, K, 1 << glog))
-    return awq::launch_skinny_st_chunked(x, DT, M, K, ldx, qw, scales, zeros, N, 1 << glog, r, y, e ? e->ydt : YDT, ldy, st, e);
+    return awq::launch_skinny_st_chunked(x, DT, M, K, ldx, qw, scales, zeros, N, 1 << glog, r, y, YDT, ldy, st);
   if (const int nblk = skinny_cu_blocks(M, N, K)) {
     // deeper ring for long K slices (few rows per block)
     const int64_t rows = (N + nblk - 1) / nblk, tiles = (rows + 15) / 16;
     const bool deep = (K / 128) * tiles >= 16 * 16;
-    if constexpr (!kHasEpi<EP>)
-      if (r) return deep ? skinny_cu_dispatch<DT, YDT, true, 4>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, nblk, st, ep)
-                         : skinny_cu_dispatch<DT, YDT, true, 2>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, nblk, st, ep);
-    return deep ? skinny_cu_dispatch<DT, YDT, false, 4>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, nblk, st, ep)
-                : skinny_cu_dispatch<DT, YDT, false, 2>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, nblk, st, ep);
+    if (r) return deep ? skinny_cu_dispatch<DT, YDT, true, 4>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, nblk, st)
+                       : skinny_cu_dispatch<DT, YDT, true, 2>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, nblk, st);
+    return deep ? skinny_cu_dispatch<DT, YDT, false, 4>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, nblk, st)
+                : skinny_cu_dispatch<DT, YDT, false, 2>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, nblk, st);
   }
   if (M <= kSkMaxM && K % 128 == 0) {
-    if constexpr (!kHasEpi<EP>)
-      if (r) return skinny_dispatch<DT, YDT, true>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, ws, st, ep);
-    return skinny_dispatch<DT, YDT, false>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, ws, st, ep);
+    if (r) return skinny_dispatch<DT, YDT, true>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, ws, st);
+    return skinny_dispatch<DT, YDT, false>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, ws, st);
   }
-  if constexpr (!kHasEpi<EP>)
-    if (r) return gemm_dispatch<DT, YDT, true>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, ws, st, ep);
-  return gemm_dispatch<DT, YDT, false>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, ws, st, ep);
+  if (r) return gemm_dispatch<DT, YDT, true>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, ws, st);
+  return gemm_dispatch<DT, YDT, false>(x, M, K, ldx, qw, scales, zeros, N, glog, r, y, ldy, ws, st);
+}
+
+// awq_w4a16_linear: the memory-bound kernels with the epilogue where they
+// serve the shape, else the tiles of k_linear.hip behind the same pre-pass.
+template <int DT>
+hipError_t linear_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
+                           const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog, void* y, int64_t ldy,
+                           const awq::Epilogue& ep, void* ws, hipStream_t st) {
+  const int group = 1 << glog;
+  if (M == 1 && awq::gemv1_supported(K, N))
+    return awq::launch_gemv1(x, DT, K, qw, scales, zeros, N, group, nullptr, y, ep.ydt, st, &ep);
+  if (awq::linear_mid(M, N, K))
+    return awq::launch_mid(x, DT, M, K, ldx, qw, scales, zeros, N, group, nullptr, y, ep.ydt, ldy, ws, st, &ep);
+  if (awq::skinny_st_chunks(M, N, K, group))
+    return awq::launch_skinny_st_chunked(x, DT, M, K, ldx, qw, scales, zeros, N, group, nullptr, y, ep.ydt, ldy, st, &ep);
+  const GemmWs w = gemm_ws(ws, M, N, K, group);
+  gemm_prep<DT, false, true>(w, x, M, K, ldx, scales, zeros, N, glog, nullptr, st);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return awq::launch_linear_tiles(w.xq, w.pm, w.en, w.ctab, qw, M, N, K, group, (float*)((char*)ws + w.bytes), y, ldy,
+                                  ep, st);
 }
 
 }  // namespace awqk
 
 namespace awq {
 
-int64_t gemm_threads(int64_t M, int64_t N) { return awqk::gemm_plan(M, N).blocks * 512; }
+// Above 32 tokens the tiles are faster on layers past 25 million weights (40
+// tokens, 4096 -> 11008: 31 us against 41; 64 tokens, 11008 -> 4096: 34 against
+// 40), below they are not (64 tokens, 4096 x 4096: 24 and 24; 33 tokens: 20
+// against 19; 24 tokens, 11008 -> 4096: 28 and 28).
+bool linear_mid(int64_t M, int64_t N, int64_t K) {
+  return mid_supported(M, N, K) && (M <= 32 || N * K <= (int64_t)25 << 20);
+}
+
+size_t linear_ws_bytes(int64_t M, int64_t N, int64_t K, int group) {
+  if (M <= 0 || N <= 0 || K <= 0 || group <= 0 || (M == 1 && gemv1_supported(K, N))) return 0;
+  if (linear_mid(M, N, K)) return mid_ws_bytes(M, N, K);
+  if (skinny_st_chunks(M, N, K, group)) return 0;
+  return awqk::gemm_ws(nullptr, M, N, K, group).bytes + linear_partial_bytes(M, N, K);
+}
+
+hipError_t launch_linear(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
+                         const uint16_t* scales, const uint8_t* zeros, int64_t N, int group, void* y, int64_t ldy,
+                         const Epilogue& ep, void* ws, hipStream_t st) {
+  using namespace awqk;
+  const uint16_t* xp = (const uint16_t*)x;
+  const int glog = group == 64 ? 6 : group == 128 ? 7 : group == 256 ? 8 : -1;
+  if (glog < 0) return hipErrorInvalidValue;
+  if (xdt == DT_F16) return linear_dispatch<DT_F16>(xp, M, K, ldx, qw, scales, zeros, N, glog, y, ldy, ep, ws, st);
+  return linear_dispatch<DT_BF16>(xp, M, K, ldx, qw, scales, zeros, N, glog, y, ldy, ep, ws, st);
+}
 
 size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int group) {
   if (M <= 0 || N <= 0 || K <= 0 || group <= 0 || (M == 1 && gemv1_supported(K, N))) return 0;
@@ -1118,17 +1096,13 @@ size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int group) {
 hipError_t launch_w4a16(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx,
                         const uint32_t* qw, const uint16_t* scales, const uint8_t* zeros,
                         int64_t N, int group, const float* inv_s, void* y, int ydt, int64_t ldy,
-                        void* ws, hipStream_t st, const Epilogue* ep) {
+                        void* ws, hipStream_t st) {
   using namespace awqk;
   const uint16_t* xp = (const uint16_t*)x;
   const int glog = group == 64 ? 6 : group == 128 ? 7 : group == 256 ? 8 : -1;
   if (glog < 0) return hipErrorInvalidValue;
-  if (ep)                                         // the output's type is the epilogue's
-    return xdt == DT_F16
-               ? w4a16_dispatch<DT_F16, DT_F32>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st, *ep)
-               : w4a16_dispatch<DT_BF16, DT_F32>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st, *ep);
 #define AWQ_WD(XT, YT) \
-  return w4a16_dispatch<XT, YT>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st, NoEpi{})
+  return w4a16_dispatch<XT, YT>(xp, M, K, ldx, qw, scales, zeros, N, glog, inv_s, y, ldy, ws, st)
   if (xdt == DT_F16) {
     if (ydt == DT_F16) AWQ_WD(DT_F16, DT_F16);
     if (ydt == DT_BF16) AWQ_WD(DT_F16, DT_BF16);
