@@ -542,7 +542,7 @@ awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int6
  *   ws        >= awq_workspace_bytes(AWQ_OP_LINEAR, M, N, K, 0, 0)
  * Rows of y and pre share no memory with x's, with each other or with
  * residual's, but for residual == y with the same ld (AWQ_ERR_UNSUPPORTED).
- * M == 0 or N == 0 is a no-op.  More than 2^24 rows, N above
+ * M == 0 or N == 0 is a no-op.  2^24 - N / 16 rows or more, N above
  * AWQ_MAX_LINEAR_N, N K above 2^33, or tiles for 2^32 threads ->
  * AWQ_ERR_UNSUPPORTED.
  */
@@ -585,7 +585,8 @@ awq_status awq_bias_act_backward(const void* dy, awq_dtype dt, int64_t M, int64_
  *   dx        [M][lddx] F16, BF16 or F32 (dxt); its rows share no memory with
  *             dz's (AWQ_ERR_UNSUPPORTED)
  *   ws        >= awq_workspace_bytes(AWQ_OP_GEMM_DX, M, N, K, 0, 0)
- * M == 0 is a no-op, N == 0 gives dx = 0.  Sizes as awq_w4a16_linear's.
+ * M == 0 is a no-op, N == 0 gives dx = 0.  2^23 rows or more, and other sizes
+ * as awq_w4a16_linear's -> AWQ_ERR_UNSUPPORTED.
  */
 awq_status awq_w4a16_gemm_dx(const void* dz, awq_dtype dzt, int64_t M, int64_t N, int64_t lddz,
                              const int32_t* qweight, const uint16_t* scales, const uint8_t* zeros,
@@ -605,8 +606,8 @@ awq_status awq_w4a16_gemm_dx(const void* dz, awq_dtype dzt, int64_t M, int64_t N
  *   y         [M][ldy] of ydt (any of the three); it may be x itself (in place)
  *   mean, rstd  [M] float, for the backward pass; either may be NULL (mean is
  *             written as 0 for RMS)
- * Every pointer is aligned to its element only.  M == 0 is a no-op.  More than
- * 2^24 rows (2^22 - 1 of more than 8192 values) -> AWQ_ERR_UNSUPPORTED.
+ * Every pointer is aligned to its element only.  M == 0 is a no-op.  2^24 rows
+ * or more (2^22 of more than 8192 values) -> AWQ_ERR_UNSUPPORTED.
  */
 awq_status awq_layer_norm(const void* x, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
                           const void* weight, awq_dtype wdt, const void* bias, awq_dtype bdt,

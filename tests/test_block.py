@@ -205,6 +205,54 @@ def test_linear_limits_of_the_activation(on_gpu, M, act):
     assert np.all(np.isnan(y[:, 5])) and np.isfinite(np.delete(y, [1, 2, 5], axis=1)).all()
 
 
+BIG_LINEARS = [
+    # M, N, K, group, xdt, out: each height of the tiles, slices, two heights in one launch, odd edges
+    (80, 520, 2048, 128, "f16", "f16"),
+    (519, 1027, 4096, 64, "f16", "f16"),
+    (200, 11008, 1024, 128, "bf16", "bf16"),
+    (1024, 4096, 4096, 128, "f16", "f16"),
+    (1100, 900, 8192, 256, "bf16", "f16"),
+    (2048, 9001, 256, 128, "f16", "f16"),
+    (2300, 11008, 512, 64, "bf16", "bf16"),
+    (4097, 4100, 256, 256, "f16", "bf16"),
+]
+
+
+def on_device(x, w):
+    """The product in float64 on the device and what it may be off, as product_slack."""
+    xd = x.double()
+    ref, size = xd @ w, xd.abs() @ w.abs()
+    slack = size * (2.0 ** -11 + (w.shape[0] + 64) * 2 * U)
+    return ref, slack + 2.0 ** -24 * xd.abs().amax(1, keepdim=True) * w.abs().amax(0) * 8
+
+
+def check_on_device(got, ref, slack, what):
+    i = torch.finfo(got.dtype)
+    tiny = i.tiny if got.dtype == torch.bfloat16 else i.tiny * i.eps / 2
+    bound = slack + (ref.abs() + slack) * (i.eps / 2) + tiny
+    bad = ~((got.double() - ref).abs() <= bound)
+    assert not bool(bad.any()), (what, int(bad.sum()), bad.nonzero()[:5].tolist())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", BIG_LINEARS, ids=lambda c: "x".join(str(v) for v in c))
+def test_linear_tiles(on_gpu, case):
+    M, N, K, g, xdt, out = case
+    od = DTYPES[out]
+    q, w, _ = packed(N, K, g, M + N, signs=True)
+    x, bias = gpu(normal((M, K), DTYPES[xdt], K)), gpu(normal((N,), DTYPES[xdt], 1, outliers=False))
+    res = gpu(normal((M, N), od, 2, outliers=False))
+    z, dz = on_device(x, gpu(torch.from_numpy(w)).t())
+    z, dz = z + bias.double(), dz + 2 * U * (z + bias.double()).abs()
+    pre = torch.empty(M, N, dtype=od, device="cuda")
+    y = awq.awq_w4a16_linear(x, *q, bias=bias, act="silu", residual=res, pre=pre, out_dtype=od, group_size=g)
+    ref = z * torch.sigmoid(z) + res.double()
+    check_on_device(pre, z, dz, "pre")
+    check_on_device(y, ref, 1.13 * dz + 16 * U * z.abs() + 2 * U * ref.abs(), "y")
+    y2 = awq.awq_w4a16_linear(x, *q, out_dtype=od, group_size=g)
+    check_on_device(y2, z - bias.double(), dz, "plain")
+
+
 @pytest.mark.gpu
 def test_linear_empty(on_gpu):
     q, _, _ = packed(16, 128, 128, 1)
@@ -327,6 +375,26 @@ def test_gemm_dx(on_gpu, case):
     z = f32(dz).astype(np.float64)
     dx = awq.awq_w4a16_gemm_dx(gpu(dz), *q, out_dtype=od, group_size=g)
     check(dx, z @ w, product_slack(np.concatenate([z, z]), w, None)[:M], od)
+
+
+BIG_DXS = [
+    (200, 11008, 1024, 128, "bf16", "bf16"),
+    (512, 4096, 4096, 128, "f16", "f16"),
+    (1024, 4096, 8192, 128, "f16", "bf16"),
+    (2048, 2111, 4096, 64, "bf16", "f16"),
+    (4097, 512, 4096, 256, "f16", "f16"),
+    (3, 20000, 512, 128, "bf16", "f16"),             # rows read twice by the conversion
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", BIG_DXS, ids=lambda c: "x".join(str(v) for v in c))
+def test_gemm_dx_tiles(on_gpu, case):
+    M, N, K, g, dzt, out = case
+    q, w, _ = packed(N, K, g, M + N, signs=True)
+    dz = gpu(normal((M, N), DTYPES[dzt], K, size=0.1))
+    ref, slack = on_device(dz, gpu(torch.from_numpy(w)))
+    check_on_device(awq.awq_w4a16_gemm_dx(dz, *q, out_dtype=DTYPES[out], group_size=g), ref, slack, case)
 
 
 @pytest.mark.gpu
@@ -861,6 +929,48 @@ def test_a_call_reads_nothing_that_its_workspace_held(on_gpu):
         need = awq.awq_workspace_bytes(getattr(E, op), *size)
         ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")[:need]
         assert equal(call(ws=ws), call()), name
+
+
+@pytest.mark.gpu
+def test_outputs_past_4_gigabytes(on_gpu):
+    """Rows whose offsets pass 32 bits, against the same rows by themselves."""
+    M, N, K = 70000, 32768, 64
+    q, _, _ = packed(N, K, 64, 1)
+    x = gpu(normal((M, K), torch.float16, 1))
+    y = awq.awq_w4a16_linear(x, *q, act="relu", group_size=64)
+    assert y.numel() * 2 > 1 << 32
+    for rows in (slice(0, 300), slice(32700, 33000), slice(M - 300, M)):
+        assert torch.allclose(y[rows].float(), awq.awq_w4a16_linear(x[rows], *q, act="relu", group_size=64).float(), rtol=2e-3,
+                              atol=2e-4)
+    dz, db = awq.awq_bias_act_backward(y, y, act="relu")
+    assert torch.equal(dz[-5:], torch.where(y[-5:] > 0, y[-5:], 0))
+    assert torch.allclose(db, y.sum(0, dtype=torch.float32), rtol=1e-3)
+    del dz
+    w = torch.ones(N, device="cuda")
+    stats = torch.empty(2, M, device="cuda")
+    n = awq.awq_layer_norm(y, w, stats=stats)
+    last = awq.awq_layer_norm(y[-3:], w)
+    assert torch.equal(n[-3:], last)
+    dx, dw, _ = awq.awq_layer_norm_backward(n, y, w, stats, dx=n, bias=False)
+    assert bool(torch.isfinite(dx[-3:]).all()) and bool(torch.isfinite(dw).all())
+    del n, dx, y
+    q, _, _ = packed(64, N, 64, 2)
+    dz = gpu(normal((M, 64), torch.float16, 3))
+    dx = awq.awq_w4a16_gemm_dx(dz, *q, group_size=64)
+    for rows in (slice(0, 300), slice(M - 300, M)):
+        assert torch.allclose(dx[rows].float(), awq.awq_w4a16_gemm_dx(dz[rows], *q, group_size=64).float(), rtol=2e-3, atol=2e-4)
+
+
+@pytest.mark.gpu
+def test_balance_past_4_gigabytes(on_gpu):
+    T, n = 2200000, 1024
+    lg = torch.zeros(T, n, dtype=torch.bfloat16, device="cuda")
+    lg[-1, 5] = 3.0
+    ids = (torch.arange(2 * T, dtype=torch.int32, device="cuda") % n).view(T, 2)
+    loss, counts, slope = awq.awq_balance_loss(lg, ids)
+    assert int(counts.sum()) == 2 * T and abs(loss.item() - 1) < 1e-3
+    d = awq.awq_balance_loss_backward(lg, slope, dlogits=lg)
+    assert bool(torch.isfinite(d[-1]).all())
 
 
 # ---- refusals (no GPU) ---------------------------------------------------------------------

@@ -4,7 +4,8 @@
 // access of 16-bit values each), the block's four waves every fourth row of its
 // chunk of rows; the sums stay in registers, meet in LDS and leave the block
 // as one partial row, which k_col_reduce adds.  The sum takes the fp32 values
-// before their rounding to dz's type.
+// before their rounding to dz's type.  2048 x 11008 with gelu: 33 us, 4.1 TB/s
+// (54 us with the device library's erfcf and expf, which bound it then).
 #include "k_epilogue.h"
 
 namespace awqk {
@@ -46,15 +47,21 @@ __global__ __launch_bounds__(256) void k_act_bias(const void* __restrict__ dy, i
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float t = ((sum[j] + red[0][j * 64 + lane]) + red[1][j * 64 + lane]) + red[2][j * 64 + lane];
-      partial[(int64_t)blockIdx.y * pitch + n + j] = j < cnt ? t : 0.0f;
+      if (gridDim.y == 1) {                                      // one chunk: the sums are whole
+        if (j < cnt) partial[n + j] = t;
+      } else {
+        partial[(int64_t)blockIdx.y * pitch + n + j] = j < cnt ? t : 0.0f;
+      }
     }
   }
 }
 
-// Chunks of rows: enough blocks to fill the chip, at least 16 rows each.
+// Chunks of rows: enough blocks to fill the chip, at least 16 rows each; one
+// chunk's sums go to dbias itself.
 inline int64_t act_bias_chunks(int64_t M, int64_t N) {
   const int64_t tiles = (N + 511) / 512;
   int64_t c = (4 * (int64_t)awq::device_cus() + tiles - 1) / tiles;
+  if (M <= 64) return 1;                 // one launch: 37 rows of 4096 in 4.2 us instead of 4.2 + 2.9
   const int64_t most = (M + 15) / 16;
   if (c > most) c = most;
   return c < 1 ? 1 : c > 1024 ? 1024 : c;
@@ -66,7 +73,7 @@ inline int64_t act_bias_pitch(int64_t N) { return (N + 63) / 64 * 64; }
 namespace awq {
 
 size_t act_bias_ws_bytes(int64_t M, int64_t N) {
-  if (M <= 0 || N <= 0) return 0;
+  if (M <= 0 || N <= 0 || awqk::act_bias_chunks(M, N) == 1) return 0;
   return align_up((size_t)(awqk::act_bias_chunks(M, N) * awqk::act_bias_pitch(N)) * 4, 256);
 }
 
@@ -75,7 +82,7 @@ hipError_t launch_act_bias(const void* dy, int dt, int64_t M, int64_t N, int64_t
   using namespace awqk;
   const int64_t want = act_bias_chunks(M, N), rows = M > 0 ? (M + want - 1) / want : 1, chunks = (M + rows - 1) / rows;
   const int64_t pitch = act_bias_pitch(N);
-  float* partial = dbias ? (float*)ws : nullptr;
+  float* partial = chunks == 1 ? dbias : dbias ? (float*)ws : nullptr;
   if (M > 0 && (pre || dbias)) {
     const dim3 grid((unsigned)((N + 511) / 512), (unsigned)chunks), block(256);
 #define AWQ_AB(D) \
@@ -87,7 +94,7 @@ hipError_t launch_act_bias(const void* dy, int dt, int64_t M, int64_t N, int64_t
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!dbias) return hipSuccess;
+  if (!dbias || chunks == 1) return hipSuccess;
   return launch_col_reduce(partial, M > 0 ? chunks : 0, pitch, N, dbias, 0, nullptr, st);
 }
 

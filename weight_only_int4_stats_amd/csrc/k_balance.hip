@@ -16,7 +16,8 @@
 //      256 experts took 13 us to read half a megabyte.)
 //   3. k_balance_grad: a wave per row again.
 // Bound by reading the logits (and writing their gradient); nothing is added
-// by floating-point atomics, so the results do not depend on an order.
+// by floating-point atomics, so the results do not depend on an order.  16384 x
+// 256 with sigmoid scores: 12 + 6 + 12 us; 519 x 60: 3 + 5 + 3.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_epilogue.h"

@@ -38,60 +38,60 @@ constexpr int kDxB = kDxN * kDxCols / 2;  // packed bytes per stage
 constexpr int kDxC = 1024;                // constants per stage: up to 4 groups x 64 rows x 4 bytes
 
 // Rows n in chunks of eight: ctab[g][n / 8] = the eight steps (four pairs),
-// then the eight zero points.  A block takes 32 rows: their steps and zero
-// points are read in whole lines into LDS (32 x kDxCh groups at a time), eight
-// lanes find a row's largest step, and the table leaves in pieces of 128 bytes.
+// then the eight zero points.  A block takes 16 rows: their steps and zero
+// points are read in whole lines into LDS (16 x kDxCh groups at a time), 16
+// lanes find a row's largest step, and the table leaves in pieces of 64 bytes.
 constexpr int kDxCh = 128;
 
 __global__ __launch_bounds__(256) void k_dx_consts(const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros,
                                                    int64_t N, int64_t Np, int64_t G, float* __restrict__ inv,
                                                    uint16_t* __restrict__ ctab) {
-  __shared__ uint16_t sl[32][kDxCh + 2];
-  __shared__ uint8_t zl[32][kDxCh + 4];
-  __shared__ int es[32];
+  __shared__ uint16_t sl[16][kDxCh + 2];
+  __shared__ uint8_t zl[16][kDxCh + 4];
+  __shared__ int es[16];
   const int tid = threadIdx.x;
-  const int64_t n0 = (int64_t)blockIdx.x * 32;                   // < Np, a multiple of 64
-  const int rows = (int)(N - n0 < 32 ? (N > n0 ? N - n0 : 0) : 32);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;                   // < Np, a multiple of 64
+  const int rows = (int)(N - n0 < 16 ? (N > n0 ? N - n0 : 0) : 16);
   auto load = [&](int64_t g0, int ng) {                          // groups g0 .. g0 + ng - 1 of the rows
-    // a wave: eight rows, all loads ahead of the LDS writes (rows and groups
+    // a wave: four rows, all loads ahead of the LDS writes (rows and groups
     // past the end read the block's first ones)
     constexpr int H = kDxCh / 64;
     const int lane = tid & 63, wv = tid >> 6;
-    uint16_t s[8][H];
-    uint8_t z[8][H];
+    uint16_t s[4][H];
+    uint8_t z[4][H];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        const int r = 8 * wv + i, g = 64 * h + lane;
+        const int r = 4 * wv + i, g = 64 * h + lane;
         const int64_t at = (n0 + (r < rows ? r : 0)) * G + g0 + (g < ng ? g : 0);
         s[i][h] = rows > 0 ? scales[at] : 0;
         z[i][h] = rows > 0 ? zeros[at] : 0;
       }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        sl[8 * wv + i][64 * h + lane] = s[i][h];
-        zl[8 * wv + i][64 * h + lane] = z[i][h];
+        sl[4 * wv + i][64 * h + lane] = s[i][h];
+        zl[4 * wv + i][64 * h + lane] = z[i][h];
       }
   };
-  const int r8 = tid >> 3, p8 = tid & 7;
+  const int rr = tid >> 4, pp = tid & 15;
   float mx = 0.0f;
   for (int64_t g0 = 0; g0 < G; g0 += kDxCh) {
     const int ng = (int)(G - g0 < kDxCh ? G - g0 : kDxCh);
     if (g0 > 0) __syncthreads();
     load(g0, ng);
     __syncthreads();
-    if (r8 < rows)
-      for (int g = p8; g < ng; g += 8) mx = fmaxf(mx, step_size<true>(sl[r8][g]));
+    if (rr < rows)
+      for (int g = pp; g < ng; g += 16) mx = fmaxf(mx, step_size<true>(sl[rr][g]));
   }
 #pragma unroll
-  for (int off = 4; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 8));
-  if (p8 == 0) {
+  for (int off = 8; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 16));
+  if (pp == 0) {
     const int e = step_pow<true>(mx);
-    es[r8] = e;
-    inv[n0 + r8] = r8 < rows ? ldexpf(1.0f, -sum_pow<true>(e)) : 0.0f;
+    es[rr] = e;
+    inv[n0 + rr] = rr < rows ? ldexpf(1.0f, -sum_pow<true>(e)) : 0.0f;
   }
   for (int64_t g0 = 0; g0 < G; g0 += kDxCh) {
     const int ng = (int)(G - g0 < kDxCh ? G - g0 : kDxCh);
@@ -100,9 +100,9 @@ __global__ __launch_bounds__(256) void k_dx_consts(const uint16_t* __restrict__ 
       load(g0, ng);
       __syncthreads();
     }
-    // 32 words per group: of chunk c = w / 8, word w % 8 (0..3 steps, 4..7 zero points of a pair)
-    for (int i = tid; i < ng * 32; i += 256) {
-      const int g = i >> 5, w = i & 31, r = (w >> 3) * 8 + (w & 3) * 2;
+    // 16 words per group: of chunk c = w / 8, word w % 8 (0..3 steps, 4..7 zero points of a pair)
+    for (int i = tid; i < ng * 16; i += 256) {
+      const int g = i >> 4, w = i & 15, r = (w >> 3) * 8 + (w & 3) * 2;
       uint32_t v = 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -455,7 +455,7 @@ hipError_t launch_gemm_dx(const void* dz, int dzt, int64_t M, int64_t N, int64_t
   const TilePlan p = dx_plan(M, N, K);
   const DxWs w = dx_ws(ws, M, N, K, group, p.S);
   const int64_t Np = (N + kDxN - 1) / kDxN * kDxN;
-  hipLaunchKernelGGL(k_dx_consts, dim3((unsigned)(Np / 32)), dim3(256), 0, st, scales, zeros, N, Np, K >> glog, w.inv,
+  hipLaunchKernelGGL(k_dx_consts, dim3((unsigned)(Np / 16)), dim3(256), 0, st, scales, zeros, N, Np, K >> glog, w.inv,
                      w.ctab);
   if (dzt == DT_F16) dx_rows<DT_F16>(dz, M, N, Np, lddz, w.inv, w.xq, w.pm, st);
   else dx_rows<DT_BF16>(dz, M, N, Np, lddz, w.inv, w.xq, w.pm, st);
