@@ -496,7 +496,7 @@ def sum_rows(M, K):
 @pytest.mark.gpu
 @pytest.mark.parametrize("rms", [False, True])
 @pytest.mark.parametrize("xdt,dyt", [("f16", "f16"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
-@pytest.mark.parametrize("shape", NORMS + [(2050, 40), (1100, 700), (600, 16400)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shape", NORMS + [(2050, 40), (1100, 700), (600, 16400), (8, 5000), (9, 5000), (128, 300), (129, 300)], ids=lambda s: "x".join(map(str, s)))
 def test_layer_norm_backward(on_gpu, shape, xdt, dyt, rms):
     M, K = shape
     x = normal(shape, DTYPES[xdt], K)
@@ -617,6 +617,9 @@ BALANCES = [
     (519, 60, 4, "softmax", "f32"),
     (257, 128, 6, "sigmoid", "bf16"),
     (300, 257, 16, "sigmoid", "f32"),
+    (64, 512, 3, "softmax", "f32"),                  # the most that one block takes, and one more
+    (65, 96, 3, "sigmoid", "bf16"),
+    (40, 1024, 8, "sigmoid", "f16"),
     (1500, 512, 8, "softmax", "bf16"),
     (70, 1000, 64, "sigmoid", "f16"),
     (2100, 1024, 2, "softmax", "f32"),
@@ -1060,7 +1063,7 @@ def test_layer_norm_refusals():
 def test_layer_norm_backward_refusals():
     c = refuses("awq_layer_norm_backward", ["dy", "dyt", "M", "K", "lddy", "x", "xdt", "ldx", "w", "wdt", "mean", "rstd", "rms", "dx",
                                             "lddx", "dw", "db", "ws", "wsb"],
-                dict(dy=A, dyt=0, M=100, K=500, lddy=500, x=A2, xdt=0, ldx=500, w=A3, wdt=0, mean=A3, rstd=A3, rms=0, dx=A4, lddx=500,
+                dict(dy=A, dyt=0, M=1000, K=500, lddy=500, x=A2, xdt=0, ldx=500, w=A3, wdt=0, mean=A3, rstd=A3, rms=0, dx=A4, lddx=500,
                      dw=A5, db=A5, ws=WS, wsb=BIG))
     c(3, dyt=3), c(3, xdt=3), c(3, wdt=3)
     c(2, M=-1), c(2, K=0), c(2, lddy=499), c(2, ldx=499), c(2, lddx=499)
@@ -1100,7 +1103,7 @@ def test_workspace_of_the_largest_batch_serves_all(N, K):
         assert awq.awq_workspace_bytes(op, (1 << 24) + 1, N, K) == awq.awq_workspace_bytes(op, 4, (1 << 22) + 1, K) == 0
         assert awq.awq_workspace_bytes(op, 4, N, 131073) == awq.awq_workspace_bytes(op, -1, N, K) == 0
     assert awq.awq_workspace_bytes(E.AWQ_OP_BALANCE_LOSS, 4, 0, 0, 1025) == 0
-    assert awq.awq_workspace_bytes(E.AWQ_OP_BALANCE_LOSS, 4, 0, 0, 1024) > 0
+    assert awq.awq_workspace_bytes(E.AWQ_OP_BALANCE_LOSS, 1000, 0, 0, 1024) > 0
 
 
 def test_binding_refuses_host_tensors_and_wrong_names():

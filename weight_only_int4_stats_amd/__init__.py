@@ -704,8 +704,9 @@ def awq_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float = 1.0,
         raise ValueError("ids must be [tokens, top_k]")
     device, dev = logits.device, logits.get_device()
     top_k = ids.shape[1]
-    out = torch.empty(2 * E + 1, dtype=torch.float32, device=device)   # one allocation: slope, counts, loss
-    slope, counts, loss = out[:E], out[E:2 * E].view(torch.int32), out[2 * E:]
+    loss = torch.empty(1, dtype=torch.float32, device=device)
+    counts = torch.empty(E, dtype=torch.int32, device=device)
+    slope = torch.empty(E, dtype=torch.float32, device=device)
     ws, wsp, wsb = _ws(AWQ_OP_BALANCE_LOSS, device, ws, T, 0, 0, E, 0)
     _launch("awq_balance_loss", dev,
             (logits.data_ptr(), _DT.get(logits.dtype, -1), T, E, ldl, _same(ids, "ids", dev, torch.int32, (T, top_k)),

@@ -167,11 +167,20 @@ struct BalanceArgs {
   const void* logits;
   const int32_t* ids;
   const uint8_t* mask;
+  float* loss;           // one block forms the results by itself
+  int32_t* counts;
+  float* slope;
+  double coef;
   float2* partial;       // [blocks][pitch]: sum of p, slots (an integer's bits); at E (the bits of) all slots, rows
   BalanceEnd* last;
   int64_t T, ldl, pitch;
   int E, top_k;
 };
+
+// The loss's derivative by a p: coef E c / (n T').
+__device__ __forceinline__ double bal_slope(double coef, int E, int c, double slots, double rows) {
+  return slots > 0.0 && rows > 0.0 ? coef * (double)E * (double)c / (slots * rows) : 0.0;
+}
 
 template <int DT, int V, int H, bool SIG>
 __global__ __launch_bounds__(64 * kBalWaves) void k_balance(const BalanceArgs a) {
@@ -182,7 +191,7 @@ __global__ __launch_bounds__(64 * kBalWaves) void k_balance(const BalanceArgs a)
   float* meet = reinterpret_cast<float*>(bal_lds + a.E + 2);     // [kBalWaves][64 N]
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   for (int e = threadIdx.x; e <= a.E + 1; e += 64 * kBalWaves) hist[e] = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.last->done = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && gridDim.x > 1) a.last->done = 0;
   __syncthreads();
   float acc[N], next[N];
 #pragma unroll
@@ -224,6 +233,29 @@ __global__ __launch_bounds__(64 * kBalWaves) void k_balance(const BalanceArgs a)
 #pragma unroll
     for (int j = 0; j < V; ++j) meet[wv * 64 * N + Map::first(lane, h) + j] = acc[h * V + j];
   __syncthreads();
+  if (gridDim.x == 1) {
+    __shared__ double part[kBalWaves];
+    const double slots = hist[a.E], rows = hist[a.E + 1];
+    double l = 0.0;
+    for (int e = threadIdx.x; e < a.E; e += 64 * kBalWaves) {
+      const double sl = bal_slope(a.coef, a.E, hist[e], slots, rows);
+      double p = 0.0;
+#pragma unroll
+      for (int w = 0; w < kBalWaves; ++w) p += meet[w * 64 * N + e];
+      l += sl * p;
+      a.counts[e] = hist[e];
+      a.slope[e] = (float)sl;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off);
+    if (lane == 0) part[wv] = l;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kBalWaves; ++w) l += part[w];
+      a.loss[0] = (float)l;
+    }
+    return;
+  }
   for (int e = threadIdx.x; e <= a.E; e += 64 * kBalWaves) {
     float2 v = make_float2(0.0f, __int_as_float(hist[e]));
     if (e < a.E) {
@@ -293,7 +325,7 @@ __global__ __launch_bounds__(1024) void k_balance_finish(const float2* __restric
     slots += tot[0][w];
     rows += tot[1][w];
   }
-  const double sl = slots > 0 && rows > 0 ? coef * (double)E * (double)c / ((double)slots * (double)rows) : 0.0;
+  const double sl = bal_slope(coef, E, c, (double)slots, (double)rows);
   double l = e < E ? sl * p : 0.0;
   if (e < E) {
     counts[e] = c;
@@ -392,8 +424,10 @@ __global__ __launch_bounds__(64 * kBalGradWaves) void k_balance_grad(const Balan
 }
 
 inline int64_t balance_blocks(int64_t T) {
+  // a row per wave up to 256 blocks; up to eight rows per wave make one block,
+  // which forms the results by itself
   const int64_t want = (T + kBalWaves - 1) / kBalWaves;
-  return want < 256 ? want : 256;
+  return want <= 8 ? 1 : want < 256 ? want : 256;
 }
 inline int64_t balance_pitch(int64_t E) { return (E + 1 + 63) / 64 * 64; }
 
@@ -432,7 +466,7 @@ hipError_t balance_typed(const A& a, int dt, bool sigmoid, int64_t blocks, hipSt
 namespace awq {
 
 size_t balance_ws_bytes(int64_t T, int64_t E) {
-  if (T <= 0 || E <= 0) return 0;
+  if (T <= 0 || E <= 0 || awqk::balance_blocks(T) == 1) return 0;
   return align_up((size_t)(awqk::balance_blocks(T) * awqk::balance_pitch(E)) * 8, 256) + 256;   // and a BalanceEnd
 }
 
@@ -447,10 +481,10 @@ hipError_t launch_balance(const void* logits, int dt, int64_t T, int64_t E, int6
   }
   BalanceEnd* last = (BalanceEnd*)ws;
   static_assert(sizeof(BalanceEnd) <= 256, "ahead of the partial rows");
-  float2* partial = (float2*)((char*)ws + 256);
-  const hipError_t e = balance_typed(BalanceArgs{logits, ids, mask, partial, last, T, ldl, pitch, (int)E, top_k}, dt,
+  float2* partial = ws ? (float2*)((char*)ws + 256) : nullptr;
+  const hipError_t e = balance_typed(BalanceArgs{logits, ids, mask, loss, counts, slope, coef, partial, last, T, ldl, pitch, (int)E, top_k}, dt,
                                      sigmoid != 0, blocks, st);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || blocks == 1) return e;
   hipLaunchKernelGGL(k_balance_finish, dim3((unsigned)((E + 63) / 64)), dim3(1024), 0, st, partial, (int)blocks, pitch,
                      (int)E, coef, loss, counts, slope, last);
   return hipGetLastError();

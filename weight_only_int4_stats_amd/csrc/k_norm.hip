@@ -166,8 +166,9 @@ struct NormGradArgs {
   const float* mean;
   const float* rstd;
   void* dx;
-  float* partial;        // [blocks][2 pitch]: dw, then db from pitch on
-  bool dw, db;           // which of them to form
+  float* partial;        // [blocks][2 pitch]: dw, then db from pitch on (one block: not used)
+  float* dw;             // the sums themselves; NULL: not formed
+  float* db;
   int64_t M, K, lddy, ldx, lddx, pitch;
   int dyt, wdt;
 };
@@ -259,8 +260,10 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W,
       store8_any(a.dx, XDT, m * a.lddx + (int64_t)(t + T * i) * 8, cnt[i], g[i]);
     }
   }
-  // the row groups' sums meet in the first one's, in their order
-  float* out = a.partial + (int64_t)blockIdx.x * 2 * a.pitch;
+  // the row groups' sums meet in the first one's, in their order; one block's
+  // are whole
+  const bool whole = gridDim.x == 1;
+  float* part = a.partial + (int64_t)blockIdx.x * 2 * a.pitch;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     float (&d)[KEEP][8] = half ? db : dw;
@@ -282,7 +285,8 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W,
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           for (int q = 0; q < RB - 1; ++q) d[i][j] += meet[(q * KEEP * 8 + i * 8 + j) * T + t];
-        if (c < a.pitch) store8_any(out, DT_F32, half * a.pitch + c, 8, d[i]);
+        if (whole) store8_any(half ? a.db : a.dw, DT_F32, c, cnt[i], d[i]);
+        else if (c < a.pitch) store8_any(part, DT_F32, half * a.pitch + c, 8, d[i]);
       }
     }
   }
@@ -383,12 +387,19 @@ inline NormGradPlan norm_grad_plan(int64_t M, int64_t K) {
   // one block per compute unit, with as many rows each as make the whole, and
   // at least four: a block's partial sums cost as much as a row or two (519 x
   // 5120: 10 us with four rows a block, 11 with three, 14 with two and two
-  // blocks per unit; 8192 x 4096: 43 us with one block per unit, 49 with two)
+  // blocks per unit; 8192 x 4096: 43 us with one block per unit, 49 with two).
+  // Up to eight make one block, whose sums are whole: no second launch.
   const int64_t sets = (M + p.groups - 1) / p.groups;
   int64_t each = (sets + cus - 1) / cus;
-  each = each < 4 && sets > 0 ? (sets < 4 ? sets : 4) : each;
-  p.blocks = each > 0 ? (sets + each - 1) / each : 0;
+  if (each < 4) each = 4;
+  if (sets <= 8 && p.waves > 0) each = 8;
+  p.blocks = (sets + each - 1) / each;
   return p;
+}
+// Whether one block forms the sums by itself.
+inline bool norm_grad_whole(int64_t M, int64_t K) {
+  const NormGradPlan p = norm_grad_plan(M, K);
+  return p.waves > 0 && p.blocks == 1;
 }
 inline int64_t norm_pitch(int64_t K) { return (K + 63) / 64 * 64; }
 
@@ -426,7 +437,7 @@ hipError_t launch_norm(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx
 }
 
 size_t norm_grad_ws_bytes(int64_t M, int64_t K) {
-  if (M <= 0 || K <= 0) return 0;
+  if (M <= 0 || K <= 0 || awqk::norm_grad_whole(M, K)) return 0;
   return (size_t)(awqk::norm_grad_plan(M, K).blocks * 2 * awqk::norm_pitch(K)) * 4;
 }
 
@@ -445,14 +456,14 @@ hipError_t launch_norm_grad(const void* dy, int dyt, int64_t M, int64_t K, int64
   const int64_t pitch = norm_pitch(K);
   const bool sums = dw || db;
   if (M > 0) {
-    const NormGradArgs a{dy, x, w, mean, rstd, dx, (float*)ws, dw != nullptr, db != nullptr, M, K, lddy, ldx, lddx, pitch, dyt, wdt};
+    const NormGradArgs a{dy, x, w, mean, rstd, dx, (float*)ws, dw, db, M, K, lddy, ldx, lddx, pitch, dyt, wdt};
     hipError_t e;
     if (xdt == DT_F16) e = rms ? norm_grad_dispatch<DT_F16, true>(a, st) : norm_grad_dispatch<DT_F16, false>(a, st);
     else if (xdt == DT_BF16) e = rms ? norm_grad_dispatch<DT_BF16, true>(a, st) : norm_grad_dispatch<DT_BF16, false>(a, st);
     else e = rms ? norm_grad_dispatch<DT_F32, true>(a, st) : norm_grad_dispatch<DT_F32, false>(a, st);
     if (e != hipSuccess) return e;
   }
-  if (!sums) return hipSuccess;
+  if (!sums || (M > 0 && norm_grad_whole(M, K))) return hipSuccess;
   return launch_col_reduce((const float*)ws, M > 0 ? norm_grad_plan(M, K).blocks : 0, 2 * pitch, K, dw, pitch, db, st);
 }
 
