@@ -598,7 +598,8 @@ awq_status awq_w4a16_gemm_dx(const void* dz, awq_dtype dzt, int64_t M, int64_t N
  * bias awq_fold_scales folds 1/s.
  *   mean = sum_k x_k / K  (rms != 0: 0),  rstd = 1 / sqrt(sum_k (x_k - mean)^2 / K + eps)
  *   y_k  = (x_k - mean) rstd weight_k + bias_k          (bias == NULL: 0)
- * in fp32, the variance from the centred values; y rounded once.
+ * in fp32, the variance from the centred values (the sum of their squares within
+ * fp32's range); y rounded once.
  *
  *   x         [M][ldx] F16, BF16 or F32 (xdt), 1 <= K <= AWQ_MAX_K
  *   weight    [K] of wdt, bias [K] of bdt (any of the three) or NULL

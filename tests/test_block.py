@@ -617,8 +617,8 @@ BALANCES = [
     (519, 60, 4, "softmax", "f32"),
     (257, 128, 6, "sigmoid", "bf16"),
     (300, 257, 16, "sigmoid", "f32"),
-    (64, 512, 3, "softmax", "f32"),                  # the most that one block takes, and one more
-    (65, 96, 3, "sigmoid", "bf16"),
+    (128, 512, 3, "softmax", "f32"),                 # the most that one block takes, and one more
+    (129, 96, 3, "sigmoid", "bf16"),
     (40, 1024, 8, "sigmoid", "f16"),
     (1500, 512, 8, "softmax", "bf16"),
     (70, 1000, 64, "sigmoid", "f16"),
@@ -1077,7 +1077,7 @@ def test_layer_norm_backward_refusals():
 
 def test_balance_refusals():
     c = refuses("awq_balance_loss", ["l", "dt", "T", "E", "ldl", "ids", "k", "mask", "score", "coef", "loss", "counts", "slope", "ws", "wsb"],
-                dict(l=A, dt=0, T=100, E=64, ldl=64, ids=A2, k=4, mask=None, score=0, coef=1.0, loss=A3, counts=A3, slope=A3, ws=WS,
+                dict(l=A, dt=0, T=1000, E=64, ldl=64, ids=A2, k=4, mask=None, score=0, coef=1.0, loss=A3, counts=A3, slope=A3, ws=WS,
                      wsb=BIG))
     c(3, dt=3), c(5, score=2), c(2, T=-1), c(2, E=0), c(2, ldl=63), c(2, k=0)
     c(5, E=1025, ldl=2000), c(5, k=65), c(5, T=(1 << 24) + 1)

@@ -64,10 +64,13 @@ size_t linear_ws_bytes_upto(int64_t M, int64_t N, int64_t K) {
   };
   upto(M);
   for (int64_t m = 1; m < M && m <= 64; ++m) upto(m);
-  // fewer rows may be split into more slices, the same for each 16 rows; past
-  // 4 rounds of the tallest tiles nothing is split
-  const int64_t split = 4 * (int64_t)device_cus() * 256;
-  for (int64_t m = 80; m < M && m <= split; m += 16) upto(m);
+  // above 64 tokens the group does not matter, and fewer rows may be split into
+  // more slices, the same for each 16 rows
+  const int64_t split = tile_split_rows(N);
+  for (int64_t m = 80; m < M && m <= split; m += 16) {
+    const size_t b = linear_ws_bytes(m, N, K, 64);
+    most = b > most ? b : most;
+  }
   return most;
 }
 

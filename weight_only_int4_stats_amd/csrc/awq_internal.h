@@ -181,6 +181,10 @@ hipError_t launch_linear_tiles(const uint16_t* xq, const int* pm, const int* en,
                                int64_t M, int64_t N, int64_t K, int group, float* partial, void* y, int64_t ldy,
                                const Epilogue& ep, hipStream_t st);
 
+// Rows up to which the tiles of k_tiles.h may split the contraction
+// (k_linear.hip).
+int64_t tile_split_rows(int64_t cols);
+
 // Column sums of partial rows (k_colsum.hip): columns [0, cols) to out0 and
 // [at1, at1 + cols) to out1 (either may be NULL); pitch a multiple of 64.
 hipError_t launch_col_reduce(const float* partial, int64_t rows, int64_t pitch, int64_t cols, float* out0,

@@ -17,14 +17,14 @@
 //   3. k_balance_grad: a wave per row again.
 // Bound by reading the logits (and writing their gradient); nothing is added
 // by floating-point atomics, so the results do not depend on an order.  16384 x
-// 256 with sigmoid scores: 12 + 6 + 12 us; 519 x 60: 3 + 5 + 3.
+// 256 with sigmoid scores: 15 us and 10 for the gradient; 519 x 60: 8 and 3.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_epilogue.h"
 
 namespace awqk {
 
-constexpr int kBalWaves = 8;           // of k_balance's block
+constexpr int kBalWaves = 16;          // of k_balance's block
 constexpr int kBalGradWaves = 4;       // of k_balance_grad's
 
 // Experts of lane l: V adjacent ones from V l on, H times, 64 V apart.
@@ -108,13 +108,18 @@ __device__ __forceinline__ void bal_store(void* p, int64_t row, int e, int E, co
     if (e + j < E) store_any(p, DT, row + e + j, v[j]);
 }
 
-// exp(x) for x <= 0: 2^(x log2 e) with the product's rounding error (and what
-// log2 e leaves of its fp32 value) put back in first order, so that far scores
-// keep fp32's precision.  Past -126 in the exponent the result is 0.
+// exp(x) for x <= 0.  For logits in 32 bits 2^(x log2 e) with the product's
+// rounding error (and what log2 e leaves of its fp32 value) put back in first
+// order, so that far scores keep fp32's precision; for 16 bits without: |x|
+// 2^-24 of the result, below what the logits themselves hold.  Past -126 in the
+// exponent the result is 0.
+template <bool WIDE>
 __device__ __forceinline__ float bal_exp(float x) {
-  constexpr float hi = 1.44269502f, lo = (float)(1.4426950408889634 - (double)1.44269502f);
-  const float p = fmaxf(x, -1000.0f) * hi;       // (-inf: no inf - inf below)
-  const float r = __builtin_fmaf(x > -1000.0f ? x : -1000.0f, hi, -p) + (x > -1000.0f ? x : -1000.0f) * lo;
+  constexpr float hi = kLog2E, lo = (float)(1.4426950408889634 - (double)kLog2E);
+  if constexpr (!WIDE) return __builtin_amdgcn_exp2f(x * hi);
+  x = x > -1000.0f ? x : -1000.0f;                 // (-inf: no inf - inf below)
+  const float p = x * hi;
+  const float r = __builtin_fmaf(x, hi, -p) + x * lo;
   const float e = __builtin_amdgcn_exp2f(p);
   return __builtin_fmaf(e, r * 0.69314718f, e);
 }
@@ -124,7 +129,7 @@ __device__ __forceinline__ float bal_exp(float x) {
 // -inf and NaN are not usable; +inf counts as the largest float.  Sigmoid
 // scores carry a common factor exp(-min(max l, 0)), so that a row of very low
 // logits does not underflow.
-template <int N, bool SIG, bool REST>
+template <int N, bool SIG, bool REST, bool WIDE>
 __device__ __forceinline__ float bal_scores(float (&s)[N], float (&rest)[N]) {
   float mx = -__builtin_inff();
 #pragma unroll
@@ -139,18 +144,18 @@ __device__ __forceinline__ float bal_scores(float (&s)[N], float (&rest)[N]) {
     return 0.0f;
   }
   float sum = 0.0f;
-  const float c = SIG ? fminf(mx, 0.0f) : mx, ec = SIG ? bal_exp(c) : 0.0f;
+  const float c = SIG ? fminf(mx, 0.0f) : mx, ec = SIG ? bal_exp<WIDE>(c) : 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if constexpr (SIG) {
       // l >= 0 (then c = 0): 1 / (1 + e^-l);  l < 0: e^(l - c) / (1 + e^(l - c) e^c)
       const float l = s[i];
-      const float a = bal_exp(l >= 0.0f ? -l : l - c);
+      const float a = bal_exp<WIDE>(l >= 0.0f ? -l : l - c);
       const float d = quick_rcp(l >= 0.0f ? 1.0f + a : __builtin_fmaf(a, ec, 1.0f));
       s[i] = l >= 0.0f ? d : a * d;
       if constexpr (REST) rest[i] = l >= 0.0f ? a * d : d;
     } else {
-      s[i] = bal_exp(s[i] - c);
+      s[i] = bal_exp<WIDE>(s[i] - c);
     }
     sum += s[i];
   }
@@ -215,7 +220,7 @@ __global__ __launch_bounds__(64 * kBalWaves) void k_balance(const BalanceArgs a)
     const bool on = next_on;
     if (t + step < a.T) fetch(t + step);
     if (!on) continue;
-    const float sum = bal_scores<N, SIG, false>(s, rest);
+    const float sum = bal_scores<N, SIG, false, DT == DT_F32>(s, rest);
     if (sum == 0.0f) continue;
     const float inv = 1.0f / sum;
 #pragma unroll
@@ -403,7 +408,7 @@ __global__ __launch_bounds__(64 * kBalGradWaves) void k_balance_grad(const Balan
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] = next[i];
     if (t + step < a.T) fetch(t + step);
-    const float sum = bal_scores<N, SIG, SIG>(s, rest);
+    const float sum = bal_scores<N, SIG, SIG, DT == DT_F32>(s, rest);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     float q = 0.0f;
 #pragma unroll

@@ -422,12 +422,11 @@ size_t gemm_dx_ws_bytes(int64_t M, int64_t N, int64_t K, int group) {
 }
 
 // The most that any M' <= M needs: fewer rows may be split into more slices.
-// Past four rounds of the tallest tiles nothing is split.
 size_t gemm_dx_ws_bytes_upto(int64_t M, int64_t N, int64_t K) {
   using namespace awqk;
   if (M <= 0 || N <= 0 || K <= 0) return 0;
   size_t most = gemm_dx_ws_bytes(M, N, K, 64);
-  const int64_t split = 4 * (int64_t)device_cus() * 256;
+  const int64_t split = tile_split_rows(K);
   for (int64_t m = 16; m < M && m <= split; m += 16) {
     const size_t b = gemm_dx_ws_bytes(m, N, K, 64);
     most = b > most ? b : most;

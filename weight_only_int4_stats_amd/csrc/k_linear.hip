@@ -288,6 +288,11 @@ hipError_t linear_launch(const LinearArgs& a, const LinearPlan& p, const Epilogu
 
 namespace awq {
 
+int64_t tile_split_rows(int64_t cols) {
+  const int64_t cus = device_cus() > 0 ? device_cus() : 256;
+  return awqk::tile_split_rows(cols, cus);
+}
+
 int64_t linear_threads(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0) return 0;
   const awqk::LinearPlan p = awqk::linear_plan(M, N, K);

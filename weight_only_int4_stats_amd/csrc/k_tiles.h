@@ -216,6 +216,12 @@ inline TilePlan tile_plan(const TileShape (&shapes)[NSHAPES], int64_t M, int64_t
   return best;
 }
 
+// Rows past which tile_plan splits nothing: two slices need fewer than 2 cus of
+// the tallest tiles.
+inline int64_t tile_split_rows(int64_t cols, int64_t cus) {
+  return 2 * cus * 256 / ((cols + kTileCols - 1) / kTileCols) + 256;
+}
+
 inline int64_t tile_blocks(int64_t items) { return kTileXcds * ((items + kTileXcds - 1) / kTileXcds); }
 
 }  // namespace awqk
