@@ -78,6 +78,50 @@ __device__ __forceinline__ void load8_any(const void* p, int dt, int64_t i, int 
     for (int j = 0; j < 8; ++j) v[j] = j < cnt ? load_any(p, dt, i + j) : 0.0f;
   }
 }
+// The same in two steps: eight values as they lie in memory (16-bit types: lo
+// alone), so that a load may be on its way while other work runs, and their
+// conversion.
+struct Raw8 {
+  u32x4 lo, hi;
+};
+__device__ __forceinline__ Raw8 raw8_load(const void* p, int dt, int64_t i, int cnt) {
+  Raw8 r{u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
+  if (cnt >= 8) {
+    if (dt == DT_F32) {
+      const u32x4a4* q = reinterpret_cast<const u32x4a4*>(reinterpret_cast<const float*>(p) + i);
+      r.lo = q[0];
+      r.hi = q[1];
+    } else {
+      r.lo = *reinterpret_cast<const u32x4a2*>(reinterpret_cast<const uint16_t*>(p) + i);
+    }
+  } else if (cnt > 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= cnt) continue;
+      if (dt == DT_F32) {
+        const uint32_t v = reinterpret_cast<const uint32_t*>(p)[i + j];
+        if (j < 4) r.lo[j] = v;
+        else r.hi[j - 4] = v;
+      } else {
+        r.lo[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i + j] << (16 * (j & 1));
+      }
+    }
+  }
+  return r;
+}
+__device__ __forceinline__ void raw8_floats(const Raw8& r, int dt, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t a = r.lo[j], b = r.hi[j];
+    if (dt == DT_F32) {
+      v[j] = __uint_as_float(a);
+      v[4 + j] = __uint_as_float(b);
+    } else {
+      v[2 * j] = dt == DT_F16 ? f16_to_f32(a & 0xFFFFu) : __uint_as_float(a << 16);
+      v[2 * j + 1] = dt == DT_F16 ? f16_to_f32(a >> 16) : __uint_as_float(a & 0xFFFF0000u);
+    }
+  }
+}
 __device__ __forceinline__ void store8_any(void* p, int dt, int64_t i, int cnt, const float (&v)[8]) {
   if (cnt >= 8) {
     if (dt == DT_F32) {

@@ -209,34 +209,52 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W,
     for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
   }
   const float inv_k = 1.0f / (float)a.K;
-  // the next row is on its way while this one's sums meet
-  float nx[KEEP][8], ng[KEEP][8], nmu = 0.0f, nr = 0.0f;
-  auto fetch = [&](int64_t m) {
+  // the next two rows are on their way, as they lie in memory, while this one's
+  // sums meet, so that a compute unit has some 48 KB in flight (8192 x 4096 from
+  // cold caches: 60 us a call with none, 55 with two); a lane with two chunks
+  // has no registers left for that
+  constexpr bool AHEAD = KEEP == 1;
+  constexpr int D = AHEAD ? 2 : 1;
+  Raw8 nx[D][KEEP], ng[D][KEEP];
+  float nmu[D], nr[D];
+  auto fetch = [&](int64_t m, int d) {
     const bool live = m < a.M;
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) {
       const int64_t c = (int64_t)(t + T * i) * 8;
-      load8_any(a.x, XDT, m * a.ldx + c, live ? cnt[i] : 0, nx[i]);
-      load8_any(a.dy, a.dyt, m * a.lddy + c, live ? cnt[i] : 0, ng[i]);
+      nx[d][i] = raw8_load(a.x, XDT, m * a.ldx + c, live ? cnt[i] : 0);
+      ng[d][i] = raw8_load(a.dy, a.dyt, m * a.lddy + c, live ? cnt[i] : 0);
     }
-    nmu = !RMS && live ? a.mean[m] : 0.0f;
-    nr = live ? a.rstd[m] : 0.0f;
+    nmu[d] = !RMS && live ? a.mean[m] : 0.0f;
+    nr[d] = live ? a.rstd[m] : 0.0f;
   };
   int turn = 0;
-  fetch((int64_t)blockIdx.x * RB + rg);
-  for (int64_t mb = (int64_t)blockIdx.x * RB; mb < a.M; mb += (int64_t)gridDim.x * RB) {
+  const int64_t step = (int64_t)gridDim.x * RB;
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch((int64_t)blockIdx.x * RB + rg + d * step, d);
+  }
+  for (int64_t mb = (int64_t)blockIdx.x * RB; mb < a.M; mb += step) {
     const int64_t m = mb + rg;
     const bool live = m < a.M;
+    if constexpr (!AHEAD) fetch(m, 0);
     float xh[KEEP][8], g[KEEP][8];
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i)
+    for (int i = 0; i < KEEP; ++i) {
+      raw8_floats(nx[0][i], XDT, xh[i]);
+      raw8_floats(ng[0][i], a.dyt, g[i]);
+    }
+    const float mu = nmu[0], r = nr[0];
+    if constexpr (AHEAD) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        xh[i][j] = nx[i][j];
-        g[i][j] = ng[i][j];
+      for (int i = 0; i < KEEP; ++i) {
+        nx[0][i] = nx[D - 1][i];
+        ng[0][i] = ng[D - 1][i];
       }
-    const float mu = nmu, r = nr;
-    fetch(m + (int64_t)gridDim.x * RB);
+      nmu[0] = nmu[D - 1];
+      nr[0] = nr[D - 1];
+      fetch(m + D * step, D - 1);
+    }
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
