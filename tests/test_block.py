@@ -1106,6 +1106,21 @@ def test_workspace_of_the_largest_batch_serves_all(N, K):
     assert awq.awq_workspace_bytes(E.AWQ_OP_BALANCE_LOSS, 1000, 0, 0, 1024) > 0
 
 
+@pytest.mark.parametrize("N,K", [(4096, 4096), (515, 512), (64, 8192), (2048, 16384), (11008, 256)])
+def test_the_workspace_asked_for_is_enough_for_every_smaller_batch(N, K):
+    # x and y overlap, which is refused after the workspace was found large enough
+    A, V = ctypes.c_void_p(1 << 32), ctypes.c_void_p(1 << 40)
+    for most in (64, 300, 5000):
+        need = {op: awq.awq_workspace_bytes(getattr(E, op), most, N, K) for op in ("AWQ_OP_LINEAR", "AWQ_OP_GEMM_DX")}
+        for M in [m for m in (1, 2, 7, 16, 17, 24, 32, 33, 48, 64, 65, 80, 100, 129, 256, 300, 519, 1000, 2048, 2500, 4097, 5000) if m <= most]:
+            for g in (64, 128, 256):
+                r = awq.lib().awq_w4a16_linear(A, 0, M, K, K, V, V, V, N, g, None, 0, 0, None, 0, None, 0, A, 0, N, V,
+                                               need["AWQ_OP_LINEAR"], None)
+                assert r == 5, ("linear", most, M, g)
+                r = awq.lib().awq_w4a16_gemm_dx(A, 0, M, N, N, V, V, V, K, g, A, 0, K, V, need["AWQ_OP_GEMM_DX"], None)
+                assert r == 5, ("dx", most, M, g)
+
+
 def test_binding_refuses_host_tensors_and_wrong_names():
     x = torch.zeros(2, 128, dtype=torch.float16)
     q = torch.zeros(8, 16, dtype=torch.int32), torch.zeros(8, 1, dtype=torch.float16), torch.zeros(8, 1, dtype=torch.uint8)

@@ -52,28 +52,6 @@ bool linear_sizes(int64_t M, int64_t N, int64_t K) {
 
 namespace awq {
 
-// The bytes for M rows serve every smaller M, whatever the group (which kernel
-// serves a shape depends on it).
-size_t linear_ws_bytes_upto(int64_t M, int64_t N, int64_t K) {
-  size_t most = 0;
-  auto upto = [&](int64_t m) {
-    for (int g = 64; g <= 256; g *= 2) {
-      const size_t b = K % g == 0 ? linear_ws_bytes(m, N, K, g) : 0;
-      most = b > most ? b : most;
-    }
-  };
-  upto(M);
-  for (int64_t m = 1; m < M && m <= 64; ++m) upto(m);
-  // above 64 tokens the group does not matter, and fewer rows may be split into
-  // more slices, the same for each 16 rows
-  const int64_t split = tile_split_rows(N);
-  for (int64_t m = 80; m < M && m <= split; m += 16) {
-    const size_t b = linear_ws_bytes(m, N, K, 64);
-    most = b > most ? b : most;
-  }
-  return most;
-}
-
 size_t block_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t T) {
   switch (op) {
     case AWQ_OP_LINEAR:

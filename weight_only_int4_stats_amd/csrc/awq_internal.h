@@ -172,7 +172,9 @@ size_t block_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t T);
 // The product with an epilogue (k_w4a16.hip chooses, k_linear.hip: the tiles)
 bool linear_mid(int64_t M, int64_t N, int64_t K);    // the 17 .. 64 token kernel serves this shape
 size_t linear_ws_bytes(int64_t M, int64_t N, int64_t K, int group);
+size_t linear_ws_bytes_upto(int64_t M, int64_t N, int64_t K);      // of any M' <= M, whatever the group
 size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K);
+size_t linear_partial_bytes_upto(int64_t M, int64_t N, int64_t K);
 int64_t linear_threads(int64_t M, int64_t N, int64_t K);   // of the largest of its launches
 hipError_t launch_linear(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                          const uint16_t* scales, const uint8_t* zeros, int64_t N, int group, void* y, int64_t ldy,
@@ -180,10 +182,6 @@ hipError_t launch_linear(const void* x, int xdt, int64_t M, int64_t K, int64_t l
 hipError_t launch_linear_tiles(const uint16_t* xq, const int* pm, const int* en, const uint32_t* ctab, const uint32_t* qw,
                                int64_t M, int64_t N, int64_t K, int group, float* partial, void* y, int64_t ldy,
                                const Epilogue& ep, hipStream_t st);
-
-// Rows up to which the tiles of k_tiles.h may split the contraction
-// (k_linear.hip).
-int64_t tile_split_rows(int64_t cols);
 
 // Column sums of partial rows (k_colsum.hip): columns [0, cols) to out0 and
 // [at1, at1 + cols) to out1 (either may be NULL); pitch a multiple of 64.

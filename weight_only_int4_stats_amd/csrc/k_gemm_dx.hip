@@ -421,17 +421,12 @@ size_t gemm_dx_ws_bytes(int64_t M, int64_t N, int64_t K, int group) {
   return dx_ws(nullptr, M, N, K, group, dx_plan(M, N, K).S).bytes;
 }
 
-// The most that any M' <= M needs: fewer rows may be split into more slices.
+// The most that any M' <= M may need: fewer rows may be split into more slices.
 size_t gemm_dx_ws_bytes_upto(int64_t M, int64_t N, int64_t K) {
   using namespace awqk;
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  size_t most = gemm_dx_ws_bytes(M, N, K, 64);
-  const int64_t split = tile_split_rows(K);
-  for (int64_t m = 16; m < M && m <= split; m += 16) {
-    const size_t b = gemm_dx_ws_bytes(m, N, K, 64);
-    most = b > most ? b : most;
-  }
-  return most;
+  const int64_t parts = tile_parts(kDxShapes, M, K, (N + kDxN - 1) / kDxN, device_cus() > 0 ? device_cus() : 256);
+  return dx_ws(nullptr, M, N, K, 64, 1).bytes + align_up((size_t)parts * K * 4, 256);
 }
 
 int64_t gemm_dx_threads(int64_t M, int64_t N, int64_t K) {

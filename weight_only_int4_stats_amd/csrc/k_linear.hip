@@ -288,11 +288,6 @@ hipError_t linear_launch(const LinearArgs& a, const LinearPlan& p, const Epilogu
 
 namespace awq {
 
-int64_t tile_split_rows(int64_t cols) {
-  const int64_t cus = device_cus() > 0 ? device_cus() : 256;
-  return awqk::tile_split_rows(cols, cus);
-}
-
 int64_t linear_threads(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0) return 0;
   const awqk::LinearPlan p = awqk::linear_plan(M, N, K);
@@ -303,6 +298,11 @@ int64_t linear_threads(int64_t M, int64_t N, int64_t K) {
 size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K) {
   const awqk::LinearPlan p = awqk::linear_plan(M, N, K);
   return p.t.S > 1 ? align_up((size_t)p.t.S * M * awqk::linear_pitch(N) * 4, 256) : 0;
+}
+
+size_t linear_partial_bytes_upto(int64_t M, int64_t N, int64_t K) {
+  const int64_t parts = awqk::tile_parts(awqk::kLinearShapes, M, N, K / awqk::kTileK, device_cus() > 0 ? device_cus() : 256);
+  return align_up((size_t)parts * awqk::linear_pitch(N) * 4, 256);
 }
 
 hipError_t launch_linear_tiles(const uint16_t* xq, const int* pm, const int* en, const uint32_t* ctab, const uint32_t* qw,

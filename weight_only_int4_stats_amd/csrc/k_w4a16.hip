@@ -1075,6 +1075,21 @@ size_t linear_ws_bytes(int64_t M, int64_t N, int64_t K, int group) {
   return awqk::gemm_ws(nullptr, M, N, K, group).bytes + linear_partial_bytes(M, N, K);
 }
 
+// The bytes for M rows serve every smaller M, whatever the group (which kernel
+// serves a shape depends on it).  Above 64 rows a bound, so that the query does
+// not try every number of rows (4 ms for a million).
+size_t linear_ws_bytes_upto(int64_t M, int64_t N, int64_t K) {
+  size_t most = 0;
+  for (int64_t m = 1; m <= (M < 64 ? M : 64); ++m)
+    for (int g = 64; g <= 256; g *= 2) {
+      const size_t b = K % g != 0 || (M > 64 && !linear_mid(m, N, K)) ? 0 : linear_ws_bytes(m, N, K, g);
+      most = b > most ? b : most;
+    }
+  if (M <= 64) return most;
+  const size_t b = awqk::gemm_ws(nullptr, M, N, K, 64).bytes + linear_partial_bytes_upto(M, N, K);
+  return b > most ? b : most;
+}
+
 hipError_t launch_linear(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                          const uint16_t* scales, const uint8_t* zeros, int64_t N, int group, void* y, int64_t ldy,
                          const Epilogue& ep, void* ws, hipStream_t st) {
