@@ -5,11 +5,11 @@
 //   a = dy w,  dx = r (a - mean a - xh mean(a xh))   (RMS: without mean a)
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 // Both are bound by memory (8192 x 4096: 32 us forward from 32 to 16 bits, 6.3
-// TB/s; 43 + 5 us backward in bf16, 4.7 TB/s in the first): a row is read once and stays in registers (the
-// variance is that of the centred values, so a large mean costs nothing), and
-// the backward pass adds up dw and db in registers over all the rows a block
-// takes, leaves one partial row per block and adds those in a second launch
-// (k_col_reduce), in a fixed order.
+// TB/s; 37 + 5 us backward in bf16, 5.5 TB/s in the first): a row is read once
+// and stays in registers (the variance is that of the centred values, so a large
+// mean costs nothing), and the backward pass adds up dw and db in registers over
+// all the rows a block takes, leaves one partial row per block and adds those in
+// a second launch (k_col_reduce), in a fixed order.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_epilogue.h"
@@ -192,7 +192,9 @@ __device__ __forceinline__ void waves_sum(float (&v)[2], float (*red)[16][2], in
 // RB row groups of W waves each (W RB <= 16), KEEP chunks of eight values per
 // lane.  Block b takes the rows b RB + i, (b + grid) RB + i, ...; W is just
 // enough for a row, so that a width of 5120 leaves no lane idle.
-template <int XDT, int KEEP, bool RMS>
+// (dy's type is known at compile time: with loads of either kind the rows on
+// their way went through scratch memory, 45 us instead of 37 at 8192 x 4096.)
+template <int XDT, int DYT, int KEEP, bool RMS>
 __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W, int RB) {
   __shared__ float red[2][16][2];
   extern __shared__ float meet[];                                // [RB - 1][KEEP 8][T], for the row groups to meet
@@ -209,12 +211,12 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W,
     for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
   }
   const float inv_k = 1.0f / (float)a.K;
-  // the next two rows are on their way, as they lie in memory, while this one's
-  // sums meet, so that a compute unit has some 48 KB in flight (8192 x 4096 from
-  // cold caches: 60 us a call with none, 55 with two); a lane with two chunks
-  // has no registers left for that
+  // the next two rows (one of 32-bit values) are on their way, as they lie in
+  // memory, while this one's sums meet, so that a compute unit has some 48 KB in
+  // flight (8192 x 4096 from cold caches: 60 us a call with none, 55 with two); a
+  // lane with two chunks has no registers left for that
   constexpr bool AHEAD = KEEP == 1;
-  constexpr int D = AHEAD ? 2 : 1;
+  constexpr int D = AHEAD && XDT != DT_F32 && DYT != DT_F32 ? 2 : 1;
   Raw8 nx[D][KEEP], ng[D][KEEP];
   float nmu[D], nr[D];
   auto fetch = [&](int64_t m, int d) {
@@ -223,7 +225,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W,
     for (int i = 0; i < KEEP; ++i) {
       const int64_t c = (int64_t)(t + T * i) * 8;
       nx[d][i] = raw8_load(a.x, XDT, m * a.ldx + c, live ? cnt[i] : 0);
-      ng[d][i] = raw8_load(a.dy, a.dyt, m * a.lddy + c, live ? cnt[i] : 0);
+      ng[d][i] = raw8_load(a.dy, DYT, m * a.lddy + c, live ? cnt[i] : 0);
     }
     nmu[d] = !RMS && live ? a.mean[m] : 0.0f;
     nr[d] = live ? a.rstd[m] : 0.0f;
@@ -242,7 +244,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W,
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) {
       raw8_floats(nx[0][i], XDT, xh[i]);
-      raw8_floats(ng[0][i], a.dyt, g[i]);
+      raw8_floats(ng[0][i], DYT, g[i]);
     }
     const float mu = nmu[0], r = nr[0];
     if constexpr (AHEAD) {
@@ -431,8 +433,17 @@ hipError_t norm_grad_dispatch(const NormGradArgs& a, hipStream_t st) {
   }
   const dim3 block((unsigned)(64 * p.waves * p.groups));
   const size_t lds = a.dw || a.db ? (size_t)(p.groups - 1) * 64 * p.waves * p.keep * 8 * 4 : 0;
-  if (p.keep == 1) hipLaunchKernelGGL((k_norm_grad<XDT, 1, RMS>), grid, block, lds, st, a, p.waves, p.groups);
-  else hipLaunchKernelGGL((k_norm_grad<XDT, 2, RMS>), grid, block, lds, st, a, p.waves, p.groups);
+#define AWQ_NG(DYT)                                                                                                  \
+  if (p.keep == 1) hipLaunchKernelGGL((k_norm_grad<XDT, DYT, 1, RMS>), grid, block, lds, st, a, p.waves, p.groups); \
+  else hipLaunchKernelGGL((k_norm_grad<XDT, DYT, 2, RMS>), grid, block, lds, st, a, p.waves, p.groups)
+  if (a.dyt == DT_F16) {
+    AWQ_NG(DT_F16);
+  } else if (a.dyt == DT_BF16) {
+    AWQ_NG(DT_BF16);
+  } else {
+    AWQ_NG(DT_F32);
+  }
+#undef AWQ_NG
   return hipGetLastError();
 }
 

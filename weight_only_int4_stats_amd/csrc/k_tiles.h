@@ -3,10 +3,12 @@
 // block of 4 WM waves (WM along the rows x 4 along the columns, each 16 MB x
 // 64), 64 of the contraction per stage, NS stages in LDS.
 //
-//  * Every stage arrives by LDS DMA, NS stages ahead: few rows leave a block
-//    little to do per stage, and what covers the memory's latency is the number
-//    of stages on their way (MB = 2, 172 blocks of 16 stages: 19.5 us with three
-//    in LDS, two on their way).
+//  * Every stage arrives by LDS DMA, NS stages ahead: as many as LDS holds (with
+//    two blocks per compute unit for the small tiles), since few rows leave a
+//    block little to do per stage.  Three cover the memory's latency already;
+//    five and six measured the same.  The small tiles are bound by the
+//    dequantization (0.5 to 0.8 us a stage, of which the products take 0.06 to
+//    0.24), the tall ones by the matrix pipe and the reads that feed it (1.8 us).
 //  * One barrier per stage, ahead of its last sub-step's products: by then
 //    every wave has read the stage's last operands into registers, so its slot
 //    takes the copies of stage s + NS, and the next stage's first operands are
