@@ -718,6 +718,19 @@ def test_balance_even_routing_and_empty(on_gpu):
     assert awq.awq_balance_loss_backward(logits[:0], slope).shape == (0, 8)
 
 
+@pytest.mark.parametrize("experts", [1, 3, 5, 6, 7, 11, 29, 60, 64])
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_balance_of_experts_that_serve_alike_has_no_gradient(on_gpu, score, dt, experts):
+    """Every token names every expert: the slopes are equal, and the gradient is 0 to the last bit."""
+    rng = np.random.default_rng(experts)
+    l = gpu(torch.from_numpy(1.5 * rng.standard_normal((333, experts))).to(DTYPES[dt]))
+    ids = gpu(torch.arange(experts, dtype=torch.int32).repeat(333, 1))
+    loss, counts, slope = awq.awq_balance_loss(l, ids, coef=0.01, score=score)
+    assert torch.all(counts == 333) and torch.all(slope == slope[0]) and abs(loss.item() - 0.01) <= 0.01 * (experts + 16) * U
+    assert torch.all(awq.awq_balance_loss_backward(l, slope, score=score) == 0)
+
+
 @pytest.mark.gpu
 def test_balance_strides_and_in_place(on_gpu):
     for dtype in DTYPES.values():

@@ -386,9 +386,10 @@ __global__ __launch_bounds__(64 * kBalGradWaves) void k_balance_grad(const Balan
   };
   if (t < a.T) fetch(t);
   // the slopes about their mean, which the gradient does not see: what is left
-  // cancels little in slope - sum p slope
+  // cancels little in slope - sum p slope.  In double, where the sum is exact and
+  // equal slopes leave 0, as their gradient is.
   float d[N];
-  float mean = 0.0f;
+  double mean = 0.0;
 #pragma unroll
   for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -400,9 +401,9 @@ __global__ __launch_bounds__(64 * kBalGradWaves) void k_balance_grad(const Balan
   const float go = a.go ? a.go[0] : 1.0f;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) mean += __shfl_xor(mean, off);
-  mean /= (float)a.E;
+  mean /= (double)a.E;
 #pragma unroll
-  for (int i = 0; i < N; ++i) d[i] -= mean;
+  for (int i = 0; i < N; ++i) d[i] = (float)((double)d[i] - mean);
   for (; t < a.T; t += step) {
     float s[N], rest[N];
 #pragma unroll
