@@ -495,7 +495,7 @@ def sum_rows(M, K):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("rms", [False, True])
-@pytest.mark.parametrize("xdt,dyt", [("f16", "f16"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("xdt,dyt", [(a, b) for a in DTYPES for b in DTYPES])
 @pytest.mark.parametrize("shape", NORMS + [(2050, 40), (1100, 700), (600, 16400), (8, 5000), (9, 5000), (128, 300), (129, 300)], ids=lambda s: "x".join(map(str, s)))
 def test_layer_norm_backward(on_gpu, shape, xdt, dyt, rms):
     M, K = shape
@@ -718,6 +718,7 @@ def test_balance_even_routing_and_empty(on_gpu):
     assert awq.awq_balance_loss_backward(logits[:0], slope).shape == (0, 8)
 
 
+@pytest.mark.gpu
 @pytest.mark.parametrize("experts", [1, 3, 5, 6, 7, 11, 29, 60, 64])
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])

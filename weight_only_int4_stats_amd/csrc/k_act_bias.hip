@@ -4,8 +4,9 @@
 // access of 16-bit values each), the block's four waves every fourth row of its
 // chunk of rows; the sums stay in registers, meet in LDS and leave the block
 // as one partial row, which k_col_reduce adds.  The sum takes the fp32 values
-// before their rounding to dz's type.  2048 x 11008 with gelu: 33 us, 4.1 TB/s
-// (54 us with the device library's erfcf and expf, which bound it then).
+// before their rounding to dz's type.  2048 x 11008 with gelu: 32 us, 4.2 TB/s
+// (33 with the activation chosen per value, 54 with the device library's erfcf
+// and expf: bound by the vector instructions as much as by memory).
 #include "k_epilogue.h"
 
 namespace awqk {
@@ -29,8 +30,9 @@ __global__ __launch_bounds__(256) void k_act_bias(const void* __restrict__ dy, i
       if (pre) {
         float z[8];
         load8_any(pre, DT, m * ldp + n, cnt, z);
+        act_slopes(act, z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] *= act_slope(act, z[j]);
+        for (int j = 0; j < 8; ++j) g[j] *= z[j];
         store8_any(dz, DT, m * lddz + n, cnt, g);
       }
 #pragma unroll

@@ -235,6 +235,19 @@ __device__ __forceinline__ float act_slope(int act, float z) {
   return __builtin_fmaf(z * du, s * t, s);
 }
 
+// act' of eight values, the choice made once: their chains of dependent
+// instructions run side by side.
+__device__ __forceinline__ void act_slopes(int act, float (&z)[8]) {
+  auto all = [&](auto kind) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = act_slope(decltype(kind)::value, z[j]);
+  };
+  if (act == awq::LINEAR_RELU) all(std::integral_constant<int, awq::LINEAR_RELU>{});
+  else if (act == awq::LINEAR_GELU) all(std::integral_constant<int, awq::LINEAR_GELU>{});
+  else if (act == awq::LINEAR_GELU_TANH) all(std::integral_constant<int, awq::LINEAR_GELU_TANH>{});
+  else all(std::integral_constant<int, awq::LINEAR_SILU>{});
+}
+
 // One output (row m, column n) in two steps: what it needs from memory, asked
 // for ahead of the work that ends in its sum (a load behind an earlier output's
 // store would wait for it: the batch-1 product of 4096 -> 11008 takes 7.9 us,
