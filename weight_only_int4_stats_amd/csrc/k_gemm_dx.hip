@@ -21,6 +21,10 @@
 //      product of two exact fp16 values, rounded once.
 //   4. k_dx_reduce where the contraction is split: the slices' fp32 sums added
 //      in their order.
+// 2048 rows, 11008 -> 4096, bf16: 5 + 17 + 226 to 244 us (0.8 PFLOP/s), bound by
+// the matrix pipe and the dequantization beside it.  37 rows, 4096 -> 11008,
+// fp16: 5.3 + 3.1 + 22 + 4.1 us against 4.5 for the packed words alone: a stage
+// costs 0.8 us whatever is in its rows, which is the dequantization.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_epilogue.h"

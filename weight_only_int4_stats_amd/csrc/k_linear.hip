@@ -9,6 +9,11 @@
 //      epilogue, with them they go to the workspace as fp32.
 //   3. k_linear_reduce (slices): the slices' sums added in their order, then the
 //      epilogue.
+// 2048 tokens, 4096 -> 11008, bf16 with bias, gelu and pre: 10 + 234 to 249 us
+// in a row of calls (0.75 PFLOP/s), 224 in all with the caches flushed between
+// calls (0.83); bound by the matrix pipe and the dequantization beside it; the
+// plain product, which rounds twice and stores one output, 182 to 198.  519 tokens, 4096 -> 1027, fp16 with bias and silu: 5.5 +
+// 23 + 6.4 us, bound by the dequantization and by what surrounds the stages.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_epilogue.h"

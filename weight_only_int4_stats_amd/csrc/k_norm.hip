@@ -407,7 +407,8 @@ inline NormGradPlan norm_grad_plan(int64_t M, int64_t K) {
   // one block per compute unit, with as many rows each as make the whole, and
   // at least four: a block's partial sums cost as much as a row or two (519 x
   // 5120: 10 us with four rows a block, 11 with three, 14 with two and two
-  // blocks per unit; 8192 x 4096: 43 us with one block per unit, 49 with two).
+  // blocks per unit; 8192 x 4096 before rows came ahead: 43 us with one block per
+  // unit, 49 with two).
   // Up to eight make one block, whose sums are whole: no second launch.
   const int64_t sets = (M + p.groups - 1) / p.groups;
   int64_t each = (sets + cus - 1) / cus;
