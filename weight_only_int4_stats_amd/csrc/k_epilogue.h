@@ -354,6 +354,19 @@ __device__ __forceinline__ u32x4 once_dequant(uint32_t w, uint32_t mult, uint32_
                __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w8 & 0x00F000F0u), c11, n) * d)};
 }
 
+// What the rounding of once_dequant's products left, exact in fp16 (but for
+// steps 2^8 below the row's largest, whose last bits are lost).
+__device__ __forceinline__ u32x4 once_rest(uint32_t w, uint32_t mult, uint32_t nz, const u32x4& it) {
+  const f16x2 c15 = as_f16x2(0x78007800u), c11 = as_f16x2(0x68006800u);
+  const f16x2 n = as_f16x2(nz), d = as_f16x2(mult);
+  const uint32_t w8 = w >> 8;
+  auto left = [&](uint32_t v, f16x2 c, uint32_t hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_elementwise_fma(as_f16x2(v), c, n), d, -as_f16x2(hi)));
+  };
+  return u32x4{left(w & 0x000F000Fu, c15, it[0]), left(w8 & 0x000F000Fu, c15, it[1]), left(w & 0x00F000F0u, c11, it[2]),
+               left(w8 & 0x00F000F0u, c11, it[3])};
+}
+
 // A step's size for the row's power of two: under an epilogue of any sign, and
 // 0 where it is not finite, so that it takes nothing from the row's others.
 template <bool ONCE>

@@ -289,6 +289,17 @@ struct DxOp {
     }
     return o;
   }
+  __device__ __forceinline__ u32x4 rest(int st, int c, const u32x4& it) const {
+    const f16x2 scale = as_f16x2(c & 1 ? 0x68006800u : 0x78007800u);
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t v = (c & 2 ? p8[j] : p[j]) & (c & 1 ? 0x00F000F0u : 0x000F000Fu);
+      o[j] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_elementwise_fma(as_f16x2(v), scale, as_f16x2(cz[st][j])),
+                                                                    as_f16x2(cm[st][j]), -as_f16x2(it[j])));
+    }
+    return o;
+  }
 };
 
 // Stages in LDS: what 160 KB hold with one block per compute unit for tall

@@ -87,6 +87,9 @@ struct LinearOp {
     const uint32_t m = c[i >> 1][2 * (i & 1)], z = c[i >> 1][2 * (i & 1) + 1];
     return once_dequant(st ? w[i].y : w[i].x, m, z);
   }
+  __device__ __forceinline__ u32x4 rest(int st, int i, const u32x4& it) const {
+    return once_rest(st ? w[i].y : w[i].x, c[i >> 1][2 * (i & 1)], c[i >> 1][2 * (i & 1) + 1], it);
+  }
 };
 
 template <int MB, int WM>

@@ -51,7 +51,13 @@ __device__ __forceinline__ bool tile_item(int64_t block, int64_t mtiles, int64_t
 // OP, the packed operand: bytes of its part of a stage (OP::Bytes), the copies
 // of this wave (op.copies, BW or one more), issue(s, lds, live), load(lds): a stage's
 // words and constants into registers, begin(st) and column(st, c): the operand
-// of column block c for k32 step st; chunk(st, b4): the A chunk that goes with it.
+// of column block c for k32 step st, rounded to fp16, and rest(st, c, it): what the
+// rounding left; chunk(st, b4): the A chunk that goes with it.
+//
+// Tiles of 16 rows multiply by the rest too (Whole): the dequantization bounds
+// them and leaves the matrix pipe room, and in the few outputs of a small batch
+// one rounding of the weights may chance to be most of the error (1.8 times the
+// plain form's over a few hundred fp16 outputs).
 template <int MB, int WM, int NS, class OP>
 struct Tile {
   static constexpr int Waves = 4 * WM;
@@ -65,6 +71,7 @@ struct Tile {
   static constexpr int H = MB > 4 ? 2 : 1;              // sub-steps per k32 step
   static constexpr int MH = MB / H;                     // 16-row blocks per sub-step
   static constexpr int BW = 8 / Waves;                  // copies of packed words per wave
+  static constexpr bool Whole = MB == 1;
   static_assert((NS - 1) * (AW + BW + 1) <= 63, "copies in flight");
 
   // rows of xq from row m0 on (pitch Kp, a multiple of 64), stages [s0, s1)
@@ -118,12 +125,15 @@ struct Tile {
     for (int j = 0; j < NS; ++j) issue(s0 + j, j);
     wait(std::integral_constant<int, NS - 1>{});
     lds_barrier();
-    u32x4 bq[4];
+    u32x4 bq[4], bl[Whole ? 4 : 1];
     load_a(lds, 0, a0);
     op.load(lds + A);
     op.begin(0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) bq[c] = op.column(0, c);
+    for (int c = 0; c < 4; ++c) {
+      bq[c] = op.column(0, c);
+      if constexpr (Whole) bl[c] = op.rest(0, c, bq[c]);
+    }
     uint32_t slot = 0;
     for (int64_t s = s0; s < s1; ++s) {
       const uint32_t nslot = slot + 1 == NS ? 0 : slot + 1;
@@ -151,10 +161,12 @@ struct Tile {
           for (int i = 0; i < MH; ++i) {
             const int b = (q % H) * MH + i;
             acc[b][c] = mfma16h(ac[i], bq[c], acc[b][c]);
+            if constexpr (Whole) acc[b][c] = mfma16h(ac[i], bl[c], acc[b][c]);
           }
           if (turn) {
             if (c == 0) op.begin(st ^ 1);
             bq[c] = op.column(st ^ 1, c);
+            if constexpr (Whole) bl[c] = op.rest(st ^ 1, c, bq[c]);
           }
         }
         if (turn && MH >= 4) {
