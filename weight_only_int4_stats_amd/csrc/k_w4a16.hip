@@ -1038,7 +1038,7 @@ hipError_t w4a16_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, 
 // awq_w4a16_linear: the memory-bound kernels with the epilogue where they
 // serve the shape, else the tiles of k_linear.hip behind the same pre-pass.  One
 // token, 4096 -> 11008 with bias and gelu_tanh: 7.9 us (3.0 TB/s; 6.7 without);
-// 24 tokens, 11008 -> 4096 with a residual: 4 + 22 + 4 us.
+// 24 tokens, 11008 -> 4096 with a residual: 4 + 23 + 4 us.
 template <int DT>
 hipError_t linear_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                            const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog, void* y, int64_t ldy,
