@@ -342,29 +342,44 @@ __device__ __forceinline__ uint32_t once_zero(uint32_t z) {
   return f32_to_f16_bits(-(float)z * 0x1p-9f) * 0x10001u;
 }
 
-// One packed word -> 8 operands in the order (0,4 | 2,6 | 1,5 | 3,7), each
-// times the two fp16 values of `mult`.
-__device__ __forceinline__ u32x4 once_dequant(uint32_t w, uint32_t mult, uint32_t nz) {
-  const f16x2 c15 = as_f16x2(0x78007800u), c11 = as_f16x2(0x68006800u);   // 2^15, 2^11
-  const f16x2 n = as_f16x2(nz), d = as_f16x2(mult);
-  const uint32_t w8 = w >> 8;
-  return u32x4{__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w & 0x000F000Fu), c15, n) * d),
-               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w8 & 0x000F000Fu), c15, n) * d),
-               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w & 0x00F000F0u), c11, n) * d),
-               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w8 & 0x00F000F0u), c11, n) * d)};
+// step 2^e as fp16; 0 has no sign.
+__device__ __forceinline__ uint32_t once_step(float d) {
+  const uint32_t b = f32_to_f16_bits(d);
+  return b & 0x7FFFu ? b : 0u;
 }
 
-// What the rounding of once_dequant's products left, exact in fp16 (but for
-// steps 2^8 below the row's largest, whose last bits are lost).
-__device__ __forceinline__ u32x4 once_rest(uint32_t w, uint32_t mult, uint32_t nz, const u32x4& it) {
-  const f16x2 c15 = as_f16x2(0x78007800u), c11 = as_f16x2(0x68006800u);
-  const f16x2 n = as_f16x2(nz), d = as_f16x2(mult);
+// Two of them as hi + lo, exactly: hi has the upper 7 bits of one unit less, so
+// that lo has at most 5 and neither is 0 or of the other sign.  (Times a code's
+// 4 bits both stay exact.  With a rest of 0 or of the other sign, an infinity
+// that meets both would end as 0 inf or inf - inf, where the weight's product
+// with it is an infinity.)  A step below 2^-19 of the row's largest loses its last bits.
+__device__ __forceinline__ void once_parts(uint32_t d, uint32_t& hi, uint32_t& lo) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  const u16x2 less = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, d), u16x2{1, 1});
+  hi = __builtin_bit_cast(uint32_t, less) & 0xFFF0FFF0u;
+  lo = __builtin_bit_cast(uint32_t, as_f16x2(d) - as_f16x2(hi));
+}
+
+// The codes (q - z) 2^-9 of one packed word, in the order (0,4 | 2,6 | 1,5 | 3,7).
+__device__ __forceinline__ u32x4 once_codes(uint32_t w, uint32_t nz) {
+  const f16x2 c15 = as_f16x2(0x78007800u), c11 = as_f16x2(0x68006800u);   // 2^15, 2^11
+  const f16x2 n = as_f16x2(nz);
   const uint32_t w8 = w >> 8;
-  auto left = [&](uint32_t v, f16x2 c, uint32_t hi) {
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_elementwise_fma(as_f16x2(v), c, n), d, -as_f16x2(hi)));
-  };
-  return u32x4{left(w & 0x000F000Fu, c15, it[0]), left(w8 & 0x000F000Fu, c15, it[1]), left(w & 0x00F000F0u, c11, it[2]),
-               left(w8 & 0x00F000F0u, c11, it[3])};
+  return u32x4{__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w & 0x000F000Fu), c15, n)),
+               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w8 & 0x000F000Fu), c15, n)),
+               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w & 0x00F000F0u), c11, n)),
+               __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(w8 & 0x00F000F0u), c11, n))};
+}
+
+// Pairs of fp16 values times the two of `mult`.
+__device__ __forceinline__ u32x4 once_times(const u32x4& c, uint32_t mult) {
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t v = c[j];
+    o[j] = __builtin_bit_cast(uint32_t, as_f16x2(v) * as_f16x2(mult));
+  }
+  return o;
 }
 
 // A step's size for the row's power of two: under an epilogue of any sign, and

@@ -111,7 +111,7 @@ __global__ __launch_bounds__(256) void k_dx_consts(const uint16_t* __restrict__ 
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (r + j >= rows) continue;
-        const uint32_t h = w & 4 ? once_zero(zl[r + j][g]) & 0xFFFFu : f32_to_f16_bits(ldexpf(f16_to_f32(sl[r + j][g]), es[r + j]));
+        const uint32_t h = w & 4 ? once_zero(zl[r + j][g]) & 0xFFFFu : once_step(ldexpf(f16_to_f32(sl[r + j][g]), es[r + j]));
         v |= h << (16 * j);
       }
       reinterpret_cast<uint32_t*>(ctab)[(g0 + g) * Np + n0 + w] = v;
@@ -223,7 +223,7 @@ struct DxOp {
   uint32_t boff[BW], coff, wlane, clane, sel;
   uint32_t w[2][8];                       // the stage's words and constants
   u32x4 cm[2], cz[2];
-  uint32_t p[4], p8[4];
+  uint32_t p[4], p8[4], mh[4], ml[4];
 
   __device__ __forceinline__ void init(const uint32_t* words, int64_t n, int64_t K, int64_t k0, const uint16_t* ctab,
                                        int64_t Np, int glog) {
@@ -271,34 +271,27 @@ struct DxOp {
     }
   }
   // the lane's halves of rows n and n + 1 side by side
+  template <bool WHOLE>
   __device__ __forceinline__ void begin(int st) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       p[j] = __builtin_amdgcn_perm(w[st][2 * j + 1], w[st][2 * j], sel);
       p8[j] = p[j] >> 8;
+      const uint32_t d = cm[st][j];
+      if constexpr (WHOLE) once_parts(d, mh[j], ml[j]);
+      else mh[j] = d;
     }
   }
-  __device__ __forceinline__ u32x4 column(int st, int c) const {
+  template <bool WHOLE>
+  __device__ __forceinline__ void column(int st, int c, u32x4& hi, u32x4& lo) const {
     const f16x2 scale = as_f16x2(c & 1 ? 0x68006800u : 0x78007800u);       // 2^11, 2^15
-    u32x4 o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t v = (c & 2 ? p8[j] : p[j]) & (c & 1 ? 0x00F000F0u : 0x000F000Fu);
-      const uint32_t d = cm[st][j], z = cz[st][j];
-      o[j] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(as_f16x2(v), scale, as_f16x2(z)) * as_f16x2(d));
+      const uint32_t v = (c & 2 ? p8[j] : p[j]) & (c & 1 ? 0x00F000F0u : 0x000F000Fu), z = cz[st][j];
+      const f16x2 code = __builtin_elementwise_fma(as_f16x2(v), scale, as_f16x2(z));
+      hi[j] = __builtin_bit_cast(uint32_t, code * as_f16x2(mh[j]));
+      if constexpr (WHOLE) lo[j] = __builtin_bit_cast(uint32_t, code * as_f16x2(ml[j]));
     }
-    return o;
-  }
-  __device__ __forceinline__ u32x4 rest(int st, int c, const u32x4& it) const {
-    const f16x2 scale = as_f16x2(c & 1 ? 0x68006800u : 0x78007800u);
-    u32x4 o;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t v = (c & 2 ? p8[j] : p[j]) & (c & 1 ? 0x00F000F0u : 0x000F000Fu);
-      o[j] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_elementwise_fma(as_f16x2(v), scale, as_f16x2(cz[st][j])),
-                                                                    as_f16x2(cm[st][j]), -as_f16x2(it[j])));
-    }
-    return o;
   }
 };
 

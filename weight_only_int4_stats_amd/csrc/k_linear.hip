@@ -82,13 +82,20 @@ struct LinearOp {
     c[0] = *reinterpret_cast<const u32x4*>(base + clane);
     c[1] = *reinterpret_cast<const u32x4*>(base + clane + 16);
   }
+  template <bool WHOLE>
   __device__ __forceinline__ void begin(int) {}
-  __device__ __forceinline__ u32x4 column(int st, int i) const {
+  template <bool WHOLE>
+  __device__ __forceinline__ void column(int st, int i, u32x4& hi, u32x4& lo) const {
     const uint32_t m = c[i >> 1][2 * (i & 1)], z = c[i >> 1][2 * (i & 1) + 1];
-    return once_dequant(st ? w[i].y : w[i].x, m, z);
-  }
-  __device__ __forceinline__ u32x4 rest(int st, int i, const u32x4& it) const {
-    return once_rest(st ? w[i].y : w[i].x, c[i >> 1][2 * (i & 1)], c[i >> 1][2 * (i & 1) + 1], it);
+    const u32x4 codes = once_codes(st ? w[i].y : w[i].x, z);
+    if constexpr (WHOLE) {
+      uint32_t mh, ml;
+      once_parts(m, mh, ml);
+      hi = once_times(codes, mh);
+      lo = once_times(codes, ml);
+    } else {
+      hi = once_times(codes, m);
+    }
   }
 };
 

@@ -197,14 +197,17 @@ __global__ __launch_bounds__(64 * kMidWaves) void k_gemm_mid(
           const float D = ldexpf(f16_to_f32(sr[d][t]), e[t]);
           u32x4 a[4];
           if constexpr (ONCE) {
-            const uint32_t mult = f32_to_f16_bits(D) * 0x10001u, nz = once_zero(zr[d][t]);
+            // two exact parts; one, rounded, for a bf16 output, which would not show the
+            // rounding (24 tokens, 11008 -> 4096: 1.5 us of 31)
+            uint32_t mult = once_step(D) * 0x10001u, rest;
+            const uint32_t nz = once_zero(zr[d][t]);
+            if (ep.ydt != DT_BF16) once_parts(mult, mult, rest);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              a[i] = once_dequant(wa[d][t][i], mult, nz);
-              // and what its rounding left, which a bf16 output would not show (24
-              // tokens, 11008 -> 4096: 1.5 us of 31)
+              const u32x4 codes = once_codes(wa[d][t][i], nz);
+              a[i] = once_times(codes, mult);
               if (ep.ydt == DT_BF16) continue;
-              const u32x4 left = once_rest(wa[d][t][i], mult, nz, a[i]);
+              const u32x4 left = once_times(codes, rest);
 #pragma unroll
               for (int g = 0; g < TG; ++g) acc[t][g] = mfma16h(left, xa[d][g][i], acc[t][g]);
             }

@@ -50,14 +50,12 @@ __device__ __forceinline__ bool tile_item(int64_t block, int64_t mtiles, int64_t
 
 // OP, the packed operand: bytes of its part of a stage (OP::Bytes), the copies
 // of this wave (op.copies, BW or one more), issue(s, lds, live), load(lds): a stage's
-// words and constants into registers, begin(st) and column(st, c): the operand
-// of column block c for k32 step st, rounded to fp16, and rest(st, c, it): what the
-// rounding left; chunk(st, b4): the A chunk that goes with it.
+// words and constants into registers, begin<Whole>(st) and column<Whole>(st, c, hi,
+// lo): the operand of column block c for k32 step st, rounded to fp16 in hi or
+// (Whole) as two exact parts; chunk(st, b4): the A chunk that goes with it.
 //
-// Tiles of 16 rows multiply by the rest too (Whole): the dequantization bounds
-// them and leaves the matrix pipe room, and in the few outputs of a small batch
-// one rounding of the weights may chance to be most of the error (1.8 times the
-// plain form's over a few hundred fp16 outputs).
+// Tiles of 16 rows multiply by both parts (Whole): the dequantization bounds
+// them and leaves the matrix pipe room.
 template <int MB, int WM, int NS, class OP>
 struct Tile {
   static constexpr int Waves = 4 * WM;
@@ -128,12 +126,9 @@ struct Tile {
     u32x4 bq[4], bl[Whole ? 4 : 1];
     load_a(lds, 0, a0);
     op.load(lds + A);
-    op.begin(0);
+    op.template begin<Whole>(0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      bq[c] = op.column(0, c);
-      if constexpr (Whole) bl[c] = op.rest(0, c, bq[c]);
-    }
+    for (int c = 0; c < 4; ++c) op.template column<Whole>(0, c, bq[c], bl[Whole ? c : 0]);
     uint32_t slot = 0;
     for (int64_t s = s0; s < s1; ++s) {
       const uint32_t nslot = slot + 1 == NS ? 0 : slot + 1;
@@ -164,9 +159,8 @@ struct Tile {
             if constexpr (Whole) acc[b][c] = mfma16h(ac[i], bl[c], acc[b][c]);
           }
           if (turn) {
-            if (c == 0) op.begin(st ^ 1);
-            bq[c] = op.column(st ^ 1, c);
-            if constexpr (Whole) bl[c] = op.rest(st ^ 1, c, bq[c]);
+            if (c == 0) op.template begin<Whole>(st ^ 1);
+            op.template column<Whole>(st ^ 1, c, bq[c], bl[Whole ? c : 0]);
           }
         }
         if (turn && MH >= 4) {

@@ -72,7 +72,7 @@ __device__ __forceinline__ void gemm_consts_block(int64_t bid, const uint16_t* _
   for (int64_t g = g0; g < g1; ++g) {
     const float D = ldexpf(f16_to_f32(sr[g]), e);   // exact: power-of-two scaling
     if constexpr (ONCE) {
-      *reinterpret_cast<uint2*>(ctab + (g * N + n) * 2) = make_uint2(f32_to_f16_bits(D) * 0x10001u, once_zero(zr[g]));
+      *reinterpret_cast<uint2*>(ctab + (g * N + n) * 2) = make_uint2(once_step(D) * 0x10001u, once_zero(zr[g]));
       continue;
     }
     const uint32_t h24 = f32_to_f16_bits(D * 16777216.0f);
