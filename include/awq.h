@@ -578,8 +578,9 @@ awq_status awq_bias_act_backward(const void* dy, awq_dtype dt, int64_t M, int64_
  *   dx[m][k] = sum_n dz[m][n] step[n][k/g] (q[n][k] - z[n][k/g])
  * dz enters as fp16 under an exact power of two per row of dz and per row of
  * the weights (values below 2^-28 of the largest of a row of dz, each times its
- * weights' power, lose bits), the dequantized weights are rounded once to fp16,
- * the sum is held in fp32 and dx rounded once.
+ * weights' power, lose bits), the dequantized weights keep all their bits (two
+ * fp16 values each; steps below 2^-19 of their row's largest lose bits), the sum is held in fp32 and dx rounded once.  An infinite or
+ * NaN dz gives what its products are.
  *
  *   dz        [M][lddz] fp16 or bf16 (dzt)
  *   qweight, scales, zeros  as written by awq_quantize_pack (steps of any sign)

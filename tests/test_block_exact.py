@@ -37,3 +37,58 @@ def test_gemm_dx_of_infinite_gradients(on_gpu, M, N, K, dt):
     keep = np.isfinite(ref)
     slack = product_slack(np.concatenate([fin, fin]), w, None)[:M]
     check(torch.from_numpy(np.where(keep, got, 0.0)), np.where(keep, ref, 0.0), slack, torch.float32)
+
+
+# ---- weights of all their bits --------------------------------------------------------
+# Steps m 2^-20 with m odd in 1025 .. 2047 (the 11 bits of an fp16 value), codes less their zero points up to 15 in
+# size, and rows of 60 whole numbers up to 8 in size, the rest 0: every product is a whole number of 2^-20, and any sum of
+# a row's is below 60 * 8 * 15 * 2047 < 2^24 of them, so fp32 holds each partial sum exactly in any order, and the result
+# is the exact one, rounded once to the output's type.  Weights rounded to 11 bits miss most of them.
+
+
+def whole_weights(N, K, g, seed):
+    gen = torch.Generator().manual_seed(seed)
+    words = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), generator=gen, dtype=torch.int32).cuda()
+    m = 2 * torch.randint(512, 1024, (N, K // g), generator=gen) + 1
+    sign = 2 * torch.randint(0, 2, (N, K // g), generator=gen) - 1
+    step = (m * sign * 2.0 ** -20).to(torch.float16).cuda()
+    zero = torch.randint(0, 16, (N, K // g), generator=gen, dtype=torch.uint8).cuda()
+    codes = ((words.unsqueeze(-1) >> torch.arange(0, 32, 4, device="cuda", dtype=torch.int32)) & 15).flatten(1).double()
+    w = (codes.unflatten(1, (-1, g)) - zero.double().unsqueeze(-1)) * step.double().unsqueeze(-1)
+    return (words, step, zero), w.flatten(1)
+
+
+def whole_rows(M, n, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.zeros(M, n)
+    at = torch.randint(0, n, (M, min(60, n)), generator=gen)
+    v = (torch.randint(1, 9, at.shape, generator=gen) * (2 * torch.randint(0, 2, at.shape, generator=gen) - 1)).float()
+    return x.scatter_(1, at, v).to(dtype).cuda()
+
+
+def rounded(ref, dtype):
+    """Exact values that fp32 holds, rounded once."""
+    assert torch.equal(ref.float().double(), ref)
+    return ref.float().to(dtype)
+
+
+WHOLE_DXS = [
+    # M, N, K, group: each height of the tiles, alone and with the contraction in slices
+    (1, 453, 64, 64), (3, 8, 64, 64), (16, 1000, 512, 128), (17, 130, 1024, 64), (40, 4096, 4096, 128), (100, 2000, 2048, 256),
+    (4266, 8, 64, 64), (1098, 472, 128, 64), (4201, 8, 320, 64), (519, 1000, 4096, 128), (1130, 990, 64, 64),
+    (2858, 8, 1408, 128), (1051, 2004, 192, 64), (1100, 700, 4096, 256), (1635, 8, 5248, 128), (4095, 1027, 4096, 128),
+    (4435, 1296, 64, 64), (733, 9430, 6912, 128),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", WHOLE_DXS, ids=lambda c: "x".join(str(v) for v in c))
+def test_gemm_dx_to_the_last_bit(on_gpu, case):
+    M, N, K, g = case
+    q, w = whole_weights(N, K, g, M)
+    for dt in (torch.float16, torch.bfloat16):
+        dz = whole_rows(M, N, dt, N)
+        ref = dz.double() @ w
+        for out in DTYPES.values():
+            dx = awq.awq_w4a16_gemm_dx(dz, *q, out_dtype=out, group_size=g)
+            assert torch.equal(dx, rounded(ref, out)), (dt, out, int((dx != rounded(ref, out)).sum()))

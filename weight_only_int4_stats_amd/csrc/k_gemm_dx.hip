@@ -17,14 +17,17 @@
 //      (exact for what lies within 2^28 of the row's largest), padded with
 //      zeros to a multiple of 64.
 //   3. k_gemm_dx: the tiles of k_tiles.h, over slices of the contraction where
-//      the tiles alone leave compute units without work.  The weights are the
-//      product of two exact fp16 values, rounded once.
+//      the tiles alone leave compute units without work.  A weight, up to 15
+//      bits, is the sum of two fp16 values and meets dz in two products: with one,
+//      rounded to 11 bits, an fp16 dx was off by 2.8e-4 of its size, 2.1e-4 with
+//      all bits, and an fp32 dx showed all of it.
 //   4. k_dx_reduce where the contraction is split: the slices' fp32 sums added
 //      in their order.
-// 2048 rows, 11008 -> 4096, bf16: 5 + 17 + 226 to 244 us (0.8 PFLOP/s), bound by
-// the matrix pipe and the dequantization beside it.  37 rows, 4096 -> 11008,
-// fp16: 5.3 + 3.1 + 22 + 4.1 us against 4.5 for the packed words alone: a stage
-// costs 0.8 us whatever is in its rows, which is the dequantization.
+// 2048 rows, 11008 -> 4096, bf16: 294 us a call (235 with one product), bound by
+// the matrix pipe: 1.3 PFLOP/s of products, what a large library product
+// reaches.  37 rows, 4096 -> 11008, fp16: 39 us (35) against 4.5 for the packed
+// words alone: a stage costs 1 us whatever is in its rows, the dequantization and
+// its products.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_epilogue.h"
@@ -214,6 +217,7 @@ struct DxOp {
   static constexpr int BW = 2 / WM;       // copies of packed words per wave
   static constexpr int Bytes = kDxB + kDxC;
   static constexpr int VAlu = 4;
+  static constexpr bool Whole = true;
   static __device__ __forceinline__ int chunk(int st, int b4) { return 4 * st + b4; }
 
   const uint8_t* qw;
@@ -298,7 +302,7 @@ struct DxOp {
 // Stages in LDS: what 160 KB hold with one block per compute unit for tall
 // tiles, with two for the small ones.
 template <int MB, int WM>
-constexpr int kDxStages = WM == 2 ? (MB == 8 ? 3 : 6) : (MB == 8 ? 3 : MB == 4 ? 4 : MB == 2 ? 5 : 6);
+constexpr int kDxStages = WM == 2 ? (MB == 8 ? 3 : 6) : (MB == 4 ? 4 : MB == 2 ? 5 : 6);
 
 // MB: 16-row blocks per wave, WM: waves along the rows.  S slices of the contraction; SPLIT: fp32 sums to
 // partial [S][M][K] instead of dx.
@@ -364,8 +368,11 @@ __global__ __launch_bounds__(256) void k_dx_zero(int64_t M, int64_t K, void* __r
   if (i < M * K) store_any(dx, dxt, i / K * lddx + i % K, 0.0f);
 }
 
-// us per stage, measured at 37 to 2048 rows, 4096 <-> 11008
-constexpr TileShape kDxShapes[] = {{8, 2, 1.90, 0.0}, {4, 2, 1.14, 0.0}, {8, 1, 1.06, 2.3}, {4, 1, 0.80, 1.40}, {2, 1, 0.58, 1.0}, {1, 1, 0.55, 0.95}};
+// us per stage, fitted to the times of every shape and number of slices at 17
+// sizes of 8 to 4096 rows, 1024 to 11008: the choice takes at most 2 % longer
+// than the fastest there.  (128 rows by four waves never were: 147 to 145 us at
+// 1500 rows of 5120 x 5120, 239 to 207 at 4096^3.)
+constexpr TileShape kDxShapes[] = {{8, 2, 2.29, 0.0}, {4, 2, 1.45, 0.0}, {4, 1, 0.97, 1.51}, {2, 1, 0.64, 1.04}, {1, 1, 0.63, 0.89}};
 
 inline TilePlan dx_plan(int64_t M, int64_t N, int64_t K) {
   return tile_plan(kDxShapes, M, K, (N + kDxN - 1) / kDxN, awq::device_cus() > 0 ? awq::device_cus() : 256);
@@ -469,7 +476,6 @@ hipError_t launch_gemm_dx(const void* dz, int dzt, int64_t M, int64_t N, int64_t
     AWQ_DX(4, 2);
   }
   switch (p.mb) {
-    case 8: AWQ_DX(8, 1);
     case 4: AWQ_DX(4, 1);
     case 2: AWQ_DX(2, 1);
     default: AWQ_DX(1, 1);

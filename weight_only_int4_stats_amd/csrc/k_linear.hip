@@ -35,6 +35,7 @@ struct LinearOp {
   static constexpr int BW = 2 / WM;
   static constexpr int WordBytes = kTileCols * kTileK / 2, Bytes = WordBytes + kTileCols * 8;
   static constexpr int VAlu = 4;
+  static constexpr bool Whole = false;
   static __device__ __forceinline__ int chunk(int st, int b4) { return 2 * b4 + st; }
 
   i32x4 brs, crs;

@@ -54,8 +54,8 @@ __device__ __forceinline__ bool tile_item(int64_t block, int64_t mtiles, int64_t
 // lo): the operand of column block c for k32 step st, rounded to fp16 in hi or
 // (Whole) as two exact parts; chunk(st, b4): the A chunk that goes with it.
 //
-// Tiles of 16 rows multiply by both parts (Whole): the dequantization bounds
-// them and leaves the matrix pipe room.
+// dx multiplies by both parts (Whole), and so does every product in tiles of 16
+// rows: the dequantization bounds them and leaves the matrix pipe room.
 template <int MB, int WM, int NS, class OP>
 struct Tile {
   static constexpr int Waves = 4 * WM;
@@ -69,7 +69,7 @@ struct Tile {
   static constexpr int H = MB > 4 ? 2 : 1;              // sub-steps per k32 step
   static constexpr int MH = MB / H;                     // 16-row blocks per sub-step
   static constexpr int BW = 8 / Waves;                  // copies of packed words per wave
-  static constexpr bool Whole = MB == 1;
+  static constexpr bool Whole = OP::Whole || MB == 1;
   static_assert((NS - 1) * (AW + BW + 1) <= 63, "copies in flight");
 
   // rows of xq from row m0 on (pitch Kp, a multiple of 64), stages [s0, s1)
