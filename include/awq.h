@@ -525,11 +525,9 @@ awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int6
  * bias == NULL, residual == NULL: 0.  1/s is expected folded (awq_fold_scales).
  * pre, if not NULL, receives z: what awq_bias_act_backward needs of the
  * forward pass.  The sum, the bias, the activation and the residual are held
- * in fp32 and y (and pre) rounded once.  The sum itself is formed as in
- * awq_w4a16_gemm: products of the exact integers q - z for one token and for
- * the shapes of up to 16 tokens that one launch stages, else of the
- * dequantized weights rounded once to fp16 (an F32 y shows that rounding;
- * small batches carry its remainder along, a bf16 y of theirs need not).
+ * in fp32 and y (and pre) rounded once.  The sum is that of products of the
+ * exact integers q - z and the step in fp32, or (17 to 64 tokens) of the
+ * dequantized weights as two fp16 values each, for a bf16 y one.
  * Activations as fp16 under exact powers of two: bf16 values below 2^-28 of
  * the largest they share one with lose bits.
  *

@@ -91,4 +91,52 @@ def test_gemm_dx_to_the_last_bit(on_gpu, case):
         ref = dz.double() @ w
         for out in DTYPES.values():
             dx = awq.awq_w4a16_gemm_dx(dz, *q, out_dtype=out, group_size=g)
-            assert torch.equal(dx, rounded(ref, out)), (dt, out, int((dx != rounded(ref, out)).sum()))
+            wrong = int((dx != rounded(ref, out)).sum())
+            assert wrong == 0, (dt, out, wrong)
+
+
+WHOLE_LINEARS = [
+    # M, N, K, group: one token, up to 16, and each height of the tiles, alone, in slices, two in one launch
+    (1, 515, 1024, 64), (1, 6200, 4096, 128), (2, 300, 512, 128), (9, 130, 192, 64), (16, 2048, 4096, 128),
+    (80, 520, 2048, 128), (300, 16, 64, 64), (635, 28, 2048, 128), (1246, 3163, 1024, 64), (510, 8465, 128, 128),
+    (519, 1027, 4096, 64), (1024, 4096, 4096, 128), (1100, 900, 8192, 256), (2048, 9001, 256, 128), (2300, 11008, 512, 64),
+    (4097, 4100, 256, 256),
+]
+
+
+def one_step_a_row(q, w, g):
+    """The same with each row's first step and zero point's sign kept for all of its groups."""
+    words, step, zero = q
+    n = step.shape[0]
+    units = w.unflatten(1, (-1, g)) / step.double().unsqueeze(-1)
+    step = step[:, :1].expand(n, step.shape[1]).contiguous()
+    return (words, step, zero), (units * step.double().unsqueeze(-1)).flatten(1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", WHOLE_LINEARS, ids=lambda c: "x".join(str(v) for v in c))
+def test_linear_to_the_last_bit(on_gpu, case):
+    M, N, K, g = case
+    q, w = one_step_a_row(*whole_weights(N, K, g, M), g)
+    for dt in (torch.float16, torch.bfloat16):
+        x = whole_rows(M, K, dt, N)
+        ref = x.double() @ w.t()
+        for out in DTYPES.values():
+            pre = torch.empty(M, N, dtype=out, device="cuda")
+            y = awq.awq_w4a16_linear(x, *q, act="relu", pre=pre, out_dtype=out, group_size=g)
+            wrong = int((pre != rounded(ref, out)).sum()), int((y != rounded(ref.clamp_min(0), out)).sum())
+            assert wrong == (0, 0), (dt, out, wrong)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", WHOLE_LINEARS, ids=lambda c: "x".join(str(v) for v in c))
+def test_linear_with_a_step_for_each_group(on_gpu, case):
+    """Steps that differ: what fp32 loses at each group (a quotient of steps, a product with it or a multiply-add, three
+    half steps of the running sum) and at each of the 60 sums, each at most the sum of all terms' sizes in size."""
+    M, N, K, g = case
+    q, w = whole_weights(N, K, g, M)
+    x = whole_rows(M, K, torch.bfloat16, N)
+    ref, size = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    y = awq.awq_w4a16_linear(x, *q, out_dtype=torch.float32, group_size=g)
+    off = (y.double() - ref).abs()
+    assert bool((off <= (3 * (K // g) + 2 * 60 + 4) * 2.0 ** -24 * size).all()), float((off / size.clamp_min(1e-30)).max() * 2 ** 24)

@@ -73,7 +73,7 @@ struct Epilogue {
 
 // ---- W4A16 product ----------------------------------------------------------
 // ep (optional, for awq_w4a16_linear): the epilogue; then inv_s is NULL and the
-// weights are rounded once (k_epilogue.h)
+// weights keep all their bits (k_epilogue.h)
 // group: input channels per step / zero point (64, 128 or 256)
 bool gemv1_supported(int64_t K, int64_t N);   // batch-1 GEMV kernels cover this shape
 hipError_t launch_gemv1(const void* x, int xdt, int64_t K, const uint32_t* qw,
@@ -179,7 +179,7 @@ int64_t linear_threads(int64_t M, int64_t N, int64_t K);   // of the largest of 
 hipError_t launch_linear(const void* x, int xdt, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                          const uint16_t* scales, const uint8_t* zeros, int64_t N, int group, void* y, int64_t ldy,
                          const Epilogue& ep, void* ws, hipStream_t st);
-hipError_t launch_linear_tiles(const uint16_t* xq, const int* pm, const int* en, const uint32_t* ctab, const uint32_t* qw,
+hipError_t launch_linear_tiles(const uint16_t* xq, const int* pm, const uint32_t* ctab, const uint32_t* qw,
                                int64_t M, int64_t N, int64_t K, int group, float* partial, void* y, int64_t ldy,
                                const Epilogue& ep, hipStream_t st);
 

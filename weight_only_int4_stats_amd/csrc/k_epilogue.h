@@ -326,14 +326,12 @@ __device__ __forceinline__ void epi_store4(const Epilogue& ep, void* y, int64_t 
   store4_any(y, ep.ydt, m * ldy + n, cnt, z);
 }
 
-// ---- weights rounded once -------------------------------------------------------
-// The kernels that feed step (q - z) to the matrix cores in fp16 form it under
-// an epilogue as the product of two exact fp16 values, (q - z) 2^-9 and
-// step 2^e with the row's largest one in [2^14, 2^15): one rounding, where the
-// plain product's D' q - D' z rounds its constant too, which an fp16 output
-// would show beside its own rounding (measured here: 2.8e-4 of an output's
-// size, 2.1e-4 with weights in fp32).  Four more vector instructions per packed
-// word.
+// ---- weights of all their bits ---------------------------------------------------
+// step (q - z) has up to 15 bits, an fp16 operand 11.  The matrix cores take it
+// under an epilogue, and for dx, as two: the code (q - z) 2^-9, exact, times
+// either part of step 2^e, with the row's largest one in [2^14, 2^15).  (The plain
+// product's D' q - D' z rounds twice, which an fp16 output would show beside its
+// own rounding: 2.8e-4 of an output's size, 2.1e-4 with weights in fp32.)
 constexpr int kOncePow = 15;          // max step 2^e < 2^15
 constexpr int kOnceUnit = 9;          // the codes carry 2^-9
 

@@ -217,7 +217,7 @@ struct DxOp {
   static constexpr int BW = 2 / WM;       // copies of packed words per wave
   static constexpr int Bytes = kDxB + kDxC;
   static constexpr int VAlu = 4;
-  static constexpr bool Whole = true;
+  static constexpr bool Whole = true, Units = false;
   static __device__ __forceinline__ int chunk(int st, int b4) { return 4 * st + b4; }
 
   const uint8_t* qw;
@@ -275,18 +275,14 @@ struct DxOp {
     }
   }
   // the lane's halves of rows n and n + 1 side by side
-  template <bool WHOLE>
   __device__ __forceinline__ void begin(int st) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       p[j] = __builtin_amdgcn_perm(w[st][2 * j + 1], w[st][2 * j], sel);
       p8[j] = p[j] >> 8;
-      const uint32_t d = cm[st][j];
-      if constexpr (WHOLE) once_parts(d, mh[j], ml[j]);
-      else mh[j] = d;
+      once_parts(cm[st][j], mh[j], ml[j]);
     }
   }
-  template <bool WHOLE>
   __device__ __forceinline__ void column(int st, int c, u32x4& hi, u32x4& lo) const {
     const f16x2 scale = as_f16x2(c & 1 ? 0x68006800u : 0x78007800u);       // 2^11, 2^15
 #pragma unroll
@@ -294,7 +290,7 @@ struct DxOp {
       const uint32_t v = (c & 2 ? p8[j] : p[j]) & (c & 1 ? 0x00F000F0u : 0x000F000Fu), z = cz[st][j];
       const f16x2 code = __builtin_elementwise_fma(as_f16x2(v), scale, as_f16x2(z));
       hi[j] = __builtin_bit_cast(uint32_t, code * as_f16x2(mh[j]));
-      if constexpr (WHOLE) lo[j] = __builtin_bit_cast(uint32_t, code * as_f16x2(ml[j]));
+      lo[j] = __builtin_bit_cast(uint32_t, code * as_f16x2(ml[j]));
     }
   }
 };

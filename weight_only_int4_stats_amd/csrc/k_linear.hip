@@ -3,17 +3,24 @@
 //   y[m][n] = act(sum_k step[n][g(k)] (q[n][k] - z[n][g(k)]) x[m][k] + bias[n]) + residual[m][n]
 //   1. k_gemm_prep (the plain product's pre-pass): activation rows as fp16 under
 //      an exact power of two per row, in the order the nibble unpack yields, and
-//      the dequantization constants.
-//   2. k_linear_tiles: tiles over slices of the contraction; without slices the
+//      steps and zero points group by group.
+//   2. k_linear_tiles: tiles over slices of the contraction.  The matrix cores
+//      multiply the activations with the exact integers (q - z) 2^-9; the sums are
+//      held in units of the current group's step: a group's first stage
+//      multiplies them by the last step over this one's (fp32), the end by the
+//      last.  So no operand is rounded.  (Weights rounded to fp16, 13 instead of
+//      9 vector instructions per eight: fp16 outputs off by 2.8e-4 of their size,
+//      2.1e-4 this way; weights as two fp16 values in two products: 333 us
+//      instead of 252 for 2048 tokens, 4096 -> 11008.)  Without slices the
 //      sums pass LDS to lanes of eight adjacent columns and go through the
 //      epilogue, with them they go to the workspace as fp32.
 //   3. k_linear_reduce (slices): the slices' sums added in their order, then the
 //      epilogue.
-// 2048 tokens, 4096 -> 11008, bf16 with bias, gelu and pre: 10 + 234 to 249 us
-// in a row of calls (0.75 PFLOP/s), 224 in all with the caches flushed between
-// calls (0.83); bound by the matrix pipe and the dequantization beside it; the
-// plain product, which rounds twice and stores one output, 182 to 198.  519 tokens, 4096 -> 1027, fp16 with bias and silu: 5.5 +
-// 23 + 6.4 us, bound by the dequantization and by what surrounds the stages.
+// 2048 tokens, 4096 -> 11008, bf16 with bias, gelu and pre: 252 us a call (274
+// with groups of 64), bound by the matrix pipe and the vector instructions beside
+// it; the plain product, which rounds the weights twice and stores one output,
+// 190 to 205.  519 tokens, 4096 -> 1027, fp16 with bias and silu: 40, bound by the
+// dequantization and by what surrounds the stages.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_epilogue.h"
@@ -33,9 +40,9 @@ namespace awqk {
 template <int WM>
 struct LinearOp {
   static constexpr int BW = 2 / WM;
-  static constexpr int WordBytes = kTileCols * kTileK / 2, Bytes = WordBytes + kTileCols * 8;
+  static constexpr int WordBytes = kTileCols * kTileK / 2, Bytes = WordBytes + kTileCols * 4;
   static constexpr int VAlu = 4;
-  static constexpr bool Whole = false;
+  static constexpr bool Whole = false, Units = true;
   static __device__ __forceinline__ int chunk(int st, int b4) { return 2 * b4 + st; }
 
   i32x4 brs, crs;
@@ -43,7 +50,9 @@ struct LinearOp {
   int copies, wv, glog;
   uint32_t boff[BW], coff, wlane, clane;
   uint2 w[4];
-  u32x4 c[2];
+  u32x4 c;
+  uint32_t nz[4];                         // fp16(-z 2^-9) twice
+  float ratio[4], last[4], any[4];        // the last unit / this one, this one, the largest step (0: the column is 0)
 
   __device__ __forceinline__ void init(const uint32_t* qw, int64_t n, int64_t K, int64_t n0, const uint32_t* ctab, int gl) {
     const int tid = threadIdx.x, lane = tid & 63;
@@ -53,50 +62,70 @@ struct LinearOp {
     glog = gl;
     const int cols = (int)(N - n0 < kTileCols ? N - n0 : kTileCols);
     brs = rsrc4(qw + n0 * (K >> 3), (uint32_t)(cols * (K >> 1)));
-    crs = rsrc4(ctab + n0 * 2, (uint32_t)((((K >> glog) - 1) * N + cols) * 8));
-    copies = wv < 2 ? BW + 1 : BW;
+    crs = rsrc4(ctab + n0, (uint32_t)((((K >> glog) - 1) * N + cols) * 4));
+    copies = wv == 0 ? BW + 1 : BW;
 #pragma unroll
     for (int u = 0; u < BW; ++u) {
       // lane i of copy j: half i / 32 of the column at place 32 j + i % 32
       const int at = 32 * (BW * wv + u) + (lane & 31), col = (at & ~63) + 4 * (at & 15) + ((at >> 4) & 3);
       boff[u] = (uint32_t)(col * (K >> 1) + (lane >> 5) * 16);
     }
-    coff = (uint32_t)((wv * 128 + lane * 2) * 8);
+    coff = (uint32_t)(lane * 16);
     const int at = wn * 64 + rl;
     wlane = (uint32_t)((at >> 5) * 1024 + (b4 >> 1) * 512 + (at & 31) * 16 + (b4 & 1) * 8);
-    clane = (uint32_t)(WordBytes + (wn * 64 + 4 * rl) * 8);
+    clane = (uint32_t)(WordBytes + (wn * 64 + 4 * rl) * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      last[i] = 1.0f;
+      any[i] = 0.0f;
+    }
   }
   __device__ __forceinline__ void issue(int64_t s, uint32_t lb, bool live) const {
     i32x4 b = brs, t = crs;
     b[2] = live ? b[2] : 0;
 #pragma unroll
     for (int u = 0; u < BW; ++u) dma16(b, lb + (BW * wv + u) * 1024, boff[u], live ? (uint32_t)(s * 32) : 0u);
-    if (wv < 2) {
+    if (wv == 0) {
       t[2] = live ? t[2] : 0;
-      dma16(t, lb + WordBytes + wv * 1024, coff, live ? (uint32_t)(((s * kTileK) >> glog) * N * 8) : 0u);
+      dma16(t, lb + WordBytes, coff, live ? (uint32_t)(((s * kTileK) >> glog) * N * 4) : 0u);
     }
   }
   __device__ __forceinline__ void load(const uint8_t* base) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)       // places 16 apart: halves of 256 bytes of blocks of 1 KB
       w[i] = *reinterpret_cast<const uint2*>(base + wlane + (i >> 1) * 1024 + (i & 1) * 256);
-    c[0] = *reinterpret_cast<const u32x4*>(base + clane);
-    c[1] = *reinterpret_cast<const u32x4*>(base + clane + 16);
+    c = *reinterpret_cast<const u32x4*>(base + clane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nz[i] = __builtin_amdgcn_perm(c[i], c[i], 0x03020302u);
   }
-  template <bool WHOLE>
-  __device__ __forceinline__ void begin(int) {}
-  template <bool WHOLE>
-  __device__ __forceinline__ void column(int st, int i, u32x4& hi, u32x4& lo) const {
-    const uint32_t m = c[i >> 1][2 * (i & 1)], z = c[i >> 1][2 * (i & 1) + 1];
-    const u32x4 codes = once_codes(st ? w[i].y : w[i].x, z);
-    if constexpr (WHOLE) {
-      uint32_t mh, ml;
-      once_parts(m, mh, ml);
-      hi = once_times(codes, mh);
-      lo = once_times(codes, ml);
-    } else {
-      hi = once_times(codes, m);
+  // whether stage s begins a group
+  __device__ __forceinline__ bool fresh(int64_t s) const { return ((s * kTileK) & (((int64_t)1 << glog) - 1)) == 0; }
+  // The sums' next unit: the loaded stage's steps.  A step of 0 counts as 2^-60,
+  // which keeps the ratios finite and is below the rounding of any other, an
+  // infinite one as 2^60, until the end (steps()).  The quotient is corrected by
+  // its remainder: equal steps give 1.
+  __device__ __forceinline__ void unit() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = c[i];
+      const float f = f16_to_f32(v & 0xFFFFu), size = fabsf(f);
+      const float d = size < 0x1p-60f ? 0x1p-60f : size == __builtin_inff() ? copysignf(0x1p60f, f) : f;
+      any[i] = fmaxf(any[i], size);
+      const float r = __builtin_amdgcn_rcpf(d), t = last[i] * r;
+      ratio[i] = __builtin_fmaf(__builtin_fmaf(-t, d, last[i]), r, t);
+      last[i] = d;
     }
+  }
+  // what the finished sums of the four columns are multiplied by
+  __device__ __forceinline__ f32x4 steps() const {
+    f32x4 d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = any[i] == 0.0f ? 0.0f : any[i] == __builtin_inff() ? last[i] * any[i] : last[i];
+    return d;
+  }
+  __device__ __forceinline__ void begin(int) {}
+  __device__ __forceinline__ void column(int st, int i, u32x4& codes, u32x4&) const {
+    codes = once_codes(st ? w[i].y : w[i].x, nz[i]);
   }
 };
 
@@ -106,7 +135,6 @@ constexpr int kLinearStages = WM == 2 ? (MB == 8 ? 3 : 5) : (MB == 4 ? 4 : MB ==
 struct LinearArgs {
   const uint16_t* xq;
   const int* pm;
-  const int* en;
   const uint32_t* ctab;
   const uint32_t* qw;
   float* partial;        // [S][M][pitch]
@@ -129,6 +157,7 @@ __device__ __forceinline__ void linear_tile(uint8_t* tile_lds, const LinearArgs&
   op.init(a.qw, a.N, a.K, n0, a.ctab, a.glog);
   f32x4 acc[MB][4];
   Tl::run(tile_lds, op, a.xq, m0, rows, a.K, bs * stages / a.S, (bs + 1) * stages / a.S, acc);
+  const f32x4 steps = op.steps();
 
   // 16 x 16 layout: column 4 (lane % 16) + c, row 4 (lane / 16) + v
   const int64_t n = n0 + wn * 64 + 4 * rl, mw = m0 + wm * 16 * MB;
@@ -142,7 +171,7 @@ __device__ __forceinline__ void linear_tile(uint8_t* tile_lds, const LinearArgs&
         const int64_t m = mw + b * 16 + 4 * b4 + v;
         if (m < a.M)                                      // pitch a multiple of 8: whole fours
           *reinterpret_cast<f32x4*>(a.partial + ((int64_t)bs * a.M + m) * a.pitch + n) =
-              f32x4{acc[b][0][v], acc[b][1][v], acc[b][2][v], acc[b][3][v]};
+              f32x4{acc[b][0][v], acc[b][1][v], acc[b][2][v], acc[b][3][v]} * steps;
       }
   } else {
     // The sums pass the wave's own LDS area so that one copy of the epilogue's
@@ -152,10 +181,7 @@ __device__ __forceinline__ void linear_tile(uint8_t* tile_lds, const LinearArgs&
     static_assert(PB >= 1 && PB * Tl::Waves * 4096 <= Tl::Lds, "the waves' staging");
     f32x4* mine = reinterpret_cast<f32x4*>(tile_lds + wv * PB * 4096) + lane;
     const int c4 = cnt > 0 ? cnt : 0;
-    int e4[4];
     float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) e4[j] = j < c4 ? a.en[n + j] : 0;
     if (ep.bias) load4_any(ep.bias, ep.bdt, n, c4, bias);
     float rn[4][4] = {};
     int pn[4] = {};
@@ -184,7 +210,7 @@ __device__ __forceinline__ void linear_tile(uint8_t* tile_lds, const LinearArgs&
           const f32x4 t = mine[(b * 4 + v) * 64];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            z[v][j] = ldexpf(t[j], -(pn[v] + e4[j])) + bias[j];
+            z[v][j] = ldexpf(t[j] * steps[j], kOnceUnit - pn[v]) + bias[j];
             r[v][j] = rn[v][j];
           }
         }
@@ -249,12 +275,14 @@ __global__ __launch_bounds__(256) void k_linear_reduce(const LinearArgs a, const
   float z[4], b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (ep.bias) load4_any(ep.bias, ep.bdt, n, cnt, b);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) z[j] = j < cnt ? ldexpf(t[j], -(pw + a.en[n + j])) + b[j] : 0.0f;
+  for (int j = 0; j < 4; ++j) z[j] = j < cnt ? ldexpf(t[j], kOnceUnit - pw) + b[j] : 0.0f;
   epi_store4(ep, a.y, a.ldy, m, n, cnt, z);
 }
 
-// us per stage, measured at 24 to 4096 rows, 1027 to 11008 columns
-constexpr TileShape kLinearShapes[] = {{8, 2, 1.84, 0.0}, {4, 2, 1.11, 0.0}, {4, 1, 0.75, 1.35}, {2, 1, 0.57, 0.94}, {1, 1, 0.50, 0.85}};
+// us per stage, fitted to the times of every shape and number of slices at 16
+// sizes of 40 to 4096 rows, 1024 to 11008: the choice takes at most 3 % longer
+// than the fastest there, 9 % at 4096 rows, 2048 -> 1027.
+constexpr TileShape kLinearShapes[] = {{8, 2, 1.77, 0.0}, {4, 2, 1.06, 0.0}, {4, 1, 0.79, 1.35}, {2, 1, 0.58, 0.89}, {1, 1, 0.50, 0.87}};
 
 struct LinearPlan {
   TilePlan t;
@@ -321,13 +349,13 @@ size_t linear_partial_bytes_upto(int64_t M, int64_t N, int64_t K) {
   return align_up((size_t)parts * awqk::linear_pitch(N) * 4, 256);
 }
 
-hipError_t launch_linear_tiles(const uint16_t* xq, const int* pm, const int* en, const uint32_t* ctab, const uint32_t* qw,
+hipError_t launch_linear_tiles(const uint16_t* xq, const int* pm, const uint32_t* ctab, const uint32_t* qw,
                                int64_t M, int64_t N, int64_t K, int group, float* partial, void* y, int64_t ldy,
                                const Epilogue& ep, hipStream_t st) {
   using namespace awqk;
   const LinearPlan p = linear_plan(M, N, K);
   const int glog = group == 64 ? 6 : group == 128 ? 7 : 8;
-  const LinearArgs a{xq, pm, en, ctab, qw, partial, y, M, N, K, ldy, linear_pitch(N), glog, p.t.S};
+  const LinearArgs a{xq, pm, ctab, qw, partial, y, M, N, K, ldy, linear_pitch(N), glog, p.t.S};
   if (p.wide) {
     constexpr size_t lds = kLinearLds<8, 2> > kLinearLds<4, 2> ? kLinearLds<8, 2> : kLinearLds<4, 2>;
     hipLaunchKernelGGL(k_linear_mixed, dim3((unsigned)p.blocks), dim3(512), lds, st, a, ep, p.wide, p.wide_blocks);

@@ -50,12 +50,11 @@ __device__ __forceinline__ bool tile_item(int64_t block, int64_t mtiles, int64_t
 
 // OP, the packed operand: bytes of its part of a stage (OP::Bytes), the copies
 // of this wave (op.copies, BW or one more), issue(s, lds, live), load(lds): a stage's
-// words and constants into registers, begin<Whole>(st) and column<Whole>(st, c, hi,
-// lo): the operand of column block c for k32 step st, rounded to fp16 in hi or
-// (Whole) as two exact parts; chunk(st, b4): the A chunk that goes with it.
-//
-// dx multiplies by both parts (Whole), and so does every product in tiles of 16
-// rows: the dequantization bounds them and leaves the matrix pipe room.
+// words and constants into registers, begin(st) and column(st, c, hi, lo): the
+// operand of column block c for k32 step st; chunk(st, b4): the A chunk that goes
+// with it.  OP::Whole: the operand is hi + lo, and both meet A.  OP::Units: the sums
+// of column block c are in a unit of their own, which unit() changes where
+// fresh(s), by a factor ratio[c].
 template <int MB, int WM, int NS, class OP>
 struct Tile {
   static constexpr int Waves = 4 * WM;
@@ -69,7 +68,6 @@ struct Tile {
   static constexpr int H = MB > 4 ? 2 : 1;              // sub-steps per k32 step
   static constexpr int MH = MB / H;                     // 16-row blocks per sub-step
   static constexpr int BW = 8 / Waves;                  // copies of packed words per wave
-  static constexpr bool Whole = OP::Whole || MB == 1;
   static_assert((NS - 1) * (AW + BW + 1) <= 63, "copies in flight");
 
   // rows of xq from row m0 on (pitch Kp, a multiple of 64), stages [s0, s1)
@@ -123,17 +121,31 @@ struct Tile {
     for (int j = 0; j < NS; ++j) issue(s0 + j, j);
     wait(std::integral_constant<int, NS - 1>{});
     lds_barrier();
-    u32x4 bq[4], bl[Whole ? 4 : 1];
+    u32x4 bq[4], bl[OP::Whole ? 4 : 1];
     load_a(lds, 0, a0);
     op.load(lds + A);
-    op.template begin<Whole>(0);
+    op.begin(0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) op.template column<Whole>(0, c, bq[c], bl[Whole ? c : 0]);
+    for (int c = 0; c < 4; ++c) op.column(0, c, bq[c], bl[OP::Whole ? c : 0]);
     uint32_t slot = 0;
     for (int64_t s = s0; s < s1; ++s) {
       const uint32_t nslot = slot + 1 == NS ? 0 : slot + 1;
       const uint8_t* cur = lds + slot * Stage;
       const uint8_t* nxt = lds + nslot * Stage;
+      if constexpr (OP::Units) {
+        // between the stages: among the products, in every stage, it took longer
+        // (2048 x 4096 x 11008: 279 us against 252, groups of 64: the same)
+        if (s == s0 || op.fresh(s)) {
+          op.unit();
+#pragma unroll
+          for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[b][c][v] *= op.ratio[c];
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
 #pragma unroll
       for (int q = 0; q < 2 * H; ++q) {
         u32x4 (&ac)[MH] = (q & 1) ? a1 : a0;
@@ -156,11 +168,11 @@ struct Tile {
           for (int i = 0; i < MH; ++i) {
             const int b = (q % H) * MH + i;
             acc[b][c] = mfma16h(ac[i], bq[c], acc[b][c]);
-            if constexpr (Whole) acc[b][c] = mfma16h(ac[i], bl[c], acc[b][c]);
+            if constexpr (OP::Whole) acc[b][c] = mfma16h(ac[i], bl[c], acc[b][c]);
           }
           if (turn) {
-            if (c == 0) op.template begin<Whole>(st ^ 1);
-            op.template column<Whole>(st ^ 1, c, bq[c], bl[Whole ? c : 0]);
+            if (c == 0) op.begin(st ^ 1);
+            op.column(st ^ 1, c, bq[c], bl[OP::Whole ? c : 0]);
           }
         }
         if (turn && MH >= 4) {

@@ -41,10 +41,10 @@ __device__ __forceinline__ void store_y(void* y, int64_t idx, float v) {
 // fp16; then, for every group g, the fp16 constants of the packed-fma
 // dequantization, group-major so a block's columns are contiguous:
 //   ctab[g][n] = (fp16(D' 2^24) | fp16(D' 2^20) << 16, fp16(-D' z) twice).
-// ONCE (for awq_w4a16_linear's tiles): max_g |step[n][g]| 2^e_n in [2^14, 2^15) and
-//   ctab[g][n] = (fp16(step 2^e_n) twice, fp16(-z 2^-9) twice).
+// UNITS (for awq_w4a16_linear's tiles): ctab[g][n] = step | fp16(-z 2^-9) << 16
+//   (32 bits), and no e_n.
 constexpr int kConstRows = 16;   // weight rows per block of the constants pre-pass
-template <bool ONCE>
+template <bool UNITS>
 __device__ __forceinline__ void gemm_consts_block(int64_t bid, const uint16_t* __restrict__ scales,
                                                   const uint8_t* __restrict__ zeros, int64_t N,
                                                   int64_t G, int* __restrict__ en,
@@ -61,20 +61,21 @@ __device__ __forceinline__ void gemm_consts_block(int64_t bid, const uint16_t* _
   const int64_t g0 = p * G / 16, g1 = (p + 1) * G / 16;
   const uint16_t* sr = scales + (ok ? n : 0) * G;
   const uint8_t* zr = zeros + (ok ? n : 0) * G;
+  if constexpr (UNITS) {
+    if (ok)
+      for (int64_t g = g0; g < g1; ++g) ctab[g * N + n] = sr[g] | (once_zero(zr[g]) << 16);
+    return;
+  }
   float mx = 0.0f;
   if (ok)
-    for (int64_t g = g0; g < g1; ++g) mx = fmaxf(mx, step_size<ONCE>(sr[g]));
+    for (int64_t g = g0; g < g1; ++g) mx = fmaxf(mx, f16_to_f32(sr[g]));
 #pragma unroll
   for (int off = 8; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
-  const int e = step_pow<ONCE>(mx);   // mx 2^e in [2^-10, 2^-9)
+  const int e = step_pow<false>(mx);   // mx 2^e in [2^-10, 2^-9)
   if (!ok) return;
-  if (p == 0) en[n] = sum_pow<ONCE>(e);
+  if (p == 0) en[n] = e;
   for (int64_t g = g0; g < g1; ++g) {
     const float D = ldexpf(f16_to_f32(sr[g]), e);   // exact: power-of-two scaling
-    if constexpr (ONCE) {
-      *reinterpret_cast<uint2*>(ctab + (g * N + n) * 2) = make_uint2(once_step(D) * 0x10001u, once_zero(zr[g]));
-      continue;
-    }
     const uint32_t h24 = f32_to_f16_bits(D * 16777216.0f);
     const uint32_t h20 = f32_to_f16_bits(D * 1048576.0f);
     const uint32_t hz = f32_to_f16_bits(-(D * (float)zr[g]));
@@ -135,7 +136,7 @@ __device__ __forceinline__ u32x4 dequant_word_f16(uint32_t w, uint32_t cx, uint3
 // ceil(N / 16) blocks build the constants, the other M convert one activation
 // row each.
 // KEEP: activation chunks per thread held in registers (16: rows up to 32768).
-template <int DT, bool HAS_R, int KEEP, bool ONCE>
+template <int DT, bool HAS_R, int KEEP, bool UNITS>
 __global__ __launch_bounds__(256) void k_gemm_prep(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                    int64_t ldx, const float* __restrict__ r,
                                                    uint16_t* __restrict__ xq, int* __restrict__ pm,
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(256) void k_gemm_prep(const uint16_t* __restrict__ 
                                                    const uint8_t* __restrict__ zeros, int64_t N, int64_t G,
                                                    int* __restrict__ en, uint32_t* __restrict__ ctab) {
   const int64_t nc = (N + kConstRows - 1) / kConstRows;
-  if ((int64_t)blockIdx.x < nc) gemm_consts_block<ONCE>(blockIdx.x, scales, zeros, N, G, en, ctab);
+  if ((int64_t)blockIdx.x < nc) gemm_consts_block<UNITS>(blockIdx.x, scales, zeros, N, G, en, ctab);
   else rows_f16_block<DT, HAS_R, true, KEEP>((int64_t)blockIdx.x - nc, x, K, ldx, r, xq, pm);
 }
 
@@ -660,15 +661,15 @@ inline GemmWs gemm_ws(void* ws, int64_t M, int64_t N, int64_t K, int group) {
   return w;
 }
 
-template <int DT, bool HAS_R, bool ONCE>
+template <int DT, bool HAS_R, bool UNITS>
 void gemm_prep(const GemmWs& w, const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint16_t* scales,
                const uint8_t* zeros, int64_t N, int glog, const float* r, hipStream_t st) {
   const dim3 pgrid((unsigned)(M + (N + kConstRows - 1) / kConstRows));
   if (K > 256 * 8 * kRowsKeep)
-    hipLaunchKernelGGL((k_gemm_prep<DT, HAS_R, 2 * kRowsKeep, ONCE>), pgrid, dim3(256), 0, st, x, M, K, ldx, r,
+    hipLaunchKernelGGL((k_gemm_prep<DT, HAS_R, 2 * kRowsKeep, UNITS>), pgrid, dim3(256), 0, st, x, M, K, ldx, r,
                        w.xq, w.pm, scales, zeros, N, K >> glog, w.en, w.ctab);
   else
-    hipLaunchKernelGGL((k_gemm_prep<DT, HAS_R, kRowsKeep, ONCE>), pgrid, dim3(256), 0, st, x, M, K, ldx, r,
+    hipLaunchKernelGGL((k_gemm_prep<DT, HAS_R, kRowsKeep, UNITS>), pgrid, dim3(256), 0, st, x, M, K, ldx, r,
                        w.xq, w.pm, scales, zeros, N, K >> glog, w.en, w.ctab);
 }
 
@@ -1054,7 +1055,7 @@ hipError_t linear_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
   gemm_prep<DT, false, true>(w, x, M, K, ldx, scales, zeros, N, glog, nullptr, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return awq::launch_linear_tiles(w.xq, w.pm, w.en, w.ctab, qw, M, N, K, group, (float*)((char*)ws + w.bytes), y, ldy,
+  return awq::launch_linear_tiles(w.xq, w.pm, w.ctab, qw, M, N, K, group, (float*)((char*)ws + w.bytes), y, ldy,
                                   ep, st);
 }
 
