@@ -527,7 +527,8 @@ awq_status awq_lora_add(const void* x, awq_dtype xdt, int64_t M, int64_t K, int6
  * forward pass.  The sum, the bias, the activation and the residual are held
  * in fp32 and y (and pre) rounded once.  The sum is that of products of the
  * exact integers q - z and the step in fp32, or (17 to 64 tokens) of the
- * dequantized weights as two fp16 values each, for a bf16 y one.
+ * dequantized weights as two fp16 values each (steps below 2^-19 of their
+ * row's largest lose bits).
  * Activations as fp16 under exact powers of two: bf16 values below 2^-28 of
  * the largest they share one with lose bits.
  *

@@ -96,8 +96,9 @@ def test_gemm_dx_to_the_last_bit(on_gpu, case):
 
 
 WHOLE_LINEARS = [
-    # M, N, K, group: one token, up to 16, and each height of the tiles, alone, in slices, two in one launch
+    # M, N, K, group: one token, up to 16, 17 to 64, and each height of the tiles, alone, in slices, two in one launch
     (1, 515, 1024, 64), (1, 6200, 4096, 128), (2, 300, 512, 128), (9, 130, 192, 64), (16, 2048, 4096, 128),
+    (17, 1040, 1024, 128), (24, 4096, 2048, 256), (33, 100, 4096, 128), (50, 5000, 256, 64), (64, 333, 8192, 256),
     (80, 520, 2048, 128), (300, 16, 64, 64), (635, 28, 2048, 128), (1246, 3163, 1024, 64), (510, 8465, 128, 128),
     (519, 1027, 4096, 64), (1024, 4096, 4096, 128), (1100, 900, 8192, 256), (2048, 9001, 256, 128), (2300, 11008, 512, 64),
     (4097, 4100, 256, 256),

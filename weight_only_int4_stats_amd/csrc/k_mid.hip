@@ -197,16 +197,14 @@ __global__ __launch_bounds__(64 * kMidWaves) void k_gemm_mid(
           const float D = ldexpf(f16_to_f32(sr[d][t]), e[t]);
           u32x4 a[4];
           if constexpr (ONCE) {
-            // two exact parts; one, rounded, for a bf16 output, which would not show the
-            // rounding (24 tokens, 11008 -> 4096: 1.5 us of 31)
-            uint32_t mult = once_step(D) * 0x10001u, rest;
+            // two exact parts (24 tokens, 11008 -> 4096: 1.5 us of 31 for the second)
+            uint32_t mult, rest;
             const uint32_t nz = once_zero(zr[d][t]);
-            if (ep.ydt != DT_BF16) once_parts(mult, mult, rest);
+            once_parts(once_step(D) * 0x10001u, mult, rest);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const u32x4 codes = once_codes(wa[d][t][i], nz);
               a[i] = once_times(codes, mult);
-              if (ep.ydt == DT_BF16) continue;
               const u32x4 left = once_times(codes, rest);
 #pragma unroll
               for (int g = 0; g < TG; ++g) acc[t][g] = mfma16h(left, xa[d][g][i], acc[t][g]);
