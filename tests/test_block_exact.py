@@ -77,7 +77,7 @@ WHOLE_DXS = [
     (1, 453, 64, 64), (3, 8, 64, 64), (16, 1000, 512, 128), (17, 130, 1024, 64), (40, 4096, 4096, 128), (100, 2000, 2048, 256),
     (4266, 8, 64, 64), (1098, 472, 128, 64), (4201, 8, 320, 64), (519, 1000, 4096, 128), (1130, 990, 64, 64),
     (2858, 8, 1408, 128), (1051, 2004, 192, 64), (1100, 700, 4096, 256), (1635, 8, 5248, 128), (4095, 1027, 4096, 128),
-    (4435, 1296, 64, 64), (733, 9430, 6912, 128),
+    (4435, 1296, 64, 64), (733, 9430, 6912, 128), (2208, 982, 64, 64), (300, 4096, 4096, 128),
 ]
 
 
@@ -101,7 +101,7 @@ WHOLE_LINEARS = [
     (17, 1040, 1024, 128), (24, 4096, 2048, 256), (33, 100, 4096, 128), (50, 5000, 256, 64), (64, 333, 8192, 256),
     (80, 520, 2048, 128), (300, 16, 64, 64), (635, 28, 2048, 128), (1246, 3163, 1024, 64), (510, 8465, 128, 128),
     (519, 1027, 4096, 64), (1024, 4096, 4096, 128), (1100, 900, 8192, 256), (2048, 9001, 256, 128), (2300, 11008, 512, 64),
-    (4097, 4100, 256, 256),
+    (4097, 4100, 256, 256), (4110, 260, 64, 64), (1050, 8, 512, 128), (200, 515, 2048, 256),
 ]
 
 

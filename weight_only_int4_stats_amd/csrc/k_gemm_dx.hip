@@ -364,15 +364,10 @@ __global__ __launch_bounds__(256) void k_dx_zero(int64_t M, int64_t K, void* __r
   if (i < M * K) store_any(dx, dxt, i / K * lddx + i % K, 0.0f);
 }
 
-// us per stage, fitted to the times of every shape and number of slices at 17
-// sizes of 8 to 4096 rows, 1024 to 11008: the choice takes at most 2 % longer
-// than the fastest there.  (128 rows by four waves never were: 147 to 145 us at
-// 1500 rows of 5120 x 5120, 239 to 207 at 4096^3.)
-constexpr TileShape kDxShapes[] = {{8, 2, 2.29, 0.0}, {4, 2, 1.45, 0.0}, {4, 1, 0.97, 1.51}, {2, 1, 0.64, 1.04}, {1, 1, 0.63, 0.89}};
+// Compute units of the current GPU.
+inline int64_t dx_cus() { return awq::device_cus() > 0 ? awq::device_cus() : 256; }
+inline TilePlan dx_plan(int64_t M, int64_t N, int64_t K) { return dx_plan(M, N, K, dx_cus()); }
 
-inline TilePlan dx_plan(int64_t M, int64_t N, int64_t K) {
-  return tile_plan(kDxShapes, M, K, (N + kDxN - 1) / kDxN, awq::device_cus() > 0 ? awq::device_cus() : 256);
-}
 inline int64_t dx_blocks(const TilePlan& p, int64_t M, int64_t K) {
   return tile_blocks((M + 16 * p.mb * p.wm - 1) / (16 * p.mb * p.wm) * ((K + kDxCols - 1) / kDxCols) * p.S);
 }
@@ -436,7 +431,7 @@ size_t gemm_dx_ws_bytes(int64_t M, int64_t N, int64_t K, int group) {
 size_t gemm_dx_ws_bytes_upto(int64_t M, int64_t N, int64_t K) {
   using namespace awqk;
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  const int64_t parts = tile_parts(kDxShapes, M, K, (N + kDxN - 1) / kDxN, device_cus() > 0 ? device_cus() : 256);
+  const int64_t parts = tile_parts(kDxShapes, M, K, (N + kDxN - 1) / kDxN, dx_cus());
   return dx_ws(nullptr, M, N, K, 64, 1).bytes + align_up((size_t)parts * K * 4, 256);
 }
 

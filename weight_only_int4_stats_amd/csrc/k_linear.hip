@@ -279,40 +279,9 @@ __global__ __launch_bounds__(256) void k_linear_reduce(const LinearArgs a, const
   epi_store4(ep, a.y, a.ldy, m, n, cnt, z);
 }
 
-// us per stage, fitted to the times of every shape and number of slices at 16
-// sizes of 40 to 4096 rows, 1024 to 11008: the choice takes at most 3 % longer
-// than the fastest there, 9 % at 4096 rows, 2048 -> 1027.
-constexpr TileShape kLinearShapes[] = {{8, 2, 1.77, 0.0}, {4, 2, 1.06, 0.0}, {4, 1, 0.79, 1.35}, {2, 1, 0.58, 0.89}, {1, 1, 0.50, 0.87}};
-
-struct LinearPlan {
-  TilePlan t;
-  int64_t wide = 0;       // > 0: column tiles 256 rows high of the mixed launch
-  int64_t blocks = 0, wide_blocks = 0;
-};
-
-inline LinearPlan linear_plan(int64_t M, int64_t N, int64_t K) {
-  const int64_t cus = awq::device_cus() > 0 ? awq::device_cus() : 256;
-  const int64_t stages = K / kTileK, ct = (N + kTileCols - 1) / kTileCols;
-  LinearPlan p;
-  p.t = tile_plan(kLinearShapes, M, N, stages, cus);
-  const int64_t m256 = (M + 255) / 256, m128 = (M + 127) / 128;
-  // only whole numbers of rounds of tall tiles are worth a cut
-  for (int64_t r = 1; r * cus / m256 < ct && r <= 64; ++r) {
-    const int64_t a = r * cus / m256;
-    if (a < 1) continue;
-    const double cost = tile_time(kLinearShapes[0], m256 * a, stages, cus) + tile_time(kLinearShapes[1], m128 * (ct - a), stages, cus);
-    if (cost < p.t.cost) {
-      p.t.cost = cost;
-      p.t.S = 1;
-      p.t.wm = 2;
-      p.wide = a;
-    }
-  }
-  const int rows = 16 * p.t.mb * p.t.wm;
-  p.wide_blocks = tile_blocks(m256 * p.wide);
-  p.blocks = p.wide ? p.wide_blocks + tile_blocks(m128 * (ct - p.wide)) : tile_blocks((M + rows - 1) / rows * ct * p.t.S);
-  return p;
-}
+// Compute units of the current GPU.
+inline int64_t linear_cus() { return awq::device_cus() > 0 ? awq::device_cus() : 256; }
+inline LinearPlan linear_plan(int64_t M, int64_t N, int64_t K) { return linear_plan(M, N, K, linear_cus()); }
 
 inline int64_t linear_pitch(int64_t N) { return (N + 7) / 8 * 8; }
 
@@ -345,7 +314,7 @@ size_t linear_partial_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 size_t linear_partial_bytes_upto(int64_t M, int64_t N, int64_t K) {
-  const int64_t parts = awqk::tile_parts(awqk::kLinearShapes, M, N, K / awqk::kTileK, device_cus() > 0 ? device_cus() : 256);
+  const int64_t parts = awqk::tile_parts(awqk::kLinearShapes, M, N, K / awqk::kTileK, awqk::linear_cus());
   return align_up((size_t)parts * awqk::linear_pitch(N) * 4, 256);
 }
 

@@ -20,12 +20,9 @@
 
 #include "awq_device.h"
 #include "k_epilogue.h"
+#include "tile_plan.h"
 
 namespace awqk {
-
-constexpr int kTileK = 64;                // contraction per stage
-constexpr int kTileCols = 256;
-constexpr int kTileXcds = 8;              // L2 slices (block i -> slice i mod 8)
 
 // Position of an A row's 16-byte chunk c in LDS: c ^ ((r / 2) mod 8).
 __device__ __forceinline__ int tile_swz(int r) { return (r >> 1) & 7; }
@@ -190,72 +187,5 @@ struct Tile {
     lds_barrier();                                        // LDS is free for what follows
   }
 };
-
-// A tile's shape and its time per stage on a compute unit by itself and two at
-// once (0: its LDS leaves room for one), in us.
-struct TileShape {
-  int mb, wm;
-  double one, two;
-};
-
-struct TilePlan {
-  int mb = 1, wm = 1, S = 1;
-  double cost = 1e300;
-};
-
-// Time of `items` tiles of `stages` stages each: whole rounds of one tile (or
-// two at once) per compute unit, and what a round costs beside its stages
-// (start, first copies, stores).
-inline double tile_time(const TileShape& h, int64_t items, int64_t stages, int64_t cus) {
-  const int64_t load = (items + cus - 1) / cus;
-  const double per = h.two > 0.0 ? (double)(load / 2) * h.two + (double)(load % 2) * h.one : (double)load * h.one;
-  const double rounds = (double)(h.two > 0.0 ? (load + 1) / 2 : load);
-  return per * (double)stages + 9.0 * rounds;
-}
-
-// Whether `tiles` tiles may be cut into S slices: up to two rounds of work, which
-// bounds what the slices' sums take (four rounds: 0.1 % less time on average
-// over 400 thousand sizes, 15 % at most, for twice the memory).
-inline bool tile_splits(int64_t tiles, int S, int64_t stages, int64_t cus) {
-  return S <= 16 && S * 2 <= stages && tiles * S <= 2 * cus;
-}
-
-// The shape and the number of slices of the contraction with the least
-// estimated time.  Slices cost a second launch and their sums' way through
-// memory (6.5 TB/s: they partly stay in the last cache).  Rows count in whole
-// 16s, so that the choice is the same up to the next multiple.
-template <int NSHAPES>
-inline TilePlan tile_plan(const TileShape (&shapes)[NSHAPES], int64_t M, int64_t cols, int64_t stages, int64_t cus) {
-  const int64_t ct = (cols + kTileCols - 1) / kTileCols, M16 = (M + 15) / 16 * 16;
-  TilePlan best;
-  for (const TileShape& h : shapes) {
-    const int64_t tiles = (M + 16 * h.mb * h.wm - 1) / (16 * h.mb * h.wm) * ct;
-    for (int S = 1; S == 1 || tile_splits(tiles, S, stages, cus); S *= 2) {
-      const double cost = tile_time(h, tiles * S, (stages + S - 1) / S, cus) + (S > 1 ? 2.5 + (double)S * M16 * cols * 8 / 6.5e6 : 0.0);
-      if (cost < best.cost) {
-        best.mb = h.mb;
-        best.wm = h.wm;
-        best.S = S;
-        best.cost = cost;
-      }
-    }
-  }
-  return best;
-}
-
-// What slices times rows may come to for any number of rows up to M.
-template <int NSHAPES>
-inline int64_t tile_parts(const TileShape (&shapes)[NSHAPES], int64_t M, int64_t cols, int64_t stages, int64_t cus) {
-  const int64_t ct = (cols + kTileCols - 1) / kTileCols;
-  int64_t most = 0;
-  for (const TileShape& h : shapes)
-    for (int S = 2; tile_splits(ct, S, stages, cus); S *= 2) {
-      const int64_t rows = 2 * cus / (S * ct) * 16 * h.mb * h.wm, r = rows < M ? rows : M;
-      most = S * r > most ? S * r : most;
-    }
-  return most;
-}
-
-inline int64_t tile_blocks(int64_t items) { return kTileXcds * ((items + kTileXcds - 1) / kTileXcds); }
 
 }  // namespace awqk
