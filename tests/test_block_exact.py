@@ -141,3 +141,44 @@ def test_linear_with_a_step_for_each_group(on_gpu, case):
     y = awq.awq_w4a16_linear(x, *q, out_dtype=torch.float32, group_size=g)
     off = (y.double() - ref).abs()
     assert bool((off <= (3 * (K // g) + 2 * 60 + 4) * 2.0 ** -24 * size).all()), float((off / size.clamp_min(1e-30)).max() * 2 ** 24)
+
+
+# ---- norms of rows far from 0 ---------------------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [9, 512, 1000, 4096, 8192, 20001, 40000, 131072])
+@pytest.mark.parametrize("mean", [0.0, 1e3, -1e4, 1e5])
+def test_layer_norm_of_rows_far_from_zero(on_gpu, K, mean):
+    """A mean of many times the spread costs no more than its own rounding where it is stored: the values themselves are off
+    by what a norm of centred values is, sums of under 160 additions (K values as 8 or more per lane, 6 steps of a wave,
+    up to 16 waves) of values the size of the spread."""
+    gen = torch.Generator().manual_seed(K)
+    x = (torch.randn(5, K, generator=gen) + mean).cuda()
+    w = torch.randn(K, generator=gen).cuda()
+    stats = torch.empty(2, 5, device="cuda")
+    y = awq.awq_layer_norm(x, w, stats=stats, eps=1e-5)
+    xd = x.double()
+    mu = xd.mean(1, keepdim=True)
+    d = xd - mu
+    rstd = 1.0 / torch.sqrt(d.square().mean(1, keepdim=True) + 1e-5)
+    u = 2.0 ** -24
+    # a centred value: the first subtraction (exact from 2 spreads on, else half a step of the value and the mean) and the
+    # second one, half a step of the spread each; the mean of what is left, 160 additions; 1 / sigma: as many again, halved
+    e_d = 2 * u * d.abs() + (160 * u + 2 * u) * d.abs().mean(1, keepdim=True)
+    ref = d * rstd * w.double()
+    e = w.double().abs() * rstd * (e_d + d.abs() * 90 * u) + w.double().abs() * d.abs() * rstd ** 3 * (d.abs() * e_d).mean(1, keepdim=True)
+    e = e + 4 * u * ref.abs()
+    assert bool(((y.double() - ref).abs() <= e).all()), float(((y.double() - ref).abs() / e).max())
+    assert bool(((stats[0].double() - mu[:, 0]).abs() <= u * mu[:, 0].abs() + 164 * u * d.abs().mean(1)).all())
+    assert bool(((stats[1].double() / rstd[:, 0] - 1).abs() <= 90 * u + 164 * u).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [7, 300, 4096, 9000, 40000])
+def test_layer_norm_of_equal_values(on_gpu, K):
+    """Rounding leaves no negative variance: finite with the smallest eps."""
+    x = torch.tensor([0.1, 1e4 / 3, -7e-3, 1e20], device="cuda")[:, None].expand(4, K).contiguous()
+    stats = torch.empty(2, 4, device="cuda")
+    y = awq.awq_layer_norm(x, torch.ones(K, device="cuda"), stats=stats, eps=1e-30)
+    assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(stats[:, :3]).all())

@@ -6,8 +6,9 @@
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 // Both are bound by memory (8192 x 4096: 32 us forward from 32 to 16 bits, 6.3
 // TB/s; 37 + 5 us backward in bf16, 5.5 TB/s in the first): a row is read once
-// and stays in registers (the variance is that of the centred values, so a large
-// mean costs nothing), and the backward pass adds up dw and db in registers over
+// and stays in registers (the variance is that of the centred values, and what
+// the first sum's rounding left in their mean is taken off again: at a mean of
+// 1e4 sigma it shifted every value by 1e-3 sigma), and the backward pass adds up dw and db in registers over
 // all the rows a block takes, leaves one partial row per block and adds those in
 // a second launch (k_col_reduce), in a fixed order.
 #include "awq_device.h"
@@ -41,6 +42,13 @@ __device__ __forceinline__ void group_sum(float (&v)[NV], float (*red)[16][NV], 
   }
 }
 
+// Of values with the mean square sq and the mean m; equal values may leave less
+// than 0 by rounding.  (NaN stays.)
+__device__ __forceinline__ float variance(float sq, float m) {
+  const float v = __builtin_fmaf(-m, m, sq);
+  return v < 0.0f ? 0.0f : v;
+}
+
 struct NormArgs {
   const void* x;
   const void* w;
@@ -56,7 +64,7 @@ struct NormArgs {
 // Lanes T of a row, KEEP chunks of eight values each in registers.
 template <int XDT, int T, int KEEP, bool RMS>
 __global__ __launch_bounds__(T > 256 ? T : 256) void k_norm(const NormArgs a) {
-  __shared__ float red[2][16][1];
+  __shared__ float red[1][16][1], red2[1][16][2];
   constexpr int RB = (T > 256 ? T : 256) / T;                    // rows per block
   const int t = threadIdx.x % T;
   const int64_t m = (int64_t)blockIdx.x * RB + threadIdx.x / T;
@@ -77,18 +85,29 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void k_norm(const NormArgs a) {
     group_sum<T, 1>(s, red, 0);
     mu = s[0] / (float)a.K;
   }
-  s[0] = 0.0f;
+  float q[2] = {0.0f, 0.0f};                       // sums of the centred values' squares and of themselves
 #pragma unroll
   for (int i = 0; i < KEEP; ++i) {
     const int64_t c = (int64_t)(t + T * i) * 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       v[i][j] = c + j < a.K ? v[i][j] - mu : 0.0f;
-      s[0] = __builtin_fmaf(v[i][j], v[i][j], s[0]);
+      q[0] = __builtin_fmaf(v[i][j], v[i][j], q[0]);
+      if constexpr (!RMS) q[1] += v[i][j];
     }
   }
-  group_sum<T, 1>(s, red, 1);
-  const float r = 1.0f / sqrtf(s[0] / (float)a.K + a.eps);
+  float left = 0.0f;
+  if constexpr (RMS) {
+    s[0] = q[0];
+    group_sum<T, 1>(s, red, 0);
+    q[0] = s[0] / (float)a.K;
+  } else {
+    group_sum<T, 2>(q, red2, 0);
+    left = q[1] / (float)a.K;
+    q[0] = variance(q[0] / (float)a.K, left);
+    mu += left;
+  }
+  const float r = 1.0f / sqrtf(q[0] + a.eps);
   if (!live) return;
   if (t == 0) {
     if (a.mean) a.mean[m] = mu;
@@ -102,7 +121,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void k_norm(const NormArgs a) {
     float w[8], o[8];
     load8_any(a.w, a.wdt, c, cnt, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = v[i][j] * r * w[j];
+    for (int j = 0; j < 8; ++j) o[j] = (v[i][j] - left) * r * w[j];
     if (a.b) {
       float b[8];
       load8_any(a.b, a.bdt, c, cnt, b);
@@ -116,7 +135,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void k_norm(const NormArgs a) {
 // Rows too long for registers: one block per row, read three times.
 template <int XDT, bool RMS>
 __global__ __launch_bounds__(1024) void k_norm_long(const NormArgs a) {
-  __shared__ float red[2][16][1];
+  __shared__ float red[1][16][1], red2[1][16][2];
   const int64_t m = blockIdx.x;
   auto cnt_at = [&](int64_t c) { return a.K - c < 8 ? (int)(a.K - c) : 8; };
   float mu = 0.0f;
@@ -131,20 +150,22 @@ __global__ __launch_bounds__(1024) void k_norm_long(const NormArgs a) {
     group_sum<1024, 1>(s, red, 0);
     mu = s[0] / (float)a.K;
   }
-  s[0] = 0.0f;
+  float q[2] = {0.0f, 0.0f};
   for (int64_t c = (int64_t)threadIdx.x * 8; c < a.K; c += 8192) {
     float v[8];
     load8_any(a.x, XDT, m * a.ldx + c, cnt_at(c), v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float d = c + j < a.K ? v[j] - mu : 0.0f;
-      s[0] = __builtin_fmaf(d, d, s[0]);
+      q[0] = __builtin_fmaf(d, d, q[0]);
+      q[1] += d;
     }
   }
-  group_sum<1024, 1>(s, red, 1);
-  const float r = 1.0f / sqrtf(s[0] / (float)a.K + a.eps);
+  group_sum<1024, 2>(q, red2, 0);
+  const float left = RMS ? 0.0f : q[1] / (float)a.K;
+  const float r = 1.0f / sqrtf(variance(q[0] / (float)a.K, left) + a.eps);
   if (threadIdx.x == 0) {
-    if (a.mean) a.mean[m] = mu;
+    if (a.mean) a.mean[m] = mu + left;
     if (a.rstd) a.rstd[m] = r;
   }
   for (int64_t c = (int64_t)threadIdx.x * 8; c < a.K; c += 8192) {
@@ -154,7 +175,7 @@ __global__ __launch_bounds__(1024) void k_norm_long(const NormArgs a) {
     load8_any(a.w, a.wdt, c, cnt, w);
     if (a.b) load8_any(a.b, a.bdt, c, cnt, b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (v[j] - mu) * r * w[j] + b[j];
+    for (int j = 0; j < 8; ++j) v[j] = (v[j] - mu - left) * r * w[j] + b[j];
     store8_any(a.y, a.ydt, m * a.ldy + c, cnt, v);
   }
 }
