@@ -154,8 +154,9 @@ int awq_abi_version(void);
 /* Human-readable name of a status value (static storage). */
 const char* awq_status_str(awq_status st);
 
-/* Workspace bytes a call needs for the given sizes (0 if it needs none), for
- * every group size.  Arguments that an op does not use are ignored.  From
+/* Workspace bytes a call needs for the given sizes on the current device (its
+ * compute units decide how work is split), 0 if it needs none, for every group
+ * size.  Arguments that an op does not use are ignored.  From
  * AWQ_OP_EXPERTS_UP on the bytes for M serve every smaller M too, and an M, N,
  * K, T or n_alpha past what the calls accept gives 0. */
 size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T, int n_alpha);

@@ -182,3 +182,41 @@ def test_layer_norm_of_equal_values(on_gpu, K):
     stats = torch.empty(2, 4, device="cuda")
     y = awq.awq_layer_norm(x, torch.ones(K, device="cuda"), stats=stats, eps=1e-30)
     assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(stats[:, :3]).all())
+
+
+# ---- workspaces -------------------------------------------------------------------------------
+
+
+def test_workspace_sizes_are_asked_of_the_tensors_gpu(monkeypatch):
+    """Two GPUs with different numbers of compute units: each call's bytes are those of the GPU its tensors are on, whichever
+    is the current one and whichever was asked first."""
+    import contextlib
+
+    import weight_only_int4_stats_amd as pkg
+
+    current = [0]
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d
+        yield
+        current[0] = before
+
+    class Stub:
+        @staticmethod
+        def awq_workspace_bytes(op, M, N, K, T, n):
+            return M * (256, 304)[current[0]]
+
+    monkeypatch.setattr(pkg, "lib", lambda: Stub)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    pkg._ws_need.cache_clear()
+    try:
+        for _ in range(2):
+            for now in (0, 1):
+                current[0] = now
+                assert pkg._ws_need(pkg.AWQ_OP_LINEAR, 10, 1, 1, 0, 0, 0) == 2560
+                assert pkg._ws_need(pkg.AWQ_OP_LINEAR, 10, 1, 1, 0, 0, 1) == 3040
+                assert current[0] == now
+    finally:
+        pkg._ws_need.cache_clear()
