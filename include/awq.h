@@ -161,6 +161,12 @@ const char* awq_status_str(awq_status st);
  * K, T or n_alpha past what the calls accept gives 0. */
 size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T, int n_alpha);
 
+/* The same for one call of exactly these sizes, where fewer rows may need more:
+ * AWQ_OP_LINEAR and AWQ_OP_GEMM_DX cut their work into slices only where rows
+ * are few (2048 rows, 4096 -> 11008: 20 MB instead of 135).  For the other ops
+ * what awq_workspace_bytes gives. */
+size_t awq_workspace_bytes_exact(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T, int n_alpha);
+
 /*
  * Calibration statistic: mean_abs[j] = average over t of |x[t][j]|.
  * "AWQ Math", section "Saliency is an activation property, not a weight

@@ -204,7 +204,7 @@ def test_workspace_sizes_are_asked_of_the_tensors_gpu(monkeypatch):
 
     class Stub:
         @staticmethod
-        def awq_workspace_bytes(op, M, N, K, T, n):
+        def awq_workspace_bytes_exact(op, M, N, K, T, n):
             return M * (256, 304)[current[0]]
 
     monkeypatch.setattr(pkg, "lib", lambda: Stub)
@@ -220,3 +220,28 @@ def test_workspace_sizes_are_asked_of_the_tensors_gpu(monkeypatch):
                 assert current[0] == now
     finally:
         pkg._ws_need.cache_clear()
+
+
+@pytest.mark.parametrize("N,K", [(11008, 4096), (4096, 11008), (515, 512), (64, 8192), (2048, 16384)])
+def test_exact_workspaces_are_what_a_call_asks_for(N, K):
+    """A byte less is refused, as many are taken (x and y overlap: refused after the workspace), and the query that serves
+    every smaller batch gives no less."""
+    lib, A, V = awq.lib(), 1 << 32, 1 << 40
+    for M in (1, 2, 16, 17, 33, 64, 65, 130, 519, 1000, 2048, 4097):
+        for op in (awq._abi.AWQ_OP_LINEAR, awq._abi.AWQ_OP_GEMM_DX):
+            need = lib.awq_workspace_bytes_exact(op, M, N, K, 0, 0)
+            assert 0 <= need <= lib.awq_workspace_bytes(op, M, N, K, 0, 0)
+
+            def status(bytes_, g):
+                if op == awq._abi.AWQ_OP_LINEAR:
+                    return lib.awq_w4a16_linear(A, 0, M, K, K, V, V, V, N, g, None, 0, 0, None, 0, None, 0, A, 0, N, V, bytes_, None)
+                return lib.awq_w4a16_gemm_dx(A, 0, M, N, N, V, V, V, K, g, A, 0, K, V, bytes_, None)
+
+            groups = [g for g in (64, 128, 256) if K % g == 0]
+            assert all(status(need, g) == 5 for g in groups)
+            assert need == 0 or any(status(need - 1, g) == 6 for g in groups)
+    assert lib.awq_workspace_bytes_exact(awq._abi.AWQ_OP_LINEAR, 2048, 11008, 4096, 0, 0) < 24e6
+    for op, size in ((awq._abi.AWQ_OP_BALANCE_LOSS, (1000, 0, 0, 64)), (awq._abi.AWQ_OP_LAYER_NORM_BACKWARD, (1000, 0, 512, 0)),
+                     (awq._abi.AWQ_OP_GEMM, (100, 512, 512, 0)), (awq._abi.AWQ_OP_LINEAR, (-1, 512, 512, 0)),
+                     (awq._abi.AWQ_OP_LINEAR, (0, 512, 512, 0)), (awq._abi.AWQ_OP_GEMM_DX, (1 << 25, 512, 512, 0))):
+        assert lib.awq_workspace_bytes_exact(op, *size, 0) == lib.awq_workspace_bytes(op, *size, 0)

@@ -343,11 +343,11 @@ def _on_stream(stream, t: torch.Tensor):
 
 @functools.lru_cache(maxsize=4096)
 def _ws_need(op: int, M: int, N: int, K: int, T: int, n: int, dev: int) -> int:
-    """awq_workspace_bytes of the operators below on GPU dev: a function of the sizes and of its compute units."""
+    """What one call of the operators below needs on GPU dev: a function of the sizes and of its compute units."""
     if dev == torch._C._cuda_getDevice():
-        return lib().awq_workspace_bytes(op, M, N, K, T, n)
+        return lib().awq_workspace_bytes_exact(op, M, N, K, T, n)
     with torch.cuda.device(dev):
-        return lib().awq_workspace_bytes(op, M, N, K, T, n)
+        return lib().awq_workspace_bytes_exact(op, M, N, K, T, n)
 
 
 def _ws(op: int, dev: torch.device, ws: torch.Tensor | None, M: int, N: int, K: int, T: int,

@@ -36,6 +36,7 @@ SIGNATURES = {
     "awq_abi_version": (ctypes.c_int, []),
     "awq_status_str": (ctypes.c_char_p, [_i]),
     "awq_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _i64, _i]),
+    "awq_workspace_bytes_exact": (_sz, [_i, _i64, _i64, _i64, _i64, _i]),
     "awq_act_stats": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _sz, _p]),
     "awq_search_scales": (_i, [_p, _i, _i64, _i64, _p, _i64, _i64, _p, _p, _i, _i, _p, _p, _p, _p,
                                _p, _sz, _p]),

@@ -67,6 +67,12 @@ size_t awq_workspace_bytes(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T
   return 0;
 }
 
+size_t awq_workspace_bytes_exact(awq_op op, int64_t M, int64_t N, int64_t K, int64_t T, int n_alpha) {
+  if (N < 0 || K < 0 || T < 0 || M < 0) return 0;
+  if (op == AWQ_OP_LINEAR || op == AWQ_OP_GEMM_DX) return awq::block_ws_bytes_exact((int)op, M, N, K, T);
+  return awq_workspace_bytes(op, M, N, K, T, n_alpha);
+}
+
 awq_status awq_act_stats(const void* x, awq_dtype xdt, int64_t T, int64_t K, int64_t ldx,
                          float* mean_abs, void* ws, size_t ws_bytes, void* stream) {
   if (!x || !mean_abs) return AWQ_ERR_NULL;

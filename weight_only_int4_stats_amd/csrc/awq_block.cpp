@@ -68,6 +68,18 @@ size_t block_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t T) {
   return 0;
 }
 
+size_t block_ws_bytes_exact(int op, int64_t M, int64_t N, int64_t K, int64_t T) {
+  if ((op != AWQ_OP_LINEAR && op != AWQ_OP_GEMM_DX) || M < 1 || N < 1 || K < 1 || !linear_sizes(M, N, K))
+    return block_ws_bytes(op, M, N, K, T);
+  size_t most = 0;
+  for (int g = 64; g <= 256; g *= 2) {              // which kernel serves a shape depends on it
+    if (K % g != 0) continue;
+    const size_t b = op == AWQ_OP_LINEAR ? linear_ws_bytes(M, N, K, g) : gemm_dx_ws_bytes(M, N, K, g);
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
 }  // namespace awq
 
 extern "C" {

@@ -167,7 +167,8 @@ int64_t lora_threads(int64_t M, int64_t N, int64_t K, int64_t n_adapters, int64_
 hipError_t launch_lora(const LoraCall& c, void* ws, hipStream_t st);
 
 // ---- operators of a block around the packed linears -----------------------------
-size_t block_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t T);
+size_t block_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t T);        // for any M' <= M
+size_t block_ws_bytes_exact(int op, int64_t M, int64_t N, int64_t K, int64_t T);
 
 // The product with an epilogue (k_w4a16.hip chooses, k_linear.hip: the tiles)
 bool linear_mid(int64_t M, int64_t N, int64_t K);    // the 17 .. 64 token kernel serves this shape
