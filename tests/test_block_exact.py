@@ -143,6 +143,36 @@ def test_linear_with_a_step_for_each_group(on_gpu, case):
     assert bool((off <= (3 * (K // g) + 2 * 60 + 4) * 2.0 ** -24 * size).all()), float((off / size.clamp_min(1e-30)).max() * 2 ** 24)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 40, 100, 519, 1300])
+@pytest.mark.parametrize("N,K,g", [(520, 1024, 64), (300, 2048, 256)])
+def test_linear_of_steps_far_apart(on_gpu, M, N, K, g):
+    """Steps of a row up to 2^18 apart, some 0, tokens that meet one group each: no group costs another its bits.  In the
+    tiles a step of 0 beside others counts as 2^-80 (its codes' sum, in units of the step, joins a sum whose unit has to
+    be other than 0): a token that meets such a group alone has 2^-80 of the sum of its codes' sizes in place of 0."""
+    gen = torch.Generator().manual_seed(M)
+    q, w = whole_weights(N, K, g, M)
+    G = K // g
+    shift = 2.0 ** -torch.randint(0, 19, (N, G), generator=gen).double()
+    shift[torch.rand(N, G, generator=gen) < 0.1] = 0.0
+    shift[3], shift[7, 1:] = 0.0, 0.0
+    base = q[1].double() * 2.0 ** 14
+    step = (base * shift.cuda()).to(torch.float16)
+    assert bool((step.double() == base * shift.cuda()).all())
+    units = w.unflatten(1, (-1, g)) / q[1].double().unsqueeze(-1)
+    w = (units * step.double().unsqueeze(-1)).flatten(1)
+    at = torch.randint(0, G, (M,), generator=gen)
+    x = torch.zeros(M, G, g)
+    x[torch.arange(M), at] = torch.randint(-8, 9, (M, g), generator=gen).float()
+    x = x.flatten(1).half().cuda()
+    ref, size = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    y = awq.awq_w4a16_linear(x, q[0], step, q[2], out_dtype=torch.float32, group_size=g)
+    assert bool((y[:, 3] == 0).all())
+    off = (y.double() - ref).abs()
+    none = x.double().abs() @ torch.where(step.repeat_interleave(g, 1) == 0, units.abs().flatten(1), 0.0).t()
+    assert bool((off <= (3 * G + 2 * g + 4) * 2.0 ** -24 * size + 2.0 ** -80 * none * 1.001).all()), float((off / size.clamp_min(1e-30)).max() * 2 ** 24)
+
+
 # ---- norms of rows far from 0 ---------------------------------------------------------------
 
 
