@@ -41,7 +41,8 @@
  *                          of the shared product
  * The rest of a pre-norm block around the packed linears, and the gradients of
  * what stays in full precision there while the packed weights are frozen (the
- * norms, the biases, the router's gate):
+ * norms, the biases; of a router's gate the balance loss's part, since the
+ * routed products have no backward pass here):
  *   awq_w4a16_linear          the product with bias, activation and residual
  *                             in its epilogue
  *   awq_bias_act_backward     the epilogue's backward pass

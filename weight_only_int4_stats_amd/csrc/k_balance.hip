@@ -17,7 +17,7 @@
 //   3. k_balance_grad: a wave per row again.
 // Bound by reading the logits (and writing their gradient); nothing is added
 // by floating-point atomics, so the results do not depend on an order.  16384 x
-// 256 with sigmoid scores: 15 us and 10 for the gradient; 519 x 60: 8 and 3.
+// 256 with sigmoid scores: 15 us and 11 for the gradient; 519 x 60: 8 and 3.
 #include "awq_device.h"
 #include "awq_internal.h"
 #include "k_epilogue.h"

@@ -214,7 +214,8 @@ __device__ __forceinline__ void waves_sum(float (&v)[2], float (*red)[16][2], in
 // lane.  Block b takes the rows b RB + i, (b + grid) RB + i, ...; W is just
 // enough for a row, so that a width of 5120 leaves no lane idle.
 // (dy's type is known at compile time: with loads of either kind the rows on
-// their way went through scratch memory, 45 us instead of 37 at 8192 x 4096.)
+// their way went through scratch memory, 45 us instead of 37 at 8192 x 4096.  Rows of 8193
+// to 16384 values with an fp32 x or dy still leave 3 to 8 registers there.)
 template <int XDT, int DYT, int KEEP, bool RMS>
 __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int W, int RB) {
   __shared__ float red[2][16][2];

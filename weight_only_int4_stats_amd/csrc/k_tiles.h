@@ -7,8 +7,8 @@
 //    two blocks per compute unit for the small tiles), since few rows leave a
 //    block little to do per stage.  Three cover the memory's latency already;
 //    five and six measured the same.  The small tiles are bound by the
-//    dequantization (0.5 to 0.8 us a stage, of which the products take 0.06 to
-//    0.24), the tall ones by the matrix pipe and the reads that feed it (1.8 us).
+//    dequantization (0.5 to 1 us a stage), the tall ones by the matrix pipe and
+//    the reads that feed it (1.8 us; 2.3 to 3 for dx, which has two products).
 //  * One barrier per stage, ahead of its last sub-step's products: by then
 //    every wave has read the stage's last operands into registers, so its slot
 //    takes the copies of stage s + NS, and the next stage's first operands are

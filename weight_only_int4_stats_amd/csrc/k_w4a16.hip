@@ -1039,7 +1039,7 @@ hipError_t w4a16_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, 
 // awq_w4a16_linear: the memory-bound kernels with the epilogue where they
 // serve the shape, else the tiles of k_linear.hip behind the same pre-pass.  One
 // token, 4096 -> 11008 with bias and gelu_tanh: 7.9 us (3.0 TB/s; 6.7 without);
-// 24 tokens, 11008 -> 4096 with a residual: 4 + 23 + 4 us.
+// 24 tokens, 11008 -> 4096 with a residual: 4 + 24 + 4 us.
 template <int DT>
 hipError_t linear_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint32_t* qw,
                            const uint16_t* scales, const uint8_t* zeros, int64_t N, int glog, void* y, int64_t ldy,
@@ -1063,10 +1063,11 @@ hipError_t linear_dispatch(const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
 
 namespace awq {
 
-// Above 32 tokens the tiles are faster on layers past 25 million weights (40
-// tokens, 4096 -> 11008: 31 us against 41; 64 tokens, 11008 -> 4096: 34 against
-// 40), below they are not (64 tokens, 4096 x 4096: 24 and 24; 33 tokens: 20
-// against 19; 24 tokens, 11008 -> 4096: 28 and 28).
+// Above 32 tokens the tiles are faster on layers past 25 million weights (us, this
+// kernel and the tiles: 40 tokens, 4096 -> 11008 46 and 36; 64 tokens, 11008 ->
+// 4096 46 and 39), below they are not (64 tokens, 4096 x 4096 28 and 28; 33 tokens
+// 24 and 26), nor are they with fewer tokens (24 tokens, 4096 -> 11008 30 and 36; 11008
+// -> 4096 36 and 35).
 bool linear_mid(int64_t M, int64_t N, int64_t K) {
   return mid_supported(M, N, K) && (M <= 32 || N * K <= (int64_t)25 << 20);
 }
